@@ -112,6 +112,10 @@ def _batch(case, seed):
         past = np.full(R, ctx, np.int64) - rng.integers(0, min(B, ctx), R)
         n = np.full(R, new, np.int64)
     past[0], n[0] = ctx, new  # the batch reaches the case's size
+    if case["op"] == "append":
+        # a piece that reaches past the next block starts at a page, as a scheduler cuts prompts (the pass then
+        # leaves its own inputs, the tail's rows, as they were, and can be made again)
+        past = np.where((past + n) // B >= past // B + 2, past // B * B, past)
     if case["op"] == "step" and R > 2:
         idle = rng.random(R)
         n = np.where(idle < 0.06, 0, np.where(idle < 0.12, -1, n))  # -1: the request has finished
