@@ -26,12 +26,15 @@ MSA_ERR_TIMEOUT = 6
 MSA_ERR_CUDA = 7
 MSA_ERR_INVALID_DOCUMENTS = 8
 MSA_ERR_SCRATCH_TOO_SMALL = 9
+MSA_ERR_INVALID_CACHE = 10
 MSA_NOALLOC_SCRATCH_BYTES = 16 << 20
 MSA_TASK_META_COLS = 6
 MSA_STAGE_PREPROCESS, MSA_STAGE_MAIN, MSA_STAGE_POSTPROCESS, MSA_STAGE_ALL = 1, 2, 4, 7
 MSA_BWD_DQ_FP32 = 8
 MSA_BWD_SELFTEST_HOLD_REDUCE = 16
 MSA_WALK_LEN = 8
+MSA_CACHE_TILE_BYTES = 9216
+MSA_CHUNK_COLS = 4
 
 HEAD_DIM, BLOCK, CHUNK, GROUP = 128, 64, 8, 16
 
@@ -62,12 +65,19 @@ class msa_problem(ctypes.Structure):
     ]
 
 
+class msa_cache_problem(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in (
+        "num_requests", "num_pages", "max_blocks", "num_q_heads", "num_kv_heads", "head_dim", "block_size",
+        "query_chunk", "topk", "token_cap", "chunk_cap", "k_exp", "v_exp")] + [("softmax_scale", ctypes.c_float)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libmsa.so is not built ({LIB_PATH}); run __graft_entry__.build() "
                           "or python -m block_sparse_top_attn_gb300.build_lib")
     lib = ctypes.CDLL(LIB_PATH)
     P = ctypes.POINTER(msa_problem)
+    C = ctypes.POINTER(msa_cache_problem)
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     sig = {
         "msa_workspace_bytes": (sz, [P, i64, i64, i32]),
@@ -89,6 +99,13 @@ def _load():
         "msa_select_topk": (ctypes.c_int, [P, vp, vp, vp, vp, vp, sz, vp]),
         "msa_plan_forward": (ctypes.c_int, [P, vp, vp, vp, vp, vp, sz, vp]),
         "msa_fwd_planned": (ctypes.c_int, [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "msa_cache_bytes": (sz, [C]),
+        "msa_cache_chunk_bound": (i64, [i64, i64]),
+        "msa_cache_step": (ctypes.c_int, [C] + [vp] * 13),
+        "msa_cache_append": (ctypes.c_int, [C] + [vp] * 11),
+        "msa_cache_read": (ctypes.c_int, [C] + [vp] * 6),
+        "msa_cache_select": (ctypes.c_int, [C] + [vp] * 7),
+        "msa_cache_fwd": (ctypes.c_int, [C] + [vp] * 9),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -438,3 +455,215 @@ def forward(p: Problem, sel, q, k, v, stream=None, plan=None):
     else:
         msa_fwd_planned(p, q, k, v, sel, plan, o, lse, st, ws, stream)
     return o, lse, st
+
+
+# ---------------------------------------------------------------------------
+# serving: the 4-bit paged cache
+# ---------------------------------------------------------------------------
+
+def make_cache_problem(num_requests, num_pages, max_blocks, num_q_heads, topk, token_cap, chunk_cap=None,
+                       softmax_scale=HEAD_DIM ** -0.5, block_size=BLOCK, k_exp=0, v_exp=0,
+                       device="cuda") -> msa_cache_problem:
+    """The C description of a cache and the sizes of one step's tensors.
+    chunk_cap defaults to the bound that holds any token_cap new tokens."""
+    s = msa_cache_problem()
+    s.num_requests, s.num_pages, s.max_blocks = int(num_requests), int(num_pages), int(max_blocks)
+    s.num_q_heads, s.num_kv_heads = int(num_q_heads), int(num_q_heads) // GROUP
+    s.head_dim, s.block_size, s.query_chunk, s.topk = HEAD_DIM, int(block_size), CHUNK, int(topk)
+    s.token_cap = int(token_cap)
+    s.chunk_cap = msa_cache_chunk_bound(token_cap, num_requests) if chunk_cap is None else int(chunk_cap)
+    s.k_exp, s.v_exp, s.softmax_scale = int(k_exp), int(v_exp), float(softmax_scale)
+    return s
+
+
+def msa_cache_bytes(c: msa_cache_problem) -> int:
+    return int(lib.msa_cache_bytes(ctypes.byref(c)))
+
+
+def msa_cache_chunk_bound(tokens: int, num_requests: int) -> int:
+    return int(lib.msa_cache_chunk_bound(int(tokens), int(num_requests)))
+
+
+def new_cache(c: msa_cache_problem, device="cuda"):
+    """A cache of zeros, uint8 [num_pages, Hkv, block_size / 64, MSA_CACHE_TILE_BYTES]."""
+    import torch
+    if msa_cache_bytes(c) == 0:
+        raise MSAError(MSA_ERR_INVALID_ARGUMENT, "msa_cache_bytes")
+    return torch.zeros((c.num_pages, c.num_kv_heads, c.block_size // BLOCK, MSA_CACHE_TILE_BYTES),
+                       dtype=torch.uint8, device=device)
+
+
+def msa_cache_step(c, new_lens, seq_lens, ring, free_ring, block_table, seq_lens_out, ring_out, cu_tokens, slot_map,
+                   positions, chunks, d_status, stream=None):
+    _check(lib.msa_cache_step(ctypes.byref(c), _ptr(new_lens), _ptr(seq_lens), _ptr(ring), _ptr(free_ring),
+                              _ptr(block_table), _ptr(seq_lens_out), _ptr(ring_out), _ptr(cu_tokens),
+                              _ptr(slot_map), _ptr(positions), _ptr(chunks), _ptr(d_status), _stream(stream)),
+           "msa_cache_step")
+
+
+def msa_cache_append(c, k, v, k_index, slot_map, cu_tokens, chunks, cache, index_tail, index_pool, d_status,
+                     stream=None):
+    _check(lib.msa_cache_append(ctypes.byref(c), _ptr(k), _ptr(v), _ptr(k_index), _ptr(slot_map), _ptr(cu_tokens),
+                                _ptr(chunks), _ptr(cache), _ptr(index_tail), _ptr(index_pool), _ptr(d_status),
+                                _stream(stream)),
+           "msa_cache_append")
+
+
+def msa_cache_read(c, slots, cache, k, v, d_status, stream=None):
+    _check(lib.msa_cache_read(ctypes.byref(c), _ptr(slots), _ptr(cache), _ptr(k), _ptr(v), _ptr(d_status),
+                              _stream(stream)),
+           "msa_cache_read")
+
+
+def msa_cache_select(c, q_index, index_pool, block_table, chunks, sel, d_status, stream=None):
+    _check(lib.msa_cache_select(ctypes.byref(c), _ptr(q_index), _ptr(index_pool), _ptr(block_table), _ptr(chunks),
+                                _ptr(sel), _ptr(d_status), _stream(stream)),
+           "msa_cache_select")
+
+
+def msa_cache_fwd(c, q, cache, block_table, chunks, sel, o, lse, d_status, stream=None):
+    _check(lib.msa_cache_fwd(ctypes.byref(c), _ptr(q), _ptr(cache), _ptr(block_table), _ptr(chunks), _ptr(sel),
+                             _ptr(o), _ptr(lse), _ptr(d_status), _stream(stream)),
+           "msa_cache_fwd")
+
+
+class Cache:
+    """A batch of requests over one 4-bit paged cache: owns the pages, the free
+    ring, the block table, the index pool and the tables of the current step.
+
+    One step, with the new tokens' tensors packed request after request:
+
+        cache.step(new_lens, tokens)     # int32 [R] on the device; tokens = rows of the tensors below
+        cache.append(k, v, k_index)
+        sel = cache.select(q_index)
+        o, lse = cache.forward(q, sel)
+
+    new_lens[r] is 0 for an idle request and -1 for one that gives its pages
+    back.  The lengths stay on the device, nothing synchronises, and the
+    buffers of a given number of rows are made once, so a step whose shapes do
+    not change can be captured into a CUDA graph after one eager run.  The
+    step's tensors (slot_map, positions, chunks, cu_tokens) and the outputs
+    belong to the object and hold until the next step of as many rows.  Calls on
+    one object run in the order of their streams: keep them on one stream, or
+    order the streams.  check_status() synchronises and raises on a device
+    error.
+    """
+
+    def __init__(self, num_requests, num_pages, max_blocks, num_q_heads, topk, block_size=BLOCK,
+                 softmax_scale=HEAD_DIM ** -0.5, k_exp=0, v_exp=0, index_keys=True, device="cuda"):
+        import torch
+        self.device = torch.empty(0, device=device).device
+        self._args = dict(num_requests=num_requests, num_pages=num_pages, max_blocks=max_blocks,
+                          num_q_heads=num_q_heads, topk=topk, softmax_scale=softmax_scale, block_size=block_size,
+                          k_exp=k_exp, v_exp=v_exp)
+        c = make_cache_problem(token_cap=1, chunk_cap=1, **self._args)
+        R, P, M, H, B = c.num_requests, c.num_pages, c.max_blocks, c.num_kv_heads, c.block_size
+        i32, dev = torch.int32, self.device
+        self.cache = new_cache(c, dev)
+        self.block_table = torch.zeros((R, M), dtype=i32, device=dev)
+        self.seq_lens = torch.zeros(R, dtype=i32, device=dev)
+        self.free_ring = torch.arange(P, dtype=i32, device=dev)
+        self.ring = torch.tensor([0, P], dtype=i32, device=dev)
+        self.cu_tokens = torch.zeros(R + 1, dtype=i32, device=dev)
+        self.status = torch.zeros(4, dtype=i32, device=dev)
+        self.index_tail = self.index_pool = None
+        if index_keys:
+            self.index_tail = torch.zeros((R, 2, B, H, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+            self.index_pool = torch.zeros((P, H, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+        self._steps = {}
+        self._now = None
+
+    def _tables(self, tokens):
+        """The problem and buffers of steps with this many token rows, made once."""
+        import torch
+        t = self._steps.get(tokens)
+        if t is None:
+            c = make_cache_problem(token_cap=tokens, **self._args)
+            if msa_cache_bytes(c) == 0:
+                raise MSAError(MSA_ERR_INVALID_ARGUMENT, "Cache.step")
+            H, dev = c.num_kv_heads, self.device
+            t = dict(c=c, slot_map=torch.full((tokens,), -1, dtype=torch.int64, device=dev),
+                     positions=torch.full((tokens,), -1, dtype=torch.int32, device=dev),
+                     chunks=torch.full((c.chunk_cap, MSA_CHUNK_COLS), -1, dtype=torch.int32, device=dev),
+                     sel=torch.full((H, c.chunk_cap, c.topk), -1, dtype=torch.int32, device=dev),
+                     o=torch.zeros((tokens, c.num_q_heads, HEAD_DIM), dtype=torch.bfloat16, device=dev),
+                     lse=torch.full((tokens, c.num_q_heads), -math.inf, dtype=torch.float32, device=dev))
+            self._steps[tokens] = t
+        return t
+
+    def _call(self, fn, *args, stream=None):
+        import torch
+        with torch.cuda.device(self.device):
+            fn(*args, self.status, stream)
+
+    def _need(self, name, x, shape, dtype):
+        import torch
+        if not isinstance(x, torch.Tensor) or x.dtype != dtype or tuple(x.shape) != tuple(shape) \
+                or x.device != self.device or not x.is_contiguous():
+            raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {tuple(shape)} on {self.device}")
+
+    def _step_tables(self):
+        if self._now is None:
+            raise RuntimeError("Cache.step comes first")
+        return self._now
+
+    def step(self, new_lens, tokens, stream=None):
+        """msa_cache_step: advances the lengths and lays out `tokens` token rows."""
+        import torch
+        self._need("new_lens", new_lens, (self._args["num_requests"],), torch.int32)
+        t = self._now = self._tables(int(tokens))
+        self.slot_map, self.positions, self.chunks = t["slot_map"], t["positions"], t["chunks"]
+        self._call(msa_cache_step, t["c"], new_lens, self.seq_lens, self.ring, self.free_ring, self.block_table,
+                   self.seq_lens, self.ring, self.cu_tokens, self.slot_map, self.positions, self.chunks,
+                   stream=stream)
+
+    def append(self, k, v, k_index=None, stream=None):
+        """msa_cache_append of the step's rows; k_index is needed where the cache keeps index keys."""
+        import torch
+        c = self._step_tables()["c"]
+        shape = (c.token_cap, c.num_kv_heads, HEAD_DIM)
+        for name, x in (("k", k), ("v", v)) + ((("k_index", k_index),) if self.index_pool is not None else ()):
+            self._need(name, x, shape, torch.bfloat16)
+        if self.index_pool is None and k_index is not None:
+            raise ValueError("k_index: this cache keeps no index keys")
+        self._call(msa_cache_append, c, k, v, k_index, self.slot_map, self.cu_tokens, self.chunks, self.cache,
+                   self.index_tail, self.index_pool, stream=stream)
+
+    def select(self, q_index, stream=None):
+        """msa_cache_select: the selection int32 [Hkv, chunk rows, topk] of the step's chunks."""
+        import torch
+        t = self._step_tables()
+        c = t["c"]
+        if self.index_pool is None:
+            raise RuntimeError("this cache keeps no index keys")
+        self._need("q_index", q_index, (c.token_cap, c.num_kv_heads, HEAD_DIM), torch.bfloat16)
+        self._call(msa_cache_select, c, q_index, self.index_pool, self.block_table, self.chunks, t["sel"],
+                   stream=stream)
+        return t["sel"]
+
+    def forward(self, q, sel, stream=None):
+        """msa_cache_fwd: (o bf16 [tokens, Hq, 128], lse fp32 [tokens, Hq])."""
+        import torch
+        t = self._step_tables()
+        c = t["c"]
+        self._need("q", q, (c.token_cap, c.num_q_heads, HEAD_DIM), torch.bfloat16)
+        self._need("sel", sel, (c.num_kv_heads, c.chunk_cap, c.topk), torch.int32)
+        self._call(msa_cache_fwd, c, q, self.cache, self.block_table, self.chunks, sel, t["o"], t["lse"],
+                   stream=stream)
+        return t["o"], t["lse"]
+
+    def read(self, slots, stream=None):
+        """msa_cache_read: bf16 (k, v) [n, Hkv, 128] of any slots; rows of slot -1 are 0."""
+        import torch
+        self._need("slots", slots, (slots.numel(),), torch.int64)
+        c = make_cache_problem(token_cap=max(1, slots.numel()), chunk_cap=1, **self._args)
+        k = torch.zeros((slots.numel(), c.num_kv_heads, HEAD_DIM), dtype=torch.bfloat16, device=self.device)
+        v = torch.zeros_like(k)
+        if slots.numel():
+            self._call(msa_cache_read, c, slots, self.cache, k, v, stream=stream)
+        return k, v
+
+    def check_status(self):
+        code = int(self.status[0].item())
+        if code != MSA_OK:
+            raise MSAError(code, "device status")

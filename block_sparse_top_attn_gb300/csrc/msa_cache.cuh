@@ -1,0 +1,70 @@
+// The 4-bit paged key/value cache: tile layout, decoding and argument checks
+// shared by the serving kernels.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "msa_common.cuh"
+#include "msa_host.cuh"
+
+namespace msa {
+namespace cache {
+
+constexpr int kTile = 64;         // tokens of a cache tile
+constexpr int kRowBytes = 64;     // 128 codes of 4 bits
+constexpr int kScales = 8;        // e4m3 scales of a row, one per 16 dims
+constexpr uint32_t OFF_KC = 0, OFF_KS = 4096, OFF_VC = 4608, OFF_VS = 8704;
+constexpr uint32_t kTileBytes = MSA_CACHE_TILE_BYTES;
+constexpr int kMaxRequests = 8192;
+constexpr int kMaxBlocks = kMaxRows;
+constexpr int kMaxCount = 1 << 24;  // pages, token rows, chunk rows
+constexpr int kMaxHeads = 1024;
+constexpr int kMaxExp = 32;
+
+// Byte of unit `u` (8 bytes: one scale group) of token `t` in the V code
+// plane.  The XOR spreads the four token rows that a quad of an MMA B fragment
+// reads (t, t + 4, t + 8, t + 12, the same unit) over all 32 banks.
+MSA_DEV uint32_t v_code_offset(int t, int u) { return (uint32_t)(t * kRowBytes + u * 8) ^ (uint32_t)((t & 12) << 3); }
+
+// Two e2m1 codes (the low and high half of a byte) as fp16 values, exact.
+MSA_DEV void e2m1x8_to_half(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+// Two e4m3 scales as fp16 values, exact (NaN stays NaN).
+MSA_DEV uint32_t e4m3x2_to_half(uint32_t two) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 s;\n\tcvt.u16.u32 s, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, s;\n\t}" : "=r"(h) : "r"(two));
+  return h;
+}
+// A code has 2 significant bits and a scale 4, so their product (magnitudes
+// from 2^-10 to 2688) is exact in fp16.
+MSA_DEV uint32_t mul_half2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// 2^e for -126 <= e <= 127.
+__host__ __device__ __forceinline__ float exp2i(int e) {
+  union { uint32_t u; float f; } x;
+  x.u = (uint32_t)(e + 127) << 23;
+  return x.f;
+}
+
+MSA_DEV int64_t tile_index(int64_t page, int head, int heads, int tiles_per_page, int tile) {
+  return (page * heads + head) * tiles_per_page + tile;
+}
+
+int check_cache_problem(const msa_cache_problem* p);
+
+}  // namespace cache
+}  // namespace msa

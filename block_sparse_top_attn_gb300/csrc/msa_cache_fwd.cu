@@ -1,0 +1,491 @@
+// Attention of a serving step's new tokens over the selected blocks of the
+// 4-bit paged cache: per (query token, KV head) the 16 query heads attend the
+// keys of the chunk's selected blocks at or before the token,
+//   s_j = scale q k_j,  o = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),
+// in one pass with a running maximum.
+//
+// Bound: a token and KV head read 144 bytes per key and do 8192 operations on
+// them, 57 per byte, so the cache's bytes set the floor.  The 16 heads of one
+// KV head are the 16 rows of an m16n8k16 MMA, which leaves no row unused; a
+// 128-row tcgen05 tile would hold one token's 16 rows and 112 empty ones.
+// Codes become fp16 in registers, in the layout of the MMA's B fragment, and
+// never go back to shared memory.
+//
+// A CTA takes one (token, KV head) and, in a cluster, a share of its key
+// tiles.  A producer warp compacts the selection, looks up the pages and
+// copies whole 9 KB tiles (codes and scales of 64 keys are contiguous) into a
+// ring; each of four consumer warps takes 16 keys of every tile, with its own
+// running maximum and output, and nothing is shared until the tiles are done.
+// The partial results of the warps, then those of the cluster's CTAs (through
+// distributed shared memory), are joined in a fixed order.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "msa_cache.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace msa {
+namespace cache {
+
+constexpr int kConsumers = 4;
+constexpr int kFwdThreads = 32 * (kConsumers + 1);
+constexpr int kStages = 6;
+constexpr int kMaxTiles = 64;   // 64-key tiles of an item: up to 32 blocks of 128 keys
+// Weights are p = 2^(s - m) with m kLift below the running maximum, which moves
+// when a score passes it by kTau: 2^kLift <= the largest p < 2^(kLift + kTau),
+// inside fp16's range, and a weight loses bits to fp16's subnormals only below
+// 2^-(14 + kLift) of the largest.
+constexpr float kTau = 8.f, kLift = 7.f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct FwdCacheArgs {
+  const uint16_t* q;
+  const uint8_t* cache;
+  const int32_t *block_table, *chunks, *sel;
+  uint16_t* o;
+  float* lse;
+  int R, P, M, B, T, NC, H, K;
+  int slots;         // token slots of a chunk in the grid
+  float scale_log2;  // softmax scale * 2^k_exp * log2 e
+  float v_mul;       // 2^v_exp
+  int32_t* status;
+};
+
+struct FwdShared {
+  alignas(128) uint8_t ring[kStages][kTileBytes];  // reused for the partial outputs
+  alignas(8) uint64_t full[kStages], empty[kStages];
+  int64_t tile[kMaxTiles];   // tile index in the cache
+  int32_t key0[kMaxTiles];   // position of its first key
+  int32_t ntiles;            // of this CTA
+  int32_t skip;              // the item is refused, or a wait gave up: no CTA of the cluster writes
+  float m[kConsumers][16], l[kConsumers][16];
+  float cm[16], cl[16];      // joined over the warps
+};
+static_assert(sizeof(float) * kConsumers * 16 * 128 <= kStages * kTileBytes, "partials fit the ring");
+
+MSA_DEV void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+      " {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+MSA_DEV uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+MSA_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// A row of q as fp16 A-fragment words: the lane's 32 dims (32 t .. 32 t + 31),
+// scaled by a power of two that puts the row's largest element at 2^14, so
+// that a bf16 element loses bits only below 2^-31 of the largest.  Returns the
+// inverse power.
+MSA_DEV float load_q_row(const uint16_t* src, uint32_t (&w)[16]) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(src) + i);
+    w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) amax = max(amax, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  const int e = max((int)(amax >> 7), 15);  // biased exponent; 15: rows of tiny values keep a normal inverse
+  const float mul = __uint_as_float((uint32_t)(268 - e) << 23);
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    w[i] = pack_half2(__uint_as_float(w[i] << 16) * mul, __uint_as_float(w[i] & 0xFFFF0000u) * mul);
+  return __uint_as_float((uint32_t)(e - 14) << 23);
+}
+
+__global__ void __launch_bounds__(kFwdThreads) fwd_cache_kernel(FwdCacheArgs a) {
+  extern __shared__ __align__(128) uint8_t s_raw[];
+  FwdShared& s = *reinterpret_cast<FwdShared*>(s_raw);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int item = blockIdx.x / ranks, h = blockIdx.y;
+  const int g = item / a.slots, slot = item % a.slots;
+  // the same for every CTA of the cluster, so all of them leave here or none
+  const int4 c = reinterpret_cast<const int4*>(a.chunks)[g];
+  if (c.x < 0 || slot >= c.z) return;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], kConsumers);
+    }
+    fence_mbar_init();
+  }
+  if (warp == kConsumers) {
+    // the chunk's tiles: every selected block gives the tiles that start at or
+    // before the chunk's last token; rank takes every ranks-th
+    bool good = !status_bad(a.status) && c.x < a.R && c.z <= kChunk && c.y >= 0 && c.y <= a.T - c.z && c.w >= 0 &&
+                c.w % kChunk + c.z <= kChunk && c.w / a.B < a.M;
+    int code = MSA_ERR_INVALID_CACHE;
+    int b = -1, page = 0, ntl = 0;
+    if (good && lane < a.K) b = a.sel[((int64_t)h * a.NC + g) * a.K + lane];
+    if (good) {
+      const bool far = b >= 0 && b > c.w / a.B;
+      const unsigned same = __match_any_sync(0xffffffffu, b);
+      if (__any_sync(0xffffffffu, far || (b >= 0 && __popc(same) > 1))) {
+        good = false;
+        code = MSA_ERR_INVALID_SELECTION;
+      }
+    }
+    if (good) {
+      if (b >= 0) {
+        page = a.block_table[(int64_t)c.x * a.M + b];
+        ntl = a.B == 128 && b * 128 + 64 <= c.w + c.z - 1 ? 2 : 1;
+      }
+      if (__any_sync(0xffffffffu, b >= 0 && (page < 0 || page >= a.P))) good = false;
+    }
+    int x = ntl;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    const int total = __shfl_sync(0xffffffffu, x, 31);
+    if (good) {
+      for (int i = 0; i < ntl; ++i) {
+        const int at = x - ntl + i;
+        if (at % ranks == rank) {
+          s.tile[at / ranks] = tile_index(page, h, a.H, a.B / kTile, i);
+          s.key0[at / ranks] = b * a.B + i * kTile;
+        }
+      }
+    } else if (lane == 0) {
+      set_status(a.status, code);
+    }
+    if (lane == 0) {
+      s.ntiles = good ? (total - rank + ranks - 1) / ranks : 0;
+      s.skip = !good;
+    }
+  }
+  __syncthreads();
+  const int ntiles = s.ntiles;
+  if (ranks == 1 && s.skip) return;
+  for (int tok = slot; tok < c.z; tok += a.slots) {
+    const int qpos = c.w + tok;
+    const int64_t row0 = (int64_t)(c.y + tok) * a.H * kGroup + h * kGroup;
+    const int done = (tok - slot) / a.slots * ntiles;  // tiles of earlier tokens
+    float o[16][4];
+    float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
+    bool ok = true;
+    int issued = 0;  // copies so far (producer)
+    if (warp == kConsumers) {
+      if (lane == 0) {
+        for (int j = 0; j < ntiles; ++j) {
+          const int n = done + j, st = n % kStages, lap = n / kStages;
+          if (lap > 0 && !(ok = mbar_wait(&s.empty[st], (lap - 1) & 1, a.status))) break;
+          mbar_arrive_expect_tx(&s.full[st], kTileBytes);
+          bulk_load(s.ring[st], a.cache + s.tile[j] * kTileBytes, kTileBytes, &s.full[st]);
+          issued = n + 1;
+        }
+      }
+      __syncwarp();
+    } else {
+      const int gid = lane >> 2, t = lane & 3;
+      uint32_t q0[16], q1[16];
+      const uint16_t* src = a.q + (row0 + gid) * 128 + 32 * t;
+      const float sc0 = load_q_row(src, q0) * a.scale_log2;
+      const float sc1 = load_q_row(src + 8 * 128, q1) * a.scale_log2;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+      for (int j = 0; j < ntiles; ++j) {
+        const int n = done + j, st = n % kStages;
+        ok = __all_sync(0xffffffffu, mbar_wait(&s.full[st], (n / kStages) & 1, a.status));
+        if (!ok) break;
+        const uint8_t* tile = s.ring[st];
+        const int k0 = s.key0[j] + 16 * warp;  // position of the warp's first key
+        if (k0 <= qpos) {
+          // S = Q K^T: column n of n-tile jj is key 4 (n >> 1) + 2 jj + (n & 1),
+          // k-step ks contracts dims 32 t + 4 ks .. + 3 of each lane t
+          float sv[2][4];
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj) {
+            const int key = 16 * warp + 4 * (gid >> 1) + 2 * jj + (gid & 1);
+            const uint4 kc = *reinterpret_cast<const uint4*>(tile + OFF_KC + key * kRowBytes + t * 16);
+            const uint32_t sh =
+                e4m3x2_to_half(*reinterpret_cast<const uint16_t*>(tile + OFF_KS + key * kScales + 2 * t));
+            const uint32_t s0 = __byte_perm(sh, sh, 0x1010), s1 = __byte_perm(sh, sh, 0x3232);
+            const uint32_t w[4] = {kc.x, kc.y, kc.z, kc.w};
+            sv[jj][0] = sv[jj][1] = sv[jj][2] = sv[jj][3] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t hk[4];
+              e2m1x8_to_half(w[i], hk);
+              const uint32_t sc = i < 2 ? s0 : s1;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) hk[e] = mul_half2(hk[e], sc);
+              mma_f16(sv[jj], q0[4 * i], q1[4 * i], q0[4 * i + 1], q1[4 * i + 1], hk[0], hk[1]);
+              mma_f16(sv[jj], q0[4 * i + 2], q1[4 * i + 2], q0[4 * i + 3], q1[4 * i + 3], hk[2], hk[3]);
+            }
+          }
+          // the lane's keys: 4 t + 2 jj + e; rows gid and gid + 8
+          uint32_t vs = *reinterpret_cast<const uint32_t*>(tile + OFF_VS + gid * kTile + 16 * warp + 4 * t);
+          float bm0 = -CUDART_INF_F, bm1 = -CUDART_INF_F;
+          const int left = qpos - k0 - 4 * t;  // keys 0 .. left of the lane's four may be attended
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const bool in = 2 * jj + e <= left;
+              sv[jj][e] = in ? sv[jj][e] * sc0 : -CUDART_INF_F;
+              sv[jj][2 + e] = in ? sv[jj][2 + e] * sc1 : -CUDART_INF_F;
+              bm0 = fmaxf(bm0, sv[jj][e]);
+              bm1 = fmaxf(bm1, sv[jj][2 + e]);
+            }
+          // keys that may not be attended hold anything: a zero scale makes
+          // their values zero (a code alone is always finite)
+          if (left < 3) vs = left < 0 ? 0u : vs & (0xFFFFFFFFu >> (8 * (3 - left)));
+          bm0 = fmaxf(bm0, __shfl_xor_sync(0xffffffffu, bm0, 1));
+          bm1 = fmaxf(bm1, __shfl_xor_sync(0xffffffffu, bm1, 1));
+          bm0 = fmaxf(bm0, __shfl_xor_sync(0xffffffffu, bm0, 2));
+          bm1 = fmaxf(bm1, __shfl_xor_sync(0xffffffffu, bm1, 2));
+          const bool up0 = bm0 > m[0] + (kLift + kTau), up1 = bm1 > m[1] + (kLift + kTau);
+          if (__any_sync(0xffffffffu, up0 || up1)) {
+            const float al0 = up0 ? ex2_approx(m[0] + kLift - bm0) : 1.f;
+            const float al1 = up1 ? ex2_approx(m[1] + kLift - bm1) : 1.f;
+            if (up0) m[0] = bm0 - kLift;
+            if (up1) m[1] = bm1 - kLift;
+            l[0] *= al0;
+            l[1] *= al1;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              o[i][0] *= al0;
+              o[i][1] *= al0;
+              o[i][2] *= al1;
+              o[i][3] *= al1;
+            }
+          }
+          const float m0 = m[0] == -CUDART_INF_F ? 0.f : m[0], m1 = m[1] == -CUDART_INF_F ? 0.f : m[1];
+          uint32_t pa[4];
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj) {
+            const float p0 = ex2_approx(sv[jj][0] - m0), p1 = ex2_approx(sv[jj][1] - m0);
+            const float p2 = ex2_approx(sv[jj][2] - m1), p3 = ex2_approx(sv[jj][3] - m1);
+            l[0] += p0 + p1;
+            l[1] += p2 + p3;
+            // fp16 keeps 11 bits of a weight, 3 more than bf16
+            pa[2 * jj] = pack_half2(p0, p1);
+            pa[2 * jj + 1] = pack_half2(p2, p3);
+          }
+          // O += P V: column n = gid of n-tile j is dim 16 gid + j, so a lane's
+          // V words are one scale group of its four keys
+          uint32_t vw[4][2];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint2 x =
+                *reinterpret_cast<const uint2*>(tile + OFF_VC + v_code_offset(16 * warp + 4 * t + e, gid));
+            vw[e][0] = x.x;
+            vw[e][1] = x.y;
+          }
+          const uint32_t s01 = e4m3x2_to_half(vs & 0xFFFFu), s23 = e4m3x2_to_half(vs >> 16);
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            // bytes of two keys' codes at one dim, even and odd dims apart
+            constexpr uint32_t LO = 0x0F0F0F0Fu;
+            uint32_t ev01[4], od01[4], ev23[4], od23[4];
+            e2m1x8_to_half((vw[0][w] & LO) | ((vw[1][w] << 4) & ~LO), ev01);
+            e2m1x8_to_half(((vw[0][w] >> 4) & LO) | (vw[1][w] & ~LO), od01);
+            e2m1x8_to_half((vw[2][w] & LO) | ((vw[3][w] << 4) & ~LO), ev23);
+            e2m1x8_to_half(((vw[2][w] >> 4) & LO) | (vw[3][w] & ~LO), od23);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              mma_f16(o[8 * w + 2 * i], pa[0], pa[1], pa[2], pa[3], mul_half2(ev01[i], s01), mul_half2(ev23[i], s23));
+              mma_f16(o[8 * w + 2 * i + 1], pa[0], pa[1], pa[2], pa[3], mul_half2(od01[i], s01),
+                      mul_half2(od23[i], s23));
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.empty[st]);
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      }
+    }
+    // every tile has landed and been read; after a wait that gave up, copies
+    // may be in flight: they land before the CTA's shared memory is let go
+    const bool bad = __syncthreads_or(!ok);
+    if (bad && warp == kConsumers && lane == 0) {
+      for (int n = max(issued - kStages, 0); n < issued; ++n)
+        mbar_wait(&s.full[n % kStages], (n / kStages) & 1, a.status);
+      s.skip = 1;
+    }
+    // join the warps: partial outputs in the ring, [warp][16 rows][128 dims],
+    // 16-byte units XORed by row so that neither side conflicts
+    float* part = reinterpret_cast<float*>(&s.ring[0][0]);
+    if (warp < kConsumers && !bad) {
+      const int gid = lane >> 2, t = lane & 3;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = gid + 8 * r;
+        if (t == 0) {
+          s.m[warp][row] = m[r];
+          s.l[warp][row] = l[r];
+        }
+        // dims 32 t + 16 e + j of the row
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int unit = 8 * t + 4 * e + i;
+            *reinterpret_cast<float4*>(part + (warp * 16 + row) * 128 + 4 * (unit ^ (row & 7))) =
+                make_float4(o[4 * i][2 * r + e], o[4 * i + 1][2 * r + e], o[4 * i + 2][2 * r + e],
+                            o[4 * i + 3][2 * r + e]);
+          }
+      }
+    }
+    __syncthreads();
+    bool skip = bad;
+    if (warp < kConsumers && !bad) {
+      // thread: one row, 16 dims (units 4 cg .. 4 cg + 3)
+      const int row = tid >> 3, cg8 = tid & 7;
+      float mm = s.m[0][row];
+#pragma unroll
+      for (int w = 1; w < kConsumers; ++w) mm = fmaxf(mm, s.m[w][row]);
+      float ll = 0.f, acc[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kConsumers; ++w) {
+        const float wm = s.m[w][row];
+        const float f = wm == -CUDART_INF_F ? 0.f : ex2_approx(wm - mm);
+        ll += f * s.l[w][row];
+        if (wm != -CUDART_INF_F || s.l[w][row] != 0.f) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 x =
+                *reinterpret_cast<const float4*>(part + (w * 16 + row) * 128 + 4 * ((4 * cg8 + i) ^ (row & 7)));
+            acc[4 * i] += f * x.x;
+            acc[4 * i + 1] += f * x.y;
+            acc[4 * i + 2] += f * x.z;
+            acc[4 * i + 3] += f * x.w;
+          }
+        }
+      }
+      if (ranks == 1) {
+        const float inv = ll == 0.f ? 0.f : a.v_mul / ll;  // a NaN stays one
+        uint4* dst = reinterpret_cast<uint4*>(a.o + (row0 + row) * 128 + 16 * cg8);
+        dst[0] = make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                            pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+        dst[1] = make_uint4(pack_bf16x2(acc[8] * inv, acc[9] * inv), pack_bf16x2(acc[10] * inv, acc[11] * inv),
+                            pack_bf16x2(acc[12] * inv, acc[13] * inv), pack_bf16x2(acc[14] * inv, acc[15] * inv));
+        if (cg8 == 0) a.lse[row0 + row] = ll == 0.f ? -CUDART_INF_F : (mm + log2f(ll)) * kLn2;
+      } else {
+        // this CTA's part of the cluster's result, in place of warp 0's
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float4*>(part + row * 128 + 4 * ((4 * cg8 + i) ^ (row & 7))) =
+              make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+        if (cg8 == 0) {
+          s.cm[row] = mm;
+          s.cl[row] = ll;
+        }
+      }
+    }
+    if (ranks > 1) {
+      cluster.sync();
+      for (int r = 0; r < ranks; ++r) skip |= *cluster.map_shared_rank(&s.skip, r) != 0;
+      // rank joins rows rank * 16 / ranks ..: a warp takes a row, a lane 4 dims
+      const int rows = 16 / ranks;
+      for (int i = warp; i < rows && !skip; i += kConsumers + 1) {
+        const int row = rank * rows + i, unit = lane;
+        float mm = -CUDART_INF_F;
+        for (int r = 0; r < ranks; ++r) mm = fmaxf(mm, *cluster.map_shared_rank(&s.cm[row], r));
+        float ll = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < ranks; ++r) {
+          const float wm = *cluster.map_shared_rank(&s.cm[row], r), wl = *cluster.map_shared_rank(&s.cl[row], r);
+          const float f = wm == -CUDART_INF_F ? 0.f : ex2_approx(wm - mm);
+          ll += f * wl;
+          const float4 x = *reinterpret_cast<const float4*>(
+              cluster.map_shared_rank(part + row * 128 + 4 * (unit ^ (row & 7)), r));
+          if (wm != -CUDART_INF_F || wl != 0.f) {
+            acc[0] += f * x.x;
+            acc[1] += f * x.y;
+            acc[2] += f * x.z;
+            acc[3] += f * x.w;
+          }
+        }
+        const float inv = ll == 0.f ? 0.f : a.v_mul / ll;
+        *reinterpret_cast<uint2*>(a.o + (row0 + row) * 128 + 4 * unit) =
+            make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+        if (unit == 0) a.lse[row0 + row] = ll == 0.f ? -CUDART_INF_F : (mm + log2f(ll)) * kLn2;
+      }
+      cluster.sync();  // the peers' parts have been read
+    }
+    if (tok + a.slots < c.z && !skip) {
+      // the ring was written by the join: order that before the next copies
+      fence_async_smem();
+      __syncthreads();
+    }
+    if (skip) return;  // the same in every CTA of the cluster
+  }
+}
+
+}  // namespace cache
+}  // namespace msa
+
+using namespace msa;
+
+extern "C" int msa_cache_fwd(const msa_cache_problem* p, const uint16_t* q, const uint8_t* kv_cache,
+                             const int32_t* block_table, const int32_t* chunks, const int32_t* sel, uint16_t* o,
+                             float* lse, int32_t* d_status, void* stream) {
+  int rc = cache::check_cache_problem(p);
+  if (rc) return rc;
+  const void* ptrs[] = {q, kv_cache, block_table, chunks, sel, o, lse, d_status};
+  for (const void* x : ptrs)
+    if (!x || !aligned16(x)) return MSA_ERR_INVALID_ARGUMENT;
+  if ((rc = check_device_current())) return rc;
+  int32_t sms = 0;
+  if ((rc = sm_count_current(&sms))) return rc;
+  cache::FwdCacheArgs a;
+  a.q = q; a.cache = kv_cache; a.block_table = block_table; a.chunks = chunks; a.sel = sel; a.o = o; a.lse = lse;
+  a.R = p->num_requests; a.P = p->num_pages; a.M = p->max_blocks; a.B = p->block_size; a.T = p->token_cap;
+  a.NC = p->chunk_cap; a.H = p->num_kv_heads; a.K = p->topk;
+  a.scale_log2 = p->softmax_scale * cache::exp2i(p->k_exp) * cache::kLog2e;
+  a.v_mul = cache::exp2i(p->v_exp);
+  a.status = d_status;
+  // Token slots of a chunk: its mean number of tokens, at most 8.  A chunk
+  // with more tokens than slots takes them in turn.
+  a.slots = (int)((p->token_cap + (int64_t)p->chunk_cap - 1) / p->chunk_cap);
+  if (a.slots > kChunk) a.slots = kChunk;
+  const int64_t items = (int64_t)p->chunk_cap * a.slots;
+  // CTAs of a cluster share an item's tiles while the items alone leave SMs
+  // idle (three CTAs fit an SM).
+  const int tiles = p->topk * (p->block_size / cache::kTile);
+  int ranks = 1;
+  while (ranks < 8 && ranks * 2 <= tiles && items * p->num_kv_heads * ranks * 2 <= 2 * sms) ranks *= 2;
+  if (items * ranks > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
+  if ((rc = cuda_status(cudaFuncSetAttribute(cache::fwd_cache_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)sizeof(cache::FwdShared)))))
+    return rc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items * ranks), (unsigned)p->num_kv_heads);
+  cfg.blockDim = dim3(cache::kFwdThreads);
+  cfg.dynamicSmemBytes = sizeof(cache::FwdShared);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)ranks;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, cache::fwd_cache_kernel, a));
+}

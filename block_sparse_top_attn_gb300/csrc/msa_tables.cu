@@ -1007,6 +1007,7 @@ const char* msa_status_string(int s) {
     case MSA_ERR_CUDA: return "CUDA error";
     case MSA_ERR_INVALID_DOCUMENTS: return "inconsistent document offsets";
     case MSA_ERR_SCRATCH_TOO_SMALL: return "problem needs more scratch than the fixed no-allocation array holds";
+    case MSA_ERR_INVALID_CACHE: return "inconsistent cache tables, lengths or slots";
     default: return "unknown status";
   }
 }

@@ -50,7 +50,8 @@ enum {
   MSA_ERR_TIMEOUT = 6,            /* a bounded device wait expired                       */
   MSA_ERR_CUDA = 7,               /* a CUDA launch or runtime call failed                */
   MSA_ERR_INVALID_DOCUMENTS = 8,  /* cu_seqlens / kv_doc_starts inconsistent (device)    */
-  MSA_ERR_SCRATCH_TOO_SMALL = 9   /* problem exceeds the no-allocation scratch array     */
+  MSA_ERR_SCRATCH_TOO_SMALL = 9,  /* problem exceeds the no-allocation scratch array     */
+  MSA_ERR_INVALID_CACHE = 10      /* cache tables, lengths or slots inconsistent (device) */
 };
 
 /* Problem description.  Mirrors run_backward's tensor contract
@@ -314,6 +315,183 @@ int msa_plan_forward(const msa_problem* p, const int32_t* sel, int32_t* schedule
 int msa_fwd_planned(const msa_problem* p, const uint16_t* q, const uint16_t* k, const uint16_t* v,
                     const int32_t* sel, const int32_t* scheduler_metadata, uint16_t* o, float* lse,
                     int32_t* d_status, void* ws, size_t ws_bytes, void* stream);
+
+/* -------------------------------------------------------------------------
+ * Serving: a paged key/value cache in 4 bits and the operators over it.
+ *
+ * The pages describe the training pass only; these calls have no counterpart
+ * there.  They carry the same method to a serving step: a batch of requests,
+ * each with `past` cached tokens and some new ones, whose new tokens attend
+ * the top-k selected key blocks of their own request.  One step is
+ *   msa_cache_step    block table, slots and query chunks from the lengths,
+ *   msa_cache_append  the new tokens' K, V and index keys into the cache,
+ *   msa_cache_select  the key blocks of every query chunk,
+ *   msa_cache_fwd     attention over the selected blocks,
+ * each asynchronous on its stream, with fixed buffers and no workspace, so a
+ * step can be captured into a CUDA graph and replayed.  The step's tables are
+ * read on the device only: no call needs a length on the host.
+ *
+ * A page holds one key block of one cache (block_size tokens of every KV
+ * head).  Position p of request r lives in page block_table[r][p / B], at
+ * offset p % B; its slot is page * B + offset.  The new tokens of a request
+ * are cut into query chunks: tokens of equal position / 8, as in the training
+ * pass, so a chunk lies in one page.
+ *
+ * Cache layout, uint8 [num_pages, Hkv, B / 64, MSA_CACHE_TILE_BYTES]: per page
+ * and head, tiles of 64 tokens, each
+ *   K codes  [64 tokens][64 bytes]     at 0
+ *   K scales [64 tokens][8]            at 4096
+ *   V codes  [64 tokens][64 bytes]     at 4608, byte o of the plane stored at
+ *                                      o ^ ((token & 12) << 3)
+ *   V scales [8][64 tokens]            at 8704
+ * Byte i of a token's codes holds dims 2i (low half) and 2i + 1 (high half)
+ * as e2m1 (sign, two exponent bits, one mantissa bit: 0, 0.5, 1, 1.5, 2, 3,
+ * 4, 6; a zero is written without a sign); scale j is the e4m3 scale of dims 16j .. 16j + 15.  A K value is
+ * code * scale * 2^k_exp, a V value code * scale * 2^v_exp; without the
+ * power of two it is exact in fp16 and bf16.
+ * ------------------------------------------------------------------------- */
+
+/* num_requests   R, rows of the block table (batch slots), 1 .. 8192.
+ * num_pages      P, pages of the cache, 1 .. 2^24.
+ * max_blocks     M, block-table columns, 1 .. 49152; M * B tokens at most.
+ * num_q_heads    Hq = 16 * num_kv_heads; index heads = KV heads (<= 1024).
+ * head_dim 128.  block_size B: 64 or 128.  query_chunk 8.  topk 1 .. 32.
+ * token_cap      T, rows of the step's token tensors (new tokens fit in it;
+ *                rows behind the last new token are padding), 1 .. 2^24.
+ * chunk_cap      NC, rows of the step's chunk table, 1 .. 2^24.
+ * k_exp, v_exp   exponents of the cache's values, -32 .. 32: an e4m3 scale
+ *                spans 2^-9 .. 448, so groups whose largest element is below
+ *                0.09 * 2^exp lose precision and those above 2688 * 2^exp
+ *                saturate.  The same values in every call on one cache.
+ * softmax_scale  scale applied to q.k, > 0 and finite. */
+typedef struct {
+  int32_t num_requests;
+  int32_t num_pages;
+  int32_t max_blocks;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t block_size;
+  int32_t query_chunk;
+  int32_t topk;
+  int32_t token_cap;
+  int32_t chunk_cap;
+  int32_t k_exp;
+  int32_t v_exp;
+  float softmax_scale;
+} msa_cache_problem;
+
+enum { MSA_CACHE_TILE_BYTES = 9216 };
+/* Columns of a row of the step's chunk table: request, first token row, token
+ * count (1 .. 8), position of the first token.  A row with request -1 is
+ * padding. */
+enum { MSA_CHUNK_COLS = 4 };
+
+/* Bytes of the cache of p (0 if p is invalid). */
+size_t msa_cache_bytes(const msa_cache_problem* p);
+/* Rows of the chunk table that hold every chunk of any `tokens` new tokens of
+ * num_requests requests: min(tokens, tokens / 8 + 2 * num_requests). */
+int64_t msa_cache_chunk_bound(int64_t tokens, int64_t num_requests);
+
+/* Block table, slot map, positions and query chunks of one step, from the
+ * lengths on the device.
+ * new_lens      device int32 [R]: new tokens of each request, 0 for an idle
+ *               one, -1 for one that has finished and gives its pages back.
+ * seq_lens      device int32 [R]: cached tokens before the step.
+ * ring          device int32 [2]: first entry and count of the free pages in
+ *               free_ring.
+ * free_ring     device int32 [P] in/out: page ids in a ring.  New blocks take
+ *               pages from its front in (request, block) order; pages given
+ *               back join its end in the same order and are not handed out
+ *               in the same step.
+ * block_table   device int32 [R, M] in/out: only the entries of the step's
+ *               new blocks are written.
+ * seq_lens_out  device int32 [R] out: past + new, 0 for a finished request.
+ * ring_out      device int32 [2] out.  seq_lens_out and ring_out may be
+ *               seq_lens and ring themselves.
+ * cu_tokens     device int32 [R + 1] out: first token row of each request.
+ * slot_map      device int64 [T] out: slot of each new token, -1 for padding.
+ * positions     device int32 [T] out: its position, -1 for padding.
+ * chunks        device int32 [NC, 4] out (MSA_CHUNK_COLS), in token order,
+ *               -1 in every column of padding.
+ * *d_status: MSA_ERR_CAPACITY when the new tokens, their chunks, a request's
+ * blocks or the pages needed exceed T, NC, M or the free pages;
+ * MSA_ERR_INVALID_CACHE when a length or the ring is out of range.  Nothing
+ * is written then.  Deterministic. */
+int msa_cache_step(const msa_cache_problem* p, const int32_t* new_lens, const int32_t* seq_lens,
+                   const int32_t* ring, int32_t* free_ring, int32_t* block_table, int32_t* seq_lens_out,
+                   int32_t* ring_out, int32_t* cu_tokens, int64_t* slot_map, int32_t* positions,
+                   int32_t* chunks, int32_t* d_status, void* stream);
+
+/* Rounds K and V of the new tokens to 4 bits and writes them to their slots,
+ * and keeps the pooled index keys that msa_cache_select scores.
+ * Rounding, per token, head and 16 dims: scale = e4m3(max |x| * 2^-exp / 6),
+ * to nearest even, at most 448; code = e2m1(x * 2^-exp / scale), to nearest
+ * even, at most 6; a zero scale gives zeros.  A group that holds an infinity
+ * or a NaN reads back as NaN.
+ * k, v         device bf16 [T, Hkv, 128].
+ * slot_map     device int64 [T]; -1 leaves the row out.  A slot outside the
+ *              cache is left out and sets MSA_ERR_INVALID_CACHE.  A slot that
+ *              appears twice holds one of its rows, in part perhaps each.
+ * cache        device uint8, msa_cache_bytes(p).
+ * k_index      device bf16 [T, Hkv, 128], index key of each new token, or
+ *              NULL: cu_tokens, chunks, index_tail and index_pool are then
+ *              not used and may be NULL.
+ * cu_tokens, chunks  as msa_cache_step wrote them.
+ * index_tail   device bf16 [R, 2, B, Hkv, 128] in/out: index keys of each
+ *              request's incomplete block b, at [r][b & 1][position % B].
+ * index_pool   device bf16 [P, Hkv, 128] out: for each block that this call
+ *              completes, the mean of its tokens' index keys (fp32 sum in
+ *              token order, divided by B, rounded to bf16). */
+int msa_cache_append(const msa_cache_problem* p, const uint16_t* k, const uint16_t* v,
+                     const uint16_t* k_index, const int64_t* slot_map, const int32_t* cu_tokens,
+                     const int32_t* chunks, uint8_t* cache, uint16_t* index_tail, uint16_t* index_pool,
+                     int32_t* d_status, void* stream);
+
+/* The values that the cache holds, rounded to bf16 (exact but for results
+ * outside bf16's normal range): for a prefill over cached tokens, to move a
+ * request, or to look at the cache.
+ * slots  device int64 [T] (any slots, in any order); -1 leaves the row of k
+ *        and v as it was, a slot outside the cache does so too and sets
+ *        MSA_ERR_INVALID_CACHE.
+ * k, v   device bf16 [T, Hkv, 128] out. */
+int msa_cache_read(const msa_cache_problem* p, const int64_t* slots, const uint8_t* cache, uint16_t* k,
+                   uint16_t* v, int32_t* d_status, void* stream);
+
+/* Top-k key blocks of every query chunk of a step, by the rule of
+ * msa_select_topk: the chunk's index query is the mean of its new tokens'
+ * index queries, a block's key its row of index_pool, the score their fp32
+ * dot product summed in ascending dim order; the block that holds the chunk
+ * first, then the topk - 1 earlier ones with the highest scores (a tie goes
+ * to the lower block) by descending score, then -1.
+ * q_index      device bf16 [T, Hkv, 128].
+ * index_pool   device bf16 [P, Hkv, 128]: every block before a chunk's own is
+ *              complete, so its row is there.
+ * block_table, chunks  as msa_cache_step wrote them.
+ * sel          device int32 [Hkv, NC, topk] out; rows of padding chunks are
+ *              left as they were.
+ * Deterministic; a NaN score may take any rank, the selection stays valid. */
+int msa_cache_select(const msa_cache_problem* p, const uint16_t* q_index, const uint16_t* index_pool,
+                     const int32_t* block_table, const int32_t* chunks, int32_t* sel, int32_t* d_status,
+                     void* stream);
+
+/* Attention of the new tokens over the selected blocks of the cache: for each
+ * query row, softmax(scale * q k^T) over the keys of its chunk's selected
+ * blocks at or before its own position, times V.  The new tokens' own keys
+ * must be in the cache (msa_cache_append first).
+ * q            device bf16 [T, Hq, 128].
+ * sel          device int32 [Hkv, NC, topk]: blocks of the chunk's request,
+ *              negative for an empty slot; distinct, and none behind the
+ *              chunk's own block (MSA_ERR_INVALID_SELECTION otherwise, and
+ *              the chunk's rows of that head are left as they were).
+ * o            device bf16 [T, Hq, 128] out;  lse device fp32 [T, Hq] out
+ *              (natural log).  A row that attends no key has o = 0 and lse =
+ *              -inf.  Rows that no chunk covers are left as they were.
+ * Cache bytes of keys that no query may attend may hold anything.
+ * Deterministic. */
+int msa_cache_fwd(const msa_cache_problem* p, const uint16_t* q, const uint8_t* cache,
+                  const int32_t* block_table, const int32_t* chunks, const int32_t* sel, uint16_t* o,
+                  float* lse, int32_t* d_status, void* stream);
 
 /* Self-test of the bounded device waits (no counterpart in the pages).
  * Launches one small kernel that waits, with the same bounded mbarrier wait
