@@ -493,37 +493,52 @@ def new_cache(c: msa_cache_problem, device="cuda"):
                        dtype=torch.uint8, device=device)
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream):
+    """The stream's handle; the current stream's without building a Stream object (a step is a few launches of a few
+    microseconds each)."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
 def msa_cache_step(c, new_lens, seq_lens, ring, free_ring, block_table, seq_lens_out, ring_out, cu_tokens, slot_map,
                    positions, chunks, d_status, stream=None):
-    _check(lib.msa_cache_step(ctypes.byref(c), _ptr(new_lens), _ptr(seq_lens), _ptr(ring), _ptr(free_ring),
-                              _ptr(block_table), _ptr(seq_lens_out), _ptr(ring_out), _ptr(cu_tokens),
-                              _ptr(slot_map), _ptr(positions), _ptr(chunks), _ptr(d_status), _stream(stream)),
+    _check(lib.msa_cache_step(c, new_lens.data_ptr(), seq_lens.data_ptr(), ring.data_ptr(), free_ring.data_ptr(),
+                              block_table.data_ptr(), seq_lens_out.data_ptr(), ring_out.data_ptr(),
+                              cu_tokens.data_ptr(), slot_map.data_ptr(), positions.data_ptr(), chunks.data_ptr(),
+                              d_status.data_ptr(), _raw_stream(stream)),
            "msa_cache_step")
 
 
 def msa_cache_append(c, k, v, k_index, slot_map, cu_tokens, chunks, cache, index_tail, index_pool, d_status,
                      stream=None):
-    _check(lib.msa_cache_append(ctypes.byref(c), _ptr(k), _ptr(v), _ptr(k_index), _ptr(slot_map), _ptr(cu_tokens),
-                                _ptr(chunks), _ptr(cache), _ptr(index_tail), _ptr(index_pool), _ptr(d_status),
-                                _stream(stream)),
+    _check(lib.msa_cache_append(c, k.data_ptr(), v.data_ptr(), _addr(k_index), slot_map.data_ptr(),
+                                _addr(cu_tokens), _addr(chunks), cache.data_ptr(), _addr(index_tail),
+                                _addr(index_pool), d_status.data_ptr(), _raw_stream(stream)),
            "msa_cache_append")
 
 
 def msa_cache_read(c, slots, cache, k, v, d_status, stream=None):
-    _check(lib.msa_cache_read(ctypes.byref(c), _ptr(slots), _ptr(cache), _ptr(k), _ptr(v), _ptr(d_status),
-                              _stream(stream)),
+    _check(lib.msa_cache_read(c, slots.data_ptr(), cache.data_ptr(), k.data_ptr(), v.data_ptr(),
+                              d_status.data_ptr(), _raw_stream(stream)),
            "msa_cache_read")
 
 
 def msa_cache_select(c, q_index, index_pool, block_table, chunks, sel, d_status, stream=None):
-    _check(lib.msa_cache_select(ctypes.byref(c), _ptr(q_index), _ptr(index_pool), _ptr(block_table), _ptr(chunks),
-                                _ptr(sel), _ptr(d_status), _stream(stream)),
+    _check(lib.msa_cache_select(c, q_index.data_ptr(), index_pool.data_ptr(), block_table.data_ptr(),
+                                chunks.data_ptr(), sel.data_ptr(), d_status.data_ptr(), _raw_stream(stream)),
            "msa_cache_select")
 
 
 def msa_cache_fwd(c, q, cache, block_table, chunks, sel, o, lse, d_status, stream=None):
-    _check(lib.msa_cache_fwd(ctypes.byref(c), _ptr(q), _ptr(cache), _ptr(block_table), _ptr(chunks), _ptr(sel),
-                             _ptr(o), _ptr(lse), _ptr(d_status), _stream(stream)),
+    _check(lib.msa_cache_fwd(c, q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), chunks.data_ptr(),
+                             sel.data_ptr(), o.data_ptr(), lse.data_ptr(), d_status.data_ptr(),
+                             _raw_stream(stream)),
            "msa_cache_fwd")
 
 

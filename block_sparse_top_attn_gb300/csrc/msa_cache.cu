@@ -42,44 +42,11 @@ struct StepArgs {
   int32_t* status;
 };
 
-constexpr int kStepThreads = 1024;
+constexpr int kStepThreads = 512;
+constexpr uint32_t kSat = 1u << 30;  // sums saturate here: above every capacity
 
-// Exclusive prefix sums over the CTA of three 64-bit values per thread.
-__device__ void scan3(int64_t (&v)[3], int64_t (&total)[3], int64_t (*s)[33]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t inc[3];
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    inc[i] = v[i];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, inc[i], o);
-      if (lane >= o) inc[i] += y;
-    }
-    if (lane == 31) s[i][warp] = inc[i];
-  }
-  __syncthreads();
-  if (warp == 0) {
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const int64_t own = s[i][lane];
-      int64_t x = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      s[i][lane] = x - own;
-      if (lane == 31) s[i][32] = x;
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    v[i] = s[i][warp] + inc[i] - v[i];
-    total[i] = s[i][32];
-  }
-}
+// Sums of non-negative counts that saturate instead of wrapping (associative).
+MSA_DEV uint32_t sat_add(uint32_t a, uint32_t b) { return min(a + b, kSat); }
 
 // Largest r in [0, n) with off[r] <= x (off ascending, off[0] <= x).
 __device__ __forceinline__ int last_at_or_below(const int32_t* off, int n, int x) {
@@ -91,127 +58,187 @@ __device__ __forceinline__ int last_at_or_below(const int32_t* off, int n, int x
   return lo;
 }
 
-// One cluster of 1 to 8 CTAs.  Every CTA scans all lengths (a few KB from L2)
-// into shared memory, so no CTA waits for another's tables; the chunks, eight
-// tokens each, are then spread over the cluster, one chunk a thread.  The
-// lengths and the ring may be updated in place, so they are written after a
-// cluster barrier that follows every read of them.  Latency-bound: the bytes
-// (12 per token, 16 per chunk) take microseconds only for 100k tokens.
-__global__ void __launch_bounds__(kStepThreads) step_kernel(StepArgs a) {
-  extern __shared__ int32_t s_off[];  // cu_tokens, cu_chunks, cu_alloc: R + 1 each
-  __shared__ int64_t s_scan[3][33];
+struct StepTables {
+  int32_t *cu, *chunks, *taken, *given;  // exclusive sums over the requests, [R + 1] each
+  int32_t* past;                         // cached lengths
+  __device__ StepTables(int32_t* s, int R)
+      : cu(s), chunks(s + (R + 1)), taken(s + 2 * (R + 1)), given(s + 3 * (R + 1)), past(s + 4 * (R + 1)) {}
+};
+constexpr int kStepArrays = 5;
+
+struct StepSums {
+  uint32_t ntok, nchunks, ntaken, ngiven;
+  int head, count;
+  int err;
+};
+
+// Every CTA scans all lengths (a few KB from L2) into its shared memory, so no
+// CTA waits for another's tables: see StepTables.  Thread t owns requests [t * per, t * per + per).
+__device__ StepSums step_scan(const StepArgs& a, int32_t* s_off) {
+  __shared__ uint32_t s_sum[4][kStepThreads / 32];
   __shared__ int s_err;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
-  const int tid = threadIdx.x;
-  int32_t* cu = s_off;
-  int32_t* cch = cu + (a.R + 1);
-  int32_t* cal = cch + (a.R + 1);
-  if (tid == 0) s_err = status_bad(a.status) ? MSA_ERR_INVALID_ARGUMENT : 0;  // any value: skip
-  __syncthreads();
-  const int head = a.ring[0], count = a.ring[1];
-  // thread t owns requests [t * per, t * per + per)
+  const StepTables s(s_off, a.R);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  StepSums z;
+  const bool stale = status_bad(a.status);
+  z.head = a.ring[0];
+  z.count = a.ring[1];
+  if (tid == 0) s_err = 0;
   const int per = (a.R + kStepThreads - 1) / kStepThreads;
-  int64_t v[3] = {0, 0, 0};  // tokens, chunks, (blocks taken << 32) + blocks given back
-  int err = 0;
+  uint32_t v[4] = {0, 0, 0, 0};
+  int err = stale ? MSA_ERR_INVALID_ARGUMENT : 0;  // any value: skip
   for (int i = 0; i < per; ++i) {
     const int r = tid * per + i;
     if (r >= a.R) break;
     const int n = a.new_lens[r], past = a.seq_lens[r];
     if (n < -1 || past < 0 || past > a.M * a.B) { err = MSA_ERR_INVALID_CACHE; break; }
-    const int held = (past + a.B - 1) / a.B;
-    if (n < 0) {
-      v[2] += held;
-    } else {
-      if (n > a.M * a.B - past) { err = MSA_ERR_CAPACITY; break; }
-      v[0] += n;
-      if (n > 0) v[1] += (past + n - 1) / kChunk - past / kChunk + 1;
-      v[2] += (int64_t)((past + n + a.B - 1) / a.B - held) << 32;
+    if (n > a.M * a.B - past) { err = MSA_ERR_CAPACITY; break; }
+    const int held = (past + a.B - 1) / a.B, m = max(n, 0);
+    s.cu[r] = (int)v[0];  // within the thread's requests; its offset is added below
+    s.chunks[r] = (int)v[1];
+    s.taken[r] = (int)v[2];
+    s.given[r] = (int)v[3];
+    s.past[r] = past;
+    v[0] = sat_add(v[0], m);
+    if (m > 0) v[1] = sat_add(v[1], (past + m - 1) / kChunk - past / kChunk + 1);
+    v[2] = sat_add(v[2], (past + m + a.B - 1) / a.B - held);
+    if (n < 0) v[3] = sat_add(v[3], held);
+  }
+  uint32_t inc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) inc[i] = v[i];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, inc[i], o);
+      if (lane >= o) inc[i] = sat_add(inc[i], y);
     }
   }
-  if (err) atomicMax(&s_err, err);
-  int64_t total[3];
-  scan3(v, total, s_scan);
-  const int64_t taken = total[2] >> 32, given = total[2] & 0xffffffff;
-  if (tid == 0 && !s_err) {
-    if (head < 0 || head >= a.P || count < 0 || count > a.P) s_err = MSA_ERR_INVALID_CACHE;
-    else if (total[0] > a.T || total[1] > a.NC || taken > count) s_err = MSA_ERR_CAPACITY;
-    else if (count - taken + given > a.P) s_err = MSA_ERR_INVALID_CACHE;
+  if (lane == 31) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s_sum[i][warp] = inc[i];
   }
   __syncthreads();
-  const bool ok = s_err == 0;
-  if (ok) {
-    for (int i = 0; i < per; ++i) {
-      const int r = tid * per + i;
-      if (r >= a.R) break;
-      const int n = max(a.new_lens[r], 0), past = a.seq_lens[r];
-      cu[r] = (int)v[0];
-      cch[r] = (int)v[1];
-      cal[r] = (int)(v[2] >> 32);
-      v[0] += n;
-      if (n > 0) v[1] += (past + n - 1) / kChunk - past / kChunk + 1;
-      if (n > 0) v[2] += (int64_t)((past + n + a.B - 1) / a.B - (past + a.B - 1) / a.B) << 32;
+  if (err) atomicMax(&s_err, err);
+  // every warp adds up the warps before it and all of them
+  uint32_t before[4], all[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = lane < kStepThreads / 32 ? s_sum[i][lane] : 0;
+    before[i] = lane < warp ? x : 0;
+    all[i] = x;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      before[i] = sat_add(before[i], __shfl_xor_sync(0xffffffffu, before[i], o));
+      all[i] = sat_add(all[i], __shfl_xor_sync(0xffffffffu, all[i], o));
     }
-    __syncthreads();
-    const int nchunks = (int)total[1], ntok = (int)total[0];
-    for (int g = rank * kStepThreads + tid; g < a.NC; g += ranks * kStepThreads) {
-      int4 row = make_int4(-1, -1, -1, -1);
-      if (g < nchunks) {
-        const int r = last_at_or_below(cch, a.R, g);
-        const int past = a.seq_lens[r], n = a.new_lens[r];
-        const int c = past / kChunk + g - cch[r];
-        const int first = max(past, c * kChunk), last = min(past + n, c * kChunk + kChunk);
-        const int held = (past + a.B - 1) / a.B, blk = first / a.B;
+  }
+  uint32_t ex[4];  // exclusive: the lanes before this one in the warp, the warps before it
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, inc[i], 1);
+    ex[i] = sat_add(before[i], lane ? y : 0);
+  }
+  for (int i = 0; i < per; ++i) {
+    const int r = tid * per + i;
+    if (r >= a.R) break;
+    s.cu[r] += (int)ex[0];  // not used when a sum has saturated
+    s.chunks[r] += (int)ex[1];
+    s.taken[r] += (int)ex[2];
+    s.given[r] += (int)ex[3];
+  }
+  if (tid == 0) s.cu[a.R] = (int)all[0];
+  __syncthreads();
+  z.ntok = all[0]; z.nchunks = all[1]; z.ntaken = all[2]; z.ngiven = all[3];
+  z.err = s_err;
+  if (!z.err) {
+    if (z.head < 0 || z.head >= a.P || z.count < 0 || z.count > a.P) z.err = MSA_ERR_INVALID_CACHE;
+    else if (z.ntok > (uint32_t)a.T || z.nchunks > (uint32_t)a.NC || z.ntaken > (uint32_t)z.count)
+      z.err = MSA_ERR_CAPACITY;
+    else if ((uint32_t)z.count - z.ntaken + z.ngiven > (uint32_t)a.P) z.err = MSA_ERR_INVALID_CACHE;
+  }
+  return z;
+}
+
+// The lengths, the ring and the pages of finished requests, by one CTA once
+// nothing reads them any more.  The pages join the ring behind its last entry,
+// in (request, block) order: those entries hold no free page, so nothing that
+// the step takes from the ring is overwritten.
+__device__ void step_finish(const StepArgs& a, const StepSums& z, const StepTables& s) {
+  for (uint32_t j = threadIdx.x; j < z.ngiven; j += kStepThreads) {
+    const int r = last_at_or_below(s.given, a.R, (int)j);
+    a.free_ring[((int64_t)z.head + z.count + j) % a.P] = __ldcg(&a.block_table[(int64_t)r * a.M + j - s.given[r]]);
+  }
+  for (int r = threadIdx.x; r < a.R; r += kStepThreads)
+    a.seq_lens_out[r] = a.new_lens[r] < 0 ? 0 : s.past[r] + s.cu[r + 1] - s.cu[r];
+  if (threadIdx.x == 0) {
+    a.ring_out[0] = (int)(((int64_t)z.head + z.ntaken) % a.P);
+    a.ring_out[1] = (int)((uint32_t)z.count - z.ntaken + z.ngiven);
+  }
+}
+
+// Latency-bound: a batch's lengths are a few KB and the outputs 12 bytes per
+// token and 16 per chunk.  A token a thread (slots and positions leave in whole
+// lines), then a chunk a thread.
+// kCluster: the grid is one cluster, and its first CTA finishes the step behind
+// a cluster barrier that follows every read of the lengths and the ring (which
+// may be updated in place).  Otherwise step_finish_kernel does, in a launch of
+// its own.
+template <bool kCluster>
+__global__ void __launch_bounds__(kStepThreads) step_kernel(StepArgs a) {
+  extern __shared__ int32_t s_off[];
+  const StepTables s(s_off, a.R);
+  const int tid = threadIdx.x, stride = gridDim.x * kStepThreads;
+  const StepSums z = step_scan(a, s_off);
+  if (!z.err) {
+    const int ntok = (int)z.ntok, nchunks = (int)z.nchunks;
+    for (int t = blockIdx.x * kStepThreads + tid; t < a.T; t += stride) {
+      int64_t slot = -1;
+      int pos = -1;
+      if (t < ntok) {
+        const int r = last_at_or_below(s.cu, a.R, t), past = s.past[r];
+        pos = past + t - s.cu[r];
+        const int held = (past + a.B - 1) / a.B, blk = pos / a.B;
         int page;
         if (blk < held) {
           page = a.block_table[(int64_t)r * a.M + blk];
         } else {
-          page = a.free_ring[(int)(((int64_t)head + cal[r] + blk - held) % a.P)];
-          if (first % a.B == 0) a.block_table[(int64_t)r * a.M + blk] = page;
+          page = a.free_ring[((int64_t)z.head + s.taken[r] + blk - held) % a.P];
+          if (pos % a.B == 0) a.block_table[(int64_t)r * a.M + blk] = page;
         }
-        row = make_int4(r, cu[r] + first - past, last - first, first);
-        const int64_t slot = (int64_t)page * a.B + first % a.B;
-        for (int i = 0; i < row.z; ++i) {
-          a.slot_map[row.y + i] = slot + i;
-          a.positions[row.y + i] = first + i;
-        }
+        slot = (int64_t)page * a.B + pos % a.B;
+      }
+      a.slot_map[t] = slot;
+      a.positions[t] = pos;
+    }
+    for (int g = blockIdx.x * kStepThreads + tid; g < a.NC; g += stride) {
+      int4 row = make_int4(-1, -1, -1, -1);
+      if (g < nchunks) {
+        const int r = last_at_or_below(s.chunks, a.R, g), past = s.past[r];
+        const int c = past / kChunk + g - s.chunks[r];
+        const int first = max(past, c * kChunk), last = min(past + s.cu[r + 1] - s.cu[r], c * kChunk + kChunk);
+        row = make_int4(r, s.cu[r] + first - past, last - first, first);
       }
       reinterpret_cast<int4*>(a.chunks)[g] = row;
     }
-    for (int t = ntok + rank * kStepThreads + tid; t < a.T; t += ranks * kStepThreads) {
-      a.slot_map[t] = -1;
-      a.positions[t] = -1;
-    }
-    if (rank == 0) {
-      for (int r = tid; r < a.R; r += kStepThreads) a.cu_tokens[r] = cu[r];
-      if (tid == 0) a.cu_tokens[a.R] = ntok;
-    }
+    if (blockIdx.x == 0)
+      for (int r = tid; r <= a.R; r += kStepThreads) a.cu_tokens[r] = s.cu[r];
   }
-  // every read of the lengths and the ring is done
-  cluster.sync();
-  if (ok && rank == 0) {
-    // pages of finished requests, in (request, block) order behind the ring's
-    // last entry: those entries hold no free page, so nothing read above is
-    // overwritten.  v[2]'s low half: this thread's first place.
-    int at = (int)(v[2] & 0xffffffff);
-    for (int i = 0; i < per; ++i) {
-      const int r = tid * per + i;
-      if (r >= a.R) break;
-      const int n = a.new_lens[r], past = a.seq_lens[r];
-      if (n < 0) {
-        const int held = (past + a.B - 1) / a.B;
-        for (int b = 0; b < held; ++b)
-          a.free_ring[(int)(((int64_t)head + count + at + b) % a.P)] = a.block_table[(int64_t)r * a.M + b];
-        at += held;
-      }
-      a.seq_lens_out[r] = n < 0 ? 0 : past + n;
-    }
-    if (tid == 0) {
-      a.ring_out[0] = (int)((head + taken) % a.P);
-      a.ring_out[1] = (int)(count - taken + given);
-    }
+  if constexpr (kCluster) {
+    cg::this_cluster().sync();
+    if (blockIdx.x == 0 && !z.err) step_finish(a, z, s);
   }
-  if (!ok && rank == 0 && tid == 0) set_status(a.status, s_err);
+  if (z.err && blockIdx.x == 0 && tid == 0) set_status(a.status, z.err);
+}
+
+__global__ void __launch_bounds__(kStepThreads) step_finish_kernel(StepArgs a) {
+  extern __shared__ int32_t s_off[];
+  const StepSums z = step_scan(a, s_off);
+  if (!z.err) step_finish(a, z, StepTables(s_off, a.R));
 }
 
 // ---------------------------------------------------------------------------
@@ -229,6 +256,18 @@ struct AppendArgs {
   int index_blocks;    // leading CTAs that keep the pooled index keys
   int32_t* status;
 };
+
+// Token and head of the u-th row: four tokens of one head, then the next head,
+// so that a warp (four rows of eight groups) covers whole sectors of a tile's
+// code rows and scales when the tokens' slots follow one another.
+MSA_DEV void row_of(int64_t u, int heads, int& t, int& h) {
+  const int64_t quad = u >> 2;
+  // 32-bit where it fits: a 64-bit division is slow
+  const int64_t tq = quad < (int64_t(1) << 32) ? (uint32_t)quad / (uint32_t)heads : quad / heads;
+  h = (int)(quad - tq * heads);
+  t = (int)(tq * 4 + (u & 3));
+}
+inline int64_t row_blocks(int64_t tokens, int64_t heads) { return ((tokens + 3) / 4 * 4 * heads * 8 + 255) / 256; }
 
 // 16 bf16 values as fp32 (exact), two 16-byte loads.
 MSA_DEV void load16(const uint16_t* src, float (&x)[16], uint32_t& amax) {
@@ -290,12 +329,16 @@ MSA_DEV uint32_t quantize16(const float (&x)[16], uint32_t amax_bits, float mul,
   return s8;
 }
 
-// Index keys of one (chunk, head), by one warp, lane l owning dims 4l..4l+3.
+// Index keys of half the dims of one (chunk, head), by one warp, a lane owning
+// two dims.
 // The chunk that ends a block averages the block's tokens, those of earlier
-// calls from the tail.  The first chunk of a request then stores the request's
-// incomplete block's rows of this call: one warp does both, so a tail buffer is
-// read before it is overwritten (a lane reads and writes its own dims only).
-MSA_DEV void index_chunk(const AppendArgs& a, int g, int h, int lane) {
+// calls from the tail; a chunk of the request's incomplete block stores its rows
+// to the tail.  Where the incomplete block uses the buffer that the first
+// block's average reads (an even number of blocks apart), the chunk that
+// averages stores them too, after it: a lane reads and writes its own dims
+// only, so the order holds.  The first block's average is made by the
+// request's first chunk, others by the chunk that ends the block.
+MSA_DEV void index_chunk(const AppendArgs& a, int g, int h, int half, int lane) {
   const int4 c = reinterpret_cast<const int4*>(a.chunks)[g];
   const int r = c.x, row0 = c.y, n = c.z, pos0 = c.w;
   if (r < 0) return;
@@ -312,57 +355,74 @@ MSA_DEV void index_chunk(const AppendArgs& a, int g, int h, int lane) {
     return;
   }
   const int64_t hs = (int64_t)a.H * 128;  // elements from one token's row to the next
-  const int d = h * 128 + lane * 4;
+  const int d = h * 128 + half * 64 + lane * 2;
   const int end = pos0 + (cu1 - row0);     // position behind the request's last new token
   const int past = pos0 - (row0 - cu0);
   uint16_t* tail = a.index_tail + (int64_t)r * 2 * a.B * hs + d;
-  // averages the block that ends at row `last` (its last token)
+  // averages the block whose last token is row `last`
   auto average = [&](int last, int blk) {
     const int64_t slot = a.slot_map[last];
     if (slot < 0 || slot >= a.slots) return;  // reported by the rows' own CTAs, or left out
     const uint16_t* old = tail + (int64_t)(blk & 1) * a.B * hs;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int i = 0; i < a.B; ++i) {
-      const int row = last - (a.B - 1) + i;
-      const uint2 w = *reinterpret_cast<const uint2*>(row >= cu0 ? a.k_index + row * hs + d : old + i * hs);
-      acc[0] = __fadd_rn(acc[0], __uint_as_float(w.x << 16));
-      acc[1] = __fadd_rn(acc[1], __uint_as_float(w.x & 0xFFFF0000u));
-      acc[2] = __fadd_rn(acc[2], __uint_as_float(w.y << 16));
-      acc[3] = __fadd_rn(acc[3], __uint_as_float(w.y & 0xFFFF0000u));
-    }
+    float lo = 0.f, hi = 0.f;
+    auto add = [&](const uint16_t* src, int rows) {  // rows in flight together; the sums keep the tokens' order
+      for (; rows > 0; rows -= 16, src += 16 * hs) {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = i < rows ? *reinterpret_cast<const uint32_t*>(src + i * hs) : 0u;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i < rows) {
+            lo = __fadd_rn(lo, __uint_as_float(w[i] << 16));
+            hi = __fadd_rn(hi, __uint_as_float(w[i] & 0xFFFF0000u));
+          }
+      }
+    };
+    const int olds = max(0, cu0 - (last - (a.B - 1)));  // tokens of earlier calls
+    add(old, olds);
+    add(a.k_index + (int64_t)(last - (a.B - 1) + olds) * hs + d, a.B - olds);
     const float inv = 1.f / (float)a.B;  // a power of two: the product is the quotient
-    uint2 o;
-    o.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-    o.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
-    *reinterpret_cast<uint2*>(a.index_pool + (slot / a.B) * hs + d) = o;
+    *reinterpret_cast<uint32_t*>(a.index_pool + (slot / a.B) * hs + d) = pack_bf16x2(lo * inv, hi * inv);
   };
-  const int blk0 = past / a.B, blk = pos0 / a.B;
-  if (blk > blk0 && (pos0 + n) % a.B == 0) average(row0 + n - 1, blk);
-  if (row0 == cu0) {
-    const int first_end = (blk0 + 1) * a.B;
-    if (first_end <= end) average(cu0 + first_end - past - 1, blk0);
-    const int open = end / a.B;  // the block that stays incomplete
+  // stores rows [p0, p1) (positions) of the incomplete block
+  const int blk0 = past / a.B, blk = pos0 / a.B, open = end / a.B;
+  auto keep = [&](int p0, int p1) {
     uint16_t* dst = tail + (int64_t)(open & 1) * a.B * hs;
-    for (int p = max(past, open * a.B); p < end; ++p)
-      *reinterpret_cast<uint2*>(dst + (p % a.B) * hs) =
-          *reinterpret_cast<const uint2*>(a.k_index + (cu0 + p - past) * hs + d);
+    for (int q = p0; q < p1; q += kChunk) {
+      uint32_t w[kChunk];
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i)
+        if (q + i < p1) w[i] = __ldg(reinterpret_cast<const uint32_t*>(a.k_index + (cu0 + q + i - past) * hs + d));
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i)
+        if (q + i < p1) *reinterpret_cast<uint32_t*>(dst + ((q + i) % a.B) * hs) = w[i];
+    }
+  };
+  const bool shared_buffer = open > blk0 && (open & 1) == (blk0 & 1) && past % a.B != 0;
+  if (row0 == cu0 && open > blk0) average(cu0 + (blk0 + 1) * a.B - past - 1, blk0);
+  if (row0 != cu0 && blk > blk0 && (pos0 + n) % a.B == 0) average(row0 + n - 1, blk);
+  if (shared_buffer) {
+    if (row0 == cu0) keep(open * a.B, end);
+  } else if (blk == open) {
+    keep(pos0, pos0 + n);
   }
 }
 
-__global__ void __launch_bounds__(256) append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(256, 4) append_kernel(AppendArgs a) {
   if (status_bad(a.status)) return;
   if ((int)blockIdx.x < a.index_blocks) {
     const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    if (w < (int64_t)a.NC * a.H) index_chunk(a, (int)(w / a.H), (int)(w % a.H), threadIdx.x & 31);
+    if (w < (int64_t)a.NC * a.H * 2)
+      index_chunk(a, (int)(w / (2 * a.H)), (int)(w / 2 % a.H), (int)(w & 1), threadIdx.x & 31);
     return;
   }
   // a thread takes one group of 16 dims of K and of V: no value crosses threads
   const int64_t i = (int64_t)(blockIdx.x - a.index_blocks) * blockDim.x + threadIdx.x;
-  const int64_t row = i >> 3;  // token * H + head
   const int grp = (int)(i & 7);
-  if (row >= (int64_t)a.T * a.H) return;
-  const int t = (int)(row / a.H), h = (int)(row % a.H);
+  int t, h;
+  row_of(i >> 3, a.H, t, h);
+  if (t >= a.T) return;
+  const int64_t row = (int64_t)t * a.H + h;
   const int64_t slot = a.slot_map[t];
   if (slot < 0 || slot >= a.slots) {
     if (slot != -1) set_status(a.status, MSA_ERR_INVALID_CACHE);
@@ -375,8 +435,9 @@ __global__ void __launch_bounds__(256) append_kernel(AppendArgs a) {
   const uint32_t ks = quantize16(x, amax, a.k_mul, kc);
   load16(a.v + row * 128 + grp * 16, x, amax);
   const uint32_t vs = quantize16(x, amax, a.v_mul, vc);
-  const int off = (int)(slot % a.B), tok = off % kTile;
-  uint8_t* tile = a.cache + tile_index(slot / a.B, h, a.H, a.B / kTile, off / kTile) * kTileBytes;
+  const int lb = a.B == 128 ? 7 : 6;  // log2 of the block
+  const int off = (int)(slot & (a.B - 1)), tok = off % kTile;
+  uint8_t* tile = a.cache + tile_index(slot >> lb, h, a.H, a.B / kTile, off / kTile) * kTileBytes;
   *reinterpret_cast<uint2*>(tile + OFF_KC + tok * kRowBytes + grp * 8) = kc;
   *reinterpret_cast<uint2*>(tile + OFF_VC + v_code_offset(tok, grp)) = vc;
   tile[OFF_KS + tok * kScales + grp] = (uint8_t)ks;
@@ -416,17 +477,19 @@ MSA_DEV void dequantize16(uint2 codes, uint32_t scale, float mul, uint16_t* dst)
 __global__ void __launch_bounds__(256) read_kernel(ReadArgs a) {
   if (status_bad(a.status)) return;
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int64_t row = i >> 3;
   const int grp = (int)(i & 7);
-  if (row >= (int64_t)a.T * a.H) return;
-  const int t = (int)(row / a.H), h = (int)(row % a.H);
+  int t, h;
+  row_of(i >> 3, a.H, t, h);
+  if (t >= a.T) return;
+  const int64_t row = (int64_t)t * a.H + h;
   const int64_t slot = a.slots[t];
   if (slot < 0 || slot >= a.nslots) {
     if (slot != -1) set_status(a.status, MSA_ERR_INVALID_CACHE);
     return;
   }
-  const int off = (int)(slot % a.B), tok = off % kTile;
-  const uint8_t* tile = a.cache + tile_index(slot / a.B, h, a.H, a.B / kTile, off / kTile) * kTileBytes;
+  const int lb = a.B == 128 ? 7 : 6;  // log2 of the block
+  const int off = (int)(slot & (a.B - 1)), tok = off % kTile;
+  const uint8_t* tile = a.cache + tile_index(slot >> lb, h, a.H, a.B / kTile, off / kTile) * kTileBytes;
   dequantize16(*reinterpret_cast<const uint2*>(tile + OFF_KC + tok * kRowBytes + grp * 8),
                tile[OFF_KS + tok * kScales + grp], a.k_mul, a.k + row * 128 + grp * 16);
   dequantize16(*reinterpret_cast<const uint2*>(tile + OFF_VC + v_code_offset(tok, grp)),
@@ -445,79 +508,56 @@ struct SelectArgs {
 };
 constexpr int kSelThreads = 256;
 
+// 32 bytes in one load (a whole sector a lane), read-only data.
+MSA_DEV void load32(const void* src, uint32_t (&u)[8]) {
+  asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+      : "l"(src));
+}
+
 // A score as an unsigned key of the same order (-0 counts as +0).
 MSA_DEV uint32_t score_key(float s) {
   const uint32_t u = __float_as_uint(__fadd_rn(s, 0.f));
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// One CTA per (chunk, head): the scores of all earlier blocks as ordered keys
-// in shared memory (one block a thread, so the sum keeps its order), then a
-// radix selection of the (K-1)-th largest key, 8 bits a pass.
-__global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a) {
-  extern __shared__ uint32_t s_key[];  // [M]
-  __shared__ float s_q[128];
-  __shared__ uint32_t s_hist[256], s_prefix, s_need, s_count;
-  __shared__ uint32_t s_topk[kMaxTopk];
-  __shared__ int s_topb[kMaxTopk];
-  if (status_bad(a.status)) return;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = blockIdx.x, h = blockIdx.y;
-  const int4 c = reinterpret_cast<const int4*>(a.chunks)[g];
-  if (c.x < 0) return;
-  const int n = c.w / a.B;  // earlier blocks
-  if (c.x >= a.R || c.z < 1 || c.z > kChunk || c.y < 0 || c.y > a.T - c.z || c.w < 0 || n >= a.M) {
-    if (tid == 0) set_status(a.status, MSA_ERR_INVALID_CACHE);
-    return;
+// Scratch of one row's selection.
+struct SelectScratch {
+  uint32_t hist[256];
+  uint32_t prefix, need, count;
+  uint32_t topk[kMaxTopk];
+  int topb[kMaxTopk];
+};
+
+// The topk - 1 largest of n keys, by NT threads (a warp, or the whole CTA): a
+// radix selection of the keep-th largest key, 8 bits a pass, then the keys above
+// it, of those equal to it the lowest blocks, and their ranks.
+template <int NT>
+__device__ void select_row(const uint32_t* key, int n, int K, SelectScratch& s, int32_t* out) {
+  const int tid = threadIdx.x % NT, lane = tid & 31;
+  auto sync = [] {
+    if constexpr (NT == 32) __syncwarp(); else __syncthreads();
+  };
+  const int keep = min(K - 1, n);
+  if (tid == 0) {
+    s.prefix = 0;
+    s.need = keep;
+    s.count = 0;
   }
-  const int64_t hs = (int64_t)a.H * 128;
-  if (tid < 128) {
-    const uint16_t* src = a.q_index + (int64_t)c.y * hs + h * 128 + tid;
-    float acc = 0.f;
-    for (int i = 0; i < c.z; ++i) acc = __fadd_rn(acc, __uint_as_float((uint32_t)src[i * hs] << 16));
-    const uint32_t m = pack_bf16x2(__fdiv_rn(acc, (float)c.z), 0.f);
-    s_q[tid] = __uint_as_float(m << 16);
-  }
-  if (tid == 0) { s_prefix = 0; s_count = 0; }
-  __syncthreads();
-  const int32_t* table = a.block_table + (int64_t)c.x * a.M;
-  for (int b = tid; b < n; b += kSelThreads) {
-    const int page = table[b];
-    float s = 0.f;
-    if (page < 0 || page >= a.P) {
-      set_status(a.status, MSA_ERR_INVALID_CACHE);
-    } else {
-      const uint4* src = reinterpret_cast<const uint4*>(a.pool + page * hs + h * 128);
-#pragma unroll 8
-      for (int i = 0; i < 16; ++i) {
-        const uint4 w = __ldg(src + i);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s = __fmaf_rn(s_q[8 * i + 2 * e], __uint_as_float(u[e] << 16), s);
-          s = __fmaf_rn(s_q[8 * i + 2 * e + 1], __uint_as_float(u[e] & 0xFFFF0000u), s);
-        }
-      }
-    }
-    s_key[b] = score_key(s);
-  }
-  const int keep = min(a.K - 1, n);
-  uint32_t thr = 0;   // keys above it are kept, of those equal to it the first s_need
   if (keep > 0 && keep < n) {
-    if (tid == 0) s_need = keep;
     for (int shift = 24; shift >= 0; shift -= 8) {
-      s_hist[tid] = 0;
-      __syncthreads();
-      const uint32_t prefix = s_prefix, need = s_need;
+      for (int i = tid; i < 256; i += NT) s.hist[i] = 0;
+      sync();
+      const uint32_t prefix = s.prefix, need = s.need;
       const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-      for (int b = tid; b < n; b += kSelThreads)
-        if ((s_key[b] & mask) == prefix) atomicAdd(&s_hist[(s_key[b] >> shift) & 255], 1u);
-      __syncthreads();
-      if (warp == 0) {
+      for (int b = tid; b < n; b += NT)
+        if ((key[b] & mask) == prefix) atomicAdd(&s.hist[(key[b] >> shift) & 255], 1u);
+      sync();
+      if (tid < 32) {
         // digits from the top: lane l holds digits 255 - 8l .. 248 - 8l
         uint32_t cnt[8], sum = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) { cnt[i] = s_hist[255 - 8 * lane - i]; sum += cnt[i]; }
+        for (int i = 0; i < 8; ++i) { cnt[i] = s.hist[255 - 8 * lane - i]; sum += cnt[i]; }
         uint32_t inc = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -531,56 +571,154 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a) {
             if (above + cnt[i] >= need) break;
             above += cnt[i];
           }
-          s_prefix = prefix | ((uint32_t)(255 - 8 * lane - i) << shift);
-          s_need = need - above;
+          s.prefix = prefix | ((uint32_t)(255 - 8 * lane - i) << shift);
+          s.need = need - above;
         }
       }
-      __syncthreads();
+      sync();
     }
-    thr = s_prefix;
   } else {
-    __syncthreads();
-    if (tid == 0) s_need = 0;  // every earlier block is kept: all keys are above 0
-    __syncthreads();
+    sync();
   }
-  // the kept blocks, in any order
+  const uint32_t thr = s.prefix;  // 0 where every block is kept
   if (keep > 0) {
-    for (int b = tid; b < n; b += kSelThreads)
-      if (keep == n || s_key[b] > thr) {
-        const uint32_t at = atomicAdd(&s_count, 1u);
-        s_topk[at] = s_key[b];
-        s_topb[at] = b;
+    for (int b = tid; b < n; b += NT)
+      if (keep == n || key[b] > thr) {
+        const uint32_t at = atomicAdd(&s.count, 1u);
+        s.topk[at] = key[b];
+        s.topb[at] = b;
       }
-    __syncthreads();
-    if (warp == 0 && keep < n) {
-      // of the keys equal to the threshold, the lowest blocks
-      uint32_t at = s_count, need = s_need;
+    sync();
+    if (tid < 32 && keep < n) {
+      uint32_t at = s.count, need = s.need;
       for (int b0 = 0; b0 < n && need; b0 += 32) {
-        const bool eq = b0 + lane < n && s_key[b0 + lane] == thr;
+        const bool eq = b0 + lane < n && key[b0 + lane] == thr;
         const uint32_t m = __ballot_sync(0xffffffffu, eq);
         const uint32_t before = __popc(m & ((1u << lane) - 1u));
         if (eq && before < need) {
-          s_topk[at + before] = thr;
-          s_topb[at + before] = b0 + lane;
+          s.topk[at + before] = thr;
+          s.topb[at + before] = b0 + lane;
         }
         const uint32_t got = min((uint32_t)__popc(m), need);
         at += got;
         need -= got;
       }
     }
-    __syncthreads();
+    sync();
   }
   // rank among the kept: higher key first, then the lower block
-  int32_t* out = a.sel + ((int64_t)h * a.NC + g) * a.K;
-  if (tid < a.K) {
+  if (tid < K) {
     if (tid == 0) out[0] = n;
     if (tid < keep) {
       int rank = 0;
       for (int i = 0; i < keep; ++i)
-        rank += s_topk[i] > s_topk[tid] || (s_topk[i] == s_topk[tid] && s_topb[i] < s_topb[tid]);
-      out[1 + rank] = s_topb[tid];
+        rank += s.topk[i] > s.topk[tid] || (s.topk[i] == s.topk[tid] && s.topb[i] < s.topb[tid]);
+      out[1 + rank] = s.topb[tid];
     }
     if (tid > keep) out[tid] = -1;
+  }
+}
+
+// A CTA scores G consecutive chunks of one head (G = 1, or 8: one warp's
+// selection each).  The keys of a request are read once for all of its chunks
+// in the CTA: a thread takes a block, so every score keeps its order of
+// additions, and reads its 256-byte pooled key as whole sectors.
+// Bound at G = 1 by those reads, at G = 8 by the FMAs (one per dim, block and
+// chunk) and the selection.
+template <int G>
+__global__ void __launch_bounds__(kSelThreads, G == 1 ? 4 : 1) select_kernel(SelectArgs a) {
+  extern __shared__ uint32_t s_key[];  // [G][M]
+  __shared__ __align__(16) float s_q[G][128];
+  __shared__ SelectScratch s_scratch[G];
+  __shared__ int s_n[G];
+  if (status_bad(a.status)) return;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  // heads fastest: CTAs that run together read neighbouring rows of a page
+  const int g0 = (int)(blockIdx.x / a.H) * G, h = (int)(blockIdx.x % a.H);
+  const int64_t hs = (int64_t)a.H * 128;
+  for (int lo = 0, hi; lo < G; lo = hi) {
+    // a run of chunks of one request
+    hi = lo + 1;
+    const int4 c = g0 + lo < a.NC ? reinterpret_cast<const int4*>(a.chunks)[g0 + lo] : make_int4(-1, 0, 0, 0);
+    if (c.x < 0) continue;
+    int most = c.w;
+    while (hi < G && g0 + hi < a.NC && a.chunks[(int64_t)(g0 + hi) * MSA_CHUNK_COLS] == c.x) {
+      most = max(most, a.chunks[(int64_t)(g0 + hi) * MSA_CHUNK_COLS + 3]);
+      ++hi;
+    }
+    __syncthreads();  // the run before has been read
+    // pooled queries and the rows' numbers of earlier blocks (-1: a bad row)
+    for (int i = tid; i < (hi - lo) * 128; i += kSelThreads) {
+      const int row = i >> 7, d = i & 127;
+      const int4 cc = reinterpret_cast<const int4*>(a.chunks)[g0 + lo + row];
+      const bool good = cc.x < a.R && cc.z >= 1 && cc.z <= kChunk && cc.y >= 0 && cc.y <= a.T - cc.z && cc.w >= 0 &&
+                        cc.w / a.B < a.M;
+      float acc = 0.f;
+      if (good) {
+        const uint16_t* src = a.q_index + (int64_t)cc.y * hs + h * 128 + d;
+        uint16_t x[kChunk];
+#pragma unroll
+        for (int k = 0; k < kChunk; ++k) x[k] = k < cc.z ? src[k * hs] : 0;
+#pragma unroll
+        for (int k = 0; k < kChunk; ++k)
+          if (k < cc.z) acc = __fadd_rn(acc, __uint_as_float((uint32_t)x[k] << 16));
+        acc = __uint_as_float(pack_bf16x2(__fdiv_rn(acc, (float)cc.z), 0.f) << 16);
+      }
+      s_q[row][d] = acc;
+      if (d == 0) {
+        s_n[row] = good ? cc.w / a.B : -1;
+        if (!good) set_status(a.status, MSA_ERR_INVALID_CACHE);
+      }
+    }
+    __syncthreads();
+    const int nmax = c.x < a.R && most >= 0 ? min(most / a.B, a.M) : 0;
+    const int32_t* table = a.block_table + (int64_t)c.x * a.M;
+    for (int b = tid; b < nmax; b += kSelThreads) {
+      const int page = table[b];
+      float s[G];
+#pragma unroll
+      for (int i = 0; i < G; ++i) s[i] = 0.f;
+      if (page < 0 || page >= a.P) {
+        set_status(a.status, MSA_ERR_INVALID_CACHE);
+      } else {
+        const uint16_t* src = a.pool + page * hs + h * 128;
+#pragma unroll 1
+        for (int i0 = 0; i0 < 8; i0 += 4) {
+          uint32_t u[4][8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) load32(src + 16 * (i0 + i), u[i]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float k0 = __uint_as_float(u[i][2 * e] << 16), k1 = __uint_as_float(u[i][2 * e] & 0xFFFF0000u);
+              const float k2 = __uint_as_float(u[i][2 * e + 1] << 16),
+                          k3 = __uint_as_float(u[i][2 * e + 1] & 0xFFFF0000u);
+#pragma unroll
+              for (int r = 0; r < G; ++r) {
+                const float4 q = *reinterpret_cast<const float4*>(&s_q[r][16 * (i0 + i) + 4 * e]);
+                s[r] = __fmaf_rn(q.x, k0, s[r]);
+                s[r] = __fmaf_rn(q.y, k1, s[r]);
+                s[r] = __fmaf_rn(q.z, k2, s[r]);
+                s[r] = __fmaf_rn(q.w, k3, s[r]);
+              }
+            }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < G; ++r)
+        if (r < hi - lo) s_key[(int64_t)r * a.M + b] = score_key(s[r]);
+    }
+    __syncthreads();
+    if constexpr (G == 1) {
+      if (s_n[0] >= 0)
+        select_row<kSelThreads>(s_key, s_n[0], a.K, s_scratch[0], a.sel + ((int64_t)h * a.NC + g0) * a.K);
+    } else {
+      static_assert(G <= kSelThreads / 32, "a warp per row");
+      if (warp < hi - lo && s_n[warp] >= 0)
+        select_row<32>(s_key + (int64_t)warp * a.M, s_n[warp], a.K, s_scratch[warp],
+                       a.sel + ((int64_t)h * a.NC + g0 + lo + warp) * a.K);
+    }
   }
 }
 
@@ -625,27 +763,37 @@ int msa_cache_step(const msa_cache_problem* p, const int32_t* new_lens, const in
   cache::StepArgs a{new_lens,  seq_lens, ring,      free_ring, block_table, seq_lens_out, ring_out,
                     cu_tokens, slot_map, positions, chunks,    p->num_requests, p->num_pages, p->max_blocks,
                     p->block_size, p->token_cap, p->chunk_cap, d_status};
-  const size_t smem = (size_t)3 * (p->num_requests + 1) * sizeof(int32_t);
-  if ((rc = cuda_status(cudaFuncSetAttribute(cache::step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             3 * (cache::kMaxRequests + 1) * (int)sizeof(int32_t)))))
-    return rc;
-  // CTAs of the cluster: one per 1024 chunks (or padding rows), at most 8
-  const int64_t rows = p->chunk_cap > p->token_cap / 8 ? p->chunk_cap : p->token_cap / 8;
-  unsigned ctas = 1;
-  while (ctas < 8 && (int64_t)ctas * cache::kStepThreads < rows) ctas *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(cache::kStepThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = ctas;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, cache::step_kernel, a));
+  const size_t smem = (size_t)cache::kStepArrays * (p->num_requests + 1) * sizeof(int32_t);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // CTAs: a token (or chunk) a thread.  Up to 8 form one cluster and one launch;
+  // above that a grid over the GPU and a second launch that finishes the step.
+  const int64_t rows = p->chunk_cap > p->token_cap ? p->chunk_cap : p->token_cap;
+  const int64_t want = (rows + cache::kStepThreads - 1) / cache::kStepThreads;
+  if (want <= 8) {
+    unsigned ctas = 1;
+    while (ctas < want) ctas *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(cache::kStepThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = ctas;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if ((rc = cuda_status(allow_smem(cache::step_kernel<true>, smem)))) return rc;
+    return cuda_status(cudaLaunchKernelEx(&cfg, cache::step_kernel<true>, a));
+  }
+  int32_t sms = 0;
+  if ((rc = sm_count_current(&sms))) return rc;
+  if ((rc = cuda_status(allow_smem(cache::step_kernel<false>, smem)))) return rc;
+  if ((rc = cuda_status(allow_smem(cache::step_finish_kernel, smem)))) return rc;
+  cache::step_kernel<false><<<(unsigned)(want < sms ? want : sms), cache::kStepThreads, smem, st>>>(a);
+  cache::step_finish_kernel<<<1, cache::kStepThreads, smem, st>>>(a);
+  return cuda_status(cudaGetLastError());
 }
 
 int msa_cache_append(const msa_cache_problem* p, const uint16_t* k, const uint16_t* v, const uint16_t* k_index,
@@ -657,7 +805,7 @@ int msa_cache_append(const msa_cache_problem* p, const uint16_t* k, const uint16
   if (bad_pointers(ptrs, k_index ? 10 : 5)) return MSA_ERR_INVALID_ARGUMENT;
   if ((rc = check_device_current())) return rc;
   const int64_t T = p->token_cap, H = p->num_kv_heads, NC = p->chunk_cap;
-  const int64_t kv_blocks = (T * H * 8 + 255) / 256, idx_blocks = k_index ? (NC * H * 32 + 255) / 256 : 0;
+  const int64_t kv_blocks = cache::row_blocks(T, H), idx_blocks = k_index ? (NC * H * 64 + 255) / 256 : 0;
   if (kv_blocks + idx_blocks > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
   cache::AppendArgs a{k, v, k_index, slot_map, cu_tokens, chunks, kv_cache, index_tail, index_pool, (int)T, (int)H,
                       p->block_size, p->num_requests, (int)NC, (int64_t)p->num_pages * p->block_size,
@@ -674,7 +822,7 @@ int msa_cache_read(const msa_cache_problem* p, const int64_t* slots, const uint8
   if (bad_pointers(ptrs, 5)) return MSA_ERR_INVALID_ARGUMENT;
   if ((rc = check_device_current())) return rc;
   const int64_t T = p->token_cap, H = p->num_kv_heads;
-  const int64_t blocks = (T * H * 8 + 255) / 256;
+  const int64_t blocks = cache::row_blocks(T, H);
   if (blocks > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
   cache::ReadArgs a{slots, kv_cache, k, v, (int)T, (int)H, p->block_size, (int64_t)p->num_pages * p->block_size,
                     cache::exp2i(p->k_exp), cache::exp2i(p->v_exp), d_status};
@@ -692,11 +840,19 @@ int msa_cache_select(const msa_cache_problem* p, const uint16_t* q_index, const 
   if ((rc = check_device_current())) return rc;
   cache::SelectArgs a{q_index, index_pool, block_table, chunks, sel, p->num_requests, p->num_pages, p->max_blocks,
                       p->block_size, p->token_cap, p->chunk_cap, p->num_kv_heads, p->topk, d_status};
-  if ((rc = cuda_status(cudaFuncSetAttribute(cache::select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             cache::kMaxBlocks * 4))))
-    return rc;
-  cache::select_kernel<<<dim3((unsigned)p->chunk_cap, (unsigned)p->num_kv_heads), cache::kSelThreads,
-                         (size_t)p->max_blocks * 4, static_cast<cudaStream_t>(stream)>>>(a);
+  // Chunks of several tokens come from prompts, whose chunks share a request's
+  // keys: 8 of them to a CTA, while 8 rows of scores fit shared memory.
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int64_t H = p->num_kv_heads, NC = p->chunk_cap;
+  if (NC * H > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
+  const size_t row = (size_t)p->max_blocks * 4;
+  if (p->token_cap / p->chunk_cap >= 3 && 8 * row <= 128 * 1024) {
+    if ((rc = cuda_status(allow_smem(cache::select_kernel<8>, 8 * row)))) return rc;
+    cache::select_kernel<8><<<(unsigned)((NC + 7) / 8 * H), cache::kSelThreads, 8 * row, st>>>(a);
+  } else {
+    if ((rc = cuda_status(allow_smem(cache::select_kernel<1>, row)))) return rc;
+    cache::select_kernel<1><<<(unsigned)(NC * H), cache::kSelThreads, row, st>>>(a);
+  }
   return cuda_status(cudaGetLastError());
 }
 

@@ -31,8 +31,13 @@ namespace msa {
 namespace cache {
 
 constexpr int kConsumers = 4;
-constexpr int kFwdThreads = 32 * (kConsumers + 1);
-constexpr int kStages = 6;
+constexpr int kFwdThreads = 32 * kConsumers;
+#ifndef KS
+#define KS 6
+#define CHUNKMIN 1
+#define KB 3
+#endif
+constexpr int kStages = KS, kPairStages = kStages / 2;
 constexpr int kMaxTiles = 64;   // 64-key tiles of an item: up to 32 blocks of 128 keys
 // Weights are p = 2^(s - m) with m kLift below the running maximum, which moves
 // when a score passes it by kTau: 2^kLift <= the largest p < 2^(kLift + kTau),
@@ -58,6 +63,8 @@ struct FwdCacheArgs {
 struct FwdShared {
   alignas(128) uint8_t ring[kStages][kTileBytes];  // reused for the partial outputs
   alignas(8) uint64_t full[kStages], empty[kStages];
+  alignas(16) uint4 q[8][32];  // the 16 query rows as A fragments of the 8 k-steps, by lane
+  float qs[16];              // powers of two that undo their scaling
   int64_t tile[kMaxTiles];   // tile index in the cache
   int32_t key0[kMaxTiles];   // position of its first key
   int32_t ntiles;            // of this CTA
@@ -109,12 +116,42 @@ MSA_DEV float load_q_row(const uint16_t* src, uint32_t (&w)[16]) {
   return __uint_as_float((uint32_t)(e - 14) << 23);
 }
 
-__global__ void __launch_bounds__(kFwdThreads) fwd_cache_kernel(FwdCacheArgs a) {
+// A chunk's selected tiles, by one warp: lane k's block (-1: none), its page and
+// the number of its 64-key tiles that start at or before the chunk's last token.
+// False (and *status) if the chunk row, the selection or a page is bad.
+MSA_DEV bool list_tiles(const FwdCacheArgs& a, const int4& c, int g, int h, int lane, int& b, int& page, int& ntl) {
+  b = -1;
+  page = 0;
+  ntl = 0;
+  int code = MSA_OK;
+  if (c.x >= a.R || c.z < 1 || c.z > kChunk || c.y < 0 || c.y > a.T - c.z || c.w < 0 || c.w % kChunk + c.z > kChunk ||
+      c.w / a.B >= a.M) {
+    code = MSA_ERR_INVALID_CACHE;
+  } else {
+    if (lane < a.K) b = a.sel[((int64_t)h * a.NC + g) * a.K + lane];
+    if (b < 0) b = -1;
+    const unsigned same = __match_any_sync(0xffffffffu, b);
+    if (__any_sync(0xffffffffu, b > c.w / a.B || (b >= 0 && __popc(same) > 1))) {
+      code = MSA_ERR_INVALID_SELECTION;
+    } else if (b >= 0) {
+      page = a.block_table[(int64_t)c.x * a.M + b];
+      ntl = a.B == 128 && b * 128 + 64 <= c.w + c.z - 1 ? 2 : 1;
+    }
+    if (__any_sync(0xffffffffu, page < 0 || page >= a.P)) code = MSA_ERR_INVALID_CACHE;
+  }
+  if (code != MSA_OK) {
+    if (lane == 0) set_status(a.status, code);
+    return false;
+  }
+  return true;
+}
+
+__global__ void __launch_bounds__(kFwdThreads, KB) fwd_cache_kernel(FwdCacheArgs a) {
   extern __shared__ __align__(128) uint8_t s_raw[];
   FwdShared& s = *reinterpret_cast<FwdShared*>(s_raw);
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, pair = warp >> 1;
   const int item = blockIdx.x / ranks, h = blockIdx.y;
   const int g = item / a.slots, slot = item % a.slots;
   // the same for every CTA of the cluster, so all of them leave here or none
@@ -123,33 +160,15 @@ __global__ void __launch_bounds__(kFwdThreads) fwd_cache_kernel(FwdCacheArgs a) 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&s.full[i], 1);
-      mbar_init(&s.empty[i], kConsumers);
+      mbar_init(&s.empty[i], 2);
     }
     fence_mbar_init();
   }
-  if (warp == kConsumers) {
-    // the chunk's tiles: every selected block gives the tiles that start at or
-    // before the chunk's last token; rank takes every ranks-th
-    bool good = !status_bad(a.status) && c.x < a.R && c.z <= kChunk && c.y >= 0 && c.y <= a.T - c.z && c.w >= 0 &&
-                c.w % kChunk + c.z <= kChunk && c.w / a.B < a.M;
-    int code = MSA_ERR_INVALID_CACHE;
-    int b = -1, page = 0, ntl = 0;
-    if (good && lane < a.K) b = a.sel[((int64_t)h * a.NC + g) * a.K + lane];
-    if (good) {
-      const bool far = b >= 0 && b > c.w / a.B;
-      const unsigned same = __match_any_sync(0xffffffffu, b);
-      if (__any_sync(0xffffffffu, far || (b >= 0 && __popc(same) > 1))) {
-        good = false;
-        code = MSA_ERR_INVALID_SELECTION;
-      }
-    }
-    if (good) {
-      if (b >= 0) {
-        page = a.block_table[(int64_t)c.x * a.M + b];
-        ntl = a.B == 128 && b * 128 + 64 <= c.w + c.z - 1 ? 2 : 1;
-      }
-      if (__any_sync(0xffffffffu, b >= 0 && (page < 0 || page >= a.P))) good = false;
-    }
+  if (warp == 0) {
+    // the chunk's tiles; rank takes every ranks-th
+    int b, page, ntl;
+    const bool good = !status_bad(a.status) && list_tiles(a, c, g, h, lane, b, page, ntl);
+    if (!good) ntl = 0;
     int x = ntl;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -165,8 +184,6 @@ __global__ void __launch_bounds__(kFwdThreads) fwd_cache_kernel(FwdCacheArgs a) 
           s.key0[at / ranks] = b * a.B + i * kTile;
         }
       }
-    } else if (lane == 0) {
-      set_status(a.status, code);
     }
     if (lane == 0) {
       s.ntiles = good ? (total - rank + ranks - 1) / ranks : 0;
@@ -179,77 +196,114 @@ __global__ void __launch_bounds__(kFwdThreads) fwd_cache_kernel(FwdCacheArgs a) 
   for (int tok = slot; tok < c.z; tok += a.slots) {
     const int qpos = c.w + tok;
     const int64_t row0 = (int64_t)(c.y + tok) * a.H * kGroup + h * kGroup;
-    const int done = (tok - slot) / a.slots * ntiles;  // tiles of earlier tokens
+    const int pdone = (tok - slot) / a.slots * ((ntiles - pair + 1) / 2);  // the pair's tiles of earlier tokens
     float o[16][4];
     float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
     bool ok = true;
-    int issued = 0;  // copies so far (producer)
-    if (warp == kConsumers) {
-      if (lane == 0) {
-        for (int j = 0; j < ntiles; ++j) {
-          const int n = done + j, st = n % kStages, lap = n / kStages;
-          if (lap > 0 && !(ok = mbar_wait(&s.empty[st], (lap - 1) & 1, a.status))) break;
-          mbar_arrive_expect_tx(&s.full[st], kTileBytes);
-          bulk_load(s.ring[st], a.cache + s.tile[j] * kTileBytes, kTileBytes, &s.full[st]);
-          issued = n + 1;
-        }
-      }
-      __syncwarp();
-    } else {
+    // tiles of this warp's pair: pair, pair + 2, ..., in the pair's own stages
+    const int mine = (ntiles - pair + 1) / 2, ptotal = pdone + mine;
+    int issued = pdone;  // copies so far (the pair's first lane)
+    auto issue = [&] {
+      const int st = pair * kPairStages + issued % kPairStages;
+      mbar_arrive_expect_tx(&s.full[st], kTileBytes);
+      bulk_load(s.ring[st], a.cache + s.tile[2 * (issued - pdone) + pair] * kTileBytes, kTileBytes, &s.full[st]);
+      ++issued;
+    };
+    const bool loader = (warp & 1) == 0 && lane == 0;
+    if (loader)
+      while (issued < ptotal && issued < pdone + kPairStages) issue();
+    {
       const int gid = lane >> 2, t = lane & 3;
-      uint32_t q0[16], q1[16];
-      const uint16_t* src = a.q + (row0 + gid) * 128 + 32 * t;
-      const float sc0 = load_q_row(src, q0) * a.scale_log2;
-      const float sc1 = load_q_row(src + 8 * 128, q1) * a.scale_log2;
+      if (warp == 3) {
+        // warp 0 has the selection, warps 0 and 2 the first copies to see to
+        uint32_t q0[16], q1[16];
+        const uint16_t* src = a.q + (row0 + gid) * 128 + 32 * t;
+        const float x0 = load_q_row(src, q0), x1 = load_q_row(src + 8 * 128, q1);
+        if (t == 0) {
+          s.qs[gid] = x0;
+          s.qs[gid + 8] = x1;
+        }
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) s.q[ks][lane] = make_uint4(q0[2 * ks], q1[2 * ks], q0[2 * ks + 1], q1[2 * ks + 1]);
+      }
+      __syncthreads();
+      const float sc0 = s.qs[gid] * a.scale_log2, sc1 = s.qs[gid + 8] * a.scale_log2;
 #pragma unroll
       for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-      for (int j = 0; j < ntiles; ++j) {
-        const int n = done + j, st = n % kStages;
-        ok = __all_sync(0xffffffffu, mbar_wait(&s.full[st], (n / kStages) & 1, a.status));
+      for (int n = pdone; n < ptotal; ++n) {
+        const int st = pair * kPairStages + n % kPairStages;
+        ok = __all_sync(0xffffffffu, mbar_wait(&s.full[st], (n / kPairStages) & 1, a.status));
         if (!ok) break;
         const uint8_t* tile = s.ring[st];
-        const int k0 = s.key0[j] + 16 * warp;  // position of the warp's first key
+        const int kw = 32 * (warp & 1);                              // the warp's first key in the tile
+        const int k0 = s.key0[2 * (n - pdone) + pair] + kw;          // and its position
         if (k0 <= qpos) {
-          // S = Q K^T: column n of n-tile jj is key 4 (n >> 1) + 2 jj + (n & 1),
-          // k-step ks contracts dims 32 t + 4 ks .. + 3 of each lane t
-          float sv[2][4];
+          // S = Q K^T: column c of n-tile jj is key 16 (jj >> 1) + 4 (c >> 1) +
+          // 2 (jj & 1) + (c & 1), k-step ks contracts dims 32 t + 4 ks .. + 3 of
+          // each lane t.  The four n-tiles' chains are interleaved.
+          float sv[4][4];
+          uint4 kc[4];
+          uint32_t ksc[4];
 #pragma unroll
-          for (int jj = 0; jj < 2; ++jj) {
-            const int key = 16 * warp + 4 * (gid >> 1) + 2 * jj + (gid & 1);
-            const uint4 kc = *reinterpret_cast<const uint4*>(tile + OFF_KC + key * kRowBytes + t * 16);
-            const uint32_t sh =
-                e4m3x2_to_half(*reinterpret_cast<const uint16_t*>(tile + OFF_KS + key * kScales + 2 * t));
-            const uint32_t s0 = __byte_perm(sh, sh, 0x1010), s1 = __byte_perm(sh, sh, 0x3232);
-            const uint32_t w[4] = {kc.x, kc.y, kc.z, kc.w};
+          for (int jj = 0; jj < 4; ++jj) {
+            const int key = kw + 16 * (jj >> 1) + 4 * (gid >> 1) + 2 * (jj & 1) + (gid & 1);
+            kc[jj] = *reinterpret_cast<const uint4*>(tile + OFF_KC + key * kRowBytes + t * 16);
+            ksc[jj] = e4m3x2_to_half(*reinterpret_cast<const uint16_t*>(tile + OFF_KS + key * kScales + 2 * t));
             sv[jj][0] = sv[jj][1] = sv[jj][2] = sv[jj][3] = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t hk[4];
-              e2m1x8_to_half(w[i], hk);
-              const uint32_t sc = i < 2 ? s0 : s1;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) hk[e] = mul_half2(hk[e], sc);
-              mma_f16(sv[jj], q0[4 * i], q1[4 * i], q0[4 * i + 1], q1[4 * i + 1], hk[0], hk[1]);
-              mma_f16(sv[jj], q0[4 * i + 2], q1[4 * i + 2], q0[4 * i + 3], q1[4 * i + 3], hk[2], hk[3]);
-            }
           }
-          // the lane's keys: 4 t + 2 jj + e; rows gid and gid + 8
-          uint32_t vs = *reinterpret_cast<const uint32_t*>(tile + OFF_VS + gid * kTile + 16 * warp + 4 * t);
-          float bm0 = -CUDART_INF_F, bm1 = -CUDART_INF_F;
-          const int left = qpos - k0 - 4 * t;  // keys 0 .. left of the lane's four may be attended
 #pragma unroll
-          for (int jj = 0; jj < 2; ++jj)
+          for (int i = 0; i < 4; ++i) {
+            uint32_t hk[4][4];
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+              e2m1x8_to_half(i == 0 ? kc[jj].x : i == 1 ? kc[jj].y : i == 2 ? kc[jj].z : kc[jj].w, hk[jj]);
+              const uint32_t sc = __byte_perm(ksc[jj], ksc[jj], i < 2 ? 0x1010 : 0x3232);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) hk[jj][e] = mul_half2(hk[jj][e], sc);
+            }
+            const uint4 qa = s.q[2 * i][lane], qb = s.q[2 * i + 1][lane];
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) mma_f16(sv[jj], qa.x, qa.y, qa.z, qa.w, hk[jj][0], hk[jj][1]);
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) mma_f16(sv[jj], qb.x, qb.y, qb.z, qb.w, hk[jj][2], hk[jj][3]);
+          }
+          // the lane's keys: 16 (jj >> 1) + 4 t + 2 (jj & 1) + e; rows gid and gid + 8
+          float bm0 = -CUDART_INF_F, bm1 = -CUDART_INF_F;
+          const int left = qpos - k0 - 4 * t;  // its keys up to this one may be attended
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const bool in = 2 * jj + e <= left;
-              sv[jj][e] = in ? sv[jj][e] * sc0 : -CUDART_INF_F;
-              sv[jj][2 + e] = in ? sv[jj][2 + e] * sc1 : -CUDART_INF_F;
-              bm0 = fmaxf(bm0, sv[jj][e]);
-              bm1 = fmaxf(bm1, sv[jj][2 + e]);
+              sv[jj][e] *= sc0;
+              sv[jj][2 + e] *= sc1;
             }
-          // keys that may not be attended hold anything: a zero scale makes
-          // their values zero (a code alone is always finite)
-          if (left < 3) vs = left < 0 ? 0u : vs & (0xFFFFFFFFu >> (8 * (3 - left)));
+          uint32_t vs[2];
+#pragma unroll
+          for (int st2 = 0; st2 < 2; ++st2)
+            vs[st2] = *reinterpret_cast<const uint32_t*>(tile + OFF_VS + gid * kTile + kw + 16 * st2 + 4 * t);
+          if (k0 + 31 > qpos) {
+            // keys that may not be attended hold anything: their scores are
+            // replaced, and a zero scale makes their values zero (a code alone is
+            // always finite)
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const bool in = 16 * (jj >> 1) + 2 * (jj & 1) + e <= left;
+                sv[jj][e] = in ? sv[jj][e] : -CUDART_INF_F;
+                sv[jj][2 + e] = in ? sv[jj][2 + e] : -CUDART_INF_F;
+              }
+#pragma unroll
+            for (int st2 = 0; st2 < 2; ++st2) {
+              const int lf = left - 16 * st2;
+              if (lf < 3) vs[st2] = lf < 0 ? 0u : vs[st2] & (0xFFFFFFFFu >> (8 * (3 - lf)));
+            }
+          }
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj) {
+            bm0 = fmaxf(bm0, fmaxf(sv[jj][0], sv[jj][1]));
+            bm1 = fmaxf(bm1, fmaxf(sv[jj][2], sv[jj][3]));
+          }
           bm0 = fmaxf(bm0, __shfl_xor_sync(0xffffffffu, bm0, 1));
           bm1 = fmaxf(bm1, __shfl_xor_sync(0xffffffffu, bm1, 1));
           bm0 = fmaxf(bm0, __shfl_xor_sync(0xffffffffu, bm0, 2));
@@ -271,9 +325,9 @@ __global__ void __launch_bounds__(kFwdThreads) fwd_cache_kernel(FwdCacheArgs a) 
             }
           }
           const float m0 = m[0] == -CUDART_INF_F ? 0.f : m[0], m1 = m[1] == -CUDART_INF_F ? 0.f : m[1];
-          uint32_t pa[4];
+          uint32_t pa[8];
 #pragma unroll
-          for (int jj = 0; jj < 2; ++jj) {
+          for (int jj = 0; jj < 4; ++jj) {
             const float p0 = ex2_approx(sv[jj][0] - m0), p1 = ex2_approx(sv[jj][1] - m0);
             const float p2 = ex2_approx(sv[jj][2] - m1), p3 = ex2_approx(sv[jj][3] - m1);
             l[0] += p0 + p1;
@@ -282,36 +336,45 @@ __global__ void __launch_bounds__(kFwdThreads) fwd_cache_kernel(FwdCacheArgs a) 
             pa[2 * jj] = pack_half2(p0, p1);
             pa[2 * jj + 1] = pack_half2(p2, p3);
           }
-          // O += P V: column n = gid of n-tile j is dim 16 gid + j, so a lane's
-          // V words are one scale group of its four keys
-          uint32_t vw[4][2];
+          // O += P V: column c = gid of n-tile j is dim 16 gid + j, so a lane's
+          // V words are one scale group of its four keys of each 16
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint2 x =
-                *reinterpret_cast<const uint2*>(tile + OFF_VC + v_code_offset(16 * warp + 4 * t + e, gid));
-            vw[e][0] = x.x;
-            vw[e][1] = x.y;
-          }
-          const uint32_t s01 = e4m3x2_to_half(vs & 0xFFFFu), s23 = e4m3x2_to_half(vs >> 16);
+          for (int st2 = 0; st2 < 2; ++st2) {
+            const uint32_t* p4 = &pa[4 * st2];
+            uint2 vw[4];
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            // bytes of two keys' codes at one dim, even and odd dims apart
-            constexpr uint32_t LO = 0x0F0F0F0Fu;
-            uint32_t ev01[4], od01[4], ev23[4], od23[4];
-            e2m1x8_to_half((vw[0][w] & LO) | ((vw[1][w] << 4) & ~LO), ev01);
-            e2m1x8_to_half(((vw[0][w] >> 4) & LO) | (vw[1][w] & ~LO), od01);
-            e2m1x8_to_half((vw[2][w] & LO) | ((vw[3][w] << 4) & ~LO), ev23);
-            e2m1x8_to_half(((vw[2][w] >> 4) & LO) | (vw[3][w] & ~LO), od23);
+            for (int e = 0; e < 4; ++e)
+              vw[e] = *reinterpret_cast<const uint2*>(tile + OFF_VC + v_code_offset(kw + 16 * st2 + 4 * t + e, gid));
+            const uint32_t s01 = e4m3x2_to_half(vs[st2] & 0xFFFFu), s23 = e4m3x2_to_half(vs[st2] >> 16);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              mma_f16(o[8 * w + 2 * i], pa[0], pa[1], pa[2], pa[3], mul_half2(ev01[i], s01), mul_half2(ev23[i], s23));
-              mma_f16(o[8 * w + 2 * i + 1], pa[0], pa[1], pa[2], pa[3], mul_half2(od01[i], s01),
-                      mul_half2(od23[i], s23));
+            for (int w = 0; w < 2; ++w) {
+              // bytes of two keys' codes at one dim, even and odd dims apart
+              constexpr uint32_t LO = 0x0F0F0F0Fu;
+              const uint32_t w0 = w ? vw[0].y : vw[0].x, w1 = w ? vw[1].y : vw[1].x;
+              const uint32_t w2 = w ? vw[2].y : vw[2].x, w3 = w ? vw[3].y : vw[3].x;
+              uint32_t ev01[4], od01[4], ev23[4], od23[4];
+              e2m1x8_to_half((w0 & LO) | ((w1 << 4) & ~LO), ev01);
+              e2m1x8_to_half((w2 & LO) | ((w3 << 4) & ~LO), ev23);
+              e2m1x8_to_half(((w0 >> 4) & LO) | (w1 & ~LO), od01);
+              e2m1x8_to_half(((w2 >> 4) & LO) | (w3 & ~LO), od23);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                mma_f16(o[8 * w + 2 * i], p4[0], p4[1], p4[2], p4[3], mul_half2(ev01[i], s01),
+                        mul_half2(ev23[i], s23));
+                mma_f16(o[8 * w + 2 * i + 1], p4[0], p4[1], p4[2], p4[3], mul_half2(od01[i], s01),
+                        mul_half2(od23[i], s23));
+              }
             }
           }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.empty[st]);
+        // refill the stage of the tile before: its other reader is rarely late
+        if (loader && n > pdone && issued < ptotal) {
+          const int pn = n - 1;
+          if (mbar_wait(&s.empty[pair * kPairStages + pn % kPairStages], (pn / kPairStages) & 1, a.status)) issue();
+        }
+        __syncwarp();
       }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -322,15 +385,15 @@ __global__ void __launch_bounds__(kFwdThreads) fwd_cache_kernel(FwdCacheArgs a) 
     // every tile has landed and been read; after a wait that gave up, copies
     // may be in flight: they land before the CTA's shared memory is let go
     const bool bad = __syncthreads_or(!ok);
-    if (bad && warp == kConsumers && lane == 0) {
-      for (int n = max(issued - kStages, 0); n < issued; ++n)
-        mbar_wait(&s.full[n % kStages], (n / kStages) & 1, a.status);
+    if (bad && loader) {
+      for (int n = max(issued - kPairStages, pdone); n < issued; ++n)
+        mbar_wait(&s.full[pair * kPairStages + n % kPairStages], (n / kPairStages) & 1, a.status);
       s.skip = 1;
     }
     // join the warps: partial outputs in the ring, [warp][16 rows][128 dims],
     // 16-byte units XORed by row so that neither side conflicts
     float* part = reinterpret_cast<float*>(&s.ring[0][0]);
-    if (warp < kConsumers && !bad) {
+    if (!bad) {
       const int gid = lane >> 2, t = lane & 3;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -353,7 +416,7 @@ __global__ void __launch_bounds__(kFwdThreads) fwd_cache_kernel(FwdCacheArgs a) 
     }
     __syncthreads();
     bool skip = bad;
-    if (warp < kConsumers && !bad) {
+    if (!bad) {
       // thread: one row, 16 dims (units 4 cg .. 4 cg + 3)
       const int row = tid >> 3, cg8 = tid & 7;
       float mm = s.m[0][row];
@@ -404,7 +467,7 @@ __global__ void __launch_bounds__(kFwdThreads) fwd_cache_kernel(FwdCacheArgs a) 
       for (int r = 0; r < ranks; ++r) skip |= *cluster.map_shared_rank(&s.skip, r) != 0;
       // rank joins rows rank * 16 / ranks ..: a warp takes a row, a lane 4 dims
       const int rows = 16 / ranks;
-      for (int i = warp; i < rows && !skip; i += kConsumers + 1) {
+      for (int i = warp; i < rows && !skip; i += kConsumers) {
         const int row = rank * rows + i, unit = lane;
         float mm = -CUDART_INF_F;
         for (int r = 0; r < ranks; ++r) mm = fmaxf(mm, *cluster.map_shared_rank(&s.cm[row], r));
@@ -441,6 +504,8 @@ __global__ void __launch_bounds__(kFwdThreads) fwd_cache_kernel(FwdCacheArgs a) 
 }  // namespace cache
 }  // namespace msa
 
+#include "msa_cache_chunk.cuh"
+
 using namespace msa;
 
 extern "C" int msa_cache_fwd(const msa_cache_problem* p, const uint16_t* q, const uint8_t* kv_cache,
@@ -461,6 +526,25 @@ extern "C" int msa_cache_fwd(const msa_cache_problem* p, const uint16_t* q, cons
   a.scale_log2 = p->softmax_scale * cache::exp2i(p->k_exp) * cache::kLog2e;
   a.v_mul = cache::exp2i(p->v_exp);
   a.status = d_status;
+  // Chunks of several tokens (more token rows than chunk rows) in batches that
+  // fill the GPU: the 128-row kernel.
+  if (p->token_cap > p->chunk_cap && (int64_t)p->chunk_cap * p->num_kv_heads >= CHUNKMIN) {
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, cache::chunk::fwd_chunk_kernel) != cudaSuccess) return MSA_ERR_CUDA;
+    // the warpgroups' register shares add up to the launch's registers, or
+    // setmaxnreg would wait for ever
+    if (attr.numRegs * 3 < 136 + 72 + 32) return MSA_ERR_CUDA;
+    if (cudaFuncSetAttribute(cache::chunk::fwd_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)cache::chunk::SMEM) != cudaSuccess ||
+        cudaFuncSetAttribute(cache::chunk::fwd_chunk_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             (int)cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+      return MSA_ERR_CUDA;
+    const int64_t chunks = (int64_t)p->chunk_cap * p->num_kv_heads;
+    const int grid = (int)(chunks < 2 * sms ? chunks : 2 * sms);
+    cache::chunk::fwd_chunk_kernel<<<grid, cache::chunk::kThreads, cache::chunk::SMEM,
+                                     static_cast<cudaStream_t>(stream)>>>(a);
+    return cuda_status(cudaGetLastError());
+  }
   // Token slots of a chunk: its mean number of tokens, at most 8.  A chunk
   // with more tokens than slots takes them in turn.
   a.slots = (int)((p->token_cap + (int64_t)p->chunk_cap - 1) / p->chunk_cap);
@@ -472,9 +556,7 @@ extern "C" int msa_cache_fwd(const msa_cache_problem* p, const uint16_t* q, cons
   int ranks = 1;
   while (ranks < 8 && ranks * 2 <= tiles && items * p->num_kv_heads * ranks * 2 <= 2 * sms) ranks *= 2;
   if (items * ranks > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
-  if ((rc = cuda_status(cudaFuncSetAttribute(cache::fwd_cache_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)sizeof(cache::FwdShared)))))
-    return rc;
+  if ((rc = cuda_status(allow_smem(cache::fwd_cache_kernel, sizeof(cache::FwdShared))))) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items * ranks), (unsigned)p->num_kv_heads);
   cfg.blockDim = dim3(cache::kFwdThreads);

@@ -49,6 +49,15 @@ size_t bwd_ws_bytes(const msa_problem* p, bool dq_fp32);
 int sm_count_current(int32_t* out);
 int check_device_current();
 
+// Dynamic shared memory above 48 KB (with the static part) needs the kernel's
+// leave; well below that the call
+// is left out (it costs a good part of a launch).
+template <class F>
+inline cudaError_t allow_smem(F* fn, size_t bytes) {
+  if (bytes <= 32 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
 inline int cuda_status(cudaError_t e) { return e == cudaSuccess ? MSA_OK : MSA_ERR_CUDA; }
 
 }  // namespace msa
