@@ -267,19 +267,20 @@ MSA_DEV void row_of(int64_t u, int heads, int& t, int& h) {
   h = (int)(quad - tq * heads);
   t = (int)(tq * 4 + (u & 3));
 }
-inline int64_t row_blocks(int64_t tokens, int64_t heads) { return ((tokens + 3) / 4 * 4 * heads * 8 + 255) / 256; }
+inline int64_t row_blocks(int64_t tokens, int64_t heads, int64_t rows) {  // CTAs of `rows` rows
+  return ((tokens + 3) / 4 * 4 * heads + rows - 1) / rows;
+}
 
-// 16 bf16 values as fp32 (exact), two 16-byte loads.
-MSA_DEV void load16(const uint16_t* src, float (&x)[16], uint32_t& amax) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(src)), b = __ldg(reinterpret_cast<const uint4*>(src) + 1);
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  amax = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    amax = max(amax, max((w[i] << 16) & 0x7FFFFFFFu, w[i] & 0x7FFF0000u));
-  }
+// 32 bytes in one load or store (a whole sector a lane); read-only data.
+MSA_DEV void load32(const void* src, uint32_t (&u)[8]) {
+  asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+      : "l"(src));
+}
+MSA_DEV void store32(void* dst, const uint32_t (&u)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(u[0]), "r"(u[1]), "r"(u[2]),
+               "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+               : "memory");
 }
 
 // Clears the sign of the codes that are zero, so that equal values have equal
@@ -289,32 +290,40 @@ MSA_DEV uint32_t unsigned_zeros(uint32_t w) {
   return w & (((m << 1 | m << 2 | m << 3) & 0x88888888u) | 0x77777777u);
 }
 
-// One group of 16 values to codes (8 bytes) and an e4m3 scale.  The quotient
-// x / s is formed as x * (1 / s): it is either a border between two codes (a
-// multiple of 1/4) or at least 2^-11 away from it, because x has 8 significant
-// bits and border * s 7.  Rounding it to a multiple of 2^-14 (the addition of
-// 1.5 * 2^9) therefore undoes the reciprocal's error, and the conversion's ties
-// are those of the exact quotient.
-MSA_DEV uint32_t quantize16(const float (&x)[16], uint32_t amax_bits, float mul, uint2& codes) {
+// One group of 16 bf16 values (8 words) to codes (8 bytes) and an e4m3 scale.
+// Quotients are formed so that the conversions' ties are those of the exact
+// ones: max / 6 with one correction step (exact where the quotient has 24 bits,
+// as every midpoint of two scales does), and x / s as x * (1 / s), which is
+// either a border between two codes (a multiple of 1/4) or at least 2^-11 away
+// from it, because x has 8 significant bits and border * s 7; rounding it to a
+// multiple of 2^-14 (the addition of 1.5 * 2^9) undoes the reciprocal's error.
+MSA_DEV uint32_t quantize16(const uint32_t (&w)[8], float mul, uint2& codes) {
   codes = make_uint2(0, 0);
-  if (amax_bits >= 0x7F800000u) return 0x7F;  // a NaN scale: the group reads back as NaN
-  // amax <= 2^128 and mul <= 2^32: an overflow to infinity saturates below
-  const float t = __fdiv_rn(__uint_as_float(amax_bits) * mul, 6.f);
+  uint32_t m2 = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m2 = __vmaxu2(m2, w[i] & 0x7FFF7FFFu);
+  const uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+  if (m >= 0x7F80u) return 0x7F;  // a NaN scale: the group reads back as NaN
+  // max * mul may overflow to infinity: the scale saturates, and so do the codes
+  const float amax = __uint_as_float(m << 16) * mul;
+  constexpr float kSixth = 1.f / 6.f;
+  const float t0 = amax * kSixth;
+  const float t = amax < 4096.f ? __fmaf_rn(__fmaf_rn(-6.f, t0, amax), kSixth, t0) : t0;  // far above 6 * 448
   uint16_t s2;
-  asm("{\n\tcvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n\t}" : "=h"(s2) : "f"(0.f), "f"(t));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s2) : "f"(0.f), "f"(t));
   const uint32_t s8 = s2 & 0xFFu;
   if (s8 == 0) return 0;
-  const uint32_t sh = e4m3x2_to_half(s8);
-  const float s = __half2float(__ushort_as_half((uint16_t)(sh & 0xFFFFu)));
-  const float inv = __fdiv_rn(1.f, s) * mul;  // a power of two apart, exact
+  const float s = __half2float(__ushort_as_half((uint16_t)(e4m3x2_to_half(s8) & 0xFFFFu)));
+  const float inv = __frcp_rn(s) * mul;
   uint32_t out[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     float q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float y = fminf(fmaxf(x[8 * h + i] * inv, -8.f), 8.f);
-      q[i] = __fadd_rn(__fadd_rn(y, 768.f), -768.f);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = w[4 * h + i];
+      q[2 * i] = __fadd_rn(__fmaf_rn(__uint_as_float(x << 16), inv, 768.f), -768.f);
+      q[2 * i + 1] = __fadd_rn(__fmaf_rn(__uint_as_float(x & 0xFFFF0000u), inv, 768.f), -768.f);
     }
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
@@ -408,7 +417,7 @@ MSA_DEV void index_chunk(const AppendArgs& a, int g, int h, int half, int lane) 
   }
 }
 
-__global__ void __launch_bounds__(256, 4) append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(256, 6) append_kernel(AppendArgs a) {
   if (status_bad(a.status)) return;
   if ((int)blockIdx.x < a.index_blocks) {
     const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
@@ -428,13 +437,11 @@ __global__ void __launch_bounds__(256, 4) append_kernel(AppendArgs a) {
     if (slot != -1) set_status(a.status, MSA_ERR_INVALID_CACHE);
     return;
   }
-  float x[16];
-  uint32_t amax;
+  uint32_t kw[8], vw[8];
+  load32(a.k + row * 128 + grp * 16, kw);
+  load32(a.v + row * 128 + grp * 16, vw);
   uint2 kc, vc;
-  load16(a.k + row * 128 + grp * 16, x, amax);
-  const uint32_t ks = quantize16(x, amax, a.k_mul, kc);
-  load16(a.v + row * 128 + grp * 16, x, amax);
-  const uint32_t vs = quantize16(x, amax, a.v_mul, vc);
+  const uint32_t ks = quantize16(kw, a.k_mul, kc), vs = quantize16(vw, a.v_mul, vc);
   const int lb = a.B == 128 ? 7 : 6;  // log2 of the block
   const int off = (int)(slot & (a.B - 1)), tok = off % kTile;
   uint8_t* tile = a.cache + tile_index(slot >> lb, h, a.H, a.B / kTile, off / kTile) * kTileBytes;
@@ -470,30 +477,50 @@ MSA_DEV void dequantize16(uint2 codes, uint32_t scale, float mul, uint16_t* dst)
                                    __half2float(__ushort_as_half((uint16_t)(y >> 16))) * mul);
     }
   }
-  reinterpret_cast<uint4*>(dst)[0] = make_uint4(out[0], out[1], out[2], out[3]);
-  reinterpret_cast<uint4*>(dst)[1] = make_uint4(out[4], out[5], out[6], out[7]);
+  store32(dst, out);
 }
 
+// A thread takes the same group of two rows, so that two chains of loads (slot,
+// then codes and scales) are in flight: the kernel is bound by their latency.
 __global__ void __launch_bounds__(256) read_kernel(ReadArgs a) {
   if (status_bad(a.status)) return;
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int grp = (int)(i & 7);
-  int t, h;
-  row_of(i >> 3, a.H, t, h);
-  if (t >= a.T) return;
-  const int64_t row = (int64_t)t * a.H + h;
-  const int64_t slot = a.slots[t];
-  if (slot < 0 || slot >= a.nslots) {
-    if (slot != -1) set_status(a.status, MSA_ERR_INVALID_CACHE);
-    return;
-  }
+  const int grp = threadIdx.x & 7;
   const int lb = a.B == 128 ? 7 : 6;  // log2 of the block
-  const int off = (int)(slot & (a.B - 1)), tok = off % kTile;
-  const uint8_t* tile = a.cache + tile_index(slot >> lb, h, a.H, a.B / kTile, off / kTile) * kTileBytes;
-  dequantize16(*reinterpret_cast<const uint2*>(tile + OFF_KC + tok * kRowBytes + grp * 8),
-               tile[OFF_KS + tok * kScales + grp], a.k_mul, a.k + row * 128 + grp * 16);
-  dequantize16(*reinterpret_cast<const uint2*>(tile + OFF_VC + v_code_offset(tok, grp)),
-               tile[OFF_VS + grp * kTile + tok], a.v_mul, a.v + row * 128 + grp * 16);
+  const uint8_t* tile[2];
+  int64_t row[2];
+  int tok[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    int t, h;
+    row_of(((int64_t)blockIdx.x * 2 + i) * (256 / 8) + (threadIdx.x >> 3), a.H, t, h);
+    tile[i] = nullptr;
+    if (t >= a.T) continue;
+    const int64_t slot = a.slots[t];
+    if (slot < 0 || slot >= a.nslots) {
+      if (slot != -1) set_status(a.status, MSA_ERR_INVALID_CACHE);
+      continue;
+    }
+    const int off = (int)(slot & (a.B - 1));
+    row[i] = ((int64_t)t * a.H + h) * 128 + grp * 16;
+    tok[i] = off % kTile;
+    tile[i] = a.cache + tile_index(slot >> lb, h, a.H, a.B / kTile, off / kTile) * kTileBytes;
+  }
+  uint2 kc[2], vc[2];
+  uint32_t ks[2], vs[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (!tile[i]) continue;
+    kc[i] = *reinterpret_cast<const uint2*>(tile[i] + OFF_KC + tok[i] * kRowBytes + grp * 8);
+    vc[i] = *reinterpret_cast<const uint2*>(tile[i] + OFF_VC + v_code_offset(tok[i], grp));
+    ks[i] = tile[i][OFF_KS + tok[i] * kScales + grp];
+    vs[i] = tile[i][OFF_VS + grp * kTile + tok[i]];
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (!tile[i]) continue;
+    dequantize16(kc[i], ks[i], a.k_mul, a.k + row[i]);
+    dequantize16(vc[i], vs[i], a.v_mul, a.v + row[i]);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -506,14 +533,6 @@ struct SelectArgs {
   int R, P, M, B, T, NC, H, K;
   int32_t* status;
 };
-constexpr int kSelThreads = 256;
-
-// 32 bytes in one load (a whole sector a lane), read-only data.
-MSA_DEV void load32(const void* src, uint32_t (&u)[8]) {
-  asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
-      : "l"(src));
-}
 
 // A score as an unsigned key of the same order (-0 counts as +0).
 MSA_DEV uint32_t score_key(float s) {
@@ -521,17 +540,19 @@ MSA_DEV uint32_t score_key(float s) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+constexpr int kCand = 128;  // candidates that the final ranking takes
+
 // Scratch of one row's selection.
 struct SelectScratch {
-  uint32_t hist[256];
-  uint32_t prefix, need, count;
-  uint32_t topk[kMaxTopk];
-  int topb[kMaxTopk];
+  uint32_t hist[256];        // digit d at [(255 - d) % 8][(255 - d) / 8]: a lane's eight lie in eight rows
+  uint32_t prefix, need, bin, count;
+  uint64_t cand[kCand];      // key, then the complement of the block: a larger number is better
 };
 
-// The topk - 1 largest of n keys, by NT threads (a warp, or the whole CTA): a
-// radix selection of the keep-th largest key, 8 bits a pass, then the keys above
-// it, of those equal to it the lowest blocks, and their ranks.
+// The topk - 1 best of n keys, by NT threads (a warp, or the whole CTA).  A
+// radix selection of the keep-th largest key, 8 bits a pass, until the keys of
+// the threshold's digits and above are few (two passes but for heavy ties); those
+// are then ranked against one another as (key, block), which settles ties.
 template <int NT>
 __device__ void select_row(const uint32_t* key, int n, int K, SelectScratch& s, int32_t* out) {
   const int tid = threadIdx.x % NT, lane = tid & 31;
@@ -542,115 +563,177 @@ __device__ void select_row(const uint32_t* key, int n, int K, SelectScratch& s, 
   if (tid == 0) {
     s.prefix = 0;
     s.need = keep;
+    s.bin = n;
     s.count = 0;
   }
-  if (keep > 0 && keep < n) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += NT) s.hist[i] = 0;
-      sync();
-      const uint32_t prefix = s.prefix, need = s.need;
-      const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
+  sync();
+  int shift = 32;  // digits above this are settled: keys >= prefix in them are candidates
+  while (shift > 0 && (uint32_t)keep - s.need + s.bin > (uint32_t)kCand) {
+    shift -= 8;
+    for (int i = tid; i < 256; i += NT) s.hist[i] = 0;
+    const uint32_t prefix = s.prefix, need = s.need;
+    sync();
+    const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
+    for (int b = tid; b < n; b += NT) {
+      const uint32_t k = key[b];
+      if ((k & mask) == prefix) {
+        const uint32_t e = 255 - ((k >> shift) & 255);
+        atomicAdd(&s.hist[(e & 7) * 32 + (e >> 3)], 1u);
+      }
+    }
+    sync();
+    if (tid < 32) {
+      // digits from the top: lane l holds digits 255 - 8l .. 248 - 8l
+      uint32_t cnt[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) { cnt[i] = s.hist[i * 32 + lane]; sum += cnt[i]; }
+      uint32_t inc = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      uint32_t above = inc - sum;
+      if (above < need && inc >= need) {
+        int i = 0;
+        for (; i < 7; ++i) {
+          if (above + cnt[i] >= need) break;
+          above += cnt[i];
+        }
+        s.prefix = prefix | ((uint32_t)(255 - 8 * lane - i) << shift);
+        s.need = need - above;
+        s.bin = cnt[i];
+      }
+    }
+    sync();
+  }
+  const uint32_t prefix = s.prefix;  // keys >= it are candidates, keep - need of them above its digits
+  if (keep > 0) {
+    if (shift > 0 || (uint32_t)keep - s.need + s.bin <= (uint32_t)kCand) {
       for (int b = tid; b < n; b += NT)
-        if ((key[b] & mask) == prefix) atomicAdd(&s.hist[(key[b] >> shift) & 255], 1u);
+        if (key[b] >= prefix) s.cand[atomicAdd(&s.count, 1u)] = (uint64_t)key[b] << 32 | (uint32_t)~b;
+      sync();
+    } else {
+      // more equal keys than the list holds: those above, then the lowest blocks
+      for (int b = tid; b < n; b += NT)
+        if (key[b] > prefix) s.cand[atomicAdd(&s.count, 1u)] = (uint64_t)key[b] << 32 | (uint32_t)~b;
       sync();
       if (tid < 32) {
-        // digits from the top: lane l holds digits 255 - 8l .. 248 - 8l
-        uint32_t cnt[8], sum = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) { cnt[i] = s.hist[255 - 8 * lane - i]; sum += cnt[i]; }
-        uint32_t inc = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += y;
+        uint32_t at = s.count, need = s.need;
+        for (int b0 = 0; b0 < n && need; b0 += 32) {
+          const bool eq = b0 + lane < n && key[b0 + lane] == prefix;
+          const uint32_t m = __ballot_sync(0xffffffffu, eq);
+          const uint32_t before = __popc(m & ((1u << lane) - 1u));
+          if (eq && before < need) s.cand[at + before] = (uint64_t)prefix << 32 | (uint32_t)~(b0 + lane);
+          const uint32_t got = min((uint32_t)__popc(m), need);
+          at += got;
+          need -= got;
         }
-        uint32_t above = inc - sum;
-        if (above < need && inc >= need) {
-          int i = 0;
-          for (; i < 7; ++i) {
-            if (above + cnt[i] >= need) break;
-            above += cnt[i];
-          }
-          s.prefix = prefix | ((uint32_t)(255 - 8 * lane - i) << shift);
-          s.need = need - above;
-        }
+        if (lane == 0) s.count = at;
       }
       sync();
     }
-  } else {
-    sync();
-  }
-  const uint32_t thr = s.prefix;  // 0 where every block is kept
-  if (keep > 0) {
-    for (int b = tid; b < n; b += NT)
-      if (keep == n || key[b] > thr) {
-        const uint32_t at = atomicAdd(&s.count, 1u);
-        s.topk[at] = key[b];
-        s.topb[at] = b;
-      }
-    sync();
-    if (tid < 32 && keep < n) {
-      uint32_t at = s.count, need = s.need;
-      for (int b0 = 0; b0 < n && need; b0 += 32) {
-        const bool eq = b0 + lane < n && key[b0 + lane] == thr;
-        const uint32_t m = __ballot_sync(0xffffffffu, eq);
-        const uint32_t before = __popc(m & ((1u << lane) - 1u));
-        if (eq && before < need) {
-          s.topk[at + before] = thr;
-          s.topb[at + before] = b0 + lane;
-        }
-        const uint32_t got = min((uint32_t)__popc(m), need);
-        at += got;
-        need -= got;
-      }
-    }
-    sync();
-  }
-  // rank among the kept: higher key first, then the lower block
-  if (tid < K) {
-    if (tid == 0) out[0] = n;
-    if (tid < keep) {
+    const int count = (int)s.count;
+    for (int i = tid; i < count; i += NT) {
+      const uint64_t mine = s.cand[i];
       int rank = 0;
-      for (int i = 0; i < keep; ++i)
-        rank += s.topk[i] > s.topk[tid] || (s.topk[i] == s.topk[tid] && s.topb[i] < s.topb[tid]);
-      out[1 + rank] = s.topb[tid];
+#pragma unroll 4
+      for (int j = 0; j < count; ++j) rank += s.cand[j] > mine;
+      if (rank < keep) out[1 + rank] = (int32_t)~(uint32_t)mine;
     }
-    if (tid > keep) out[tid] = -1;
   }
+  if (tid == 0) out[0] = n;
+  for (int i = tid; i < K; i += NT)
+    if (i > keep) out[i] = -1;
 }
 
 // A CTA scores G consecutive chunks of one head (G = 1, or 8: one warp's
-// selection each).  The keys of a request are read once for all of its chunks
-// in the CTA: a thread takes a block, so every score keeps its order of
-// additions, and reads its 256-byte pooled key as whole sectors.
-// Bound at G = 1 by those reads, at G = 8 by the FMAs (one per dim, block and
-// chunk) and the selection.
-template <int G>
-__global__ void __launch_bounds__(kSelThreads, G == 1 ? 4 : 1) select_kernel(SelectArgs a) {
-  extern __shared__ uint32_t s_key[];  // [G][M]
-  __shared__ __align__(16) float s_q[G][128];
-  __shared__ SelectScratch s_scratch[G];
-  __shared__ int s_n[G];
-  if (status_bad(a.status)) return;
-  const int tid = threadIdx.x, warp = tid >> 5;
+// selection each).  The pooled keys of a request are read once for all of its
+// chunks in the CTA: a warp copies 32 of them (256 bytes each, from 32 pages)
+// into shared memory, two whole rows per asynchronous copy, and a lane then
+// takes a key, so that every score keeps its order of additions.  Read by each
+// lane from global memory instead, 32 rows per load cost 32 cycles of the L1's
+// tags (64 x 8 rows of 1024 keys: 42 us); one bulk copy a row is held to about
+// 18 cycles each (34 us).  Rows are 272 bytes apart: eight lanes' 16-byte reads
+// cover all banks.
+template <int G, int W>
+struct SelectShared {
+  static constexpr int kWarps = W;
+  static constexpr int kPitch = 272;
+  alignas(16) uint8_t rows[kWarps][32 * kPitch];
+  alignas(16) float q[G][128];
+  SelectScratch scratch[G];
+  int n[G];
+};
+
+template <int G, int W>
+__global__ void __launch_bounds__(32 * W) select_kernel(SelectArgs a) {
+  using S = SelectShared<G, W>;
+  constexpr int kThreads = 32 * S::kWarps;
+  extern __shared__ __align__(16) uint8_t s_raw[];
+  S& s = *reinterpret_cast<S*>(s_raw);
+  uint32_t* s_key = reinterpret_cast<uint32_t*>(s_raw + sizeof(S));  // [G][M]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // heads fastest: CTAs that run together read neighbouring rows of a page
   const int g0 = (int)(blockIdx.x / a.H) * G, h = (int)(blockIdx.x % a.H);
   const int64_t hs = (int64_t)a.H * 128;
+  if (status_bad(a.status)) return;
+  // lane r of every warp holds chunk row g0 + r
+  int4 mine = make_int4(-1, 0, 0, 0);
+  if (lane < G && g0 + lane < a.NC) mine = reinterpret_cast<const int4*>(a.chunks)[g0 + lane];
   for (int lo = 0, hi; lo < G; lo = hi) {
     // a run of chunks of one request
     hi = lo + 1;
-    const int4 c = g0 + lo < a.NC ? reinterpret_cast<const int4*>(a.chunks)[g0 + lo] : make_int4(-1, 0, 0, 0);
-    if (c.x < 0) continue;
-    int most = c.w;
-    while (hi < G && g0 + hi < a.NC && a.chunks[(int64_t)(g0 + hi) * MSA_CHUNK_COLS] == c.x) {
-      most = max(most, a.chunks[(int64_t)(g0 + hi) * MSA_CHUNK_COLS + 3]);
-      ++hi;
+    const int request = __shfl_sync(0xffffffffu, mine.x, lo);
+    if (request < 0) continue;
+    if constexpr (G > 1) {
+      const unsigned other = __ballot_sync(0xffffffffu, lane >= G || mine.x != request) >> lo;
+      hi = lo + __ffs(other) - 1;  // lane 31 is always another
+    }
+    int most = lane >= lo && lane < hi ? mine.w : -1;
+    if constexpr (G > 1) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    } else {
+      most = __shfl_sync(0xffffffffu, most, 0);
     }
     __syncthreads();  // the run before has been read
+    const int nmax = request < a.R && most >= 0 ? min(most / a.B, a.M) : 0;
+    const int32_t* table = a.block_table + (int64_t)request * a.M;
+    // this lane's page of the 32 keys from block b0 on
+    auto page_of = [&](int b0) {
+      int page = b0 + lane < nmax ? __ldg(table + b0 + lane) : 0;
+      if (page < 0 || page >= a.P) {
+        set_status(a.status, MSA_ERR_INVALID_CACHE);
+        page = 0;
+      }
+      return page;
+    };
+    auto copy = [&](int b0, int pages) {
+      const int part = lane & 15;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int row = 2 * i + (lane >> 4);
+        const int64_t page = __shfl_sync(0xffffffffu, pages, row);
+        if (b0 + row < nmax)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                           smem_u32(&s.rows[warp][row * S::kPitch + part * 16])),
+                       "l"(a.pool + page * hs + h * 128 + part * 8)
+                       : "memory");
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int pages = 0;
+    if (warp * 32 < nmax) {
+      copy(warp * 32, page_of(warp * 32));
+      pages = page_of(warp * 32 + kThreads);
+    }
     // pooled queries and the rows' numbers of earlier blocks (-1: a bad row)
-    for (int i = tid; i < (hi - lo) * 128; i += kSelThreads) {
+    for (int i = tid; i < (hi - lo) * 128; i += kThreads) {
       const int row = i >> 7, d = i & 127;
-      const int4 cc = reinterpret_cast<const int4*>(a.chunks)[g0 + lo + row];
+      const int src_lane = lo + row;  // the same for a warp's 32 dims
+      const int4 cc = make_int4(__shfl_sync(0xffffffffu, mine.x, src_lane), __shfl_sync(0xffffffffu, mine.y, src_lane),
+                                __shfl_sync(0xffffffffu, mine.z, src_lane), __shfl_sync(0xffffffffu, mine.w, src_lane));
       const bool good = cc.x < a.R && cc.z >= 1 && cc.z <= kChunk && cc.y >= 0 && cc.y <= a.T - cc.z && cc.w >= 0 &&
                         cc.w / a.B < a.M;
       float acc = 0.f;
@@ -664,59 +747,55 @@ __global__ void __launch_bounds__(kSelThreads, G == 1 ? 4 : 1) select_kernel(Sel
           if (k < cc.z) acc = __fadd_rn(acc, __uint_as_float((uint32_t)x[k] << 16));
         acc = __uint_as_float(pack_bf16x2(__fdiv_rn(acc, (float)cc.z), 0.f) << 16);
       }
-      s_q[row][d] = acc;
+      s.q[row][d] = acc;
       if (d == 0) {
-        s_n[row] = good ? cc.w / a.B : -1;
+        s.n[row] = good ? cc.w / a.B : -1;
         if (!good) set_status(a.status, MSA_ERR_INVALID_CACHE);
       }
     }
     __syncthreads();
-    const int nmax = c.x < a.R && most >= 0 ? min(most / a.B, a.M) : 0;
-    const int32_t* table = a.block_table + (int64_t)c.x * a.M;
-    for (int b = tid; b < nmax; b += kSelThreads) {
-      const int page = table[b];
-      float s[G];
+    for (int b0 = warp * 32; b0 < nmax; b0 += kThreads) {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncwarp();
+      float x[G];
 #pragma unroll
-      for (int i = 0; i < G; ++i) s[i] = 0.f;
-      if (page < 0 || page >= a.P) {
-        set_status(a.status, MSA_ERR_INVALID_CACHE);
-      } else {
-        const uint16_t* src = a.pool + page * hs + h * 128;
-#pragma unroll 1
-        for (int i0 = 0; i0 < 8; i0 += 4) {
-          uint32_t u[4][8];
+      for (int r = 0; r < G; ++r) x[r] = 0.f;
+      const uint8_t* src = &s.rows[warp][lane * S::kPitch];
+#pragma unroll 4
+      for (int i = 0; i < 16; ++i) {
+        const uint4 u = *reinterpret_cast<const uint4*>(src + 16 * i);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) load32(src + 16 * (i0 + i), u[i]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float k0 = __uint_as_float(u[i][2 * e] << 16), k1 = __uint_as_float(u[i][2 * e] & 0xFFFF0000u);
-              const float k2 = __uint_as_float(u[i][2 * e + 1] << 16),
-                          k3 = __uint_as_float(u[i][2 * e + 1] & 0xFFFF0000u);
-#pragma unroll
-              for (int r = 0; r < G; ++r) {
-                const float4 q = *reinterpret_cast<const float4*>(&s_q[r][16 * (i0 + i) + 4 * e]);
-                s[r] = __fmaf_rn(q.x, k0, s[r]);
-                s[r] = __fmaf_rn(q.y, k1, s[r]);
-                s[r] = __fmaf_rn(q.z, k2, s[r]);
-                s[r] = __fmaf_rn(q.w, k3, s[r]);
-              }
-            }
+        for (int r = 0; r < G; ++r) {
+          const float4 qa = *reinterpret_cast<const float4*>(&s.q[r][8 * i]);
+          const float4 qb = *reinterpret_cast<const float4*>(&s.q[r][8 * i + 4]);
+          x[r] = __fmaf_rn(qa.x, __uint_as_float(u.x << 16), x[r]);
+          x[r] = __fmaf_rn(qa.y, __uint_as_float(u.x & 0xFFFF0000u), x[r]);
+          x[r] = __fmaf_rn(qa.z, __uint_as_float(u.y << 16), x[r]);
+          x[r] = __fmaf_rn(qa.w, __uint_as_float(u.y & 0xFFFF0000u), x[r]);
+          x[r] = __fmaf_rn(qb.x, __uint_as_float(u.z << 16), x[r]);
+          x[r] = __fmaf_rn(qb.y, __uint_as_float(u.z & 0xFFFF0000u), x[r]);
+          x[r] = __fmaf_rn(qb.z, __uint_as_float(u.w << 16), x[r]);
+          x[r] = __fmaf_rn(qb.w, __uint_as_float(u.w & 0xFFFF0000u), x[r]);
         }
       }
+      __syncwarp();  // every lane has read its key: the rows may be overwritten
+      if (b0 + kThreads < nmax) {
+        copy(b0 + kThreads, pages);
+        pages = page_of(b0 + 2 * kThreads);
+      }
+      if (b0 + lane < nmax) {
 #pragma unroll
-      for (int r = 0; r < G; ++r)
-        if (r < hi - lo) s_key[(int64_t)r * a.M + b] = score_key(s[r]);
+        for (int r = 0; r < G; ++r)
+          if (r < hi - lo) s_key[(int64_t)r * a.M + b0 + lane] = score_key(x[r]);
+      }
     }
     __syncthreads();
     if constexpr (G == 1) {
-      if (s_n[0] >= 0)
-        select_row<kSelThreads>(s_key, s_n[0], a.K, s_scratch[0], a.sel + ((int64_t)h * a.NC + g0) * a.K);
+      if (s.n[0] >= 0) select_row<kThreads>(s_key, s.n[0], a.K, s.scratch[0], a.sel + ((int64_t)h * a.NC + g0) * a.K);
     } else {
-      static_assert(G <= kSelThreads / 32, "a warp per row");
-      if (warp < hi - lo && s_n[warp] >= 0)
-        select_row<32>(s_key + (int64_t)warp * a.M, s_n[warp], a.K, s_scratch[warp],
+      static_assert(G <= S::kWarps, "a warp per row");
+      if (warp < hi - lo && s.n[warp] >= 0)
+        select_row<32>(s_key + (int64_t)warp * a.M, s.n[warp], a.K, s.scratch[warp],
                        a.sel + ((int64_t)h * a.NC + g0 + lo + warp) * a.K);
     }
   }
@@ -805,7 +884,7 @@ int msa_cache_append(const msa_cache_problem* p, const uint16_t* k, const uint16
   if (bad_pointers(ptrs, k_index ? 10 : 5)) return MSA_ERR_INVALID_ARGUMENT;
   if ((rc = check_device_current())) return rc;
   const int64_t T = p->token_cap, H = p->num_kv_heads, NC = p->chunk_cap;
-  const int64_t kv_blocks = cache::row_blocks(T, H), idx_blocks = k_index ? (NC * H * 64 + 255) / 256 : 0;
+  const int64_t kv_blocks = cache::row_blocks(T, H, 32), idx_blocks = k_index ? (NC * H * 64 + 255) / 256 : 0;
   if (kv_blocks + idx_blocks > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
   cache::AppendArgs a{k, v, k_index, slot_map, cu_tokens, chunks, kv_cache, index_tail, index_pool, (int)T, (int)H,
                       p->block_size, p->num_requests, (int)NC, (int64_t)p->num_pages * p->block_size,
@@ -822,7 +901,7 @@ int msa_cache_read(const msa_cache_problem* p, const int64_t* slots, const uint8
   if (bad_pointers(ptrs, 5)) return MSA_ERR_INVALID_ARGUMENT;
   if ((rc = check_device_current())) return rc;
   const int64_t T = p->token_cap, H = p->num_kv_heads;
-  const int64_t blocks = cache::row_blocks(T, H);
+  const int64_t blocks = cache::row_blocks(T, H, 64);
   if (blocks > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
   cache::ReadArgs a{slots, kv_cache, k, v, (int)T, (int)H, p->block_size, (int64_t)p->num_pages * p->block_size,
                     cache::exp2i(p->k_exp), cache::exp2i(p->v_exp), d_status};
@@ -841,19 +920,30 @@ int msa_cache_select(const msa_cache_problem* p, const uint16_t* q_index, const 
   cache::SelectArgs a{q_index, index_pool, block_table, chunks, sel, p->num_requests, p->num_pages, p->max_blocks,
                       p->block_size, p->token_cap, p->chunk_cap, p->num_kv_heads, p->topk, d_status};
   // Chunks of several tokens come from prompts, whose chunks share a request's
-  // keys: 8 of them to a CTA, while 8 rows of scores fit shared memory.
+  // keys: 8 of them to a CTA, while 8 rows of scores fit shared memory.  (One to
+  // a CTA: 62 us for the same prompts.)
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int64_t H = p->num_kv_heads, NC = p->chunk_cap;
   if (NC * H > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
   const size_t row = (size_t)p->max_blocks * 4;
-  if (p->token_cap / p->chunk_cap >= 3 && 8 * row <= 128 * 1024) {
-    if ((rc = cuda_status(allow_smem(cache::select_kernel<8>, 8 * row)))) return rc;
-    cache::select_kernel<8><<<(unsigned)((NC + 7) / 8 * H), cache::kSelThreads, 8 * row, st>>>(a);
-  } else {
-    if ((rc = cuda_status(allow_smem(cache::select_kernel<1>, row)))) return rc;
-    cache::select_kernel<1><<<(unsigned)(NC * H), cache::kSelThreads, row, st>>>(a);
+  auto launch = [&](auto kernel, size_t smem, int64_t ctas, int threads) {
+    if ((rc = cuda_status(allow_smem(kernel, smem)))) return rc;
+    kernel<<<(unsigned)ctas, threads, smem, st>>>(a);
+    return cuda_status(cudaGetLastError());
+  };
+  constexpr size_t kSmem = 227 * 1024;
+  if (p->token_cap / p->chunk_cap >= 3) {
+    // 16 warps share the eight chunks' 500 keys better than 8 do (21 against
+    // 24 us for 2 x 2048 tokens over 32k cached ones)
+    const size_t s16 = sizeof(cache::SelectShared<8, 16>) + 8 * row, s8 = sizeof(cache::SelectShared<8, 8>) + 8 * row;
+    if (s16 <= kSmem) return launch(cache::select_kernel<8, 16>, s16, (NC + 7) / 8 * H, 512);
+    if (s8 <= kSmem) return launch(cache::select_kernel<8, 8>, s8, (NC + 7) / 8 * H, 256);
   }
-  return cuda_status(cudaGetLastError());
+  if (sizeof(cache::SelectShared<1, 4>) + row <= kSmem)
+    return launch(cache::select_kernel<1, 4>, sizeof(cache::SelectShared<1, 4>) + row, NC * H, 128);
+  // the longest tables: a warp less, so that the scores fit
+  static_assert(sizeof(cache::SelectShared<1, 3>) + cache::kMaxBlocks * 4 <= kSmem, "the longest table's scores fit");
+  return launch(cache::select_kernel<1, 3>, sizeof(cache::SelectShared<1, 3>) + row, NC * H, 96);
 }
 
 }  // extern "C"

@@ -436,7 +436,8 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
         }
         int total = -1, x = 0, ntl = 0, page = 0, b = -1;
         if (!end) {
-          if (!list_tiles(a, c, (int)(w / a.H), h, lane, b, page, ntl)) continue;
+          const int entry = lane < a.K ? a.sel[((int64_t)h * a.NC + w / a.H) * a.K + lane] : -1;
+          if (!list_tiles(a, c, entry, lane, b, page, ntl)) continue;
           x = ntl;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {

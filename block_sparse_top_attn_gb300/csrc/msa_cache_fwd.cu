@@ -32,12 +32,7 @@ namespace cache {
 
 constexpr int kConsumers = 4;
 constexpr int kFwdThreads = 32 * kConsumers;
-#ifndef KS
-#define KS 6
-#define CHUNKMIN 1
-#define KB 3
-#endif
-constexpr int kStages = KS, kPairStages = kStages / 2;
+constexpr int kStages = 6, kPairStages = kStages / 2;
 constexpr int kMaxTiles = 64;   // 64-key tiles of an item: up to 32 blocks of 128 keys
 // Weights are p = 2^(s - m) with m kLift below the running maximum, which moves
 // when a score passes it by kTau: 2^kLift <= the largest p < 2^(kLift + kTau),
@@ -86,13 +81,6 @@ MSA_DEV uint32_t pack_half2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-MSA_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // A row of q as fp16 A-fragment words: the lane's 32 dims (32 t .. 32 t + 31),
 // scaled by a power of two that puts the row's largest element at 2^14, so
 // that a bf16 element loses bits only below 2^-31 of the largest.  Returns the
@@ -119,8 +107,9 @@ MSA_DEV float load_q_row(const uint16_t* src, uint32_t (&w)[16]) {
 // A chunk's selected tiles, by one warp: lane k's block (-1: none), its page and
 // the number of its 64-key tiles that start at or before the chunk's last token.
 // False (and *status) if the chunk row, the selection or a page is bad.
-MSA_DEV bool list_tiles(const FwdCacheArgs& a, const int4& c, int g, int h, int lane, int& b, int& page, int& ntl) {
-  b = -1;
+// entry: this lane's slot of the selection (-1 beyond topk).
+MSA_DEV bool list_tiles(const FwdCacheArgs& a, const int4& c, int entry, int lane, int& b, int& page, int& ntl) {
+  b = max(entry, -1);
   page = 0;
   ntl = 0;
   int code = MSA_OK;
@@ -128,8 +117,6 @@ MSA_DEV bool list_tiles(const FwdCacheArgs& a, const int4& c, int g, int h, int 
       c.w / a.B >= a.M) {
     code = MSA_ERR_INVALID_CACHE;
   } else {
-    if (lane < a.K) b = a.sel[((int64_t)h * a.NC + g) * a.K + lane];
-    if (b < 0) b = -1;
     const unsigned same = __match_any_sync(0xffffffffu, b);
     if (__any_sync(0xffffffffu, b > c.w / a.B || (b >= 0 && __popc(same) > 1))) {
       code = MSA_ERR_INVALID_SELECTION;
@@ -146,7 +133,7 @@ MSA_DEV bool list_tiles(const FwdCacheArgs& a, const int4& c, int g, int h, int 
   return true;
 }
 
-__global__ void __launch_bounds__(kFwdThreads, KB) fwd_cache_kernel(FwdCacheArgs a) {
+__global__ void __launch_bounds__(kFwdThreads, 3) fwd_cache_kernel(FwdCacheArgs a) {
   extern __shared__ __align__(128) uint8_t s_raw[];
   FwdShared& s = *reinterpret_cast<FwdShared*>(s_raw);
   cg::cluster_group cluster = cg::this_cluster();
@@ -154,6 +141,13 @@ __global__ void __launch_bounds__(kFwdThreads, KB) fwd_cache_kernel(FwdCacheArgs
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, pair = warp >> 1;
   const int item = blockIdx.x / ranks, h = blockIdx.y;
   const int g = item / a.slots, slot = item % a.slots;
+  // three loads in flight together: a chain of them is a good part of an item
+  int entry = -1;
+  bool stale = false;
+  if (warp == 0) {
+    stale = status_bad(a.status);
+    if (lane < a.K) entry = a.sel[((int64_t)h * a.NC + g) * a.K + lane];
+  }
   // the same for every CTA of the cluster, so all of them leave here or none
   const int4 c = reinterpret_cast<const int4*>(a.chunks)[g];
   if (c.x < 0 || slot >= c.z) return;
@@ -167,7 +161,7 @@ __global__ void __launch_bounds__(kFwdThreads, KB) fwd_cache_kernel(FwdCacheArgs
   if (warp == 0) {
     // the chunk's tiles; rank takes every ranks-th
     int b, page, ntl;
-    const bool good = !status_bad(a.status) && list_tiles(a, c, g, h, lane, b, page, ntl);
+    const bool good = !stale && list_tiles(a, c, entry, lane, b, page, ntl);
     if (!good) ntl = 0;
     int x = ntl;
 #pragma unroll
@@ -190,6 +184,23 @@ __global__ void __launch_bounds__(kFwdThreads, KB) fwd_cache_kernel(FwdCacheArgs
       s.skip = !good;
     }
   }
+  // the 16 query rows of a token, by warp 3 (warp 0 has the list, warps 0 and 2
+  // the copies to see to).  A row outside the tensor belongs to a refused chunk.
+  auto stage_q = [&](int tok) {
+    if (warp != 3) return;
+    const int gid = lane >> 2, t = lane & 3;
+    const int64_t row0 = (int64_t)min(max(c.y + tok, 0), a.T - 1) * a.H * kGroup + h * kGroup;
+    uint32_t q0[16], q1[16];
+    const uint16_t* src = a.q + (row0 + gid) * 128 + 32 * t;
+    const float x0 = load_q_row(src, q0), x1 = load_q_row(src + 8 * 128, q1);
+    if (t == 0) {
+      s.qs[gid] = x0;
+      s.qs[gid + 8] = x1;
+    }
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) s.q[ks][lane] = make_uint4(q0[2 * ks], q1[2 * ks], q0[2 * ks + 1], q1[2 * ks + 1]);
+  };
+  stage_q(slot);
   __syncthreads();
   const int ntiles = s.ntiles;
   if (ranks == 1 && s.skip) return;
@@ -214,19 +225,10 @@ __global__ void __launch_bounds__(kFwdThreads, KB) fwd_cache_kernel(FwdCacheArgs
       while (issued < ptotal && issued < pdone + kPairStages) issue();
     {
       const int gid = lane >> 2, t = lane & 3;
-      if (warp == 3) {
-        // warp 0 has the selection, warps 0 and 2 the first copies to see to
-        uint32_t q0[16], q1[16];
-        const uint16_t* src = a.q + (row0 + gid) * 128 + 32 * t;
-        const float x0 = load_q_row(src, q0), x1 = load_q_row(src + 8 * 128, q1);
-        if (t == 0) {
-          s.qs[gid] = x0;
-          s.qs[gid + 8] = x1;
-        }
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks) s.q[ks][lane] = make_uint4(q0[2 * ks], q1[2 * ks], q0[2 * ks + 1], q1[2 * ks + 1]);
+      if (tok != slot) {
+        stage_q(tok);
+        __syncthreads();
       }
-      __syncthreads();
       const float sc0 = s.qs[gid] * a.scale_log2, sc1 = s.qs[gid + 8] * a.scale_log2;
 #pragma unroll
       for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
@@ -526,9 +528,13 @@ extern "C" int msa_cache_fwd(const msa_cache_problem* p, const uint16_t* q, cons
   a.scale_log2 = p->softmax_scale * cache::exp2i(p->k_exp) * cache::kLog2e;
   a.v_mul = cache::exp2i(p->v_exp);
   a.status = d_status;
-  // Chunks of several tokens (more token rows than chunk rows) in batches that
-  // fill the GPU: the 128-row kernel.
-  if (p->token_cap > p->chunk_cap && (int64_t)p->chunk_cap * p->num_kv_heads >= CHUNKMIN) {
+  // Chunks of two tokens and more on average, in batches of a few tokens per SM:
+  // the 128-row kernel.  It takes the same time for one token of a chunk as for
+  // eight (16 tiles 23 us, 32 tiles 38 us, for up to two items per SM), the
+  // single-token kernel about 0.08 us per token, head and 32 tiles on top of 9:
+  // 8 tokens x 16 requests x 8 heads x 32 tiles 50 against 108 us, 3 tokens x 8
+  // requests 38 against 28.
+  if (p->token_cap / p->chunk_cap >= 2 && (int64_t)p->token_cap * p->num_kv_heads * 2 >= 5 * sms) {
     cudaFuncAttributes attr;
     if (cudaFuncGetAttributes(&attr, cache::chunk::fwd_chunk_kernel) != cudaSuccess) return MSA_ERR_CUDA;
     // the warpgroups' register shares add up to the launch's registers, or
@@ -545,9 +551,12 @@ extern "C" int msa_cache_fwd(const msa_cache_problem* p, const uint16_t* q, cons
                                      static_cast<cudaStream_t>(stream)>>>(a);
     return cuda_status(cudaGetLastError());
   }
-  // Token slots of a chunk: its mean number of tokens, at most 8.  A chunk
-  // with more tokens than slots takes them in turn.
+  // Token slots of a chunk in the grid: one where tokens and chunk rows are
+  // equal in number (decode), else twice the mean, at most 8.  A chunk with more
+  // tokens than slots takes them in turn; a slot without a token costs the
+  // launch of a CTA that leaves at once.
   a.slots = (int)((p->token_cap + (int64_t)p->chunk_cap - 1) / p->chunk_cap);
+  if (a.slots > 1) a.slots *= 2;
   if (a.slots > kChunk) a.slots = kChunk;
   const int64_t items = (int64_t)p->chunk_cap * a.slots;
   // CTAs of a cluster share an item's tiles while the items alone leave SMs
