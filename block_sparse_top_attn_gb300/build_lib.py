@@ -15,7 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmsa.so")
 SOURCES = ["msa_tables.cu", "msa_bwd.cu", "msa_fwd.cu", "msa_score.cu", "msa_cache.cu", "msa_cache_fwd.cu"]
-HEADERS = ["msa_common.cuh", "msa_cache.cuh", "msa_cache_chunk.cuh", "msa_host.cuh", "msa_tmap.cuh", "msa_bwd_ws.cuh"]
+HEADERS = ["msa_common.cuh", "msa_cache.cuh", "msa_cache_batch.cuh", "msa_cache_chunk.cuh", "msa_host.cuh", "msa_tmap.cuh", "msa_bwd_ws.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "-I", os.path.join(ROOT, "include")]

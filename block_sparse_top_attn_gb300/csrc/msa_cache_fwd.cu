@@ -104,6 +104,144 @@ MSA_DEV float load_q_row(const uint16_t* src, uint32_t (&w)[16]) {
   return __uint_as_float((uint32_t)(e - 14) << 23);
 }
 
+// One warp's 32 keys (from key kw of a tile) for the 16 rows whose A fragments
+// are q: scores, running maximum m and sum l, output o.  Keys 0 .. reach of the
+// 32 may be attended (reach >= 0).  sc0, sc1: the factors that turn the scores of
+// rows gid and gid + 8 into powers of two.
+MSA_DEV void attend32(const uint8_t* tile, int kw, int reach, const uint4 (*q)[32], float sc0, float sc1, int lane,
+            float (&o)[16][4], float (&m)[2], float (&l)[2]) {
+  const int gid = lane >> 2, t = lane & 3;
+  // S = Q K^T: column c of n-tile jj is key 16 (jj >> 1) + 4 (c >> 1) +
+  // 2 (jj & 1) + (c & 1), k-step ks contracts dims 32 t + 4 ks .. + 3 of
+  // each lane t.  The four n-tiles' chains are interleaved.
+  float sv[4][4];
+  uint4 kc[4];
+  uint32_t ksc[4];
+#pragma unroll
+  for (int jj = 0; jj < 4; ++jj) {
+    const int key = kw + 16 * (jj >> 1) + 4 * (gid >> 1) + 2 * (jj & 1) + (gid & 1);
+    kc[jj] = *reinterpret_cast<const uint4*>(tile + OFF_KC + key * kRowBytes + t * 16);
+    ksc[jj] = e4m3x2_to_half(*reinterpret_cast<const uint16_t*>(tile + OFF_KS + key * kScales + 2 * t));
+    sv[jj][0] = sv[jj][1] = sv[jj][2] = sv[jj][3] = 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t hk[4][4];
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj) {
+      e2m1x8_to_half(i == 0 ? kc[jj].x : i == 1 ? kc[jj].y : i == 2 ? kc[jj].z : kc[jj].w, hk[jj]);
+      const uint32_t sc = __byte_perm(ksc[jj], ksc[jj], i < 2 ? 0x1010 : 0x3232);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) hk[jj][e] = mul_half2(hk[jj][e], sc);
+    }
+    const uint4 qa = q[2 * i][lane], qb = q[2 * i + 1][lane];
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj) mma_f16(sv[jj], qa.x, qa.y, qa.z, qa.w, hk[jj][0], hk[jj][1]);
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj) mma_f16(sv[jj], qb.x, qb.y, qb.z, qb.w, hk[jj][2], hk[jj][3]);
+  }
+  // the lane's keys: 16 (jj >> 1) + 4 t + 2 (jj & 1) + e; rows gid and gid + 8
+  float bm0 = -CUDART_INF_F, bm1 = -CUDART_INF_F;
+  const int left = reach - 4 * t;  // its keys up to this one may be attended
+#pragma unroll
+  for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      sv[jj][e] *= sc0;
+      sv[jj][2 + e] *= sc1;
+    }
+  uint32_t vs[2];
+#pragma unroll
+  for (int st2 = 0; st2 < 2; ++st2)
+    vs[st2] = *reinterpret_cast<const uint32_t*>(tile + OFF_VS + gid * kTile + kw + 16 * st2 + 4 * t);
+  if (reach < 31) {
+    // keys that may not be attended hold anything: their scores are
+    // replaced, and a zero scale makes their values zero (a code alone is
+    // always finite)
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const bool in = 16 * (jj >> 1) + 2 * (jj & 1) + e <= left;
+        sv[jj][e] = in ? sv[jj][e] : -CUDART_INF_F;
+        sv[jj][2 + e] = in ? sv[jj][2 + e] : -CUDART_INF_F;
+      }
+#pragma unroll
+    for (int st2 = 0; st2 < 2; ++st2) {
+      const int lf = left - 16 * st2;
+      if (lf < 3) vs[st2] = lf < 0 ? 0u : vs[st2] & (0xFFFFFFFFu >> (8 * (3 - lf)));
+    }
+  }
+#pragma unroll
+  for (int jj = 0; jj < 4; ++jj) {
+    bm0 = fmaxf(bm0, fmaxf(sv[jj][0], sv[jj][1]));
+    bm1 = fmaxf(bm1, fmaxf(sv[jj][2], sv[jj][3]));
+  }
+  bm0 = fmaxf(bm0, __shfl_xor_sync(0xffffffffu, bm0, 1));
+  bm1 = fmaxf(bm1, __shfl_xor_sync(0xffffffffu, bm1, 1));
+  bm0 = fmaxf(bm0, __shfl_xor_sync(0xffffffffu, bm0, 2));
+  bm1 = fmaxf(bm1, __shfl_xor_sync(0xffffffffu, bm1, 2));
+  const bool up0 = bm0 > m[0] + (kLift + kTau), up1 = bm1 > m[1] + (kLift + kTau);
+  if (__any_sync(0xffffffffu, up0 || up1)) {
+    const float al0 = up0 ? ex2_approx(m[0] + kLift - bm0) : 1.f;
+    const float al1 = up1 ? ex2_approx(m[1] + kLift - bm1) : 1.f;
+    if (up0) m[0] = bm0 - kLift;
+    if (up1) m[1] = bm1 - kLift;
+    l[0] *= al0;
+    l[1] *= al1;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      o[i][0] *= al0;
+      o[i][1] *= al0;
+      o[i][2] *= al1;
+      o[i][3] *= al1;
+    }
+  }
+  const float m0 = m[0] == -CUDART_INF_F ? 0.f : m[0], m1 = m[1] == -CUDART_INF_F ? 0.f : m[1];
+  uint32_t pa[8];
+#pragma unroll
+  for (int jj = 0; jj < 4; ++jj) {
+    const float p0 = ex2_approx(sv[jj][0] - m0), p1 = ex2_approx(sv[jj][1] - m0);
+    const float p2 = ex2_approx(sv[jj][2] - m1), p3 = ex2_approx(sv[jj][3] - m1);
+    l[0] += p0 + p1;
+    l[1] += p2 + p3;
+    // fp16 keeps 11 bits of a weight, 3 more than bf16
+    pa[2 * jj] = pack_half2(p0, p1);
+    pa[2 * jj + 1] = pack_half2(p2, p3);
+  }
+  // O += P V: column c = gid of n-tile j is dim 16 gid + j, so a lane's
+  // V words are one scale group of its four keys of each 16
+#pragma unroll
+  for (int st2 = 0; st2 < 2; ++st2) {
+    const uint32_t* p4 = &pa[4 * st2];
+    uint2 vw[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      vw[e] = *reinterpret_cast<const uint2*>(tile + OFF_VC + v_code_offset(kw + 16 * st2 + 4 * t + e, gid));
+    const uint32_t s01 = e4m3x2_to_half(vs[st2] & 0xFFFFu), s23 = e4m3x2_to_half(vs[st2] >> 16);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      // bytes of two keys' codes at one dim, even and odd dims apart
+      constexpr uint32_t LO = 0x0F0F0F0Fu;
+      const uint32_t w0 = w ? vw[0].y : vw[0].x, w1 = w ? vw[1].y : vw[1].x;
+      const uint32_t w2 = w ? vw[2].y : vw[2].x, w3 = w ? vw[3].y : vw[3].x;
+      uint32_t ev01[4], od01[4], ev23[4], od23[4];
+      e2m1x8_to_half((w0 & LO) | ((w1 << 4) & ~LO), ev01);
+      e2m1x8_to_half((w2 & LO) | ((w3 << 4) & ~LO), ev23);
+      e2m1x8_to_half(((w0 >> 4) & LO) | (w1 & ~LO), od01);
+      e2m1x8_to_half(((w2 >> 4) & LO) | (w3 & ~LO), od23);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        mma_f16(o[8 * w + 2 * i], p4[0], p4[1], p4[2], p4[3], mul_half2(ev01[i], s01),
+                mul_half2(ev23[i], s23));
+        mma_f16(o[8 * w + 2 * i + 1], p4[0], p4[1], p4[2], p4[3], mul_half2(od01[i], s01),
+                mul_half2(od23[i], s23));
+      }
+    }
+  }
+}
+
+
 // A chunk's selected tiles, by one warp: lane k's block (-1: none), its page and
 // the number of its 64-key tiles that start at or before the chunk's last token.
 // False (and *status) if the chunk row, the selection or a page is bad.
@@ -224,7 +362,7 @@ __global__ void __launch_bounds__(kFwdThreads, 3) fwd_cache_kernel(FwdCacheArgs 
     if (loader)
       while (issued < ptotal && issued < pdone + kPairStages) issue();
     {
-      const int gid = lane >> 2, t = lane & 3;
+      const int gid = lane >> 2;
       if (tok != slot) {
         stage_q(tok);
         __syncthreads();
@@ -240,134 +378,7 @@ __global__ void __launch_bounds__(kFwdThreads, 3) fwd_cache_kernel(FwdCacheArgs 
         const int kw = 32 * (warp & 1);                              // the warp's first key in the tile
         const int k0 = s.key0[2 * (n - pdone) + pair] + kw;          // and its position
         if (k0 <= qpos) {
-          // S = Q K^T: column c of n-tile jj is key 16 (jj >> 1) + 4 (c >> 1) +
-          // 2 (jj & 1) + (c & 1), k-step ks contracts dims 32 t + 4 ks .. + 3 of
-          // each lane t.  The four n-tiles' chains are interleaved.
-          float sv[4][4];
-          uint4 kc[4];
-          uint32_t ksc[4];
-#pragma unroll
-          for (int jj = 0; jj < 4; ++jj) {
-            const int key = kw + 16 * (jj >> 1) + 4 * (gid >> 1) + 2 * (jj & 1) + (gid & 1);
-            kc[jj] = *reinterpret_cast<const uint4*>(tile + OFF_KC + key * kRowBytes + t * 16);
-            ksc[jj] = e4m3x2_to_half(*reinterpret_cast<const uint16_t*>(tile + OFF_KS + key * kScales + 2 * t));
-            sv[jj][0] = sv[jj][1] = sv[jj][2] = sv[jj][3] = 0.f;
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t hk[4][4];
-#pragma unroll
-            for (int jj = 0; jj < 4; ++jj) {
-              e2m1x8_to_half(i == 0 ? kc[jj].x : i == 1 ? kc[jj].y : i == 2 ? kc[jj].z : kc[jj].w, hk[jj]);
-              const uint32_t sc = __byte_perm(ksc[jj], ksc[jj], i < 2 ? 0x1010 : 0x3232);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) hk[jj][e] = mul_half2(hk[jj][e], sc);
-            }
-            const uint4 qa = s.q[2 * i][lane], qb = s.q[2 * i + 1][lane];
-#pragma unroll
-            for (int jj = 0; jj < 4; ++jj) mma_f16(sv[jj], qa.x, qa.y, qa.z, qa.w, hk[jj][0], hk[jj][1]);
-#pragma unroll
-            for (int jj = 0; jj < 4; ++jj) mma_f16(sv[jj], qb.x, qb.y, qb.z, qb.w, hk[jj][2], hk[jj][3]);
-          }
-          // the lane's keys: 16 (jj >> 1) + 4 t + 2 (jj & 1) + e; rows gid and gid + 8
-          float bm0 = -CUDART_INF_F, bm1 = -CUDART_INF_F;
-          const int left = qpos - k0 - 4 * t;  // its keys up to this one may be attended
-#pragma unroll
-          for (int jj = 0; jj < 4; ++jj)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              sv[jj][e] *= sc0;
-              sv[jj][2 + e] *= sc1;
-            }
-          uint32_t vs[2];
-#pragma unroll
-          for (int st2 = 0; st2 < 2; ++st2)
-            vs[st2] = *reinterpret_cast<const uint32_t*>(tile + OFF_VS + gid * kTile + kw + 16 * st2 + 4 * t);
-          if (k0 + 31 > qpos) {
-            // keys that may not be attended hold anything: their scores are
-            // replaced, and a zero scale makes their values zero (a code alone is
-            // always finite)
-#pragma unroll
-            for (int jj = 0; jj < 4; ++jj)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const bool in = 16 * (jj >> 1) + 2 * (jj & 1) + e <= left;
-                sv[jj][e] = in ? sv[jj][e] : -CUDART_INF_F;
-                sv[jj][2 + e] = in ? sv[jj][2 + e] : -CUDART_INF_F;
-              }
-#pragma unroll
-            for (int st2 = 0; st2 < 2; ++st2) {
-              const int lf = left - 16 * st2;
-              if (lf < 3) vs[st2] = lf < 0 ? 0u : vs[st2] & (0xFFFFFFFFu >> (8 * (3 - lf)));
-            }
-          }
-#pragma unroll
-          for (int jj = 0; jj < 4; ++jj) {
-            bm0 = fmaxf(bm0, fmaxf(sv[jj][0], sv[jj][1]));
-            bm1 = fmaxf(bm1, fmaxf(sv[jj][2], sv[jj][3]));
-          }
-          bm0 = fmaxf(bm0, __shfl_xor_sync(0xffffffffu, bm0, 1));
-          bm1 = fmaxf(bm1, __shfl_xor_sync(0xffffffffu, bm1, 1));
-          bm0 = fmaxf(bm0, __shfl_xor_sync(0xffffffffu, bm0, 2));
-          bm1 = fmaxf(bm1, __shfl_xor_sync(0xffffffffu, bm1, 2));
-          const bool up0 = bm0 > m[0] + (kLift + kTau), up1 = bm1 > m[1] + (kLift + kTau);
-          if (__any_sync(0xffffffffu, up0 || up1)) {
-            const float al0 = up0 ? ex2_approx(m[0] + kLift - bm0) : 1.f;
-            const float al1 = up1 ? ex2_approx(m[1] + kLift - bm1) : 1.f;
-            if (up0) m[0] = bm0 - kLift;
-            if (up1) m[1] = bm1 - kLift;
-            l[0] *= al0;
-            l[1] *= al1;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              o[i][0] *= al0;
-              o[i][1] *= al0;
-              o[i][2] *= al1;
-              o[i][3] *= al1;
-            }
-          }
-          const float m0 = m[0] == -CUDART_INF_F ? 0.f : m[0], m1 = m[1] == -CUDART_INF_F ? 0.f : m[1];
-          uint32_t pa[8];
-#pragma unroll
-          for (int jj = 0; jj < 4; ++jj) {
-            const float p0 = ex2_approx(sv[jj][0] - m0), p1 = ex2_approx(sv[jj][1] - m0);
-            const float p2 = ex2_approx(sv[jj][2] - m1), p3 = ex2_approx(sv[jj][3] - m1);
-            l[0] += p0 + p1;
-            l[1] += p2 + p3;
-            // fp16 keeps 11 bits of a weight, 3 more than bf16
-            pa[2 * jj] = pack_half2(p0, p1);
-            pa[2 * jj + 1] = pack_half2(p2, p3);
-          }
-          // O += P V: column c = gid of n-tile j is dim 16 gid + j, so a lane's
-          // V words are one scale group of its four keys of each 16
-#pragma unroll
-          for (int st2 = 0; st2 < 2; ++st2) {
-            const uint32_t* p4 = &pa[4 * st2];
-            uint2 vw[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              vw[e] = *reinterpret_cast<const uint2*>(tile + OFF_VC + v_code_offset(kw + 16 * st2 + 4 * t + e, gid));
-            const uint32_t s01 = e4m3x2_to_half(vs[st2] & 0xFFFFu), s23 = e4m3x2_to_half(vs[st2] >> 16);
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              // bytes of two keys' codes at one dim, even and odd dims apart
-              constexpr uint32_t LO = 0x0F0F0F0Fu;
-              const uint32_t w0 = w ? vw[0].y : vw[0].x, w1 = w ? vw[1].y : vw[1].x;
-              const uint32_t w2 = w ? vw[2].y : vw[2].x, w3 = w ? vw[3].y : vw[3].x;
-              uint32_t ev01[4], od01[4], ev23[4], od23[4];
-              e2m1x8_to_half((w0 & LO) | ((w1 << 4) & ~LO), ev01);
-              e2m1x8_to_half((w2 & LO) | ((w3 << 4) & ~LO), ev23);
-              e2m1x8_to_half(((w0 >> 4) & LO) | (w1 & ~LO), od01);
-              e2m1x8_to_half(((w2 >> 4) & LO) | (w3 & ~LO), od23);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                mma_f16(o[8 * w + 2 * i], p4[0], p4[1], p4[2], p4[3], mul_half2(ev01[i], s01),
-                        mul_half2(ev23[i], s23));
-                mma_f16(o[8 * w + 2 * i + 1], p4[0], p4[1], p4[2], p4[3], mul_half2(od01[i], s01),
-                        mul_half2(od23[i], s23));
-              }
-            }
-          }
+          attend32(tile, kw, qpos - k0, s.q, sc0, sc1, lane, o, m, l);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.empty[st]);
@@ -506,6 +517,7 @@ __global__ void __launch_bounds__(kFwdThreads, 3) fwd_cache_kernel(FwdCacheArgs 
 }  // namespace cache
 }  // namespace msa
 
+#include "msa_cache_batch.cuh"
 #include "msa_cache_chunk.cuh"
 
 using namespace msa;
@@ -565,6 +577,20 @@ extern "C" int msa_cache_fwd(const msa_cache_problem* p, const uint16_t* q, cons
   int ranks = 1;
   while (ranks < 8 && ranks * 2 <= tiles && items * p->num_kv_heads * ranks * 2 <= 2 * sms) ranks *= 2;
   if (items * ranks > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
+  if (ranks == 1) {
+    // enough items to keep every SM busy: persistent CTAs
+    if (cudaFuncSetAttribute(cache::batch::fwd_batch_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)sizeof(cache::batch::Shared)) != cudaSuccess ||
+        cudaFuncSetAttribute(cache::batch::fwd_batch_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             (int)cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+      return MSA_ERR_CUDA;
+    const int64_t all = (int64_t)p->chunk_cap * p->num_kv_heads;
+    const int64_t slots = (int64_t)cache::batch::kCtasPerSm * sms;
+    const int grid = (int)(all < slots ? all : slots);
+    cache::batch::fwd_batch_kernel<<<grid, cache::batch::kThreads, sizeof(cache::batch::Shared),
+                                     static_cast<cudaStream_t>(stream)>>>(a);
+    return cuda_status(cudaGetLastError());
+  }
   if ((rc = cuda_status(allow_smem(cache::fwd_cache_kernel, sizeof(cache::FwdShared))))) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items * ranks), (unsigned)p->num_kv_heads);

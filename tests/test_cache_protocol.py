@@ -1,0 +1,336 @@
+"""CPU model check of the hand-offs of the two persistent cached-attention
+kernels (no GPU): `msa_cache_batch.cuh` (a service warp that feeds a ring, two
+pairs of attending warps, joins through shared memory) and `msa_cache_chunk.cuh`
+(list warp, decoders, MMA issuer, softmax warps).
+
+The model replays the kernels' order of waits, arrivals, copies and MMAs under
+random interleavings.  A parity wait is correct only while the barrier is on
+the awaited phase or has just completed it; copies land in any order, MMAs in
+issue order; a buffer may be overwritten only once its readers are done, and
+every reader must find its own tile, item or part.  Odd rings, and one phase of
+the query barrier for items without tiles, fail it."""
+import random
+
+import pytest
+
+
+class _Bar:
+    def __init__(self, name, count=1):
+        self.name, self.done, self.count, self.arr = name, 0, count, 0
+
+    def arrive(self):
+        self.arr += 1
+        assert self.arr <= self.count, f"surplus arrival on {self.name}"
+        if self.arr == self.count:
+            self.arr, self.done = 0, self.done + 1
+
+    def ready(self, k):
+        assert self.done in (k, k + 1), f"parity alias on {self.name}: phase {k}, completed {self.done}"
+        return self.done == k + 1
+
+
+class _Slot:
+    """A buffer with its content and the number of readers still to come."""
+
+    def __init__(self, name):
+        self.name, self.tag, self.readers = name, None, 0
+
+    def write(self, tag, readers):
+        assert self.readers == 0, f"{self.name} overwritten before {self.readers} reads of {self.tag}"
+        self.tag, self.readers = tag, readers
+
+    def read(self, tag):
+        assert self.tag == tag, f"{self.name} holds {self.tag}, wanted {tag}"
+        self.readers -= 1
+
+
+def _run(threads, rng, pending=(), bias=None):
+    """Steps generators in random order until all end; pending: callables that make asynchronous work progress.
+    bias: names of threads that run ten times as often."""
+    live = dict(threads)
+    idle = 0
+    while live:
+        names = list(live)
+        weights = [10 if bias and n in bias else 1 for n in names]
+        progress = False
+        if pending and rng.random() < 0.4:
+            progress = any([p(rng) for p in pending])
+        name = rng.choices(names, weights)[0]
+        try:
+            progress = next(live[name]) is not None or progress
+        except StopIteration:
+            del live[name]
+            progress = True
+        idle = 0 if progress else idle + 1
+        assert idle < 200000, f"deadlock: {list(live)}"
+
+
+def _wait(bar, k):
+    while not bar.ready(k):
+        yield None
+    yield 1
+
+
+# ---------------------------------------------------------------------------
+# batch kernel
+# ---------------------------------------------------------------------------
+
+def _batch(items, seed, ring=8, bias=None):
+    rng = random.Random(seed)
+    full = [_Bar(f"full{i}") for i in range(ring)]
+    empty = [_Bar(f"empty{i}", 2) for i in range(ring)]
+    item_full = [_Bar(f"item_full{i}") for i in range(2)]
+    item_free = [_Bar(f"item_free{i}", 4) for i in range(2)]
+    part_full = [_Bar(f"part_full{i}") for i in range(2)]
+    part_free = [_Bar(f"part_free{i}") for i in range(2)]
+    pair_full = _Bar("pair_full")
+    stage = [_Slot(f"stage{i}") for i in range(ring)]
+    item = [_Slot(f"item{i}") for i in range(2)]
+    part = [_Slot(f"part{i}") for i in range(2)]
+    flying, seen, written = [], {}, []
+
+    def service():
+        n = 0
+        for i, nt in enumerate(items + [-1]):
+            if i >= 2:
+                yield from _wait(item_free[i & 1], (i >> 1) - 1)
+            item[i & 1].write(i, 4)
+            item_full[i & 1].arrive()
+            yield 1
+            for _ in range(max(nt, 0)):
+                st, lap = n % ring, n // ring
+                if lap > 0:
+                    yield from _wait(empty[st], lap - 1)
+                flying.append(n)
+                n += 1
+                yield 1
+
+    def land(r):
+        if not flying:
+            return False
+        n = flying.pop(r.randrange(len(flying)))
+        stage[n % ring].write(n, 2)
+        full[n % ring].arrive()
+        return True
+
+    def attend(w):
+        pair, base = w >> 1, 0
+        for i, nt in enumerate(items + [-1]):
+            yield from _wait(item_full[i & 1], i >> 1)
+            assert item[i & 1].tag == i
+            if nt < 0:
+                return
+            n = base + ((base ^ pair) & 1)
+            while n < base + nt:
+                yield from _wait(full[n % ring], n // ring)
+                stage[n % ring].read(n)
+                seen.setdefault(n, []).append(w & 1)
+                yield 1
+                empty[n % ring].arrive()
+                n += 2
+            base += nt
+            if w & 1:
+                if i >= 1:
+                    yield from _wait(part_free[pair], i - 1)
+                part[pair].write(("odd", i), 1)
+                part_full[pair].arrive()
+            else:
+                yield from _wait(part_full[pair], i)
+                part[pair].read(("odd", i))
+                yield 1
+                if w == 2:
+                    part[1].write(("pair", i), 1)
+                    pair_full.arrive()
+                else:
+                    part_free[0].arrive()
+                    yield from _wait(pair_full, i)
+                    part[1].read(("pair", i))
+                    yield 1
+                    part_free[1].arrive()
+                    assert item[i & 1].tag == i
+                    written.append(i)
+            item[i & 1].read(i)
+            item_free[i & 1].arrive()
+            yield 1
+
+    threads = {"service": service(), **{f"w{w}": attend(w) for w in range(4)}}
+    _run(threads, rng, [land], bias)
+    assert not flying and written == list(range(len(items)))
+    assert all(sorted(seen[n]) == [0, 1] for n in range(sum(items)))
+
+
+ITEMS = [[32] * 3, [1, 2, 3, 4, 5, 6, 7], [0, 0, 5, 0, 1, 0, 0, 2], [], [0], [64, 1, 64], [3, 3, 3, 3, 3]]
+
+
+@pytest.mark.parametrize("items", ITEMS)
+@pytest.mark.parametrize("bias", [None, ["w0", "w1"], ["w2", "w3"], ["service"], ["w1"]])
+def test_batch_hand_offs(items, bias):
+    for seed in range(12):
+        _batch(items, seed, bias=bias)
+
+
+def test_batch_model_rejects_an_odd_ring():
+    """A pair that skips every other phase of a stage takes the phase before it for its own."""
+    with pytest.raises(AssertionError, match="parity alias|holds|surplus|overwritten"):
+        for seed in range(300):
+            _batch([40], seed, ring=5, bias=["w0", "w1", "service"])
+
+
+# ---------------------------------------------------------------------------
+# chunk kernel
+# ---------------------------------------------------------------------------
+
+def _chunk(items, seed, warps=2, q_phase_per_item=False, bias=None):
+    rng = random.Random(seed)
+    q_full, s_read = _Bar("q_full", warps), _Bar("s_read", warps)
+    k_full = [_Bar(f"k_full{i}", warps) for i in range(2)]
+    v_full = [_Bar(f"v_full{i}", warps) for i in range(2)]
+    s_full = [_Bar(f"s_full{i}") for i in range(2)]
+    p_full = [_Bar(f"p_full{i}", warps) for i in range(2)]
+    pv_done = [_Bar(f"pv_done{i}") for i in range(2)]
+    list_full = [_Bar(f"list_full{i}") for i in range(2)]
+    list_free = [_Bar(f"list_free{i}", 2 * warps + 1) for i in range(2)]
+    lists = [_Slot(f"list{i}") for i in range(2)]
+    K = [[_Slot(f"K{b}.{w}") for w in range(warps)] for b in range(2)]
+    V = [[_Slot(f"V{b}.{w}") for w in range(warps)] for b in range(2)]
+    P = [[_Slot(f"P{b}.{w}") for w in range(warps)] for b in range(2)]
+    Q = [None] * warps
+    S, O = {"tag": None, "left": 0}, {"tag": None}
+    mma, stored = [], []
+
+    def run_mma(r):
+        if not mma:
+            return False
+        kind, n, i, first = mma.pop(0)
+        if kind == "S":
+            assert Q == [i] * warps, (Q, i)
+            for x in K[n & 1]:
+                x.read(n)
+            assert S["left"] == 0, "S overwritten before it was read"
+            S.update(tag=n, left=warps)
+            s_full[n & 1].arrive()
+        else:
+            for x in V[n & 1] + P[n & 1]:
+                x.read(n)
+            if first:
+                assert O["tag"] is None or O["tag"][0] in stored, "O overwritten before it was stored"
+            else:
+                assert O["tag"] == (i, n - 1)
+            O["tag"] = (i, n)
+            pv_done[n & 1].arrive()
+        return True
+
+    def list_warp():
+        for i, nt in enumerate(items + [-1]):
+            if i >= 2:
+                yield from _wait(list_free[i & 1], (i >> 1) - 1)
+            lists[i & 1].write(i, 2 * warps + 1)
+            list_full[i & 1].arrive()
+            yield 1
+
+    def issuer():
+        seq, nq = 0, 0
+        for i, nt in enumerate(items + [-1]):
+            yield from _wait(list_full[i & 1], i >> 1)
+            if nt < 0:
+                return
+            lists[i & 1].read(i)
+            list_free[i & 1].arrive()
+            if nt > 0 or q_phase_per_item:
+                yield from _wait(q_full, nq)
+                nq += 1
+            if nt > 0:
+                if seq > 0:
+                    yield from _wait(s_read, seq - 1)
+                yield from _wait(k_full[seq & 1], seq >> 1)
+                mma.append(("S", seq, i, None))
+            for j in range(nt):
+                n = seq + j
+                if j + 1 < nt:
+                    yield from _wait(k_full[(n + 1) & 1], (n + 1) >> 1)
+                    yield from _wait(s_read, n)
+                    mma.append(("S", n + 1, i, None))
+                yield from _wait(p_full[n & 1], n >> 1)
+                yield from _wait(v_full[n & 1], n >> 1)
+                mma.append(("PV", n, i, j == 0))
+                yield 1
+            seq += nt
+
+    def decoder(w):
+        n = 0
+        for i, nt in enumerate(items + [-1]):
+            yield from _wait(list_full[i & 1], i >> 1)
+            if nt < 0:
+                return
+            for _ in range(nt):
+                if n >= 2:
+                    yield from _wait(s_full[n & 1], (n >> 1) - 1)
+                K[n & 1][w].write(n, 1)
+                k_full[n & 1].arrive()
+                yield 1
+                if n >= 2:
+                    yield from _wait(pv_done[n & 1], (n >> 1) - 1)
+                assert lists[i & 1].tag == i
+                V[n & 1][w].write(n, 1)
+                v_full[n & 1].arrive()
+                n += 1
+                yield 1
+            lists[i & 1].read(i)
+            list_free[i & 1].arrive()
+
+    def softmax(w):
+        seq = 0
+        for i, nt in enumerate(items + [-1]):
+            yield from _wait(list_full[i & 1], i >> 1)
+            if nt < 0:
+                return
+            if nt > 0 or q_phase_per_item:
+                Q[w] = i
+                q_full.arrive()
+                yield 1
+            for j in range(nt):
+                n = seq + j
+                yield from _wait(s_full[n & 1], n >> 1)
+                assert S["tag"] == n
+                S["left"] -= 1
+                s_read.arrive()
+                yield 1
+                if j > 0:
+                    yield from _wait(pv_done[(n - 1) & 1], (n - 1) >> 1)
+                    assert O["tag"] == (i, n - 1)
+                P[n & 1][w].write(n, 1)
+                p_full[n & 1].arrive()
+                yield 1
+            if nt > 0:
+                n = seq + nt - 1
+                yield from _wait(pv_done[n & 1], n >> 1)
+                assert O["tag"] == (i, n)
+                if w == warps - 1:
+                    pass
+                done.setdefault(i, set()).add(w)
+                if len(done[i]) == warps:
+                    stored.append(i)
+            yield 1
+            assert lists[i & 1].tag == i
+            lists[i & 1].read(i)
+            list_free[i & 1].arrive()
+            seq += nt
+
+    done = {}
+    threads = {"list": list_warp(), "issuer": issuer(), **{f"d{w}": decoder(w) for w in range(warps)},
+               **{f"s{w}": softmax(w) for w in range(warps)}}
+    _run(threads, rng, [run_mma], bias)
+    assert stored == [i for i, nt in enumerate(items) if nt > 0] and not mma
+
+
+@pytest.mark.parametrize("items", ITEMS)
+@pytest.mark.parametrize("bias", [None, ["s0", "s1"], ["d0", "d1"], ["issuer"], ["list", "d0"], ["s0"]])
+def test_chunk_hand_offs(items, bias):
+    for seed in range(8):
+        _chunk(items, seed, bias=bias)
+
+
+def test_chunk_model_rejects_a_query_phase_for_items_without_tiles():
+    with pytest.raises(AssertionError, match="parity alias|deadlock"):
+        for seed in range(200):
+            _chunk([0, 0, 0, 0, 2, 0, 0, 0], seed, q_phase_per_item=True, bias=["s0", "s1", "list", "d0", "d1"])
