@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) fwd_batch_kernel(FwdCach
       const Shared::Item& it = s.item[i & 1];
       const int ntiles = it.ntiles, qpos = it.qpos;
       if (ntiles < 0) break;
-      const float sc0 = it.qs[gid] * a.scale_log2, sc1 = it.qs[gid + 8] * a.scale_log2;
+      const float sc0 = score_factor(it.qs[gid], a.scale_log2), sc1 = score_factor(it.qs[gid + 8], a.scale_log2);
       float o[16][4], m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;

@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
         }
         const int ex = max((int)(amax >> 7), 15);
         const float mul = __uint_as_float((uint32_t)(268 - ex) << 23);
-        sc = __uint_as_float((uint32_t)(ex - 14) << 23) * a.scale_log2;
+        sc = score_factor(__uint_as_float((uint32_t)(ex - 14) << 23), a.scale_log2);
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};

@@ -81,6 +81,11 @@ MSA_DEV uint32_t pack_half2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// The factor that turns a row's products into powers of two.  Not below the
+// smallest normal number: a masked score is -inf and has to stay it, and 0 * inf
+// is not.
+MSA_DEV float score_factor(float row_scale, float scale_log2) { return fmaxf(row_scale * scale_log2, 1.17549435e-38f); }
+
 // A row of q as fp16 A-fragment words: the lane's 32 dims (32 t .. 32 t + 31),
 // scaled by a power of two that puts the row's largest element at 2^14, so
 // that a bf16 element loses bits only below 2^-31 of the largest.  Returns the
@@ -143,13 +148,6 @@ MSA_DEV void attend32(const uint8_t* tile, int kw, int reach, const uint4 (*q)[3
   // the lane's keys: 16 (jj >> 1) + 4 t + 2 (jj & 1) + e; rows gid and gid + 8
   float bm0 = -CUDART_INF_F, bm1 = -CUDART_INF_F;
   const int left = reach - 4 * t;  // its keys up to this one may be attended
-#pragma unroll
-  for (int jj = 0; jj < 4; ++jj)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      sv[jj][e] *= sc0;
-      sv[jj][2 + e] *= sc1;
-    }
   uint32_t vs[2];
 #pragma unroll
   for (int st2 = 0; st2 < 2; ++st2)
@@ -181,6 +179,8 @@ MSA_DEV void attend32(const uint8_t* tile, int kw, int reach, const uint4 (*q)[3
   bm1 = fmaxf(bm1, __shfl_xor_sync(0xffffffffu, bm1, 1));
   bm0 = fmaxf(bm0, __shfl_xor_sync(0xffffffffu, bm0, 2));
   bm1 = fmaxf(bm1, __shfl_xor_sync(0xffffffffu, bm1, 2));
+  bm0 *= sc0;  // sc > 0, so the maximum of the scaled scores
+  bm1 *= sc1;
   const bool up0 = bm0 > m[0] + (kLift + kTau), up1 = bm1 > m[1] + (kLift + kTau);
   if (__any_sync(0xffffffffu, up0 || up1)) {
     const float al0 = up0 ? ex2_approx(m[0] + kLift - bm0) : 1.f;
@@ -197,12 +197,12 @@ MSA_DEV void attend32(const uint8_t* tile, int kw, int reach, const uint4 (*q)[3
       o[i][3] *= al1;
     }
   }
-  const float m0 = m[0] == -CUDART_INF_F ? 0.f : m[0], m1 = m[1] == -CUDART_INF_F ? 0.f : m[1];
+  const float m0 = m[0] == -CUDART_INF_F ? 0.f : -m[0], m1 = m[1] == -CUDART_INF_F ? 0.f : -m[1];
   uint32_t pa[8];
 #pragma unroll
   for (int jj = 0; jj < 4; ++jj) {
-    const float p0 = ex2_approx(sv[jj][0] - m0), p1 = ex2_approx(sv[jj][1] - m0);
-    const float p2 = ex2_approx(sv[jj][2] - m1), p3 = ex2_approx(sv[jj][3] - m1);
+    const float p0 = ex2_approx(__fmaf_rn(sv[jj][0], sc0, m0)), p1 = ex2_approx(__fmaf_rn(sv[jj][1], sc0, m0));
+    const float p2 = ex2_approx(__fmaf_rn(sv[jj][2], sc1, m1)), p3 = ex2_approx(__fmaf_rn(sv[jj][3], sc1, m1));
     l[0] += p0 + p1;
     l[1] += p2 + p3;
     // fp16 keeps 11 bits of a weight, 3 more than bf16
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kFwdThreads, 3) fwd_cache_kernel(FwdCacheArgs 
         stage_q(tok);
         __syncthreads();
       }
-      const float sc0 = s.qs[gid] * a.scale_log2, sc1 = s.qs[gid + 8] * a.scale_log2;
+      const float sc0 = score_factor(s.qs[gid], a.scale_log2), sc1 = score_factor(s.qs[gid + 8], a.scale_log2);
 #pragma unroll
       for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
       for (int n = pdone; n < ptotal; ++n) {

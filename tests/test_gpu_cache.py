@@ -473,7 +473,7 @@ def test_attention_over_batch_sizes(B, R):
 
 @pytest.mark.parametrize("kw", [dict(k_exp=-8, k_scale=2.0 ** -8), dict(v_exp=20, v_scale=2.0 ** 20),
                                 dict(k_exp=32, k_scale=2.0 ** 30, scale=2.0 ** -34), dict(q_scale=2.0 ** 40, scale=2.0 ** -44),
-                                dict(q_scale=2.0 ** -100), dict(q_scale=30.0), dict(v_exp=-32, v_scale=2.0 ** -34)])
+                                dict(q_scale=2.0 ** -100), dict(q_scale=30.0), dict(q_scale=0.0, scale=2.0 ** -60), dict(v_exp=-32, v_scale=2.0 ** -34)])
 def test_attention_over_magnitudes(B, kw):
     """Cache exponents, queries far from 1, and scores in the hundreds (one key takes all the weight)."""
     _attend_case(B, past=[300, 70], new=[1, 12], H=1, topk=6, **kw)
