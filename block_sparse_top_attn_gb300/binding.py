@@ -554,55 +554,61 @@ class Cache:
         o, lse = cache.forward(q, sel)
 
     new_lens[r] is 0 for an idle request and -1 for one that gives its pages
-    back.  The lengths stay on the device, nothing synchronises, and the
-    buffers of a given number of rows are made once, so a step whose shapes do
-    not change can be captured into a CUDA graph after one eager run.  The
-    step's tensors (slot_map, positions, chunks, cu_tokens) and the outputs
-    belong to the object and hold until the next step of as many rows.  Calls on
-    one object run in the order of their streams: keep them on one stream, or
-    order the streams.  check_status() synchronises and raises on a device
-    error.
+    back.  The lengths stay on the device, nothing synchronises and nothing is
+    allocated after construction, so a step whose shapes do not change can be
+    captured into a CUDA graph.  A step's tables (slot_map, positions, chunks,
+    cu_tokens) and outputs are views of buffers made for max_tokens rows: they
+    hold until the next step's calls.  Calls on one object run in the order of
+    their streams: keep them on one stream, or order the streams.
+    check_status() synchronises and raises on a device error; until reset_status()
+    later calls do nothing.
     """
 
-    def __init__(self, num_requests, num_pages, max_blocks, num_q_heads, topk, block_size=BLOCK,
+    def __init__(self, num_requests, num_pages, max_blocks, num_q_heads, topk, max_tokens, block_size=BLOCK,
                  softmax_scale=HEAD_DIM ** -0.5, k_exp=0, v_exp=0, index_keys=True, device="cuda"):
         import torch
         self.device = torch.empty(0, device=device).device
         self._args = dict(num_requests=num_requests, num_pages=num_pages, max_blocks=max_blocks,
                           num_q_heads=num_q_heads, topk=topk, softmax_scale=softmax_scale, block_size=block_size,
                           k_exp=k_exp, v_exp=v_exp)
-        c = make_cache_problem(token_cap=1, chunk_cap=1, **self._args)
-        R, P, M, H, B = c.num_requests, c.num_pages, c.max_blocks, c.num_kv_heads, c.block_size
-        i32, dev = torch.int32, self.device
-        self.cache = new_cache(c, dev)
+        c = make_cache_problem(token_cap=max_tokens, **self._args)
+        R, P, M, H, B, T, NC = (c.num_requests, c.num_pages, c.max_blocks, c.num_kv_heads, c.block_size, c.token_cap,
+                                c.chunk_cap)
+        i32, bf16, dev = torch.int32, torch.bfloat16, self.device
+        self.cache = new_cache(c, dev)      # checks the description
+        self.max_tokens = T
         self.block_table = torch.zeros((R, M), dtype=i32, device=dev)
         self.seq_lens = torch.zeros(R, dtype=i32, device=dev)
         self.free_ring = torch.arange(P, dtype=i32, device=dev)
         self.ring = torch.tensor([0, P], dtype=i32, device=dev)
         self.cu_tokens = torch.zeros(R + 1, dtype=i32, device=dev)
         self.status = torch.zeros(4, dtype=i32, device=dev)
+        self._slot_map = torch.full((T,), -1, dtype=torch.int64, device=dev)
+        self._positions = torch.full((T,), -1, dtype=i32, device=dev)
+        self._chunks = torch.full((NC, MSA_CHUNK_COLS), -1, dtype=i32, device=dev)
+        self._sel = torch.full((H * NC * c.topk,), -1, dtype=i32, device=dev)
+        self._o = torch.zeros((T, c.num_q_heads, HEAD_DIM), dtype=bf16, device=dev)
+        self._lse = torch.full((T, c.num_q_heads), -math.inf, dtype=torch.float32, device=dev)
         self.index_tail = self.index_pool = None
         if index_keys:
-            self.index_tail = torch.zeros((R, 2, B, H, HEAD_DIM), dtype=torch.bfloat16, device=dev)
-            self.index_pool = torch.zeros((P, H, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+            self.index_tail = torch.zeros((R, 2, B, H, HEAD_DIM), dtype=bf16, device=dev)
+            self.index_pool = torch.zeros((P, H, HEAD_DIM), dtype=bf16, device=dev)
         self._steps = {}
         self._now = None
 
     def _tables(self, tokens):
-        """The problem and buffers of steps with this many token rows, made once."""
-        import torch
+        """The problem and the buffers' views of steps with this many token rows."""
         t = self._steps.get(tokens)
         if t is None:
+            if not 1 <= tokens <= self.max_tokens:
+                raise ValueError(f"tokens: {tokens} rows, made for 1 to {self.max_tokens}")
+            if len(self._steps) >= 64:  # views only: made again when needed
+                self._steps.clear()
             c = make_cache_problem(token_cap=tokens, **self._args)
-            if msa_cache_bytes(c) == 0:
-                raise MSAError(MSA_ERR_INVALID_ARGUMENT, "Cache.step")
-            H, dev = c.num_kv_heads, self.device
-            t = dict(c=c, slot_map=torch.full((tokens,), -1, dtype=torch.int64, device=dev),
-                     positions=torch.full((tokens,), -1, dtype=torch.int32, device=dev),
-                     chunks=torch.full((c.chunk_cap, MSA_CHUNK_COLS), -1, dtype=torch.int32, device=dev),
-                     sel=torch.full((H, c.chunk_cap, c.topk), -1, dtype=torch.int32, device=dev),
-                     o=torch.zeros((tokens, c.num_q_heads, HEAD_DIM), dtype=torch.bfloat16, device=dev),
-                     lse=torch.full((tokens, c.num_q_heads), -math.inf, dtype=torch.float32, device=dev))
+            H, NC, K = c.num_kv_heads, c.chunk_cap, c.topk
+            t = dict(c=c, slot_map=self._slot_map[:tokens], positions=self._positions[:tokens],
+                     chunks=self._chunks[:NC], sel=self._sel[:H * NC * K].view(H, NC, K), o=self._o[:tokens],
+                     lse=self._lse[:tokens])
             self._steps[tokens] = t
         return t
 
@@ -682,3 +688,7 @@ class Cache:
         code = int(self.status[0].item())
         if code != MSA_OK:
             raise MSAError(code, "device status")
+
+    def reset_status(self):
+        """Clears a device error: the next calls run again (a refused step has changed nothing)."""
+        self.status.zero_()

@@ -99,7 +99,7 @@ def test_status_string(B):
 def test_cache_object_checks_its_arguments(B):
     """Wrong types, shapes, strides and order of calls raise before anything is launched (buffers on the CPU)."""
     import torch
-    kv = B.Cache(num_requests=2, num_pages=4, max_blocks=2, num_q_heads=16, topk=2, device="cpu")
+    kv = B.Cache(num_requests=2, num_pages=4, max_blocks=2, num_q_heads=16, topk=2, max_tokens=4, device="cpu")
     with pytest.raises(RuntimeError):
         kv.append(torch.zeros(1), torch.zeros(1))
     with pytest.raises(RuntimeError):
@@ -110,8 +110,9 @@ def test_cache_object_checks_its_arguments(B):
         kv.step(torch.zeros(2, dtype=torch.int64), 2)
     with pytest.raises(ValueError):
         kv.step([1, 1], 2)
-    with pytest.raises(B.MSAError):
-        kv._tables(0)
+    for tokens in (0, -1, 5):
+        with pytest.raises(ValueError, match="tokens"):
+            kv.step(torch.zeros(2, dtype=torch.int32), tokens)
     kv._now = t = kv._tables(3)
     kv.slot_map, kv.positions, kv.chunks = t["slot_map"], t["positions"], t["chunks"]
     x = torch.zeros((3, 1, 128), dtype=torch.bfloat16)
@@ -129,9 +130,26 @@ def test_cache_object_checks_its_arguments(B):
         kv.forward(torch.zeros((3, 16, 128), dtype=torch.bfloat16), t["sel"].long())
     with pytest.raises(ValueError, match="slots"):
         kv.read(torch.zeros(3, dtype=torch.int32))
-    bare = B.Cache(num_requests=2, num_pages=4, max_blocks=2, num_q_heads=16, topk=2, index_keys=False, device="cpu")
+    bare = B.Cache(num_requests=2, num_pages=4, max_blocks=2, num_q_heads=16, topk=2, max_tokens=3, index_keys=False,
+                   device="cpu")
     bare._now = bare._tables(3)
     with pytest.raises(ValueError, match="k_index"):
         bare.append(x, x, x)
     with pytest.raises(RuntimeError):
         bare.select(x)
+
+
+def test_cache_object_views_share_their_buffers(B):
+    """Steps of any number of rows use prefixes of buffers made once; a bad description is refused at once."""
+    import torch
+    kv = B.Cache(num_requests=2, num_pages=4, max_blocks=2, num_q_heads=32, topk=3, max_tokens=200, device="cpu")
+    for tokens in list(range(1, 201)) + [1, 200]:
+        t = kv._tables(tokens)
+        assert t["c"].token_cap == tokens and t["c"].chunk_cap == min(tokens, tokens // 8 + 4)
+        assert t["o"].shape == (tokens, 32, 128) and t["sel"].shape == (2, t["c"].chunk_cap, 3)
+        for name in ("slot_map", "positions", "chunks", "o", "lse", "sel"):
+            assert t[name].is_contiguous() and t[name].data_ptr() == getattr(kv, "_" + name).data_ptr()
+    for bad in (dict(topk=33), dict(num_q_heads=24), dict(block_size=96), dict(max_tokens=0), dict(k_exp=40)):
+        with pytest.raises(B.MSAError):
+            B.Cache(**{**dict(num_requests=2, num_pages=4, max_blocks=2, num_q_heads=32, topk=3, max_tokens=8,
+                              device="cpu"), **bad})

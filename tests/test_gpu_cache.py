@@ -623,7 +623,8 @@ def test_serving_run(B):
     import torch
     rng = np.random.default_rng(11)
     H, block, K, R = 2, 64, 3, 4
-    kv = B.Cache(num_requests=R, num_pages=14, max_blocks=6, num_q_heads=16 * H, topk=K, block_size=block)
+    kv = B.Cache(num_requests=R, num_pages=14, max_blocks=6, num_q_heads=16 * H, topk=K, block_size=block,
+                 max_tokens=300)
     f = Follow(B, kv, H, block, K)
     for new in ([100, 0, 1, 60], [1, 130, 1, 4], [1, 1, 1, 1], [3, 5, 2, 1], [1, -1, 1, -1], [1, 70, 0, 0],
                 [-1, 1, 1, 200], [150, 1, -1, 1], [1, -1, 90, -1], [1, 64, 1, 64], [1] * 4, [1] * 4):
@@ -648,10 +649,11 @@ def test_captured_step_replays(B, block):
     made = []
     for i in range(2):
         rng = np.random.default_rng(20 + i)
-        kv = B.Cache(num_requests=R, num_pages=30, max_blocks=8, num_q_heads=16 * H, topk=K, block_size=block)
+        kv = B.Cache(num_requests=R, num_pages=30, max_blocks=8, num_q_heads=16 * H, topk=K, block_size=block,
+                     max_tokens=183)
         f = Follow(B, kv, H, block, K)
         _drive(B, kv, f, [120, 3, 60], 183, rng)
-        _drive(B, kv, f, [1, 2, 1], T, rng)       # the buffers of T rows exist from here on
+        _drive(B, kv, f, [1, 2, 1], T, rng)
         bufs = {n: torch.zeros((T, H, 128), dtype=torch.bfloat16, device="cuda") for n in ("k", "v", "ki", "qi")}
         bufs["q"] = torch.zeros((T, 16 * H, 128), dtype=torch.bfloat16, device="cuda")
         bufs["new"] = torch.zeros(R, dtype=torch.int32, device="cuda")
@@ -676,7 +678,7 @@ def test_steps_on_two_streams(B):
     runs = []
     for i, st in enumerate(streams):
         rng = np.random.default_rng(30 + i)
-        kv = B.Cache(num_requests=2, num_pages=20, max_blocks=8, num_q_heads=32, topk=4)
+        kv = B.Cache(num_requests=2, num_pages=20, max_blocks=8, num_q_heads=32, topk=4, max_tokens=300)
         f = Follow(B, kv, 2, 64, 4)
         x = [dict(k=_bf16(rng, (T, 2, 128)), v=_bf16(rng, (T, 2, 128)), ki=_bf16(rng, (T, 2, 128)),
                   qi=_bf16(rng, (T, 2, 128)), q=_bf16(rng, (T, 32, 128))) for T in (300, 2)]
@@ -688,7 +690,9 @@ def test_steps_on_two_streams(B):
         for i, (kv, f, st, x, d, new) in enumerate(runs):
             kv.step(new[j], T, stream=st)
             kv.append(d[j]["k"], d[j]["v"], d[j]["ki"], stream=st)
-            outs[i, j] = kv.forward(d[j]["q"], kv.select(d[j]["qi"], stream=st), stream=st)
+            o, lse = kv.forward(d[j]["q"], kv.select(d[j]["qi"], stream=st), stream=st)
+            with torch.cuda.stream(st):
+                outs[i, j] = o.clone(), lse.clone()     # the next step's calls write the same buffers
     torch.cuda.synchronize()
     for i, (kv, f, st, x, d, new) in enumerate(runs):
         kv.check_status()
@@ -705,7 +709,7 @@ def test_whole_prompt_matches_the_training_forward(B):
     H, K, n = 2, 5, 700
     bits = {m: _bf16(rng, (n, h, 128)) for m, h in (("k", H), ("v", H), ("ki", H), ("qi", H), ("q", 16 * H))}
     d = {m: to_bf16_tensor(x, "cuda") for m, x in bits.items()}
-    kv = B.Cache(num_requests=1, num_pages=20, max_blocks=12, num_q_heads=16 * H, topk=K)
+    kv = B.Cache(num_requests=1, num_pages=20, max_blocks=12, num_q_heads=16 * H, topk=K, max_tokens=n)
     kv.step(_dev([n]), n)
     kv.append(d["k"], d["v"], d["ki"])
     sel = kv.select(d["qi"])
@@ -742,3 +746,57 @@ def test_repeated_append_of_a_step_keeps_the_index(B):
         out.append((tail.clone(), pool.clone(), cache.clone()))
     assert s.code() == 0
     assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+def test_largest_batch_of_requests(B):
+    """8192 requests, the most that a step takes: tables of more than 48 KB of shared memory a CTA."""
+    rng = np.random.default_rng(50)
+    s = Setup(B, rng.integers(0, 200, 8192), rng.integers(-1, 3, 8192), kv=False)
+    got = _run_step(B, s, in_place=True)
+    assert s.code() == 0
+    assert np.array_equal(got["slots"], s.want["slot_map"]) and np.array_equal(got["chunks"], s.want["chunks"])
+    assert np.array_equal(got["table"], s.want["block_table"]) and np.array_equal(got["ring"], s.want["free_ring"])
+    assert np.array_equal(got["lens_out"], s.want["seq_lens"])
+
+
+@pytest.mark.parametrize("past, new, H, kernel", [([0] * 60, [25] * 60, 2, "chunks"), ([300] * 200, [1] * 200, 2, "batch"),
+                                                  ([900, 3], [1, 1], 1, "cluster")])
+def test_captured_attention_of_every_kernel(B, past, new, H, kernel):
+    """Each of the three attention kernels captured on a side stream and replayed: the same bits as the eager call."""
+    import torch
+    s = Setup(B, past=past, new=new, H=H, topk=6)
+    s.fill()
+    sel, q = s.selection(), s.queries()
+    want_o, want_lse = s.forward(q, sel)
+    assert s.code() == 0
+    _close(want_o, want_lse, C.attend(q, *s.values(), s.want["chunks"], sel, s.block, s.scale))
+    d = dict(q=to_bf16_tensor(q, "cuda"), table=_dev(s.full), chunks=s.chunk_table(), sel=_dev(sel))
+    o, lse = torch.zeros_like(want_o), torch.zeros_like(want_lse)
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=side):
+        B.msa_cache_fwd(s.c, d["q"], s.cache, d["table"], d["chunks"], d["sel"], o, lse, s.status)
+    for _ in range(3):
+        o.zero_()
+        lse.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want_o) and torch.equal(lse, want_lse)
+
+
+def test_refused_step_can_be_repaired(B):
+    """A step that finds no free page changes nothing; after reset_status the batch goes on as before it."""
+    import torch
+    rng = np.random.default_rng(60)
+    kv = B.Cache(num_requests=2, num_pages=3, max_blocks=4, num_q_heads=16, topk=2, max_tokens=130)
+    f = Follow(B, kv, 1, 64, 2)
+    _drive(B, kv, f, [64, 1], 65, rng)
+    kv.step(_dev([1, 128]), 129)
+    torch.cuda.synchronize()
+    with pytest.raises(B.MSAError) as e:
+        kv.check_status()
+    assert e.value.code == B.MSA_ERR_CAPACITY
+    kv.reset_status()
+    _drive(B, kv, f, [1, 63], 64, rng)
+    _drive(B, kv, f, [-1, 0], 1, rng)
+    _drive(B, kv, f, [0, 65], 65, rng)
