@@ -219,11 +219,11 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
         }
         float m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-        for (int e = 0; e < 64; e += 4) {
+        for (int e = 0; e < 64; e += 8) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) m4[r] = fmaxf(m4[r], xs[e + r]);
+          for (int r = 0; r < 4; ++r) m4[r] = max3(m4[r], xs[e + 2 * r], xs[e + 2 * r + 1]);
         }
-        const float bmax = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc;  // log2 units (sc > 0)
+        const float bmax = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * sc;  // log2 units (sc > 0)
         const bool upd = bmax > m_run + (kLift + kTau);
         const bool resc = upd && m_run > -CUDART_INF_F;
         const float alpha = upd ? ex2_approx(m_run + kLift - bmax) : 1.f;

@@ -172,8 +172,8 @@ MSA_DEV void attend32(const uint8_t* tile, int kw, int reach, const uint4 (*q)[3
   }
 #pragma unroll
   for (int jj = 0; jj < 4; ++jj) {
-    bm0 = fmaxf(bm0, fmaxf(sv[jj][0], sv[jj][1]));
-    bm1 = fmaxf(bm1, fmaxf(sv[jj][2], sv[jj][3]));
+    bm0 = max3(bm0, sv[jj][0], sv[jj][1]);
+    bm1 = max3(bm1, sv[jj][2], sv[jj][3]);
   }
   bm0 = fmaxf(bm0, __shfl_xor_sync(0xffffffffu, bm0, 1));
   bm1 = fmaxf(bm1, __shfl_xor_sync(0xffffffffu, bm1, 1));
