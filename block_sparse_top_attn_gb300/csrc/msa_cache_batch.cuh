@@ -11,7 +11,8 @@
 // their part in shared memory for the even ones and go on; warp 2 then leaves its
 // own for warp 0, which writes the rows.  Nothing synchronises the whole CTA.
 //
-// 256 tokens x 8 heads x 2048 keys: BATCH_US us against 156 with one CTA an item.
+// 256 tokens x 8 heads x 2048 keys: 149 us (4.1 TB/s of cache bytes, 227 TFLOP/s) against
+// 156 with one CTA an item; x 64 keys 23 against 30.
 #pragma once
 
 namespace msa {

@@ -4,20 +4,32 @@
 //   s_j = scale q k_j,  o = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),
 // in one pass with a running maximum.
 //
-// Bound: a token and KV head read 144 bytes per key and do 8192 operations on
-// them, 57 per byte, so the cache's bytes set the floor.  The 16 heads of one
-// KV head are the 16 rows of an m16n8k16 MMA, which leaves no row unused; a
-// 128-row tcgen05 tile would hold one token's 16 rows and 112 empty ones.
-// Codes become fp16 in registers, in the layout of the MMA's B fragment, and
-// never go back to shared memory.
+// Three kernels share the rounding, the tile lists and the result's definition:
+//  - here, for few items: a cluster of CTAs per (token, KV head), each with a
+//    share of the tiles, joined through distributed shared memory;
+//  - msa_cache_batch.cuh, for many single tokens: persistent CTAs;
+//  - msa_cache_chunk.cuh, for chunks of several tokens: 128 rows on tcgen05.
 //
-// A CTA takes one (token, KV head) and, in a cluster, a share of its key
-// tiles.  A producer warp compacts the selection, looks up the pages and
-// copies whole 9 KB tiles (codes and scales of 64 keys are contiguous) into a
-// ring; each of four consumer warps takes 16 keys of every tile, with its own
-// running maximum and output, and nothing is shared until the tiles are done.
-// The partial results of the warps, then those of the cluster's CTAs (through
-// distributed shared memory), are joined in a fixed order.
+// Single tokens.  A token and KV head read 144 bytes per key and do 8192
+// operations on them, 57 per byte, so the cache's bytes set the floor.  The 16
+// heads of one KV head are the 16 rows of an m16n8k16 MMA, which leaves no row
+// unused; a 128-row tcgen05 tile would hold one token's 16 rows and 112 empty
+// ones, and its operands would have to be decoded into shared memory (64 KB
+// written and read per 128 keys, more than the time of their DRAM bytes).  Codes
+// become fp16 in registers, in the layout of the MMA's B fragment.  A warp takes
+// 32 keys, so that four chains of score MMAs overlap (16 keys: 198 us for 256
+// tokens x 8 heads x 2048 keys, 32 keys: 163).
+// What bounds it now: about 600 instructions per 32 keys and warp, of them 128
+// conversions and 128 products at two cycles each and 64 MMAs at eight; such a mix
+// issues at most about 0.6 instructions a cycle, and the kernel reaches 0.46.
+// 8 warps with 200 registers and 12 with 128 take the same time.
+//
+// In this kernel warp 0 compacts the selection and looks up the pages while warp
+// 3 stages the query; whole 9 KB tiles (codes and scales of 64 keys are
+// contiguous) come by bulk copies.  Two pairs of warps take alternate tiles, each
+// with its own stages; each warp has its own running maximum and output, and
+// nothing is shared until the tiles are done.  The parts of the warps, then those
+// of the cluster's CTAs, are joined in a fixed order.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -341,7 +353,6 @@ __global__ void __launch_bounds__(kFwdThreads, 3) fwd_cache_kernel(FwdCacheArgs 
   stage_q(slot);
   __syncthreads();
   const int ntiles = s.ntiles;
-  if (ranks == 1 && s.skip) return;
   for (int tok = slot; tok < c.z; tok += a.slots) {
     const int qpos = c.w + tok;
     const int64_t row0 = (int64_t)(c.y + tok) * a.H * kGroup + h * kGroup;
@@ -455,56 +466,44 @@ __global__ void __launch_bounds__(kFwdThreads, 3) fwd_cache_kernel(FwdCacheArgs 
           }
         }
       }
-      if (ranks == 1) {
-        const float inv = ll == 0.f ? 0.f : a.v_mul / ll;  // a NaN stays one
-        uint4* dst = reinterpret_cast<uint4*>(a.o + (row0 + row) * 128 + 16 * cg8);
-        dst[0] = make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
-                            pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
-        dst[1] = make_uint4(pack_bf16x2(acc[8] * inv, acc[9] * inv), pack_bf16x2(acc[10] * inv, acc[11] * inv),
-                            pack_bf16x2(acc[12] * inv, acc[13] * inv), pack_bf16x2(acc[14] * inv, acc[15] * inv));
-        if (cg8 == 0) a.lse[row0 + row] = ll == 0.f ? -CUDART_INF_F : (mm + log2f(ll)) * kLn2;
-      } else {
-        // this CTA's part of the cluster's result, in place of warp 0's
+      // this CTA's part of the cluster's result, in place of warp 0's
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<float4*>(part + row * 128 + 4 * ((4 * cg8 + i) ^ (row & 7))) =
-              make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
-        if (cg8 == 0) {
-          s.cm[row] = mm;
-          s.cl[row] = ll;
-        }
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<float4*>(part + row * 128 + 4 * ((4 * cg8 + i) ^ (row & 7))) =
+            make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+      if (cg8 == 0) {
+        s.cm[row] = mm;
+        s.cl[row] = ll;
       }
     }
-    if (ranks > 1) {
-      cluster.sync();
-      for (int r = 0; r < ranks; ++r) skip |= *cluster.map_shared_rank(&s.skip, r) != 0;
-      // rank joins rows rank * 16 / ranks ..: a warp takes a row, a lane 4 dims
-      const int rows = 16 / ranks;
-      for (int i = warp; i < rows && !skip; i += kConsumers) {
-        const int row = rank * rows + i, unit = lane;
-        float mm = -CUDART_INF_F;
-        for (int r = 0; r < ranks; ++r) mm = fmaxf(mm, *cluster.map_shared_rank(&s.cm[row], r));
-        float ll = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int r = 0; r < ranks; ++r) {
-          const float wm = *cluster.map_shared_rank(&s.cm[row], r), wl = *cluster.map_shared_rank(&s.cl[row], r);
-          const float f = wm == -CUDART_INF_F ? 0.f : ex2_approx(wm - mm);
-          ll += f * wl;
-          const float4 x = *reinterpret_cast<const float4*>(
-              cluster.map_shared_rank(part + row * 128 + 4 * (unit ^ (row & 7)), r));
-          if (wm != -CUDART_INF_F || wl != 0.f) {
-            acc[0] += f * x.x;
-            acc[1] += f * x.y;
-            acc[2] += f * x.z;
-            acc[3] += f * x.w;
-          }
+    cluster.sync();
+    for (int r = 0; r < ranks; ++r) skip |= *cluster.map_shared_rank(&s.skip, r) != 0;
+    // rank joins rows rank * 16 / ranks ..: a warp takes a row, a lane 4 dims
+    const int rows = 16 / ranks;
+    for (int i = warp; i < rows && !skip; i += kConsumers) {
+      const int row = rank * rows + i, unit = lane;
+      float mm = -CUDART_INF_F;
+      for (int r = 0; r < ranks; ++r) mm = fmaxf(mm, *cluster.map_shared_rank(&s.cm[row], r));
+      float ll = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int r = 0; r < ranks; ++r) {
+        const float wm = *cluster.map_shared_rank(&s.cm[row], r), wl = *cluster.map_shared_rank(&s.cl[row], r);
+        const float f = wm == -CUDART_INF_F ? 0.f : ex2_approx(wm - mm);
+        ll += f * wl;
+        const float4 x = *reinterpret_cast<const float4*>(
+            cluster.map_shared_rank(part + row * 128 + 4 * (unit ^ (row & 7)), r));
+        if (wm != -CUDART_INF_F || wl != 0.f) {
+          acc[0] += f * x.x;
+          acc[1] += f * x.y;
+          acc[2] += f * x.z;
+          acc[3] += f * x.w;
         }
-        const float inv = ll == 0.f ? 0.f : a.v_mul / ll;
-        *reinterpret_cast<uint2*>(a.o + (row0 + row) * 128 + 4 * unit) =
-            make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-        if (unit == 0) a.lse[row0 + row] = ll == 0.f ? -CUDART_INF_F : (mm + log2f(ll)) * kLn2;
       }
-      cluster.sync();  // the peers' parts have been read
+      const float inv = ll == 0.f ? 0.f : a.v_mul / ll;
+      *reinterpret_cast<uint2*>(a.o + (row0 + row) * 128 + 4 * unit) =
+          make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+      if (unit == 0) a.lse[row0 + row] = ll == 0.f ? -CUDART_INF_F : (mm + log2f(ll)) * kLn2;
     }
+    cluster.sync();  // the peers' parts have been read
     if (tok + a.slots < c.z && !skip) {
       // the ring was written by the join: order that before the next copies
       fence_async_smem();
@@ -539,6 +538,7 @@ extern "C" int msa_cache_fwd(const msa_cache_problem* p, const uint16_t* q, cons
   a.NC = p->chunk_cap; a.H = p->num_kv_heads; a.K = p->topk;
   a.scale_log2 = p->softmax_scale * cache::exp2i(p->k_exp) * cache::kLog2e;
   a.v_mul = cache::exp2i(p->v_exp);
+  a.slots = 1;
   a.status = d_status;
   // Chunks of two tokens and more on average, in batches of a few tokens per SM:
   // the 128-row kernel.  It takes the same time for one token of a chunk as for
@@ -571,8 +571,9 @@ extern "C" int msa_cache_fwd(const msa_cache_problem* p, const uint16_t* q, cons
   if (a.slots > 1) a.slots *= 2;
   if (a.slots > kChunk) a.slots = kChunk;
   const int64_t items = (int64_t)p->chunk_cap * a.slots;
-  // CTAs of a cluster share an item's tiles while the items alone leave SMs
-  // idle (three CTAs fit an SM).
+  // CTAs of a cluster share an item's tiles while that leaves at most two CTAs to
+  // an SM.  Beyond that it loses: an item's start and join cost about 6 us
+  // whatever its tiles (2048 items in clusters of 2: 291 us against 162).
   const int tiles = p->topk * (p->block_size / cache::kTile);
   int ranks = 1;
   while (ranks < 8 && ranks * 2 <= tiles && items * p->num_kv_heads * ranks * 2 <= 2 * sms) ranks *= 2;
