@@ -193,6 +193,7 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(StepArgs a) {
   extern __shared__ int32_t s_off[];
   const StepTables s(s_off, a.R);
   const int tid = threadIdx.x, stride = gridDim.x * kStepThreads;
+  after_previous_kernel();
   const StepSums z = step_scan(a, s_off);
   if (!z.err) {
     const int ntok = (int)z.ntok, nchunks = (int)z.nchunks;
@@ -237,6 +238,7 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(StepArgs a) {
 
 __global__ void __launch_bounds__(kStepThreads) step_finish_kernel(StepArgs a) {
   extern __shared__ int32_t s_off[];
+  after_previous_kernel();
   const StepSums z = step_scan(a, s_off);
   if (!z.err) step_finish(a, z, StepTables(s_off, a.R));
 }
@@ -418,6 +420,7 @@ MSA_DEV void index_chunk(const AppendArgs& a, int g, int h, int half, int lane) 
 }
 
 __global__ void __launch_bounds__(256, 6) append_kernel(AppendArgs a) {
+  after_previous_kernel();
   if (status_bad(a.status)) return;
   if ((int)blockIdx.x < a.index_blocks) {
     const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
@@ -483,6 +486,7 @@ MSA_DEV void dequantize16(uint2 codes, uint32_t scale, float mul, uint16_t* dst)
 // A thread takes the same group of two rows, so that two chains of loads (slot,
 // then codes and scales) are in flight: the kernel is bound by their latency.
 __global__ void __launch_bounds__(256) read_kernel(ReadArgs a) {
+  after_previous_kernel();
   if (status_bad(a.status)) return;
   const int grp = threadIdx.x & 7;
   const int lb = a.B == 128 ? 7 : 6;  // log2 of the block
@@ -677,6 +681,7 @@ __global__ void __launch_bounds__(32 * W) select_kernel(SelectArgs a) {
   // heads fastest: CTAs that run together read neighbouring rows of a page
   const int g0 = (int)(blockIdx.x / a.H) * G, h = (int)(blockIdx.x % a.H);
   const int64_t hs = (int64_t)a.H * 128;
+  after_previous_kernel();
   if (status_bad(a.status)) return;
   // lane r of every warp holds chunk row g0 + r
   int4 mine = make_int4(-1, 0, 0, 0);
@@ -843,36 +848,21 @@ int msa_cache_step(const msa_cache_problem* p, const int32_t* new_lens, const in
                     cu_tokens, slot_map, positions, chunks,    p->num_requests, p->num_pages, p->max_blocks,
                     p->block_size, p->token_cap, p->chunk_cap, d_status};
   const size_t smem = (size_t)cache::kStepArrays * (p->num_requests + 1) * sizeof(int32_t);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // CTAs: a token (or chunk) a thread.  Up to 8 form one cluster and one launch;
+  // CTAs: a token (or chunk) a thread.  Up to 32 x 512 rows form one cluster and one launch;
   // above that a grid over the GPU and a second launch that finishes the step.
   const int64_t rows = p->chunk_cap > p->token_cap ? p->chunk_cap : p->token_cap;
   const int64_t want = (rows + cache::kStepThreads - 1) / cache::kStepThreads;
-  if (want <= 8) {
+  if (want <= 32) {
     unsigned ctas = 1;
-    while (ctas < want) ctas *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(cache::kStepThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = ctas;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if ((rc = cuda_status(allow_smem(cache::step_kernel<true>, smem)))) return rc;
-    return cuda_status(cudaLaunchKernelEx(&cfg, cache::step_kernel<true>, a));
+    while (ctas < 8 && ctas < want) ctas *= 2;
+    return cache::launch_kernel(cache::step_kernel<true>, dim3(ctas), cache::kStepThreads, smem, stream, ctas, a);
   }
   int32_t sms = 0;
   if ((rc = sm_count_current(&sms))) return rc;
-  if ((rc = cuda_status(allow_smem(cache::step_kernel<false>, smem)))) return rc;
-  if ((rc = cuda_status(allow_smem(cache::step_finish_kernel, smem)))) return rc;
-  cache::step_kernel<false><<<(unsigned)(want < sms ? want : sms), cache::kStepThreads, smem, st>>>(a);
-  cache::step_finish_kernel<<<1, cache::kStepThreads, smem, st>>>(a);
-  return cuda_status(cudaGetLastError());
+  rc = cache::launch_kernel(cache::step_kernel<false>, dim3((unsigned)(want < sms ? want : sms)), cache::kStepThreads,
+                            smem, stream, 1, a);
+  if (rc) return rc;
+  return cache::launch_kernel(cache::step_finish_kernel, dim3(1), cache::kStepThreads, smem, stream, 1, a);
 }
 
 int msa_cache_append(const msa_cache_problem* p, const uint16_t* k, const uint16_t* v, const uint16_t* k_index,
@@ -889,8 +879,7 @@ int msa_cache_append(const msa_cache_problem* p, const uint16_t* k, const uint16
   cache::AppendArgs a{k, v, k_index, slot_map, cu_tokens, chunks, kv_cache, index_tail, index_pool, (int)T, (int)H,
                       p->block_size, p->num_requests, (int)NC, (int64_t)p->num_pages * p->block_size,
                       cache::exp2i(-p->k_exp), cache::exp2i(-p->v_exp), (int)idx_blocks, d_status};
-  cache::append_kernel<<<(unsigned)(kv_blocks + idx_blocks), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return cuda_status(cudaGetLastError());
+  return cache::launch_kernel(cache::append_kernel, dim3((unsigned)(kv_blocks + idx_blocks)), 256, 0, stream, 1, a);
 }
 
 int msa_cache_read(const msa_cache_problem* p, const int64_t* slots, const uint8_t* kv_cache, uint16_t* k, uint16_t* v,
@@ -905,8 +894,7 @@ int msa_cache_read(const msa_cache_problem* p, const int64_t* slots, const uint8
   if (blocks > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
   cache::ReadArgs a{slots, kv_cache, k, v, (int)T, (int)H, p->block_size, (int64_t)p->num_pages * p->block_size,
                     cache::exp2i(p->k_exp), cache::exp2i(p->v_exp), d_status};
-  cache::read_kernel<<<(unsigned)blocks, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return cuda_status(cudaGetLastError());
+  return cache::launch_kernel(cache::read_kernel, dim3((unsigned)blocks), 256, 0, stream, 1, a);
 }
 
 int msa_cache_select(const msa_cache_problem* p, const uint16_t* q_index, const uint16_t* index_pool,
@@ -922,14 +910,11 @@ int msa_cache_select(const msa_cache_problem* p, const uint16_t* q_index, const 
   // Chunks of several tokens come from prompts, whose chunks share a request's
   // keys: 8 of them to a CTA, while 8 rows of scores fit shared memory.  (One to
   // a CTA: 62 us for the same prompts.)
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int64_t H = p->num_kv_heads, NC = p->chunk_cap;
   if (NC * H > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
   const size_t row = (size_t)p->max_blocks * 4;
   auto launch = [&](auto kernel, size_t smem, int64_t ctas, int threads) {
-    if ((rc = cuda_status(allow_smem(kernel, smem)))) return rc;
-    kernel<<<(unsigned)ctas, threads, smem, st>>>(a);
-    return cuda_status(cudaGetLastError());
+    return cache::launch_kernel(kernel, dim3((unsigned)ctas), threads, smem, stream, 1, a);
   };
   constexpr size_t kSmem = 227 * 1024;
   if (p->token_cap / p->chunk_cap >= 3) {

@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) fwd_batch_kernel(FwdCach
     mbar_init(&s.pair_full, 1);
     fence_mbar_init();
   }
+  after_previous_kernel<false>();
   __syncthreads();
   // Tiles are numbered through all items of the CTA: tile n uses stage n % kRing,
   // lap n / kRing.  Item i uses buffer i & 1, and has one phase of every part

@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
   const uintptr_t raw = reinterpret_cast<uintptr_t>(smem_raw);
   const uintptr_t pad = ((raw + 1023) & ~uintptr_t(1023)) - raw;
   if (pad > ALIGN_SLACK) {  // uniform across the block: nothing has started yet
+    after_previous_kernel<false>();
     if (threadIdx.x == 0) set_status(a.status, MSA_ERR_CUDA);
     return;
   }
@@ -129,6 +130,7 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
     tmem_alloc(&ct.tmem, TMEM_COLS);
     tmem_relinquish();
   }
+  after_previous_kernel<false>();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

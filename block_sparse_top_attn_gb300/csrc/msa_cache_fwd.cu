@@ -291,6 +291,7 @@ __global__ void __launch_bounds__(kFwdThreads, 3) fwd_cache_kernel(FwdCacheArgs 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, pair = warp >> 1;
   const int item = blockIdx.x / ranks, h = blockIdx.y;
   const int g = item / a.slots, slot = item % a.slots;
+  after_previous_kernel<false>();
   // three loads in flight together: a chain of them is a good part of an item
   int entry = -1;
   bool stale = false;
@@ -552,16 +553,13 @@ extern "C" int msa_cache_fwd(const msa_cache_problem* p, const uint16_t* q, cons
     // the warpgroups' register shares add up to the launch's registers, or
     // setmaxnreg would wait for ever
     if (attr.numRegs * 3 < 136 + 72 + 32) return MSA_ERR_CUDA;
-    if (cudaFuncSetAttribute(cache::chunk::fwd_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)cache::chunk::SMEM) != cudaSuccess ||
-        cudaFuncSetAttribute(cache::chunk::fwd_chunk_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+    if (cudaFuncSetAttribute(cache::chunk::fwd_chunk_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                              (int)cudaSharedmemCarveoutMaxShared) != cudaSuccess)
       return MSA_ERR_CUDA;
     const int64_t chunks = (int64_t)p->chunk_cap * p->num_kv_heads;
     const int grid = (int)(chunks < 2 * sms ? chunks : 2 * sms);
-    cache::chunk::fwd_chunk_kernel<<<grid, cache::chunk::kThreads, cache::chunk::SMEM,
-                                     static_cast<cudaStream_t>(stream)>>>(a);
-    return cuda_status(cudaGetLastError());
+    return cache::launch_kernel(cache::chunk::fwd_chunk_kernel, dim3((unsigned)grid), cache::chunk::kThreads,
+                                cache::chunk::SMEM, stream, 1, a);
   }
   // Token slots of a chunk in the grid: one where tokens and chunk rows are
   // equal in number (decode), else twice the mean, at most 8.  A chunk with more
@@ -580,30 +578,16 @@ extern "C" int msa_cache_fwd(const msa_cache_problem* p, const uint16_t* q, cons
   if (items * ranks > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
   if (ranks == 1) {
     // enough items to keep every SM busy: persistent CTAs
-    if (cudaFuncSetAttribute(cache::batch::fwd_batch_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)sizeof(cache::batch::Shared)) != cudaSuccess ||
-        cudaFuncSetAttribute(cache::batch::fwd_batch_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+    if (cudaFuncSetAttribute(cache::batch::fwd_batch_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                              (int)cudaSharedmemCarveoutMaxShared) != cudaSuccess)
       return MSA_ERR_CUDA;
     const int64_t all = (int64_t)p->chunk_cap * p->num_kv_heads;
     const int64_t slots = (int64_t)cache::batch::kCtasPerSm * sms;
     const int grid = (int)(all < slots ? all : slots);
-    cache::batch::fwd_batch_kernel<<<grid, cache::batch::kThreads, sizeof(cache::batch::Shared),
-                                     static_cast<cudaStream_t>(stream)>>>(a);
-    return cuda_status(cudaGetLastError());
+    return cache::launch_kernel(cache::batch::fwd_batch_kernel, dim3((unsigned)grid), cache::batch::kThreads,
+                                sizeof(cache::batch::Shared), stream, 1, a);
   }
-  if ((rc = cuda_status(allow_smem(cache::fwd_cache_kernel, sizeof(cache::FwdShared))))) return rc;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(items * ranks), (unsigned)p->num_kv_heads);
-  cfg.blockDim = dim3(cache::kFwdThreads);
-  cfg.dynamicSmemBytes = sizeof(cache::FwdShared);
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)ranks;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, cache::fwd_cache_kernel, a));
+  return cache::launch_kernel(cache::fwd_cache_kernel,
+                              dim3((unsigned)(items * ranks), (unsigned)p->num_kv_heads), cache::kFwdThreads,
+                              sizeof(cache::FwdShared), stream, (unsigned)ranks, a);
 }
