@@ -255,6 +255,7 @@ struct AppendArgs {
   int T, H, B, R, NC;
   int64_t slots;  // P * B
   float k_mul, v_mul;  // 2^-exp
+  bool wide;           // k and v are aligned to 32 bytes
   int index_blocks;    // leading CTAs that keep the pooled index keys
   int32_t* status;
 };
@@ -273,16 +274,31 @@ inline int64_t row_blocks(int64_t tokens, int64_t heads, int64_t rows) {  // CTA
   return ((tokens + 3) / 4 * 4 * heads + rows - 1) / rows;
 }
 
-// 32 bytes in one load or store (a whole sector a lane); read-only data.
-MSA_DEV void load32(const void* src, uint32_t (&u)[8]) {
-  asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
-      : "l"(src));
+// 32 bytes in one load or store (a whole sector a lane), or in two where the
+// tensors are aligned to 16 bytes only.
+MSA_DEV void load32(const void* src, bool wide, uint32_t (&u)[8]) {
+  if (wide) {
+    asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+        : "l"(src));
+  } else {
+    const uint4 a = __ldg(static_cast<const uint4*>(src)), b = __ldg(static_cast<const uint4*>(src) + 1);
+    u[0] = a.x; u[1] = a.y; u[2] = a.z; u[3] = a.w;
+    u[4] = b.x; u[5] = b.y; u[6] = b.z; u[7] = b.w;
+  }
 }
-MSA_DEV void store32(void* dst, const uint32_t (&u)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(u[0]), "r"(u[1]), "r"(u[2]),
-               "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
-               : "memory");
+MSA_DEV void store32(void* dst, bool wide, const uint32_t (&u)[8]) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(u[0]), "r"(u[1]), "r"(u[2]),
+                 "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+    static_cast<uint4*>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+  }
+}
+inline bool aligned32(const void* a, const void* b) {
+  return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 31u) == 0;
 }
 
 // Clears the sign of the codes that are zero, so that equal values have equal
@@ -441,8 +457,8 @@ __global__ void __launch_bounds__(256, 6) append_kernel(AppendArgs a) {
     return;
   }
   uint32_t kw[8], vw[8];
-  load32(a.k + row * 128 + grp * 16, kw);
-  load32(a.v + row * 128 + grp * 16, vw);
+  load32(a.k + row * 128 + grp * 16, a.wide, kw);
+  load32(a.v + row * 128 + grp * 16, a.wide, vw);
   uint2 kc, vc;
   const uint32_t ks = quantize16(kw, a.k_mul, kc), vs = quantize16(vw, a.v_mul, vc);
   const int lb = a.B == 128 ? 7 : 6;  // log2 of the block
@@ -461,11 +477,12 @@ struct ReadArgs {
   int T, H, B;
   int64_t nslots;
   float k_mul, v_mul;  // 2^exp
+  bool wide;           // k and v are aligned to 32 bytes
   int32_t* status;
 };
 
 // 16 codes and their scale as bf16.
-MSA_DEV void dequantize16(uint2 codes, uint32_t scale, float mul, uint16_t* dst) {
+MSA_DEV void dequantize16(uint2 codes, uint32_t scale, float mul, uint16_t* dst, bool wide) {
   uint32_t s = e4m3x2_to_half(scale);
   s = __byte_perm(s, s, 0x1010);
   uint32_t out[8];
@@ -480,7 +497,7 @@ MSA_DEV void dequantize16(uint2 codes, uint32_t scale, float mul, uint16_t* dst)
                                    __half2float(__ushort_as_half((uint16_t)(y >> 16))) * mul);
     }
   }
-  store32(dst, out);
+  store32(dst, wide, out);
 }
 
 // A thread takes the same group of two rows, so that two chains of loads (slot,
@@ -522,8 +539,8 @@ __global__ void __launch_bounds__(256) read_kernel(ReadArgs a) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     if (!tile[i]) continue;
-    dequantize16(kc[i], ks[i], a.k_mul, a.k + row[i]);
-    dequantize16(vc[i], vs[i], a.v_mul, a.v + row[i]);
+    dequantize16(kc[i], ks[i], a.k_mul, a.k + row[i], a.wide);
+    dequantize16(vc[i], vs[i], a.v_mul, a.v + row[i], a.wide);
   }
 }
 
@@ -878,7 +895,7 @@ int msa_cache_append(const msa_cache_problem* p, const uint16_t* k, const uint16
   if (kv_blocks + idx_blocks > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
   cache::AppendArgs a{k, v, k_index, slot_map, cu_tokens, chunks, kv_cache, index_tail, index_pool, (int)T, (int)H,
                       p->block_size, p->num_requests, (int)NC, (int64_t)p->num_pages * p->block_size,
-                      cache::exp2i(-p->k_exp), cache::exp2i(-p->v_exp), (int)idx_blocks, d_status};
+                      cache::exp2i(-p->k_exp), cache::exp2i(-p->v_exp), cache::aligned32(k, v), (int)idx_blocks, d_status};
   return cache::launch_kernel(cache::append_kernel, dim3((unsigned)(kv_blocks + idx_blocks)), 256, 0, stream, 1, a);
 }
 
@@ -893,7 +910,7 @@ int msa_cache_read(const msa_cache_problem* p, const int64_t* slots, const uint8
   const int64_t blocks = cache::row_blocks(T, H, 64);
   if (blocks > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
   cache::ReadArgs a{slots, kv_cache, k, v, (int)T, (int)H, p->block_size, (int64_t)p->num_pages * p->block_size,
-                    cache::exp2i(p->k_exp), cache::exp2i(p->v_exp), d_status};
+                    cache::exp2i(p->k_exp), cache::exp2i(p->v_exp), cache::aligned32(k, v), d_status};
   return cache::launch_kernel(cache::read_kernel, dim3((unsigned)blocks), 256, 0, stream, 1, a);
 }
 

@@ -800,3 +800,50 @@ def test_refused_step_can_be_repaired(B):
     _drive(B, kv, f, [1, 63], 64, rng)
     _drive(B, kv, f, [-1, 0], 1, rng)
     _drive(B, kv, f, [0, 65], 65, rng)
+
+
+def _off(t):
+    """A copy of t that is aligned to 16 bytes and to no more."""
+    import torch
+    n = 16 // t.element_size()
+    base = torch.zeros(t.numel() + 2 * n + 64, dtype=t.dtype, device=t.device)
+    at = n if base.data_ptr() % 32 == 0 else 0
+    x = base[at:at + t.numel()].view(t.shape)
+    assert x.data_ptr() % 32 == 16
+    x.copy_(t)
+    return x
+
+
+@pytest.mark.parametrize("past, new", [([300, 90, 1], [1, 1, 1]), ([3] * 40, [70] * 40), ([0], [5])])
+def test_tensors_aligned_to_16_bytes_only(B, past, new):
+    """Every call with every pointer 16 bytes off a 32-byte border gives the same bits."""
+    import torch
+    s = Setup(B, past, new, H=2, topk=3)
+    T, R, P = s.c.token_cap, len(past), s.c.num_pages
+    i32 = torch.int32
+
+    def run(f):
+        new_, lens, at = f(_dev(s.new)), f(_dev(s.past)), f(_dev([s.start["head"], s.start["count"]]))
+        ring, table = f(_dev(s.start["ring"])), f(_dev(s.start["table"]))
+        cu, slots = f(torch.zeros(R + 1, dtype=i32, device="cuda")), f(torch.zeros(T, dtype=torch.int64, device="cuda"))
+        pos, chunks = f(torch.zeros(T, dtype=i32, device="cuda")), f(torch.zeros((s.c.chunk_cap, 4), dtype=i32, device="cuda"))
+        st = f(torch.zeros(4, dtype=i32, device="cuda"))
+        B.msa_cache_step(s.c, new_, lens, at, ring, table, lens, at, cu, slots, pos, chunks, st)
+        g = torch.Generator(device="cuda")
+        g.manual_seed(3)
+        rnd = lambda *shape: f(torch.randn(shape, generator=g, device="cuda").bfloat16())
+        k, v, ki, qi, q = rnd(T, 2, 128), rnd(T, 2, 128), rnd(T, 2, 128), rnd(T, 2, 128), rnd(T, 32, 128)
+        tail, pool, cache = rnd(R, 2, 64, 2, 128), rnd(P, 2, 128), f(B.new_cache(s.c))
+        B.msa_cache_append(s.c, k, v, ki, slots, cu, chunks, cache, tail, pool, st)
+        sel = f(torch.full((2, s.c.chunk_cap, 3), -1, dtype=i32, device="cuda"))
+        B.msa_cache_select(s.c, qi, pool, table, chunks, sel, st)
+        o, lse = f(torch.zeros((T, 32, 128), dtype=torch.bfloat16, device="cuda")), f(torch.zeros((T, 32), device="cuda"))
+        B.msa_cache_fwd(s.c, q, cache, table, chunks, sel, o, lse, st)
+        rk, rv = f(torch.zeros_like(k)), f(torch.zeros_like(v))
+        B.msa_cache_read(s.c, slots, cache, rk, rv, st)
+        torch.cuda.synchronize()
+        assert int(st[0].item()) == 0
+        return [lens, at, ring, table, cu, slots, pos, chunks, cache, tail, pool, sel, o, lse, rk, rv]
+
+    for a, b in zip(run(lambda t: t), run(_off)):
+        assert torch.equal(a, b)
