@@ -356,16 +356,17 @@ MSA_DEV uint32_t quantize16(const uint32_t (&w)[8], float mul, uint2& codes) {
   return s8;
 }
 
-// Index keys of half the dims of one (chunk, head), by one warp, a lane owning
-// two dims.
+// Index keys of one chunk, by one CTA: a warp takes half the dims of a head at a
+// time, a lane two dims.
 // The chunk that ends a block averages the block's tokens, those of earlier
 // calls from the tail; a chunk of the request's incomplete block stores its rows
 // to the tail.  Where the incomplete block uses the buffer that the first
 // block's average reads (an even number of blocks apart), the chunk that
 // averages stores them too, after it: a lane reads and writes its own dims
 // only, so the order holds.  The first block's average is made by the
-// request's first chunk, others by the chunk that ends the block.
-MSA_DEV void index_chunk(const AppendArgs& a, int g, int h, int half, int lane) {
+// request's first chunk, others by the chunk that ends the block.  Most chunks of
+// a prompt have nothing to do.
+MSA_DEV void index_chunk(const AppendArgs& a, int g) {
   const int4 c = reinterpret_cast<const int4*>(a.chunks)[g];
   const int r = c.x, row0 = c.y, n = c.z, pos0 = c.w;
   if (r < 0) return;
@@ -378,42 +379,56 @@ MSA_DEV void index_chunk(const AppendArgs& a, int g, int h, int half, int lane) 
            pos0 % a.B + n <= a.B;
   }
   if (!good) {
-    if (lane == 0) set_status(a.status, MSA_ERR_INVALID_CACHE);
+    if (threadIdx.x == 0) set_status(a.status, MSA_ERR_INVALID_CACHE);
     return;
   }
-  const int64_t hs = (int64_t)a.H * 128;  // elements from one token's row to the next
-  const int d = h * 128 + half * 64 + lane * 2;
   const int end = pos0 + (cu1 - row0);     // position behind the request's last new token
   const int past = pos0 - (row0 - cu0);
-  uint16_t* tail = a.index_tail + (int64_t)r * 2 * a.B * hs + d;
-  // averages the block whose last token is row `last`
-  auto average = [&](int last, int blk) {
-    const int64_t slot = a.slot_map[last];
-    if (slot < 0 || slot >= a.slots) return;  // reported by the rows' own CTAs, or left out
-    const uint16_t* old = tail + (int64_t)(blk & 1) * a.B * hs;
-    float lo = 0.f, hi = 0.f;
-    auto add = [&](const uint16_t* src, int rows) {  // rows in flight together; the sums keep the tokens' order
-      for (; rows > 0; rows -= 16, src += 16 * hs) {
-        uint32_t w[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = i < rows ? *reinterpret_cast<const uint32_t*>(src + i * hs) : 0u;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (i < rows) {
-            lo = __fadd_rn(lo, __uint_as_float(w[i] << 16));
-            hi = __fadd_rn(hi, __uint_as_float(w[i] & 0xFFFF0000u));
-          }
-      }
-    };
-    const int olds = max(0, cu0 - (last - (a.B - 1)));  // tokens of earlier calls
-    add(old, olds);
-    add(a.k_index + (int64_t)(last - (a.B - 1) + olds) * hs + d, a.B - olds);
-    const float inv = 1.f / (float)a.B;  // a power of two: the product is the quotient
-    *reinterpret_cast<uint32_t*>(a.index_pool + (slot / a.B) * hs + d) = pack_bf16x2(lo * inv, hi * inv);
-  };
-  // stores rows [p0, p1) (positions) of the incomplete block
   const int blk0 = past / a.B, blk = pos0 / a.B, open = end / a.B;
-  auto keep = [&](int p0, int p1) {
+  const bool shared_buffer = open > blk0 && (open & 1) == (blk0 & 1) && past % a.B != 0;
+  // the last token's row of the block to average (-1: none), positions to store
+  int last = -1;
+  if (row0 == cu0 && open > blk0) last = cu0 + (blk0 + 1) * a.B - past - 1;
+  else if (row0 != cu0 && blk > blk0 && (pos0 + n) % a.B == 0) last = row0 + n - 1;
+  int p0 = 0, p1 = 0;
+  if (shared_buffer) {
+    if (row0 == cu0) { p0 = open * a.B; p1 = end; }
+  } else if (blk == open) {
+    p0 = pos0;
+    p1 = pos0 + n;
+  }
+  if (last < 0 && p0 >= p1) return;
+  const int64_t hs = (int64_t)a.H * 128;  // elements from one token's row to the next
+  const int avg_blk = row0 == cu0 ? blk0 : blk;
+  for (int unit = threadIdx.x >> 5; unit < 2 * a.H; unit += blockDim.x >> 5) {
+    const int d = unit * 64 + (threadIdx.x & 31) * 2;
+    uint16_t* tail = a.index_tail + (int64_t)r * 2 * a.B * hs + d;
+    auto average = [&] {
+      const int64_t slot = a.slot_map[last];
+      if (slot < 0 || slot >= a.slots) return;  // reported by the rows' own CTAs, or left out
+      const uint16_t* old = tail + (int64_t)(avg_blk & 1) * a.B * hs;
+      float lo = 0.f, hi = 0.f;
+      auto add = [&](const uint16_t* src, int rows) {  // rows in flight together; the sums keep the tokens' order
+        for (; rows > 0; rows -= 16, src += 16 * hs) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = i < rows ? *reinterpret_cast<const uint32_t*>(src + i * hs) : 0u;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (i < rows) {
+              lo = __fadd_rn(lo, __uint_as_float(w[i] << 16));
+              hi = __fadd_rn(hi, __uint_as_float(w[i] & 0xFFFF0000u));
+            }
+        }
+      };
+      const int olds = max(0, cu0 - (last - (a.B - 1)));  // tokens of earlier calls
+      add(old, olds);
+      add(a.k_index + (int64_t)(last - (a.B - 1) + olds) * hs + d, a.B - olds);
+      const float inv = 1.f / (float)a.B;  // a power of two: the product is the quotient
+      *reinterpret_cast<uint32_t*>(a.index_pool + (slot / a.B) * hs + d) = pack_bf16x2(lo * inv, hi * inv);
+    };
+    if (last >= 0) average();
+    // the rows of the incomplete block
     uint16_t* dst = tail + (int64_t)(open & 1) * a.B * hs;
     for (int q = p0; q < p1; q += kChunk) {
       uint32_t w[kChunk];
@@ -424,14 +439,6 @@ MSA_DEV void index_chunk(const AppendArgs& a, int g, int h, int half, int lane) 
       for (int i = 0; i < kChunk; ++i)
         if (q + i < p1) *reinterpret_cast<uint32_t*>(dst + ((q + i) % a.B) * hs) = w[i];
     }
-  };
-  const bool shared_buffer = open > blk0 && (open & 1) == (blk0 & 1) && past % a.B != 0;
-  if (row0 == cu0 && open > blk0) average(cu0 + (blk0 + 1) * a.B - past - 1, blk0);
-  if (row0 != cu0 && blk > blk0 && (pos0 + n) % a.B == 0) average(row0 + n - 1, blk);
-  if (shared_buffer) {
-    if (row0 == cu0) keep(open * a.B, end);
-  } else if (blk == open) {
-    keep(pos0, pos0 + n);
   }
 }
 
@@ -439,9 +446,7 @@ __global__ void __launch_bounds__(256, 6) append_kernel(AppendArgs a) {
   after_previous_kernel();
   if (status_bad(a.status)) return;
   if ((int)blockIdx.x < a.index_blocks) {
-    const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    if (w < (int64_t)a.NC * a.H * 2)
-      index_chunk(a, (int)(w / (2 * a.H)), (int)(w / 2 % a.H), (int)(w & 1), threadIdx.x & 31);
+    index_chunk(a, blockIdx.x);
     return;
   }
   // a thread takes one group of 16 dims of K and of V: no value crosses threads
@@ -891,7 +896,7 @@ int msa_cache_append(const msa_cache_problem* p, const uint16_t* k, const uint16
   if (bad_pointers(ptrs, k_index ? 10 : 5)) return MSA_ERR_INVALID_ARGUMENT;
   if ((rc = check_device_current())) return rc;
   const int64_t T = p->token_cap, H = p->num_kv_heads, NC = p->chunk_cap;
-  const int64_t kv_blocks = cache::row_blocks(T, H, 32), idx_blocks = k_index ? (NC * H * 64 + 255) / 256 : 0;
+  const int64_t kv_blocks = cache::row_blocks(T, H, 32), idx_blocks = k_index ? NC : 0;
   if (kv_blocks + idx_blocks > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
   cache::AppendArgs a{k, v, k_index, slot_map, cu_tokens, chunks, kv_cache, index_tail, index_pool, (int)T, (int)H,
                       p->block_size, p->num_requests, (int)NC, (int64_t)p->num_pages * p->block_size,
