@@ -693,7 +693,7 @@ struct SelectShared {
 };
 
 template <int G, int W>
-__global__ void __launch_bounds__(32 * W) select_kernel(SelectArgs a) {
+__global__ void __launch_bounds__(32 * W, 1) select_kernel(SelectArgs a) {
   using S = SelectShared<G, W>;
   constexpr int kThreads = 32 * S::kWarps;
   extern __shared__ __align__(16) uint8_t s_raw[];
