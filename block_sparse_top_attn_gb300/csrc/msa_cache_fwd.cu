@@ -126,7 +126,7 @@ MSA_DEV float load_q_row(const uint16_t* src, uint32_t (&w)[16]) {
 // 32 may be attended (reach >= 0).  sc0, sc1: the factors that turn the scores of
 // rows gid and gid + 8 into powers of two.
 MSA_DEV void attend32(const uint8_t* tile, int kw, int reach, const uint4 (*q)[32], float sc0, float sc1, int lane,
-            float (&o)[16][4], float (&m)[2], float (&l)[2]) {
+                      float (&o)[16][4], float (&m)[2], float (&l)[2]) {
   const int gid = lane >> 2, t = lane & 3;
   // S = Q K^T: column c of n-tile jj is key 16 (jj >> 1) + 4 (c >> 1) +
   // 2 (jj & 1) + (c & 1), k-step ks contracts dims 32 t + 4 ks .. + 3 of

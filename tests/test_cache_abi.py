@@ -35,6 +35,14 @@ def test_sizes(B):
     assert B.msa_cache_bytes(big) == (1 << 20) * 8 * 9216
 
 
+def test_binding_has_the_headers_values(B):
+    import pathlib
+    import re
+    text = (pathlib.Path(__file__).parent.parent / "include" / "msa.h").read_text()
+    for name in ("MSA_ERR_INVALID_CACHE", "MSA_CACHE_TILE_BYTES", "MSA_CHUNK_COLS"):
+        assert getattr(B, name) == int(re.search(rf"\b{name} = (\d+)", text).group(1))
+
+
 def test_chunk_bound_holds_every_step():
     """No lengths need more chunks than the bound (brute force over small batches)."""
     import itertools

@@ -784,6 +784,31 @@ def test_captured_attention_of_every_kernel(B, past, new, H, kernel):
         assert torch.equal(o, want_o) and torch.equal(lse, want_lse)
 
 
+def test_cache_without_index_keys(B):
+    """A cache whose caller brings the selection: no index buffers, and read of the step's slots with padding."""
+    import torch
+    rng = np.random.default_rng(70)
+    kv = B.Cache(num_requests=2, num_pages=9, max_blocks=4, num_q_heads=32, topk=2, max_tokens=210, index_keys=False)
+    bits = {m: _bf16(rng, (210, h, 128)) for m, h in (("k", 2), ("v", 2), ("q", 32))}
+    d = {m: to_bf16_tensor(x, "cuda") for m, x in bits.items()}
+    kv.step(_dev([70, 130]), 210)
+    kv.append(d["k"], d["v"])
+    want = C.step([70, 130], [0, 0], 0, 9, np.arange(9), np.zeros((2, 4), int), 64)
+    sel = np.full((2, kv._tables(210)["c"].chunk_cap, 2), -1)
+    for g, (r, row, n, first) in enumerate(want["chunks"]):
+        sel[:, g, 0], sel[:, g, 1] = first // 64, (0 if first >= 64 else -1)
+    kv._o.fill_(7.0)
+    kv._lse.fill_(7.0)
+    o, lse = kv.forward(d["q"], _dev(sel))
+    k, v = kv.read(kv.slot_map)
+    torch.cuda.synchronize()
+    kv.check_status()
+    kq, vq = C.round_rows(bits["k"][:200], 0)[2], C.round_rows(bits["v"][:200], 0)[2]
+    _close(o, lse, C.attend(bits["q"], [kq[:70], kq[70:]], [vq[:70], vq[70:]], want["chunks"], sel, 64, 128 ** -0.5))
+    for x, y in ((k, kq), (v, vq)):
+        assert np.array_equal(O.bf16_to_f64(from_bf16_tensor(x))[:200], y) and not bool(x[200:].any())
+
+
 def test_refused_step_can_be_repaired(B):
     """A step that finds no free page changes nothing; after reset_status the batch goes on as before it."""
     import torch
@@ -847,3 +872,47 @@ def test_tensors_aligned_to_16_bytes_only(B, past, new):
 
     for a, b in zip(run(lambda t: t), run(_off)):
         assert torch.equal(a, b)
+
+
+def test_captured_step_with_a_join(B):
+    """Calls captured behind a fork and a join with another stream's work (copies, kernels of others): the launches'
+    programmatic serialisation must not skip a dependency."""
+    import torch
+    rng = np.random.default_rng(80)
+    H, T = 2, 64
+    kv = B.Cache(num_requests=T, num_pages=300, max_blocks=4, num_q_heads=16 * H, topk=2, block_size=64,
+                 max_tokens=64 * T)
+    f = Follow(B, kv, H, 64, 2)
+    _drive(B, kv, f, [40 + i % 30 for i in range(T)], 64 * T, rng)
+    _drive(B, kv, f, [1] * T, T, rng)
+    names = {"k": H, "v": H, "ki": H, "qi": H, "q": 16 * H}
+    src = {n: torch.zeros((T, h, 128), dtype=torch.bfloat16, device="cuda") for n, h in names.items()}
+    dst = {n: torch.zeros_like(x) for n, x in src.items()}
+    new = torch.ones(T, dtype=torch.int32, device="cuda")
+    big = torch.zeros(1 << 26, device="cuda")
+    g, side, other = torch.cuda.CUDAGraph(), torch.cuda.Stream(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=side):
+        other.wait_stream(side)
+        kv.step(new, T)
+        with torch.cuda.stream(other):
+            big.add_(1.0)                                   # keeps the other branch behind the step
+            for n in ("k", "v", "ki"):
+                dst[n].copy_(src[n])
+        side.wait_stream(other)
+        kv.append(dst["k"], dst["v"], dst["ki"])
+        for n in ("qi", "q"):
+            dst[n].copy_(src[n])
+        sel = kv.select(dst["qi"])
+        o, lse = kv.forward(dst["q"], sel)
+        keep_o, keep_lse, keep_sel = o.clone(), lse.clone(), sel.clone()
+    for _ in range(4):
+        x = {n: _bf16(rng, (T, h, 128)) for n, h in names.items()}
+        for n in names:
+            src[n].copy_(to_bf16_tensor(x[n], "cuda"))
+        g.replay()
+        torch.cuda.synchronize()
+        kv.check_status()
+        s, wsel, want = f.step([1] * T, *(x[n] for n in ("k", "v", "ki", "qi", "q")))
+        assert np.array_equal(keep_sel.cpu().numpy()[:, :wsel.shape[1]], wsel)
+        _close(keep_o, keep_lse, want)
