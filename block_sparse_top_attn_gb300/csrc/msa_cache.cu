@@ -274,33 +274,6 @@ inline int64_t row_blocks(int64_t tokens, int64_t heads, int64_t rows) {  // CTA
   return ((tokens + 3) / 4 * 4 * heads + rows - 1) / rows;
 }
 
-// 32 bytes in one load or store (a whole sector a lane), or in two where the
-// tensors are aligned to 16 bytes only.
-MSA_DEV void load32(const void* src, bool wide, uint32_t (&u)[8]) {
-  if (wide) {
-    asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
-        : "l"(src));
-  } else {
-    const uint4 a = __ldg(static_cast<const uint4*>(src)), b = __ldg(static_cast<const uint4*>(src) + 1);
-    u[0] = a.x; u[1] = a.y; u[2] = a.z; u[3] = a.w;
-    u[4] = b.x; u[5] = b.y; u[6] = b.z; u[7] = b.w;
-  }
-}
-MSA_DEV void store32(void* dst, bool wide, const uint32_t (&u)[8]) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(u[0]), "r"(u[1]), "r"(u[2]),
-                 "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
-                 : "memory");
-  } else {
-    static_cast<uint4*>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-    static_cast<uint4*>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
-  }
-}
-inline bool aligned32(const void* a, const void* b) {
-  return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 31u) == 0;
-}
-
 // Clears the sign of the codes that are zero, so that equal values have equal
 // bytes.
 MSA_DEV uint32_t unsigned_zeros(uint32_t w) {

@@ -60,6 +60,33 @@ __host__ __device__ __forceinline__ float exp2i(int e) {
   return x.f;
 }
 
+// 32 bytes in one load or store (a whole sector a lane), or in two where the
+// tensors are aligned to 16 bytes only.
+MSA_DEV void load32(const void* src, bool wide, uint32_t (&u)[8]) {
+  if (wide) {
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+        : "l"(src));
+  } else {
+    const uint4 a = __ldg(static_cast<const uint4*>(src)), b = __ldg(static_cast<const uint4*>(src) + 1);
+    u[0] = a.x; u[1] = a.y; u[2] = a.z; u[3] = a.w;
+    u[4] = b.x; u[5] = b.y; u[6] = b.z; u[7] = b.w;
+  }
+}
+MSA_DEV void store32(void* dst, bool wide, const uint32_t (&u)[8]) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(u[0]), "r"(u[1]), "r"(u[2]),
+                 "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+    static_cast<uint4*>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+  }
+}
+inline bool aligned32(const void* a, const void* b) {
+  return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 31u) == 0;
+}
+
 MSA_DEV int64_t tile_index(int64_t page, int head, int heads, int tiles_per_page, int tile) {
   return (page * heads + head) * tiles_per_page + tile;
 }

@@ -7,44 +7,57 @@
 // fp16 shared-memory operands by four warps of their own.
 //
 // A tile is decoded once for the 128 rows, against once per token in the
-// single-token kernel.  Bound by shared memory: per 64-key tile 32 KB are
-// stored by the decoders and 64 KB read by the MMAs (Q again for every tile),
-// 768 cycles at 128 bytes a cycle, against about 700 of MMA issue.  The codes
-// go from global memory to the decoders' registers one tile ahead and never
-// through shared memory, which keeps 18 KB per tile off that path.
+// single-token kernel.  Per 64-key tile 32 KB are stored to shared memory by the
+// decoders and 64 KB read by the MMAs (Q again for every tile): 768 cycles at 128
+// bytes a cycle, against about 700 of MMA issue and 1400 measured: instruction
+// issue, shared memory and the chain S, softmax, P V are all about half used.
+// The codes go from global memory to the decoders' registers one tile ahead and
+// never through shared memory, which keeps 18 KB per tile off that path.
 //
-// Warps 0-3: softmax, one row per thread.  Warps 4-7: decoders.  Warp 8: MMA
-// issue.  Warp 9: the tile lists, one item ahead.  Nothing synchronises the
-// whole CTA between items: the decoders run ahead into the next item as far as
-// the two K and V buffers allow.
+// S has two buffers, so that S_{n+1} runs during the softmax of S_n; P_n takes the
+// place of its own S_n, which is what makes room for them in the 256 columns that
+// two CTAs per SM leave each (with one S and two P: 248 against 243 us for 3.4k new
+// tokens x 4 heads x 2048 keys).  S and P V are issued by threads of their own,
+// whose waits then do not delay each other's MMAs.
+//
+// Warps 0-3: softmax, one row per thread.  Warps 4-7: decoders.  Warps 8 and 9: issue of
+// the S and the P V MMAs.  Warp 10: the tile lists, one item ahead, and what takes a
+// chain of loads: the next item's Q on its way to L2, NaNs among the chunk's own
+// values (236 us with these, 241 without).  Nothing synchronises the whole CTA
+// between items: the decoders run ahead into the next item as far as the two K
+// and V buffers allow.
 #pragma once
 
 namespace msa {
 namespace cache {
 namespace chunk {
 
-constexpr int kThreads = 384;            // three warpgroups; two warps of the last stay idle
-constexpr int kDecodeWarp = 4, kIssueWarp = 8, kListWarp = 9;
+constexpr int kThreads = 384;            // three warpgroups; a warp of the last stays idle
+// of a thread, by warpgroup; the softmax needs no more, as it reads S in halves (136, 72, 32: 251 against 241 us)
+constexpr int kSoftmaxRegs = 104, kDecodeRegs = 72, kOtherRegs = 64;
+constexpr int kDecodeWarp = 4, kScoreWarp = 8, kOutWarp = 9, kListWarp = 10;
 constexpr uint32_t OFF_Q = 0;            // [2 halves][128 rows][128 B]
 constexpr uint32_t OFF_K = 32768;        // 2 buffers x [2 halves][64 keys][128 B]
 constexpr uint32_t OFF_V = 65536;        // 2 buffers x [2 halves][64 keys][128 B]
 constexpr uint32_t OFF_CTL = 98304;
 constexpr uint32_t ALIGN_SLACK = 768;
 constexpr uint32_t TMEM_COLS = 256;
-constexpr uint32_t COL_S = 0, COL_P = 64, COL_O = 128;  // S 64 columns, P 2 x 32 (fp16 pairs), O 128
+constexpr uint32_t COL_S = 0, COL_O = 128;  // S 2 x 64 columns (P, fp16 pairs, over the first 32 of its own), O 128
 
 struct Control {
   uint64_t q_full;                  // Q written (4 softmax warps), one phase per item with tiles
   uint64_t k_full[2], v_full[2];    // decoded (4 decoder warps)
   uint64_t s_full[2];               // S_n done (MMA commit), by n & 1: K buffer n & 1 is free too
-  uint64_t s_read;                  // S_n read (4 softmax warps)
   uint64_t p_full[2];               // P_n written, O rescaled (4 softmax warps)
-  uint64_t pv_done[2];              // P_n V_n done (MMA commit), by n & 1: V buffer n & 1 is free too
+  uint64_t pv_done[2];              // P_n V_n done (MMA commit), by n & 1: V and S buffer n & 1 are free too
   uint64_t list_full[2], list_free[2];
   uint32_t tmem;
   struct List {
     int4 row;                       // the chunk-table row
     int32_t head, ntiles;           // ntiles: -1 ends the walk
+    // bit p of byte g: the value of the chunk's position p (of 8) is NaN in dims
+    // 16 g .. 16 g + 15; bits of positions without a token hold anything
+    alignas(8) uint8_t nan[8];
     int64_t tile[kMaxTiles];
     int32_t key0[kMaxTiles];
   } list[2];
@@ -52,6 +65,14 @@ struct Control {
 constexpr uint32_t SMEM = OFF_CTL + sizeof(Control) + ALIGN_SLACK;
 static_assert(2 * (SMEM + 1024) <= 227 * 1024, "two CTAs per SM");
 
+MSA_DEV void tmem_st16x(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0],"
+      " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 template <int N>
 MSA_DEV void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -64,16 +85,13 @@ MSA_DEV bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
 // One decoder thread's share of a tile: 64 dims (half a row) of one key, of K
 // and of V, with their scales.
 struct Codes {
-  uint4 k[2], v[2];
+  uint32_t k[8], v[8];
   uint32_t ks, vs;  // four e4m3 scales each
 };
+template <bool kWide>
 MSA_DEV void load_codes(Codes& c, const uint8_t* tile, int key, int half) {
-  const uint4* k = reinterpret_cast<const uint4*>(tile + OFF_KC + key * kRowBytes + half * 32);
-  const uint4* v = reinterpret_cast<const uint4*>(tile + OFF_VC + v_code_offset(key, half * 4));
-  c.k[0] = __ldg(k);
-  c.k[1] = __ldg(k + 1);
-  c.v[0] = __ldg(v);
-  c.v[1] = __ldg(v + 1);
+  load32(tile + OFF_KC + key * kRowBytes + half * 32, kWide, c.k);
+  load32(tile + OFF_VC + v_code_offset(key, half * 4), kWide, c.v);
   c.ks = __ldg(reinterpret_cast<const uint32_t*>(tile + OFF_KS + key * kScales + half * 4));
   const uint8_t* s = tile + OFF_VS + half * 4 * kTile + key;
   c.vs = __ldg(s) | __ldg(s + kTile) << 8 | __ldg(s + 2 * kTile) << 16 | (uint32_t)__ldg(s + 3 * kTile) << 24;
@@ -82,7 +100,7 @@ MSA_DEV void load_codes(Codes& c, const uint8_t* tile, int key, int half) {
 MSA_DEV uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w, 0x7F7F7F7Fu); }
 
 // 64 codes to fp16 in the 128-byte swizzled row at dst (row = key).
-MSA_DEV void decode_row(uint8_t* dst, const uint4 (&c)[2], uint32_t scales, int key) {
+MSA_DEV void decode_row(uint8_t* dst, const uint32_t (&c)[8], uint32_t scales, int key) {
   const uint32_t s01 = e4m3x2_to_half(scales & 0xFFFFu), s23 = e4m3x2_to_half(scales >> 16);
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
@@ -91,15 +109,17 @@ MSA_DEV void decode_row(uint8_t* dst, const uint4 (&c)[2], uint32_t scales, int 
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int w = 2 * g + h;  // word of 8 dims
-      const uint4& q = c[w >> 2];
       uint32_t x[4];
-      e2m1x8_to_half((w & 3) == 0 ? q.x : (w & 3) == 1 ? q.y : (w & 3) == 2 ? q.z : q.w, x);
+      e2m1x8_to_half(c[w], x);
       *reinterpret_cast<uint4*>(dst + ((w ^ (key & 7)) << 4)) =
           make_uint4(mul_half2(x[0], sc), mul_half2(x[1], sc), mul_half2(x[2], sc), mul_half2(x[3], sc));
     }
   }
 }
 
+// kWide: q, o and the cache are aligned to 32 bytes (a flag at run time is two
+// paths in the decoders' loop: 234 against 231 us)
+template <bool kWide>
 __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) {
   extern __shared__ uint8_t smem_raw[];
   const uintptr_t raw = reinterpret_cast<uintptr_t>(smem_raw);
@@ -114,7 +134,6 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     mbar_init(&ct.q_full, 4);
-    mbar_init(&ct.s_read, 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ct.k_full[i], 4);
       mbar_init(&ct.v_full[i], 4);
@@ -122,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
       mbar_init(&ct.p_full[i], 4);
       mbar_init(&ct.pv_done[i], 1);
       mbar_init(&ct.list_full[i], 1);
-      mbar_init(&ct.list_free[i], 9);  // softmax and decoder warps, the issuer
+      mbar_init(&ct.list_free[i], 10);  // softmax and decoder warps, the two issuers
     }
     fence_mbar_init();
   }
@@ -139,12 +158,12 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
   constexpr uint32_t ID_S = idesc_f16_f32(128, 64, false, false);
   constexpr uint32_t ID_O = idesc_f16_f32(128, 128, false, true);
   const int64_t items = (int64_t)a.H * a.NC;
-  // Tiles are numbered through all items of the CTA: tile n uses K, V and P
+  // Tiles are numbered through all items of the CTA: tile n uses K, V and S
   // buffer n & 1 and parity (n >> 1) & 1 of their barriers.  Item i uses list
   // buffer i & 1.
   if (warp < kDecodeWarp) {
     // ---------------- softmax, one row per thread ----------------
-    regs_inc<136>();
+    regs_inc<kSoftmaxRegs>();
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
     uint32_t seq = 0;
     for (uint32_t i = 0;; ++i) {
@@ -162,31 +181,28 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
       // warps from running through several such items ahead of the issuer.
       float sc = 0.f;
       if (ntiles > 0) {
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + row * 128);
-        uint4 v[16];
+        uint32_t v[8][8];
         uint32_t amax = 0;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          v[k] = __ldg(src + k);
-          const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+        for (int k = 0; k < 8; ++k) {
+          load32(a.q + row * 128 + k * 16, kWide, v[k]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) amax = max(amax, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+          for (int e = 0; e < 8; ++e) amax = max(amax, max(v[k][e] & 0x7FFFu, (v[k][e] >> 16) & 0x7FFFu));
         }
         const int ex = max((int)(amax >> 7), 15);
         const float mul = __uint_as_float((uint32_t)(268 - ex) << 23);
         sc = score_factor(__uint_as_float((uint32_t)(ex - 14) << 23), a.scale_log2);
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
           uint32_t y[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            y[e] = pack_half2(__uint_as_float(w[e] << 16) * mul, __uint_as_float(w[e] & 0xFFFF0000u) * mul);
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t w = v[k >> 1][(k & 1) * 4 + e];
+            y[e] = pack_half2(__uint_as_float(w << 16) * mul, __uint_as_float(w & 0xFFFF0000u) * mul);
+          }
           *reinterpret_cast<uint4*>(sm + OFF_Q + (k >> 3) * 16384 + tid * 128 + (((k & 7) ^ (tid & 7)) << 4)) =
               make_uint4(y[0], y[1], y[2], y[3]);
         }
-      }
-      if (ntiles > 0) {
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ct.q_full);
@@ -198,32 +214,26 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
         const int key0 = li.key0[j];
         if (!(ok = warp_wait(&ct.s_full[bf], (n >> 1) & 1, a.status))) break;
         tc_fence_after();
-        float xs[64];
-        {
-          uint32_t sv0[32], sv1[32];
-          tmem_ld32x(tmem + lane_base + COL_S, sv0);
-          tmem_ld32x(tmem + lane_base + COL_S + 32, sv1);
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            xs[e] = __uint_as_float(sv0[e]);
-            xs[32 + e] = __uint_as_float(sv1[e]);
-          }
-        }
-        // S_n is in registers: the next S GEMM may overwrite it
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ct.s_read);
-        if (key0 + 63 > c.w) {  // not every key precedes every row
-#pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (key0 + e > qpos) xs[e] = -CUDART_INF_F;
-        }
+        const uint32_t col = tmem + lane_base + COL_S + bf * 64;
+        // Two halves of 32 columns, read once for the maximum and once for the weights:
+        // half the instructions of one long run, and half the registers.
         float m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll 1
+        for (int hf = 0; hf < 64; hf += 32) {
+          uint32_t sv[32];
+          tmem_ld32x(col + hf, sv);
+          tmem_ld_wait();
+          if (key0 + 63 > c.w) {  // not every key precedes every row
 #pragma unroll
-        for (int e = 0; e < 64; e += 8) {
+            for (int e = 0; e < 32; ++e)
+              if (key0 + hf + e > qpos) sv[e] = 0xFF800000u;
+          }
 #pragma unroll
-          for (int r = 0; r < 4; ++r) m4[r] = max3(m4[r], xs[e + 2 * r], xs[e + 2 * r + 1]);
+          for (int e = 0; e < 32; e += 8) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              m4[r] = max3(m4[r], __uint_as_float(sv[e + 2 * r]), __uint_as_float(sv[e + 2 * r + 1]));
+          }
         }
         const float bmax = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * sc;  // log2 units (sc > 0)
         const bool upd = bmax > m_run + (kLift + kTau);
@@ -234,16 +244,27 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
           m_run = bmax - kLift;
         }
         const float nm = m_run == -CUDART_INF_F ? 0.f : -m_run;
-        uint32_t pk[32];
         const uint64_t sc2 = f2_pack(sc, sc), nm2 = f2_pack(nm, nm);
         uint64_t ls2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll 1
+        for (int hf = 0; hf < 64; hf += 32) {
+          uint32_t sv[32], pk[16];
+          tmem_ld32x(col + hf, sv);
+          tmem_ld_wait();
+          if (key0 + 63 > c.w) {
 #pragma unroll
-        for (int e = 0; e < 64; e += 2) {
-          float y0, y1;
-          f2_unpack(f2_fma(f2_pack(xs[e], xs[e + 1]), sc2, nm2), y0, y1);
-          const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
-          ls2[(e >> 1) & 1] = f2_add(ls2[(e >> 1) & 1], f2_pack(p0, p1));
-          pk[e >> 1] = pack_half2(p0, p1);  // fp16: 11 bits of a weight
+            for (int e = 0; e < 32; ++e)
+              if (key0 + hf + e > qpos) sv[e] = 0xFF800000u;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float y0, y1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), sc2, nm2), y0, y1);
+            const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
+            ls2[(e >> 1) & 1] = f2_add(ls2[(e >> 1) & 1], f2_pack(p0, p1));
+            pk[e >> 1] = pack_half2(p0, p1);  // fp16: 11 bits of a weight
+          }
+          tmem_st16x(col + hf / 2, pk);  // columns that have been read
         }
         {
           float a0, a1, b0, b1;
@@ -266,7 +287,6 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
             tmem_st32x(tmem + lane_base + COL_O + c0, ov);
           }
         }
-        tmem_st32x(tmem + lane_base + COL_P + bf * 32, pk);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -278,25 +298,15 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
       if (qpos >= 0) a.lse[row] = l_run == 0.f ? -CUDART_INF_F : (m_run + log2f(l_run)) * kLn2;
       const float inv = l_run == 0.f ? 0.f : a.v_mul / l_run;  // a NaN stays one
       // dims (groups of 16) in which a token of the chunk that this row attends
-      // has a NaN value (see the decoders): the chunk's own tile, if selected
+      // has a NaN value (see the decoders)
       uint32_t nan_groups = 0;
-      if (c.z > 1) {
-        for (int j = 0; j < ntiles; ++j)
-          if (li.key0[j] == c.w / kTile * kTile) {
-            const int at = c.w % kTile / 8 * 8;  // the chunk's 8 positions in the tile
-            const uint8_t* vs = a.cache + li.tile[j] * kTileBytes + OFF_VS + at;
+      const uint64_t nan = *reinterpret_cast<const uint64_t*>(li.nan);
+      if (nan && qpos >= 0) {
+        const uint32_t mine = (2u << (qpos & 7)) - (2u << (c.w & 7));  // positions c.w + 1 .. qpos
 #pragma unroll
-            for (int g = 0; g < 8; ++g) {
-              const uint2 s8 = __ldg(reinterpret_cast<const uint2*>(vs + g * kTile));
-              const uint64_t nan = (uint64_t)nan_bytes(s8.y) << 32 | nan_bytes(s8.x);
-              // positions c.w + 1 .. qpos
-              const int lo = c.w % 8 + 1, hi = qpos < 0 ? 0 : qpos % 8 + 1;
-              const uint64_t mine = hi > lo ? (~uint64_t(0) >> (64 - 8 * (hi - lo))) << (8 * lo) : 0;
-              if (nan & mine) nan_groups |= 1u << g;
-            }
-          }
+        for (int g = 0; g < 8; ++g)
+          if ((uint32_t)(nan >> (8 * g)) & mine & 0xFFu) nan_groups |= 1u << g;
       }
-      uint4* dst = reinterpret_cast<uint4*>(a.o + row * 128);
 #pragma unroll
       for (int c0 = 0; c0 < 128; c0 += 32) {
         uint32_t v[32];
@@ -314,12 +324,13 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
         }
         if (qpos >= 0) {
 #pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4)
-            dst[c0 / 8 + q4] = make_uint4(
-                pack_bf16x2(__uint_as_float(v[8 * q4 + 0]) * inv, __uint_as_float(v[8 * q4 + 1]) * inv),
-                pack_bf16x2(__uint_as_float(v[8 * q4 + 2]) * inv, __uint_as_float(v[8 * q4 + 3]) * inv),
-                pack_bf16x2(__uint_as_float(v[8 * q4 + 4]) * inv, __uint_as_float(v[8 * q4 + 5]) * inv),
-                pack_bf16x2(__uint_as_float(v[8 * q4 + 6]) * inv, __uint_as_float(v[8 * q4 + 7]) * inv));
+          for (int k = 0; k < 32; k += 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              w[e] = pack_bf16x2(__uint_as_float(v[k + 2 * e]) * inv, __uint_as_float(v[k + 2 * e + 1]) * inv);
+            store32(a.o + row * 128 + c0 + k, kWide, w);
+          }
         }
       }
       tc_fence_before();
@@ -327,9 +338,9 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
       __syncwarp();
       if (lane == 0) mbar_arrive(&ct.list_free[i & 1]);
     }
-  } else if (warp < kIssueWarp) {
+  } else if (warp < kScoreWarp) {
     // ---------------- decoders ----------------
-    regs_dec<72>();
+    regs_dec<kDecodeRegs>();
     const int t = tid - 32 * kDecodeWarp, key = t & 63, half = t >> 6;
     uint32_t n = 0;
     for (uint32_t i = 0;; ++i) {
@@ -339,10 +350,10 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
       if (ntiles < 0) break;
       bool ok = true;
       Codes cur, nxt;
-      if (ntiles > 0) load_codes(cur, a.cache + li.tile[0] * kTileBytes, key, half);
+      if (ntiles > 0) load_codes<kWide>(cur, a.cache + li.tile[0] * kTileBytes, key, half);
       for (int j = 0; j < ntiles; ++j, ++n) {
         const uint32_t bf = n & 1, ph = (n >> 1) & 1;
-        if (j + 1 < ntiles) load_codes(nxt, a.cache + li.tile[j + 1] * kTileBytes, key, half);
+        if (j + 1 < ntiles) load_codes<kWide>(nxt, a.cache + li.tile[j + 1] * kTileBytes, key, half);
         if (n >= 2 && !(ok = warp_wait(&ct.s_full[bf], ph ^ 1, a.status))) break;  // S_{n-2} has read its K
         decode_row(sm + OFF_K + bf * 16384 + half * 8192 + key * 128, cur.k, cur.ks, key);
         fence_async_smem();
@@ -367,79 +378,91 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
       if (lane == 0) mbar_arrive(&ct.list_free[i & 1]);
     }
   } else {
-    regs_dec<32>();
-    if (warp == kIssueWarp) {
-      // ---------------- MMA issue ----------------
-      uint32_t seq = 0, nq = 0;  // nq: items with tiles
-      bool ok = true;
-      auto issue_s = [&](uint32_t n) {
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t half = kk >> 2, sub = (kk & 3) * 32;
-            umma_bf16(tmem + COL_S, sdesc_sw128(sbase + OFF_Q + half * 16384 + sub, 16, 1024),
-                      sdesc_sw128(sbase + OFF_K + (n & 1) * 16384 + half * 8192 + sub, 16, 1024), ID_S, kk > 0);
-          }
-          umma_commit(&ct.s_full[n & 1]);
-        }
-        __syncwarp();
-      };
-      for (uint32_t i = 0;; ++i) {
-        if (!warp_wait(&ct.list_full[i & 1], (i >> 1) & 1, a.status)) break;
-        const int ntiles = ct.list[i & 1].ntiles;
-        if (ntiles < 0) break;
-        // the list is not looked at again
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ct.list_free[i & 1]);
-        if (ntiles > 0) {
-          if (!(ok = warp_wait(&ct.q_full, nq++ & 1, a.status))) break;
-          // the S columns: every softmax warp has read the last item's before it wrote Q
-          if (seq > 0 && !(ok = warp_wait(&ct.s_read, (seq - 1) & 1, a.status))) break;
-          if (!(ok = warp_wait(&ct.k_full[seq & 1], (seq >> 1) & 1, a.status))) break;
-          tc_fence_after();
-          issue_s(seq);
-        }
-        for (int j = 0; j < ntiles; ++j) {
-          const uint32_t n = seq + j, bf = n & 1;
-          if (j + 1 < ntiles) {
-            ok = warp_wait(&ct.k_full[bf ^ 1], ((n + 1) >> 1) & 1, a.status) && warp_wait(&ct.s_read, n & 1, a.status);
+    regs_dec<kOtherRegs>();
+    if (warp == kScoreWarp) {
+      // ---------------- S = Q K^T: one thread ----------------
+      if (elect_one()) {
+        uint32_t n = 0, nq = 0;  // nq: items with tiles
+        bool ok = true;
+        for (uint32_t i = 0; ok; ++i) {
+          if (!mbar_wait(&ct.list_full[i & 1], (i >> 1) & 1, a.status)) break;
+          const int ntiles = ct.list[i & 1].ntiles;
+          if (ntiles < 0) break;
+          mbar_arrive(&ct.list_free[i & 1]);  // the list is not looked at again
+          if (ntiles > 0 && !mbar_wait(&ct.q_full, nq++ & 1, a.status)) break;
+          for (int j = 0; j < ntiles; ++j, ++n) {
+            ok = mbar_wait(&ct.k_full[n & 1], (n >> 1) & 1, a.status);
+            // the S columns: P_{n-2} has been read from them
+            if (ok && n >= 2) ok = mbar_wait(&ct.pv_done[n & 1], ((n >> 1) & 1) ^ 1, a.status);
             if (!ok) break;
             tc_fence_after();
-            issue_s(n + 1);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t half = kk >> 2, sub = (kk & 3) * 32;
+              umma_bf16(tmem + COL_S + (n & 1) * 64, sdesc_sw128(sbase + OFF_Q + half * 16384 + sub, 16, 1024),
+                        sdesc_sw128(sbase + OFF_K + (n & 1) * 16384 + half * 8192 + sub, 16, 1024), ID_S, kk > 0);
+            }
+            umma_commit(&ct.s_full[n & 1]);
           }
-          ok = warp_wait(&ct.p_full[bf], (n >> 1) & 1, a.status) && warp_wait(&ct.v_full[bf], (n >> 1) & 1, a.status);
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
+        }
+      }
+    } else if (warp == kOutWarp) {
+      // ---------------- O += P V: one thread ----------------
+      if (elect_one()) {
+        uint32_t n = 0;
+        bool ok = true;
+        for (uint32_t i = 0; ok; ++i) {
+          if (!mbar_wait(&ct.list_full[i & 1], (i >> 1) & 1, a.status)) break;
+          const int ntiles = ct.list[i & 1].ntiles;
+          if (ntiles < 0) break;
+          mbar_arrive(&ct.list_free[i & 1]);
+          for (int j = 0; j < ntiles; ++j, ++n) {
+            const uint32_t bf = n & 1;
+            ok = mbar_wait(&ct.v_full[bf], (n >> 1) & 1, a.status) && mbar_wait(&ct.p_full[bf], (n >> 1) & 1, a.status);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              umma_bf16_ts(tmem + COL_O, tmem + COL_P + bf * 32 + kk * 8,
+              umma_bf16_ts(tmem + COL_O, tmem + COL_S + bf * 64 + kk * 8,
                            sdesc_sw128(sbase + OFF_V + bf * 16384 + kk * 2048, 8192, 1024), ID_O,
                            (j > 0 || kk > 0) ? 1u : 0u);
             umma_commit(&ct.pv_done[bf]);
           }
-          __syncwarp();
         }
-        if (!ok) break;
-        seq += ntiles;
       }
     } else if (warp == kListWarp) {
       // ---------------- tile lists ----------------
       const bool stale = status_bad(a.status);
       uint32_t i = 0;
+      int4 c_next;
+      int entry_next;
+      auto fetch = [&](int64_t w) {  // chunk row and selection, one item ahead
+        c_next = make_int4(-1, 0, 0, 0);
+        entry_next = -1;
+        if (w >= items) return;
+        const int64_t g = w / a.H;
+        c_next = reinterpret_cast<const int4*>(a.chunks)[g];
+        if (lane < a.K) entry_next = a.sel[((w - g * a.H) * a.NC + g) * a.K + lane];
+      };
+      if (!stale) fetch(blockIdx.x);
       for (int64_t w = blockIdx.x;; w += gridDim.x) {
-        int4 c = make_int4(-1, 0, 0, 0);
-        int h = 0;
-        bool end = stale || w >= items;
+        const int4 c = c_next;
+        const int entry = entry_next;
+        const int h = (int)(w % a.H);  // heads fastest: neighbouring CTAs read neighbouring tiles
+        const bool end = stale || w >= items;
         if (!end) {
-          h = (int)(w % a.H);  // heads fastest: neighbouring CTAs read neighbouring tiles
-          c = reinterpret_cast<const int4*>(a.chunks)[w / a.H];
+          fetch(w + gridDim.x);
           if (c.x < 0) continue;
         }
         int total = -1, x = 0, ntl = 0, page = 0, b = -1;
+        uint32_t nan = 0;
         if (!end) {
-          const int entry = lane < a.K ? a.sel[((int64_t)h * a.NC + w / a.H) * a.K + lane] : -1;
           if (!list_tiles(a, c, entry, lane, b, page, ntl)) continue;
+          // Q of the item: on its way to L2 while the item before is attended
+          for (int tok = 0; tok < c.z; ++tok) {
+            const uint16_t* line = a.q + ((int64_t)(c.y + tok) * a.H + h) * kGroup * 128 + lane * 64;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
+          }
           x = ntl;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -447,6 +470,19 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
             if (lane >= o) x += y;
           }
           total = __shfl_sync(0xffffffffu, x, 31);
+          // NaN scales of the values of the chunk's own positions, if its block is selected
+          const uint32_t own = __ballot_sync(0xffffffffu, c.z > 1 && b == c.w / a.B);
+          if (own) {
+            const int own_page = __shfl_sync(0xffffffffu, page, __ffs(own) - 1);
+            if (lane < 8) {
+              const uint8_t* vs = a.cache + tile_index(own_page, h, a.H, a.B / kTile, c.w % a.B / kTile) * kTileBytes +
+                                  OFF_VS + lane * kTile + c.w % kTile / 8 * 8;
+              const uint2 s8 = __ldg(reinterpret_cast<const uint2*>(vs));
+              // one bit of each byte, gathered in the top four
+              nan = ((nan_bytes(s8.x) & 0x01010101u) * 0x10204080u) >> 28 |
+                    ((nan_bytes(s8.y) & 0x01010101u) * 0x10204080u) >> 28 << 4;
+            }
+          }
         }
         if (i >= 2 && !warp_wait(&ct.list_free[i & 1], ((i >> 1) & 1) ^ 1, a.status)) break;
         Control::List& li = ct.list[i & 1];
@@ -459,6 +495,7 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
           li.head = h;
           li.ntiles = total;
         }
+        if (lane < 8) li.nan[lane] = (uint8_t)nan;
         __syncwarp();
         if (lane == 0) mbar_arrive(&ct.list_full[i & 1]);
         ++i;

@@ -548,18 +548,20 @@ extern "C" int msa_cache_fwd(const msa_cache_problem* p, const uint16_t* q, cons
   // 8 tokens x 16 requests x 8 heads x 32 tiles 50 against 108 us, 3 tokens x 8
   // requests 38 against 28.
   if (p->token_cap / p->chunk_cap >= 2 && (int64_t)p->token_cap * p->num_kv_heads * 2 >= 5 * sms) {
+    const bool wide = cache::aligned32(q, o) && cache::aligned32(kv_cache, nullptr);
+    const auto kernel = wide ? cache::chunk::fwd_chunk_kernel<true> : cache::chunk::fwd_chunk_kernel<false>;
     cudaFuncAttributes attr;
-    if (cudaFuncGetAttributes(&attr, cache::chunk::fwd_chunk_kernel) != cudaSuccess) return MSA_ERR_CUDA;
+    if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess) return MSA_ERR_CUDA;
     // the warpgroups' register shares add up to the launch's registers, or
     // setmaxnreg would wait for ever
-    if (attr.numRegs * 3 < 136 + 72 + 32) return MSA_ERR_CUDA;
-    if (cudaFuncSetAttribute(cache::chunk::fwd_chunk_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+    if (attr.numRegs * 3 < cache::chunk::kSoftmaxRegs + cache::chunk::kDecodeRegs + cache::chunk::kOtherRegs)
+      return MSA_ERR_CUDA;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                              (int)cudaSharedmemCarveoutMaxShared) != cudaSuccess)
       return MSA_ERR_CUDA;
     const int64_t chunks = (int64_t)p->chunk_cap * p->num_kv_heads;
     const int grid = (int)(chunks < 2 * sms ? chunks : 2 * sms);
-    return cache::launch_kernel(cache::chunk::fwd_chunk_kernel, dim3((unsigned)grid), cache::chunk::kThreads,
-                                cache::chunk::SMEM, stream, 1, a);
+    return cache::launch_kernel(kernel, dim3((unsigned)grid), cache::chunk::kThreads, cache::chunk::SMEM, stream, 1, a);
   }
   // Token slots of a chunk in the grid: one where tokens and chunk rows are
   // equal in number (decode), else twice the mean, at most 8.  A chunk with more

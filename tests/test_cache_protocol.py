@@ -1,14 +1,15 @@
 """CPU model check of the hand-offs of the two persistent cached-attention
 kernels (no GPU): `msa_cache_batch.cuh` (a service warp that feeds a ring, two
 pairs of attending warps, joins through shared memory) and `msa_cache_chunk.cuh`
-(list warp, decoders, MMA issuer, softmax warps).
+(list warp, decoders, two MMA issuers, softmax warps).
 
 The model replays the kernels' order of waits, arrivals, copies and MMAs under
 random interleavings.  A parity wait is correct only while the barrier is on
 the awaited phase or has just completed it; copies land in any order, MMAs in
-issue order; a buffer may be overwritten only once its readers are done, and
-every reader must find its own tile, item or part.  Odd rings, and one phase of
-the query barrier for items without tiles, fail it."""
+the order of their issuing thread; a buffer may be overwritten only once its
+readers are done, and every reader must find its own tile, item or part.  Odd
+rings, one phase of the query barrier for items without tiles, and scores
+written over weights that are still read fail it."""
 import random
 
 import pytest
@@ -180,38 +181,41 @@ def test_batch_model_rejects_an_odd_ring():
 # chunk kernel
 # ---------------------------------------------------------------------------
 
-def _chunk(items, seed, warps=2, q_phase_per_item=False, bias=None):
+def _chunk(items, seed, warps=2, q_phase_per_item=False, early_scores=False, bias=None):
     rng = random.Random(seed)
-    q_full, s_read = _Bar("q_full", warps), _Bar("s_read", warps)
+    q_full = _Bar("q_full", warps)
     k_full = [_Bar(f"k_full{i}", warps) for i in range(2)]
     v_full = [_Bar(f"v_full{i}", warps) for i in range(2)]
     s_full = [_Bar(f"s_full{i}") for i in range(2)]
     p_full = [_Bar(f"p_full{i}", warps) for i in range(2)]
     pv_done = [_Bar(f"pv_done{i}") for i in range(2)]
     list_full = [_Bar(f"list_full{i}") for i in range(2)]
-    list_free = [_Bar(f"list_free{i}", 2 * warps + 1) for i in range(2)]
+    list_free = [_Bar(f"list_free{i}", 2 * warps + 2) for i in range(2)]
     lists = [_Slot(f"list{i}") for i in range(2)]
     K = [[_Slot(f"K{b}.{w}") for w in range(warps)] for b in range(2)]
     V = [[_Slot(f"V{b}.{w}") for w in range(warps)] for b in range(2)]
-    P = [[_Slot(f"P{b}.{w}") for w in range(warps)] for b in range(2)]
+    SP = [[_Slot(f"SP{b}.{w}") for w in range(warps)] for b in range(2)]   # a warp's rows of S, then of P
     Q = [None] * warps
-    S, O = {"tag": None, "left": 0}, {"tag": None}
-    mma, stored = [], []
+    O, stored = {"tag": None}, []
+    mma = {"S": [], "PV": []}   # in order within an issuing thread, in any order between the two
 
     def run_mma(r):
-        if not mma:
+        kind = r.choice(["S", "PV"])
+        if not mma[kind]:
             return False
-        kind, n, i, first = mma.pop(0)
+        n, i, first = mma[kind].pop(0)
         if kind == "S":
             assert Q == [i] * warps, (Q, i)
             for x in K[n & 1]:
                 x.read(n)
-            assert S["left"] == 0, "S overwritten before it was read"
-            S.update(tag=n, left=warps)
+            for x in SP[n & 1]:
+                x.write(("S", n), 1)
             s_full[n & 1].arrive()
         else:
-            for x in V[n & 1] + P[n & 1]:
+            for x in V[n & 1]:
                 x.read(n)
+            for x in SP[n & 1]:
+                x.read(("P", n))
             if first:
                 assert O["tag"] is None or O["tag"][0] in stored, "O overwritten before it was stored"
             else:
@@ -224,12 +228,12 @@ def _chunk(items, seed, warps=2, q_phase_per_item=False, bias=None):
         for i, nt in enumerate(items + [-1]):
             if i >= 2:
                 yield from _wait(list_free[i & 1], (i >> 1) - 1)
-            lists[i & 1].write(i, 2 * warps + 1)
+            lists[i & 1].write(i, 2 * warps + 2)
             list_full[i & 1].arrive()
             yield 1
 
-    def issuer():
-        seq, nq = 0, 0
+    def score_issuer():
+        n = nq = 0
         for i, nt in enumerate(items + [-1]):
             yield from _wait(list_full[i & 1], i >> 1)
             if nt < 0:
@@ -239,22 +243,28 @@ def _chunk(items, seed, warps=2, q_phase_per_item=False, bias=None):
             if nt > 0 or q_phase_per_item:
                 yield from _wait(q_full, nq)
                 nq += 1
-            if nt > 0:
-                if seq > 0:
-                    yield from _wait(s_read, seq - 1)
-                yield from _wait(k_full[seq & 1], seq >> 1)
-                mma.append(("S", seq, i, None))
-            for j in range(nt):
-                n = seq + j
-                if j + 1 < nt:
-                    yield from _wait(k_full[(n + 1) & 1], (n + 1) >> 1)
-                    yield from _wait(s_read, n)
-                    mma.append(("S", n + 1, i, None))
-                yield from _wait(p_full[n & 1], n >> 1)
-                yield from _wait(v_full[n & 1], n >> 1)
-                mma.append(("PV", n, i, j == 0))
+            for _ in range(nt):
+                yield from _wait(k_full[n & 1], n >> 1)
+                if n >= 2 and not early_scores:
+                    yield from _wait(pv_done[n & 1], (n >> 1) - 1)
+                mma["S"].append((n, i, None))
+                n += 1
                 yield 1
-            seq += nt
+
+    def out_issuer():
+        n = 0
+        for i, nt in enumerate(items + [-1]):
+            yield from _wait(list_full[i & 1], i >> 1)
+            if nt < 0:
+                return
+            lists[i & 1].read(i)
+            list_free[i & 1].arrive()
+            for j in range(nt):
+                yield from _wait(v_full[n & 1], n >> 1)
+                yield from _wait(p_full[n & 1], n >> 1)
+                mma["PV"].append((n, i, j == 0))
+                n += 1
+                yield 1
 
     def decoder(w):
         n = 0
@@ -291,22 +301,18 @@ def _chunk(items, seed, warps=2, q_phase_per_item=False, bias=None):
             for j in range(nt):
                 n = seq + j
                 yield from _wait(s_full[n & 1], n >> 1)
-                assert S["tag"] == n
-                S["left"] -= 1
-                s_read.arrive()
+                SP[n & 1][w].read(("S", n))
                 yield 1
+                SP[n & 1][w].write(("P", n), 1)
                 if j > 0:
                     yield from _wait(pv_done[(n - 1) & 1], (n - 1) >> 1)
                     assert O["tag"] == (i, n - 1)
-                P[n & 1][w].write(n, 1)
                 p_full[n & 1].arrive()
                 yield 1
             if nt > 0:
                 n = seq + nt - 1
                 yield from _wait(pv_done[n & 1], n >> 1)
                 assert O["tag"] == (i, n)
-                if w == warps - 1:
-                    pass
                 done.setdefault(i, set()).add(w)
                 if len(done[i]) == warps:
                     stored.append(i)
@@ -317,14 +323,14 @@ def _chunk(items, seed, warps=2, q_phase_per_item=False, bias=None):
             seq += nt
 
     done = {}
-    threads = {"list": list_warp(), "issuer": issuer(), **{f"d{w}": decoder(w) for w in range(warps)},
+    threads = {"list": list_warp(), "s_issuer": score_issuer(), "o_issuer": out_issuer(), **{f"d{w}": decoder(w) for w in range(warps)},
                **{f"s{w}": softmax(w) for w in range(warps)}}
     _run(threads, rng, [run_mma], bias)
-    assert stored == [i for i, nt in enumerate(items) if nt > 0] and not mma
+    assert stored == [i for i, nt in enumerate(items) if nt > 0] and not mma["S"] and not mma["PV"]
 
 
 @pytest.mark.parametrize("items", ITEMS)
-@pytest.mark.parametrize("bias", [None, ["s0", "s1"], ["d0", "d1"], ["issuer"], ["list", "d0"], ["s0"]])
+@pytest.mark.parametrize("bias", [None, ["s0", "s1"], ["d0", "d1"], ["s_issuer"], ["o_issuer"], ["list", "d0"], ["s0"]])
 def test_chunk_hand_offs(items, bias):
     for seed in range(8):
         _chunk(items, seed, bias=bias)
@@ -334,3 +340,9 @@ def test_chunk_model_rejects_a_query_phase_for_items_without_tiles():
     with pytest.raises(AssertionError, match="parity alias|deadlock"):
         for seed in range(200):
             _chunk([0, 0, 0, 0, 2, 0, 0, 0], seed, q_phase_per_item=True, bias=["s0", "s1", "list", "d0", "d1"])
+
+
+def test_chunk_model_rejects_scores_over_weights_in_use():
+    with pytest.raises(AssertionError, match="SP|parity alias|holds"):
+        for seed in range(200):
+            _chunk([9], seed, early_scores=True, bias=["d0", "d1", "s_issuer"])
