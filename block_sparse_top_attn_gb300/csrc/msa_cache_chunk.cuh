@@ -9,23 +9,28 @@
 // A tile is decoded once for the 128 rows, against once per token in the
 // single-token kernel.  Per 64-key tile 32 KB are stored to shared memory by the
 // decoders and 64 KB read by the MMAs (Q again for every tile): 768 cycles at 128
-// bytes a cycle, against about 700 of MMA issue and 1400 measured: instruction
-// issue, shared memory and the chain S, softmax, P V are all about half used.
-// The codes go from global memory to the decoders' registers one tile ahead and
-// never through shared memory, which keeps 18 KB per tile off that path.
+// bytes a cycle, against about 700 of MMA issue and 1300 measured: instruction
+// issue, shared memory and the chain S, softmax, P V are all half used.
+// The codes go from global memory to the decoders' registers and never through
+// shared memory, which keeps 18 KB per tile off that path.  A row's next codes are
+// loaded as soon as its registers are free, K after K, V after V: loads before the
+// decoding of K hold up its stores, and S waits for K (220 against 217 us).
 //
 // S has two buffers, so that S_{n+1} runs during the softmax of S_n; P_n takes the
 // place of its own S_n, which is what makes room for them in the 256 columns that
-// two CTAs per SM leave each (with one S and two P: 248 against 243 us for 3.4k new
-// tokens x 4 heads x 2048 keys).  S and P V are issued by threads of their own,
-// whose waits then do not delay each other's MMAs.
+// two CTAs per SM leave each (with one S and two P: 248 against 243 us).  S and P V
+// are issued by threads of their own, whose waits then do not delay each other's MMAs.
 //
 // Warps 0-3: softmax, one row per thread.  Warps 4-7: decoders.  Warps 8 and 9: issue of
 // the S and the P V MMAs.  Warp 10: the tile lists, one item ahead, and what takes a
 // chain of loads: the next item's Q on its way to L2, NaNs among the chunk's own
 // values (236 us with these, 241 without).  Nothing synchronises the whole CTA
 // between items: the decoders run ahead into the next item as far as the two K
-// and V buffers allow.
+// and V buffers allow.  (A next item's Q or codes loaded before this one's end:
+// 239 and 232 us, slower although the waits are shorter.)
+//
+// Times: 3.4k new tokens x 4 heads x 2048 keys, 207 us (924 TFLOP/s); 4k x 8 heads
+// the same 517 us (1047 TFLOP/s).
 #pragma once
 
 namespace msa {
@@ -33,8 +38,9 @@ namespace cache {
 namespace chunk {
 
 constexpr int kThreads = 384;            // three warpgroups; a warp of the last stays idle
-// of a thread, by warpgroup; the softmax needs no more, as it reads S in halves (136, 72, 32: 251 against 241 us)
-constexpr int kSoftmaxRegs = 104, kDecodeRegs = 72, kOtherRegs = 64;
+// of a thread, by warpgroup: the softmax needs no more, as it reads S in halves, and the issuers keep
+// their descriptors (88, 72, 80 gives 210 us, 104, 72, 64 214, none of its own to a warpgroup 221, against 207)
+constexpr int kSoftmaxRegs = 104, kDecodeRegs = 64, kOtherRegs = 72;
 constexpr int kDecodeWarp = 4, kScoreWarp = 8, kOutWarp = 9, kListWarp = 10;
 constexpr uint32_t OFF_Q = 0;            // [2 halves][128 rows][128 B]
 constexpr uint32_t OFF_K = 32768;        // 2 buffers x [2 halves][64 keys][128 B]
@@ -85,16 +91,19 @@ MSA_DEV bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
 // One decoder thread's share of a tile: 64 dims (half a row) of one key, of K
 // and of V, with their scales.
 struct Codes {
-  uint32_t k[8], v[8];
-  uint32_t ks, vs;  // four e4m3 scales each
+  uint32_t w[8];
+  uint32_t scales;  // four e4m3
 };
 template <bool kWide>
-MSA_DEV void load_codes(Codes& c, const uint8_t* tile, int key, int half) {
-  load32(tile + OFF_KC + key * kRowBytes + half * 32, kWide, c.k);
-  load32(tile + OFF_VC + v_code_offset(key, half * 4), kWide, c.v);
-  c.ks = __ldg(reinterpret_cast<const uint32_t*>(tile + OFF_KS + key * kScales + half * 4));
+MSA_DEV void load_k(Codes& c, const uint8_t* tile, int key, int half) {
+  load32(tile + OFF_KC + key * kRowBytes + half * 32, kWide, c.w);
+  c.scales = __ldg(reinterpret_cast<const uint32_t*>(tile + OFF_KS + key * kScales + half * 4));
+}
+template <bool kWide>
+MSA_DEV void load_v(Codes& c, const uint8_t* tile, int key, int half) {
+  load32(tile + OFF_VC + v_code_offset(key, half * 4), kWide, c.w);
   const uint8_t* s = tile + OFF_VS + half * 4 * kTile + key;
-  c.vs = __ldg(s) | __ldg(s + kTile) << 8 | __ldg(s + 2 * kTile) << 16 | (uint32_t)__ldg(s + 3 * kTile) << 24;
+  c.scales = __ldg(s) | __ldg(s + kTile) << 8 | __ldg(s + 2 * kTile) << 16 | (uint32_t)__ldg(s + 3 * kTile) << 24;
 }
 // Bytes of w that are the e4m3 NaN (0x7F; scales have no sign), as 0xFF.
 MSA_DEV uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w, 0x7F7F7F7Fu); }
@@ -272,10 +281,10 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
           f2_unpack(ls2[1], b0, b1);
           l_run += (a0 + a1) + (b0 + b1);
         }
-        // P V of the tile before: done before O is rescaled and before its
-        // successor's P is signalled, so its phases are taken in order
-        if (j > 0 && !(ok = warp_wait(&ct.pv_done[bf ^ 1], ((n - 1) >> 1) & 1, a.status))) break;
         if (__any_sync(0xffffffffu, resc)) {  // warp-collective TMEM access
+          // P V of the tile before.  (Its phase cannot be taken for the one before it:
+          // S_{n-1} was issued after P_{n-3} V_{n-3}.)
+          if (!(ok = warp_wait(&ct.pv_done[bf ^ 1], ((n - 1) >> 1) & 1, a.status))) break;
           tc_fence_after();
 #pragma unroll 1
           for (int c0 = 0; c0 < 128; c0 += 32) {
@@ -349,16 +358,21 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
       const int ntiles = li.ntiles, last = li.row.w + li.row.z - 1;  // the chunk's last position
       if (ntiles < 0) break;
       bool ok = true;
-      Codes cur, nxt;
-      if (ntiles > 0) load_codes<kWide>(cur, a.cache + li.tile[0] * kTileBytes, key, half);
+      Codes k, v;
+      if (ntiles > 0) {
+        const uint8_t* tile = a.cache + li.tile[0] * kTileBytes;
+        load_k<kWide>(k, tile, key, half);
+        load_v<kWide>(v, tile, key, half);
+      }
       for (int j = 0; j < ntiles; ++j, ++n) {
         const uint32_t bf = n & 1, ph = (n >> 1) & 1;
-        if (j + 1 < ntiles) load_codes<kWide>(nxt, a.cache + li.tile[j + 1] * kTileBytes, key, half);
+        const uint8_t* next = a.cache + li.tile[min(j + 1, ntiles - 1)] * kTileBytes;
         if (n >= 2 && !(ok = warp_wait(&ct.s_full[bf], ph ^ 1, a.status))) break;  // S_{n-2} has read its K
-        decode_row(sm + OFF_K + bf * 16384 + half * 8192 + key * 128, cur.k, cur.ks, key);
+        decode_row(sm + OFF_K + bf * 16384 + half * 8192 + key * 128, k.w, k.scales, key);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ct.k_full[bf]);
+        if (j + 1 < ntiles) load_k<kWide>(k, next, key, half);
         if (n >= 2 && !(ok = warp_wait(&ct.pv_done[bf], ph ^ 1, a.status))) break;  // P V_{n-2} has read its V
         // Keys behind the chunk hold anything: a zero scale makes them zero (a
         // code alone is always finite; a weight of zero times NaN would not be).
@@ -366,13 +380,13 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
         // before it: it counts as zero here, and the softmax warps put it into the
         // rows that attend it.
         const int pos = li.key0[j] + key;
-        uint32_t vs = cur.vs;
+        uint32_t vs = v.scales;
         if (pos > li.row.w) vs = pos <= last ? vs & ~nan_bytes(vs) : 0u;
-        decode_row(sm + OFF_V + bf * 16384 + half * 8192 + key * 128, cur.v, vs, key);
+        decode_row(sm + OFF_V + bf * 16384 + half * 8192 + key * 128, v.w, vs, key);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ct.v_full[bf]);
-        cur = nxt;
+        if (j + 1 < ntiles) load_v<kWide>(v, next, key, half);
       }
       if (!ok) break;
       if (lane == 0) mbar_arrive(&ct.list_free[i & 1]);
@@ -382,6 +396,8 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
     if (warp == kScoreWarp) {
       // ---------------- S = Q K^T: one thread ----------------
       if (elect_one()) {
+        // a descriptor's low bits are the address / 16: offsets add to it
+        const uint64_t qdesc = sdesc_sw128(sbase + OFF_Q, 16, 1024), kdesc0 = sdesc_sw128(sbase + OFF_K, 16, 1024);
         uint32_t n = 0, nq = 0;  // nq: items with tiles
         bool ok = true;
         for (uint32_t i = 0; ok; ++i) {
@@ -396,12 +412,11 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
             if (ok && n >= 2) ok = mbar_wait(&ct.pv_done[n & 1], ((n >> 1) & 1) ^ 1, a.status);
             if (!ok) break;
             tc_fence_after();
+            const uint64_t kdesc = kdesc0 + (n & 1) * (16384 >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const uint32_t half = kk >> 2, sub = (kk & 3) * 32;
-              umma_bf16(tmem + COL_S + (n & 1) * 64, sdesc_sw128(sbase + OFF_Q + half * 16384 + sub, 16, 1024),
-                        sdesc_sw128(sbase + OFF_K + (n & 1) * 16384 + half * 8192 + sub, 16, 1024), ID_S, kk > 0);
-            }
+            for (int kk = 0; kk < 8; ++kk)
+              umma_bf16(tmem + COL_S + (n & 1) * 64, qdesc + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                        kdesc + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), ID_S, kk > 0);
             umma_commit(&ct.s_full[n & 1]);
           }
         }
@@ -409,6 +424,7 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
     } else if (warp == kOutWarp) {
       // ---------------- O += P V: one thread ----------------
       if (elect_one()) {
+        const uint64_t vdesc = sdesc_sw128(sbase + OFF_V, 8192, 1024);
         uint32_t n = 0;
         bool ok = true;
         for (uint32_t i = 0; ok; ++i) {
@@ -418,13 +434,13 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
           mbar_arrive(&ct.list_free[i & 1]);
           for (int j = 0; j < ntiles; ++j, ++n) {
             const uint32_t bf = n & 1;
-            ok = mbar_wait(&ct.v_full[bf], (n >> 1) & 1, a.status) && mbar_wait(&ct.p_full[bf], (n >> 1) & 1, a.status);
+            ok = mbar_wait(&ct.p_full[bf], (n >> 1) & 1, a.status) && mbar_wait(&ct.v_full[bf], (n >> 1) & 1, a.status);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               umma_bf16_ts(tmem + COL_O, tmem + COL_S + bf * 64 + kk * 8,
-                           sdesc_sw128(sbase + OFF_V + bf * 16384 + kk * 2048, 8192, 1024), ID_O,
+                           vdesc + ((bf * 16384 + kk * 2048) >> 4), ID_O,
                            (j > 0 || kk > 0) ? 1u : 0u);
             umma_commit(&ct.pv_done[bf]);
           }

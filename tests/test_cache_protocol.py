@@ -260,8 +260,8 @@ def _chunk(items, seed, warps=2, q_phase_per_item=False, early_scores=False, bia
             lists[i & 1].read(i)
             list_free[i & 1].arrive()
             for j in range(nt):
-                yield from _wait(v_full[n & 1], n >> 1)
                 yield from _wait(p_full[n & 1], n >> 1)
+                yield from _wait(v_full[n & 1], n >> 1)
                 mma["PV"].append((n, i, j == 0))
                 n += 1
                 yield 1
@@ -304,8 +304,10 @@ def _chunk(items, seed, warps=2, q_phase_per_item=False, early_scores=False, bia
                 SP[n & 1][w].read(("S", n))
                 yield 1
                 SP[n & 1][w].write(("P", n), 1)
-                if j > 0:
+                if j > 0 and rng.random() < 0.3:        # this warp rescales its rows of O
                     yield from _wait(pv_done[(n - 1) & 1], (n - 1) >> 1)
+                    assert O["tag"] == (i, n - 1)
+                    yield 1
                     assert O["tag"] == (i, n - 1)
                 p_full[n & 1].arrive()
                 yield 1
