@@ -9,8 +9,9 @@
 // A tile is decoded once for the 128 rows, against once per token in the
 // single-token kernel.  Per 64-key tile 32 KB are stored to shared memory by the
 // decoders and 64 KB read by the MMAs (Q again for every tile): 768 cycles at 128
-// bytes a cycle, against about 700 of MMA issue and 1300 measured: instruction
-// issue, shared memory and the chain S, softmax, P V are all half used.
+// bytes a cycle, against about 700 of MMA issue and 1230 measured: instruction
+// issue, shared memory and the chain S, softmax, P V are all half used, and
+// instruction fetches are the most frequent of the stalls that are not waits.
 // The codes go from global memory to the decoders' registers and never through
 // shared memory, which keeps 18 KB per tile off that path.  A row's next codes are
 // loaded as soon as its registers are free, K after K, V after V: loads before the
@@ -29,8 +30,8 @@
 // and V buffers allow.  (A next item's Q or codes loaded before this one's end:
 // 239 and 232 us, slower although the waits are shorter.)
 //
-// Times: 3.4k new tokens x 4 heads x 2048 keys, 207 us (924 TFLOP/s); 4k x 8 heads
-// the same 517 us (1047 TFLOP/s).
+// Times: 3.4k new tokens x 4 heads x 2048 keys, 198 us (966 TFLOP/s); 4k x 8 heads
+// the same 497 us (1090 TFLOP/s).
 #pragma once
 
 namespace msa {
@@ -58,6 +59,7 @@ struct Control {
   uint64_t pv_done[2];              // P_n V_n done (MMA commit), by n & 1: V and S buffer n & 1 are free too
   uint64_t list_full[2], list_free[2];
   uint32_t tmem;
+  int32_t gave_up;                  // a wait ran out
   struct List {
     int4 row;                       // the chunk-table row
     int32_t head, ntiles;           // ntiles: -1 ends the walk
@@ -84,8 +86,21 @@ MSA_DEV void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"
 template <int N>
 MSA_DEV void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-MSA_DEV bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
+// mbar_wait in few instructions: six roles' loops share the instruction cache (208
+// us with mbar_wait, 199 with this).  A wait that gives up leaves a mark, which
+// becomes the status at the end.
+MSA_DEV bool short_wait(uint64_t* bar, uint32_t parity, int32_t* gave_up) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+#pragma unroll 1
+  do {
+    if (mbar_try_wait(bar, parity)) return true;
+  } while (global_ns() - t0 <= kWaitLimitNs);
+  *gave_up = 1;
+  return false;
+}
+MSA_DEV bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* gave_up) {
+  return __all_sync(0xffffffffu, short_wait(bar, parity, gave_up));
 }
 
 // One decoder thread's share of a tile: 64 dims (half a row) of one key, of K
@@ -142,6 +157,7 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
   Control& ct = *reinterpret_cast<Control*>(sm + OFF_CTL);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
+    ct.gave_up = 0;
     mbar_init(&ct.q_full, 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ct.k_full[i], 4);
@@ -176,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
     uint32_t seq = 0;
     for (uint32_t i = 0;; ++i) {
-      if (!warp_wait(&ct.list_full[i & 1], (i >> 1) & 1, a.status)) break;
+      if (!warp_wait(&ct.list_full[i & 1], (i >> 1) & 1, &ct.gave_up)) break;
       const Control::List& li = ct.list[i & 1];
       const int4 c = li.row;
       const int h = li.head, ntiles = li.ntiles;
@@ -221,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
       for (int j = 0; j < ntiles; ++j) {
         const uint32_t n = seq + j, bf = n & 1;
         const int key0 = li.key0[j];
-        if (!(ok = warp_wait(&ct.s_full[bf], (n >> 1) & 1, a.status))) break;
+        if (!(ok = warp_wait(&ct.s_full[bf], (n >> 1) & 1, &ct.gave_up))) break;
         tc_fence_after();
         const uint32_t col = tmem + lane_base + COL_S + bf * 64;
         // Two halves of 32 columns, read once for the maximum and once for the weights:
@@ -284,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
         if (__any_sync(0xffffffffu, resc)) {  // warp-collective TMEM access
           // P V of the tile before.  (Its phase cannot be taken for the one before it:
           // S_{n-1} was issued after P_{n-3} V_{n-3}.)
-          if (!(ok = warp_wait(&ct.pv_done[bf ^ 1], ((n - 1) >> 1) & 1, a.status))) break;
+          if (!(ok = warp_wait(&ct.pv_done[bf ^ 1], ((n - 1) >> 1) & 1, &ct.gave_up))) break;
           tc_fence_after();
 #pragma unroll 1
           for (int c0 = 0; c0 < 128; c0 += 32) {
@@ -302,7 +318,8 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
         if (lane == 0) mbar_arrive(&ct.p_full[bf]);
       }
       if (!ok) break;
-      if (ntiles > 0 && !warp_wait(&ct.pv_done[(seq + ntiles - 1) & 1], ((seq + ntiles - 1) >> 1) & 1, a.status)) break;
+      const uint32_t nl = seq + ntiles - 1;  // the item's last tile
+      if (ntiles > 0 && !warp_wait(&ct.pv_done[nl & 1], (nl >> 1) & 1, &ct.gave_up)) break;
       tc_fence_after();
       if (qpos >= 0) a.lse[row] = l_run == 0.f ? -CUDART_INF_F : (m_run + log2f(l_run)) * kLn2;
       const float inv = l_run == 0.f ? 0.f : a.v_mul / l_run;  // a NaN stays one
@@ -316,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
         for (int g = 0; g < 8; ++g)
           if ((uint32_t)(nan >> (8 * g)) & mine & 0xFFu) nan_groups |= 1u << g;
       }
-#pragma unroll
+#pragma unroll 1
       for (int c0 = 0; c0 < 128; c0 += 32) {
         uint32_t v[32];
         if (ntiles > 0) {
@@ -329,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
         if (nan_groups) {
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (nan_groups >> ((c0 + e) / 16) & 1) v[e] = 0x7FC00000u;
+            if (nan_groups >> (c0 / 16 + e / 16) & 1) v[e] = 0x7FC00000u;
         }
         if (qpos >= 0) {
 #pragma unroll
@@ -353,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
     const int t = tid - 32 * kDecodeWarp, key = t & 63, half = t >> 6;
     uint32_t n = 0;
     for (uint32_t i = 0;; ++i) {
-      if (!warp_wait(&ct.list_full[i & 1], (i >> 1) & 1, a.status)) break;
+      if (!warp_wait(&ct.list_full[i & 1], (i >> 1) & 1, &ct.gave_up)) break;
       const Control::List& li = ct.list[i & 1];
       const int ntiles = li.ntiles, last = li.row.w + li.row.z - 1;  // the chunk's last position
       if (ntiles < 0) break;
@@ -367,13 +384,13 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
       for (int j = 0; j < ntiles; ++j, ++n) {
         const uint32_t bf = n & 1, ph = (n >> 1) & 1;
         const uint8_t* next = a.cache + li.tile[min(j + 1, ntiles - 1)] * kTileBytes;
-        if (n >= 2 && !(ok = warp_wait(&ct.s_full[bf], ph ^ 1, a.status))) break;  // S_{n-2} has read its K
+        if (n >= 2 && !(ok = warp_wait(&ct.s_full[bf], ph ^ 1, &ct.gave_up))) break;  // S_{n-2} has read its K
         decode_row(sm + OFF_K + bf * 16384 + half * 8192 + key * 128, k.w, k.scales, key);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ct.k_full[bf]);
         if (j + 1 < ntiles) load_k<kWide>(k, next, key, half);
-        if (n >= 2 && !(ok = warp_wait(&ct.pv_done[bf], ph ^ 1, a.status))) break;  // P V_{n-2} has read its V
+        if (n >= 2 && !(ok = warp_wait(&ct.pv_done[bf], ph ^ 1, &ct.gave_up))) break;  // P V_{n-2} has read its V
         // Keys behind the chunk hold anything: a zero scale makes them zero (a
         // code alone is always finite; a weight of zero times NaN would not be).
         // A NaN value of one of the chunk's own tokens must not reach the tokens
@@ -401,15 +418,15 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
         uint32_t n = 0, nq = 0;  // nq: items with tiles
         bool ok = true;
         for (uint32_t i = 0; ok; ++i) {
-          if (!mbar_wait(&ct.list_full[i & 1], (i >> 1) & 1, a.status)) break;
+          if (!short_wait(&ct.list_full[i & 1], (i >> 1) & 1, &ct.gave_up)) break;
           const int ntiles = ct.list[i & 1].ntiles;
           if (ntiles < 0) break;
           mbar_arrive(&ct.list_free[i & 1]);  // the list is not looked at again
-          if (ntiles > 0 && !mbar_wait(&ct.q_full, nq++ & 1, a.status)) break;
+          if (ntiles > 0 && !short_wait(&ct.q_full, nq++ & 1, &ct.gave_up)) break;
           for (int j = 0; j < ntiles; ++j, ++n) {
-            ok = mbar_wait(&ct.k_full[n & 1], (n >> 1) & 1, a.status);
+            ok = short_wait(&ct.k_full[n & 1], (n >> 1) & 1, &ct.gave_up);
             // the S columns: P_{n-2} has been read from them
-            if (ok && n >= 2) ok = mbar_wait(&ct.pv_done[n & 1], ((n >> 1) & 1) ^ 1, a.status);
+            if (ok && n >= 2) ok = short_wait(&ct.pv_done[n & 1], ((n >> 1) & 1) ^ 1, &ct.gave_up);
             if (!ok) break;
             tc_fence_after();
             const uint64_t kdesc = kdesc0 + (n & 1) * (16384 >> 4);
@@ -428,13 +445,14 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
         uint32_t n = 0;
         bool ok = true;
         for (uint32_t i = 0; ok; ++i) {
-          if (!mbar_wait(&ct.list_full[i & 1], (i >> 1) & 1, a.status)) break;
+          if (!short_wait(&ct.list_full[i & 1], (i >> 1) & 1, &ct.gave_up)) break;
           const int ntiles = ct.list[i & 1].ntiles;
           if (ntiles < 0) break;
           mbar_arrive(&ct.list_free[i & 1]);
           for (int j = 0; j < ntiles; ++j, ++n) {
             const uint32_t bf = n & 1;
-            ok = mbar_wait(&ct.p_full[bf], (n >> 1) & 1, a.status) && mbar_wait(&ct.v_full[bf], (n >> 1) & 1, a.status);
+            ok = short_wait(&ct.p_full[bf], (n >> 1) & 1, &ct.gave_up) &&
+                 short_wait(&ct.v_full[bf], (n >> 1) & 1, &ct.gave_up);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -500,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
             }
           }
         }
-        if (i >= 2 && !warp_wait(&ct.list_free[i & 1], ((i >> 1) & 1) ^ 1, a.status)) break;
+        if (i >= 2 && !warp_wait(&ct.list_free[i & 1], ((i >> 1) & 1) ^ 1, &ct.gave_up)) break;
         Control::List& li = ct.list[i & 1];
         for (int k = 0; k < ntl; ++k) {
           li.tile[x - ntl + k] = tile_index(page, h, a.H, a.B / kTile, k);
@@ -525,6 +543,7 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (tid == 0 && ct.gave_up) set_status(a.status, MSA_ERR_TIMEOUT);
   if (warp == 0) tmem_dealloc(tmem, TMEM_COLS);
 }
 
