@@ -541,13 +541,30 @@ extern "C" int msa_cache_fwd(const msa_cache_problem* p, const uint16_t* q, cons
   a.v_mul = cache::exp2i(p->v_exp);
   a.slots = 1;
   a.status = d_status;
-  // Chunks of two tokens and more on average, in batches of a few tokens per SM:
-  // the 128-row kernel.  It takes the same time for one token of a chunk as for
-  // eight (16 tiles 23 us, 32 tiles 38 us, for up to two items per SM), the
-  // single-token kernel about 0.08 us per token, head and 32 tiles on top of 9:
-  // 8 tokens x 16 requests x 8 heads x 32 tiles 50 against 108 us, 3 tokens x 8
-  // requests 38 against 28.
-  if (p->token_cap / p->chunk_cap >= 2 && (int64_t)p->token_cap * p->num_kv_heads * 2 >= 5 * sms) {
+  // Token slots of a chunk in the grid: one where tokens and chunk rows are
+  // equal in number (decode), else twice the mean, at most 8.  A chunk with more
+  // tokens than slots takes them in turn; a slot without a token costs the
+  // launch of a CTA that leaves at once.
+  a.slots = (int)((p->token_cap + (int64_t)p->chunk_cap - 1) / p->chunk_cap);
+  if (a.slots > 1) a.slots *= 2;
+  if (a.slots > kChunk) a.slots = kChunk;
+  const int64_t items = (int64_t)p->chunk_cap * a.slots;
+  // CTAs of a cluster share an item's tiles while that leaves at most two CTAs to
+  // an SM.  Beyond that it loses: an item's start and join cost about 6 us
+  // whatever its tiles (2048 items in clusters of 2: 291 us against 162).
+  const int tiles = p->topk * (p->block_size / cache::kTile);
+  int ranks = 1;
+  while (ranks < 8 && ranks * 2 <= tiles && items * p->num_kv_heads * ranks * 2 <= 2 * sms) ranks *= 2;
+  if (ranks > 1)
+    return cache::launch_kernel(cache::fwd_cache_kernel, dim3((unsigned)(items * ranks), (unsigned)p->num_kv_heads),
+                                cache::kFwdThreads, sizeof(cache::FwdShared), stream, (unsigned)ranks, a);
+  // Chunk rows with 1.25 tokens and more on average (3 new tokens a request and
+  // more): the 128-row kernel, which takes the same time for one token of a chunk
+  // as for eight, where the single-token kernel takes them one after another (32
+  // tiles, 8 heads: 3 tokens x 8 requests 30 against 47 us, 8 tokens x 16 requests 41
+  // against 149; 2 tokens x 64 requests 85 against 87).  In clusters the single-token
+  // kernel is faster (32 tokens x 2 heads x 32 tiles 16 against 30).
+  if (4 * (int64_t)p->token_cap >= 5 * (int64_t)p->chunk_cap) {
     const bool wide = cache::aligned32(q, o) && cache::aligned32(kv_cache, nullptr);
     const auto kernel = wide ? cache::chunk::fwd_chunk_kernel<true> : cache::chunk::fwd_chunk_kernel<false>;
     cudaFuncAttributes attr;
@@ -563,33 +580,13 @@ extern "C" int msa_cache_fwd(const msa_cache_problem* p, const uint16_t* q, cons
     const int grid = (int)(chunks < 2 * sms ? chunks : 2 * sms);
     return cache::launch_kernel(kernel, dim3((unsigned)grid), cache::chunk::kThreads, cache::chunk::SMEM, stream, 1, a);
   }
-  // Token slots of a chunk in the grid: one where tokens and chunk rows are
-  // equal in number (decode), else twice the mean, at most 8.  A chunk with more
-  // tokens than slots takes them in turn; a slot without a token costs the
-  // launch of a CTA that leaves at once.
-  a.slots = (int)((p->token_cap + (int64_t)p->chunk_cap - 1) / p->chunk_cap);
-  if (a.slots > 1) a.slots *= 2;
-  if (a.slots > kChunk) a.slots = kChunk;
-  const int64_t items = (int64_t)p->chunk_cap * a.slots;
-  // CTAs of a cluster share an item's tiles while that leaves at most two CTAs to
-  // an SM.  Beyond that it loses: an item's start and join cost about 6 us
-  // whatever its tiles (2048 items in clusters of 2: 291 us against 162).
-  const int tiles = p->topk * (p->block_size / cache::kTile);
-  int ranks = 1;
-  while (ranks < 8 && ranks * 2 <= tiles && items * p->num_kv_heads * ranks * 2 <= 2 * sms) ranks *= 2;
-  if (items * ranks > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
-  if (ranks == 1) {
-    // enough items to keep every SM busy: persistent CTAs
-    if (cudaFuncSetAttribute(cache::batch::fwd_batch_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                             (int)cudaSharedmemCarveoutMaxShared) != cudaSuccess)
-      return MSA_ERR_CUDA;
-    const int64_t all = (int64_t)p->chunk_cap * p->num_kv_heads;
-    const int64_t slots = (int64_t)cache::batch::kCtasPerSm * sms;
-    const int grid = (int)(all < slots ? all : slots);
-    return cache::launch_kernel(cache::batch::fwd_batch_kernel, dim3((unsigned)grid), cache::batch::kThreads,
-                                sizeof(cache::batch::Shared), stream, 1, a);
-  }
-  return cache::launch_kernel(cache::fwd_cache_kernel,
-                              dim3((unsigned)(items * ranks), (unsigned)p->num_kv_heads), cache::kFwdThreads,
-                              sizeof(cache::FwdShared), stream, (unsigned)ranks, a);
+  // enough items to keep every SM busy: persistent CTAs
+  if (cudaFuncSetAttribute(cache::batch::fwd_batch_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                           (int)cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+    return MSA_ERR_CUDA;
+  const int64_t all = (int64_t)p->chunk_cap * p->num_kv_heads;
+  const int64_t slots = (int64_t)cache::batch::kCtasPerSm * sms;
+  const int grid = (int)(all < slots ? all : slots);
+  return cache::launch_kernel(cache::batch::fwd_batch_kernel, dim3((unsigned)grid), cache::batch::kThreads,
+                              sizeof(cache::batch::Shared), stream, 1, a);
 }
