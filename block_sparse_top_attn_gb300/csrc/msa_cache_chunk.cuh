@@ -468,8 +468,8 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
       // ---------------- tile lists ----------------
       const bool stale = status_bad(a.status);
       uint32_t i = 0;
-      int4 c_next;
-      int entry_next;
+      int4 c_next = make_int4(-1, 0, 0, 0);
+      int entry_next = -1;
       auto fetch = [&](int64_t w) {  // chunk row and selection, one item ahead
         c_next = make_int4(-1, 0, 0, 0);
         entry_next = -1;

@@ -502,6 +502,42 @@ def test_attention_of_non_finite_values(B):
     assert np.isfinite(np.delete(x[0], 3, 0)).all() and np.isfinite(np.delete(x[1], 4, 0)).all()
 
 
+@pytest.mark.parametrize("H, past, new", [(1, [100, 61], [4, 30]), (8, [100, 61], [4, 30]),
+                                          (16, [0, 56, 130], [60, 8, 3])])
+@pytest.mark.parametrize("block", [64, 128])
+def test_attention_of_nan_values_inside_chunks(B, H, past, new, block):
+    """Values that are NaN at positions of the new tokens themselves and before them, every block selected: the rows at
+    and behind such a position have NaN in the dims of its group, all else is as without it."""
+    import torch
+    s = Setup(B, past=past, new=new, H=H, block=block, topk=4, garbage=0xFF)
+    clean = s.v_bits.copy()
+    marks = [(r, past[r] + t, 16 * g) for r, t, g in ((0, 2, 1), (0, 3, 7), (1, 0, 0), (1, 5, 3), (1, 7, 7))]
+    marks.append((1, 9, 5))                                     # a past token
+    for r, pos, d in marks:
+        s.v_bits[s.first[r] + pos, :, d + 3] = 0xFF80
+    s.fill()
+    sel, q = s.selection(), s.queries()
+    for g, (r, row, n, first) in enumerate(s.want["chunks"]):
+        sel[:, g] = -1
+        sel[:, g, :first // block + 1] = np.arange(first // block + 1)
+    o, lse = s.forward(q, sel)
+    assert s.code() == 0
+    s.v_bits = clean
+    want = C.attend(q, *s.values(), s.want["chunks"], sel, block, s.scale)
+    got = from_bf16_tensor(o)
+    bad = np.zeros(got.shape, bool)
+    for g, (r, row, n, first) in enumerate(s.want["chunks"]):
+        for t in range(n):
+            for rr, pos, d in marks:
+                if rr == r and pos <= first + t:
+                    d -= d % 16                             # of the group that holds the mark
+                    bad[row + t, :, d:d + 16] = True
+    x = o.float().cpu().numpy()
+    assert np.array_equal(np.isnan(x), bad)
+    got[bad] = O.f64_to_bf16(want[0])[bad]
+    _close(to_bf16_tensor(got, "cuda"), lse, want)
+
+
 def test_attention_far_into_a_large_cache(B):
     """Pages beyond 2^32 bytes of cache."""
     kw = dict(past=[500, 130], new=[1, 3], H=4, topk=5, page_base=150000)
