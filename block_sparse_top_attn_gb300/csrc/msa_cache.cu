@@ -873,7 +873,8 @@ int msa_cache_append(const msa_cache_problem* p, const uint16_t* k, const uint16
   if (kv_blocks + idx_blocks > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
   cache::AppendArgs a{k, v, k_index, slot_map, cu_tokens, chunks, kv_cache, index_tail, index_pool, (int)T, (int)H,
                       p->block_size, p->num_requests, (int)NC, (int64_t)p->num_pages * p->block_size,
-                      cache::exp2i(-p->k_exp), cache::exp2i(-p->v_exp), cache::aligned32(k, v), (int)idx_blocks, d_status};
+                      cache::exp2i(-p->k_exp), cache::exp2i(-p->v_exp), cache::aligned32(k, v), (int)idx_blocks,
+                      d_status};
   return cache::launch_kernel(cache::append_kernel, dim3((unsigned)(kv_blocks + idx_blocks)), 256, 0, stream, 1, a);
 }
 

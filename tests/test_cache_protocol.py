@@ -325,7 +325,8 @@ def _chunk(items, seed, warps=2, q_phase_per_item=False, early_scores=False, bia
             seq += nt
 
     done = {}
-    threads = {"list": list_warp(), "s_issuer": score_issuer(), "o_issuer": out_issuer(), **{f"d{w}": decoder(w) for w in range(warps)},
+    threads = {"list": list_warp(), "s_issuer": score_issuer(), "o_issuer": out_issuer(),
+               **{f"d{w}": decoder(w) for w in range(warps)},
                **{f"s{w}": softmax(w) for w in range(warps)}}
     _run(threads, rng, [run_mma], bias)
     assert stored == [i for i, nt in enumerate(items) if nt > 0] and not mma["S"] and not mma["PV"]

@@ -479,6 +479,18 @@ def test_attention_over_magnitudes(B, kw):
     _attend_case(B, past=[300, 70], new=[1, 12], H=1, topk=6, **kw)
 
 
+@pytest.mark.parametrize("kw", [dict(k_exp=-8, k_scale=2.0 ** -8), dict(v_exp=20, v_scale=2.0 ** 20),
+                                dict(k_exp=32, k_scale=2.0 ** 30, scale=2.0 ** -34),
+                                dict(q_scale=2.0 ** 40, scale=2.0 ** -44), dict(q_scale=2.0 ** -100),
+                                dict(q_scale=30.0), dict(q_scale=0.0, scale=2.0 ** -60)])
+def test_chunk_attention_over_magnitudes(B, kw):
+    """The same for chunks of several tokens with many heads (the 128-row kernel), and twice with the same bits."""
+    import torch
+    s, q, sel = _attend_case(B, past=[300, 70, 0], new=[12, 9, 3], H=8, topk=6, garbage=0xFF, **kw)
+    a, b = s.forward(q, sel), s.forward(q, sel)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_attention_of_non_finite_values(B):
     """A NaN among the values of an attended key reaches the dims of its group, in the rows that attend it; a NaN key
     makes its rows NaN; rows that may not attend them stay exact."""
