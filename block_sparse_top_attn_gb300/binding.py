@@ -554,12 +554,14 @@ class Cache:
         o, lse = cache.forward(q, sel)
 
     new_lens[r] is 0 for an idle request and -1 for one that gives its pages
-    back.  The lengths stay on the device, nothing synchronises and nothing is
-    allocated after construction, so a step whose shapes do not change can be
-    captured into a CUDA graph.  A step's tables (slot_map, positions, chunks,
-    cu_tokens) and outputs are views of buffers made for max_tokens rows: they
-    hold until the next step's calls.  Calls on one object run in the order of
-    their streams: keep them on one stream, or order the streams.
+    back.  The lengths stay on the device, nothing synchronises and a step
+    allocates nothing (read does: its outputs are new tensors), so a step whose
+    shapes do not change can be captured into a CUDA graph.  A step's tables
+    (slot_map, positions, chunks, cu_tokens) and outputs are views of buffers
+    made for max_tokens rows: they hold until the next step's calls.  Calls on
+    one object run in the order of their streams: keep them on one stream, or
+    order the streams.  The constructor, check_status and reset_status work on
+    the current stream.
     check_status() synchronises and raises on a device error; until reset_status()
     later calls do nothing.
     """
@@ -674,12 +676,14 @@ class Cache:
         return t["o"], t["lse"]
 
     def read(self, slots, stream=None):
-        """msa_cache_read: bf16 (k, v) [n, Hkv, 128] of any slots; rows of slot -1 are 0."""
+        """msa_cache_read: bf16 (k, v) [n, Hkv, 128] of any slots; rows of slot -1 are 0.  The outputs are new tensors
+        of the call's stream: their zeros come before the kernel there."""
         import torch
         self._need("slots", slots, (slots.numel(),), torch.int64)
         c = make_cache_problem(token_cap=max(1, slots.numel()), chunk_cap=1, **self._args)
-        k = torch.zeros((slots.numel(), c.num_kv_heads, HEAD_DIM), dtype=torch.bfloat16, device=self.device)
-        v = torch.zeros_like(k)
+        with torch.cuda.stream(stream):     # None: the current one
+            k = torch.zeros((slots.numel(), c.num_kv_heads, HEAD_DIM), dtype=torch.bfloat16, device=self.device)
+            v = torch.zeros_like(k)
         if slots.numel():
             self._call(msa_cache_read, c, slots, self.cache, k, v, stream=stream)
         return k, v

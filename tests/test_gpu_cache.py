@@ -964,3 +964,47 @@ def test_captured_step_with_a_join(B):
         s, wsel, want = f.step([1] * T, *(x[n] for n in ("k", "v", "ki", "qi", "q")))
         assert np.array_equal(keep_sel.cpu().numpy()[:, :wsel.shape[1]], wsel)
         _close(keep_o, keep_lse, want)
+
+
+def _keep_busy():
+    """Work of some 20 ms on the current stream: what is queued there next comes later than another stream's work."""
+    import torch
+    x = torch.zeros(1 << 28, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(60):
+        x.add_(1.0)
+    return x
+
+
+def test_read_on_a_side_stream(B):
+    """read(stream=s) while the current stream is busy: the rows' first values and the kernel's are both s's work, so the
+    result is there once s is done, rows of slot -1 are zero, and memory that the current stream still reads is not
+    handed to it."""
+    import torch
+    rng = np.random.default_rng(90)
+    kv = B.Cache(num_requests=1, num_pages=4, max_blocks=4, num_q_heads=32, topk=2, max_tokens=130, index_keys=False)
+    bits = [_bf16(rng, (130, 2, 128)) for _ in range(2)]
+    kv.step(_dev([130]), 130)
+    kv.append(*(to_bf16_tensor(x, "cuda") for x in bits))
+    slots = kv.slot_map.clone()
+    slots[5] = -1
+    want = [C.round_rows(x, 0)[2] for x in bits]
+    for x in want:
+        x[5] = 0.0
+    side = torch.cuda.Stream()
+    kv.read(slots, stream=side)             # the kernel is loaded: its first launch may wait for the whole device
+    old = [torch.full((130, 2, 128), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    busy = _keep_busy()
+    seen = [x.clone() for x in old]         # queued behind the work; the memory goes back to the allocator at once
+    del old
+    got = kv.read(slots, stream=side)
+    side.synchronize()
+    first = [x.clone() for x in got]
+    torch.cuda.synchronize()
+    kv.check_status()
+    del busy
+    assert all(bool((x == 3.0).all()) for x in seen)
+    for late, early, w in zip(got, first, want):
+        assert np.array_equal(O.bf16_to_f64(from_bf16_tensor(late)), w)
+        assert torch.equal(late, early)
