@@ -349,10 +349,11 @@ def plan_forward(p: Problem, sel, stream=None):
     work_count [1], status tensor)."""
     import torch
     dev = p.d_cu.device
-    meta = torch.empty((p.num_index_heads * p.num_chunks, MSA_TASK_META_COLS), dtype=torch.int32, device=dev)
-    wc = torch.zeros(4, dtype=torch.int32, device=dev)
-    st = torch.zeros(4, dtype=torch.int32, device=dev)
-    ws = torch.empty(msa_workspace_bytes(p, 1, 1, 0), dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(stream):     # None: the current one
+        meta = torch.empty((p.num_index_heads * p.num_chunks, MSA_TASK_META_COLS), dtype=torch.int32, device=dev)
+        wc = torch.zeros(4, dtype=torch.int32, device=dev)
+        st = torch.zeros(4, dtype=torch.int32, device=dev)
+        ws = torch.empty(msa_workspace_bytes(p, 1, 1, 0), dtype=torch.uint8, device=dev)
     msa_plan_forward(p, sel, meta, wc, st, ws, stream)
     return meta, wc, st
 
@@ -361,9 +362,10 @@ def select_topk(p: Problem, q_index, k_index, stream=None):
     """msa_select_topk convenience: returns (sel int32 [Hi, NC, topk], status tensor)."""
     import torch
     dev = p.d_cu.device
-    sel = torch.empty((p.num_index_heads, p.num_chunks, p.topk), dtype=torch.int32, device=dev)
-    st = torch.zeros(4, dtype=torch.int32, device=dev)
-    ws = torch.empty(msa_workspace_bytes(p, 1, 1, 0), dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(stream):     # None: the current one
+        sel = torch.empty((p.num_index_heads, p.num_chunks, p.topk), dtype=torch.int32, device=dev)
+        st = torch.zeros(4, dtype=torch.int32, device=dev)
+        ws = torch.empty(msa_workspace_bytes(p, 1, 1, 0), dtype=torch.uint8, device=dev)
     msa_select_topk(p, q_index, k_index, sel, st, ws, stream)
     return sel, st
 
@@ -446,10 +448,11 @@ def forward(p: Problem, sel, q, k, v, stream=None, plan=None):
     [T, Hq], status tensor)."""
     import torch
     dev = p.d_cu.device
-    o = torch.empty((p.total_tokens, p.num_q_heads, HEAD_DIM), dtype=torch.bfloat16, device=dev)
-    lse = torch.empty((p.total_tokens, p.num_q_heads), dtype=torch.float32, device=dev)
-    st = torch.zeros(4, dtype=torch.int32, device=dev)
-    ws = torch.empty(max(256, 8 * (p.num_docs + 1) + 256), dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(stream):     # None: the current one
+        o = torch.empty((p.total_tokens, p.num_q_heads, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+        lse = torch.empty((p.total_tokens, p.num_q_heads), dtype=torch.float32, device=dev)
+        st = torch.zeros(4, dtype=torch.int32, device=dev)
+        ws = torch.empty(max(256, 8 * (p.num_docs + 1) + 256), dtype=torch.uint8, device=dev)
     if plan is None:
         msa_fwd(p, q, k, v, sel, o, lse, st, ws, stream)
     else:
