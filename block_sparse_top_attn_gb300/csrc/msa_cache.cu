@@ -677,10 +677,13 @@ __global__ void __launch_bounds__(32 * W, 1) select_kernel(SelectArgs a) {
   const int g0 = (int)(blockIdx.x / a.H) * G, h = (int)(blockIdx.x % a.H);
   const int64_t hs = (int64_t)a.H * 128;
   after_previous_kernel();
-  if (status_bad(a.status)) return;
   // lane r of every warp holds chunk row g0 + r
   int4 mine = make_int4(-1, 0, 0, 0);
   if (lane < G && g0 + lane < a.NC) mine = reinterpret_cast<const int4*>(a.chunks)[g0 + lane];
+  // One decision for the CTA: another CTA may set the status between two warps'
+  // reads, and a warp that left would leave shared memory behind that the others
+  // take rows' lengths and list positions from.
+  if (__syncthreads_or(status_bad(a.status))) return;
   for (int lo = 0, hi; lo < G; lo = hi) {
     // a run of chunks of one request
     hi = lo + 1;

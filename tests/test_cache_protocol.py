@@ -349,3 +349,48 @@ def test_chunk_model_rejects_scores_over_weights_in_use():
     with pytest.raises(AssertionError, match="SP|parity alias|holds"):
         for seed in range(200):
             _chunk([9], seed, early_scores=True, bias=["d0", "d1", "s_issuer"])
+
+
+# ---------------------------------------------------------------------------
+# the status word, which other CTAs of a launch may set while a CTA starts
+# ---------------------------------------------------------------------------
+
+def _start(seed, voted, warps=4):
+    """A CTA of select_kernel: every warp reads the status once, at a time of its own, and another CTA sets it at some
+    time.  voted: the CTA leaves as a whole if any warp saw it set.  Warp 0 writes the row's length and the list's
+    counters, every warp uses them behind a barrier (which a warp that has left does not hold up)."""
+    rng = random.Random(seed)
+    order = [f"w{w}" for w in range(warps)] + ["other CTA"]
+    rng.shuffle(order)
+    saw = {w: order.index(f"w{w}") > order.index("other CTA") for w in range(warps)}
+    if voted:
+        saw = dict.fromkeys(saw, any(saw.values()))
+    stay = [w for w in saw if not saw[w]]
+    written = 0 in stay
+    for w in stay:
+        assert written, f"warp {w} goes on with what warp 0 has not written"
+
+
+def test_a_voted_status_keeps_a_cta_together():
+    for seed in range(500):
+        _start(seed, voted=True)
+
+
+def test_status_model_rejects_a_decision_by_warp():
+    with pytest.raises(AssertionError, match="has not written"):
+        for seed in range(500):
+            _start(seed, voted=False)
+
+
+def _kernel_source(file, name):
+    import pathlib
+    import re
+    text = (pathlib.Path(__file__).parent.parent / "block_sparse_top_attn_gb300" / "csrc" / file).read_text()
+    body = re.search(rf"\b{name}\(\w+ a\) {{\n(.*?)\n}}\n", text, re.S).group(1)
+    return re.sub(r"//[^\n]*", "", body)
+
+
+def test_select_decides_on_the_status_by_a_vote():
+    """What the model above stands for: the kernel's one look at the status is a vote of the CTA."""
+    body = _kernel_source("msa_cache.cu", "select_kernel")
+    assert body.count("status_bad(") == 1 and body.count("__syncthreads_or(status_bad(a.status))") == 1

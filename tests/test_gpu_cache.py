@@ -1008,3 +1008,38 @@ def test_read_on_a_side_stream(B):
     for late, early, w in zip(got, first, want):
         assert np.array_equal(O.bf16_to_f64(from_bf16_tensor(late)), w)
         assert torch.equal(late, early)
+
+
+@pytest.mark.parametrize("past, new, H", [([3000] * 200, [1] * 200, 4), ([900, 64, 4000], [900, 300, 500], 4)])
+def test_selection_with_bad_rows_among_many(B, past, new, H):
+    """Bad chunk rows and pages in a launch of many CTAs, for single tokens and for prompts: the error is reported, bad
+    rows are left as they were, and a good row is either the oracle's or, where its CTA came up behind the error, left."""
+    s = Setup(B, past, new, H=H, topk=8, kv=False)
+    qi, pool = _bf16(s.rng, (s.c.token_cap, H, 128)), _bf16(s.rng, (s.c.num_pages, H, 128), 0.125)
+    want = C.select(qi, pool, s.full, s.want["chunks"], 64, 8)
+    import torch
+    d = dict(qi=to_bf16_tensor(qi, "cuda"), pool=to_bf16_tensor(pool, "cuda"), table=_dev(s.full))
+    for kind in ("row", "page"):
+        chunks, table = s.chunk_table(), d["table"].clone()
+        bad = np.zeros(s.c.chunk_cap, bool)
+        if kind == "row":
+            at = s.rng.permutation(len(s.want["chunks"]))[:12]
+            for i, g in enumerate(at):
+                col, value = [(0, len(past)), (1, -1), (1, s.T), (2, 0), (2, 9), (3, -1)][i % 6]
+                chunks[int(g), col] = value
+            bad[at] = True
+        else:
+            r = len(past) // 2
+            table[r, 0] = s.c.num_pages
+            bad[[g for g, c in enumerate(s.want["chunks"]) if c[0] == r]] = True
+        for _ in range(5):
+            s.status.zero_()
+            sel = torch.full((H, s.c.chunk_cap, 8), -5, dtype=torch.int32, device="cuda")
+            B.msa_cache_select(s.c, d["qi"], d["pool"], table, chunks, sel, s.status)
+            assert s.code() == B.MSA_ERR_INVALID_CACHE
+            got = sel.cpu().numpy()
+            left = (got == -5).all(2)
+            if kind == "row":
+                assert left[:, bad].all()
+            ok = ~left & ~bad[None]
+            assert np.array_equal(got[ok], want[ok])
