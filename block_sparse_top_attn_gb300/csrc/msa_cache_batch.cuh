@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) fwd_batch_kernel(FwdCach
   if (warp == 4) {
     // ---------------- service: items, copies ----------------
     const int64_t items = (int64_t)a.H * a.NC;
-    const bool stale = status_bad(a.status);  // an earlier error: no items
+    const bool stale = __any_sync(0xffffffffu, status_bad(a.status));  // an earlier error: no items
     bool ok = true;
     uint32_t i = 0, n = 0;
     for (int64_t w = blockIdx.x; !stale && ok && w < items; w += gridDim.x) {

@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
       }
     } else if (warp == kListWarp) {
       // ---------------- tile lists ----------------
-      const bool stale = status_bad(a.status);
+      const bool stale = __any_sync(0xffffffffu, status_bad(a.status));
       uint32_t i = 0;
       int4 c_next = make_int4(-1, 0, 0, 0);
       int entry_next = -1;

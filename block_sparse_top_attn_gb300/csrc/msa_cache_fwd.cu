@@ -310,9 +310,10 @@ __global__ void __launch_bounds__(kFwdThreads, 3) fwd_cache_kernel(FwdCacheArgs 
     fence_mbar_init();
   }
   if (warp == 0) {
-    // the chunk's tiles; rank takes every ranks-th
+    // the chunk's tiles; rank takes every ranks-th.  The lanes vote on the status:
+    // list_tiles needs all of them or none.
     int b, page, ntl;
-    const bool good = !stale && list_tiles(a, c, entry, lane, b, page, ntl);
+    const bool good = !__any_sync(0xffffffffu, stale) && list_tiles(a, c, entry, lane, b, page, ntl);
     if (!good) ntl = 0;
     int x = ntl;
 #pragma unroll

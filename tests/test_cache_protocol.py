@@ -394,3 +394,19 @@ def test_select_decides_on_the_status_by_a_vote():
     """What the model above stands for: the kernel's one look at the status is a vote of the CTA."""
     body = _kernel_source("msa_cache.cu", "select_kernel")
     assert body.count("status_bad(") == 1 and body.count("__syncthreads_or(status_bad(a.status))") == 1
+
+
+@pytest.mark.parametrize("file, name", [("msa_cache_fwd.cu", "fwd_cache_kernel"),
+                                        ("msa_cache_batch.cuh", "fwd_batch_kernel"),
+                                        ("msa_cache_chunk.cuh", "fwd_chunk_kernel")])
+def test_attention_decides_on_the_status_by_a_vote(file, name):
+    """In the attention kernels one warp looks at the status, and what it does next needs all of its lanes or none:
+    every look is a vote of the warp, in place or, where the read has to be early, of the value read."""
+    import re
+    body = _kernel_source(file, name)
+    looks = re.findall(r"[^;]*status_bad\(a\.status\)[^;]*;", body)
+    assert len(looks) == 1
+    if "__any_sync(0xffffffffu, status_bad(a.status))" not in looks[0]:
+        assert re.search(r"\bstale = status_bad\(a\.status\)", looks[0])
+        uses = re.findall(r"[^;]*\bstale\b[^;]*;", body.replace(looks[0], ""))
+        assert uses and all("__any_sync(0xffffffffu, stale)" in u or "bool stale = false" in u for u in uses)
