@@ -331,6 +331,13 @@ int msa_fwd_planned(const msa_problem* p, const uint16_t* q, const uint16_t* k, 
  * step can be captured into a CUDA graph and replayed.  The step's tables are
  * read on the device only: no call needs a length on the host.
  *
+ * Errors.  A call that finds *d_status set does nothing.  A call other than
+ * msa_cache_step that sets it itself leaves out what is at fault and, besides,
+ * whatever parts of its own launch come up behind the error: which these are is
+ * not determined (a row of a tensor, a head of it or 16 of its dims may be left
+ * as it was).  What it does write is what it would have written without the
+ * error, but for selections over a bad page.
+ *
  * A page holds one key block of one cache (block_size tokens of every KV
  * head).  Position p of request r lives in page block_table[r][p / B], at
  * offset p % B; its slot is page * B + offset.  The new tokens of a request
@@ -439,7 +446,10 @@ int msa_cache_step(const msa_cache_problem* p, const int32_t* new_lens, const in
  *              not used and may be NULL.
  * cu_tokens, chunks  as msa_cache_step wrote them.
  * index_tail   device bf16 [R, 2, B, Hkv, 128] in/out: index keys of each
- *              request's incomplete block b, at [r][b & 1][position % B].
+ *              request's incomplete block b, at [r][b & 1][position % B].  (The
+ *              rows that a request's first block is completed with are still
+ *              there after the call, unless the call's last block of the
+ *              request is an even number of blocks, and not 0, behind it.)
  * index_pool   device bf16 [P, Hkv, 128] out: for each block that this call
  *              completes, the mean of its tokens' index keys (fp32 sum in
  *              token order, divided by B, rounded to bf16). */
@@ -470,7 +480,11 @@ int msa_cache_read(const msa_cache_problem* p, const int64_t* slots, const uint8
  * block_table, chunks  as msa_cache_step wrote them.
  * sel          device int32 [Hkv, NC, topk] out; rows of padding chunks are
  *              left as they were.
- * Deterministic; a NaN score may take any rank, the selection stays valid. */
+ * A chunk row that does not fit and a page outside the cache set
+ * MSA_ERR_INVALID_CACHE: such a chunk's rows are left as they were, and the
+ * rows of the page's request mean nothing.
+ * Deterministic where no error is found; a NaN score may take any rank, the
+ * selection stays valid. */
 int msa_cache_select(const msa_cache_problem* p, const uint16_t* q_index, const uint16_t* index_pool,
                      const int32_t* block_table, const int32_t* chunks, int32_t* sel, int32_t* d_status,
                      void* stream);
@@ -488,7 +502,7 @@ int msa_cache_select(const msa_cache_problem* p, const uint16_t* q_index, const 
  *              (natural log).  A row that attends no key has o = 0 and lse =
  *              -inf.  Rows that no chunk covers are left as they were.
  * Cache bytes of keys that no query may attend may hold anything.
- * Deterministic. */
+ * Deterministic where no error is found. */
 int msa_cache_fwd(const msa_cache_problem* p, const uint16_t* q, const uint8_t* cache,
                   const int32_t* block_table, const int32_t* chunks, const int32_t* sel, uint16_t* o,
                   float* lse, int32_t* d_status, void* stream);

@@ -1043,3 +1043,142 @@ def test_selection_with_bad_rows_among_many(B, past, new, H):
                 assert left[:, bad].all()
             ok = ~left & ~bad[None]
             assert np.array_equal(got[ok], want[ok])
+
+
+def _attention_kernel(s):
+    """Which of the three attention kernels msa_cache_fwd picks for a case, from the sizes, as it does."""
+    import torch
+    c, sms = s.c, torch.cuda.get_device_properties(0).multi_processor_count
+    slots = -(-c.token_cap // c.chunk_cap)
+    slots = min(8, 2 * slots if slots > 1 else 1)
+    ranks, tiles = 1, c.topk * (c.block_size // 64)
+    while ranks < 8 and 2 * ranks <= tiles and c.chunk_cap * slots * c.num_kv_heads * 2 * ranks <= 2 * sms:
+        ranks *= 2
+    return "cluster" if ranks > 1 else "chunks" if 4 * c.token_cap >= 5 * c.chunk_cap else "batch"
+
+
+# sizes that the persistent kernels take, more items than they have CTAs
+PERSISTENT = {
+    "batch": dict(past=[(37 * i) % 500 for i in range(200)], new=[1] * 200, H=2),
+    "batch, some of several tokens": dict(past=[(37 * i) % 500 for i in range(200)],
+                                          new=[{3: 3, 50: 2, 120: 8, 199: 5}.get(i, 1) for i in range(200)], H=2),
+    "chunks": dict(past=[(61 * i) % 300 for i in range(24)], new=[20, 3, 8, 1] * 6, H=8),
+}
+
+
+@pytest.mark.parametrize("block", [64, 128])
+@pytest.mark.parametrize("case", list(PERSISTENT))
+def test_persistent_attention_over_any_selection(B, case, block):
+    """Empty slots anywhere, blocks in any order, chunks without their own block, and runs of chunks that select
+    nothing, in the two persistent kernels."""
+    s = Setup(B, topk=4, block=block, garbage=0xFF, seed=4, token_pad=3, chunk_pad=2, **PERSISTENT[case])
+    assert _attention_kernel(s) == case.split(",")[0]
+    s.fill()
+    sel, q = s.selection("holes"), s.queries()
+    nothing = s.rng.random(sel.shape[:2]) < 0.4
+    sel[nothing] = -1
+    assert (sel < 0).all(2).mean() > 0.3
+    o, lse = s.forward(q, sel)
+    assert s.code() == 0
+    _close(o, lse, C.attend(q, *s.values(), s.want["chunks"], sel, block, s.scale))
+
+
+@pytest.mark.parametrize("kind, code", [("twice", 5), ("future", 5), ("page", 10), ("request", 10), ("count", 10),
+                                        ("row", 10), ("position", 10), ("straddle", 10)])
+@pytest.mark.parametrize("case", list(PERSISTENT))
+def test_persistent_attention_refuses_bad_tables(B, case, kind, code):
+    """Bad selections, pages and chunk rows among many, in the persistent kernels: reported, their rows left as they
+    were.  Other rows are right, or left by a CTA that came up behind the error; with the error standing, a call writes
+    nothing; without it the same tensors serve again."""
+    import torch
+    s = Setup(B, topk=4, **PERSISTENT[case])
+    assert _attention_kernel(s) == case.split(",")[0]
+    s.fill()
+    sel, q, chunks, table = s.selection(), s.queries(), s.chunk_table(), _dev(s.full)
+    good = sel.copy()
+    want = C.attend(q, *s.values(), s.want["chunks"], sel, 64, s.scale)
+    T, H = s.T, s.H
+    bad = np.zeros((T, 16 * H), bool)
+    for g in [0, 7, len(s.want["chunks"]) - 1] + s.rng.choice(len(s.want["chunks"]), 4).tolist():
+        r, row, n, first = (int(x) for x in s.want["chunks"][g])
+        hs = slice(0, 16 * H)
+        if kind in ("twice", "future"):
+            hs = slice(16, 32)
+            sel[1, g, :2] = first // 64 if kind == "twice" else [first // 64 + 1, -1]
+        elif kind == "page":
+            sel[:, g, :] = [first // 64, -1, -1, -1]
+            table[r, first // 64] = s.c.num_pages if g else -1
+            for x, c in enumerate(s.want["chunks"]):    # other chunks of the request may select the page
+                if c[0] == r:
+                    bad[c[1]:c[1] + c[2]] = True
+        else:
+            col = dict(request=0, row=1, count=2, position=3, straddle=3)[kind]
+            chunks[g, col] = {"request": len(s.past), "row": T, "count": 9, "position": 64 * s.c.max_blocks,
+                              "straddle": first // 8 * 8 + 9 - n}[kind]
+            if kind == "straddle" and n == 1:
+                chunks[g, 2] = 2                        # position 8 k + 7 with two tokens
+                chunks[g, 3] = first // 8 * 8 + 7
+        bad[row:row + n, hs] = True
+    o, lse = s.forward(q, sel, chunks, table)
+    assert s.code() == code
+    got = o.float().cpu().numpy()
+    left = (got == 7.0).all(2) & (lse.cpu().numpy() == 7.0)
+    if kind != "page":
+        assert left[bad].all()
+    live = want[1].copy()
+    live[left] = np.nan                                 # as _close has them: not written
+    rest = live.copy()
+    rest[bad] = np.nan
+    o2, lse2 = o.clone(), lse.clone()
+    mask = torch.as_tensor(bad, device="cuda")
+    o2[mask], lse2[mask] = 7.0, 7.0                     # bad rows are not compared
+    _close(o2, lse2, (want[0], rest, *want[2:]))
+    o, lse = s.forward(q, good)
+    torch.cuda.synchronize()
+    assert bool((o == 7.0).all()) and bool((lse == 7.0).all())
+    s.status.zero_()
+    o, lse = s.forward(q, good)
+    assert s.code() == 0
+    _close(o, lse, want)
+
+
+def test_append_and_read_with_bad_slots_among_many(B):
+    """Slots outside the cache in launches of many CTAs: reported and left out; the other rows are right, or left as
+    they were by CTAs that came up behind the error."""
+    import torch
+    rng = np.random.default_rng(91)
+    P, T, H = 100, 6000, 2
+    slots = rng.permutation(P * 64)[:T].astype(np.int64)
+    at = rng.permutation(T)[:9]
+    broken = slots.copy()
+    broken[at] = [P * 64, -2, 1 << 40] * 3
+    c = B.make_cache_problem(num_requests=1, num_pages=P, max_blocks=1, num_q_heads=16 * H, topk=1, token_cap=T,
+                             chunk_cap=1)
+    bits = _bf16(rng, (T, H, 128))
+    x = to_bf16_tensor(bits, "cuda")
+    st = torch.zeros(4, dtype=torch.int32, device="cuda")
+    want = C.round_rows(bits, 0)[2]
+    cache = B.new_cache(c)
+    B.msa_cache_append(c, x, x, None, _dev(broken, torch.int64), None, None, cache, None, None, st)
+    torch.cuda.synchronize()
+    assert int(st[0].item()) == B.MSA_ERR_INVALID_CACHE
+    st.zero_()
+    out = [torch.full((T, H, 128), 9.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    B.msa_cache_read(c, _dev(slots, torch.int64), cache, *out, st)
+    torch.cuda.synchronize()
+    assert int(st[0].item()) == 0
+    for y in out:       # per token, head and 16 dims: what the row holds, or the zeros of before
+        y = O.bf16_to_f64(from_bf16_tensor(y)).reshape(T, H, 8, 16)
+        right, zero = (y == want.reshape(y.shape)).all(3), (y == 0).all(3)
+        assert zero[at].all() and (right | zero).all()
+    cache = B.new_cache(c)
+    B.msa_cache_append(c, x, x, None, _dev(slots, torch.int64), None, None, cache, None, None, st)
+    for y in out:
+        y.fill_(9.0)
+    B.msa_cache_read(c, _dev(broken, torch.int64), cache, *out, st)
+    torch.cuda.synchronize()
+    assert int(st[0].item()) == B.MSA_ERR_INVALID_CACHE
+    for y in out:
+        y = O.bf16_to_f64(from_bf16_tensor(y)).reshape(T, H, 8, 16)
+        right, left = (y == want.reshape(y.shape)).all(3), (y == 9.0).all(3)
+        assert left[at].all() and (right | left).all()
