@@ -845,7 +845,8 @@ int msa_cache_step(const msa_cache_problem* p, const int32_t* new_lens, const in
   cache::StepArgs a{new_lens,  seq_lens, ring,      free_ring, block_table, seq_lens_out, ring_out,
                     cu_tokens, slot_map, positions, chunks,    p->num_requests, p->num_pages, p->max_blocks,
                     p->block_size, p->token_cap, p->chunk_cap, d_status};
-  const size_t smem = (size_t)cache::kStepArrays * (p->num_requests + 1) * sizeof(int32_t);
+  const size_t row = (size_t)cache::kStepArrays * sizeof(int32_t);
+  const size_t smem = row * (p->num_requests + 1), largest = row * (cache::kMaxRequests + 1);
   // CTAs: a token (or chunk) a thread.  Up to 32 x 512 rows form one cluster and one launch;
   // above that a grid over the GPU and a second launch that finishes the step.
   const int64_t rows = p->chunk_cap > p->token_cap ? p->chunk_cap : p->token_cap;
@@ -853,14 +854,15 @@ int msa_cache_step(const msa_cache_problem* p, const int32_t* new_lens, const in
   if (want <= 32) {
     unsigned ctas = 1;
     while (ctas < 8 && ctas < want) ctas *= 2;
-    return cache::launch_kernel(cache::step_kernel<true>, dim3(ctas), cache::kStepThreads, smem, stream, ctas, a);
+    return cache::launch_kernel(cache::step_kernel<true>, dim3(ctas), cache::kStepThreads, smem, stream, ctas, a,
+                                largest);
   }
   int32_t sms = 0;
   if ((rc = sm_count_current(&sms))) return rc;
   rc = cache::launch_kernel(cache::step_kernel<false>, dim3((unsigned)(want < sms ? want : sms)), cache::kStepThreads,
-                            smem, stream, 1, a);
+                            smem, stream, 1, a, largest);
   if (rc) return rc;
-  return cache::launch_kernel(cache::step_finish_kernel, dim3(1), cache::kStepThreads, smem, stream, 1, a);
+  return cache::launch_kernel(cache::step_finish_kernel, dim3(1), cache::kStepThreads, smem, stream, 1, a, largest);
 }
 
 int msa_cache_append(const msa_cache_problem* p, const uint16_t* k, const uint16_t* v, const uint16_t* k_index,
@@ -912,10 +914,10 @@ int msa_cache_select(const msa_cache_problem* p, const uint16_t* q_index, const 
   const int64_t H = p->num_kv_heads, NC = p->chunk_cap;
   if (NC * H > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
   const size_t row = (size_t)p->max_blocks * 4;
-  auto launch = [&](auto kernel, size_t smem, int64_t ctas, int threads) {
-    return cache::launch_kernel(kernel, dim3((unsigned)ctas), threads, smem, stream, 1, a);
-  };
   constexpr size_t kSmem = 227 * 1024;
+  auto launch = [&](auto kernel, size_t smem, int64_t ctas, int threads) {
+    return cache::launch_kernel(kernel, dim3((unsigned)ctas), threads, smem, stream, 1, a, kSmem);
+  };
   if (p->token_cap / p->chunk_cap >= 3) {
     // 16 warps share the eight chunks' 500 keys better than 8 do (21 against
     // 24 us for 2 x 2048 tokens over 32k cached ones)

@@ -107,11 +107,11 @@ MSA_DEV void after_previous_kernel() {
 }
 
 // Launches kernel(args) that way; cluster > 1: in clusters of that many CTAs
-// along x.
+// along x.  largest: the kernel's largest dynamic shared memory, where it varies.
 template <class Args>
 inline int launch_kernel(void (*kernel)(Args), dim3 grid, int threads, size_t smem, void* stream, unsigned cluster,
-                         const Args& args) {
-  cudaError_t e = allow_smem(kernel, smem);
+                         const Args& args, size_t largest = 0) {
+  cudaError_t e = allow_smem(kernel, smem, largest ? largest : smem);
   if (e != cudaSuccess) return MSA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;

@@ -50,12 +50,14 @@ int sm_count_current(int32_t* out);
 int check_device_current();
 
 // Dynamic shared memory above 48 KB (with the static part) needs the kernel's
-// leave; well below that the call
-// is left out (it costs a good part of a launch).
+// leave; well below that the call is left out (it costs a good part of a
+// launch).  largest: the most that any launch of the kernel asks for, the same in
+// every call: the limit is the kernel's, not the launch's, and another thread's
+// smaller one between this call and the launch would refuse the launch.
 template <class F>
-inline cudaError_t allow_smem(F* fn, size_t bytes) {
+inline cudaError_t allow_smem(F* fn, size_t bytes, size_t largest) {
   if (bytes <= 32 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)largest);
 }
 
 inline int cuda_status(cudaError_t e) { return e == cudaSuccess ? MSA_OK : MSA_ERR_CUDA; }

@@ -1182,3 +1182,44 @@ def test_append_and_read_with_bad_slots_among_many(B):
         y = O.bf16_to_f64(from_bf16_tensor(y)).reshape(T, H, 8, 16)
         right, left = (y == want.reshape(y.shape)).all(3), (y == 9.0).all(3)
         assert left[at].all() and (right | left).all()
+
+
+def test_calls_from_several_threads(B):
+    """Host threads with caches of very different sizes on streams of their own: a call must not fail because another
+    thread's launch of the same kernel needs less shared memory.  (The entry points are called without the binding's
+    checks, which hold the interpreter's lock: the threads then meet inside the library.)"""
+    import ctypes
+    import threading
+    import torch
+
+    def made(R, M):
+        c = B.make_cache_problem(num_requests=R, num_pages=4, max_blocks=M, num_q_heads=16, topk=1, token_cap=1,
+                                 chunk_cap=1)
+        i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32, device="cuda")
+        step = (i32(R), i32(R), _dev([0, 4]), _dev(np.arange(4)), i32(R, M), i32(R), i32(2), i32(R + 1),
+                torch.zeros(1, dtype=torch.int64, device="cuda"), i32(1), i32(1, 4) - 1, i32(4))
+        rows = torch.zeros((4, 1, 128), dtype=torch.bfloat16, device="cuda")
+        select = (rows[:1], rows, step[4], step[10], i32(1, 1, 1), step[11])
+        stream = torch.cuda.Stream()
+        fix = lambda t: [ctypes.byref(c)] + [ctypes.c_void_p(x.data_ptr()) for x in t] + [ctypes.c_void_p(stream.cuda_stream)]
+        return (c, step, select, stream), fix(step), fix(select)
+
+    work = [made(*x) for x in [(8192, 40000), (2000, 12000), (8000, 30000), (1900, 9000)]]
+    torch.cuda.synchronize()
+    failed, start = [0] * len(work), threading.Barrier(len(work))
+
+    def run(i):
+        _, step, select = work[i]
+        start.wait()
+        for _ in range(15000):
+            failed[i] += B.lib.msa_cache_step(*step) != 0
+            failed[i] += B.lib.msa_cache_select(*select) != 0
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(work))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert failed == [0] * len(work)
+    assert all(int(keep[1][-1][0].item()) == 0 for keep, _, _ in work)
