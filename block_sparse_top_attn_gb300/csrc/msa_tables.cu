@@ -1105,17 +1105,20 @@ int msa_build_k2q(const msa_problem* p, const int32_t* sel, int32_t* row_ptr, in
   // shared memory: the staged piece, then per row of a window a counter
   // (pass 1) or a cursor (pass 4) and a chunk mask
   a.win = NB < kRowWindow ? NB : kRowWindow;
-  const size_t count_smem = sizeof(K2QStage) + 2 * sizeof(int) * a.win;
-  const size_t scatter_smem = sizeof(K2QStage) + 2 * sizeof(int) * a.win;
+  const size_t smem = sizeof(K2QStage) + 2 * sizeof(int) * a.win;
+  // The limit is the kernels', not this call's: the same for every problem, or a
+  // thread with a small one could lower it under another thread's launch, and the
+  // passes behind a refused launch would read counts that nothing wrote.
+  constexpr int kLargest = (int)(sizeof(K2QStage) + 2 * sizeof(int) * kRowWindow);
   if ((rc = cuda_status(cudaFuncSetAttribute(k2q_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)count_smem))) ||
+                                             kLargest))) ||
       (rc = cuda_status(cudaFuncSetAttribute(k2q_scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)scatter_smem))))
+                                             kLargest))))
     return rc;
-  k2q_count_kernel<<<dim3((unsigned)nS, Hi), kCountThreads, count_smem, st>>>(a);
+  k2q_count_kernel<<<dim3((unsigned)nS, Hi), kCountThreads, smem, st>>>(a);
   k2q_group_offsets_kernel<<<dim3((unsigned)((NB + 31) / 32), Hi), 1024, 0, st>>>(a);
   k2q_row_ptr_kernel<<<Hi, 1024, 0, st>>>(a);
-  k2q_scatter_kernel<<<dim3((unsigned)nS, Hi), kScatterThreads, scatter_smem, st>>>(a);
+  k2q_scatter_kernel<<<dim3((unsigned)nS, Hi), kScatterThreads, smem, st>>>(a);
   return cuda_status(cudaGetLastError());
 }
 

@@ -51,3 +51,48 @@ def test_a_call_on_a_side_stream_is_that_streams_alone(B, call):
             x, y, w = x[:1], y[:1], w[:1]
         assert torch.equal(x, w) and torch.equal(y, w)
     assert int(got[-1][0].item()) == 0
+
+
+def test_tables_of_two_sizes_from_two_threads(B):
+    """Two host threads build the tables of a problem with many key blocks and of a small one, on streams of their own:
+    every call succeeds and writes the tables of a call alone.  (The shared-memory limit of the build's kernels does not
+    depend on the problem.)"""
+    import ctypes
+    import threading
+    import torch
+
+    def made(length, topk, seed):
+        pb = W.make_problem(lengths=[length], num_index_heads=1, topk=topk, policy="diag_uniform", seed=seed, values=False)
+        prob, t = upload(pb)
+        bw = B.Backward(prob)
+        B.msa_build_k2q(prob, t["sel"], bw.row_ptr, bw.q_indices, bw.edge_cap, bw.status, bw.ws)
+        torch.cuda.synchronize()
+        n = int(bw.row_ptr[0, -1].item())
+        want = bw.row_ptr.clone(), bw.q_indices[:, :n].clone()
+        bw.row_ptr.fill_(-7)
+        bw.q_indices.fill_(-7)
+        c, stream = prob.c_struct(), torch.cuda.Stream()
+        p = lambda x: ctypes.c_void_p(x.data_ptr())
+        args = [ctypes.byref(c), p(t["sel"]), p(bw.row_ptr), p(bw.q_indices), ctypes.c_int64(bw.edge_cap), p(bw.status),
+                p(bw.ws), ctypes.c_size_t(bw.ws.numel()), ctypes.c_void_p(stream.cuda_stream)]
+        return (c, prob, t, stream), bw, want, args, n
+
+    work = [made(400000, 1, 1), made(200, 2, 2)]
+    torch.cuda.synchronize()
+    failed, start = [0, 0], threading.Barrier(2)
+
+    def run(i):
+        start.wait()
+        for _ in range(2000):
+            failed[i] += B.lib.msa_build_k2q(*work[i][3]) != 0
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert failed == [0, 0]
+    for _, bw, (row_ptr, q_indices), _, n in work:
+        assert int(bw.status[0].item()) == 0
+        assert torch.equal(bw.row_ptr, row_ptr) and torch.equal(bw.q_indices[:, :n], q_indices)
