@@ -407,7 +407,7 @@ MSA_DEV void index_chunk(const AppendArgs& a, int g) {
       uint32_t w[kChunk];
 #pragma unroll
       for (int i = 0; i < kChunk; ++i)
-        if (q + i < p1) w[i] = __ldg(reinterpret_cast<const uint32_t*>(a.k_index + (cu0 + q + i - past) * hs + d));
+        if (q + i < p1) w[i] = *reinterpret_cast<const uint32_t*>(a.k_index + (cu0 + q + i - past) * hs + d);
 #pragma unroll
       for (int i = 0; i < kChunk; ++i)
         if (q + i < p1) *reinterpret_cast<uint32_t*>(dst + ((q + i) % a.B) * hs) = w[i];
@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(32 * W, 1) select_kernel(SelectArgs a) {
     const int32_t* table = a.block_table + (int64_t)request * a.M;
     // this lane's page of the 32 keys from block b0 on
     auto page_of = [&](int b0) {
-      int page = b0 + lane < nmax ? __ldg(table + b0 + lane) : 0;
+      int page = b0 + lane < nmax ? table[b0 + lane] : 0;
       if (page < 0 || page >= a.P) {
         set_status(a.status, MSA_ERR_INVALID_CACHE);
         page = 0;

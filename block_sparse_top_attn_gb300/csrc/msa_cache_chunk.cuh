@@ -112,13 +112,13 @@ struct Codes {
 template <bool kWide>
 MSA_DEV void load_k(Codes& c, const uint8_t* tile, int key, int half) {
   load32(tile + OFF_KC + key * kRowBytes + half * 32, kWide, c.w);
-  c.scales = __ldg(reinterpret_cast<const uint32_t*>(tile + OFF_KS + key * kScales + half * 4));
+  c.scales = *reinterpret_cast<const uint32_t*>(tile + OFF_KS + key * kScales + half * 4);
 }
 template <bool kWide>
 MSA_DEV void load_v(Codes& c, const uint8_t* tile, int key, int half) {
   load32(tile + OFF_VC + v_code_offset(key, half * 4), kWide, c.w);
   const uint8_t* s = tile + OFF_VS + half * 4 * kTile + key;
-  c.scales = __ldg(s) | __ldg(s + kTile) << 8 | __ldg(s + 2 * kTile) << 16 | (uint32_t)__ldg(s + 3 * kTile) << 24;
+  c.scales = s[0] | s[kTile] << 8 | s[2 * kTile] << 16 | (uint32_t)s[3 * kTile] << 24;
 }
 // Bytes of w that are the e4m3 NaN (0x7F; scales have no sign), as 0xFF.
 MSA_DEV uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w, 0x7F7F7F7Fu); }
@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_chunk_kernel(FwdCacheArgs a) 
             if (lane < 8) {
               const uint8_t* vs = a.cache + tile_index(own_page, h, a.H, a.B / kTile, c.w % a.B / kTile) * kTileBytes +
                                   OFF_VS + lane * kTile + c.w % kTile / 8 * 8;
-              const uint2 s8 = __ldg(reinterpret_cast<const uint2*>(vs));
+              const uint2 s8 = *reinterpret_cast<const uint2*>(vs);
               // one bit of each byte, gathered in the top four
               nan = ((nan_bytes(s8.x) & 0x01010101u) * 0x10204080u) >> 28 |
                     ((nan_bytes(s8.y) & 0x01010101u) * 0x10204080u) >> 28 << 4;

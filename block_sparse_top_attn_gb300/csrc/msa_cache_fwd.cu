@@ -106,7 +106,7 @@ MSA_DEV float load_q_row(const uint16_t* src, uint32_t (&w)[16]) {
   uint32_t amax = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(src) + i);
+    const uint4 x = reinterpret_cast<const uint4*>(src)[i];
     w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
   }
 #pragma unroll

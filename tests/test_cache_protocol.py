@@ -410,3 +410,17 @@ def test_attention_decides_on_the_status_by_a_vote(file, name):
         assert re.search(r"\bstale = status_bad\(a\.status\)", looks[0])
         uses = re.findall(r"[^;]*\bstale\b[^;]*;", body.replace(looks[0], ""))
         assert uses and all("__any_sync(0xffffffffu, stale)" in u or "bool stale = false" in u for u in uses)
+
+
+def test_serving_kernels_read_by_plain_loads():
+    """The serving kernels may come up while the kernel before them still writes, so none of them reads through the path
+    for memory that is constant for a kernel's life (nor lets the compiler choose it)."""
+    import pathlib
+    import re
+    csrc = pathlib.Path(__file__).parent.parent / "block_sparse_top_attn_gb300" / "csrc"
+    files = sorted(csrc.glob("msa_cache*"))
+    assert len(files) >= 5
+    for f in files:
+        code = re.sub(r"//[^\n]*", "", f.read_text())
+        for word in ("__ldg", "ld.global.nc", "__restrict__"):
+            assert word not in code, (f.name, word)
