@@ -253,6 +253,7 @@ struct AppendArgs {
   uint8_t* cache;
   uint16_t *index_tail, *index_pool;
   int T, H, B, R, NC;
+  int positions;  // M * B: a request's most tokens
   int64_t slots;  // P * B
   float k_mul, v_mul;  // 2^-exp
   bool wide;           // k and v are aligned to 32 bytes
@@ -349,7 +350,7 @@ MSA_DEV void index_chunk(const AppendArgs& a, int g) {
     cu0 = a.cu_tokens[r];
     cu1 = a.cu_tokens[r + 1];
     good = cu0 >= 0 && cu0 <= row0 && cu1 >= row0 + n && cu1 <= a.T && pos0 >= row0 - cu0 &&
-           pos0 % a.B + n <= a.B;
+           pos0 <= a.positions - (cu1 - row0) && pos0 % a.B + n <= a.B;
   }
   if (!good) {
     if (threadIdx.x == 0) set_status(a.status, MSA_ERR_INVALID_CACHE);
@@ -877,9 +878,9 @@ int msa_cache_append(const msa_cache_problem* p, const uint16_t* k, const uint16
   const int64_t kv_blocks = cache::row_blocks(T, H, 32), idx_blocks = k_index ? NC : 0;
   if (kv_blocks + idx_blocks > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
   cache::AppendArgs a{k, v, k_index, slot_map, cu_tokens, chunks, kv_cache, index_tail, index_pool, (int)T, (int)H,
-                      p->block_size, p->num_requests, (int)NC, (int64_t)p->num_pages * p->block_size,
-                      cache::exp2i(-p->k_exp), cache::exp2i(-p->v_exp), cache::aligned32(k, v), (int)idx_blocks,
-                      d_status};
+                      p->block_size, p->num_requests, (int)NC, p->max_blocks * p->block_size,
+                      (int64_t)p->num_pages * p->block_size, cache::exp2i(-p->k_exp), cache::exp2i(-p->v_exp),
+                      cache::aligned32(k, v), (int)idx_blocks, d_status};
   return cache::launch_kernel(cache::append_kernel, dim3((unsigned)(kv_blocks + idx_blocks)), 256, 0, stream, 1, a);
 }
 

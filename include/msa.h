@@ -444,7 +444,9 @@ int msa_cache_step(const msa_cache_problem* p, const int32_t* new_lens, const in
  * k_index      device bf16 [T, Hkv, 128], index key of each new token, or
  *              NULL: cu_tokens, chunks, index_tail and index_pool are then
  *              not used and may be NULL.
- * cu_tokens, chunks  as msa_cache_step wrote them.
+ * cu_tokens, chunks  as msa_cache_step wrote them.  A chunk row that does not
+ *              fit (the token rows, its block, max_blocks) is left out and
+ *              sets MSA_ERR_INVALID_CACHE.
  * index_tail   device bf16 [R, 2, B, Hkv, 128] in/out: index keys of each
  *              request's incomplete block b, at [r][b & 1][position % B].  (The
  *              rows that a request's first block is completed with are still

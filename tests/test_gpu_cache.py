@@ -1223,3 +1223,37 @@ def test_calls_from_several_threads(B):
     torch.cuda.synchronize()
     assert failed == [0] * len(work)
     assert all(int(keep[1][-1][0].item()) == 0 for keep, _, _ in work)
+
+
+@pytest.mark.parametrize("position, count, append_ok, select_ok", [
+    (3, 5, True, True), (62, 5, False, True), (60, 5, False, True), (59, 5, True, True), (1 << 30, 5, False, False),
+    (64 * 3, 5, False, False), (64 * 3 - 5, 5, True, True), ((1 << 31) - 6, 5, False, False), (0, 5, True, True)])
+def test_append_and_select_check_positions(B, position, count, append_ok, select_ok):
+    """A chunk row whose position does not fit: one that leaves its block is refused by append, one behind the block
+    table by both, the largest int among them; any other is followed, and its rows of the index tail are those of its
+    position."""
+    import torch
+    s = Setup(B, [3], [5])
+    assert s.c.max_blocks == 3
+    ki = _bf16(s.rng, (5, 1, 128))
+    di = to_bf16_tensor(ki, "cuda")
+    chunks = s.chunk_table()
+    chunks[0, 2:] = torch.tensor([count, position], dtype=torch.int32)
+    tail = torch.zeros((1, 2, 64, 1, 128), dtype=torch.bfloat16, device="cuda")
+    pool = torch.zeros((s.c.num_pages, 1, 128), dtype=torch.bfloat16, device="cuda")
+    B.msa_cache_append(s.c, di, di, di, _dev(s.want["slot_map"], torch.int64), _dev(s.want["cu_tokens"]), chunks,
+                       B.new_cache(s.c), tail, pool, s.status)
+    want = np.zeros((1, 2, 64, 1, 128), np.uint16)
+    assert s.code() == (0 if append_ok else B.MSA_ERR_INVALID_CACHE)
+    if append_ok and (position + 5) % 64:
+        want[0, position // 64 & 1, position % 64:position % 64 + 5] = ki
+    if not append_ok or (position + 5) % 64:
+        assert np.array_equal(from_bf16_tensor(tail), want) and not bool(pool.any())
+    s.status.zero_()
+    sel = torch.full((1, s.c.chunk_cap, s.K), -5, dtype=torch.int32, device="cuda")
+    B.msa_cache_select(s.c, di, pool, torch.zeros((1, 3), dtype=torch.int32, device="cuda"), chunks, sel, s.status)
+    assert s.code() == (0 if select_ok else B.MSA_ERR_INVALID_CACHE)
+    if select_ok:
+        assert int(sel[0, 0, 0].item()) == position // 64
+    else:
+        assert bool((sel == -5).all())
