@@ -909,9 +909,10 @@ int msa_cache_select(const msa_cache_problem* p, const uint16_t* q_index, const 
   if ((rc = check_device_current())) return rc;
   cache::SelectArgs a{q_index, index_pool, block_table, chunks, sel, p->num_requests, p->num_pages, p->max_blocks,
                       p->block_size, p->token_cap, p->chunk_cap, p->num_kv_heads, p->topk, d_status};
-  // Chunks of several tokens come from prompts, whose chunks share a request's
-  // keys: 8 of them to a CTA, while 8 rows of scores fit shared memory.  (One to
-  // a CTA: 62 us for the same prompts.)
+  // Chunks of several tokens (by the capacities: the lengths are on the device)
+  // come from prompts, whose chunks share a request's keys: 8 of them to a CTA,
+  // while 8 rows of scores fit shared memory.  (One to a CTA: 62 us for the same
+  // prompts.)
   const int64_t H = p->num_kv_heads, NC = p->chunk_cap;
   if (NC * H > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
   const size_t row = (size_t)p->max_blocks * 4;

@@ -30,8 +30,8 @@
 // and V buffers allow.  (A next item's Q or codes loaded before this one's end:
 // 239 and 232 us, slower although the waits are shorter.)
 //
-// Times: 3.4k new tokens x 4 heads x 2048 keys, 198 us (966 TFLOP/s); 4k x 8 heads
-// the same 497 us (1090 TFLOP/s).
+// Times: 3.4k new tokens x 4 heads x 2048 keys, 195 us (983 TFLOP/s); 4k x 8 heads
+// the same 492 us (1102 TFLOP/s).
 #pragma once
 
 namespace msa {

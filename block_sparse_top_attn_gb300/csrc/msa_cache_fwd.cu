@@ -17,12 +17,13 @@
 // ones, and its operands would have to be decoded into shared memory (64 KB
 // written and read per 128 keys, more than the time of their DRAM bytes).  Codes
 // become fp16 in registers, in the layout of the MMA's B fragment.  A warp takes
-// 32 keys, so that four chains of score MMAs overlap (16 keys: 198 us for 256
-// tokens x 8 heads x 2048 keys, 32 keys: 163).
+// 32 keys, so that four chains of score MMAs overlap (256 tokens x 8 heads x 2048
+// keys: 162 us, and 214 for a form with 16 keys a warp).
 // What bounds it now: about 600 instructions per 32 keys and warp, of them 128
-// conversions and 128 products at two cycles each and 64 MMAs at eight; such a mix
-// issues at most about 0.6 instructions a cycle, and the kernel reaches 0.46.
-// 8 warps with 200 registers and 12 with 128 take the same time.
+// conversions and 128 products at two cycles each and 64 MMAs at eight.  Such a mix
+// issues at most about 0.6 instructions a cycle, which would be 114 us for that
+// case; the kernel takes 149 at 0.46, the rest being the latency of a tile's own
+// chain.  8 warps with 200 registers: 149 us, 12 with 128: 154.
 //
 // In this kernel warp 0 compacts the selection and looks up the pages while warp
 // 3 stages the query; whole 9 KB tiles (codes and scales of 64 keys are
@@ -542,6 +543,10 @@ extern "C" int msa_cache_fwd(const msa_cache_problem* p, const uint16_t* q, cons
   a.v_mul = cache::exp2i(p->v_exp);
   a.slots = 1;
   a.status = d_status;
+  // This rule and the next ones know the capacities only: the lengths are on the
+  // device.  Where chunk_cap is a bound (msa_cache_chunk_bound counts idle requests
+  // too) and well above the chunks there are, few long pieces may look like single
+  // tokens; the results are the same, the time is not.
   // Token slots of a chunk in the grid: one where tokens and chunk rows are
   // equal in number (decode), else twice the mean, at most 8.  A chunk with more
   // tokens than slots takes them in turn; a slot without a token costs the
@@ -560,11 +565,12 @@ extern "C" int msa_cache_fwd(const msa_cache_problem* p, const uint16_t* q, cons
     return cache::launch_kernel(cache::fwd_cache_kernel, dim3((unsigned)(items * ranks), (unsigned)p->num_kv_heads),
                                 cache::kFwdThreads, sizeof(cache::FwdShared), stream, (unsigned)ranks, a);
   // Chunk rows with 1.25 tokens and more on average (3 new tokens a request and
-  // more): the 128-row kernel, which takes the same time for one token of a chunk
-  // as for eight, where the single-token kernel takes them one after another (32
-  // tiles, 8 heads: 3 tokens x 8 requests 30 against 47 us, 8 tokens x 16 requests 41
-  // against 149; 2 tokens x 64 requests 85 against 87).  In clusters the single-token
-  // kernel is faster (32 tokens x 2 heads x 32 tiles 16 against 30).
+  // more, where all requests have some): the 128-row kernel, which takes the same
+  // time for one token of a chunk as for eight, where the single-token kernel takes
+  // them one after another (32 tiles, 8 heads: 3 tokens x 8 requests 30 against 47
+  // us, 8 tokens x 16 requests 41 against 149; 2 tokens x 64 requests 85 against 87).
+  // In clusters the single-token kernel is faster (32 tokens x 2 heads x 32 tiles 16
+  // against 30).
   if (4 * (int64_t)p->token_cap >= 5 * (int64_t)p->chunk_cap) {
     const bool wide = cache::aligned32(q, o) && cache::aligned32(kv_cache, nullptr);
     const auto kernel = wide ? cache::chunk::fwd_chunk_kernel<true> : cache::chunk::fwd_chunk_kernel<false>;
