@@ -1083,20 +1083,35 @@ def test_persistent_attention_over_any_selection(B, case, block):
     _close(o, lse, C.attend(q, *s.values(), s.want["chunks"], sel, block, s.scale))
 
 
+@pytest.fixture(scope="module")
+def persistent(B):
+    """The sizes above with everything in the cache, a selection, queries and the oracle's result: made once a case."""
+    made = {}
+
+    def get(case):
+        if case not in made:
+            s = Setup(B, topk=4, **PERSISTENT[case])
+            assert _attention_kernel(s) == case.split(",")[0]
+            s.fill()
+            sel, q = s.selection(), s.queries()
+            made[case] = s, sel, q, C.attend(q, *s.values(), s.want["chunks"], sel, 64, s.scale)
+        return made[case]
+
+    yield get
+    made.clear()
+
+
 @pytest.mark.parametrize("kind, code", [("twice", 5), ("future", 5), ("page", 10), ("request", 10), ("count", 10),
                                         ("row", 10), ("position", 10), ("straddle", 10)])
 @pytest.mark.parametrize("case", list(PERSISTENT))
-def test_persistent_attention_refuses_bad_tables(B, case, kind, code):
+def test_persistent_attention_refuses_bad_tables(persistent, case, kind, code):
     """Bad selections, pages and chunk rows among many, in the persistent kernels: reported, their rows left as they
     were.  Other rows are right, or left by a CTA that came up behind the error; with the error standing, a call writes
     nothing; without it the same tensors serve again."""
     import torch
-    s = Setup(B, topk=4, **PERSISTENT[case])
-    assert _attention_kernel(s) == case.split(",")[0]
-    s.fill()
-    sel, q, chunks, table = s.selection(), s.queries(), s.chunk_table(), _dev(s.full)
-    good = sel.copy()
-    want = C.attend(q, *s.values(), s.want["chunks"], sel, 64, s.scale)
+    s, good, q, want = persistent(case)
+    sel, chunks, table = good.copy(), s.chunk_table(), _dev(s.full)
+    s.status.zero_()
     T, H = s.T, s.H
     bad = np.zeros((T, 16 * H), bool)
     for g in [0, 7, len(s.want["chunks"]) - 1] + s.rng.choice(len(s.want["chunks"]), 4).tolist():
