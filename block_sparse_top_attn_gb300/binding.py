@@ -35,6 +35,8 @@ MSA_BWD_SELFTEST_HOLD_REDUCE = 16
 MSA_WALK_LEN = 8
 MSA_CACHE_TILE_BYTES = 9216
 MSA_CHUNK_COLS = 4
+MSA_ROPE_Q, MSA_ROPE_K, MSA_ROPE_Q_INDEX, MSA_ROPE_K_INDEX, MSA_ROPE_V, MSA_ROPE_TENSORS = 0, 1, 2, 3, 4, 5
+MSA_ROPE_NORM, MSA_ROPE_ROTATE, MSA_ROPE_PER_HEAD, MSA_ROPE_WEIGHT_FP32 = 1, 2, 4, 8
 
 HEAD_DIM, BLOCK, CHUNK, GROUP = 128, 64, 8, 16
 
@@ -71,6 +73,21 @@ class msa_cache_problem(ctypes.Structure):
         "query_chunk", "topk", "token_cap", "chunk_cap", "k_exp", "v_exp")] + [("softmax_scale", ctypes.c_float)]
 
 
+class msa_rope_tensor(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int32), ("flags", ctypes.c_uint32), ("weight", ctypes.c_void_p)] + \
+               [(name, ctypes.c_int64) for name in ("x_token", "x_head", "y_token", "y_head")]
+
+
+class msa_rope_pair(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_uint64), ("axis", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class msa_rope_problem(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in ("tokens", "head_dim", "rotary_dim", "num_axes", "adjacent")] + \
+               [(name, ctypes.c_float) for name in ("eps", "weight_offset", "cos_scale")] + \
+               [("pairs", ctypes.c_void_p), ("tensor", msa_rope_tensor * MSA_ROPE_TENSORS)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libmsa.so is not built ({LIB_PATH}); run __graft_entry__.build() "
@@ -78,6 +95,7 @@ def _load():
     lib = ctypes.CDLL(LIB_PATH)
     P = ctypes.POINTER(msa_problem)
     C = ctypes.POINTER(msa_cache_problem)
+    N = ctypes.POINTER(msa_rope_problem)
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     sig = {
         "msa_workspace_bytes": (sz, [P, i64, i64, i32]),
@@ -106,6 +124,11 @@ def _load():
         "msa_cache_read": (ctypes.c_int, [C] + [vp] * 6),
         "msa_cache_select": (ctypes.c_int, [C] + [vp] * 7),
         "msa_cache_fwd": (ctypes.c_int, [C] + [vp] * 9),
+        "msa_rope_pairs": (ctypes.c_int, [vp, vp, i32, ctypes.POINTER(msa_rope_pair)]),
+        "msa_norm_rope": (ctypes.c_int, [N] + [vp] * 5),
+        "msa_norm_rope_bwd_bytes": (sz, [N]),
+        "msa_norm_rope_bwd": (ctypes.c_int, [N] + [vp] * 7 + [sz, vp]),
+        "msa_cache_append_rope": (ctypes.c_int, [C, N] + [vp] * 16),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -545,6 +568,256 @@ def msa_cache_fwd(c, q, cache, block_table, chunks, sel, o, lse, d_status, strea
            "msa_cache_fwd")
 
 
+# ---------------------------------------------------------------------------
+# norm and rotary positions
+# ---------------------------------------------------------------------------
+
+class RopePairs:
+    """The frequencies and position columns of the rotated pairs, on the device (msa_rope_pair [rotary_dim / 2])."""
+
+    def __init__(self, table, rotary_dim, num_axes):
+        self.table, self.rotary_dim, self.num_axes = table, rotary_dim, num_axes
+
+
+def rope_pairs(inv_freq, axes=None, device="cuda") -> RopePairs:
+    """Table of pairs from angular frequencies (radians per position; rotary_dim / 2 numbers, fp64) and each pair's
+    position column (None: one column for all)."""
+    import torch
+    f = np.ascontiguousarray([float(x) for x in inv_freq], np.float64)
+    ax = np.zeros(len(f), np.int32) if axes is None else np.ascontiguousarray([int(x) for x in axes], np.int32)
+    if f.shape != ax.shape:
+        raise ValueError(f"axes: {len(ax)} columns for {len(f)} pairs")
+    if 2 * len(f) not in (32, 64, 96, 128):
+        raise ValueError(f"inv_freq: {len(f)} pairs, need 16, 32, 48 or 64")
+    out = (msa_rope_pair * len(f))()
+    _check(lib.msa_rope_pairs(f.ctypes.data, ax.ctypes.data, len(f), out), "msa_rope_pairs")
+    table = torch.from_numpy(np.frombuffer(out, np.int64).reshape(-1, 2).copy()).to(device)
+    return RopePairs(table, 2 * len(f), int(ax.max()) + 1)
+
+
+def rope_frequencies(rotary_dim, base=10000.0):
+    """base ** (-2 p / rotary_dim) for the pairs p, fp64."""
+    return float(base) ** (-2.0 * np.arange(rotary_dim // 2, dtype=np.float64) / rotary_dim)
+
+
+class RopeTensor:
+    """One tensor of a norm and rotary call: heads, what is done to them, the norm's weight (bf16 or fp32, [128] or
+    [heads, 128]) and the strides (token, head) of its rows in and out, in elements (None: contiguous)."""
+
+    def __init__(self, heads, norm=True, rotate=True, weight=None, x_strides=None, y_strides=None):
+        import torch
+        self.heads, self.weight = int(heads), weight
+        self.flags = (MSA_ROPE_NORM if norm else 0) | (MSA_ROPE_ROTATE if rotate else 0)
+        if weight is not None:
+            if not norm:
+                raise ValueError("weight: a weight needs a norm")
+            if weight.dtype not in (torch.bfloat16, torch.float32) or not weight.is_contiguous() \
+                    or tuple(weight.shape) not in ((HEAD_DIM,), (self.heads, HEAD_DIM)):
+                raise ValueError(f"weight: need a contiguous bf16 or fp32 tensor of shape ({HEAD_DIM},) or "
+                                 f"({self.heads}, {HEAD_DIM})")
+            self.flags |= (MSA_ROPE_PER_HEAD if weight.dim() == 2 else 0) \
+                | (MSA_ROPE_WEIGHT_FP32 if weight.dtype == torch.float32 else 0)
+        self.x_strides = tuple(x_strides or (self.heads * HEAD_DIM, HEAD_DIM))
+        self.y_strides = tuple(y_strides or (self.heads * HEAD_DIM, HEAD_DIM))
+
+
+def make_rope_problem(tokens, pairs, q=None, k=None, q_index=None, k_index=None, v=None, adjacent=False, eps=1e-6,
+                      weight_offset=0.0, cos_scale=1.0, num_axes=None) -> msa_rope_problem:
+    """The C description of a norm and rotary call: RopePairs (None: nothing is rotated) and RopeTensors (None: the call
+    has no such tensor; v is for msa_cache_append_rope).  It keeps the pairs and weights alive.  num_axes: the
+    positions' columns, where they are more than the pairs use."""
+    s = msa_rope_problem()
+    s.tokens, s.head_dim, s.adjacent = int(tokens), HEAD_DIM, int(bool(adjacent))
+    s.rotary_dim = pairs.rotary_dim if pairs is not None else 0
+    s.num_axes = int(num_axes or (pairs.num_axes if pairs is not None else 1))
+    s.eps, s.weight_offset, s.cos_scale = float(eps), float(weight_offset), float(cos_scale)
+    s.pairs = pairs.table.data_ptr() if pairs is not None else None
+    for i, t in enumerate((q, k, q_index, k_index, v)):
+        if t is not None:
+            s.tensor[i] = msa_rope_tensor(t.heads, t.flags, _addr(t.weight), *t.x_strides, *t.y_strides)
+    s._keep = (pairs, q, k, q_index, k_index, v)
+    return s
+
+
+def _addrs(tensors):
+    """A C array of the device addresses of q, k, q_index and k_index (None: NULL)."""
+    return (ctypes.c_void_p * 4)(*[None if t is None else t.data_ptr() for t in tensors])
+
+
+def msa_norm_rope(p, xs, positions, ys, d_status, stream=None):
+    """xs, ys: [q, k, q_index, k_index], None where p has no such tensor."""
+    _check(lib.msa_norm_rope(p, _addrs(xs), positions.data_ptr(), _addrs(ys), d_status.data_ptr(),
+                             _raw_stream(stream)),
+           "msa_norm_rope")
+
+
+def msa_norm_rope_bwd_bytes(p) -> int:
+    return int(lib.msa_norm_rope_bwd_bytes(p))
+
+
+def msa_norm_rope_bwd(p, dys, xs, positions, dxs, dws, d_status, ws, stream=None):
+    """dys, xs, dxs, dws: [q, k, q_index, k_index], None where p has no such tensor (dws: or no gradient is wanted)."""
+    _check(lib.msa_norm_rope_bwd(p, _addrs(dys), _addrs(xs), positions.data_ptr(), _addrs(dxs), _addrs(dws),
+                                 d_status.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                 _raw_stream(stream)),
+           "msa_norm_rope_bwd")
+
+
+def msa_cache_append_rope(c, p, q, k, v, q_index, k_index, positions, slot_map, cu_tokens, chunks, q_out, q_index_out,
+                          cache, index_tail, index_pool, d_status, stream=None):
+    _check(lib.msa_cache_append_rope(c, p, _addr(q), k.data_ptr(), v.data_ptr(), _addr(q_index), _addr(k_index),
+                                     positions.data_ptr(), slot_map.data_ptr(), _addr(cu_tokens), _addr(chunks),
+                                     _addr(q_out), _addr(q_index_out), cache.data_ptr(), _addr(index_tail),
+                                     _addr(index_pool), d_status.data_ptr(), _raw_stream(stream)),
+           "msa_cache_append_rope")
+
+
+class Rope:
+    """Norm and rotary positions of one attention layer: the norms' weights, the frequencies, and the calls that apply
+    them in training (forward, backward) and in serving (Cache.append_rope).
+
+        rope = Rope(inv_freq, q_weight=wq, k_weight=wk)
+        q, k = rope.forward(positions, q, k)                       # then msa_fwd
+        (dq, dk), (dwq, dwk) = rope.backward(positions, (dq, dk), (q_in, k_in))     # behind msa_bwd
+
+    inv_freq    radians per position of each of the rotary_dim / 2 pairs (rope_frequencies gives the usual ones).
+    axes        position column of each pair, for positions int32 [tokens, axes]; None: positions int32 [tokens].
+    norm        False: rotation only.  index_norm: the same for q_index and k_index.
+    *_weight    bf16 or fp32, [128] for all heads or [heads, 128]; None: a norm without weights.
+    The tensors are bf16 [tokens, heads, 128] whose last dim is contiguous (views of one projection's output will do).
+    Outputs are new tensors of the call's stream, or those given as `out`.  Nothing synchronises; calls keep no state
+    but the problem descriptions, so that one object may serve several streams and captured graphs.
+    """
+
+    NAMES = ("q", "k", "q_index", "k_index")
+
+    def __init__(self, inv_freq, axes=None, q_weight=None, k_weight=None, q_index_weight=None, k_index_weight=None,
+                 norm=True, index_norm=True, adjacent=False, eps=1e-6, weight_offset=0.0, cos_scale=1.0,
+                 device="cuda"):
+        import torch
+        self.device = torch.empty(0, device=device).device
+        self.pairs = rope_pairs(inv_freq, axes, self.device)
+        self.columns = None if axes is None else self.pairs.num_axes
+        self.weights = (q_weight, k_weight, q_index_weight, k_index_weight)
+        self.norms = (norm, norm, index_norm, index_norm)
+        for name, w in zip(self.NAMES, self.weights):
+            if w is not None and w.device != self.device:
+                raise ValueError(f"{name}_weight: need a tensor on {self.device}")
+        self._args = dict(adjacent=adjacent, eps=eps, weight_offset=weight_offset, cos_scale=cos_scale)
+        self._problems = {}
+
+    def _rows(self, name, x, tokens, heads=None):
+        import torch
+        if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16 or x.dim() != 3 or x.shape[0] != tokens \
+                or x.shape[2] != HEAD_DIM or x.device != self.device or (x.numel() and x.stride(2) != 1) \
+                or (heads is not None and x.shape[1] != heads):
+            raise ValueError(f"{name}: need a bf16 tensor of shape ({tokens}, {heads or 'heads'}, {HEAD_DIM}) on "
+                             f"{self.device} whose last dim is contiguous")
+
+    def _positions(self, positions):
+        import torch
+        ok = isinstance(positions, torch.Tensor) and positions.dtype == torch.int32 and positions.is_contiguous() \
+            and positions.device == self.device
+        cols = self.columns
+        if not ok or (positions.dim() != 1 if cols is None else positions.dim() != 2 or positions.shape[1] != cols):
+            raise ValueError(f"positions: need a contiguous int32 tensor of shape "
+                             f"{'(tokens,)' if cols is None else ('tokens', cols)} on {self.device}")
+        return positions.shape[0]
+
+    @staticmethod
+    def _strides(x):
+        # a dim of one row has no stride to speak of
+        T, H, _ = x.shape
+        return (x.stride(0) if T > 1 else H * HEAD_DIM, x.stride(1) if H > 1 else HEAD_DIM)
+
+    def _problem(self, tokens, xs, ys, v=None):
+        """The description of calls with these tensors' shapes and strides."""
+        every = (*xs, v) if v is not None else xs
+        key = (tokens, *((x.shape[1], *self._strides(x), *(self._strides(y) if y is not None else ()))
+                         if x is not None else None for x, y in zip(every, (*ys, None))))
+        p = self._problems.get(key)
+        if p is None:
+            if len(self._problems) >= 64:
+                self._problems.clear()
+            ts = [None if x is None else RopeTensor(x.shape[1], norm, True, w, self._strides(x),
+                                                    None if y is None else self._strides(y))
+                  for x, y, norm, w in zip(xs, ys, self.norms, self.weights)]
+            tv = None if v is None else RopeTensor(v.shape[1], False, False, None, self._strides(v))
+            p = self._problems[key] = make_rope_problem(tokens, self.pairs, *ts, tv, **self._args)
+        return p
+
+    def _given(self, tokens, **named):
+        for name, x in named.items():
+            if x is not None:
+                self._rows(name, x, tokens)
+        return tuple(named.values())
+
+    def _outputs(self, name, out, xs, tokens):
+        import torch
+        if out is None:
+            return tuple(None if x is None else torch.empty(x.shape, dtype=torch.bfloat16, device=self.device)
+                         for x in xs)
+        out = tuple(out)
+        if len(out) != sum(x is not None for x in xs):
+            raise ValueError(f"{name}: {len(out)} tensors, need one for each input")
+        rest = iter(out)
+        out = tuple(None if x is None else next(rest) for x in xs)
+        for what, x, y in zip(self.NAMES, xs, out):
+            if x is not None:
+                self._rows(f"{name} of {what}", y, tokens, x.shape[1])
+        return out
+
+    def forward(self, positions, q=None, k=None, q_index=None, k_index=None, out=None, status=None, stream=None):
+        """msa_norm_rope of the tensors that are given: a tuple of their results, in that order.  out: tensors to
+        write to (the inputs themselves will do).  Rows of padding (a negative first position) are left as they were."""
+        import torch
+        T = self._positions(positions)
+        xs = self._given(T, q=q, k=k, q_index=q_index, k_index=k_index)
+        with torch.cuda.device(self.device), torch.cuda.stream(stream):
+            ys = self._outputs("out", out, xs, T)
+            st = torch.zeros(4, dtype=torch.int32, device=self.device) if status is None else status
+            if T:
+                msa_norm_rope(self._problem(T, xs, ys), xs, positions, ys, st)
+        return tuple(y for y in ys if y is not None)
+
+    def backward(self, positions, grads, inputs, out=None, status=None, stream=None):
+        """msa_norm_rope_bwd: grads and inputs (what forward was given) are q, k, q_index, k_index in order, as many as
+        there are (None: no such tensor).  Returns (gradients of the inputs, gradients of the weights), each a tuple like
+        `inputs`; a weight's is None where there is none.  out: tensors for the inputs' gradients, with the inputs'
+        strides (views of the projection's gradient, where the inputs are views of its output)."""
+        import torch
+        T = self._positions(positions)
+        n = len(inputs)
+        if n > 4 or len(grads) != n or any((g is None) != (x is None) for g, x in zip(grads, inputs)):
+            raise ValueError("grads: need one for each input")
+        pad = (None,) * (4 - n)
+        xs = self._given(T, **dict(zip(self.NAMES, (*inputs, *pad))))
+        dys = (*grads, *pad)
+        for name, g, x in zip(self.NAMES, dys, xs):
+            if g is not None:
+                self._rows(f"gradient of {name}", g, T, x.shape[1])
+        with torch.cuda.device(self.device), torch.cuda.stream(stream):
+            if out is None:
+                dxs = tuple(None if x is None else torch.empty_strided(x.shape, x.stride(), dtype=x.dtype,
+                                                                       device=x.device) for x in xs)
+            else:
+                dxs = self._outputs("out", out, xs, T)
+                for name, dx, x in zip(self.NAMES, dxs, xs):
+                    if x is not None and self._strides(dx) != self._strides(x):
+                        raise ValueError(f"out of {name}: need the input's strides")
+            dws = tuple(None if x is None or w is None else torch.empty_like(w) for x, w in zip(xs, self.weights))
+            st = torch.zeros(4, dtype=torch.int32, device=self.device) if status is None else status
+            if T:
+                p = self._problem(T, xs, dys)
+                ws = torch.empty(msa_norm_rope_bwd_bytes(p), dtype=torch.uint8, device=self.device)
+                msa_norm_rope_bwd(p, dys, xs, positions, dxs, dws, st, ws)
+            else:
+                for dw in dws:
+                    if dw is not None:
+                        dw.zero_()
+        return dxs[:n], dws[:n]
+
+
 class Cache:
     """A batch of requests over one 4-bit paged cache: owns the pages, the free
     ring, the block table, the index pool and the tables of the current step.
@@ -654,6 +927,36 @@ class Cache:
             raise ValueError("k_index: this cache keeps no index keys")
         self._call(msa_cache_append, c, k, v, k_index, self.slot_map, self.cu_tokens, self.chunks, self.cache,
                    self.index_tail, self.index_pool, stream=stream)
+
+    def append_rope(self, rope, q, k, v, q_index=None, k_index=None, positions=None, out=None, stream=None):
+        """msa_cache_append_rope: the step's q, k, v and index vectors as the projections give them (bf16
+        [tokens, heads, 128], views will do), normed and rotated by `rope` (a Rope) on their way.  Returns (q, q_index)
+        for forward and select, new tensors or those given as `out` (q_index None where there is none).  positions:
+        the step's own, or int32 [tokens, axes] where rope has several axes."""
+        import torch
+        t = self._step_tables()
+        c = t["c"]
+        T = c.token_cap
+        if rope.device != self.device:
+            raise ValueError(f"rope: need one on {self.device}")
+        if positions is None:
+            if rope.columns is not None:
+                raise ValueError("positions: a rope with several axes needs them")
+            positions = self.positions
+        if rope._positions(positions) != T:
+            raise ValueError(f"positions: need {T} rows")
+        for name, x, heads in (("q", q, c.num_q_heads), ("k", k, c.num_kv_heads), ("v", v, c.num_kv_heads),
+                               ("q_index", q_index, c.num_kv_heads), ("k_index", k_index, c.num_kv_heads)):
+            if x is not None or name in ("q", "k", "v") or (name == "k_index" and self.index_pool is not None):
+                rope._rows(name, x, T, heads)
+        if self.index_pool is None and k_index is not None:
+            raise ValueError("k_index: this cache keeps no index keys")
+        with torch.cuda.device(self.device), torch.cuda.stream(stream):
+            yq, _, yi, _ = rope._outputs("out", out, (q, None, q_index, None), T)
+            p = rope._problem(T, (q, k, q_index, k_index), (yq, None, yi, None), v)
+            msa_cache_append_rope(c, p, q, k, v, q_index, k_index, positions, self.slot_map, self.cu_tokens,
+                                  self.chunks, yq, yi, self.cache, self.index_tail, self.index_pool, self.status)
+        return yq, yi
 
     def select(self, q_index, stream=None):
         """msa_cache_select: the selection int32 [Hkv, chunk rows, topk] of the step's chunks."""

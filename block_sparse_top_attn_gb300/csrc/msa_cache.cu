@@ -275,143 +275,38 @@ inline int64_t row_blocks(int64_t tokens, int64_t heads, int64_t rows) {  // CTA
   return ((tokens + 3) / 4 * 4 * heads + rows - 1) / rows;
 }
 
-// Clears the sign of the codes that are zero, so that equal values have equal
-// bytes.
-MSA_DEV uint32_t unsigned_zeros(uint32_t w) {
-  const uint32_t m = w & 0x77777777u;
-  return w & (((m << 1 | m << 2 | m << 3) & 0x88888888u) | 0x77777777u);
-}
-
-// One group of 16 bf16 values (8 words) to codes (8 bytes) and an e4m3 scale.
-// Quotients are formed so that the conversions' ties are those of the exact
-// ones: max / 6 with one correction step (exact where the quotient has 24 bits,
-// as every midpoint of two scales does), and x / s as x * (1 / s), which is
-// either a border between two codes (a multiple of 1/4) or at least 2^-11 away
-// from it, because x has 8 significant bits and border * s 7; rounding it to a
-// multiple of 2^-14 (the addition of 1.5 * 2^9) undoes the reciprocal's error.
-MSA_DEV uint32_t quantize16(const uint32_t (&w)[8], float mul, uint2& codes) {
-  codes = make_uint2(0, 0);
-  uint32_t m2 = w[0] & 0x7FFF7FFFu;
-#pragma unroll
-  for (int i = 1; i < 8; ++i) m2 = __vmaxu2(m2, w[i] & 0x7FFF7FFFu);
-  const uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
-  if (m >= 0x7F80u) return 0x7F;  // a NaN scale: the group reads back as NaN
-  // max * mul may overflow to infinity: the scale saturates, and so do the codes
-  const float amax = __uint_as_float(m << 16) * mul;
-  constexpr float kSixth = 1.f / 6.f;
-  const float t0 = amax * kSixth;
-  const float t = amax < 4096.f ? __fmaf_rn(__fmaf_rn(-6.f, t0, amax), kSixth, t0) : t0;  // far above 6 * 448
-  uint16_t s2;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s2) : "f"(0.f), "f"(t));
-  const uint32_t s8 = s2 & 0xFFu;
-  if (s8 == 0) return 0;
-  const float s = __half2float(__ushort_as_half((uint16_t)(e4m3x2_to_half(s8) & 0xFFFFu)));
-  const float inv = __frcp_rn(s) * mul;
-  uint32_t out[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float q[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t x = w[4 * h + i];
-      q[2 * i] = __fadd_rn(__fmaf_rn(__uint_as_float(x << 16), inv, 768.f), -768.f);
-      q[2 * i + 1] = __fadd_rn(__fmaf_rn(__uint_as_float(x & 0xFFFF0000u), inv, 768.f), -768.f);
-    }
-    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
-        "mov.b32 %0, {a, b, c, d};\n\t}"
-        : "=r"(out[h])
-        : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
-  }
-  codes = make_uint2(unsigned_zeros(out[0]), unsigned_zeros(out[1]));
-  return s8;
-}
-
 // Index keys of one chunk, by one CTA: a warp takes half the dims of a head at a
-// time, a lane two dims.
-// The chunk that ends a block averages the block's tokens, those of earlier
-// calls from the tail; a chunk of the request's incomplete block stores its rows
-// to the tail.  Where the incomplete block uses the buffer that the first
-// block's average reads (an even number of blocks apart), the chunk that
-// averages stores them too, after it: a lane reads and writes its own dims
-// only, so the order holds.  The first block's average is made by the
-// request's first chunk, others by the chunk that ends the block.  Most chunks of
-// a prompt have nothing to do.
+// time, a lane two dims, which it alone reads and writes (so that what is averaged
+// before it is overwritten is read before).
 MSA_DEV void index_chunk(const AppendArgs& a, int g) {
-  const int4 c = reinterpret_cast<const int4*>(a.chunks)[g];
-  const int r = c.x, row0 = c.y, n = c.z, pos0 = c.w;
-  if (r < 0) return;
-  int cu0 = 0, cu1 = 0;
-  bool good = r < a.R && n >= 1 && n <= kChunk && row0 >= 0 && row0 <= a.T - n && pos0 >= 0;
-  if (good) {
-    cu0 = a.cu_tokens[r];
-    cu1 = a.cu_tokens[r + 1];
-    good = cu0 >= 0 && cu0 <= row0 && cu1 >= row0 + n && cu1 <= a.T && pos0 >= row0 - cu0 &&
-           pos0 <= a.positions - (cu1 - row0) && pos0 % a.B + n <= a.B;
-  }
-  if (!good) {
-    if (threadIdx.x == 0) set_status(a.status, MSA_ERR_INVALID_CACHE);
-    return;
-  }
-  const int end = pos0 + (cu1 - row0);     // position behind the request's last new token
-  const int past = pos0 - (row0 - cu0);
-  const int blk0 = past / a.B, blk = pos0 / a.B, open = end / a.B;
-  const bool shared_buffer = open > blk0 && (open & 1) == (blk0 & 1) && past % a.B != 0;
-  // the last token's row of the block to average (-1: none), positions to store
-  int last = -1;
-  if (row0 == cu0 && open > blk0) last = cu0 + (blk0 + 1) * a.B - past - 1;
-  else if (row0 != cu0 && blk > blk0 && (pos0 + n) % a.B == 0) last = row0 + n - 1;
-  int p0 = 0, p1 = 0;
-  if (shared_buffer) {
-    if (row0 == cu0) { p0 = open * a.B; p1 = end; }
-  } else if (blk == open) {
-    p0 = pos0;
-    p1 = pos0 + n;
-  }
-  if (last < 0 && p0 >= p1) return;
+  IndexPlan x;
+  if (!plan_index(a, g, x)) return;
   const int64_t hs = (int64_t)a.H * 128;  // elements from one token's row to the next
-  const int avg_blk = row0 == cu0 ? blk0 : blk;
   for (int unit = threadIdx.x >> 5; unit < 2 * a.H; unit += blockDim.x >> 5) {
     const int d = unit * 64 + (threadIdx.x & 31) * 2;
-    uint16_t* tail = a.index_tail + (int64_t)r * 2 * a.B * hs + d;
+    uint16_t* tail = a.index_tail + (int64_t)x.r * 2 * a.B * hs + d;
     auto average = [&] {
-      const int64_t slot = a.slot_map[last];
+      const int64_t slot = a.slot_map[x.last];
       if (slot < 0 || slot >= a.slots) return;  // reported by the rows' own CTAs, or left out
-      const uint16_t* old = tail + (int64_t)(avg_blk & 1) * a.B * hs;
+      const uint16_t* old = tail + (int64_t)(x.avg_blk & 1) * a.B * hs;
       float lo = 0.f, hi = 0.f;
-      auto add = [&](const uint16_t* src, int rows) {  // rows in flight together; the sums keep the tokens' order
-        for (; rows > 0; rows -= 16, src += 16 * hs) {
-          uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = i < rows ? *reinterpret_cast<const uint32_t*>(src + i * hs) : 0u;
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (i < rows) {
-              lo = __fadd_rn(lo, __uint_as_float(w[i] << 16));
-              hi = __fadd_rn(hi, __uint_as_float(w[i] & 0xFFFF0000u));
-            }
-        }
-      };
-      const int olds = max(0, cu0 - (last - (a.B - 1)));  // tokens of earlier calls
-      add(old, olds);
-      add(a.k_index + (int64_t)(last - (a.B - 1) + olds) * hs + d, a.B - olds);
+      const int olds = max(0, x.cu0 - (x.last - (a.B - 1)));  // tokens of earlier calls
+      add_rows(old, hs, olds, lo, hi);
+      add_rows(a.k_index + (int64_t)(x.last - (a.B - 1) + olds) * hs + d, hs, a.B - olds, lo, hi);
       const float inv = 1.f / (float)a.B;  // a power of two: the product is the quotient
       *reinterpret_cast<uint32_t*>(a.index_pool + (slot / a.B) * hs + d) = pack_bf16x2(lo * inv, hi * inv);
     };
-    if (last >= 0) average();
+    if (x.last >= 0) average();
     // the rows of the incomplete block
-    uint16_t* dst = tail + (int64_t)(open & 1) * a.B * hs;
-    for (int q = p0; q < p1; q += kChunk) {
+    uint16_t* dst = tail + (int64_t)(x.open & 1) * a.B * hs;
+    for (int q = x.p0; q < x.p1; q += kChunk) {
       uint32_t w[kChunk];
 #pragma unroll
       for (int i = 0; i < kChunk; ++i)
-        if (q + i < p1) w[i] = *reinterpret_cast<const uint32_t*>(a.k_index + (cu0 + q + i - past) * hs + d);
+        if (q + i < x.p1) w[i] = *reinterpret_cast<const uint32_t*>(a.k_index + (x.cu0 + q + i - x.past) * hs + d);
 #pragma unroll
       for (int i = 0; i < kChunk; ++i)
-        if (q + i < p1) *reinterpret_cast<uint32_t*>(dst + ((q + i) % a.B) * hs) = w[i];
+        if (q + i < x.p1) *reinterpret_cast<uint32_t*>(dst + ((q + i) % a.B) * hs) = w[i];
     }
   }
 }

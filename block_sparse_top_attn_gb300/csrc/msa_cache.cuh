@@ -91,6 +91,131 @@ inline bool aligned32(const void* a, const void* b) {
   return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 31u) == 0;
 }
 
+// Clears the sign of the codes that are zero, so that equal values have equal
+// bytes.
+MSA_DEV uint32_t unsigned_zeros(uint32_t w) {
+  const uint32_t m = w & 0x77777777u;
+  return w & (((m << 1 | m << 2 | m << 3) & 0x88888888u) | 0x77777777u);
+}
+
+// One group of 16 bf16 values (8 words) to codes (8 bytes) and an e4m3 scale.
+// Quotients are formed so that the conversions' ties are those of the exact
+// ones: max / 6 with one correction step (exact where the quotient has 24 bits,
+// as every midpoint of two scales does), and x / s as x * (1 / s), which is
+// either a border between two codes (a multiple of 1/4) or at least 2^-11 away
+// from it, because x has 8 significant bits and border * s 7; rounding it to a
+// multiple of 2^-14 (the addition of 1.5 * 2^9) undoes the reciprocal's error.
+MSA_DEV uint32_t quantize16(const uint32_t (&w)[8], float mul, uint2& codes) {
+  codes = make_uint2(0, 0);
+  uint32_t m2 = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m2 = __vmaxu2(m2, w[i] & 0x7FFF7FFFu);
+  const uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+  if (m >= 0x7F80u) return 0x7F;  // a NaN scale: the group reads back as NaN
+  // max * mul may overflow to infinity: the scale saturates, and so do the codes
+  const float amax = __uint_as_float(m << 16) * mul;
+  constexpr float kSixth = 1.f / 6.f;
+  const float t0 = amax * kSixth;
+  const float t = amax < 4096.f ? __fmaf_rn(__fmaf_rn(-6.f, t0, amax), kSixth, t0) : t0;  // far above 6 * 448
+  uint16_t s2;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s2) : "f"(0.f), "f"(t));
+  const uint32_t s8 = s2 & 0xFFu;
+  if (s8 == 0) return 0;
+  const float s = __half2float(__ushort_as_half((uint16_t)(e4m3x2_to_half(s8) & 0xFFFFu)));
+  const float inv = __frcp_rn(s) * mul;
+  uint32_t out[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = w[4 * h + i];
+      q[2 * i] = __fadd_rn(__fmaf_rn(__uint_as_float(x << 16), inv, 768.f), -768.f);
+      q[2 * i + 1] = __fadd_rn(__fmaf_rn(__uint_as_float(x & 0xFFFF0000u), inv, 768.f), -768.f);
+    }
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(out[h])
+        : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+  }
+  codes = make_uint2(unsigned_zeros(out[0]), unsigned_zeros(out[1]));
+  return s8;
+}
+
+// What a chunk does for the pooled index keys.
+// The chunk that ends a block averages the block's tokens, those of earlier
+// calls from the tail; a chunk of the request's incomplete block stores its rows
+// to the tail.  Where the incomplete block uses the buffer that the first
+// block's average reads (an even number of blocks apart), the chunk that
+// averages stores them too, after it.  The first block's average is made by the
+// request's first chunk, others by the chunk that ends the block.  Most chunks of
+// a prompt have nothing to do.
+struct IndexPlan {
+  int r, cu0, past;  // request, its first token row, its cached tokens
+  int open;          // its incomplete block
+  int last;          // the last token's row of the block to average (-1: none)
+  int avg_blk;       // that block
+  int p0, p1;        // positions to store
+};
+
+// False where the chunk has nothing to do or is not there; every thread of the
+// CTA calls it.
+template <class Args>
+MSA_DEV bool plan_index(const Args& a, int g, IndexPlan& x) {
+  const int4 c = reinterpret_cast<const int4*>(a.chunks)[g];
+  const int r = c.x, row0 = c.y, n = c.z, pos0 = c.w;
+  if (r < 0) return false;
+  int cu0 = 0, cu1 = 0;
+  bool good = r < a.R && n >= 1 && n <= kChunk && row0 >= 0 && row0 <= a.T - n && pos0 >= 0;
+  if (good) {
+    cu0 = a.cu_tokens[r];
+    cu1 = a.cu_tokens[r + 1];
+    good = cu0 >= 0 && cu0 <= row0 && cu1 >= row0 + n && cu1 <= a.T && pos0 >= row0 - cu0 &&
+           pos0 <= a.positions - (cu1 - row0) && pos0 % a.B + n <= a.B;
+  }
+  if (!good) {
+    if (threadIdx.x == 0) set_status(a.status, MSA_ERR_INVALID_CACHE);
+    return false;
+  }
+  const int end = pos0 + (cu1 - row0);     // position behind the request's last new token
+  const int past = pos0 - (row0 - cu0);
+  const int blk0 = past / a.B, blk = pos0 / a.B, open = end / a.B;
+  const bool shared_buffer = open > blk0 && (open & 1) == (blk0 & 1) && past % a.B != 0;
+  x.r = r; x.cu0 = cu0; x.past = past; x.open = open;
+  x.last = -1;
+  if (row0 == cu0 && open > blk0) x.last = cu0 + (blk0 + 1) * a.B - past - 1;
+  else if (row0 != cu0 && blk > blk0 && (pos0 + n) % a.B == 0) x.last = row0 + n - 1;
+  x.avg_blk = row0 == cu0 ? blk0 : blk;
+  x.p0 = x.p1 = 0;
+  if (shared_buffer) {
+    if (row0 == cu0) { x.p0 = open * a.B; x.p1 = end; }
+  } else if (blk == open) {
+    x.p0 = pos0;
+    x.p1 = pos0 + n;
+  }
+  return x.last >= 0 || x.p0 < x.p1;
+}
+
+// Adds rows' two dims (bf16, `stride` elements apart) to lo and hi, in order, 16 in
+// flight.
+MSA_DEV void add_rows(const uint16_t* src, int64_t stride, int rows, float& lo, float& hi) {
+  for (; rows > 0; rows -= 16, src += 16 * stride) {
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = i < rows ? *reinterpret_cast<const uint32_t*>(src + i * stride) : 0u;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < rows) {
+        lo = __fadd_rn(lo, __uint_as_float(w[i] << 16));
+        hi = __fadd_rn(hi, __uint_as_float(w[i] & 0xFFFF0000u));
+      }
+  }
+}
+
 MSA_DEV int64_t tile_index(int64_t page, int head, int heads, int tiles_per_page, int tile) {
   return (page * heads + head) * tiles_per_page + tile;
 }

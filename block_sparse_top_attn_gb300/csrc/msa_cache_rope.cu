@@ -1,0 +1,499 @@
+// Serving: a step's tensors normed, rotated and appended to the 4-bit cache in one
+// launch (msa_rope.cuh has a row's arithmetic, msa_cache.cuh the cache's).
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <initializer_list>
+
+#include "msa_rope.cuh"
+
+namespace msa {
+namespace rope {
+
+constexpr int kIndexRows = kThreads / 8;
+
+struct AppendRopeArgs {
+  RowsArgs q;    // q and q_index: rows in and out
+  Tensor k, ki;  // their `end` is not used
+  const uint16_t* v;
+  int64_t v_token, v_head;
+  const int64_t* slot_map;
+  const int32_t *cu_tokens, *chunks;
+  uint8_t* cache;
+  uint16_t *index_tail, *index_pool;
+  int T, H, B, R, NC;
+  int positions;         // max_blocks * B: a request's most tokens
+  int64_t slots;         // num_pages * B
+  float k_mul, v_mul;    // 2^-exp
+  bool wide;             // rows of v are aligned to 32 bytes
+  int index_blocks, kv_blocks;  // leading CTAs: pooled index keys, then K and V
+  int kv_tile, kv_groups, kv_heads;  // tokens of a tile; groups of heads side by side, heads of a group
+  int32_t* status;
+};
+
+// ---------------------------------------------------------------------------
+// K: codes of the exact value
+// ---------------------------------------------------------------------------
+// The cache keeps a value by the interval it lies in, so an error of fp32 counts
+// only next to a border, and there by a whole code.  With amp = |a cos| + |b sin| and
+// u = 2^-24, fp32 forms y to within 23 u amp: 13.5 u for the normed a and b (the sum
+// of 128 squares in chains of 8 and 4 more additions, halved by the root; rsqrtf 2
+// ulp, two products), 5 u for the angle's function (1 ulp; its argument's rounding
+// and the scale), the products and the sum; the code's quotient adds 2 u.  What lies
+// nearer to a border than 32 u amp is decided in fp64, from the inputs: about one
+// value in 20,000, and a scale in 10,000.
+constexpr float kUlps = 32.f;
+
+struct Row {  // where a K row comes from
+  const uint16_t* x;
+  int64_t w;  // first weight
+  int64_t t;  // token
+};
+
+// 1 / sqrt(mean + eps) of the rows in fp64; whole warps call it.
+MSA_DEV double exact_inverse_rms(uint4 ua, uint4 ub, float eps, bool norm) {
+  float v[16];
+  unpack8(ua, v);
+  unpack8(ub, v + 8);
+  double s = 0.0;
+#pragma unroll 4
+  for (int i = 0; i < 16; ++i) s = fma((double)v[i], (double)v[i], s);
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return norm ? 1.0 / sqrt(s * (1.0 / 128.0) + (double)eps) : 1.0;
+}
+
+// Dim `d` of a K row, normed and rotated, in fp64.
+template <bool kAdjacent>
+__device__ __noinline__ double exact_value(const AppendRopeArgs& a, const Row& row, double r, int d) {
+  auto normed = [&](int i) {
+    double x = (double)__uint_as_float((uint32_t)row.x[i] << 16) * r;
+    if ((a.k.flags & MSA_ROPE_NORM) && a.k.w) {
+      const float w = a.k.flags & MSA_ROPE_WEIGHT_FP32
+                          ? static_cast<const float*>(a.k.w)[row.w + i]
+                          : __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.k.w)[row.w + i] << 16);
+      x *= (double)w + (double)a.q.offset;
+    }
+    return x;
+  };
+  const int R = a.q.an.R;
+  if (!(a.k.flags & MSA_ROPE_ROTATE) || d >= R) return normed(d);
+  const bool second = kAdjacent ? d & 1 : d >= R / 2;
+  const int p = kAdjacent ? d >> 1 : second ? d - R / 2 : d;
+  const int other = kAdjacent ? d ^ 1 : second ? p : d + R / 2;
+  double s, c;
+  sincospi((double)(int64_t)turn_of(a.q.an, p, row.t) * 1.0842021724855044e-19, &s, &c);  // 2^-63: half turns
+  const double x = normed(d), y = normed(other);
+  return (second ? fma(x, c, y * s) : fma(x, c, -(y * s))) * (double)a.q.an.scale;
+}
+
+// e4m3 scale of a group whose largest magnitude (times 2^-exp) is exactly `amax`,
+// found from a scale nearby.
+__device__ __noinline__ uint32_t exact_scale(double amax, uint32_t s8) {
+  auto six_mids = [](uint32_t lo) {  // six times the border between scales lo and lo + 1
+    const uint32_t h = cache::e4m3x2_to_half(lo | (lo + 1) << 8);
+    return 3.0 * ((double)__half2float(__ushort_as_half((uint16_t)(h & 0xFFFFu))) +
+                  (double)__half2float(__ushort_as_half((uint16_t)(h >> 16))));
+  };
+  auto above = [&](uint32_t lo) {  // of lo and lo + 1, the upper one is nearer (a tie goes to the even one)
+    const double m = six_mids(lo);
+    return amax > m || (amax == m && (lo & 1));
+  };
+  while (s8 < 126 && above(s8)) ++s8;
+  while (s8 > 0 && !above(s8 - 1)) --s8;
+  return s8;
+}
+MSA_DEV uint32_t exact_code(double y, double s) {
+  const double m = fabs(y);
+  const uint32_t c = (m > 0.25 * s) + (m >= 0.75 * s) + (m > 1.25 * s) + (m >= 1.75 * s) + (m > 2.5 * s) +
+                     (m >= 3.5 * s) + (m > 5.0 * s);
+  return c && y < 0.0 ? c | 8u : c;
+}
+
+// Half of a scale group: a lane's eight values, its neighbour's the rest.
+struct Half {
+  float amax, amp;  // of the group, amax times 2^-exp
+  uint32_t scale;
+  bool nan, doubt;  // the scale needs fp64
+};
+// Distance of x from the nearest border of a rounding that keeps `kBits` mantissa
+// bits, in units of its last place; below `least` the kept bits are those of `least`.
+template <int kBits>
+MSA_DEV uint32_t border_distance(float x, float least) {
+  const uint32_t z = __float_as_uint(x < least ? x + least : x) & ((1u << (23 - kBits)) - 1u);
+  return __sad((int)z, 1 << (22 - kBits), 0u);
+}
+MSA_DEV Half group_scale(const float* v, float amp, float mul, bool exact) {
+  Half h;
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  h.amp = fmaxf(amp, __shfl_xor_sync(0xffffffffu, amp, 1));
+  h.nan = m >= 0x7F800000u;
+  h.amax = __uint_as_float(m) * mul;
+  constexpr float kSixth = 1.f / 6.f;
+  const float t0 = h.amax * kSixth;
+  const float t = h.amax < 4096.f ? __fmaf_rn(__fmaf_rn(-6.f, t0, h.amax), kSixth, t0) : t0;
+  uint16_t s2;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s2) : "f"(0.f), "f"(t));
+  h.scale = h.nan ? 0x7Fu : s2 & 0xFFu;
+  // relative error of t, in its last places; without a doubt where nothing is rounded
+  const float ulps = fmaf(h.amp * mul / h.amax, kUlps, 4.f);
+  h.doubt = !exact && !h.nan && h.amp > 0.f && t < 450.f && !((float)border_distance<3>(t, 0.015625f) > ulps);
+  return h;
+}
+MSA_DEV float scale_value(uint32_t s8) {
+  return __half2float(__ushort_as_half((uint16_t)(cache::e4m3x2_to_half(s8) & 0xFFFFu)));
+}
+// Codes of eight values; bits of those that need fp64.
+MSA_DEV uint32_t half_codes(const float* v, const Half& h, float mul, bool exact, uint32_t& doubt) {
+  doubt = 0;
+  if (h.nan || h.scale == 0) return 0;
+  const float inv = __frcp_rn(scale_value(h.scale)) * mul;
+  const uint32_t ulps = (uint32_t)fminf(fmaf(h.amp * inv, kUlps / 2.f, 3.f), 4194304.f);
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    q[i] = v[i] * inv;
+    if (exact) q[i] = __fadd_rn(__fmaf_rn(v[i], inv, 768.f), -768.f);  // quantize16's rule
+    else doubt |= (uint32_t)(border_distance<1>(fabsf(q[i]), 1.f) <= ulps) << i;
+  }
+  uint32_t out;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(out)
+      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+  return cache::unsigned_zeros(out);
+}
+
+// K and V of a tile of tokens and a group of heads.
+template <bool kAdjacent>
+MSA_DEV void kv_block(const AppendRopeArgs& a, int block, Table<kTile>& tab) {
+  const int tid = threadIdx.x, lane = tid & 31, j = lane & 7;
+  const int tile = block / a.kv_groups, group = block - tile * a.kv_groups;
+  const int64_t t0 = (int64_t)tile * a.kv_tile;
+  const int n = (int)min((int64_t)a.kv_tile, a.T - t0);
+  const int h0 = group * a.kv_heads, hn = min(a.kv_heads, a.H - h0);
+  fill_table<kAdjacent>(tab, a.q.an, t0, n);
+  __syncthreads();
+  const bool norm = a.k.flags & MSA_ROPE_NORM, turn = a.k.flags & MSA_ROPE_ROTATE;
+  const bool exact = !norm && (!turn || j >= a.q.an.R >> 4);  // the lane's values are its inputs
+  int da, db;
+  lane_dims(j, a.q.an.R, da, db);
+  const int shift = 31 - __clz(a.kv_tile);
+  // four tokens of a head side by side in a warp: their cache rows follow one another
+  for (int base = (tid >> 5) * 4; base < hn << shift; base += kThreads / 8) {
+    const int u = base + (lane >> 3), i = u & (a.kv_tile - 1), hs = u >> shift, h = h0 + hs;
+    const int64_t t = t0 + i;
+    bool live = i < n && hs < hn;
+    int64_t slot = -1;
+    if (live) {
+      slot = a.slot_map[t];
+      const bool padding = a.q.an.positions[t * a.q.an.A] < 0;
+      if (slot < 0 || slot >= a.slots || padding) {
+        if (slot != -1) set_status(a.status, MSA_ERR_INVALID_CACHE);
+        live = false;
+      }
+    }
+    uint4 ua = make_uint4(0, 0, 0, 0), ub = ua;
+    uint32_t vw[8] = {};
+    const Row row{a.k.x + t * a.k.x_token + h * a.k.x_head, a.k.flags & MSA_ROPE_PER_HEAD ? h * 128 : 0, t};
+    if (live) {
+      ua = *reinterpret_cast<const uint4*>(row.x + da);
+      ub = *reinterpret_cast<const uint4*>(row.x + db);
+      cache::load32(a.v + t * a.v_token + h * a.v_head + 16 * j, a.wide, vw);
+    }
+    float v[16], w[16];
+    unpack8(ua, v);
+    unpack8(ub, v + 8);
+    load_weights(a.k, live ? h : 0, da, db, a.q.offset, w);
+    float4 cs[4];
+    load_angles(tab.cs[turn && live ? i : kTile], j, cs);
+    {
+      float scale;
+      const float sum = row_sum(squares(v));
+      const float inv = inverse_rms(v, norm ? sum : 0.f, a.q.eps, scale);
+      const float r = norm ? inv : 1.f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = v[e] * r * w[e];
+    }
+    float amp[2] = {0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float c = fabsf(e & 1 ? cs[e >> 1].z : cs[e >> 1].x), s = fabsf(e & 1 ? cs[e >> 1].w : cs[e >> 1].y);
+      const float x = fabsf(v[kAdjacent ? 2 * e : e]), y = fabsf(v[kAdjacent ? 2 * e + 1 : e + 8]);
+      const float first = fmaf(x, c, y * s), second = fmaf(y, c, x * s);
+      amp[kAdjacent ? e >> 2 : 0] = fmaxf(amp[kAdjacent ? e >> 2 : 0], first);
+      amp[kAdjacent ? e >> 2 : 1] = fmaxf(amp[kAdjacent ? e >> 2 : 1], second);
+    }
+    rotate<kAdjacent, false>(v, cs);
+    Half half[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) half[s] = group_scale(v + 8 * s, amp[s], a.k_mul, exact);
+    double r64 = 0.0;
+    bool have = false;
+    if (__any_sync(0xffffffffu, half[0].doubt || half[1].doubt)) {
+      r64 = exact_inverse_rms(ua, ub, a.q.eps, norm);
+      have = true;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const Half& x = half[s];
+        // the largest is among those within twice the error of it
+        const float least = x.amax - 2.f * kUlps * 5.9604644775390625e-8f * x.amp * a.k_mul;
+        uint32_t left = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) left |= (uint32_t)!(fabsf(v[8 * s + e]) * a.k_mul < least) << e;
+        double m = 0.0;
+        for (left = x.doubt && live ? left : 0; left; left &= left - 1)
+          m = fmax(m, fabs(exact_value<kAdjacent>(a, row, r64, (s ? db : da) + __ffs(left) - 1)));
+        m = fmax(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        if (x.doubt && live) half[s].scale = exact_scale(m * (double)a.k_mul, x.scale);
+      }
+    }
+    uint32_t codes[2], doubt[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) codes[s] = half_codes(v + 8 * s, half[s], a.k_mul, exact, doubt[s]);
+    if (__any_sync(0xffffffffu, doubt[0] | doubt[1])) {
+      if (!have) r64 = exact_inverse_rms(ua, ub, a.q.eps, norm);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        for (uint32_t left = live ? doubt[s] : 0; left; left &= left - 1) {
+          const int e = __ffs(left) - 1;
+          const double y = exact_value<kAdjacent>(a, row, r64, (s ? db : da) + e);
+          const uint32_t c = exact_code(y * (double)a.k_mul, (double)scale_value(half[s].scale));
+          codes[s] = (codes[s] & ~(15u << 4 * e)) | c << 4 * e;
+        }
+    }
+    if (!live) continue;
+    uint2 vc;
+    const uint32_t vs = cache::quantize16(vw, a.v_mul, vc);
+    const int lb = a.B == 128 ? 7 : 6;  // log2 of the block
+    const int off = (int)(slot & (a.B - 1)), tok = off % cache::kTile;
+    uint8_t* out = a.cache + cache::tile_index(slot >> lb, h, a.H, a.B / cache::kTile, off / cache::kTile) *
+                                 cache::kTileBytes;
+    *reinterpret_cast<uint32_t*>(out + cache::OFF_KC + tok * cache::kRowBytes + (da >> 1)) = codes[0];
+    *reinterpret_cast<uint32_t*>(out + cache::OFF_KC + tok * cache::kRowBytes + (db >> 1)) = codes[1];
+    // of the two lanes of a group, one stores the first granules' scale, one the second's
+    out[cache::OFF_KS + tok * cache::kScales + ((j & 1 ? db : da) >> 4)] =
+        (uint8_t)(j & 1 ? half[1].scale : half[0].scale);
+    *reinterpret_cast<uint2*>(out + cache::OFF_VC + cache::v_code_offset(tok, j)) = vc;
+    out[cache::OFF_VS + j * cache::kTile + tok] = (uint8_t)vs;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// index keys
+// ---------------------------------------------------------------------------
+struct IndexShared {
+  Table<kIndexRows> tab;
+  uint4 rows[kIndexRows][16];  // bf16, normed and rotated
+};
+
+// Index keys of one chunk, by one CTA: up to eight heads at a time, 32 rows of
+// them (four tokens of eight heads, 32 tokens of one) per pass.  What is averaged
+// goes through shared memory and is added in the order of the tokens, so that the
+// mean does not depend on how a prompt was cut.
+template <bool kAdjacent>
+MSA_DEV void index_block(const AppendRopeArgs& a, int g, IndexShared& s) {
+  cache::IndexPlan x;
+  if (!cache::plan_index(a, g, x)) return;
+  const int tid = threadIdx.x, j = tid & 7;
+  const int64_t hs = (int64_t)a.H * 128;
+  const bool norm = a.ki.flags & MSA_ROPE_NORM, turn = a.ki.flags & MSA_ROPE_ROTATE;
+  int da, db;
+  lane_dims(j, a.q.an.R, da, db);
+  const int64_t slot = x.last >= 0 ? a.slot_map[x.last] : -1;
+  const bool average = slot >= 0 && slot < a.slots;  // else reported by the rows' own CTAs, or left out
+  const int olds = average ? max(0, x.cu0 - (x.last - (a.B - 1))) : 0;  // tokens of earlier calls
+  for (int h0 = 0; h0 < a.H; h0 += 8) {
+    const int hn = min(8, a.H - h0);
+    const int hb = hn > 4 ? 8 : hn > 2 ? 4 : hn;  // rows of a token
+    const int tb = kIndexRows / hb;
+    const int hsub = (tid >> 3) & (hb - 1), tsub = (tid >> 3) / hb;
+    const bool there = hsub < hn;
+    const int h = h0 + (there ? hsub : 0);
+    float w[16];
+    load_weights(a.ki, h, da, db, a.q.offset, w);
+    const uint16_t* src = a.ki.x + h * a.ki.x_head;
+    // tokens t .. t + n - 1 (n <= tb): this thread's part of its row
+    auto rows = [&](int64_t t, int n, uint4& oa, uint4& ob) {
+      uint4 ua = make_uint4(0, 0, 0, 0), ub = ua;
+      if (there && tsub < n) {
+        ua = *reinterpret_cast<const uint4*>(src + (t + tsub) * a.ki.x_token + da);
+        ub = *reinterpret_cast<const uint4*>(src + (t + tsub) * a.ki.x_token + db);
+      }
+      fill_table<kAdjacent>(s.tab, a.q.an, t, n);
+      __syncthreads();
+      float v[16];
+      unpack8(ua, v);
+      unpack8(ub, v + 8);
+      float4 cs[4];
+      load_angles(s.tab.cs[turn && tsub < n ? tsub : kIndexRows], j, cs);
+      norm_rotate<kAdjacent>(v, w, cs, norm, a.q.eps);
+      oa = pack8(v);
+      ob = pack8(v + 8);
+    };
+    uint16_t* tail = a.index_tail + (int64_t)x.r * 2 * a.B * hs + h0 * 128;
+    if (average) {
+      // a thread adds two dims at a time of up to two words
+      float lo[2] = {0.f, 0.f}, hi[2] = {0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int word = tid + i * kThreads;
+        if (word < hn * 64)
+          cache::add_rows(tail + (int64_t)(x.avg_blk & 1) * a.B * hs + 2 * word, hs, olds, lo[i], hi[i]);
+      }
+      const int64_t first = x.last - (a.B - 1) + olds;
+      for (int m = 0; m < a.B - olds; m += tb) {
+        const int n = min(tb, a.B - olds - m);
+        uint4 oa, ob;
+        rows(first + m, n, oa, ob);
+        s.rows[tid >> 3][da >> 3] = oa;
+        s.rows[tid >> 3][db >> 3] = ob;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int word = tid + i * kThreads;
+          if (word < hn * 64)
+            for (int k = 0; k < n; ++k) {
+              const uint32_t u = reinterpret_cast<const uint32_t*>(s.rows[k * hb + (word >> 6)])[word & 63];
+              lo[i] = __fadd_rn(lo[i], __uint_as_float(u << 16));
+              hi[i] = __fadd_rn(hi[i], __uint_as_float(u & 0xFFFF0000u));
+            }
+        }
+      }
+      const float inv = 1.f / (float)a.B;  // a power of two: the product is the quotient
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int word = tid + i * kThreads;
+        if (word < hn * 64)
+          *reinterpret_cast<uint32_t*>(a.index_pool + (slot / a.B) * hs + h0 * 128 + 2 * word) =
+              pack_bf16x2(lo[i] * inv, hi[i] * inv);
+      }
+    }
+    // the rows of the incomplete block, behind the barrier in rows() that follows the tail's last reads
+    uint16_t* dst = tail + (int64_t)(x.open & 1) * a.B * hs + hsub * 128;
+    for (int q = x.p0; q < x.p1; q += tb) {
+      const int n = min(tb, x.p1 - q);
+      uint4 oa, ob;
+      rows(x.cu0 + q - x.past, n, oa, ob);
+      if (there && tsub < n) {
+        uint16_t* row = dst + ((q + tsub) % a.B) * hs;
+        *reinterpret_cast<uint4*>(row + da) = oa;
+        *reinterpret_cast<uint4*>(row + db) = ob;
+      }
+      __syncthreads();  // the table has been read
+    }
+    __syncthreads();
+  }
+}
+
+template <bool kAdjacent>
+__global__ void __launch_bounds__(kThreads) append_rope_kernel(AppendRopeArgs a) {
+  __shared__ union {
+    Table<kTile> tab;
+    IndexShared index;
+  } s;
+  cache::after_previous_kernel();
+  if (status_bad(a.status)) return;
+  int block = blockIdx.x;
+  if (block < a.index_blocks) {
+    index_block<kAdjacent>(a, block, s.index);
+    return;
+  }
+  block -= a.index_blocks;
+  if (block < a.kv_blocks) kv_block<kAdjacent>(a, block, s.tab);
+  else rows_block<kAdjacent>(a.q, block - a.kv_blocks, s.tab);
+}
+
+}  // namespace rope
+}  // namespace msa
+
+using namespace msa;
+
+extern "C" int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_problem* p, const uint16_t* q,
+                                     const uint16_t* k, const uint16_t* v, const uint16_t* q_index,
+                                     const uint16_t* k_index, const int32_t* positions, const int64_t* slot_map,
+                                     const int32_t* cu_tokens, const int32_t* chunks, uint16_t* q_out,
+                                     uint16_t* q_index_out, uint8_t* kv_cache, uint16_t* index_tail,
+                                     uint16_t* index_pool, int32_t* d_status, void* stream) {
+  int rc = cache::check_cache_problem(c);
+  if (rc || (rc = rope::check_problem(p))) return rc;
+  const msa_rope_tensor* t = p->tensor;
+  const int H = c->num_kv_heads;
+  if (p->tokens != c->token_cap || t[MSA_ROPE_K].heads != H || t[MSA_ROPE_V].heads != H || t[MSA_ROPE_V].flags ||
+      (t[MSA_ROPE_Q].heads && t[MSA_ROPE_Q].heads != c->num_q_heads) ||
+      (t[MSA_ROPE_Q_INDEX].heads && t[MSA_ROPE_Q_INDEX].heads != H) ||
+      (t[MSA_ROPE_K_INDEX].heads && t[MSA_ROPE_K_INDEX].heads != H))
+    return MSA_ERR_INVALID_ARGUMENT;
+  auto bad = [](std::initializer_list<const void*> ptrs) {
+    for (const void* x : ptrs)
+      if (!x || !aligned16(x)) return true;
+    return false;
+  };
+  const bool index = t[MSA_ROPE_K_INDEX].heads > 0;
+  if (bad({k, v, positions, slot_map, kv_cache, d_status})) return MSA_ERR_INVALID_ARGUMENT;
+  if (t[MSA_ROPE_Q].heads && bad({q, q_out})) return MSA_ERR_INVALID_ARGUMENT;
+  if (t[MSA_ROPE_Q_INDEX].heads && bad({q_index, q_index_out})) return MSA_ERR_INVALID_ARGUMENT;
+  if (index && bad({k_index, cu_tokens, chunks, index_tail, index_pool})) return MSA_ERR_INVALID_ARGUMENT;
+  if ((rc = check_device_current())) return rc;
+  int32_t sms = 0;
+  if ((rc = sm_count_current(&sms))) return rc;
+  rope::AppendRopeArgs a{};
+  auto tensor = [&](int i, const uint16_t* x, int end) {
+    return rope::Tensor{t[i].heads ? x : nullptr, t[i].weight, t[i].x_token, t[i].x_head, t[i].flags, end};
+  };
+  a.T = p->tokens; a.H = H; a.B = c->block_size; a.R = c->num_requests; a.NC = c->chunk_cap;
+  // q and index q as two of the row kernel's tensors, the others empty
+  const int nq = t[MSA_ROPE_Q].heads, ni = t[MSA_ROPE_Q_INDEX].heads;
+  a.q.t[0] = tensor(MSA_ROPE_Q, q, nq);
+  a.q.t[1] = tensor(MSA_ROPE_Q_INDEX, q_index, nq + ni);
+  a.q.t[2] = a.q.t[3] = a.q.t[1];
+  const int role[2] = {MSA_ROPE_Q, MSA_ROPE_Q_INDEX};
+  for (int i = 0; i < 2; ++i) {
+    a.q.y_token[i] = t[role[i]].y_token;
+    a.q.y_head[i] = t[role[i]].y_head;
+  }
+  a.q.y[0] = q_out;
+  a.q.y[1] = q_index_out;
+  a.q.an = rope::angles_of(p, positions, d_status);
+  a.q.eps = p->eps;
+  a.q.offset = p->weight_offset;
+  a.q.T = a.T;
+  a.q.heads = nq + ni;
+  a.q.status = a.status = d_status;
+  int64_t q_blocks = 0;
+  if (a.q.heads) {
+    const rope::Cut cut = rope::cut_heads(a.q.heads);
+    a.q.groups = cut.groups; a.q.units = cut.units; a.q.phases = cut.phases;
+    a.q.tile = rope::cut_tokens(a.T, cut.groups, sms, rope::kTile, 1);
+    q_blocks = (int64_t)((a.T + a.q.tile - 1) / a.q.tile) * cut.groups;
+  }
+  a.k = tensor(MSA_ROPE_K, k, 0);
+  a.ki = tensor(MSA_ROPE_K_INDEX, k_index, 0);
+  a.v = v;
+  a.v_token = t[MSA_ROPE_V].x_token;
+  a.v_head = t[MSA_ROPE_V].x_head;
+  a.wide = cache::aligned32(v, nullptr) && a.v_token % 16 == 0 && a.v_head % 16 == 0;
+  a.slot_map = slot_map; a.cu_tokens = cu_tokens; a.chunks = chunks;
+  a.cache = kv_cache; a.index_tail = index_tail; a.index_pool = index_pool;
+  a.positions = c->max_blocks * c->block_size;
+  a.slots = (int64_t)c->num_pages * c->block_size;
+  a.k_mul = cache::exp2i(-c->k_exp);
+  a.v_mul = cache::exp2i(-c->v_exp);
+  a.kv_groups = (H + 7) / 8;
+  a.kv_heads = (H + a.kv_groups - 1) / a.kv_groups;
+  a.kv_tile = rope::cut_tokens(a.T, a.kv_groups, sms, rope::kTile, 4);
+  const int64_t kv_blocks = (int64_t)((a.T + a.kv_tile - 1) / a.kv_tile) * a.kv_groups;
+  const int64_t index_blocks = index ? c->chunk_cap : 0;
+  if (index_blocks + kv_blocks + q_blocks > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
+  a.index_blocks = (int)index_blocks;
+  a.kv_blocks = (int)kv_blocks;
+  return cache::launch_kernel(p->adjacent ? rope::append_rope_kernel<true> : rope::append_rope_kernel<false>,
+                              dim3((unsigned)(index_blocks + kv_blocks + q_blocks)), rope::kThreads, 0, stream, 1, a);
+}

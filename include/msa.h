@@ -509,6 +509,133 @@ int msa_cache_fwd(const msa_cache_problem* p, const uint16_t* q, const uint8_t* 
                   const int32_t* block_table, const int32_t* chunks, const int32_t* sel, uint16_t* o,
                   float* lse, int32_t* d_status, void* stream);
 
+/* -------------------------------------------------------------------------
+ * Norm and rotary positions of queries, keys and index vectors: what lies
+ * between the projections and msa_select_topk / msa_fwd / msa_cache_append, and
+ * its gradients behind msa_bwd.  (The pages start from tensors that have both;
+ * these calls have no counterpart there.)
+ *
+ * Every head (128 dims) of every token of a tensor is normed (MSA_ROPE_NORM),
+ *   n = x * (w + weight_offset) / sqrt(mean(x^2) + eps),
+ * and its first R = rotary_dim dims are rotated (MSA_ROPE_ROTATE): pair p of
+ * R / 2 is dims (p, p + R / 2), or (2p, 2p + 1) where `adjacent` is set, and
+ *   (a, b) -> cos_scale * (a cos t - b sin t, b cos t + a sin t)
+ * with t = 2 pi * turns[p] / 2^64 * position[axis[p]]: each pair follows one of a
+ * token's num_axes positions (one for text; time, height and width of images and
+ * video).  Angles are formed in 64-bit fixed point, so that they are as exact at
+ * position 2^31 as at 1.  All else is fp32, rounded to bf16 once.
+ *
+ * The tensors of one call share a launch and their tokens' angles.  x and y may
+ * be strided (parts of one projection's output), with strides in elements.
+ * ------------------------------------------------------------------------- */
+enum { MSA_ROPE_Q = 0, MSA_ROPE_K = 1, MSA_ROPE_Q_INDEX = 2, MSA_ROPE_K_INDEX = 3, MSA_ROPE_V = 4, MSA_ROPE_TENSORS = 5 };
+enum { MSA_ROPE_NORM = 1, MSA_ROPE_ROTATE = 2, MSA_ROPE_PER_HEAD = 4, MSA_ROPE_WEIGHT_FP32 = 8 };
+
+/* heads     of this tensor; 0: the call has no such tensor.
+ * flags     MSA_ROPE_NORM, MSA_ROPE_ROTATE; MSA_ROPE_PER_HEAD: a weight per head
+ *           ([heads, 128], else [128]); MSA_ROPE_WEIGHT_FP32: the weight (and
+ *           its gradient) is fp32, else bf16.
+ * weight    device, or NULL for a norm without one (w + weight_offset is then 1).
+ * x_token, x_head, y_token, y_head  elements from one token's row, and one head's,
+ *           to the next: positive multiples of 8 that keep the rows apart. */
+typedef struct {
+  int32_t heads;
+  uint32_t flags;
+  const void* weight;
+  int64_t x_token, x_head, y_token, y_head;
+} msa_rope_tensor;
+
+/* One pair: turns per position in units of 2^-64, and the position's column. */
+typedef struct {
+  uint64_t turns;
+  int32_t axis;
+  int32_t reserved;
+} msa_rope_pair;
+
+/* tokens        rows of every tensor, 0 .. 2^24.
+ * head_dim      128.
+ * rotary_dim    R: 32, 64, 96 or 128 (0 if no tensor is rotated).
+ * num_axes      columns of the positions, 1 .. 4.
+ * eps           2^-100 .. 2^100.
+ * cos_scale     > 0 and finite; 1 but for stretched contexts.
+ * pairs         device [R / 2], written from msa_rope_pairs' output.  An axis out
+ *               of range counts as 0 and sets MSA_ERR_INVALID_ARGUMENT. */
+typedef struct {
+  int32_t tokens;
+  int32_t head_dim;
+  int32_t rotary_dim;
+  int32_t num_axes;
+  int32_t adjacent;
+  float eps;
+  float weight_offset;
+  float cos_scale;
+  const msa_rope_pair* pairs;
+  msa_rope_tensor tensor[MSA_ROPE_TENSORS];
+} msa_rope_problem;
+
+/* Fills pairs[0 .. num_pairs) on the host from angular frequencies (radians per
+ * position, as rotary tables give them) and position columns (NULL: 0). */
+int msa_rope_pairs(const double* inv_freq, const int32_t* axes, int32_t num_pairs, msa_rope_pair* pairs);
+
+/* The forward.
+ * x, y       host arrays of four device pointers (MSA_ROPE_Q .. MSA_ROPE_K_INDEX; p's
+ *            V tensor is not used): bf16 rows in and out.  Entries of tensors with
+ *            no heads are not looked at.  y may be x itself, with the same strides.
+ * positions  device int32 [tokens, num_axes].  A token whose first position is
+ *            negative is padding: its rows of y are left as they were.  Other
+ *            columns may be negative.
+ * Deterministic; a row's result does not depend on the call's other rows. */
+int msa_norm_rope(const msa_rope_problem* p, const uint16_t* const* x, const int32_t* positions, uint16_t* const* y,
+                  int32_t* d_status, void* stream);
+
+/* Bytes of workspace of msa_norm_rope_bwd (0 if p is invalid; at least 256). */
+size_t msa_norm_rope_bwd_bytes(const msa_rope_problem* p);
+
+/* Its gradients.
+ * dy         bf16, laid out by p's y strides: the gradients of y.
+ * x          the forward's input (not its output: with y = x it is gone).
+ * dx         bf16 out, laid out by p's x strides; may be x itself, or dy itself
+ *            where the strides agree.  Rows of padding are left as they were.
+ * dw         host array of four device pointers, entries NULL where the gradient
+ *            is not wanted or there is no weight: [128] or [heads, 128], in the
+ *            weight's type, summed in fp32 over the tokens that are no padding
+ *            (and over the heads that share it).  Overwritten, not added to.
+ * ws         msa_norm_rope_bwd_bytes(p), overwritten before it is read.
+ * Deterministic. */
+int msa_norm_rope_bwd(const msa_rope_problem* p, const uint16_t* const* dy, const uint16_t* const* x,
+                      const int32_t* positions, uint16_t* const* dx, void* const* dw, int32_t* d_status, void* ws,
+                      size_t ws_bytes, void* stream);
+
+/* msa_cache_append of tensors that are not normed and rotated yet, with all that
+ * a step's other calls need, in one launch:
+ *  - q and q_index normed and rotated to q_out and q_index_out, as msa_norm_rope
+ *    does;
+ *  - K normed, rotated and rounded to 4 bits by msa_cache_append's rule, V rounded
+ *    as it is, both written to the tokens' slots.  K is not rounded to bf16 in
+ *    between: its codes and scales are those of the exact value of y (what lies
+ *    closer to a border than fp32 can tell is computed again in fp64);
+ *  - index keys normed, rotated and rounded to bf16 as msa_norm_rope does, and kept
+ *    by msa_cache_append's rule (index_tail and index_pool hold the same, bit for
+ *    bit, as after the two calls).
+ * p          the tensors of the step: K and V with c's num_kv_heads and V without
+ *            flags; Q with c's num_q_heads or 0 heads (q and q_out are not used
+ *            then); Q_INDEX with num_kv_heads or 0; K_INDEX with num_kv_heads, or
+ *            0 in a call without index keys (its other arguments may be NULL).
+ *            K and V are written to the cache: their y strides, and K_INDEX's, are
+ *            not used.  p.tokens = c.token_cap.
+ * positions  device int32 [T, num_axes]; msa_cache_step's positions where there is
+ *            one axis.  A token whose slot is -1, or whose first position is negative,
+ *            is padding: none of its rows are written (a slot of the cache beside a
+ *            negative first position, or a slot outside it, sets
+ *            MSA_ERR_INVALID_CACHE).  With index keys, the rows that chunks covers
+ *            must not be padding.
+ * Other arguments as for msa_cache_append.  Deterministic where no error is found. */
+int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_problem* p, const uint16_t* q, const uint16_t* k,
+                          const uint16_t* v, const uint16_t* q_index, const uint16_t* k_index,
+                          const int32_t* positions, const int64_t* slot_map, const int32_t* cu_tokens,
+                          const int32_t* chunks, uint16_t* q_out, uint16_t* q_index_out, uint8_t* cache,
+                          uint16_t* index_tail, uint16_t* index_pool, int32_t* d_status, void* stream);
+
 /* Self-test of the bounded device waits (no counterpart in the pages).
  * Launches one small kernel that waits, with the same bounded mbarrier wait
  * every kernel of this library uses, for an mbarrier phase that nothing
