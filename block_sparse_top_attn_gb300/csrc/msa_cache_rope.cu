@@ -181,8 +181,8 @@ MSA_DEV void kv_block(const AppendRopeArgs& a, int block, Table<kTile>& tab) {
   const int h0 = group * a.kv_heads, hn = min(a.kv_heads, a.H - h0);
   fill_table<kAdjacent>(tab, a.q.an, t0, n);
   __syncthreads();
-  const bool norm = a.k.flags & MSA_ROPE_NORM, turn = a.k.flags & MSA_ROPE_ROTATE;
-  const bool exact = !norm && (!turn || j >= a.q.an.R >> 4);  // the lane's values are its inputs
+  const bool norm = a.k.flags & MSA_ROPE_NORM, turn = turns(a.k, j, a.q.an.R);
+  const bool exact = !norm && !turn;  // the lane's values are its inputs
   int da, db;
   lane_dims(j, a.q.an.R, da, db);
   const int shift = 31 - __clz(a.kv_tile);
@@ -212,8 +212,6 @@ MSA_DEV void kv_block(const AppendRopeArgs& a, int block, Table<kTile>& tab) {
     unpack8(ua, v);
     unpack8(ub, v + 8);
     load_weights(a.k, live ? h : 0, da, db, a.q.offset, w);
-    float4 cs[4];
-    load_angles(tab.cs[turn && live ? i : kTile], j, cs);
     {
       float scale;
       const float sum = row_sum(squares(v));
@@ -223,15 +221,22 @@ MSA_DEV void kv_block(const AppendRopeArgs& a, int block, Table<kTile>& tab) {
       for (int e = 0; e < 16; ++e) v[e] = v[e] * r * w[e];
     }
     float amp[2] = {0.f, 0.f};
+    if (turn) {
+      float4 cs[4];
+      load_angles(tab.cs[i], j, cs);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float c = fabsf(e & 1 ? cs[e >> 1].z : cs[e >> 1].x), s = fabsf(e & 1 ? cs[e >> 1].w : cs[e >> 1].y);
-      const float x = fabsf(v[kAdjacent ? 2 * e : e]), y = fabsf(v[kAdjacent ? 2 * e + 1 : e + 8]);
-      const float first = fmaf(x, c, y * s), second = fmaf(y, c, x * s);
-      amp[kAdjacent ? e >> 2 : 0] = fmaxf(amp[kAdjacent ? e >> 2 : 0], first);
-      amp[kAdjacent ? e >> 2 : 1] = fmaxf(amp[kAdjacent ? e >> 2 : 1], second);
+      for (int e = 0; e < 8; ++e) {
+        const float c = fabsf(e & 1 ? cs[e >> 1].z : cs[e >> 1].x), s = fabsf(e & 1 ? cs[e >> 1].w : cs[e >> 1].y);
+        const float x = fabsf(v[kAdjacent ? 2 * e : e]), y = fabsf(v[kAdjacent ? 2 * e + 1 : e + 8]);
+        const float first = fmaf(x, c, y * s), second = fmaf(y, c, x * s);
+        amp[kAdjacent ? e >> 2 : 0] = fmaxf(amp[kAdjacent ? e >> 2 : 0], first);
+        amp[kAdjacent ? e >> 2 : 1] = fmaxf(amp[kAdjacent ? e >> 2 : 1], second);
+      }
+      rotate<kAdjacent, false>(v, cs);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) amp[e >> 3] = fmaxf(amp[e >> 3], fabsf(v[e]));
     }
-    rotate<kAdjacent, false>(v, cs);
     Half half[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) half[s] = group_scale(v + 8 * s, amp[s], a.k_mul, exact);
@@ -304,7 +309,7 @@ MSA_DEV void index_block(const AppendRopeArgs& a, int g, IndexShared& s) {
   if (!cache::plan_index(a, g, x)) return;
   const int tid = threadIdx.x, j = tid & 7;
   const int64_t hs = (int64_t)a.H * 128;
-  const bool norm = a.ki.flags & MSA_ROPE_NORM, turn = a.ki.flags & MSA_ROPE_ROTATE;
+  const bool norm = a.ki.flags & MSA_ROPE_NORM, turn = turns(a.ki, j, a.q.an.R);
   int da, db;
   lane_dims(j, a.q.an.R, da, db);
   const int64_t slot = x.last >= 0 ? a.slot_map[x.last] : -1;
@@ -332,9 +337,7 @@ MSA_DEV void index_block(const AppendRopeArgs& a, int g, IndexShared& s) {
       float v[16];
       unpack8(ua, v);
       unpack8(ub, v + 8);
-      float4 cs[4];
-      load_angles(s.tab.cs[turn && tsub < n ? tsub : kIndexRows], j, cs);
-      norm_rotate<kAdjacent>(v, w, cs, norm, a.q.eps);
+      norm_rotate<kAdjacent>(v, w, s.tab.cs[tsub], j, norm, turn && tsub < n, a.q.eps);
       oa = pack8(v);
       ob = pack8(v + 8);
     };

@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(GradArgs a) {
   lane_dims(j, a.an.R, da, db);
   const int k = tensor_of(a, live ? hh : 0, head);
   const Tensor& t = a.t[k];
-  const bool norm = t.flags & MSA_ROPE_NORM, turn = t.flags & MSA_ROPE_ROTATE;
+  const bool norm = t.flags & MSA_ROPE_NORM, turn = turns(t, j, a.an.R);
   float w[16], dw[16];
   load_weights(t, head, da, db, a.offset, w);
 #pragma unroll
@@ -117,9 +117,11 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(GradArgs a) {
       unpack8(gb, g + 8);
       unpack8(xa, v);
       unpack8(xb, v + 8);
-      float4 cs[4];
-      load_angles(s_tab.cs[turn ? i : kTile], j, cs);
-      rotate<kAdjacent, true>(g, cs);
+      if (turn) {
+        float4 cs[4];
+        load_angles(s_tab.cs[i], j, cs);
+        rotate<kAdjacent, true>(g, cs);
+      }
       float scale;
       const float sum = row_sum(squares(v));
       const float r = inverse_rms(v, norm ? sum : 0.f, a.eps, scale);

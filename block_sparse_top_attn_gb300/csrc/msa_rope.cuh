@@ -39,6 +39,9 @@ struct Tensor {
   int end;  // heads of this tensor and those before it
 };
 
+// Whether lane j's dims of a tensor are rotated.
+MSA_DEV bool turns(const Tensor& t, int j, int R) { return (t.flags & MSA_ROPE_ROTATE) && j < R >> 4; }
+
 // First dims of lane j's granules.
 MSA_DEV void lane_dims(int j, int R, int& a, int& b) {
   const int n = R >> 4;
@@ -83,30 +86,27 @@ MSA_DEV uint64_t turn_of(const Angles& a, int p, int64_t t) {
   return turns * (uint64_t)(int64_t)a.positions[t * a.A + axis];
 }
 
-// Entries 2 * e2 and 2 * e2 + 1 of lane j at a token: (cos, sin, cos, sin).
+// Entries 2 * e2 and 2 * e2 + 1 of lane j < R / 16 at a token: (cos, sin, cos, sin).
 template <bool kAdjacent>
 MSA_DEV float4 entry_pair(const Angles& a, int j, int e2, int64_t t) {
-  float4 x = make_float4(1.f, 0.f, 1.f, 0.f);
-  if (j < a.R >> 4) {
-    cos_sin(turn_of(a, pair_of<kAdjacent>(j, 2 * e2, a.R), t), a.scale, x.x, x.y);
-    cos_sin(turn_of(a, pair_of<kAdjacent>(j, 2 * e2 + 1, a.R), t), a.scale, x.z, x.w);
-  }
+  float4 x;
+  cos_sin(turn_of(a, pair_of<kAdjacent>(j, 2 * e2, a.R), t), a.scale, x.x, x.y);
+  cos_sin(turn_of(a, pair_of<kAdjacent>(j, 2 * e2 + 1, a.R), t), a.scale, x.z, x.w);
   return x;
 }
 
 // A tile's angles in shared memory: a row of [4][8] float4 per token (lane j's
 // entries 2 * e2 .. at [e2][j], so that eight lanes read 128 bytes side by side).
-// Row `rows` is the rotation by nothing, for tensors that are only normed.
+// Lanes j >= R / 16 have none.
 template <int kRows>
 struct Table {
-  float4 cs[kRows + 1][32];
+  float4 cs[kRows][32];
 };
 template <bool kAdjacent, int kRows>
 MSA_DEV void fill_table(Table<kRows>& tab, const Angles& a, int64_t t0, int n) {
-  for (int i = threadIdx.x; i < (n + 1) * 32; i += kThreads) {
+  for (int i = threadIdx.x; i < n * 32; i += kThreads) {
     const int row = i >> 5, e2 = (i >> 3) & 3, j = i & 7;
-    if (row < n) tab.cs[row][i & 31] = entry_pair<kAdjacent>(a, j, e2, t0 + row);
-    else tab.cs[kRows][i & 31] = make_float4(1.f, 0.f, 1.f, 0.f);
+    if (j < a.R >> 4) tab.cs[row][i & 31] = entry_pair<kAdjacent>(a, j, e2, t0 + row);
   }
 }
 MSA_DEV void load_angles(const float4* row, int j, float4 (&cs)[4]) {
@@ -200,16 +200,22 @@ MSA_DEV void rotate(float (&v)[16], const float4 (&cs)[4]) {
   }
 }
 
-// One row: normed if `norm`, then turned.
+// One row: normed if `norm`, then turned by the angles at `row` if `turn` (this
+// lane's dims are: a turn by nothing would carry infinities from pair to pair).
 template <bool kAdjacent>
-MSA_DEV void norm_rotate(float (&v)[16], const float (&w)[16], const float4 (&cs)[4], bool norm, float eps) {
+MSA_DEV void norm_rotate(float (&v)[16], const float (&w)[16], const float4* row, int j, bool norm, bool turn,
+                         float eps) {
   float scale;
   const float sum = row_sum(squares(v));
   const float inv = inverse_rms(v, norm ? sum : 0.f, eps, scale);
   const float r = norm ? inv : 1.f;  // w is 1 without a norm
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = v[i] * r * w[i];
-  rotate<kAdjacent, false>(v, cs);
+  if (turn) {
+    float4 cs[4];
+    load_angles(row, j, cs);
+    rotate<kAdjacent, false>(v, cs);
+  }
 }
 
 // Host side.
@@ -281,7 +287,7 @@ MSA_DEV void rows_block(const RowsArgs& a, int64_t block, Table<kTile>& tab) {
   lane_dims(j, a.an.R, da, db);
   const int k = tensor_of(a, live ? hh : 0, head);
   const Tensor& t = a.t[k];
-  const bool norm = t.flags & MSA_ROPE_NORM, turn = t.flags & MSA_ROPE_ROTATE;
+  const bool norm = t.flags & MSA_ROPE_NORM, turn = turns(t, j, a.an.R);
   float w[16];
   load_weights(t, head, da, db, a.offset, w);
   const uint16_t* x = t.x + t0 * t.x_token + head * t.x_head;
@@ -297,9 +303,7 @@ MSA_DEV void rows_block(const RowsArgs& a, int64_t block, Table<kTile>& tab) {
     float v[16];
     unpack8(ua, v);
     unpack8(ub, v + 8);
-    float4 cs[4];
-    load_angles(tab.cs[turn ? i : kTile], j, cs);
-    norm_rotate<kAdjacent>(v, w, cs, norm, a.eps);
+    norm_rotate<kAdjacent>(v, w, tab.cs[i], j, norm, turn, a.eps);
     if (live && a.an.positions[(t0 + i) * a.an.A] >= 0) {
       *reinterpret_cast<uint4*>(y + i * a.y_token[k] + da) = pack8(v);
       *reinterpret_cast<uint4*>(y + i * a.y_token[k] + db) = pack8(v + 8);
