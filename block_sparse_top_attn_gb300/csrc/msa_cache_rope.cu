@@ -10,7 +10,7 @@
 namespace msa {
 namespace rope {
 
-constexpr int kIndexRows = kThreads / 8;
+constexpr int kIndexRows = kThreads / 8;  // rows of a pass
 
 struct AppendRopeArgs {
   RowsArgs q;    // q and q_index: rows in and out
@@ -51,10 +51,12 @@ struct Row {  // where a K row comes from
 };
 
 // 1 / sqrt(mean + eps) of the rows in fp64; whole warps call it.
+template <bool kAdjacent>
 MSA_DEV double exact_inverse_rms(uint4 ua, uint4 ub, float eps, bool norm) {
+  Values u;
   float v[16];
-  unpack8(ua, v);
-  unpack8(ub, v + 8);
+  unpack<kAdjacent>(ua, ub, u);
+  in_order<kAdjacent>(u, v);
   double s = 0.0;
 #pragma unroll 4
   for (int i = 0; i < 16; ++i) s = fma((double)v[i], (double)v[i], s);
@@ -82,7 +84,7 @@ __device__ __noinline__ double exact_value(const AppendRopeArgs& a, const Row& r
   const int p = kAdjacent ? d >> 1 : second ? d - R / 2 : d;
   const int other = kAdjacent ? d ^ 1 : second ? p : d + R / 2;
   double s, c;
-  sincospi((double)(int64_t)turn_of(a.q.an, p, row.t) * 1.0842021724855044e-19, &s, &c);  // 2^-63: half turns
+  sincospi((double)(int64_t)turn_of(a.q.an, load_pair(a.q.an, p), row.t) * 1.0842021724855044e-19, &s, &c);  // 2^-63: half turns
   const double x = normed(d), y = normed(other);
   return (second ? fma(x, c, y * s) : fma(x, c, -(y * s))) * (double)a.q.an.scale;
 }
@@ -171,6 +173,23 @@ MSA_DEV uint32_t half_codes(const float* v, const Half& h, float mul, bool exact
   return cache::unsigned_zeros(out);
 }
 
+// Largest |a cos| + |b sin| of each granule of a normed row.
+template <bool kAdjacent>
+MSA_DEV void amplitudes(const Values& v, const float4* row, int j, bool turn, float (&amp)[2]) {
+  amp[0] = amp[1] = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 x = turn ? row[i * 8 + j] : make_float4(1.f, 1.f, 0.f, 0.f);
+    float a0, a1, b0, b1;
+    f2_unpack(v.a[i], a0, a1);
+    f2_unpack(v.b[i], b0, b1);
+    const float fa = fmaxf(fmaf(fabsf(a0), fabsf(x.x), fabsf(b0 * x.z)), fmaf(fabsf(a1), fabsf(x.y), fabsf(b1 * x.w)));
+    const float fb = fmaxf(fmaf(fabsf(b0), fabsf(x.x), fabsf(a0 * x.z)), fmaf(fabsf(b1), fabsf(x.y), fabsf(a1 * x.w)));
+    amp[kAdjacent ? i >> 1 : 0] = fmaxf(amp[kAdjacent ? i >> 1 : 0], fa);
+    amp[kAdjacent ? i >> 1 : 1] = fmaxf(amp[kAdjacent ? i >> 1 : 1], fb);
+  }
+}
+
 // K and V of a tile of tokens and a group of heads.
 template <bool kAdjacent>
 MSA_DEV void kv_block(const AppendRopeArgs& a, int block, Table<kTile>& tab) {
@@ -179,7 +198,8 @@ MSA_DEV void kv_block(const AppendRopeArgs& a, int block, Table<kTile>& tab) {
   const int64_t t0 = (int64_t)tile * a.kv_tile;
   const int n = (int)min((int64_t)a.kv_tile, a.T - t0);
   const int h0 = group * a.kv_heads, hn = min(a.kv_heads, a.H - h0);
-  fill_table<kAdjacent>(tab, a.q.an, t0, n);
+  const Filler<kAdjacent> filler(a.q.an);
+  filler.fill(tab, a.q.an, t0, n);
   __syncthreads();
   const bool norm = a.k.flags & MSA_ROPE_NORM, turn = turns(a.k, j, a.q.an.R);
   const bool exact = !norm && !turn;  // the lane's values are its inputs
@@ -208,42 +228,21 @@ MSA_DEV void kv_block(const AppendRopeArgs& a, int block, Table<kTile>& tab) {
       ub = *reinterpret_cast<const uint4*>(row.x + db);
       cache::load32(a.v + t * a.v_token + h * a.v_head + 16 * j, a.wide, vw);
     }
-    float v[16], w[16];
-    unpack8(ua, v);
-    unpack8(ub, v + 8);
-    load_weights(a.k, live ? h : 0, da, db, a.q.offset, w);
-    {
-      float scale;
-      const float sum = row_sum(squares(v));
-      const float inv = inverse_rms(v, norm ? sum : 0.f, a.q.eps, scale);
-      const float r = norm ? inv : 1.f;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = v[e] * r * w[e];
-    }
-    float amp[2] = {0.f, 0.f};
-    if (turn) {
-      float4 cs[4];
-      load_angles(tab.cs[i], j, cs);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float c = fabsf(e & 1 ? cs[e >> 1].z : cs[e >> 1].x), s = fabsf(e & 1 ? cs[e >> 1].w : cs[e >> 1].y);
-        const float x = fabsf(v[kAdjacent ? 2 * e : e]), y = fabsf(v[kAdjacent ? 2 * e + 1 : e + 8]);
-        const float first = fmaf(x, c, y * s), second = fmaf(y, c, x * s);
-        amp[kAdjacent ? e >> 2 : 0] = fmaxf(amp[kAdjacent ? e >> 2 : 0], first);
-        amp[kAdjacent ? e >> 2 : 1] = fmaxf(amp[kAdjacent ? e >> 2 : 1], second);
-      }
-      rotate<kAdjacent, false>(v, cs);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) amp[e >> 3] = fmaxf(amp[e >> 3], fabsf(v[e]));
-    }
+    Values val, w;
+    unpack<kAdjacent>(ua, ub, val);
+    load_weights<kAdjacent>(a.k, live ? h : 0, da, db, a.q.offset, w);
+    normalize(val, w, norm, a.q.eps);
+    float amp[2], v[16];
+    amplitudes<kAdjacent>(val, tab.cs[i], j, turn, amp);
+    if (turn) rotate<false>(val, tab.cs[i], j);
+    in_order<kAdjacent>(val, v);
     Half half[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) half[s] = group_scale(v + 8 * s, amp[s], a.k_mul, exact);
     double r64 = 0.0;
     bool have = false;
     if (__any_sync(0xffffffffu, half[0].doubt || half[1].doubt)) {
-      r64 = exact_inverse_rms(ua, ub, a.q.eps, norm);
+      r64 = exact_inverse_rms<kAdjacent>(ua, ub, a.q.eps, norm);
       have = true;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
@@ -264,7 +263,7 @@ MSA_DEV void kv_block(const AppendRopeArgs& a, int block, Table<kTile>& tab) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) codes[s] = half_codes(v + 8 * s, half[s], a.k_mul, exact, doubt[s]);
     if (__any_sync(0xffffffffu, doubt[0] | doubt[1])) {
-      if (!have) r64 = exact_inverse_rms(ua, ub, a.q.eps, norm);
+      if (!have) r64 = exact_inverse_rms<kAdjacent>(ua, ub, a.q.eps, norm);
 #pragma unroll
       for (int s = 0; s < 2; ++s)
         for (uint32_t left = live ? doubt[s] : 0; left; left &= left - 1) {
@@ -312,6 +311,7 @@ MSA_DEV void index_block(const AppendRopeArgs& a, int g, IndexShared& s) {
   const bool norm = a.ki.flags & MSA_ROPE_NORM, turn = turns(a.ki, j, a.q.an.R);
   int da, db;
   lane_dims(j, a.q.an.R, da, db);
+  const Filler<kAdjacent> filler(a.q.an);
   const int64_t slot = x.last >= 0 ? a.slot_map[x.last] : -1;
   const bool average = slot >= 0 && slot < a.slots;  // else reported by the rows' own CTAs, or left out
   const int olds = average ? max(0, x.cu0 - (x.last - (a.B - 1))) : 0;  // tokens of earlier calls
@@ -322,8 +322,8 @@ MSA_DEV void index_block(const AppendRopeArgs& a, int g, IndexShared& s) {
     const int hsub = (tid >> 3) & (hb - 1), tsub = (tid >> 3) / hb;
     const bool there = hsub < hn;
     const int h = h0 + (there ? hsub : 0);
-    float w[16];
-    load_weights(a.ki, h, da, db, a.q.offset, w);
+    Values w;
+    load_weights<kAdjacent>(a.ki, h, da, db, a.q.offset, w);
     const uint16_t* src = a.ki.x + h * a.ki.x_head;
     // tokens t .. t + n - 1 (n <= tb): this thread's part of its row
     auto rows = [&](int64_t t, int n, uint4& oa, uint4& ob) {
@@ -332,14 +332,12 @@ MSA_DEV void index_block(const AppendRopeArgs& a, int g, IndexShared& s) {
         ua = *reinterpret_cast<const uint4*>(src + (t + tsub) * a.ki.x_token + da);
         ub = *reinterpret_cast<const uint4*>(src + (t + tsub) * a.ki.x_token + db);
       }
-      fill_table<kAdjacent>(s.tab, a.q.an, t, n);
+      filler.fill(s.tab, a.q.an, t, n);
       __syncthreads();
-      float v[16];
-      unpack8(ua, v);
-      unpack8(ub, v + 8);
-      norm_rotate<kAdjacent>(v, w, s.tab.cs[tsub], j, norm, turn && tsub < n, a.q.eps);
-      oa = pack8(v);
-      ob = pack8(v + 8);
+      Values v;
+      unpack<kAdjacent>(ua, ub, v);
+      norm_rotate(v, w, s.tab.cs[tsub], j, norm, turn && tsub < n, a.q.eps);
+      pack<kAdjacent>(v, oa, ob);
     };
     uint16_t* tail = a.index_tail + (int64_t)x.r * 2 * a.B * hs + h0 * 128;
     if (average) {
@@ -396,22 +394,21 @@ MSA_DEV void index_block(const AppendRopeArgs& a, int g, IndexShared& s) {
   }
 }
 
+constexpr int kAppendCtas = 2;  // of an SM
+static_assert(sizeof(IndexShared) <= sizeof(RowsShared), "one size for every CTA");
 template <bool kAdjacent>
-__global__ void __launch_bounds__(kThreads) append_rope_kernel(AppendRopeArgs a) {
-  __shared__ union {
-    Table<kTile> tab;
-    IndexShared index;
-  } s;
+__global__ void __launch_bounds__(kThreads, kAppendCtas) append_rope_kernel(AppendRopeArgs a) {
+  extern __shared__ __align__(16) uint8_t s_raw[];
   cache::after_previous_kernel();
   if (status_bad(a.status)) return;
   int block = blockIdx.x;
   if (block < a.index_blocks) {
-    index_block<kAdjacent>(a, block, s.index);
+    index_block<kAdjacent>(a, block, *reinterpret_cast<IndexShared*>(s_raw));
     return;
   }
   block -= a.index_blocks;
-  if (block < a.kv_blocks) kv_block<kAdjacent>(a, block, s.tab);
-  else rows_block<kAdjacent>(a.q, block - a.kv_blocks, s.tab);
+  if (block < a.kv_blocks) kv_block<kAdjacent>(a, block, *reinterpret_cast<Table<kTile>*>(s_raw));
+  else rows_block<kAdjacent>(a.q, block - a.kv_blocks, *reinterpret_cast<RowsShared*>(s_raw));
 }
 
 }  // namespace rope
@@ -472,10 +469,8 @@ extern "C" int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_
   a.q.status = a.status = d_status;
   int64_t q_blocks = 0;
   if (a.q.heads) {
-    const rope::Cut cut = rope::cut_heads(a.q.heads);
-    a.q.groups = cut.groups; a.q.units = cut.units; a.q.phases = cut.phases;
-    a.q.tile = rope::cut_tokens(a.T, cut.groups, sms, rope::kTile, 1);
-    q_blocks = (int64_t)((a.T + a.q.tile - 1) / a.q.tile) * cut.groups;
+    a.q.cut = rope::cut_rows(a.q.heads, a.T, (int64_t)rope::kAppendCtas * sms);
+    q_blocks = (int64_t)a.q.cut.slices * a.q.cut.groups;
   }
   a.k = tensor(MSA_ROPE_K, k, 0);
   a.ki = tensor(MSA_ROPE_K_INDEX, k_index, 0);
@@ -498,5 +493,6 @@ extern "C" int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_
   a.index_blocks = (int)index_blocks;
   a.kv_blocks = (int)kv_blocks;
   return cache::launch_kernel(p->adjacent ? rope::append_rope_kernel<true> : rope::append_rope_kernel<false>,
-                              dim3((unsigned)(index_blocks + kv_blocks + q_blocks)), rope::kThreads, 0, stream, 1, a);
+                              dim3((unsigned)(index_blocks + kv_blocks + q_blocks)), rope::kThreads,
+                              sizeof(rope::RowsShared), stream, 1, a);
 }

@@ -42,12 +42,13 @@ int check_problem(const msa_rope_problem* p) {
   return MSA_OK;
 }
 
+constexpr int kRowCtas = 4;  // of an SM
 template <bool kAdjacent>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(RowsArgs a) {
-  __shared__ Table<kTile> s_tab;
+__global__ void __launch_bounds__(kThreads, kRowCtas) norm_rope_kernel(RowsArgs a) {
+  extern __shared__ __align__(16) uint8_t s_raw[];
   cache::after_previous_kernel();
   if (status_bad(a.status)) return;
-  rows_block<kAdjacent>(a, blockIdx.x, s_tab);
+  rows_block<kAdjacent>(a, blockIdx.x, *reinterpret_cast<RowsShared*>(s_raw));
 }
 
 // ---------------------------------------------------------------------------
@@ -68,111 +69,143 @@ struct GradArgs {
   int first[kTensors];  // group that the tensor's first head is in
   Angles an;
   float eps, offset;
-  int T, heads;
-  int tile, tiles, slices, groups, units, phases, slots;
+  int T, heads, slots;
+  Cut cut;
   float* partial;  // [slices][slots][128]
   int32_t* status;
 };
 
+constexpr int kGradStages = 3, kGradCtas = 2;
+struct GradShared {
+  Table<kTile> tab[2];
+  union {
+    uint4 ring[kWarps][kGradStages][4][32];  // x and dy
+    float dw[kThreads / 8][128];
+  };
+};
+
 template <bool kAdjacent>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(GradArgs a) {
-  __shared__ Table<kTile> s_tab;
-  __shared__ float s_dw[kThreads / 8][128];
+__global__ void __launch_bounds__(kThreads, kGradCtas) norm_rope_bwd_kernel(GradArgs a) {
+  extern __shared__ __align__(16) uint8_t s_raw[];
+  GradShared& s = *reinterpret_cast<GradShared*>(s_raw);
   cache::after_previous_kernel();
   if (status_bad(a.status)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, j = lane & 7;
-  const int slice = blockIdx.x / a.groups, group = blockIdx.x - slice * a.groups;
-  const int phase = warp / a.units, unit = group * a.units + warp - phase * a.units;
+  const int slice = blockIdx.x / a.cut.groups, group = blockIdx.x - slice * a.cut.groups;
+  const int64_t t0 = (int64_t)a.T * slice / a.cut.slices;
+  const int n = (int)((int64_t)a.T * (slice + 1) / a.cut.slices - t0);
+  const int phase = warp / a.cut.units, unit = group * a.cut.units + warp - phase * a.cut.units;
   const int hh = unit * 4 + (lane >> 3);
-  const bool live = hh < a.heads && phase < a.phases;
+  const bool mine = phase < a.cut.phases, live = mine && hh < a.heads;
   int da, db, head;
   lane_dims(j, a.an.R, da, db);
   const int k = tensor_of(a, live ? hh : 0, head);
   const Tensor& t = a.t[k];
-  const bool norm = t.flags & MSA_ROPE_NORM, turn = turns(t, j, a.an.R);
-  float w[16], dw[16];
-  load_weights(t, head, da, db, a.offset, w);
+  const int64_t x0 = t0 * t.x_token + head * t.x_head, x_token = t.x_token, y_token = a.y_token[k];
+  const uint16_t *x = t.x + x0, *dy = a.dy[k] + t0 * y_token + head * a.y_head[k];
+  uint16_t* dx = a.dx[k] + x0;
+  const int phases = a.cut.phases;
+  auto copy = [&](int i, int stage) {
+    if (live && i < n) {
+      copy16(&s.ring[warp][stage][0][lane], x + i * x_token + da);
+      copy16(&s.ring[warp][stage][1][lane], x + i * x_token + db);
+      copy16(&s.ring[warp][stage][2][lane], dy + i * y_token + da);
+      copy16(&s.ring[warp][stage][3][lane], dy + i * y_token + db);
+    }
+    copies_commit();
+  };
 #pragma unroll
-  for (int i = 0; i < 16; ++i) dw[i] = 0.f;
-  for (int tile = slice; tile < a.tiles; tile += a.slices) {
-    const int64_t t0 = (int64_t)tile * a.tile;
-    const int n = (int)min((int64_t)a.tile, a.T - t0);
-    __syncthreads();  // the tile before has been read
-    fill_table<kAdjacent>(s_tab, a.an, t0, n);
-    __syncthreads();
-    const int64_t x0 = t0 * t.x_token + head * t.x_head, y0 = t0 * a.y_token[k] + head * a.y_head[k];
-    for (int i = phase; i < n && phase < a.phases; i += a.phases) {
-      const bool here = live && a.an.positions[(t0 + i) * a.an.A] >= 0;
-      uint4 xa = make_uint4(0, 0, 0, 0), xb = xa, ga = xa, gb = xa;
-      if (here) {
-        const uint16_t* x = t.x + x0 + i * t.x_token;
-        const uint16_t* dy = a.dy[k] + y0 + i * a.y_token[k];
-        xa = *reinterpret_cast<const uint4*>(x + da);
-        xb = *reinterpret_cast<const uint4*>(x + db);
-        ga = *reinterpret_cast<const uint4*>(dy + da);
-        gb = *reinterpret_cast<const uint4*>(dy + db);
-      }
-      float g[16], v[16];
-      unpack8(ga, g);
-      unpack8(gb, g + 8);
-      unpack8(xa, v);
-      unpack8(xb, v + 8);
-      if (turn) {
-        float4 cs[4];
-        load_angles(s_tab.cs[i], j, cs);
-        rotate<kAdjacent, true>(g, cs);
-      }
+  for (int i = 0; i < kGradStages - 1; ++i) copy(phase + i * phases, i);
+  const bool norm = t.flags & MSA_ROPE_NORM, turn = turns(t, j, a.an.R);
+  const Filler<kAdjacent> filler(a.an);
+  Values w, dw;
+  load_weights<kAdjacent>(t, head, da, db, a.offset, w);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) dw.a[i] = dw.b[i] = 0;
+  filler.fill(s.tab[0], a.an, t0, min(n, kTile));
+  __syncthreads();
+  int stage = 0, i = phase;
+  for (int at = 0, buf = 0; at < n; at += kTile, buf ^= 1) {
+    const int end = min(at + kTile, n);
+    if (end < n) filler.fill(s.tab[buf ^ 1], a.an, t0 + end, min(n - end, kTile));
+    for (; i < end && mine; i += phases) {
+      copies_wait<kGradStages - 2>();
+      // rows of padding count as zeros: they may hold anything
+      const bool here = live && s.tab[buf].live[i - at];
+      uint4 u[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) u[c] = here ? s.ring[warp][stage][c][lane] : make_uint4(0, 0, 0, 0);
+      Values v, g;
+      unpack<kAdjacent>(u[0], u[1], v);
+      unpack<kAdjacent>(u[2], u[3], g);
+      copy(i + (kGradStages - 1) * phases, (stage + kGradStages - 1) % kGradStages);
+      stage = (stage + 1) % kGradStages;
+      if (turn) rotate<true>(g, s.tab[buf].cs[i - at], j);
       float scale;
       const float sum = row_sum(squares(v));
       const float r = inverse_rms(v, norm ? sum : 0.f, a.eps, scale);
-      float dot = 0.f;
+      times(v, r);  // the normed row without its weight
+      uint64_t dot = 0;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        v[e] *= r;  // the normed row without its weight
-        if (norm) dw[e] = fmaf(g[e], v[e], dw[e]);
-        g[e] *= w[e];
-        dot = fmaf(g[e], v[e], dot);
+      for (int e = 0; e < 4; ++e) {
+        if (norm) {
+          dw.a[e] = f2_fma(g.a[e], v.a[e], dw.a[e]);
+          dw.b[e] = f2_fma(g.b[e], v.b[e], dw.b[e]);
+        }
+        g.a[e] = f2_mul(g.a[e], w.a[e]);
+        g.b[e] = f2_mul(g.b[e], w.b[e]);
+        dot = f2_fma(g.a[e], v.a[e], dot);
+        dot = f2_fma(g.b[e], v.b[e], dot);
       }
-      const float mean = row_sum(dot) * (1.f / 128.f);
+      float lo, hi;
+      f2_unpack(dot, lo, hi);
+      const float mean = row_sum(lo + hi) * (-1.f / 128.f);
       if (norm) {
-        const float rr = r * scale;
+        const uint64_t m = f2_pack(mean, mean);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) g[e] = rr * fmaf(-v[e], mean, g[e]);
+        for (int e = 0; e < 4; ++e) {
+          g.a[e] = f2_fma(v.a[e], m, g.a[e]);
+          g.b[e] = f2_fma(v.b[e], m, g.b[e]);
+        }
+        times(g, r * scale);
       }
+      pack<kAdjacent>(g, u[0], u[1]);
       if (here) {
-        uint16_t* dx = a.dx[k] + x0 + i * t.x_token;
-        *reinterpret_cast<uint4*>(dx + da) = pack8(g);
-        *reinterpret_cast<uint4*>(dx + db) = pack8(g + 8);
+        *reinterpret_cast<uint4*>(dx + i * x_token + da) = u[0];
+        *reinterpret_cast<uint4*>(dx + i * x_token + db) = u[1];
       }
     }
+    __syncthreads();
   }
   // the CTA's sums: heads that share a weight in the order of the warps and rows
-  float* mine = s_dw[tid >> 3];
+  float* row = s.dw[tid >> 3];
+  float sums[16];
+  in_order<kAdjacent>(dw, sums);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    mine[da + i] = live ? dw[i] : 0.f;
-    mine[db + i] = live ? dw[8 + i] : 0.f;
+    row[da + i] = live ? sums[i] : 0.f;
+    row[db + i] = live ? sums[8 + i] : 0.f;
   }
   __syncthreads();
-  const int d = tid & 127;
+  const int d = tid & 127, units = a.cut.units;
   float* out = a.partial + (int64_t)slice * a.slots * 128 + d;
   for (int i = 0, before = 0; i < kTensors; ++i) {
     const int end = a.t[i].end;
     if (a.slot[i] >= 0) {
       // this CTA's heads of the tensor, and its rows (of the warps' first phase)
-      const int lo = max(before, group * a.units * 4), hi = min(end, (group + 1) * a.units * 4);
-      const int row0 = lo - group * a.units * 4, rows = hi - lo;
+      const int lo = max(before, group * units * 4), hi = min(end, (group + 1) * units * 4);
+      const int row0 = lo - group * units * 4, rows = hi - lo;
       if (a.t[i].flags & MSA_ROPE_PER_HEAD) {
         for (int r = tid >> 7; r < rows; r += 2) {
-          float s = 0.f;
-          for (int p = 0; p < a.phases; ++p) s += s_dw[p * a.units * 4 + row0 + r][d];
-          out[(int64_t)(a.slot[i] + lo - before + r) * 128] = s;
+          float s1 = 0.f;
+          for (int p = 0; p < phases; ++p) s1 += s.dw[p * units * 4 + row0 + r][d];
+          out[(int64_t)(a.slot[i] + lo - before + r) * 128] = s1;
         }
       } else if (rows > 0 && tid < 128) {
-        float s = 0.f;
-        for (int p = 0; p < a.phases; ++p)
-          for (int r = 0; r < rows; ++r) s += s_dw[p * a.units * 4 + row0 + r][d];
-        out[(int64_t)(a.slot[i] + group - a.first[i]) * 128] = s;
+        float s1 = 0.f;
+        for (int p = 0; p < phases; ++p)
+          for (int r = 0; r < rows; ++r) s1 += s.dw[p * units * 4 + row0 + r][d];
+        out[(int64_t)(a.slot[i] + group - a.first[i]) * 128] = s1;
       }
     }
     before = end;
@@ -219,20 +252,14 @@ __global__ void __launch_bounds__(128 * kSumParts) weight_sum_kernel(SumArgs a) 
 // alone: the workspace's size and the order of the sums do.
 struct GradCut {
   Cut c;
-  int heads, tile, tiles, slices, slots;
+  int heads, slots;
   int slot[kTensors], first[kTensors], per[kTensors];
 };
-constexpr int kGradCtas = 2 * 152;
 static GradCut cut_grad(const msa_rope_problem* p) {
   GradCut g{};
   for (int i = 0; i < kTensors; ++i) g.heads += p->tensor[i].heads;
   if (g.heads == 0) return g;
-  g.c = cut_heads(g.heads);
-  g.tile = cut_tokens(p->tokens, g.c.groups, 152, kTile, 1);
-  if (g.tile < g.c.phases) g.tile = g.c.phases;
-  g.tiles = (p->tokens + g.tile - 1) / g.tile;
-  const int want = (kGradCtas + g.c.groups - 1) / g.c.groups;
-  g.slices = g.tiles < want ? g.tiles : want;
+  g.c = cut_rows(g.heads, p->tokens, kGradCtas * 152);
   int at = 0;
   for (int i = 0; i < kTensors; ++i) {
     const msa_rope_tensor& t = p->tensor[i];
@@ -311,22 +338,19 @@ int msa_norm_rope(const msa_rope_problem* p, const uint16_t* const* x, const int
   a.eps = p->eps;
   a.offset = p->weight_offset;
   a.T = p->tokens;
-  const rope::Cut c = rope::cut_heads(a.heads);
-  a.groups = c.groups; a.units = c.units; a.phases = c.phases;
   int32_t sms = 0;
   if ((rc = sm_count_current(&sms))) return rc;
-  a.tile = rope::cut_tokens(a.T, a.groups, sms, rope::kTile, 1);
+  a.cut = rope::cut_rows(a.heads, a.T, (int64_t)rope::kRowCtas * sms);
   a.status = d_status;
-  const int64_t ctas = (int64_t)((a.T + a.tile - 1) / a.tile) * a.groups;
-  if (ctas > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
   return cache::launch_kernel(p->adjacent ? rope::norm_rope_kernel<true> : rope::norm_rope_kernel<false>,
-                              dim3((unsigned)ctas), rope::kThreads, 0, stream, 1, a);
+                              dim3((unsigned)(a.cut.slices * a.cut.groups)), rope::kThreads, sizeof(rope::RowsShared),
+                              stream, 1, a);
 }
 
 size_t msa_norm_rope_bwd_bytes(const msa_rope_problem* p) {
   if (rope::check_problem(p)) return 0;
   const rope::GradCut g = rope::cut_grad(p);
-  return round_up((size_t)g.slices * g.slots * 512 + 256, 256);
+  return round_up((size_t)g.c.slices * g.slots * 512 + 256, 256);
 }
 
 int msa_norm_rope_bwd(const msa_rope_problem* p, const uint16_t* const* dy, const uint16_t* const* x,
@@ -366,7 +390,7 @@ int msa_norm_rope_bwd(const msa_rope_problem* p, const uint16_t* const* dy, cons
     a.first[i] = g.first[i];
   }
   s.partial = static_cast<const float*>(ws);
-  s.slices = g.slices;
+  s.slices = g.c.slices;
   s.slots = g.slots;
   s.status = d_status;
   if (p->tokens) {
@@ -375,12 +399,13 @@ int msa_norm_rope_bwd(const msa_rope_problem* p, const uint16_t* const* dy, cons
     a.offset = p->weight_offset;
     a.T = p->tokens;
     a.heads = g.heads;
-    a.tile = g.tile; a.tiles = g.tiles; a.slices = g.slices; a.slots = g.slots;
-    a.groups = g.c.groups; a.units = g.c.units; a.phases = g.c.phases;
+    a.slots = g.slots;
+    a.cut = g.c;
     a.partial = static_cast<float*>(ws);
     a.status = d_status;
     rc = cache::launch_kernel(p->adjacent ? rope::norm_rope_bwd_kernel<true> : rope::norm_rope_bwd_kernel<false>,
-                              dim3((unsigned)(g.slices * g.c.groups)), rope::kThreads, 0, stream, 1, a);
+                              dim3((unsigned)(g.c.slices * g.c.groups)), rope::kThreads, sizeof(rope::GradShared),
+                              stream, 1, a);
     if (rc) return rc;
   }
   if (rows == 0) return MSA_OK;

@@ -77,76 +77,133 @@ MSA_DEV int pair_of(int j, int e, int R) {
   else return 8 * j + e;
 }
 
-// Fraction of a turn of pair p at token t.
-MSA_DEV uint64_t turn_of(const Angles& a, int p, int64_t t) {
+// Turns per position of pair p, and its position column.
+struct Pair {
+  uint64_t turns;
+  int axis;
+};
+MSA_DEV Pair load_pair(const Angles& a, int p) {
   const int4 w = reinterpret_cast<const int4*>(a.pairs)[p];
-  const uint64_t turns = (uint64_t)(uint32_t)w.y << 32 | (uint32_t)w.x;
-  const int axis = (unsigned)w.z < (unsigned)a.A ? w.z : 0;
-  if (axis != w.z) set_status(a.status, MSA_ERR_INVALID_ARGUMENT);
-  return turns * (uint64_t)(int64_t)a.positions[t * a.A + axis];
-}
-
-// Entries 2 * e2 and 2 * e2 + 1 of lane j < R / 16 at a token: (cos, sin, cos, sin).
-template <bool kAdjacent>
-MSA_DEV float4 entry_pair(const Angles& a, int j, int e2, int64_t t) {
-  float4 x;
-  cos_sin(turn_of(a, pair_of<kAdjacent>(j, 2 * e2, a.R), t), a.scale, x.x, x.y);
-  cos_sin(turn_of(a, pair_of<kAdjacent>(j, 2 * e2 + 1, a.R), t), a.scale, x.z, x.w);
+  Pair x;
+  x.turns = (uint64_t)(uint32_t)w.y << 32 | (uint32_t)w.x;
+  x.axis = (unsigned)w.z < (unsigned)a.A ? w.z : 0;
+  if (x.axis != w.z) set_status(a.status, MSA_ERR_INVALID_ARGUMENT);
   return x;
 }
+// Fraction of a turn at token t.
+MSA_DEV uint64_t turn_of(const Angles& a, const Pair& p, int64_t t) {
+  return p.turns * (uint64_t)(int64_t)a.positions[t * a.A + p.axis];
+}
 
-// A tile's angles in shared memory: a row of [4][8] float4 per token (lane j's
-// entries 2 * e2 .. at [e2][j], so that eight lanes read 128 bytes side by side).
-// Lanes j >= R / 16 have none.
+// A tile's angles in shared memory: a row of [4][8] float4 per token, lane j's
+// entries 2 * e2 and 2 * e2 + 1 at [e2][j] as (cos, cos, sin, sin): eight lanes read
+// 128 bytes side by side, and two entries are one operand of the packed
+// arithmetic.  Lanes j >= R / 16 have none.
 template <int kRows>
 struct Table {
   float4 cs[kRows][32];
+  int live[kRows];  // the token is no padding
 };
-template <bool kAdjacent, int kRows>
-MSA_DEV void fill_table(Table<kRows>& tab, const Angles& a, int64_t t0, int n) {
-  for (int i = threadIdx.x; i < n * 32; i += kThreads) {
-    const int row = i >> 5, e2 = (i >> 3) & 3, j = i & 7;
-    if (j < a.R >> 4) tab.cs[row][i & 31] = entry_pair<kAdjacent>(a, j, e2, t0 + row);
+// Fills tables: a thread has the same two pairs in every row.
+template <bool kAdjacent>
+struct Filler {
+  Pair p0, p1;
+  MSA_DEV Filler(const Angles& a) {
+    const int e2 = (threadIdx.x >> 3) & 3, j = threadIdx.x & 7;
+    p0 = p1 = Pair{0, 0};
+    if (j < a.R >> 4) {
+      p0 = load_pair(a, pair_of<kAdjacent>(j, 2 * e2, a.R));
+      p1 = load_pair(a, pair_of<kAdjacent>(j, 2 * e2 + 1, a.R));
+    }
+  }
+  template <int kRows>
+  MSA_DEV void fill(Table<kRows>& tab, const Angles& a, int64_t t0, int n) const {
+    const int at = threadIdx.x & 31;
+    for (int row = threadIdx.x >> 5; row < n; row += kWarps) {
+      if ((at & 7) < a.R >> 4) {
+        float4 x;
+        cos_sin(turn_of(a, p0, t0 + row), a.scale, x.x, x.z);
+        cos_sin(turn_of(a, p1, t0 + row), a.scale, x.y, x.w);
+        tab.cs[row][at] = x;
+      }
+      if (at == 31) tab.live[row] = a.positions[(t0 + row) * a.A] >= 0;
+    }
+  }
+};
+
+// A lane's 16 values as its eight pairs (a, b), two pairs a word: dims (p, p + R / 2)
+// come from its two granules, dims (2p, 2p + 1) from the halves of its words.
+struct Values {
+  uint64_t a[4], b[4];
+};
+template <bool kAdjacent>
+MSA_DEV void unpack(uint4 ua, uint4 ub, Values& v) {
+  const uint32_t w[8] = {ua.x, ua.y, ua.z, ua.w, ub.x, ub.y, ub.z, ub.w};
+  auto lo = [&](int i) { return __uint_as_float(w[i] << 16); };
+  auto hi = [&](int i) { return __uint_as_float(w[i] & 0xFFFF0000u); };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v.a[i] = kAdjacent ? f2_pack(lo(2 * i), lo(2 * i + 1)) : f2_pack(lo(i), hi(i));
+    v.b[i] = kAdjacent ? f2_pack(hi(2 * i), hi(2 * i + 1)) : f2_pack(lo(4 + i), hi(4 + i));
   }
 }
-MSA_DEV void load_angles(const float4* row, int j, float4 (&cs)[4]) {
+// The values in the order of the granules' dims.
+template <bool kAdjacent>
+MSA_DEV void in_order(const Values& v, float (&x)[16]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) cs[i] = row[i * 8 + j];
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kAdjacent) {
+      f2_unpack(v.a[i], x[4 * i], x[4 * i + 2]);
+      f2_unpack(v.b[i], x[4 * i + 1], x[4 * i + 3]);
+    } else {
+      f2_unpack(v.a[i], x[2 * i], x[2 * i + 1]);
+      f2_unpack(v.b[i], x[8 + 2 * i], x[8 + 2 * i + 1]);
+    }
+  }
 }
-
-MSA_DEV void unpack8(uint4 u, float* v) {
-  v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xFFFF0000u);
-  v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xFFFF0000u);
-  v[4] = __uint_as_float(u.z << 16); v[5] = __uint_as_float(u.z & 0xFFFF0000u);
-  v[6] = __uint_as_float(u.w << 16); v[7] = __uint_as_float(u.w & 0xFFFF0000u);
+template <bool kAdjacent>
+MSA_DEV void from_order(const float (&x)[16], Values& v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v.a[i] = kAdjacent ? f2_pack(x[4 * i], x[4 * i + 2]) : f2_pack(x[2 * i], x[2 * i + 1]);
+    v.b[i] = kAdjacent ? f2_pack(x[4 * i + 1], x[4 * i + 3]) : f2_pack(x[8 + 2 * i], x[8 + 2 * i + 1]);
+  }
 }
-MSA_DEV uint4 pack8(const float* v) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                    pack_bf16x2(v[6], v[7]));
+template <bool kAdjacent>
+MSA_DEV void pack(const Values& v, uint4& ua, uint4& ub) {
+  float x[16];
+  in_order<kAdjacent>(v, x);
+  ua = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  ub = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]), pack_bf16x2(x[12], x[13]),
+                  pack_bf16x2(x[14], x[15]));
 }
 
 // A lane's 16 weights of a head, the offset added; 1 where there are none.
-MSA_DEV void load_weights(const Tensor& t, int head, int a, int b, float offset, float (&w)[16]) {
+template <bool kAdjacent>
+MSA_DEV void load_weights(const Tensor& t, int head, int a, int b, float offset, Values& w) {
+  float x[16];
   if (!(t.flags & MSA_ROPE_NORM) || !t.w) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = 1.f;
-    return;
-  }
-  const int64_t at = t.flags & MSA_ROPE_PER_HEAD ? (int64_t)head * 128 : 0;
-  if (t.flags & MSA_ROPE_WEIGHT_FP32) {
-    const float* p = static_cast<const float*>(t.w) + at;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 u = *reinterpret_cast<const float4*>(p + (i < 2 ? a : b) + 4 * (i & 1));
-      w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
-    }
+    for (int i = 0; i < 16; ++i) x[i] = 1.f;
   } else {
-    const uint16_t* p = static_cast<const uint16_t*>(t.w) + at;
-    unpack8(*reinterpret_cast<const uint4*>(p + a), w);
-    unpack8(*reinterpret_cast<const uint4*>(p + b), w + 8);
-  }
+    const int64_t at = t.flags & MSA_ROPE_PER_HEAD ? (int64_t)head * 128 : 0;
+    if (t.flags & MSA_ROPE_WEIGHT_FP32) {
+      const float* p = static_cast<const float*>(t.w) + at;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) w[i] += offset;
+      for (int i = 0; i < 4; ++i) {
+        const float4 u = *reinterpret_cast<const float4*>(p + (i < 2 ? a : b) + 4 * (i & 1));
+        x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = u.z; x[4 * i + 3] = u.w;
+      }
+    } else {
+      const uint16_t* p = static_cast<const uint16_t*>(t.w) + at;
+      Values u;
+      unpack<kAdjacent>(*reinterpret_cast<const uint4*>(p + a), *reinterpret_cast<const uint4*>(p + b), u);
+      in_order<kAdjacent>(u, x);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] += offset;
+  }
+  from_order<kAdjacent>(x, w);
 }
 
 // Sum over the eight lanes of a row; all of them get it.
@@ -155,21 +212,38 @@ MSA_DEV float row_sum(float x) {
   for (int o = 1; o < 8; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
-MSA_DEV float squares(const float (&v)[16]) {
-  float s0 = 0.f, s1 = 0.f;
+MSA_DEV float squares(const Values& v) {
+  uint64_t s = f2_mul(v.a[0], v.a[0]), t = f2_mul(v.b[0], v.b[0]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    s0 = fmaf(v[i], v[i], s0);
-    s1 = fmaf(v[8 + i], v[8 + i], s1);
+  for (int i = 1; i < 4; ++i) {
+    s = f2_fma(v.a[i], v.a[i], s);
+    t = f2_fma(v.b[i], v.b[i], t);
   }
-  return s0 + s1;
+  float lo, hi;
+  f2_unpack(f2_add(s, t), lo, hi);
+  return lo + hi;
+}
+MSA_DEV void times(Values& v, float x) {
+  const uint64_t xx = f2_pack(x, x);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v.a[i] = f2_mul(v.a[i], xx);
+    v.b[i] = f2_mul(v.b[i], xx);
+  }
+}
+MSA_DEV void times(Values& v, const Values& w) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v.a[i] = f2_mul(v.a[i], w.a[i]);
+    v.b[i] = f2_mul(v.b[i], w.b[i]);
+  }
 }
 
 // 1 / sqrt(mean + eps) of a row's sum of squares.  Rows whose squares leave fp32's
 // range (elements above 10^18) are scaled by 2^-64 first, where eps does not count.
 // Whole warps call this; v holds the row times `scale` after it (v * result is the
 // normed row either way).
-MSA_DEV float inverse_rms(float (&v)[16], float sum, float eps, float& scale) {
+MSA_DEV float inverse_rms(Values& v, float sum, float eps, float& scale) {
   scale = 1.f;
   if (__any_sync(0xffffffffu, !(sum < kInf))) {
     const bool far = !(sum < kInf);
@@ -177,45 +251,40 @@ MSA_DEV float inverse_rms(float (&v)[16], float sum, float eps, float& scale) {
       scale = 5.421010862427522e-20f;  // 2^-64
       eps = 0.f;
     }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] *= scale;
+    times(v, scale);
     const float again = row_sum(squares(v));
     if (far) sum = again;
   }
   return rsqrtf(fmaf(sum, 1.f / 128.f, eps));
 }
 
-// The lane's pairs turned; kBack: by the opposite angle.
-template <bool kAdjacent, bool kBack>
-MSA_DEV void rotate(float (&v)[16], const float4 (&cs)[4]) {
+// The lane's pairs turned by the angles of a table's row; kBack: the other way.
+template <bool kBack>
+MSA_DEV void rotate(Values& v, const float4* row, int j) {
+  constexpr uint64_t kSigns = 0x8000000080000000ull;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float c = e & 1 ? cs[e >> 1].z : cs[e >> 1].x;
-    const float s0 = e & 1 ? cs[e >> 1].w : cs[e >> 1].y;
-    const float s = kBack ? -s0 : s0;
-    const int i = kAdjacent ? 2 * e : e, k = kAdjacent ? 2 * e + 1 : e + 8;
-    const float a = v[i], b = v[k];
-    v[i] = fmaf(a, c, -(b * s));
-    v[k] = fmaf(b, c, a * s);
+  for (int i = 0; i < 4; ++i) {
+    const float4 x = row[i * 8 + j];
+    const uint64_t c = f2_pack(x.x, x.y), s = f2_pack(x.z, x.w), minus = s ^ kSigns;
+    const uint64_t a = v.a[i], b = v.b[i];
+    v.a[i] = f2_fma(a, c, f2_mul(b, kBack ? s : minus));
+    v.b[i] = f2_fma(b, c, f2_mul(a, kBack ? minus : s));
   }
 }
 
-// One row: normed if `norm`, then turned by the angles at `row` if `turn` (this
-// lane's dims are: a turn by nothing would carry infinities from pair to pair).
-template <bool kAdjacent>
-MSA_DEV void norm_rotate(float (&v)[16], const float (&w)[16], const float4* row, int j, bool norm, bool turn,
-                         float eps) {
+// The row normed if `norm` (without a norm w is 1), not turned yet.
+MSA_DEV void normalize(Values& v, const Values& w, bool norm, float eps) {
   float scale;
   const float sum = row_sum(squares(v));
   const float inv = inverse_rms(v, norm ? sum : 0.f, eps, scale);
-  const float r = norm ? inv : 1.f;  // w is 1 without a norm
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = v[i] * r * w[i];
-  if (turn) {
-    float4 cs[4];
-    load_angles(row, j, cs);
-    rotate<kAdjacent, false>(v, cs);
-  }
+  times(v, norm ? inv : 1.f);
+  times(v, w);
+}
+// One row: normed, then turned by the angles at `row` if `turn` (this lane's dims
+// are: a turn by nothing would carry infinities from pair to pair).
+MSA_DEV void norm_rotate(Values& v, const Values& w, const float4* row, int j, bool norm, bool turn, float eps) {
+  normalize(v, w, norm, eps);
+  if (turn) rotate<false>(v, row, j);
 }
 
 // Host side.
@@ -227,16 +296,19 @@ inline const Angles angles_of(const msa_rope_problem* p, const int32_t* position
 // How the rows of a call's tensors are cut: a unit is four heads (of the tensors'
 // heads one after the other) of a token, a warp's share; `units` of them to a
 // CTA's warps, `groups` CTAs side by side; with few units, `phases` warps take
-// a tile's tokens in turn.
+// tokens in turn.  A CTA keeps its heads, and so their weights, and takes one of
+// `slices` equal shares of the tokens.
 struct Cut {
-  int groups, units, phases;
+  int groups, units, phases, slices;
 };
-inline Cut cut_heads(int64_t heads) {
+inline Cut cut_rows(int64_t heads, int64_t tokens, int64_t ctas) {
   const int64_t u = (heads + 3) / 4;
   Cut c;
   c.groups = (int)((u + kWarps - 1) / kWarps);
   c.units = (int)((u + c.groups - 1) / c.groups);
   c.phases = kWarps / c.units;
+  const int64_t most = ctas / c.groups > 1 ? ctas / c.groups : 1;
+  c.slices = (int)(tokens < most ? tokens : most);
   return c;
 }
 // Tokens of a tile: the most whose tiles still give every SM two CTAs.
@@ -246,7 +318,7 @@ inline int cut_tokens(int64_t tokens, int64_t groups, int sms, int most, int lea
   return tile;
 }
 
-// Rows in and out, by CTAs of (tile of tokens, group of heads).
+// Rows in and out, by CTAs of (slice of the tokens, group of heads).
 struct RowsArgs {
   Tensor t[kTensors];
   uint16_t* y[kTensors];
@@ -254,7 +326,7 @@ struct RowsArgs {
   Angles an;
   float eps, offset;
   int T, heads;  // of all tensors
-  int tile, groups, units, phases;
+  Cut cut;
   int32_t* status;
 };
 
@@ -272,42 +344,72 @@ MSA_DEV int tensor_of(const Args& a, int hh, int& head) {
   return i;
 }
 
+MSA_DEV void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+MSA_DEV void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+MSA_DEV void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
+
+// Rows on their way: a lane copies its own granules and reads them back itself, so
+// that no barrier is needed, and the bytes in flight take no registers.
+constexpr int kStages = 4;
+struct RowsShared {
+  Table<kTile> tab[2];
+  uint4 ring[kWarps][kStages][2][32];
+};
+
 template <bool kAdjacent>
-MSA_DEV void rows_block(const RowsArgs& a, int64_t block, Table<kTile>& tab) {
+MSA_DEV void rows_block(const RowsArgs& a, int block, RowsShared& s) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, j = lane & 7;
-  const int64_t tile = block / a.groups;
-  const int group = (int)(block - tile * a.groups);
-  const int64_t t0 = tile * a.tile;
-  const int n = (int)min((int64_t)a.tile, a.T - t0);
-  fill_table<kAdjacent>(tab, a.an, t0, n);
-  const int phase = warp / a.units, unit = group * a.units + warp - phase * a.units;
+  const int slice = block / a.cut.groups, group = block - slice * a.cut.groups;
+  const int64_t t0 = (int64_t)a.T * slice / a.cut.slices;
+  const int n = (int)((int64_t)a.T * (slice + 1) / a.cut.slices - t0);
+  const int phase = warp / a.cut.units, unit = group * a.cut.units + warp - phase * a.cut.units;
   const int hh = unit * 4 + (lane >> 3);
-  const bool live = hh < a.heads;
+  const bool mine = phase < a.cut.phases, live = mine && hh < a.heads;
   int da, db, head;
   lane_dims(j, a.an.R, da, db);
   const int k = tensor_of(a, live ? hh : 0, head);
   const Tensor& t = a.t[k];
-  const bool norm = t.flags & MSA_ROPE_NORM, turn = turns(t, j, a.an.R);
-  float w[16];
-  load_weights(t, head, da, db, a.offset, w);
   const uint16_t* x = t.x + t0 * t.x_token + head * t.x_head;
   uint16_t* y = a.y[k] + t0 * a.y_token[k] + head * a.y_head[k];
+  const int64_t x_token = t.x_token, y_token = a.y_token[k];
+  const int phases = a.cut.phases;
+  auto copy = [&](int i, int stage) {
+    if (live && i < n) {
+      copy16(&s.ring[warp][stage][0][lane], x + i * x_token + da);
+      copy16(&s.ring[warp][stage][1][lane], x + i * x_token + db);
+    }
+    copies_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) copy(phase + i * phases, i);
+  const bool norm = t.flags & MSA_ROPE_NORM, turn = turns(t, j, a.an.R);
+  const Filler<kAdjacent> filler(a.an);
+  Values w;
+  load_weights<kAdjacent>(t, head, da, db, a.offset, w);
+  filler.fill(s.tab[0], a.an, t0, min(n, kTile));
   __syncthreads();
-  if (phase >= a.phases) return;
-  for (int i = phase; i < n; i += a.phases) {
-    uint4 ua = make_uint4(0, 0, 0, 0), ub = ua;
-    if (live) {
-      ua = *reinterpret_cast<const uint4*>(x + i * t.x_token + da);
-      ub = *reinterpret_cast<const uint4*>(x + i * t.x_token + db);
+  int stage = 0, i = phase;
+  for (int at = 0, buf = 0; at < n; at += kTile, buf ^= 1) {
+    const int end = min(at + kTile, n);
+    if (end < n) filler.fill(s.tab[buf ^ 1], a.an, t0 + end, min(n - end, kTile));
+    for (; i < end && mine; i += phases) {
+      copies_wait<kStages - 2>();
+      uint4 ua = s.ring[warp][stage][0][lane], ub = s.ring[warp][stage][1][lane];
+      Values v;
+      unpack<kAdjacent>(ua, ub, v);
+      copy(i + (kStages - 1) * phases, (stage + kStages - 1) % kStages);
+      stage = (stage + 1) % kStages;
+      norm_rotate(v, w, s.tab[buf].cs[i - at], j, norm, turn, a.eps);
+      pack<kAdjacent>(v, ua, ub);
+      if (live && s.tab[buf].live[i - at]) {
+        *reinterpret_cast<uint4*>(y + i * y_token + da) = ua;
+        *reinterpret_cast<uint4*>(y + i * y_token + db) = ub;
+      }
     }
-    float v[16];
-    unpack8(ua, v);
-    unpack8(ub, v + 8);
-    norm_rotate<kAdjacent>(v, w, tab.cs[i], j, norm, turn, a.eps);
-    if (live && a.an.positions[(t0 + i) * a.an.A] >= 0) {
-      *reinterpret_cast<uint4*>(y + i * a.y_token[k] + da) = pack8(v);
-      *reinterpret_cast<uint4*>(y + i * a.y_token[k] + db) = pack8(v + 8);
-    }
+    __syncthreads();
   }
 }
 
