@@ -469,7 +469,7 @@ extern "C" int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_
   a.q.status = a.status = d_status;
   int64_t q_blocks = 0;
   if (a.q.heads) {
-    a.q.cut = rope::cut_rows(a.q.heads, a.T, (int64_t)rope::kAppendCtas * sms);
+    a.q.cut = rope::cut_rows(a.q.heads, a.T, sms, rope::kAppendCtas * rope::kWarps);
     q_blocks = (int64_t)a.q.cut.slices * a.q.cut.groups;
   }
   a.k = tensor(MSA_ROPE_K, k, 0);

@@ -42,9 +42,9 @@ int check_problem(const msa_rope_problem* p) {
   return MSA_OK;
 }
 
-constexpr int kRowCtas = 4;  // of an SM
+constexpr int kRowWarps = 24;  // of an SM
 template <bool kAdjacent>
-__global__ void __launch_bounds__(kThreads, kRowCtas) norm_rope_kernel(RowsArgs a) {
+__global__ void __launch_bounds__(kThreads, kRowWarps / kWarps) norm_rope_kernel(RowsArgs a) {
   extern __shared__ __align__(16) uint8_t s_raw[];
   cache::after_previous_kernel();
   if (status_bad(a.status)) return;
@@ -75,17 +75,17 @@ struct GradArgs {
   int32_t* status;
 };
 
-constexpr int kGradStages = 3, kGradCtas = 2;
+constexpr int kGradStages = 3, kGradWarps = 16;
 struct GradShared {
   Table<kTile> tab[2];
   union {
-    uint4 ring[kWarps][kGradStages][4][32];  // x and dy
+    Stage ring[kWarps][kGradStages][2];  // x and dy
     float dw[kThreads / 8][128];
   };
 };
 
 template <bool kAdjacent>
-__global__ void __launch_bounds__(kThreads, kGradCtas) norm_rope_bwd_kernel(GradArgs a) {
+__global__ void __launch_bounds__(kThreads, kGradWarps / kWarps) norm_rope_bwd_kernel(GradArgs a) {
   extern __shared__ __align__(16) uint8_t s_raw[];
   GradShared& s = *reinterpret_cast<GradShared*>(s_raw);
   cache::after_previous_kernel();
@@ -101,21 +101,29 @@ __global__ void __launch_bounds__(kThreads, kGradCtas) norm_rope_bwd_kernel(Grad
   lane_dims(j, a.an.R, da, db);
   const int k = tensor_of(a, live ? hh : 0, head);
   const Tensor& t = a.t[k];
-  const int64_t x0 = t0 * t.x_token + head * t.x_head, x_token = t.x_token, y_token = a.y_token[k];
-  const uint16_t *x = t.x + x0, *dy = a.dy[k] + t0 * y_token + head * a.y_head[k];
-  uint16_t* dx = a.dx[k] + x0;
+  const int sa = granule_slot(da >> 3), sb = granule_slot(db >> 3);
   const int phases = a.cut.phases;
-  auto copy = [&](int i, int stage) {
-    if (live && i < n) {
-      copy16(&s.ring[warp][stage][0][lane], x + i * x_token + da);
-      copy16(&s.ring[warp][stage][1][lane], x + i * x_token + db);
-      copy16(&s.ring[warp][stage][2][lane], dy + i * y_token + da);
-      copy16(&s.ring[warp][stage][3][lane], dy + i * y_token + db);
+  const int64_t x_step = phases * t.x_token, y_step = phases * a.y_token[k];
+  const int64_t x0 = (t0 + phase) * t.x_token + head * t.x_head;
+  const uint16_t *x = t.x + x0, *dy = a.dy[k] + (t0 + phase) * a.y_token[k] + head * a.y_head[k];  // next to copy
+  uint16_t* dx = a.dx[k] + x0;
+  auto& ring = s.ring[warp];
+  int ahead = phase;
+  auto copy = [&](int stage) {
+    if (live && ahead < n) {
+      copy_row(ring[stage][0], x, lane);
+      copy_row(ring[stage][1], dy, lane);
     }
     copies_commit();
+    ahead += phases;
+    x += x_step;
+    dy += y_step;
   };
 #pragma unroll
-  for (int i = 0; i < kGradStages - 1; ++i) copy(phase + i * phases, i);
+  for (int i = 0; i < kGradStages - 1; ++i) copy(i);
+  if (!live)  // rows that are not there count as zeros
+    for (int i = lane & 7; i < kGradStages * 2 * 16; i += 8)
+      ring[i >> 5][i >> 4 & 1].row[lane >> 3][i & 15] = make_uint4(0, 0, 0, 0);
   const bool norm = t.flags & MSA_ROPE_NORM, turn = turns(t, j, a.an.R);
   const Filler<kAdjacent> filler(a.an);
   Values w, dw;
@@ -124,56 +132,57 @@ __global__ void __launch_bounds__(kThreads, kGradCtas) norm_rope_bwd_kernel(Grad
   for (int i = 0; i < 4; ++i) dw.a[i] = dw.b[i] = 0;
   filler.fill(s.tab[0], a.an, t0, min(n, kTile));
   __syncthreads();
-  int stage = 0, i = phase;
+  int stage = 0, next = kGradStages - 1, i = mine ? phase : n;
   for (int at = 0, buf = 0; at < n; at += kTile, buf ^= 1) {
     const int end = min(at + kTile, n);
     if (end < n) filler.fill(s.tab[buf ^ 1], a.an, t0 + end, min(n - end, kTile));
-    for (; i < end && mine; i += phases) {
+    for (; i < end; i += phases) {
       copies_wait<kGradStages - 2>();
-      // rows of padding count as zeros: they may hold anything
-      const bool here = live && s.tab[buf].live[i - at];
-      uint4 u[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) u[c] = here ? s.ring[warp][stage][c][lane] : make_uint4(0, 0, 0, 0);
-      Values v, g;
-      unpack<kAdjacent>(u[0], u[1], v);
-      unpack<kAdjacent>(u[2], u[3], g);
-      copy(i + (kGradStages - 1) * phases, (stage + kGradStages - 1) % kGradStages);
-      stage = (stage + 1) % kGradStages;
-      if (turn) rotate<true>(g, s.tab[buf].cs[i - at], j);
-      float scale;
-      const float sum = row_sum(squares(v));
-      const float r = inverse_rms(v, norm ? sum : 0.f, a.eps, scale);
-      times(v, r);  // the normed row without its weight
-      uint64_t dot = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      __syncwarp();  // the lanes' copies have landed; the stage before has been read
+      const uint4 *xr = ring[stage][0].row[lane >> 3], *gr = ring[stage][1].row[lane >> 3];
+      uint4 xa = xr[sa], xb = xr[sb], ga = gr[sa], gb = gr[sb];
+      copy(next);
+      next = stage;
+      stage = stage + 1 == kGradStages ? 0 : stage + 1;
+      if (s.tab[buf].live[i - at]) {
+        Values v, g;
+        unpack<kAdjacent>(xa, xb, v);
+        unpack<kAdjacent>(ga, gb, g);
+        if (turn) rotate<true>(g, s.tab[buf].cs[i - at], j);
+        float scale;
+        const float sum = row_sum(squares(v));
+        const float r = inverse_rms(v, norm ? sum : 0.f, a.eps, scale);
         if (norm) {
-          dw.a[e] = f2_fma(g.a[e], v.a[e], dw.a[e]);
-          dw.b[e] = f2_fma(g.b[e], v.b[e], dw.b[e]);
-        }
-        g.a[e] = f2_mul(g.a[e], w.a[e]);
-        g.b[e] = f2_mul(g.b[e], w.b[e]);
-        dot = f2_fma(g.a[e], v.a[e], dot);
-        dot = f2_fma(g.b[e], v.b[e], dot);
-      }
-      float lo, hi;
-      f2_unpack(dot, lo, hi);
-      const float mean = row_sum(lo + hi) * (-1.f / 128.f);
-      if (norm) {
-        const uint64_t m = f2_pack(mean, mean);
+          times(v, r);  // the normed row without its weight
+          uint64_t dot = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          g.a[e] = f2_fma(v.a[e], m, g.a[e]);
-          g.b[e] = f2_fma(v.b[e], m, g.b[e]);
+          for (int e = 0; e < 4; ++e) {
+            dw.a[e] = f2_fma(g.a[e], v.a[e], dw.a[e]);
+            dw.b[e] = f2_fma(g.b[e], v.b[e], dw.b[e]);
+            g.a[e] = f2_mul(g.a[e], w.a[e]);
+            g.b[e] = f2_mul(g.b[e], w.b[e]);
+            dot = f2_fma(g.a[e], v.a[e], dot);
+            dot = f2_fma(g.b[e], v.b[e], dot);
+          }
+          float lo, hi;
+          f2_unpack(dot, lo, hi);
+          // the rows' lanes are those of one tensor
+          const float mean = row_sum(lo + hi, 0xFFu << (lane & 24)) * (-1.f / 128.f);
+          const uint64_t m = f2_pack(mean, mean);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            g.a[e] = f2_fma(v.a[e], m, g.a[e]);
+            g.b[e] = f2_fma(v.b[e], m, g.b[e]);
+          }
+          times(g, r * scale);
         }
-        times(g, r * scale);
+        pack<kAdjacent>(g, ga, gb);
+        if (live) {
+          *reinterpret_cast<uint4*>(dx + da) = ga;
+          *reinterpret_cast<uint4*>(dx + db) = gb;
+        }
       }
-      pack<kAdjacent>(g, u[0], u[1]);
-      if (here) {
-        *reinterpret_cast<uint4*>(dx + i * x_token + da) = u[0];
-        *reinterpret_cast<uint4*>(dx + i * x_token + db) = u[1];
-      }
+      dx += x_step;
     }
     __syncthreads();
   }
@@ -187,6 +196,8 @@ __global__ void __launch_bounds__(kThreads, kGradCtas) norm_rope_bwd_kernel(Grad
     row[db + i] = live ? sums[8 + i] : 0.f;
   }
   __syncthreads();
+  // threads behind the last 128 of the CTA have no part in it
+  if (tid >> 7 >= (int)blockDim.x >> 7) return;
   const int d = tid & 127, units = a.cut.units;
   float* out = a.partial + (int64_t)slice * a.slots * 128 + d;
   for (int i = 0, before = 0; i < kTensors; ++i) {
@@ -196,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, kGradCtas) norm_rope_bwd_kernel(Grad
       const int lo = max(before, group * units * 4), hi = min(end, (group + 1) * units * 4);
       const int row0 = lo - group * units * 4, rows = hi - lo;
       if (a.t[i].flags & MSA_ROPE_PER_HEAD) {
-        for (int r = tid >> 7; r < rows; r += 2) {
+        for (int r = tid >> 7; r < rows; r += (int)blockDim.x >> 7) {
           float s1 = 0.f;
           for (int p = 0; p < phases; ++p) s1 += s.dw[p * units * 4 + row0 + r][d];
           out[(int64_t)(a.slot[i] + lo - before + r) * 128] = s1;
@@ -222,21 +233,36 @@ struct SumArgs {
   int32_t* status;
 };
 
-// A CTA adds up one row of weights: thread (part, dim) every eighth partial row.
+// A CTA adds up one row of weights: thread (part, dim) every eighth slice, sixteen
+// loads in flight (of 300 slices: one at a time 7 us, this way 2).
 constexpr int kSumParts = 8;
 __global__ void __launch_bounds__(128 * kSumParts) weight_sum_kernel(SumArgs a) {
   __shared__ float s_part[kSumParts][128];
   cache::after_previous_kernel();
   if (status_bad(a.status)) return;
-  int k = 0, before = 0;
-  while (k + 1 < kTensors && (int)blockIdx.x >= a.end[k]) before = a.end[k++];
-  const int row = blockIdx.x - before, d = threadIdx.x & 127, part = threadIdx.x >> 7;
-  const int per = a.per[k];
-  const float* src = a.partial + (int64_t)(a.slot[k] + row * per) * 128 + d;
+  int row = blockIdx.x, slot = a.slot[0], per = a.per[0], wide = a.wide[0];
+  void* dw = a.dw[0];
+#pragma unroll
+  for (int i = 1; i < kTensors; ++i)
+    if ((int)blockIdx.x >= a.end[i - 1]) {
+      row = blockIdx.x - a.end[i - 1];
+      slot = a.slot[i];
+      per = a.per[i];
+      wide = a.wide[i];
+      dw = a.dw[i];
+    }
+  const int d = threadIdx.x & 127, part = threadIdx.x >> 7;
+  const int64_t step = (int64_t)a.slots * 128;
   float s = 0.f;
-  for (int i = part; i < a.slices * per; i += kSumParts) {
-    const int slice = i / per;
-    s += src[((int64_t)slice * a.slots + i - slice * per) * 128];
+  for (int p = 0; p < per; ++p) {
+    const float* src = a.partial + (int64_t)(slot + row * per + p) * 128 + d;
+    for (int i0 = part; i0 < a.slices; i0 += 16 * kSumParts) {
+      float x[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = i0 + i * kSumParts < a.slices ? src[(i0 + i * kSumParts) * step] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s += x[i];
+    }
   }
   s_part[part][d] = s;
   __syncthreads();
@@ -244,8 +270,8 @@ __global__ void __launch_bounds__(128 * kSumParts) weight_sum_kernel(SumArgs a) 
   s = 0.f;
 #pragma unroll
   for (int i = 0; i < kSumParts; ++i) s += s_part[i][d];
-  if (a.wide[k]) static_cast<float*>(a.dw[k])[(int64_t)row * 128 + d] = s;
-  else static_cast<uint16_t*>(a.dw[k])[(int64_t)row * 128 + d] = (uint16_t)(pack_bf16x2(s, 0.f) & 0xFFFFu);
+  if (wide) static_cast<float*>(dw)[(int64_t)row * 128 + d] = s;
+  else static_cast<uint16_t*>(dw)[(int64_t)row * 128 + d] = (uint16_t)(pack_bf16x2(s, 0.f) & 0xFFFFu);
 }
 
 // How the gradients' tokens and partial sums are cut.  It depends on the problem
@@ -259,7 +285,7 @@ static GradCut cut_grad(const msa_rope_problem* p) {
   GradCut g{};
   for (int i = 0; i < kTensors; ++i) g.heads += p->tensor[i].heads;
   if (g.heads == 0) return g;
-  g.c = cut_rows(g.heads, p->tokens, kGradCtas * 152);
+  g.c = cut_rows(g.heads, p->tokens, 152, kGradWarps);
   int at = 0;
   for (int i = 0; i < kTensors; ++i) {
     const msa_rope_tensor& t = p->tensor[i];
@@ -340,10 +366,10 @@ int msa_norm_rope(const msa_rope_problem* p, const uint16_t* const* x, const int
   a.T = p->tokens;
   int32_t sms = 0;
   if ((rc = sm_count_current(&sms))) return rc;
-  a.cut = rope::cut_rows(a.heads, a.T, (int64_t)rope::kRowCtas * sms);
+  a.cut = rope::cut_rows(a.heads, a.T, sms, rope::kRowWarps);
   a.status = d_status;
   return cache::launch_kernel(p->adjacent ? rope::norm_rope_kernel<true> : rope::norm_rope_kernel<false>,
-                              dim3((unsigned)(a.cut.slices * a.cut.groups)), rope::kThreads, sizeof(rope::RowsShared),
+                              dim3((unsigned)(a.cut.slices * a.cut.groups)), a.cut.threads(), sizeof(rope::RowsShared),
                               stream, 1, a);
 }
 
@@ -404,7 +430,7 @@ int msa_norm_rope_bwd(const msa_rope_problem* p, const uint16_t* const* dy, cons
     a.partial = static_cast<float*>(ws);
     a.status = d_status;
     rc = cache::launch_kernel(p->adjacent ? rope::norm_rope_bwd_kernel<true> : rope::norm_rope_bwd_kernel<false>,
-                              dim3((unsigned)(g.c.slices * g.c.groups)), rope::kThreads, sizeof(rope::GradShared),
+                              dim3((unsigned)(g.c.slices * g.c.groups)), g.c.threads(), sizeof(rope::GradShared),
                               stream, 1, a);
     if (rc) return rc;
   }

@@ -108,26 +108,31 @@ struct Table {
 template <bool kAdjacent>
 struct Filler {
   Pair p0, p1;
+  int at, row0, step;  // place in a row, the thread's first row, rows between two of its rows
   MSA_DEV Filler(const Angles& a) {
-    const int e2 = (threadIdx.x >> 3) & 3, j = threadIdx.x & 7;
+    const int lanes = a.R >> 4, row = 4 * lanes;
     p0 = p1 = Pair{0, 0};
-    if (j < a.R >> 4) {
-      p0 = load_pair(a, pair_of<kAdjacent>(j, 2 * e2, a.R));
-      p1 = load_pair(a, pair_of<kAdjacent>(j, 2 * e2 + 1, a.R));
-    }
+    at = -1;
+    row0 = step = 0;
+    if (lanes == 0) return;
+    step = (int)blockDim.x / row;
+    row0 = (int)threadIdx.x / row;
+    if (row0 >= step) return;
+    const int i = (int)threadIdx.x - row0 * row, e2 = i / lanes, j = i - e2 * lanes;
+    at = e2 * 8 + j;
+    p0 = load_pair(a, pair_of<kAdjacent>(j, 2 * e2, a.R));
+    p1 = load_pair(a, pair_of<kAdjacent>(j, 2 * e2 + 1, a.R));
   }
   template <int kRows>
   MSA_DEV void fill(Table<kRows>& tab, const Angles& a, int64_t t0, int n) const {
-    const int at = threadIdx.x & 31;
-    for (int row = threadIdx.x >> 5; row < n; row += kWarps) {
-      if ((at & 7) < a.R >> 4) {
+    if (at >= 0)
+      for (int row = row0; row < n; row += step) {
         float4 x;
         cos_sin(turn_of(a, p0, t0 + row), a.scale, x.x, x.z);
         cos_sin(turn_of(a, p1, t0 + row), a.scale, x.y, x.w);
         tab.cs[row][at] = x;
       }
-      if (at == 31) tab.live[row] = a.positions[(t0 + row) * a.A] >= 0;
-    }
+    if ((int)threadIdx.x < n) tab.live[threadIdx.x] = a.positions[(t0 + threadIdx.x) * a.A] >= 0;
   }
 };
 
@@ -207,9 +212,9 @@ MSA_DEV void load_weights(const Tensor& t, int head, int a, int b, float offset,
 }
 
 // Sum over the eight lanes of a row; all of them get it.
-MSA_DEV float row_sum(float x) {
+MSA_DEV float row_sum(float x, unsigned lanes = 0xffffffffu) {
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  for (int o = 1; o < 8; o <<= 1) x += __shfl_xor_sync(lanes, x, o);
   return x;
 }
 MSA_DEV float squares(const Values& v) {
@@ -261,14 +266,18 @@ MSA_DEV float inverse_rms(Values& v, float sum, float eps, float& scale) {
 // The lane's pairs turned by the angles of a table's row; kBack: the other way.
 template <bool kBack>
 MSA_DEV void rotate(Values& v, const float4* row, int j) {
-  constexpr uint64_t kSigns = 0x8000000080000000ull;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float4 x = row[i * 8 + j];
-    const uint64_t c = f2_pack(x.x, x.y), s = f2_pack(x.z, x.w), minus = s ^ kSigns;
+    const uint64_t c = f2_pack(x.x, x.y), s = f2_pack(x.z, x.w);
     const uint64_t a = v.a[i], b = v.b[i];
-    v.a[i] = f2_fma(a, c, f2_mul(b, kBack ? s : minus));
-    v.b[i] = f2_fma(b, c, f2_mul(a, kBack ? minus : s));
+    if constexpr (kBack) {
+      v.a[i] = f2_fma(a, c, f2_mul(b, s));
+      v.b[i] = f2_sub(f2_mul(b, c), f2_mul(a, s));
+    } else {
+      v.a[i] = f2_sub(f2_mul(a, c), f2_mul(b, s));
+      v.b[i] = f2_fma(b, c, f2_mul(a, s));
+    }
   }
 }
 
@@ -297,18 +306,19 @@ inline const Angles angles_of(const msa_rope_problem* p, const int32_t* position
 // heads one after the other) of a token, a warp's share; `units` of them to a
 // CTA's warps, `groups` CTAs side by side; with few units, `phases` warps take
 // tokens in turn.  A CTA keeps its heads, and so their weights, and takes one of
-// `slices` equal shares of the tokens.
+// `slices` equal shares of the tokens, as many as `warps` of an SM hold.
 struct Cut {
   int groups, units, phases, slices;
+  int threads() const { return 32 * units * phases; }
 };
-inline Cut cut_rows(int64_t heads, int64_t tokens, int64_t ctas) {
+inline Cut cut_rows(int64_t heads, int64_t tokens, int64_t sms, int warps) {
   const int64_t u = (heads + 3) / 4;
   Cut c;
   c.groups = (int)((u + kWarps - 1) / kWarps);
   c.units = (int)((u + c.groups - 1) / c.groups);
   c.phases = kWarps / c.units;
-  const int64_t most = ctas / c.groups > 1 ? ctas / c.groups : 1;
-  c.slices = (int)(tokens < most ? tokens : most);
+  const int64_t most = sms * (warps / (c.units * c.phases)) / c.groups;
+  c.slices = (int)(tokens < most ? tokens : most > 1 ? most : 1);
   return c;
 }
 // Tokens of a tile: the most whose tiles still give every SM two CTAs.
@@ -351,12 +361,24 @@ MSA_DEV void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory
 template <int kLeft>
 MSA_DEV void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
 
-// Rows on their way: a lane copies its own granules and reads them back itself, so
-// that no barrier is needed, and the bytes in flight take no registers.
-constexpr int kStages = 4;
+// Rows on their way to a warp: four rows a stage, in whole lines, whatever dims a
+// lane then takes (two lines of 128 bytes a row for any R; the lanes' own granules
+// are 64 bytes apart and less for R < 128).  The bytes in flight take no registers.
+// The upper granules are stored with their halves exchanged, so that the lanes'
+// reads of R = 64 meet no bank twice.
+constexpr int kStages = 4;  // a power of two
+struct Stage {
+  uint4 row[4][16];
+};
+MSA_DEV int granule_slot(int g) { return g ^ (g >> 1 & 4); }
+MSA_DEV void copy_row(Stage& s, const uint16_t* row, int lane) {
+  const int r = lane >> 3, j = lane & 7;
+  copy16(&s.row[r][granule_slot(j)], row + 8 * j);
+  copy16(&s.row[r][granule_slot(j + 8)], row + 64 + 8 * j);
+}
 struct RowsShared {
   Table<kTile> tab[2];
-  uint4 ring[kWarps][kStages][2][32];
+  Stage ring[kWarps][kStages];
 };
 
 template <bool kAdjacent>
@@ -372,42 +394,49 @@ MSA_DEV void rows_block(const RowsArgs& a, int block, RowsShared& s) {
   lane_dims(j, a.an.R, da, db);
   const int k = tensor_of(a, live ? hh : 0, head);
   const Tensor& t = a.t[k];
-  const uint16_t* x = t.x + t0 * t.x_token + head * t.x_head;
-  uint16_t* y = a.y[k] + t0 * a.y_token[k] + head * a.y_head[k];
-  const int64_t x_token = t.x_token, y_token = a.y_token[k];
+  const int sa = granule_slot(da >> 3), sb = granule_slot(db >> 3);
   const int phases = a.cut.phases;
-  auto copy = [&](int i, int stage) {
-    if (live && i < n) {
-      copy16(&s.ring[warp][stage][0][lane], x + i * x_token + da);
-      copy16(&s.ring[warp][stage][1][lane], x + i * x_token + db);
-    }
+  const int64_t x_step = phases * t.x_token, y_step = phases * a.y_token[k];
+  const uint16_t* x = t.x + (t0 + phase) * t.x_token + head * t.x_head;  // of the next row to copy
+  uint16_t* y = a.y[k] + (t0 + phase) * a.y_token[k] + head * a.y_head[k];
+  Stage* ring = s.ring[warp];
+  int ahead = phase;  // its token
+  auto copy = [&](int stage) {
+    if (live && ahead < n) copy_row(ring[stage], x, lane);
     copies_commit();
+    ahead += phases;
+    x += x_step;
   };
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) copy(phase + i * phases, i);
+  for (int i = 0; i < kStages - 1; ++i) copy(i);
   const bool norm = t.flags & MSA_ROPE_NORM, turn = turns(t, j, a.an.R);
   const Filler<kAdjacent> filler(a.an);
   Values w;
   load_weights<kAdjacent>(t, head, da, db, a.offset, w);
   filler.fill(s.tab[0], a.an, t0, min(n, kTile));
   __syncthreads();
-  int stage = 0, i = phase;
+  int stage = 0, i = mine ? phase : n;
   for (int at = 0, buf = 0; at < n; at += kTile, buf ^= 1) {
     const int end = min(at + kTile, n);
     if (end < n) filler.fill(s.tab[buf ^ 1], a.an, t0 + end, min(n - end, kTile));
-    for (; i < end && mine; i += phases) {
+    for (; i < end; i += phases) {
       copies_wait<kStages - 2>();
-      uint4 ua = s.ring[warp][stage][0][lane], ub = s.ring[warp][stage][1][lane];
-      Values v;
-      unpack<kAdjacent>(ua, ub, v);
-      copy(i + (kStages - 1) * phases, (stage + kStages - 1) % kStages);
-      stage = (stage + 1) % kStages;
-      norm_rotate(v, w, s.tab[buf].cs[i - at], j, norm, turn, a.eps);
-      pack<kAdjacent>(v, ua, ub);
-      if (live && s.tab[buf].live[i - at]) {
-        *reinterpret_cast<uint4*>(y + i * y_token + da) = ua;
-        *reinterpret_cast<uint4*>(y + i * y_token + db) = ub;
+      __syncwarp();  // the lanes' copies have landed; the stage before has been read
+      const uint4* row = ring[stage].row[lane >> 3];
+      uint4 ua = row[sa], ub = row[sb];
+      copy((stage + kStages - 1) & (kStages - 1));
+      stage = (stage + 1) & (kStages - 1);
+      if (s.tab[buf].live[i - at]) {
+        Values v;
+        unpack<kAdjacent>(ua, ub, v);
+        norm_rotate(v, w, s.tab[buf].cs[i - at], j, norm, turn, a.eps);
+        pack<kAdjacent>(v, ua, ub);
+        if (live) {
+          *reinterpret_cast<uint4*>(y + da) = ua;
+          *reinterpret_cast<uint4*>(y + db) = ub;
+        }
       }
+      y += y_step;
     }
     __syncthreads();
   }
