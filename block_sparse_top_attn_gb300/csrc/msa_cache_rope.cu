@@ -10,6 +10,7 @@
 namespace msa {
 namespace rope {
 
+constexpr int kKvTile = 16;  // most tokens of a tile of K and V
 constexpr int kIndexRows = kThreads / 8;  // rows of a pass
 
 struct AppendRopeArgs {
@@ -192,13 +193,13 @@ MSA_DEV void amplitudes(const Values& v, const float4* row, int j, bool turn, fl
 
 // K and V of a tile of tokens and a group of heads.
 template <bool kAdjacent>
-MSA_DEV void kv_block(const AppendRopeArgs& a, int block, Table<kTile>& tab) {
+MSA_DEV void kv_block(const AppendRopeArgs& a, int block, Table<kKvTile>& tab) {
   const int tid = threadIdx.x, lane = tid & 31, j = lane & 7;
   const int tile = block / a.kv_groups, group = block - tile * a.kv_groups;
   const int64_t t0 = (int64_t)tile * a.kv_tile;
   const int n = (int)min((int64_t)a.kv_tile, a.T - t0);
   const int h0 = group * a.kv_heads, hn = min(a.kv_heads, a.H - h0);
-  const Filler<kAdjacent> filler(a.q.an);
+  const Filler<kAdjacent> filler(a.q.an, threadIdx.x, kThreads);
   filler.fill(tab, a.q.an, t0, n);
   __syncthreads();
   const bool norm = a.k.flags & MSA_ROPE_NORM, turn = turns(a.k, j, a.q.an.R);
@@ -311,7 +312,7 @@ MSA_DEV void index_block(const AppendRopeArgs& a, int g, IndexShared& s) {
   const bool norm = a.ki.flags & MSA_ROPE_NORM, turn = turns(a.ki, j, a.q.an.R);
   int da, db;
   lane_dims(j, a.q.an.R, da, db);
-  const Filler<kAdjacent> filler(a.q.an);
+  const Filler<kAdjacent> filler(a.q.an, threadIdx.x, kThreads);
   const int64_t slot = x.last >= 0 ? a.slot_map[x.last] : -1;
   const bool average = slot >= 0 && slot < a.slots;  // else reported by the rows' own CTAs, or left out
   const int olds = average ? max(0, x.cu0 - (x.last - (a.B - 1))) : 0;  // tokens of earlier calls
@@ -407,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_rope_kernel(Appe
     return;
   }
   block -= a.index_blocks;
-  if (block < a.kv_blocks) kv_block<kAdjacent>(a, block, *reinterpret_cast<Table<kTile>*>(s_raw));
+  if (block < a.kv_blocks) kv_block<kAdjacent>(a, block, *reinterpret_cast<Table<kKvTile>*>(s_raw));
   else rows_block<kAdjacent>(a.q, block - a.kv_blocks, *reinterpret_cast<RowsShared*>(s_raw));
 }
 
@@ -469,7 +470,7 @@ extern "C" int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_
   a.q.status = a.status = d_status;
   int64_t q_blocks = 0;
   if (a.q.heads) {
-    a.q.cut = rope::cut_rows(a.q.heads, a.T, sms, rope::kAppendCtas * rope::kWarps);
+    a.q.cut = rope::cut_rows(a.q.heads, a.T, sms, rope::kAppendCtas * rope::kWarps, rope::kWarps - 1);
     q_blocks = (int64_t)a.q.cut.slices * a.q.cut.groups;
   }
   a.k = tensor(MSA_ROPE_K, k, 0);
@@ -486,7 +487,7 @@ extern "C" int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_
   a.v_mul = cache::exp2i(-c->v_exp);
   a.kv_groups = (H + 7) / 8;
   a.kv_heads = (H + a.kv_groups - 1) / a.kv_groups;
-  a.kv_tile = rope::cut_tokens(a.T, a.kv_groups, sms, rope::kTile, 4);
+  a.kv_tile = rope::cut_tokens(a.T, a.kv_groups, sms, rope::kKvTile, 4);
   const int64_t kv_blocks = (int64_t)((a.T + a.kv_tile - 1) / a.kv_tile) * a.kv_groups;
   const int64_t index_blocks = index ? c->chunk_cap : 0;
   if (index_blocks + kv_blocks + q_blocks > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;

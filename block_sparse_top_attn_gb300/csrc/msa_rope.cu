@@ -42,9 +42,13 @@ int check_problem(const msa_rope_problem* p) {
   return MSA_OK;
 }
 
-constexpr int kRowWarps = 24;  // of an SM
+// CTAs of the largest size on an SM.  More of them read no faster and keep more of
+// the memory's rows open at once: 131k tokens x 152 heads take 1600 us with two,
+// 1725 with three; 32k x 68 180 and 208.
+constexpr int kRowCtas = 2;
+constexpr int kRowThreads = 32 * (kRowWarps + 1);
 template <bool kAdjacent>
-__global__ void __launch_bounds__(kThreads, kRowWarps / kWarps) norm_rope_kernel(RowsArgs a) {
+__global__ void __launch_bounds__(kRowThreads, kRowCtas) norm_rope_kernel(RowsArgs a) {
   extern __shared__ __align__(16) uint8_t s_raw[];
   cache::after_previous_kernel();
   if (status_bad(a.status)) return;
@@ -75,37 +79,32 @@ struct GradArgs {
   int32_t* status;
 };
 
-constexpr int kGradStages = 3, kGradWarps = 16;
+constexpr int kGradStages = 3, kGradCtas = 2, kGradWarps = 9, kGradThreads = 32 * (kGradWarps + 1);
 struct GradShared {
   Table<kTile> tab[2];
   union {
-    Stage ring[kWarps][kGradStages][2];  // x and dy
-    float dw[kThreads / 8][128];
+    Stage ring[kGradWarps][kGradStages][2];  // x and dy
+    float dw[kGradWarps * 4][128];
   };
 };
 
+// The rows of one warp.
 template <bool kAdjacent>
-__global__ void __launch_bounds__(kThreads, kGradWarps / kWarps) norm_rope_bwd_kernel(GradArgs a) {
-  extern __shared__ __align__(16) uint8_t s_raw[];
-  GradShared& s = *reinterpret_cast<GradShared*>(s_raw);
-  cache::after_previous_kernel();
-  if (status_bad(a.status)) return;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, j = lane & 7;
-  const int slice = blockIdx.x / a.cut.groups, group = blockIdx.x - slice * a.cut.groups;
-  const int64_t t0 = (int64_t)a.T * slice / a.cut.slices;
-  const int n = (int)((int64_t)a.T * (slice + 1) / a.cut.slices - t0);
+MSA_DEV void grad_rows(const GradArgs& a, GradShared& s, int slice, int group, int n, int apart) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane & 7;
   const int phase = warp / a.cut.units, unit = group * a.cut.units + warp - phase * a.cut.units;
   const int hh = unit * 4 + (lane >> 3);
-  const bool mine = phase < a.cut.phases, live = mine && hh < a.heads;
+  const bool live = hh < a.heads;
   int da, db, head;
   lane_dims(j, a.an.R, da, db);
   const int k = tensor_of(a, live ? hh : 0, head);
   const Tensor& t = a.t[k];
   const int sa = granule_slot(da >> 3), sb = granule_slot(db >> 3);
   const int phases = a.cut.phases;
-  const int64_t x_step = phases * t.x_token, y_step = phases * a.y_token[k];
-  const int64_t x0 = (t0 + phase) * t.x_token + head * t.x_head;
-  const uint16_t *x = t.x + x0, *dy = a.dy[k] + (t0 + phase) * a.y_token[k] + head * a.y_head[k];  // next to copy
+  const int64_t first = slice + (int64_t)phase * apart, step = (int64_t)phases * apart;  // this warp's tokens
+  const int64_t x_step = step * t.x_token, y_step = step * a.y_token[k];
+  const int64_t x0 = first * t.x_token + head * t.x_head;
+  const uint16_t *x = t.x + x0, *dy = a.dy[k] + first * a.y_token[k] + head * a.y_head[k];  // next to copy
   uint16_t* dx = a.dx[k] + x0;
   auto& ring = s.ring[warp];
   int ahead = phase;
@@ -125,18 +124,15 @@ __global__ void __launch_bounds__(kThreads, kGradWarps / kWarps) norm_rope_bwd_k
     for (int i = lane & 7; i < kGradStages * 2 * 16; i += 8)
       ring[i >> 5][i >> 4 & 1].row[lane >> 3][i & 15] = make_uint4(0, 0, 0, 0);
   const bool norm = t.flags & MSA_ROPE_NORM, turn = turns(t, j, a.an.R);
-  const Filler<kAdjacent> filler(a.an);
   Values w, dw;
   load_weights<kAdjacent>(t, head, da, db, a.offset, w);
 #pragma unroll
   for (int i = 0; i < 4; ++i) dw.a[i] = dw.b[i] = 0;
-  filler.fill(s.tab[0], a.an, t0, min(n, kTile));
-  __syncthreads();
-  int stage = 0, next = kGradStages - 1, i = mine ? phase : n;
-  for (int at = 0, buf = 0; at < n; at += kTile, buf ^= 1) {
-    const int end = min(at + kTile, n);
-    if (end < n) filler.fill(s.tab[buf ^ 1], a.an, t0 + end, min(n - end, kTile));
-    for (; i < end; i += phases) {
+  __syncthreads();  // the first table
+  int stage = 0, next = kGradStages - 1, i = phase;
+  for (int at = 0, table = 0; at < n; at += kTile, ++table) {
+    const Table<kTile>& tab = s.tab[table & 1];
+    for (; i < min(at + kTile, n); i += phases) {
       copies_wait<kGradStages - 2>();
       __syncwarp();  // the lanes' copies have landed; the stage before has been read
       const uint4 *xr = ring[stage][0].row[lane >> 3], *gr = ring[stage][1].row[lane >> 3];
@@ -144,11 +140,11 @@ __global__ void __launch_bounds__(kThreads, kGradWarps / kWarps) norm_rope_bwd_k
       copy(next);
       next = stage;
       stage = stage + 1 == kGradStages ? 0 : stage + 1;
-      if (s.tab[buf].live[i - at]) {
+      if (tab.live[i - at]) {
         Values v, g;
         unpack<kAdjacent>(xa, xb, v);
         unpack<kAdjacent>(ga, gb, g);
-        if (turn) rotate<true>(g, s.tab[buf].cs[i - at], j);
+        if (turn) rotate<true>(g, tab.cs[i - at], j);
         float scale;
         const float sum = row_sum(squares(v));
         const float r = inverse_rms(v, norm ? sum : 0.f, a.eps, scale);
@@ -184,21 +180,35 @@ __global__ void __launch_bounds__(kThreads, kGradWarps / kWarps) norm_rope_bwd_k
       }
       dx += x_step;
     }
-    __syncthreads();
+    __syncthreads();  // it has been read, the next one is there
   }
-  // the CTA's sums: heads that share a weight in the order of the warps and rows
-  float* row = s.dw[tid >> 3];
+  // the sums, by rows of the CTA (the rings have been read)
+  float* row = s.dw[warp * 4 + (lane >> 3)];
   float sums[16];
   in_order<kAdjacent>(dw, sums);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    row[da + i] = live ? sums[i] : 0.f;
-    row[db + i] = live ? sums[8 + i] : 0.f;
+  for (int e = 0; e < 8; ++e) {
+    row[da + e] = live ? sums[e] : 0.f;
+    row[db + e] = live ? sums[8 + e] : 0.f;
   }
+}
+
+template <bool kAdjacent>
+__global__ void __launch_bounds__(kGradThreads, kGradCtas) norm_rope_bwd_kernel(GradArgs a) {
+  extern __shared__ __align__(16) uint8_t s_raw[];
+  GradShared& s = *reinterpret_cast<GradShared*>(s_raw);
+  cache::after_previous_kernel();
+  if (status_bad(a.status)) return;
+  const int tid = threadIdx.x, slice = blockIdx.x / a.cut.groups, group = blockIdx.x - slice * a.cut.groups;
+  const int apart = a.cut.slices, n = (a.T - slice + apart - 1) / apart;
+  const int row_threads = 32 * a.cut.units * a.cut.phases;
+  if (tid >= row_threads) fill_tables<kAdjacent>(a.an, s.tab, row_threads, slice, n, apart);
+  else grad_rows<kAdjacent>(a, s, slice, group, n, apart);
+  // the CTA's sums: heads that share a weight in the order of the warps and rows
   __syncthreads();
   // threads behind the last 128 of the CTA have no part in it
   if (tid >> 7 >= (int)blockDim.x >> 7) return;
-  const int d = tid & 127, units = a.cut.units;
+  const int d = tid & 127, units = a.cut.units, phases = a.cut.phases;
   float* out = a.partial + (int64_t)slice * a.slots * 128 + d;
   for (int i = 0, before = 0; i < kTensors; ++i) {
     const int end = a.t[i].end;
@@ -285,7 +295,7 @@ static GradCut cut_grad(const msa_rope_problem* p) {
   GradCut g{};
   for (int i = 0; i < kTensors; ++i) g.heads += p->tensor[i].heads;
   if (g.heads == 0) return g;
-  g.c = cut_rows(g.heads, p->tokens, 152, kGradWarps);
+  g.c = cut_rows(g.heads, p->tokens, 152, kGradCtas * (kGradWarps + 1), kGradWarps);
   int at = 0;
   for (int i = 0; i < kTensors; ++i) {
     const msa_rope_tensor& t = p->tensor[i];
@@ -366,7 +376,8 @@ int msa_norm_rope(const msa_rope_problem* p, const uint16_t* const* x, const int
   a.T = p->tokens;
   int32_t sms = 0;
   if ((rc = sm_count_current(&sms))) return rc;
-  a.cut = rope::cut_rows(a.heads, a.T, sms, rope::kRowWarps);
+  a.cut = rope::cut_rows(a.heads, a.T, sms, rope::kRowCtas * (rope::kRowWarps + 1),
+                         rope::kRowWarps);
   a.status = d_status;
   return cache::launch_kernel(p->adjacent ? rope::norm_rope_kernel<true> : rope::norm_rope_kernel<false>,
                               dim3((unsigned)(a.cut.slices * a.cut.groups)), a.cut.threads(), sizeof(rope::RowsShared),

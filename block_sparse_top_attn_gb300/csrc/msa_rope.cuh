@@ -18,9 +18,10 @@ namespace msa {
 namespace rope {
 
 constexpr int kTensors = 4;   // q, k, q_index, k_index
-constexpr int kTile = 16;     // most tokens of a tile
+constexpr int kTile = 16;     // tokens of a table of angles
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kRowWarps = 8;  // warps of a CTA that take rows, beside one for the angles
 constexpr float kInf = __builtin_huge_valf();
 
 struct Angles {  // where a call's angles come from
@@ -58,9 +59,11 @@ MSA_DEV void lane_dims(int j, int R, int& a, int& b) {
 // so what the functions get is below 1/8 turn and as exact as its 24 bits.
 MSA_DEV void cos_sin(uint64_t turn, float scale, float& c, float& s) {
   const uint64_t shifted = turn + (1ull << 61);
-  const int64_t rest = (int64_t)(turn - (shifted & (3ull << 62)));
+  const uint64_t rest = turn - (shifted & (3ull << 62));
+  // in half turns: the high word times 2^-31, the low one times 2^-63
+  const float x = fmaf((float)(uint32_t)rest, 1.0842021724855044e-19f, (float)(int)(rest >> 32) * 4.656612873077393e-10f);
   float sn, cs;
-  sincospif((float)rest * 1.0842021724855044e-19f, &sn, &cs);  // 2^-63: half turns
+  sincospif(x, &sn, &cs);
   sn *= scale;
   cs *= scale;
   const int quarter = (int)(shifted >> 62);
@@ -90,9 +93,10 @@ MSA_DEV Pair load_pair(const Angles& a, int p) {
   if (x.axis != w.z) set_status(a.status, MSA_ERR_INVALID_ARGUMENT);
   return x;
 }
-// Fraction of a turn at token t.
+// Fraction of a turn at a position, and at token t.
+MSA_DEV uint64_t turn_at(const Pair& p, int position) { return p.turns * (uint64_t)(int64_t)position; }
 MSA_DEV uint64_t turn_of(const Angles& a, const Pair& p, int64_t t) {
-  return p.turns * (uint64_t)(int64_t)a.positions[t * a.A + p.axis];
+  return turn_at(p, a.positions[t * a.A + p.axis]);
 }
 
 // A tile's angles in shared memory: a row of [4][8] float4 per token, lane j's
@@ -104,35 +108,40 @@ struct Table {
   float4 cs[kRows][32];
   int live[kRows];  // the token is no padding
 };
-// Fills tables: a thread has the same two pairs in every row.
+// Fills tables, by `threads` threads of which this is `thread`: it has the same two
+// pairs in every row.
 template <bool kAdjacent>
 struct Filler {
   Pair p0, p1;
+  int thread;
   int at, row0, step;  // place in a row, the thread's first row, rows between two of its rows
-  MSA_DEV Filler(const Angles& a) {
+  MSA_DEV Filler(const Angles& a, int thread_, int threads) : thread(thread_) {
     const int lanes = a.R >> 4, row = 4 * lanes;
     p0 = p1 = Pair{0, 0};
     at = -1;
     row0 = step = 0;
     if (lanes == 0) return;
-    step = (int)blockDim.x / row;
-    row0 = (int)threadIdx.x / row;
+    step = threads / row;
+    row0 = thread / row;
     if (row0 >= step) return;
-    const int i = (int)threadIdx.x - row0 * row, e2 = i / lanes, j = i - e2 * lanes;
+    const int i = thread - row0 * row, e2 = i / lanes, j = i - e2 * lanes;
     at = e2 * 8 + j;
     p0 = load_pair(a, pair_of<kAdjacent>(j, 2 * e2, a.R));
     p1 = load_pair(a, pair_of<kAdjacent>(j, 2 * e2 + 1, a.R));
   }
+  // Of tokens t0, t0 + apart, .., n of them (no more than there are threads).
   template <int kRows>
-  MSA_DEV void fill(Table<kRows>& tab, const Angles& a, int64_t t0, int n) const {
-    if (at >= 0)
-      for (int row = row0; row < n; row += step) {
-        float4 x;
-        cos_sin(turn_of(a, p0, t0 + row), a.scale, x.x, x.z);
-        cos_sin(turn_of(a, p1, t0 + row), a.scale, x.y, x.w);
-        tab.cs[row][at] = x;
-      }
-    if ((int)threadIdx.x < n) tab.live[threadIdx.x] = a.positions[(t0 + threadIdx.x) * a.A] >= 0;
+  MSA_DEV void fill(Table<kRows>& tab, const Angles& a, int64_t t0, int n, int apart = 1) const {
+    if (thread < n) tab.live[thread] = a.positions[(t0 + (int64_t)thread * apart) * a.A] >= 0;
+    if (at < 0) return;
+#pragma unroll 4
+    for (int row = row0; row < n; row += step) {
+      const int64_t t = t0 + (int64_t)row * apart;
+      float4 x;
+      cos_sin(turn_of(a, p0, t), a.scale, x.x, x.z);
+      cos_sin(turn_of(a, p1, t), a.scale, x.y, x.w);
+      tab.cs[row][at] = x;
+    }
   }
 };
 
@@ -306,18 +315,19 @@ inline const Angles angles_of(const msa_rope_problem* p, const int32_t* position
 // heads one after the other) of a token, a warp's share; `units` of them to a
 // CTA's warps, `groups` CTAs side by side; with few units, `phases` warps take
 // tokens in turn.  A CTA keeps its heads, and so their weights, and takes one of
-// `slices` equal shares of the tokens, as many as `warps` of an SM hold.
+// `slices` equal shares of the tokens, every slices-th one, as many as `warps` of an
+// SM hold.
 struct Cut {
   int groups, units, phases, slices;
-  int threads() const { return 32 * units * phases; }
+  int threads() const { return 32 * (units * phases + 1); }  // and a warp for the angles
 };
-inline Cut cut_rows(int64_t heads, int64_t tokens, int64_t sms, int warps) {
+inline Cut cut_rows(int64_t heads, int64_t tokens, int64_t sms, int warps, int most_units) {
   const int64_t u = (heads + 3) / 4;
   Cut c;
-  c.groups = (int)((u + kWarps - 1) / kWarps);
+  c.groups = (int)((u + most_units - 1) / most_units);
   c.units = (int)((u + c.groups - 1) / c.groups);
-  c.phases = kWarps / c.units;
-  const int64_t most = sms * (warps / (c.units * c.phases)) / c.groups;
+  c.phases = most_units / c.units;
+  const int64_t most = sms * (warps / (c.units * c.phases + 1)) / c.groups;
   c.slices = (int)(tokens < most ? tokens : most > 1 ? most : 1);
   return c;
 }
@@ -376,29 +386,48 @@ MSA_DEV void copy_row(Stage& s, const uint16_t* row, int lane) {
   copy16(&s.row[r][granule_slot(j)], row + 8 * j);
   copy16(&s.row[r][granule_slot(j + 8)], row + 64 + 8 * j);
 }
+// Two tables in turn: the CTA's warps behind those of the rows (one, as a rule) fill
+// one while the others use the other.
+// (Filled by all warps, each its part, between a barrier and the next: 32k tokens x
+// 68 heads 203 us, and the warps' registers spill.)
+template <bool kAdjacent>
+MSA_DEV void fill_tables(const Angles& a, Table<kTile> (&tab)[2], int before, int64_t first, int n, int apart) {
+  const Filler<kAdjacent> filler(a, threadIdx.x - before, blockDim.x - before);
+  auto fill = [&](int k) {
+    if (k * kTile < n)
+      filler.fill(tab[k & 1], a, first + (int64_t)k * kTile * apart, min(n - k * kTile, kTile), apart);
+    __syncthreads();
+  };
+  fill(0);
+  for (int k = 0; k * kTile < n; ++k) fill(k + 1);
+}
 struct RowsShared {
   Table<kTile> tab[2];
-  Stage ring[kWarps][kStages];
+  Stage ring[kRowWarps][kStages];
 };
 
 template <bool kAdjacent>
 MSA_DEV void rows_block(const RowsArgs& a, int block, RowsShared& s) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, j = lane & 7;
   const int slice = block / a.cut.groups, group = block - slice * a.cut.groups;
-  const int64_t t0 = (int64_t)a.T * slice / a.cut.slices;
-  const int n = (int)((int64_t)a.T * (slice + 1) / a.cut.slices - t0);
+  const int apart = a.cut.slices, n = (a.T - slice + apart - 1) / apart;
+  if (warp >= a.cut.units * a.cut.phases) {
+    fill_tables<kAdjacent>(a.an, s.tab, 32 * a.cut.units * a.cut.phases, slice, n, apart);
+    return;
+  }
   const int phase = warp / a.cut.units, unit = group * a.cut.units + warp - phase * a.cut.units;
   const int hh = unit * 4 + (lane >> 3);
-  const bool mine = phase < a.cut.phases, live = mine && hh < a.heads;
+  const bool live = hh < a.heads;
   int da, db, head;
   lane_dims(j, a.an.R, da, db);
   const int k = tensor_of(a, live ? hh : 0, head);
   const Tensor& t = a.t[k];
   const int sa = granule_slot(da >> 3), sb = granule_slot(db >> 3);
   const int phases = a.cut.phases;
-  const int64_t x_step = phases * t.x_token, y_step = phases * a.y_token[k];
-  const uint16_t* x = t.x + (t0 + phase) * t.x_token + head * t.x_head;  // of the next row to copy
-  uint16_t* y = a.y[k] + (t0 + phase) * a.y_token[k] + head * a.y_head[k];
+  const int64_t first = slice + (int64_t)phase * apart, step = (int64_t)phases * apart;  // this warp's tokens
+  const int64_t x_step = step * t.x_token, y_step = step * a.y_token[k];
+  const uint16_t* x = t.x + first * t.x_token + head * t.x_head;  // of the next row to copy
+  uint16_t* y = a.y[k] + first * a.y_token[k] + head * a.y_head[k];
   Stage* ring = s.ring[warp];
   int ahead = phase;  // its token
   auto copy = [&](int stage) {
@@ -410,26 +439,23 @@ MSA_DEV void rows_block(const RowsArgs& a, int block, RowsShared& s) {
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) copy(i);
   const bool norm = t.flags & MSA_ROPE_NORM, turn = turns(t, j, a.an.R);
-  const Filler<kAdjacent> filler(a.an);
   Values w;
   load_weights<kAdjacent>(t, head, da, db, a.offset, w);
-  filler.fill(s.tab[0], a.an, t0, min(n, kTile));
-  __syncthreads();
-  int stage = 0, i = mine ? phase : n;
-  for (int at = 0, buf = 0; at < n; at += kTile, buf ^= 1) {
-    const int end = min(at + kTile, n);
-    if (end < n) filler.fill(s.tab[buf ^ 1], a.an, t0 + end, min(n - end, kTile));
-    for (; i < end; i += phases) {
+  __syncthreads();  // the first table
+  int stage = 0, i = phase;
+  for (int at = 0, table = 0; at < n; at += kTile, ++table) {
+    const Table<kTile>& tab = s.tab[table & 1];
+    for (; i < min(at + kTile, n); i += phases) {
       copies_wait<kStages - 2>();
       __syncwarp();  // the lanes' copies have landed; the stage before has been read
       const uint4* row = ring[stage].row[lane >> 3];
       uint4 ua = row[sa], ub = row[sb];
       copy((stage + kStages - 1) & (kStages - 1));
       stage = (stage + 1) & (kStages - 1);
-      if (s.tab[buf].live[i - at]) {
+      if (tab.live[i - at]) {
         Values v;
         unpack<kAdjacent>(ua, ub, v);
-        norm_rotate(v, w, s.tab[buf].cs[i - at], j, norm, turn, a.eps);
+        norm_rotate(v, w, tab.cs[i - at], j, norm, turn, a.eps);
         pack<kAdjacent>(v, ua, ub);
         if (live) {
           *reinterpret_cast<uint4*>(y + da) = ua;
@@ -438,7 +464,7 @@ MSA_DEV void rows_block(const RowsArgs& a, int block, RowsShared& s) {
       }
       y += y_step;
     }
-    __syncthreads();
+    __syncthreads();  // it has been read, the next one is there
   }
 }
 
