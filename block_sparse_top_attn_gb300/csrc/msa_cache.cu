@@ -280,7 +280,7 @@ inline int64_t row_blocks(int64_t tokens, int64_t heads, int64_t rows) {  // CTA
 // before it is overwritten is read before).
 MSA_DEV void index_chunk(const AppendArgs& a, int g) {
   IndexPlan x;
-  if (!plan_index(a, g, x)) return;
+  if (!plan_index(a, g, threadIdx.x == 0, x)) return;
   const int64_t hs = (int64_t)a.H * 128;  // elements from one token's row to the next
   for (int unit = threadIdx.x >> 5; unit < 2 * a.H; unit += blockDim.x >> 5) {
     const int d = unit * 64 + (threadIdx.x & 31) * 2;

@@ -162,10 +162,10 @@ struct IndexPlan {
   int p0, p1;        // positions to store
 };
 
-// False where the chunk has nothing to do or is not there; every thread of the
-// CTA calls it.
+// False where the chunk has nothing to do or is not there.  report: this thread
+// reports a row that does not fit.
 template <class Args>
-MSA_DEV bool plan_index(const Args& a, int g, IndexPlan& x) {
+MSA_DEV bool plan_index(const Args& a, int g, bool report, IndexPlan& x) {
   const int4 c = reinterpret_cast<const int4*>(a.chunks)[g];
   const int r = c.x, row0 = c.y, n = c.z, pos0 = c.w;
   if (r < 0) return false;
@@ -178,7 +178,7 @@ MSA_DEV bool plan_index(const Args& a, int g, IndexPlan& x) {
            pos0 <= a.positions - (cu1 - row0) && pos0 % a.B + n <= a.B;
   }
   if (!good) {
-    if (threadIdx.x == 0) set_status(a.status, MSA_ERR_INVALID_CACHE);
+    if (report) set_status(a.status, MSA_ERR_INVALID_CACHE);
     return false;
   }
   const int end = pos0 + (cu1 - row0);     // position behind the request's last new token

@@ -12,6 +12,8 @@ namespace rope {
 
 constexpr int kKvTile = 16;  // most tokens of a tile of K and V
 constexpr int kIndexRows = kThreads / 8;  // rows of a pass
+constexpr int kIndexTokens = 64;          // whose angles are made at once
+constexpr int kIndexHeads = 4;            // heads of index keys of a CTA
 
 struct AppendRopeArgs {
   RowsArgs q;    // q and q_index: rows in and out
@@ -27,7 +29,8 @@ struct AppendRopeArgs {
   int64_t slots;         // num_pages * B
   float k_mul, v_mul;    // 2^-exp
   bool wide;             // rows of v are aligned to 32 bytes
-  int index_blocks, kv_blocks;  // leading CTAs: pooled index keys, then K and V
+  int index_blocks, kv_blocks;  // CTAs of index keys, of K and V; the others take q's rows
+  int index_groups;                  // CTAs of a chunk's heads side by side
   int kv_tile, kv_groups, kv_heads;  // tokens of a tile; groups of heads side by side, heads of a group
   int32_t* status;
 };
@@ -294,19 +297,61 @@ MSA_DEV void kv_block(const AppendRopeArgs& a, int block, Table<kKvTile>& tab) {
 // ---------------------------------------------------------------------------
 // index keys
 // ---------------------------------------------------------------------------
+// A CTA takes eight chunks, a warp each.  A warp stores its chunk's rows to the
+// tail by itself (a decode step's one token, the last tokens of a prompt).  A chunk
+// that completes a block is the CTA's work, after that.
 struct IndexShared {
-  Table<kIndexRows> tab;
-  uint4 rows[kIndexRows][16];  // bf16, normed and rotated
+  union {
+    Table<kChunk> own[kWarps];
+    struct {
+      Table<kIndexTokens> tab;
+      uint4 rows[2][kIndexRows][16];  // bf16, normed and rotated
+    };
+  };
+  int average[kWarps];
 };
 
-// Index keys of one chunk, by one CTA: up to eight heads at a time, 32 rows of
+template <bool kAdjacent>
+MSA_DEV void store_tail(const AppendRopeArgs& a, const cache::IndexPlan& x, int first_head, int heads,
+                        Table<kChunk>& tab) {
+  const int lane = threadIdx.x & 31, j = lane & 7, n = x.p1 - x.p0;  // at most a chunk
+  const int64_t hs = (int64_t)a.H * 128, t0 = x.cu0 + x.p0 - x.past;
+  const bool norm = a.ki.flags & MSA_ROPE_NORM, turn = turns(a.ki, j, a.q.an.R);
+  int da, db;
+  lane_dims(j, a.q.an.R, da, db);
+  Filler<kAdjacent>(a.q.an, lane, 32).fill(tab, a.q.an, t0, n);
+  __syncwarp();
+  uint16_t* tail = a.index_tail + ((int64_t)x.r * 2 + (x.open & 1)) * a.B * hs;
+  for (int r0 = 0; r0 < n * heads; r0 += 4) {
+    const int r = r0 + (lane >> 3);
+    const bool live = r < n * heads;
+    const int i = live ? r / heads : 0, h = first_head + (live ? r - i * heads : 0);
+    uint4 ua = make_uint4(0, 0, 0, 0), ub = ua;
+    if (live) {
+      const uint16_t* src = a.ki.x + (t0 + i) * a.ki.x_token + h * a.ki.x_head;
+      ua = *reinterpret_cast<const uint4*>(src + da);
+      ub = *reinterpret_cast<const uint4*>(src + db);
+    }
+    Values v, w;
+    unpack<kAdjacent>(ua, ub, v);
+    load_weights<kAdjacent>(a.ki, h, da, db, a.q.offset, w);
+    norm_rotate(v, w, tab.cs[i], j, norm, turn, a.q.eps);
+    pack<kAdjacent>(v, ua, ub);
+    if (live) {
+      uint16_t* row = tail + ((x.p0 + i) % a.B) * hs + h * 128;
+      *reinterpret_cast<uint4*>(row + da) = ua;
+      *reinterpret_cast<uint4*>(row + db) = ub;
+    }
+  }
+}
+
+// A chunk that completes a block, by the CTA: up to eight heads at a time, 32 rows of
 // them (four tokens of eight heads, 32 tokens of one) per pass.  What is averaged
 // goes through shared memory and is added in the order of the tokens, so that the
 // mean does not depend on how a prompt was cut.
 template <bool kAdjacent>
-MSA_DEV void index_block(const AppendRopeArgs& a, int g, IndexShared& s) {
-  cache::IndexPlan x;
-  if (!cache::plan_index(a, g, x)) return;
+MSA_DEV void average_block(const AppendRopeArgs& a, const cache::IndexPlan& x, int first_head, int last_head,
+                           IndexShared& s) {
   const int tid = threadIdx.x, j = tid & 7;
   const int64_t hs = (int64_t)a.H * 128;
   const bool norm = a.ki.flags & MSA_ROPE_NORM, turn = turns(a.ki, j, a.q.an.R);
@@ -316,8 +361,8 @@ MSA_DEV void index_block(const AppendRopeArgs& a, int g, IndexShared& s) {
   const int64_t slot = x.last >= 0 ? a.slot_map[x.last] : -1;
   const bool average = slot >= 0 && slot < a.slots;  // else reported by the rows' own CTAs, or left out
   const int olds = average ? max(0, x.cu0 - (x.last - (a.B - 1))) : 0;  // tokens of earlier calls
-  for (int h0 = 0; h0 < a.H; h0 += 8) {
-    const int hn = min(8, a.H - h0);
+  for (int h0 = first_head; h0 < last_head; h0 += 8) {
+    const int hn = min(8, last_head - h0);
     const int hb = hn > 4 ? 8 : hn > 2 ? 4 : hn;  // rows of a token
     const int tb = kIndexRows / hb;
     const int hsub = (tid >> 3) & (hb - 1), tsub = (tid >> 3) / hb;
@@ -326,21 +371,37 @@ MSA_DEV void index_block(const AppendRopeArgs& a, int g, IndexShared& s) {
     Values w;
     load_weights<kAdjacent>(a.ki, h, da, db, a.q.offset, w);
     const uint16_t* src = a.ki.x + h * a.ki.x_head;
-    // tokens t .. t + n - 1 (n <= tb): this thread's part of its row
-    auto rows = [&](int64_t t, int n, uint4& oa, uint4& ob) {
-      uint4 ua = make_uint4(0, 0, 0, 0), ub = ua;
-      if (there && tsub < n) {
-        ua = *reinterpret_cast<const uint4*>(src + (t + tsub) * a.ki.x_token + da);
-        ub = *reinterpret_cast<const uint4*>(src + (t + tsub) * a.ki.x_token + db);
-      }
-      filler.fill(s.tab, a.q.an, t, n);
-      __syncthreads();
-      Values v;
-      unpack<kAdjacent>(ua, ub, v);
-      norm_rotate(v, w, s.tab.cs[tsub], j, norm, turn && tsub < n, a.q.eps);
-      pack<kAdjacent>(v, oa, ob);
-    };
     uint16_t* tail = a.index_tail + (int64_t)x.r * 2 * a.B * hs + h0 * 128;
+    // `count` tokens from t on, in passes of tb: this thread's part of its row to `take`, then a barrier, then `after`.
+    // The angles of 64 tokens are made at once: their loads and functions then overlap.
+    auto passes = [&](int64_t t, int count, auto take, auto after) {
+      uint4 ua, ub;
+      auto load = [&](int m) {
+        ua = ub = make_uint4(0, 0, 0, 0);
+        if (there && m + tsub < count) {
+          ua = *reinterpret_cast<const uint4*>(src + (t + m + tsub) * a.ki.x_token + da);
+          ub = *reinterpret_cast<const uint4*>(src + (t + m + tsub) * a.ki.x_token + db);
+        }
+      };
+      load(0);
+      for (int m = 0, p = 0; m < count; m += tb, p ^= 1) {
+        const int in_table = m % kIndexTokens;
+        if (in_table == 0) {  // the table before has been read: a barrier followed
+          filler.fill(s.tab, a.q.an, t + m, min(kIndexTokens, count - m));
+          __syncthreads();
+        }
+        Values v;
+        unpack<kAdjacent>(ua, ub, v);
+        load(m + tb);
+        const bool here = there && m + tsub < count;
+        norm_rotate(v, w, s.tab.cs[in_table + tsub], j, norm, turn && here, a.q.eps);
+        uint4 oa, ob;
+        pack<kAdjacent>(v, oa, ob);
+        take(m, p, here, oa, ob);
+        __syncthreads();
+        after(m, p);
+      }
+    };
     if (average) {
       // a thread adds two dims at a time of up to two words
       float lo[2] = {0.f, 0.f}, hi[2] = {0.f, 0.f};
@@ -350,25 +411,27 @@ MSA_DEV void index_block(const AppendRopeArgs& a, int g, IndexShared& s) {
         if (word < hn * 64)
           cache::add_rows(tail + (int64_t)(x.avg_blk & 1) * a.B * hs + 2 * word, hs, olds, lo[i], hi[i]);
       }
-      const int64_t first = x.last - (a.B - 1) + olds;
-      for (int m = 0; m < a.B - olds; m += tb) {
-        const int n = min(tb, a.B - olds - m);
-        uint4 oa, ob;
-        rows(first + m, n, oa, ob);
-        s.rows[tid >> 3][da >> 3] = oa;
-        s.rows[tid >> 3][db >> 3] = ob;
-        __syncthreads();
+      const int count = a.B - olds;
+      passes(x.last - (a.B - 1) + olds, count,
+             [&](int, int p, bool, uint4 oa, uint4 ob) {
+               s.rows[p][tid >> 3][da >> 3] = oa;
+               s.rows[p][tid >> 3][db >> 3] = ob;
+             },
+             [&](int m, int p) {
+               const int n = min(tb, count - m);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int word = tid + i * kThreads;
-          if (word < hn * 64)
-            for (int k = 0; k < n; ++k) {
-              const uint32_t u = reinterpret_cast<const uint32_t*>(s.rows[k * hb + (word >> 6)])[word & 63];
-              lo[i] = __fadd_rn(lo[i], __uint_as_float(u << 16));
-              hi[i] = __fadd_rn(hi[i], __uint_as_float(u & 0xFFFF0000u));
-            }
-        }
-      }
+               for (int i = 0; i < 2; ++i) {
+                 const int word = tid + i * kThreads;
+                 if (word < hn * 64) {
+                   const uint32_t* row = reinterpret_cast<const uint32_t*>(s.rows[p][word >> 6]) + (word & 63);
+                   for (int k = 0; k < n; ++k) {
+                     const uint32_t u = row[k * hb * 64];
+                     lo[i] = __fadd_rn(lo[i], __uint_as_float(u << 16));
+                     hi[i] = __fadd_rn(hi[i], __uint_as_float(u & 0xFFFF0000u));
+                   }
+                 }
+               }
+             });
       const float inv = 1.f / (float)a.B;  // a power of two: the product is the quotient
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -378,38 +441,66 @@ MSA_DEV void index_block(const AppendRopeArgs& a, int g, IndexShared& s) {
               pack_bf16x2(lo[i] * inv, hi[i] * inv);
       }
     }
-    // the rows of the incomplete block, behind the barrier in rows() that follows the tail's last reads
+    // the rows of the incomplete block, behind the barriers that follow the tail's last reads
+    __syncthreads();
     uint16_t* dst = tail + (int64_t)(x.open & 1) * a.B * hs + hsub * 128;
-    for (int q = x.p0; q < x.p1; q += tb) {
-      const int n = min(tb, x.p1 - q);
-      uint4 oa, ob;
-      rows(x.cu0 + q - x.past, n, oa, ob);
-      if (there && tsub < n) {
-        uint16_t* row = dst + ((q + tsub) % a.B) * hs;
-        *reinterpret_cast<uint4*>(row + da) = oa;
-        *reinterpret_cast<uint4*>(row + db) = ob;
-      }
-      __syncthreads();  // the table has been read
-    }
+    if (x.p0 < x.p1)
+      passes(x.cu0 + x.p0 - x.past, x.p1 - x.p0,
+             [&](int m, int, bool here, uint4 oa, uint4 ob) {
+               if (!here) return;
+               uint16_t* row = dst + ((x.p0 + m + tsub) % a.B) * hs;
+               *reinterpret_cast<uint4*>(row + da) = oa;
+               *reinterpret_cast<uint4*>(row + db) = ob;
+             },
+             [](int, int) {});
     __syncthreads();
   }
 }
 
+template <bool kAdjacent>
+MSA_DEV void index_block(const AppendRopeArgs& a, int block, IndexShared& s) {
+  const int row = block / a.index_groups, h0 = (block - row * a.index_groups) * kIndexHeads;
+  const int h1 = min(a.H, h0 + kIndexHeads);
+  const int warp = threadIdx.x >> 5, g0 = row * kWarps;
+  cache::IndexPlan x;
+  const bool todo = g0 + warp < a.NC && cache::plan_index(a, g0 + warp, (threadIdx.x & 31) == 0, x);
+  const bool average = todo && x.last >= 0;
+  if (todo && !average) store_tail<kAdjacent>(a, x, h0, h1 - h0, s.own[warp]);
+  if ((threadIdx.x & 31) == 0) s.average[warp] = average;
+  __syncthreads();
+  for (int i = 0; i < kWarps; ++i)
+    if (s.average[i]) {
+      cache::plan_index(a, g0 + i, false, x);
+      average_block<kAdjacent>(a, x, h0, h1, s);
+    }
+}
+
 constexpr int kAppendCtas = 2;  // of an SM
-static_assert(sizeof(IndexShared) <= sizeof(RowsShared), "one size for every CTA");
+constexpr size_t kAppendShared = sizeof(IndexShared) > sizeof(RowsShared) ? sizeof(IndexShared) : sizeof(RowsShared);
+// The CTAs of index keys come first: a block's mean takes longest.  Those of K and V
+// and of Q then take turns in proportion to their numbers: K's are bound by
+// instructions and Q's by memory, and an SM should hold both.
+MSA_DEV bool takes_turn(int64_t& block, int64_t count, int64_t of) {
+  const int64_t before = block * count / of, after = (block + 1) * count / of;
+  block = after > before ? before : block - before;
+  return after > before;
+}
 template <bool kAdjacent>
 __global__ void __launch_bounds__(kThreads, kAppendCtas) append_rope_kernel(AppendRopeArgs a) {
   extern __shared__ __align__(16) uint8_t s_raw[];
   cache::after_previous_kernel();
-  if (status_bad(a.status)) return;
-  int block = blockIdx.x;
+  // one decision for the CTA: another may set the status between two warps' reads
+  if (__syncthreads_or(status_bad(a.status))) return;
+  int64_t block = blockIdx.x;
   if (block < a.index_blocks) {
-    index_block<kAdjacent>(a, block, *reinterpret_cast<IndexShared*>(s_raw));
+    index_block<kAdjacent>(a, (int)block, *reinterpret_cast<IndexShared*>(s_raw));
     return;
   }
   block -= a.index_blocks;
-  if (block < a.kv_blocks) kv_block<kAdjacent>(a, block, *reinterpret_cast<Table<kKvTile>*>(s_raw));
-  else rows_block<kAdjacent>(a.q, block - a.kv_blocks, *reinterpret_cast<RowsShared*>(s_raw));
+  if (takes_turn(block, a.kv_blocks, (int64_t)gridDim.x - a.index_blocks))
+    kv_block<kAdjacent>(a, (int)block, *reinterpret_cast<Table<kKvTile>*>(s_raw));
+  else
+    rows_block<kAdjacent>(a.q, (int)block, *reinterpret_cast<RowsShared*>(s_raw));
 }
 
 }  // namespace rope
@@ -471,6 +562,8 @@ extern "C" int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_
   int64_t q_blocks = 0;
   if (a.q.heads) {
     a.q.cut = rope::cut_rows(a.q.heads, a.T, sms, rope::kAppendCtas * rope::kWarps, rope::kWarps - 1);
+    // shares of 64 tokens or fewer, so that they mix with the other CTAs
+    if (a.q.cut.slices < (a.T + 63) / 64) a.q.cut.slices = (a.T + 63) / 64;
     q_blocks = (int64_t)a.q.cut.slices * a.q.cut.groups;
   }
   a.k = tensor(MSA_ROPE_K, k, 0);
@@ -489,11 +582,12 @@ extern "C" int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_
   a.kv_heads = (H + a.kv_groups - 1) / a.kv_groups;
   a.kv_tile = rope::cut_tokens(a.T, a.kv_groups, sms, rope::kKvTile, 4);
   const int64_t kv_blocks = (int64_t)((a.T + a.kv_tile - 1) / a.kv_tile) * a.kv_groups;
-  const int64_t index_blocks = index ? c->chunk_cap : 0;
+  a.index_groups = (H + rope::kIndexHeads - 1) / rope::kIndexHeads;
+  const int64_t index_blocks = index ? ((int64_t)c->chunk_cap + rope::kWarps - 1) / rope::kWarps * a.index_groups : 0;
   if (index_blocks + kv_blocks + q_blocks > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
   a.index_blocks = (int)index_blocks;
   a.kv_blocks = (int)kv_blocks;
   return cache::launch_kernel(p->adjacent ? rope::append_rope_kernel<true> : rope::append_rope_kernel<false>,
                               dim3((unsigned)(index_blocks + kv_blocks + q_blocks)), rope::kThreads,
-                              sizeof(rope::RowsShared), stream, 1, a);
+                              rope::kAppendShared, stream, 1, a);
 }

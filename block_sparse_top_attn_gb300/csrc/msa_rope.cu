@@ -51,7 +51,7 @@ template <bool kAdjacent>
 __global__ void __launch_bounds__(kRowThreads, kRowCtas) norm_rope_kernel(RowsArgs a) {
   extern __shared__ __align__(16) uint8_t s_raw[];
   cache::after_previous_kernel();
-  if (status_bad(a.status)) return;
+  if (__syncthreads_or(status_bad(a.status))) return;  // one decision for the CTA
   rows_block<kAdjacent>(a, blockIdx.x, *reinterpret_cast<RowsShared*>(s_raw));
 }
 
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradCtas) norm_rope_bwd_kernel(
   extern __shared__ __align__(16) uint8_t s_raw[];
   GradShared& s = *reinterpret_cast<GradShared*>(s_raw);
   cache::after_previous_kernel();
-  if (status_bad(a.status)) return;
+  if (__syncthreads_or(status_bad(a.status))) return;  // one decision for the CTA
   const int tid = threadIdx.x, slice = blockIdx.x / a.cut.groups, group = blockIdx.x - slice * a.cut.groups;
   const int apart = a.cut.slices, n = (a.T - slice + apart - 1) / apart;
   const int row_threads = 32 * a.cut.units * a.cut.phases;
@@ -243,25 +243,26 @@ struct SumArgs {
   int32_t* status;
 };
 
-// A CTA adds up one row of weights: thread (part, dim) every eighth slice, sixteen
-// loads in flight (of 300 slices: one at a time 7 us, this way 2).
-constexpr int kSumParts = 8;
-__global__ void __launch_bounds__(128 * kSumParts) weight_sum_kernel(SumArgs a) {
-  __shared__ float s_part[kSumParts][128];
+// A CTA adds up 32 dims of one row of weights: a warp every 16th slice, sixteen loads
+// in flight.
+constexpr int kSumParts = 16;
+__global__ void __launch_bounds__(32 * kSumParts) weight_sum_kernel(SumArgs a) {
+  __shared__ float s_part[kSumParts][32];
   cache::after_previous_kernel();
-  if (status_bad(a.status)) return;
-  int row = blockIdx.x, slot = a.slot[0], per = a.per[0], wide = a.wide[0];
+  if (__syncthreads_or(status_bad(a.status))) return;
+  const int all = blockIdx.x >> 2;  // row of all tensors' weights
+  int row = all, slot = a.slot[0], per = a.per[0], wide = a.wide[0];
   void* dw = a.dw[0];
 #pragma unroll
   for (int i = 1; i < kTensors; ++i)
-    if ((int)blockIdx.x >= a.end[i - 1]) {
-      row = blockIdx.x - a.end[i - 1];
+    if (all >= a.end[i - 1]) {
+      row = all - a.end[i - 1];
       slot = a.slot[i];
       per = a.per[i];
       wide = a.wide[i];
       dw = a.dw[i];
     }
-  const int d = threadIdx.x & 127, part = threadIdx.x >> 7;
+  const int d = (blockIdx.x & 3) * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
   const int64_t step = (int64_t)a.slots * 128;
   float s = 0.f;
   for (int p = 0; p < per; ++p) {
@@ -274,12 +275,12 @@ __global__ void __launch_bounds__(128 * kSumParts) weight_sum_kernel(SumArgs a) 
       for (int i = 0; i < 16; ++i) s += x[i];
     }
   }
-  s_part[part][d] = s;
+  s_part[part][threadIdx.x & 31] = s;
   __syncthreads();
   if (part) return;
   s = 0.f;
 #pragma unroll
-  for (int i = 0; i < kSumParts; ++i) s += s_part[i][d];
+  for (int i = 0; i < kSumParts; ++i) s += s_part[i][threadIdx.x];
   if (wide) static_cast<float*>(dw)[(int64_t)row * 128 + d] = s;
   else static_cast<uint16_t*>(dw)[(int64_t)row * 128 + d] = (uint16_t)(pack_bf16x2(s, 0.f) & 0xFFFFu);
 }
@@ -446,7 +447,7 @@ int msa_norm_rope_bwd(const msa_rope_problem* p, const uint16_t* const* dy, cons
     if (rc) return rc;
   }
   if (rows == 0) return MSA_OK;
-  return cache::launch_kernel(rope::weight_sum_kernel, dim3((unsigned)rows), 128 * rope::kSumParts, 0, stream, 1, s);
+  return cache::launch_kernel(rope::weight_sum_kernel, dim3((unsigned)rows * 4), 32 * rope::kSumParts, 0, stream, 1, s);
 }
 
 }  // extern "C"
