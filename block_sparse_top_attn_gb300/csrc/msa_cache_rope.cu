@@ -10,7 +10,7 @@
 namespace msa {
 namespace rope {
 
-constexpr int kKvTile = 16;  // most tokens of a tile of K and V
+constexpr int kKvTile = 32;  // most tokens of a tile of K and V
 constexpr int kIndexRows = kThreads / 8;  // rows of a pass
 constexpr int kIndexTokens = 64;          // whose angles are made at once
 constexpr int kIndexHeads = 4;            // heads of index keys of a CTA
@@ -30,7 +30,7 @@ struct AppendRopeArgs {
   float k_mul, v_mul;    // 2^-exp
   bool wide;             // rows of v are aligned to 32 bytes
   int index_blocks, kv_blocks;  // CTAs of index keys, of K and V; the others take q's rows
-  int index_groups;                  // CTAs of a chunk's heads side by side
+  int index_groups, index_chunks;    // CTAs of a chunk's heads side by side; chunks of a CTA
   int kv_tile, kv_groups, kv_heads;  // tokens of a tile; groups of heads side by side, heads of a group
   int32_t* status;
 };
@@ -41,61 +41,42 @@ struct AppendRopeArgs {
 // The cache keeps a value by the interval it lies in, so an error of fp32 counts
 // only next to a border, and there by a whole code.  With amp = |a cos| + |b sin| and
 // u = 2^-24, fp32 forms y to within 23 u amp: 13.5 u for the normed a and b (the sum
-// of 128 squares in chains of 8 and 4 more additions, halved by the root; rsqrtf 2
-// ulp, two products), 5 u for the angle's function (1 ulp; its argument's rounding
-// and the scale), the products and the sum; the code's quotient adds 2 u.  What lies
-// nearer to a border than 32 u amp is decided in fp64, from the inputs: about one
-// value in 20,000, and a scale in 10,000.
+// of 128 squares in chains of 4 and 6 more additions, halved by the root; rsqrtf 2
+// ulp, two products, the weight's offset), 5 u for the angle's function (1 ulp; its
+// argument's rounding and the scale), the products and the sum; the code's quotient
+// adds 2 u.  A group with a value (or a scale) nearer to a border than 32 u amp is
+// done again in fp64, from the inputs, behind the others: one group in 1,000.
 constexpr float kUlps = 32.f;
 
-struct Row {  // where a K row comes from
-  const uint16_t* x;
-  int64_t w;  // first weight
-  int64_t t;  // token
-};
-
-// 1 / sqrt(mean + eps) of the rows in fp64; whole warps call it.
+// Dim `d` of a K row, normed (r: its inverse rms) and rotated, in fp64.
 template <bool kAdjacent>
-MSA_DEV double exact_inverse_rms(uint4 ua, uint4 ub, float eps, bool norm) {
-  Values u;
-  float v[16];
-  unpack<kAdjacent>(ua, ub, u);
-  in_order<kAdjacent>(u, v);
-  double s = 0.0;
-#pragma unroll 4
-  for (int i = 0; i < 16; ++i) s = fma((double)v[i], (double)v[i], s);
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return norm ? 1.0 / sqrt(s * (1.0 / 128.0) + (double)eps) : 1.0;
-}
-
-// Dim `d` of a K row, normed and rotated, in fp64.
-template <bool kAdjacent>
-__device__ __noinline__ double exact_value(const AppendRopeArgs& a, const Row& row, double r, int d) {
+MSA_DEV double exact_value(const AppendRopeArgs& a, const uint16_t* x, int head, int64_t t, double r, int d) {
   auto normed = [&](int i) {
-    double x = (double)__uint_as_float((uint32_t)row.x[i] << 16) * r;
+    double v = (double)__uint_as_float((uint32_t)x[i] << 16) * r;
     if ((a.k.flags & MSA_ROPE_NORM) && a.k.w) {
+      const int64_t at = (a.k.flags & MSA_ROPE_PER_HEAD ? head * 128 : 0) + i;
       const float w = a.k.flags & MSA_ROPE_WEIGHT_FP32
-                          ? static_cast<const float*>(a.k.w)[row.w + i]
-                          : __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.k.w)[row.w + i] << 16);
-      x *= (double)w + (double)a.q.offset;
+                          ? static_cast<const float*>(a.k.w)[at]
+                          : __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.k.w)[at] << 16);
+      v *= (double)w + (double)a.q.offset;
     }
-    return x;
+    return v;
   };
   const int R = a.q.an.R;
-  if (!(a.k.flags & MSA_ROPE_ROTATE) || d >= R) return normed(d);
+  const double own = normed(d);
+  if (!(a.k.flags & MSA_ROPE_ROTATE) || d >= R) return own;
   const bool second = kAdjacent ? d & 1 : d >= R / 2;
   const int p = kAdjacent ? d >> 1 : second ? d - R / 2 : d;
-  const int other = kAdjacent ? d ^ 1 : second ? p : d + R / 2;
+  const int partner = kAdjacent ? d ^ 1 : second ? p : d + R / 2;
   double s, c;
-  sincospi((double)(int64_t)turn_of(a.q.an, load_pair(a.q.an, p), row.t) * 1.0842021724855044e-19, &s, &c);  // 2^-63: half turns
-  const double x = normed(d), y = normed(other);
-  return (second ? fma(x, c, y * s) : fma(x, c, -(y * s))) * (double)a.q.an.scale;
+  // half turns
+  sincospi((double)(int64_t)turn_of(a.q.an, load_pair(a.q.an, p), t) * 1.0842021724855044e-19, &s, &c);
+  const double other = normed(partner);
+  return (second ? fma(own, c, other * s) : fma(own, c, -(other * s))) * (double)a.q.an.scale;
 }
 
-// e4m3 scale of a group whose largest magnitude (times 2^-exp) is exactly `amax`,
-// found from a scale nearby.
-__device__ __noinline__ uint32_t exact_scale(double amax, uint32_t s8) {
+// e4m3 scale of a group whose largest magnitude (times 2^-exp) is `amax`.
+MSA_DEV uint32_t exact_scale(double amax) {
   auto six_mids = [](uint32_t lo) {  // six times the border between scales lo and lo + 1
     const uint32_t h = cache::e4m3x2_to_half(lo | (lo + 1) << 8);
     return 3.0 * ((double)__half2float(__ushort_as_half((uint16_t)(h & 0xFFFFu))) +
@@ -105,6 +86,9 @@ __device__ __noinline__ uint32_t exact_scale(double amax, uint32_t s8) {
     const double m = six_mids(lo);
     return amax > m || (amax == m && (lo & 1));
   };
+  uint16_t s2;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s2) : "f"(0.f), "f"((float)(amax / 6.0)));
+  uint32_t s8 = s2 & 0xFFu;  // the scale or one beside it
   while (s8 < 126 && above(s8)) ++s8;
   while (s8 > 0 && !above(s8 - 1)) --s8;
   return s8;
@@ -113,14 +97,55 @@ MSA_DEV uint32_t exact_code(double y, double s) {
   const double m = fabs(y);
   const uint32_t c = (m > 0.25 * s) + (m >= 0.75 * s) + (m > 1.25 * s) + (m >= 1.75 * s) + (m > 2.5 * s) +
                      (m >= 3.5 * s) + (m > 5.0 * s);
-  return c && y < 0.0 ? c | 8u : c;
+  return c && y < 0.0 && s > 0.0 ? c | 8u : s > 0.0 ? c : 0u;
+}
+MSA_DEV float scale_value(uint32_t s8) {
+  return __half2float(__ushort_as_half((uint16_t)(cache::e4m3x2_to_half(s8) & 0xFFFFu)));
+}
+
+MSA_DEV uint8_t* cache_tile(const AppendRopeArgs& a, int64_t slot, int head, int& tok) {
+  const int lb = a.B == 128 ? 7 : 6;  // log2 of the block
+  const int off = (int)(slot & (a.B - 1));
+  tok = off % cache::kTile;
+  return a.cache + cache::tile_index(slot >> lb, head, a.H, a.B / cache::kTile, off / cache::kTile) *
+                       cache::kTileBytes;
+}
+
+// Codes and scale of 16 dims from dim0 on of token t's K row, in fp64, by a warp: lanes
+// 0 .. 15 a dim each (16 .. 31 the same ones).
+template <bool kAdjacent>
+MSA_DEV void exact_group(const AppendRopeArgs& a, int64_t t, int head, int dim0) {
+  const int lane = threadIdx.x & 31;
+  const uint16_t* x = a.k.x + t * a.k.x_token + head * a.k.x_head;
+  double r = 1.0;
+  if (a.k.flags & MSA_ROPE_NORM) {
+    const uint2 u = *reinterpret_cast<const uint2*>(x + lane * 4);
+    const double v[4] = {(double)__uint_as_float(u.x << 16), (double)__uint_as_float(u.x & 0xFFFF0000u),
+                         (double)__uint_as_float(u.y << 16), (double)__uint_as_float(u.y & 0xFFFF0000u)};
+    double s = v[0] * v[0] + v[1] * v[1] + v[2] * v[2] + v[3] * v[3];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    r = 1.0 / sqrt(s * (1.0 / 128.0) + (double)a.q.eps);
+  }
+  const double y = exact_value<kAdjacent>(a, x, head, t, r, dim0 + (lane & 15)) * (double)a.k_mul;
+  double m = fabs(y);
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const uint32_t s8 = exact_scale(m);
+  uint32_t codes = exact_code(y, (double)scale_value(s8)) << 4 * (lane & 7);
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) codes |= __shfl_xor_sync(0xffffffffu, codes, o);
+  int tok;
+  uint8_t* out = cache_tile(a, a.slot_map[t], head, tok);
+  if (lane == 0 || lane == 8)
+    *reinterpret_cast<uint32_t*>(out + cache::OFF_KC + tok * cache::kRowBytes + (dim0 >> 1) + (lane >> 1)) = codes;
+  if (lane == 0) out[cache::OFF_KS + tok * cache::kScales + (dim0 >> 4)] = (uint8_t)s8;
 }
 
 // Half of a scale group: a lane's eight values, its neighbour's the rest.
 struct Half {
-  float amax, amp;  // of the group, amax times 2^-exp
-  uint32_t scale;
-  bool nan, doubt;  // the scale needs fp64
+  uint32_t codes, scale;  // codes of the lane's eight, the group's scale
+  bool doubt;             // fp32 does not tell
 };
 // Distance of x from the nearest border of a rounding that keeps `kBits` mantissa
 // bits, in units of its last place; below `least` the kept bits are those of `least`.
@@ -129,52 +154,51 @@ MSA_DEV uint32_t border_distance(float x, float least) {
   const uint32_t z = __float_as_uint(x < least ? x + least : x) & ((1u << (23 - kBits)) - 1u);
   return __sad((int)z, 1 << (22 - kBits), 0u);
 }
-MSA_DEV Half group_scale(const float* v, float amp, float mul, bool exact) {
+// exact: the values are the inputs themselves, and rounded by quantize16's rule.
+MSA_DEV Half round_half(const float* v, float amp, float mul, bool exact) {
   Half h;
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  h.amp = fmaxf(amp, __shfl_xor_sync(0xffffffffu, amp, 1));
-  h.nan = m >= 0x7F800000u;
-  h.amax = __uint_as_float(m) * mul;
+  amp = fmaxf(amp, __shfl_xor_sync(0xffffffffu, amp, 1));
+  const float amax = __uint_as_float(m) * mul;
   constexpr float kSixth = 1.f / 6.f;
-  const float t0 = h.amax * kSixth;
-  const float t = h.amax < 4096.f ? __fmaf_rn(__fmaf_rn(-6.f, t0, h.amax), kSixth, t0) : t0;
+  const float t0 = amax * kSixth;
+  const float t = amax < 4096.f ? __fmaf_rn(__fmaf_rn(-6.f, t0, amax), kSixth, t0) : t0;
   uint16_t s2;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s2) : "f"(0.f), "f"(t));
-  h.scale = h.nan ? 0x7Fu : s2 & 0xFFu;
-  // relative error of t, in its last places; without a doubt where nothing is rounded
-  const float ulps = fmaf(h.amp * mul / h.amax, kUlps, 4.f);
-  h.doubt = !exact && !h.nan && h.amp > 0.f && t < 450.f && !((float)border_distance<3>(t, 0.015625f) > ulps);
-  return h;
-}
-MSA_DEV float scale_value(uint32_t s8) {
-  return __half2float(__ushort_as_half((uint16_t)(cache::e4m3x2_to_half(s8) & 0xFFFFu)));
-}
-// Codes of eight values; bits of those that need fp64.
-MSA_DEV uint32_t half_codes(const float* v, const Half& h, float mul, bool exact, uint32_t& doubt) {
-  doubt = 0;
-  if (h.nan || h.scale == 0) return 0;
+  h.scale = s2 & 0xFFu;
+  h.codes = 0;
+  h.doubt = false;
+  if (m >= 0x7F800000u) {
+    h.scale = 0x7F;  // a NaN scale: the group reads back as NaN
+    return h;
+  }
+  // the relative error of t, in its last places
+  if (!exact && amp > 0.f && t < 450.f)
+    h.doubt = !((float)border_distance<3>(t, 0.015625f) > fmaf(amp * mul / amax, kUlps, 4.f));
+  if (h.scale == 0) return h;
   const float inv = __frcp_rn(scale_value(h.scale)) * mul;
-  const uint32_t ulps = (uint32_t)fminf(fmaf(h.amp * inv, kUlps / 2.f, 3.f), 4194304.f);
+  const uint32_t ulps = (uint32_t)fminf(fmaf(amp * inv, kUlps / 2.f, 3.f), 4194304.f);
   float q[8];
+  uint32_t least = 0xFFFFFFFFu;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    q[i] = v[i] * inv;
-    if (exact) q[i] = __fadd_rn(__fmaf_rn(v[i], inv, 768.f), -768.f);  // quantize16's rule
-    else doubt |= (uint32_t)(border_distance<1>(fabsf(q[i]), 1.f) <= ulps) << i;
+    q[i] = exact ? __fadd_rn(__fmaf_rn(v[i], inv, 768.f), -768.f) : v[i] * inv;
+    least = min(least, border_distance<1>(fabsf(q[i]), 1.f));
   }
-  uint32_t out;
+  h.doubt |= !exact && least <= ulps;
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
       "mov.b32 %0, {a, b, c, d};\n\t}"
-      : "=r"(out)
+      : "=r"(h.codes)
       : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
-  return cache::unsigned_zeros(out);
+  h.codes = cache::unsigned_zeros(h.codes);
+  return h;
 }
 
 // Largest |a cos| + |b sin| of each granule of a normed row.
@@ -196,108 +220,92 @@ MSA_DEV void amplitudes(const Values& v, const float4* row, int j, bool turn, fl
 
 // K and V of a tile of tokens and a group of heads.
 template <bool kAdjacent>
-MSA_DEV void kv_block(const AppendRopeArgs& a, int block, Table<kKvTile>& tab) {
+MSA_DEV void kv_block(const AppendRopeArgs& a, int block, bool bad, Table<kKvTile>& tab) {
   const int tid = threadIdx.x, lane = tid & 31, j = lane & 7;
   const int tile = block / a.kv_groups, group = block - tile * a.kv_groups;
   const int64_t t0 = (int64_t)tile * a.kv_tile;
   const int n = (int)min((int64_t)a.kv_tile, a.T - t0);
   const int h0 = group * a.kv_heads, hn = min(a.kv_heads, a.H - h0);
-  const Filler<kAdjacent> filler(a.q.an, threadIdx.x, kThreads);
-  filler.fill(tab, a.q.an, t0, n);
-  __syncthreads();
   const bool norm = a.k.flags & MSA_ROPE_NORM, turn = turns(a.k, j, a.q.an.R);
   const bool exact = !norm && !turn;  // the lane's values are its inputs
   int da, db;
   lane_dims(j, a.q.an.R, da, db);
   const int shift = 31 - __clz(a.kv_tile);
   // four tokens of a head side by side in a warp: their cache rows follow one another
+  uint4 ua, ub;
+  uint32_t vw[8];
+  int64_t slot;
+  int first;  // position
+  auto load = [&](int u) {
+    const int i = u & (a.kv_tile - 1), hs = u >> shift;
+    ua = ub = make_uint4(0, 0, 0, 0);
+    slot = -1;
+    first = 0;
+    if (i < n && hs < hn) {
+      const int64_t t = t0 + i, h = h0 + hs;
+      const uint16_t* x = a.k.x + t * a.k.x_token + h * a.k.x_head;
+      slot = a.slot_map[t];
+      first = a.q.an.positions[t * a.q.an.A];
+      ua = *reinterpret_cast<const uint4*>(x + da);
+      ub = *reinterpret_cast<const uint4*>(x + db);
+      cache::load32(a.v + t * a.v_token + h * a.v_head + 16 * j, a.wide, vw);
+    }
+  };
+  load(tid >> 3);  // ahead of the angles: one chain of loads for both
+  Values w;
+  load_weights<kAdjacent>(a.k, h0, da, db, a.q.offset, w);
+  Filler<kAdjacent>(a.q.an, tid, kThreads).fill(tab, a.q.an, t0, n);
+  if (__syncthreads_or(bad)) return;
   for (int base = (tid >> 5) * 4; base < hn << shift; base += kThreads / 8) {
     const int u = base + (lane >> 3), i = u & (a.kv_tile - 1), hs = u >> shift, h = h0 + hs;
     const int64_t t = t0 + i;
+    if (base >= kThreads / 8) load(u);
+    if (a.k.flags & MSA_ROPE_PER_HEAD) load_weights<kAdjacent>(a.k, hs < hn ? h : h0, da, db, a.q.offset, w);
     bool live = i < n && hs < hn;
-    int64_t slot = -1;
-    if (live) {
-      slot = a.slot_map[t];
-      const bool padding = a.q.an.positions[t * a.q.an.A] < 0;
-      if (slot < 0 || slot >= a.slots || padding) {
-        if (slot != -1) set_status(a.status, MSA_ERR_INVALID_CACHE);
-        live = false;
-      }
+    if (live && (slot < 0 || slot >= a.slots || first < 0)) {
+      if (slot != -1) set_status(a.status, MSA_ERR_INVALID_CACHE);
+      live = false;
     }
-    uint4 ua = make_uint4(0, 0, 0, 0), ub = ua;
-    uint32_t vw[8] = {};
-    const Row row{a.k.x + t * a.k.x_token + h * a.k.x_head, a.k.flags & MSA_ROPE_PER_HEAD ? h * 128 : 0, t};
-    if (live) {
-      ua = *reinterpret_cast<const uint4*>(row.x + da);
-      ub = *reinterpret_cast<const uint4*>(row.x + db);
-      cache::load32(a.v + t * a.v_token + h * a.v_head + 16 * j, a.wide, vw);
-    }
-    Values val, w;
+    if (!live) ua = ub = make_uint4(0, 0, 0, 0);  // padding may hold anything
+    Values val;
     unpack<kAdjacent>(ua, ub, val);
-    load_weights<kAdjacent>(a.k, live ? h : 0, da, db, a.q.offset, w);
     normalize(val, w, norm, a.q.eps);
     float amp[2], v[16];
     amplitudes<kAdjacent>(val, tab.cs[i], j, turn, amp);
     if (turn) rotate<false>(val, tab.cs[i], j);
     in_order<kAdjacent>(val, v);
-    Half half[2];
+    const Half ha = round_half(v, amp[0], a.k_mul, exact), hb = round_half(v + 8, amp[1], a.k_mul, exact);
+    if (live) {
+      int tok;
+      uint8_t* out = cache_tile(a, slot, h, tok);
+      *reinterpret_cast<uint32_t*>(out + cache::OFF_KC + tok * cache::kRowBytes + (da >> 1)) = ha.codes;
+      *reinterpret_cast<uint32_t*>(out + cache::OFF_KC + tok * cache::kRowBytes + (db >> 1)) = hb.codes;
+      // of the two lanes of a group, one stores the first granules' scale, one the second's
+      out[cache::OFF_KS + tok * cache::kScales + ((j & 1 ? db : da) >> 4)] = (uint8_t)(j & 1 ? hb.scale : ha.scale);
+      uint2 vc;
+      const uint32_t vs = cache::quantize16(vw, a.v_mul, vc);
+      *reinterpret_cast<uint2*>(out + cache::OFF_VC + cache::v_code_offset(tok, j)) = vc;
+      out[cache::OFF_VS + j * cache::kTile + tok] = (uint8_t)vs;
+    }
 #pragma unroll
-    for (int s = 0; s < 2; ++s) half[s] = group_scale(v + 8 * s, amp[s], a.k_mul, exact);
-    double r64 = 0.0;
-    bool have = false;
-    if (__any_sync(0xffffffffu, half[0].doubt || half[1].doubt)) {
-      r64 = exact_inverse_rms<kAdjacent>(ua, ub, a.q.eps, norm);
-      have = true;
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const Half& x = half[s];
-        // the largest is among those within twice the error of it
-        const float least = x.amax - 2.f * kUlps * 5.9604644775390625e-8f * x.amp * a.k_mul;
-        uint32_t left = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) left |= (uint32_t)!(fabsf(v[8 * s + e]) * a.k_mul < least) << e;
-        double m = 0.0;
-        for (left = x.doubt && live ? left : 0; left; left &= left - 1)
-          m = fmax(m, fabs(exact_value<kAdjacent>(a, row, r64, (s ? db : da) + __ffs(left) - 1)));
-        m = fmax(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        if (x.doubt && live) half[s].scale = exact_scale(m * (double)a.k_mul, x.scale);
+    for (int s = 0; s < 2; ++s) {
+      const bool doubt = live && (s ? hb.doubt : ha.doubt);  // one of a group's lanes, or both
+      unsigned groups = __ballot_sync(0xffffffffu, doubt);
+      groups = (groups | groups >> 1) & 0x55555555u;
+      if (groups) __syncwarp();  // what is there of the group is overwritten
+      for (; groups; groups &= groups - 1) {
+        const int from = __ffs(groups) - 1;
+        exact_group<kAdjacent>(a, __shfl_sync(0xffffffffu, t, from), __shfl_sync(0xffffffffu, h, from),
+                               __shfl_sync(0xffffffffu, s ? db : da, from));
       }
     }
-    uint32_t codes[2], doubt[2];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) codes[s] = half_codes(v + 8 * s, half[s], a.k_mul, exact, doubt[s]);
-    if (__any_sync(0xffffffffu, doubt[0] | doubt[1])) {
-      if (!have) r64 = exact_inverse_rms<kAdjacent>(ua, ub, a.q.eps, norm);
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        for (uint32_t left = live ? doubt[s] : 0; left; left &= left - 1) {
-          const int e = __ffs(left) - 1;
-          const double y = exact_value<kAdjacent>(a, row, r64, (s ? db : da) + e);
-          const uint32_t c = exact_code(y * (double)a.k_mul, (double)scale_value(half[s].scale));
-          codes[s] = (codes[s] & ~(15u << 4 * e)) | c << 4 * e;
-        }
-    }
-    if (!live) continue;
-    uint2 vc;
-    const uint32_t vs = cache::quantize16(vw, a.v_mul, vc);
-    const int lb = a.B == 128 ? 7 : 6;  // log2 of the block
-    const int off = (int)(slot & (a.B - 1)), tok = off % cache::kTile;
-    uint8_t* out = a.cache + cache::tile_index(slot >> lb, h, a.H, a.B / cache::kTile, off / cache::kTile) *
-                                 cache::kTileBytes;
-    *reinterpret_cast<uint32_t*>(out + cache::OFF_KC + tok * cache::kRowBytes + (da >> 1)) = codes[0];
-    *reinterpret_cast<uint32_t*>(out + cache::OFF_KC + tok * cache::kRowBytes + (db >> 1)) = codes[1];
-    // of the two lanes of a group, one stores the first granules' scale, one the second's
-    out[cache::OFF_KS + tok * cache::kScales + ((j & 1 ? db : da) >> 4)] =
-        (uint8_t)(j & 1 ? half[1].scale : half[0].scale);
-    *reinterpret_cast<uint2*>(out + cache::OFF_VC + cache::v_code_offset(tok, j)) = vc;
-    out[cache::OFF_VS + j * cache::kTile + tok] = (uint8_t)vs;
   }
 }
 
 // ---------------------------------------------------------------------------
 // index keys
 // ---------------------------------------------------------------------------
-// A CTA takes eight chunks, a warp each.  A warp stores its chunk's rows to the
+// A CTA takes up to eight chunks, a warp each.  A warp stores its chunk's rows to the
 // tail by itself (a decode step's one token, the last tokens of a prompt).  A chunk
 // that completes a block is the CTA's work, after that.
 struct IndexShared {
@@ -458,24 +466,24 @@ MSA_DEV void average_block(const AppendRopeArgs& a, const cache::IndexPlan& x, i
 }
 
 template <bool kAdjacent>
-MSA_DEV void index_block(const AppendRopeArgs& a, int block, IndexShared& s) {
+MSA_DEV void index_block(const AppendRopeArgs& a, int block, bool bad, IndexShared& s) {
   const int row = block / a.index_groups, h0 = (block - row * a.index_groups) * kIndexHeads;
   const int h1 = min(a.H, h0 + kIndexHeads);
-  const int warp = threadIdx.x >> 5, g0 = row * kWarps;
+  const int warp = threadIdx.x >> 5, g0 = row * a.index_chunks;
   cache::IndexPlan x;
-  const bool todo = g0 + warp < a.NC && cache::plan_index(a, g0 + warp, (threadIdx.x & 31) == 0, x);
+  const bool todo = !__any_sync(0xffffffffu, bad) && warp < a.index_chunks && g0 + warp < a.NC &&
+                    cache::plan_index(a, g0 + warp, (threadIdx.x & 31) == 0, x);
   const bool average = todo && x.last >= 0;
   if (todo && !average) store_tail<kAdjacent>(a, x, h0, h1 - h0, s.own[warp]);
   if ((threadIdx.x & 31) == 0) s.average[warp] = average;
   __syncthreads();
-  for (int i = 0; i < kWarps; ++i)
+  for (int i = 0; i < a.index_chunks; ++i)
     if (s.average[i]) {
       cache::plan_index(a, g0 + i, false, x);
       average_block<kAdjacent>(a, x, h0, h1, s);
     }
 }
 
-constexpr int kAppendCtas = 2;  // of an SM
 constexpr size_t kAppendShared = sizeof(IndexShared) > sizeof(RowsShared) ? sizeof(IndexShared) : sizeof(RowsShared);
 // The CTAs of index keys come first: a block's mean takes longest.  Those of K and V
 // and of Q then take turns in proportion to their numbers: K's are bound by
@@ -485,22 +493,24 @@ MSA_DEV bool takes_turn(int64_t& block, int64_t count, int64_t of) {
   block = after > before ? before : block - before;
   return after > before;
 }
-template <bool kAdjacent>
-__global__ void __launch_bounds__(kThreads, kAppendCtas) append_rope_kernel(AppendRopeArgs a) {
+// kCtas: of an SM.  Two of them hold their values in registers (a step of 256 tokens 20
+// us, with three 23); large calls are bound by memory, where three count (4 x 8192
+// tokens 505 us, with three 461).
+template <bool kAdjacent, int kCtas>
+__global__ void __launch_bounds__(kThreads, kCtas) append_rope_kernel(AppendRopeArgs a) {
   extern __shared__ __align__(16) uint8_t s_raw[];
   cache::after_previous_kernel();
-  // one decision for the CTA: another may set the status between two warps' reads
-  if (__syncthreads_or(status_bad(a.status))) return;
+  const bool bad = status_bad(a.status);
   int64_t block = blockIdx.x;
   if (block < a.index_blocks) {
-    index_block<kAdjacent>(a, (int)block, *reinterpret_cast<IndexShared*>(s_raw));
+    index_block<kAdjacent>(a, (int)block, bad, *reinterpret_cast<IndexShared*>(s_raw));
     return;
   }
   block -= a.index_blocks;
   if (takes_turn(block, a.kv_blocks, (int64_t)gridDim.x - a.index_blocks))
-    kv_block<kAdjacent>(a, (int)block, *reinterpret_cast<Table<kKvTile>*>(s_raw));
+    kv_block<kAdjacent>(a, (int)block, bad, *reinterpret_cast<Table<kKvTile>*>(s_raw));
   else
-    rows_block<kAdjacent>(a.q, (int)block, *reinterpret_cast<RowsShared*>(s_raw));
+    rows_block<kAdjacent>(a.q, (int)block, bad, *reinterpret_cast<RowsShared*>(s_raw));
 }
 
 }  // namespace rope
@@ -559,13 +569,6 @@ extern "C" int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_
   a.q.T = a.T;
   a.q.heads = nq + ni;
   a.q.status = a.status = d_status;
-  int64_t q_blocks = 0;
-  if (a.q.heads) {
-    a.q.cut = rope::cut_rows(a.q.heads, a.T, sms, rope::kAppendCtas * rope::kWarps, rope::kWarps - 1);
-    // shares of 64 tokens or fewer, so that they mix with the other CTAs
-    if (a.q.cut.slices < (a.T + 63) / 64) a.q.cut.slices = (a.T + 63) / 64;
-    q_blocks = (int64_t)a.q.cut.slices * a.q.cut.groups;
-  }
   a.k = tensor(MSA_ROPE_K, k, 0);
   a.ki = tensor(MSA_ROPE_K_INDEX, k_index, 0);
   a.v = v;
@@ -580,14 +583,32 @@ extern "C" int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_
   a.v_mul = cache::exp2i(-c->v_exp);
   a.kv_groups = (H + 7) / 8;
   a.kv_heads = (H + a.kv_groups - 1) / a.kv_groups;
-  a.kv_tile = rope::cut_tokens(a.T, a.kv_groups, sms, rope::kKvTile, 4);
+  int rows = 4;  // tokens that give a CTA's eight warps work
+  while (rows < rope::kKvTile && rows * a.kv_heads < rope::kIndexRows) rows *= 2;
+  a.kv_tile = rope::cut_tokens(a.T, a.kv_groups, sms, rows < 16 ? 16 : rows, rows);
   const int64_t kv_blocks = (int64_t)((a.T + a.kv_tile - 1) / a.kv_tile) * a.kv_groups;
+  // chunks of a CTA: fewer where the CTAs find room, so that blocks that end in neighbouring chunks (requests of one
+  // length) do not wait for one another
   a.index_groups = (H + rope::kIndexHeads - 1) / rope::kIndexHeads;
-  const int64_t index_blocks = index ? ((int64_t)c->chunk_cap + rope::kWarps - 1) / rope::kWarps * a.index_groups : 0;
+  a.index_chunks = rope::kWarps;
+  auto index_ctas = [&](int64_t chunks) { return (c->chunk_cap + chunks - 1) / chunks * a.index_groups; };
+  while (a.index_chunks > 1 && index_ctas(a.index_chunks / 2) <= sms) a.index_chunks /= 2;
+  const int64_t index_blocks = index ? index_ctas(a.index_chunks) : 0;
+  int64_t q_blocks = 0;
+  if (a.q.heads) {
+    a.q.cut = rope::cut_rows(a.q.heads, a.T, sms, 2 * rope::kWarps, rope::kWarps - 1);
+    // shares of 12 to 64 tokens: few enough CTAs for a step's to run at once, enough to mix with K's in a large call
+    const int64_t per = (int64_t)a.T * a.q.cut.groups / (8 * (int64_t)sms);
+    const int64_t tokens = per < 12 ? 12 : per > 64 ? 64 : per;
+    a.q.cut.slices = (int)((a.T + tokens - 1) / tokens);
+    q_blocks = (int64_t)a.q.cut.slices * a.q.cut.groups;
+  }
   if (index_blocks + kv_blocks + q_blocks > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
   a.index_blocks = (int)index_blocks;
   a.kv_blocks = (int)kv_blocks;
-  return cache::launch_kernel(p->adjacent ? rope::append_rope_kernel<true> : rope::append_rope_kernel<false>,
-                              dim3((unsigned)(index_blocks + kv_blocks + q_blocks)), rope::kThreads,
+  const bool large = index_blocks + kv_blocks + q_blocks > 8 * (int64_t)sms;
+  auto* kernel = p->adjacent ? (large ? rope::append_rope_kernel<true, 3> : rope::append_rope_kernel<true, 2>)
+                             : (large ? rope::append_rope_kernel<false, 3> : rope::append_rope_kernel<false, 2>);
+  return cache::launch_kernel(kernel, dim3((unsigned)(index_blocks + kv_blocks + q_blocks)), rope::kThreads,
                               rope::kAppendShared, stream, 1, a);
 }

@@ -42,17 +42,17 @@ int check_problem(const msa_rope_problem* p) {
   return MSA_OK;
 }
 
-// CTAs of the largest size on an SM.  More of them read no faster and keep more of
-// the memory's rows open at once: 131k tokens x 152 heads take 1600 us with two,
-// 1725 with three; 32k x 68 180 and 208.
-constexpr int kRowCtas = 2;
+constexpr int kRowCtas = 3;  // of the largest size on an SM
+// Most tokens of a CTA: SMs differ in speed, and shares that all start at once end
+// when the slowest does (131k tokens x 152 heads 1725 us, in shares of 32 tokens
+// 1464; 32k x 68 208 and 172).
+constexpr int kRowTokens = 32;
 constexpr int kRowThreads = 32 * (kRowWarps + 1);
 template <bool kAdjacent>
 __global__ void __launch_bounds__(kRowThreads, kRowCtas) norm_rope_kernel(RowsArgs a) {
   extern __shared__ __align__(16) uint8_t s_raw[];
   cache::after_previous_kernel();
-  if (__syncthreads_or(status_bad(a.status))) return;  // one decision for the CTA
-  rows_block<kAdjacent>(a, blockIdx.x, *reinterpret_cast<RowsShared*>(s_raw));
+  rows_block<kAdjacent>(a, blockIdx.x, status_bad(a.status), *reinterpret_cast<RowsShared*>(s_raw));
 }
 
 // ---------------------------------------------------------------------------
@@ -88,9 +88,9 @@ struct GradShared {
   };
 };
 
-// The rows of one warp.
+// The rows of one warp; false if the status was set (rows_block).
 template <bool kAdjacent>
-MSA_DEV void grad_rows(const GradArgs& a, GradShared& s, int slice, int group, int n, int apart) {
+MSA_DEV bool grad_rows(const GradArgs& a, GradShared& s, bool bad, int slice, int group, int n, int apart) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane & 7;
   const int phase = warp / a.cut.units, unit = group * a.cut.units + warp - phase * a.cut.units;
   const int hh = unit * 4 + (lane >> 3);
@@ -128,7 +128,10 @@ MSA_DEV void grad_rows(const GradArgs& a, GradShared& s, int slice, int group, i
   load_weights<kAdjacent>(t, head, da, db, a.offset, w);
 #pragma unroll
   for (int i = 0; i < 4; ++i) dw.a[i] = dw.b[i] = 0;
-  __syncthreads();  // the first table
+  if (__syncthreads_or(bad)) {  // the first table is there
+    copies_wait<0>();
+    return false;
+  }
   int stage = 0, next = kGradStages - 1, i = phase;
   for (int at = 0, table = 0; at < n; at += kTile, ++table) {
     const Table<kTile>& tab = s.tab[table & 1];
@@ -191,6 +194,7 @@ MSA_DEV void grad_rows(const GradArgs& a, GradShared& s, int slice, int group, i
     row[da + e] = live ? sums[e] : 0.f;
     row[db + e] = live ? sums[8 + e] : 0.f;
   }
+  return true;
 }
 
 template <bool kAdjacent>
@@ -198,12 +202,15 @@ __global__ void __launch_bounds__(kGradThreads, kGradCtas) norm_rope_bwd_kernel(
   extern __shared__ __align__(16) uint8_t s_raw[];
   GradShared& s = *reinterpret_cast<GradShared*>(s_raw);
   cache::after_previous_kernel();
-  if (__syncthreads_or(status_bad(a.status))) return;  // one decision for the CTA
+  const bool bad = status_bad(a.status);
   const int tid = threadIdx.x, slice = blockIdx.x / a.cut.groups, group = blockIdx.x - slice * a.cut.groups;
   const int apart = a.cut.slices, n = (a.T - slice + apart - 1) / apart;
   const int row_threads = 32 * a.cut.units * a.cut.phases;
-  if (tid >= row_threads) fill_tables<kAdjacent>(a.an, s.tab, row_threads, slice, n, apart);
-  else grad_rows<kAdjacent>(a, s, slice, group, n, apart);
+  if (tid >= row_threads) {
+    if (!fill_tables<kAdjacent>(a.an, s.tab, bad, row_threads, slice, n, apart)) return;
+  } else if (!grad_rows<kAdjacent>(a, s, bad, slice, group, n, apart)) {
+    return;
+  }
   // the CTA's sums: heads that share a weight in the order of the warps and rows
   __syncthreads();
   // threads behind the last 128 of the CTA have no part in it
@@ -379,6 +386,7 @@ int msa_norm_rope(const msa_rope_problem* p, const uint16_t* const* x, const int
   if ((rc = sm_count_current(&sms))) return rc;
   a.cut = rope::cut_rows(a.heads, a.T, sms, rope::kRowCtas * (rope::kRowWarps + 1),
                          rope::kRowWarps);
+  a.cut.at_most(a.T, rope::kRowTokens);
   a.status = d_status;
   return cache::launch_kernel(p->adjacent ? rope::norm_rope_kernel<true> : rope::norm_rope_kernel<false>,
                               dim3((unsigned)(a.cut.slices * a.cut.groups)), a.cut.threads(), sizeof(rope::RowsShared),

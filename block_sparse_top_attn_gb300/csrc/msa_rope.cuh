@@ -18,7 +18,7 @@ namespace msa {
 namespace rope {
 
 constexpr int kTensors = 4;   // q, k, q_index, k_index
-constexpr int kTile = 16;     // tokens of a table of angles
+constexpr int kTile = 8;      // tokens of a table of angles
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRowWarps = 8;  // warps of a CTA that take rows, beside one for the angles
@@ -319,6 +319,10 @@ inline const Angles angles_of(const msa_rope_problem* p, const int32_t* position
 // SM hold.
 struct Cut {
   int groups, units, phases, slices;
+  void at_most(int64_t tokens, int64_t per_cta) {
+    const int64_t least = (tokens + per_cta - 1) / per_cta;
+    if (slices < least) slices = (int)least;
+  }
   int threads() const { return 32 * (units * phases + 1); }  // and a warp for the angles
 };
 inline Cut cut_rows(int64_t heads, int64_t tokens, int64_t sms, int warps, int most_units) {
@@ -391,28 +395,36 @@ MSA_DEV void copy_row(Stage& s, const uint16_t* row, int lane) {
 // (Filled by all warps, each its part, between a barrier and the next: 32k tokens x
 // 68 heads 203 us, and the warps' registers spill.)
 template <bool kAdjacent>
-MSA_DEV void fill_tables(const Angles& a, Table<kTile> (&tab)[2], int before, int64_t first, int n, int apart) {
+MSA_DEV bool fill_tables(const Angles& a, Table<kTile> (&tab)[2], bool bad, int before, int64_t first, int n,
+                         int apart) {
   const Filler<kAdjacent> filler(a, threadIdx.x - before, blockDim.x - before);
   auto fill = [&](int k) {
     if (k * kTile < n)
       filler.fill(tab[k & 1], a, first + (int64_t)k * kTile * apart, min(n - k * kTile, kTile), apart);
-    __syncthreads();
   };
   fill(0);
-  for (int k = 0; k * kTile < n; ++k) fill(k + 1);
+  if (__syncthreads_or(bad)) return false;
+  for (int k = 0; k * kTile < n; ++k) {
+    fill(k + 1);
+    __syncthreads();
+  }
+  return true;
 }
 struct RowsShared {
   Table<kTile> tab[2];
   Stage ring[kRowWarps][kStages];
 };
 
+// bad: the status was set before the call.  The CTA decides on it at its first
+// barrier, so that the load does not hold up the others, and as a whole: another
+// CTA may set the status between two warps' reads.
 template <bool kAdjacent>
-MSA_DEV void rows_block(const RowsArgs& a, int block, RowsShared& s) {
+MSA_DEV void rows_block(const RowsArgs& a, int block, bool bad, RowsShared& s) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, j = lane & 7;
   const int slice = block / a.cut.groups, group = block - slice * a.cut.groups;
   const int apart = a.cut.slices, n = (a.T - slice + apart - 1) / apart;
   if (warp >= a.cut.units * a.cut.phases) {
-    fill_tables<kAdjacent>(a.an, s.tab, 32 * a.cut.units * a.cut.phases, slice, n, apart);
+    fill_tables<kAdjacent>(a.an, s.tab, bad, 32 * a.cut.units * a.cut.phases, slice, n, apart);
     return;
   }
   const int phase = warp / a.cut.units, unit = group * a.cut.units + warp - phase * a.cut.units;
@@ -441,7 +453,10 @@ MSA_DEV void rows_block(const RowsArgs& a, int block, RowsShared& s) {
   const bool norm = t.flags & MSA_ROPE_NORM, turn = turns(t, j, a.an.R);
   Values w;
   load_weights<kAdjacent>(t, head, da, db, a.offset, w);
-  __syncthreads();  // the first table
+  if (__syncthreads_or(bad)) {  // the first table is there
+    copies_wait<0>();
+    return;
+  }
   int stage = 0, i = phase;
   for (int at = 0, table = 0; at < n; at += kTile, ++table) {
     const Table<kTile>& tab = s.tab[table & 1];
