@@ -13,7 +13,7 @@ namespace rope {
 constexpr int kKvTile = 32;  // most tokens of a tile of K and V
 constexpr int kIndexRows = kThreads / 8;  // rows of a pass
 constexpr int kIndexTokens = 64;          // whose angles are made at once
-constexpr int kIndexHeads = 4;            // heads of index keys of a CTA
+constexpr int kIndexHeads = 2;            // heads of index keys of a CTA: 1 or 2
 
 struct AppendRopeArgs {
   RowsArgs q;    // q and q_index: rows in and out
@@ -48,59 +48,71 @@ struct AppendRopeArgs {
 // done again in fp64, from the inputs, behind the others: one group in 1,000.
 constexpr float kUlps = 32.f;
 
-// Dim `d` of a K row, normed (r: its inverse rms) and rotated, in fp64.
+// Dim `d` of a K row times its weight and rotated, in fp64; what is left of the norm
+// is the row's inverse rms.
 template <bool kAdjacent>
-MSA_DEV double exact_value(const AppendRopeArgs& a, const uint16_t* x, int head, int64_t t, double r, int d) {
-  auto normed = [&](int i) {
-    double v = (double)__uint_as_float((uint32_t)x[i] << 16) * r;
-    if ((a.k.flags & MSA_ROPE_NORM) && a.k.w) {
-      const int64_t at = (a.k.flags & MSA_ROPE_PER_HEAD ? head * 128 : 0) + i;
-      const float w = a.k.flags & MSA_ROPE_WEIGHT_FP32
-                          ? static_cast<const float*>(a.k.w)[at]
-                          : __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.k.w)[at] << 16);
-      v *= (double)w + (double)a.q.offset;
-    }
-    return v;
+MSA_DEV double turned_dim(const AppendRopeArgs& a, const uint16_t* x, int head, int64_t t, int d) {
+  auto weighted = [&](int i) {
+    const double v = (double)__uint_as_float((uint32_t)x[i] << 16);
+    if (!(a.k.flags & MSA_ROPE_NORM) || !a.k.w) return v;
+    const int64_t at = (a.k.flags & MSA_ROPE_PER_HEAD ? head * 128 : 0) + i;
+    const float w = a.k.flags & MSA_ROPE_WEIGHT_FP32
+                        ? static_cast<const float*>(a.k.w)[at]
+                        : __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.k.w)[at] << 16);
+    return v * ((double)w + (double)a.q.offset);
   };
   const int R = a.q.an.R;
-  const double own = normed(d);
+  const double own = weighted(d);
   if (!(a.k.flags & MSA_ROPE_ROTATE) || d >= R) return own;
   const bool second = kAdjacent ? d & 1 : d >= R / 2;
   const int p = kAdjacent ? d >> 1 : second ? d - R / 2 : d;
   const int partner = kAdjacent ? d ^ 1 : second ? p : d + R / 2;
+  const double other = weighted(partner);
   double s, c;
   // half turns
   sincospi((double)(int64_t)turn_of(a.q.an, load_pair(a.q.an, p), t) * 1.0842021724855044e-19, &s, &c);
-  const double other = normed(partner);
   return (second ? fma(own, c, other * s) : fma(own, c, -(other * s))) * (double)a.q.an.scale;
 }
 
+MSA_DEV float scale_value(uint32_t s8) {
+  return __half2float(__ushort_as_half((uint16_t)(cache::e4m3x2_to_half(s8) & 0xFFFFu)));
+}
+
+// A non-negative fp64 value as two fp32: compared with a border that fp32 holds, the
+// second part decides where the first is equal.
+struct Split {
+  float hi, lo;
+};
+MSA_DEV Split split(double x) {
+  Split s;
+  s.hi = (float)x;
+  s.lo = s.hi < kInf ? (float)(x - (double)s.hi) : 0.f;
+  return s;
+}
+// x lies above the border, or on it and `up`.
+MSA_DEV bool beyond(const Split& x, float border, bool up) {
+  return x.hi > border || (x.hi == border && (x.lo > 0.f || (x.lo == 0.f && up)));
+}
 // e4m3 scale of a group whose largest magnitude (times 2^-exp) is `amax`.
-MSA_DEV uint32_t exact_scale(double amax) {
-  auto six_mids = [](uint32_t lo) {  // six times the border between scales lo and lo + 1
-    const uint32_t h = cache::e4m3x2_to_half(lo | (lo + 1) << 8);
-    return 3.0 * ((double)__half2float(__ushort_as_half((uint16_t)(h & 0xFFFFu))) +
-                  (double)__half2float(__ushort_as_half((uint16_t)(h >> 16))));
-  };
+MSA_DEV uint32_t exact_scale(const Split& amax) {
   auto above = [&](uint32_t lo) {  // of lo and lo + 1, the upper one is nearer (a tie goes to the even one)
-    const double m = six_mids(lo);
-    return amax > m || (amax == m && (lo & 1));
+    const uint32_t h = cache::e4m3x2_to_half(lo | (lo + 1) << 8);  // six times their middle has 8 bits at most
+    return beyond(amax, 3.f * (__half2float(__ushort_as_half((uint16_t)(h & 0xFFFFu))) +
+                               __half2float(__ushort_as_half((uint16_t)(h >> 16)))), lo & 1);
   };
   uint16_t s2;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s2) : "f"(0.f), "f"((float)(amax / 6.0)));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s2) : "f"(0.f), "f"(amax.hi * (1.f / 6.f)));
   uint32_t s8 = s2 & 0xFFu;  // the scale or one beside it
   while (s8 < 126 && above(s8)) ++s8;
   while (s8 > 0 && !above(s8 - 1)) --s8;
   return s8;
 }
-MSA_DEV uint32_t exact_code(double y, double s) {
-  const double m = fabs(y);
-  const uint32_t c = (m > 0.25 * s) + (m >= 0.75 * s) + (m > 1.25 * s) + (m >= 1.75 * s) + (m > 2.5 * s) +
-                     (m >= 3.5 * s) + (m > 5.0 * s);
-  return c && y < 0.0 && s > 0.0 ? c | 8u : s > 0.0 ? c : 0u;
-}
-MSA_DEV float scale_value(uint32_t s8) {
-  return __half2float(__ushort_as_half((uint16_t)(cache::e4m3x2_to_half(s8) & 0xFFFFu)));
+MSA_DEV uint32_t exact_code(const Split& m, bool negative, float s) {
+  if (!(s > 0.f)) return 0;
+  const uint32_t c = beyond(m, 0.25f * s, false) + beyond(m, 0.75f * s, true) + beyond(m, 1.25f * s, false) +
+                     beyond(m, 1.75f * s, true) + beyond(m, 2.5f * s, false) + beyond(m, 3.5f * s, true) +
+                     beyond(m, 5.f * s, false);
+  return c && negative ? c | 8u : c;
 }
 
 MSA_DEV uint8_t* cache_tile(const AppendRopeArgs& a, int64_t slot, int head, int& tok) {
@@ -117,22 +129,28 @@ template <bool kAdjacent>
 MSA_DEV void exact_group(const AppendRopeArgs& a, int64_t t, int head, int dim0) {
   const int lane = threadIdx.x & 31;
   const uint16_t* x = a.k.x + t * a.k.x_token + head * a.k.x_head;
+  const int d = dim0 + (lane & 15);
+  const double turned = turned_dim<kAdjacent>(a, x, head, t, d);
   double r = 1.0;
   if (a.k.flags & MSA_ROPE_NORM) {
     const uint2 u = *reinterpret_cast<const uint2*>(x + lane * 4);
     const double v[4] = {(double)__uint_as_float(u.x << 16), (double)__uint_as_float(u.x & 0xFFFF0000u),
                          (double)__uint_as_float(u.y << 16), (double)__uint_as_float(u.y & 0xFFFF0000u)};
-    double s = v[0] * v[0] + v[1] * v[1] + v[2] * v[2] + v[3] * v[3];
+    double s = (v[0] * v[0] + v[1] * v[1]) + (v[2] * v[2] + v[3] * v[3]);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    r = 1.0 / sqrt(s * (1.0 / 128.0) + (double)a.q.eps);
+    r = rsqrt(s * (1.0 / 128.0) + (double)a.q.eps);
   }
-  const double y = exact_value<kAdjacent>(a, x, head, t, r, dim0 + (lane & 15)) * (double)a.k_mul;
-  double m = fabs(y);
+  const double y = turned * (r * (double)a.k_mul);
+  const Split own = split(fabs(y));
+  Split m = own;
 #pragma unroll
-  for (int o = 1; o < 16; o <<= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = 1; o < 16; o <<= 1) {
+    const Split other{__shfl_xor_sync(0xffffffffu, m.hi, o), __shfl_xor_sync(0xffffffffu, m.lo, o)};
+    if (other.hi > m.hi || (other.hi == m.hi && other.lo > m.lo)) m = other;
+  }
   const uint32_t s8 = exact_scale(m);
-  uint32_t codes = exact_code(y, (double)scale_value(s8)) << 4 * (lane & 7);
+  uint32_t codes = exact_code(own, y < 0.0, scale_value(s8)) << 4 * (lane & 7);
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) codes |= __shfl_xor_sync(0xffffffffu, codes, o);
   int tok;
@@ -305,182 +323,175 @@ MSA_DEV void kv_block(const AppendRopeArgs& a, int block, bool bad, Table<kKvTil
 // ---------------------------------------------------------------------------
 // index keys
 // ---------------------------------------------------------------------------
-// A CTA takes up to eight chunks, a warp each.  A warp stores its chunk's rows to the
-// tail by itself (a decode step's one token, the last tokens of a prompt).  A chunk
-// that completes a block is the CTA's work, after that.
+// A CTA takes up to two heads of up to eight chunks, a warp each.  A warp stores its
+// chunk's rows to the tail by itself (a decode step's one token, the last tokens of
+// a prompt).  A chunk that completes a block is the CTA's work, after that.  All of a
+// warp's or CTA's loads are under way together, the angles made behind them.
 struct IndexShared {
   union {
     Table<kChunk> own[kWarps];
     struct {
       Table<kIndexTokens> tab;
-      uint4 rows[2][kIndexRows][16];  // bf16, normed and rotated
+      uint4 rows[kIndexTokens][kIndexHeads][16];  // bf16, normed and rotated
     };
   };
   int average[kWarps];
 };
 
+// Up to four rows of a lane's row group: loaded, then normed and rotated.
+struct IndexRows {
+  uint4 ua[4], ub[4];
+};
+constexpr int kIndexSteps = 4;
+static_assert(kIndexTokens * kIndexHeads <= kIndexSteps * kIndexRows && kChunk * kIndexHeads <= kIndexSteps * 4,
+              "a CTA's rows of 64 tokens and a warp's of a chunk");
+
 template <bool kAdjacent>
-MSA_DEV void store_tail(const AppendRopeArgs& a, const cache::IndexPlan& x, int first_head, int heads,
-                        Table<kChunk>& tab) {
+MSA_DEV void store_tail(const AppendRopeArgs& a, const cache::IndexPlan& x, int h0, int hn, Table<kChunk>& tab) {
   const int lane = threadIdx.x & 31, j = lane & 7, n = x.p1 - x.p0;  // at most a chunk
   const int64_t hs = (int64_t)a.H * 128, t0 = x.cu0 + x.p0 - x.past;
   const bool norm = a.ki.flags & MSA_ROPE_NORM, turn = turns(a.ki, j, a.q.an.R);
   int da, db;
   lane_dims(j, a.q.an.R, da, db);
+  // row r is token r / hn and head r % hn: the lane's head is the same in every step
+  const int shift = hn - 1, h = h0 + (lane >> 3 & shift);
+  IndexRows u;
+#pragma unroll
+  for (int s = 0; s < kIndexSteps; ++s) {
+    const int i = (s * 4 + (lane >> 3)) >> shift;
+    u.ua[s] = u.ub[s] = make_uint4(0, 0, 0, 0);
+    if (i < n) {
+      const uint16_t* src = a.ki.x + (t0 + i) * a.ki.x_token + h * a.ki.x_head;
+      u.ua[s] = *reinterpret_cast<const uint4*>(src + da);
+      u.ub[s] = *reinterpret_cast<const uint4*>(src + db);
+    }
+  }
+  Values w;
+  load_weights<kAdjacent>(a.ki, h, da, db, a.q.offset, w);
   Filler<kAdjacent>(a.q.an, lane, 32).fill(tab, a.q.an, t0, n);
   __syncwarp();
-  uint16_t* tail = a.index_tail + ((int64_t)x.r * 2 + (x.open & 1)) * a.B * hs;
-  for (int r0 = 0; r0 < n * heads; r0 += 4) {
-    const int r = r0 + (lane >> 3);
-    const bool live = r < n * heads;
-    const int i = live ? r / heads : 0, h = first_head + (live ? r - i * heads : 0);
-    uint4 ua = make_uint4(0, 0, 0, 0), ub = ua;
-    if (live) {
-      const uint16_t* src = a.ki.x + (t0 + i) * a.ki.x_token + h * a.ki.x_head;
-      ua = *reinterpret_cast<const uint4*>(src + da);
-      ub = *reinterpret_cast<const uint4*>(src + db);
-    }
-    Values v, w;
-    unpack<kAdjacent>(ua, ub, v);
-    load_weights<kAdjacent>(a.ki, h, da, db, a.q.offset, w);
-    norm_rotate(v, w, tab.cs[i], j, norm, turn, a.q.eps);
-    pack<kAdjacent>(v, ua, ub);
-    if (live) {
-      uint16_t* row = tail + ((x.p0 + i) % a.B) * hs + h * 128;
-      *reinterpret_cast<uint4*>(row + da) = ua;
-      *reinterpret_cast<uint4*>(row + db) = ub;
+  uint16_t* tail = a.index_tail + ((int64_t)x.r * 2 + (x.open & 1)) * a.B * hs + h * 128;
+#pragma unroll
+  for (int s = 0; s < kIndexSteps; ++s) {
+    if (s * 4 >= n << shift) break;
+    const int i = (s * 4 + (lane >> 3)) >> shift;
+    Values v;
+    unpack<kAdjacent>(u.ua[s], u.ub[s], v);
+    norm_rotate(v, w, tab.cs[i < n ? i : 0], j, norm, turn, a.q.eps);
+    pack<kAdjacent>(v, u.ua[s], u.ub[s]);
+    if (i < n) {
+      uint16_t* row = tail + ((x.p0 + i) & (a.B - 1)) * hs;
+      *reinterpret_cast<uint4*>(row + da) = u.ua[s];
+      *reinterpret_cast<uint4*>(row + db) = u.ub[s];
     }
   }
 }
 
-// A chunk that completes a block, by the CTA: up to eight heads at a time, 32 rows of
-// them (four tokens of eight heads, 32 tokens of one) per pass.  What is averaged
-// goes through shared memory and is added in the order of the tokens, so that the
-// mean does not depend on how a prompt was cut.
+// A chunk that completes a block, by the CTA: 64 tokens of the block at a time, those
+// of earlier calls as they are in the tail, those of this call normed and rotated, go
+// to shared memory and are added in the order of the tokens, so that the mean does not
+// depend on how a prompt was cut.
 template <bool kAdjacent>
-MSA_DEV void average_block(const AppendRopeArgs& a, const cache::IndexPlan& x, int first_head, int last_head,
-                           IndexShared& s) {
-  const int tid = threadIdx.x, j = tid & 7;
+MSA_DEV void average_block(const AppendRopeArgs& a, const cache::IndexPlan& x, int h0, int hn, IndexShared& s) {
+  const int tid = threadIdx.x, g = tid >> 3, j = tid & 7;
   const int64_t hs = (int64_t)a.H * 128;
   const bool norm = a.ki.flags & MSA_ROPE_NORM, turn = turns(a.ki, j, a.q.an.R);
   int da, db;
   lane_dims(j, a.q.an.R, da, db);
-  const Filler<kAdjacent> filler(a.q.an, threadIdx.x, kThreads);
-  const int64_t slot = x.last >= 0 ? a.slot_map[x.last] : -1;
-  const bool average = slot >= 0 && slot < a.slots;  // else reported by the rows' own CTAs, or left out
-  const int olds = average ? max(0, x.cu0 - (x.last - (a.B - 1))) : 0;  // tokens of earlier calls
-  for (int h0 = first_head; h0 < last_head; h0 += 8) {
-    const int hn = min(8, last_head - h0);
-    const int hb = hn > 4 ? 8 : hn > 2 ? 4 : hn;  // rows of a token
-    const int tb = kIndexRows / hb;
-    const int hsub = (tid >> 3) & (hb - 1), tsub = (tid >> 3) / hb;
-    const bool there = hsub < hn;
-    const int h = h0 + (there ? hsub : 0);
-    Values w;
-    load_weights<kAdjacent>(a.ki, h, da, db, a.q.offset, w);
-    const uint16_t* src = a.ki.x + h * a.ki.x_head;
-    uint16_t* tail = a.index_tail + (int64_t)x.r * 2 * a.B * hs + h0 * 128;
-    // `count` tokens from t on, in passes of tb: this thread's part of its row to `take`, then a barrier, then `after`.
-    // The angles of 64 tokens are made at once: their loads and functions then overlap.
-    auto passes = [&](int64_t t, int count, auto take, auto after) {
-      uint4 ua, ub;
-      auto load = [&](int m) {
-        ua = ub = make_uint4(0, 0, 0, 0);
-        if (there && m + tsub < count) {
-          ua = *reinterpret_cast<const uint4*>(src + (t + m + tsub) * a.ki.x_token + da);
-          ub = *reinterpret_cast<const uint4*>(src + (t + m + tsub) * a.ki.x_token + db);
-        }
-      };
-      load(0);
-      for (int m = 0, p = 0; m < count; m += tb, p ^= 1) {
-        const int in_table = m % kIndexTokens;
-        if (in_table == 0) {  // the table before has been read: a barrier followed
-          filler.fill(s.tab, a.q.an, t + m, min(kIndexTokens, count - m));
-          __syncthreads();
-        }
-        Values v;
-        unpack<kAdjacent>(ua, ub, v);
-        load(m + tb);
-        const bool here = there && m + tsub < count;
-        norm_rotate(v, w, s.tab.cs[in_table + tsub], j, norm, turn && here, a.q.eps);
-        uint4 oa, ob;
-        pack<kAdjacent>(v, oa, ob);
-        take(m, p, here, oa, ob);
-        __syncthreads();
-        after(m, p);
-      }
-    };
-    if (average) {
-      // a thread adds two dims at a time of up to two words
-      float lo[2] = {0.f, 0.f}, hi[2] = {0.f, 0.f};
+  const int shift = hn - 1, sub = g & shift, h = h0 + sub;
+  const Filler<kAdjacent> filler(a.q.an, tid, kThreads);
+  Values w;
+  load_weights<kAdjacent>(a.ki, h, da, db, a.q.offset, w);
+  const uint16_t* src = a.ki.x + h * a.ki.x_head;
+  uint16_t* tail = a.index_tail + (int64_t)x.r * 2 * a.B * hs + h * 128;
+  // `count` (<= 64) tokens, of which the first `olds` are rows of `old`, the others the call's from token t on: each
+  // thread's parts of its rows to take(token, first granule, second granule).
+  auto rows = [&](const uint16_t* old, int olds, int64_t t, int count, auto take) {
+    IndexRows u;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int word = tid + i * kThreads;
-        if (word < hn * 64)
-          cache::add_rows(tail + (int64_t)(x.avg_blk & 1) * a.B * hs + 2 * word, hs, olds, lo[i], hi[i]);
-      }
-      const int count = a.B - olds;
-      passes(x.last - (a.B - 1) + olds, count,
-             [&](int, int p, bool, uint4 oa, uint4 ob) {
-               s.rows[p][tid >> 3][da >> 3] = oa;
-               s.rows[p][tid >> 3][db >> 3] = ob;
-             },
-             [&](int m, int p) {
-               const int n = min(tb, count - m);
-#pragma unroll
-               for (int i = 0; i < 2; ++i) {
-                 const int word = tid + i * kThreads;
-                 if (word < hn * 64) {
-                   const uint32_t* row = reinterpret_cast<const uint32_t*>(s.rows[p][word >> 6]) + (word & 63);
-                   for (int k = 0; k < n; ++k) {
-                     const uint32_t u = row[k * hb * 64];
-                     lo[i] = __fadd_rn(lo[i], __uint_as_float(u << 16));
-                     hi[i] = __fadd_rn(hi[i], __uint_as_float(u & 0xFFFF0000u));
-                   }
-                 }
-               }
-             });
-      const float inv = 1.f / (float)a.B;  // a power of two: the product is the quotient
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int word = tid + i * kThreads;
-        if (word < hn * 64)
-          *reinterpret_cast<uint32_t*>(a.index_pool + (slot / a.B) * hs + h0 * 128 + 2 * word) =
-              pack_bf16x2(lo[i] * inv, hi[i] * inv);
+    for (int e = 0; e < kIndexSteps; ++e) {
+      const int i = (e * kIndexRows + g) >> shift;
+      u.ua[e] = u.ub[e] = make_uint4(0, 0, 0, 0);
+      if (i < count) {
+        const uint16_t* row = i < olds ? old + i * hs : src + (t + i - olds) * a.ki.x_token;
+        u.ua[e] = *reinterpret_cast<const uint4*>(row + da);
+        u.ub[e] = *reinterpret_cast<const uint4*>(row + db);
       }
     }
-    // the rows of the incomplete block, behind the barriers that follow the tail's last reads
+    if (olds < count) filler.fill(s.tab, a.q.an, t, count - olds);
     __syncthreads();
-    uint16_t* dst = tail + (int64_t)(x.open & 1) * a.B * hs + hsub * 128;
-    if (x.p0 < x.p1)
-      passes(x.cu0 + x.p0 - x.past, x.p1 - x.p0,
-             [&](int m, int, bool here, uint4 oa, uint4 ob) {
-               if (!here) return;
-               uint16_t* row = dst + ((x.p0 + m + tsub) % a.B) * hs;
-               *reinterpret_cast<uint4*>(row + da) = oa;
-               *reinterpret_cast<uint4*>(row + db) = ob;
-             },
-             [](int, int) {});
+#pragma unroll
+    for (int e = 0; e < kIndexSteps; ++e) {
+      const int i = (e * kIndexRows + g) >> shift;
+      const bool fresh = i >= olds && i < count;
+      if (__any_sync(0xffffffffu, fresh)) {
+        Values v;
+        unpack<kAdjacent>(u.ua[e], u.ub[e], v);
+        norm_rotate(v, w, s.tab.cs[fresh ? i - olds : 0], j, norm, turn && fresh, a.q.eps);
+        uint4 oa, ob;
+        pack<kAdjacent>(v, oa, ob);
+        if (fresh) {
+          u.ua[e] = oa;
+          u.ub[e] = ob;
+        }
+      }
+      if (i < count) take(i, u.ua[e], u.ub[e]);
+    }
     __syncthreads();
+  };
+  const int64_t slot = x.last >= 0 ? a.slot_map[x.last] : -1;
+  if (slot >= 0 && slot < a.slots) {  // else reported by the rows' own CTAs, or left out
+    const int olds = max(0, x.cu0 - (x.last - (a.B - 1)));  // tokens of earlier calls
+    const int64_t t = x.last - (a.B - 1);                    // token of the block's first position, were it of this call
+    float lo = 0.f, hi = 0.f;
+    for (int at = 0; at < a.B; at += kIndexTokens) {
+      rows(tail + ((int64_t)(x.avg_blk & 1) * a.B + at) * hs, max(0, min(kIndexTokens, olds - at)), t + max(at, olds),
+           kIndexTokens, [&](int i, uint4 ua, uint4 ub) {
+             s.rows[i][sub][da >> 3] = ua;
+             s.rows[i][sub][db >> 3] = ub;
+           });
+      if (tid < hn * 64) {
+        const uint32_t* row = reinterpret_cast<const uint32_t*>(s.rows[0][tid >> 6]) + (tid & 63);
+#pragma unroll 16
+        for (int i = 0; i < kIndexTokens; ++i) {
+          const uint32_t u = row[i * kIndexHeads * 64];
+          lo = __fadd_rn(lo, __uint_as_float(u << 16));
+          hi = __fadd_rn(hi, __uint_as_float(u & 0xFFFF0000u));
+        }
+      }
+    }
+    const float inv = 1.f / (float)a.B;  // a power of two: the product is the quotient
+    if (tid < hn * 64)
+      *reinterpret_cast<uint32_t*>(a.index_pool + (slot / a.B) * hs + h0 * 128 + 2 * tid) =
+          pack_bf16x2(lo * inv, hi * inv);
   }
+  // the rows of the incomplete block, behind the barriers that follow the tail's last reads
+  uint16_t* dst = tail + (int64_t)(x.open & 1) * a.B * hs;
+  for (int q = x.p0; q < x.p1; q += kIndexTokens)
+    rows(nullptr, 0, x.cu0 + q - x.past, min(kIndexTokens, x.p1 - q), [&](int i, uint4 ua, uint4 ub) {
+      uint16_t* row = dst + ((q + i) & (a.B - 1)) * hs;
+      *reinterpret_cast<uint4*>(row + da) = ua;
+      *reinterpret_cast<uint4*>(row + db) = ub;
+    });
+  __syncthreads();  // the shared memory is the next chunk's
 }
 
 template <bool kAdjacent>
 MSA_DEV void index_block(const AppendRopeArgs& a, int block, bool bad, IndexShared& s) {
   const int row = block / a.index_groups, h0 = (block - row * a.index_groups) * kIndexHeads;
-  const int h1 = min(a.H, h0 + kIndexHeads);
+  const int hn = min(kIndexHeads, a.H - h0);
   const int warp = threadIdx.x >> 5, g0 = row * a.index_chunks;
   cache::IndexPlan x;
   const bool todo = !__any_sync(0xffffffffu, bad) && warp < a.index_chunks && g0 + warp < a.NC &&
                     cache::plan_index(a, g0 + warp, (threadIdx.x & 31) == 0, x);
   const bool average = todo && x.last >= 0;
-  if (todo && !average) store_tail<kAdjacent>(a, x, h0, h1 - h0, s.own[warp]);
+  if (todo && !average) store_tail<kAdjacent>(a, x, h0, hn, s.own[warp]);
   if ((threadIdx.x & 31) == 0) s.average[warp] = average;
   __syncthreads();
   for (int i = 0; i < a.index_chunks; ++i)
     if (s.average[i]) {
       cache::plan_index(a, g0 + i, false, x);
-      average_block<kAdjacent>(a, x, h0, h1, s);
+      average_block<kAdjacent>(a, x, h0, hn, s);
     }
 }
 
