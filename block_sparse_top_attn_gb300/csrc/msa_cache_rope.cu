@@ -13,7 +13,7 @@ namespace rope {
 constexpr int kKvTile = 32;  // most tokens of a tile of K and V
 constexpr int kIndexRows = kThreads / 8;  // rows of a pass
 constexpr int kIndexTokens = 64;          // whose angles are made at once
-constexpr int kIndexHeads = 2;            // heads of index keys of a CTA: 1 or 2
+constexpr int kIndexHeads = 2;            // heads of index keys that a CTA takes at once
 
 struct AppendRopeArgs {
   RowsArgs q;    // q and q_index: rows in and out
@@ -30,7 +30,7 @@ struct AppendRopeArgs {
   float k_mul, v_mul;    // 2^-exp
   bool wide;             // rows of v are aligned to 32 bytes
   int index_blocks, kv_blocks;  // CTAs of index keys, of K and V; the others take q's rows
-  int index_groups, index_chunks;    // CTAs of a chunk's heads side by side; chunks of a CTA
+  int index_heads, index_groups, index_chunks;  // heads of a CTA, CTAs of a chunk's heads, chunks of a CTA
   int kv_tile, kv_groups, kv_heads;  // tokens of a tile; groups of heads side by side, heads of a group
   int32_t* status;
 };
@@ -45,7 +45,8 @@ struct AppendRopeArgs {
 // ulp, two products, the weight's offset), 5 u for the angle's function (1 ulp; its
 // argument's rounding and the scale), the products and the sum; the code's quotient
 // adds 2 u.  A group with a value (or a scale) nearer to a border than 32 u amp is
-// done again in fp64, from the inputs, behind the others: one group in 1,000.
+// done again in fp64, from the inputs, behind the others: one group in 1,000, which
+// costs a step of 256 tokens 1 us of 10.
 constexpr float kUlps = 32.f;
 
 // Dim `d` of a K row times its weight and rotated, in fp64; what is left of the norm
@@ -165,57 +166,63 @@ struct Half {
   uint32_t codes, scale;  // codes of the lane's eight, the group's scale
   bool doubt;             // fp32 does not tell
 };
-// Distance of x from the nearest border of a rounding that keeps `kBits` mantissa
-// bits, in units of its last place; below `least` the kept bits are those of `least`.
-template <int kBits>
-MSA_DEV uint32_t border_distance(float x, float least) {
-  const uint32_t z = __float_as_uint(x < least ? x + least : x) & ((1u << (23 - kBits)) - 1u);
-  return __sad((int)z, 1 << (22 - kBits), 0u);
-}
-// exact: the values are the inputs themselves, and rounded by quantize16's rule.
-MSA_DEV Half round_half(const float* v, float amp, float mul, bool exact) {
-  Half h;
-  uint32_t m = 0;
+// Eight e2m1 codes, zeros without a sign.
+MSA_DEV uint32_t codes8(const uint64_t (&q)[4]) {
+  float x[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  amp = fmaxf(amp, __shfl_xor_sync(0xffffffffu, amp, 1));
-  const float amax = __uint_as_float(m) * mul;
-  constexpr float kSixth = 1.f / 6.f;
-  const float t0 = amax * kSixth;
-  const float t = amax < 4096.f ? __fmaf_rn(__fmaf_rn(-6.f, t0, amax), kSixth, t0) : t0;
-  uint16_t s2;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s2) : "f"(0.f), "f"(t));
-  h.scale = s2 & 0xFFu;
-  h.codes = 0;
-  h.doubt = false;
-  if (m >= 0x7F800000u) {
-    h.scale = 0x7F;  // a NaN scale: the group reads back as NaN
-    return h;
-  }
-  // the relative error of t, in its last places
-  if (!exact && amp > 0.f && t < 450.f)
-    h.doubt = !((float)border_distance<3>(t, 0.015625f) > fmaf(amp * mul / amax, kUlps, 4.f));
-  if (h.scale == 0) return h;
-  const float inv = __frcp_rn(scale_value(h.scale)) * mul;
-  const uint32_t ulps = (uint32_t)fminf(fmaf(amp * inv, kUlps / 2.f, 3.f), 4194304.f);
-  float q[8];
-  uint32_t least = 0xFFFFFFFFu;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    q[i] = exact ? __fadd_rn(__fmaf_rn(v[i], inv, 768.f), -768.f) : v[i] * inv;
-    least = min(least, border_distance<1>(fabsf(q[i]), 1.f));
-  }
-  h.doubt |= !exact && least <= ulps;
+  for (int i = 0; i < 4; ++i) f2_unpack(q[i], x[2 * i], x[2 * i + 1]);
+  uint32_t out;
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
       "mov.b32 %0, {a, b, c, d};\n\t}"
-      : "=r"(h.codes)
-      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
-  h.codes = cache::unsigned_zeros(h.codes);
+      : "=r"(out)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return cache::unsigned_zeros(out);
+}
+// Rounds with the error to either side: where the results differ, there is a border
+// between them.  exact: the values are the inputs themselves, and rounded by
+// quantize16's rule.
+MSA_DEV Half round_half(const float* v, float amp, float mul, bool exact) {
+  Half h;
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  amp = fmaxf(amp, __shfl_xor_sync(0xffffffffu, amp, 1));  // by every lane, whether it is exact or not
+  const float amax = __uint_as_float(m) * mul;
+  constexpr float kSixth = 1.f / 6.f, kError = kUlps * 5.9604644775390625e-8f;  // 2^-24
+  const float t0 = amax * kSixth;
+  const float t = amax < 4096.f ? __fmaf_rn(__fmaf_rn(-6.f, t0, amax), kSixth, t0) : t0;
+  // t is two roundings from amax / 6
+  const float dt = exact ? 0.f : fmaf(amp * mul, kError * kSixth, t * 2.384185791015625e-7f);  // 2^-22
+  uint16_t two;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(t + dt), "f"(fmaxf(t - dt, 0.f)));
+  h.scale = two & 0xFFu;
+  h.codes = 0;
+  h.doubt = h.scale != (uint32_t)two >> 8;
+  if (m >= 0x7F800000u) {  // a NaN scale: the group reads back as NaN
+    h.scale = 0x7F;
+    h.doubt = false;
+  } else if (h.scale) {
+    const float inv = __frcp_rn(scale_value(h.scale)) * mul;
+    // a quotient is at most 6.4 here, three more roundings of it 2^-20
+    const float dq = exact ? 0.f : fmaf(amp * inv, kError, 9.5367431640625e-7f);
+    const uint64_t inv2 = f2_pack(inv, inv), up = f2_pack(dq, dq), down = f2_pack(-dq, -dq);
+    const uint64_t snap = f2_pack(768.f, 768.f);
+    uint64_t lo[4], hi[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t x = f2_pack(v[2 * i], v[2 * i + 1]);
+      const uint64_t q = exact ? f2_sub(f2_fma(x, inv2, snap), snap) : f2_mul(x, inv2);
+      lo[i] = f2_add(q, down);
+      hi[i] = f2_add(q, up);
+    }
+    h.codes = codes8(lo);
+    h.doubt |= h.codes != codes8(hi);
+  }
   return h;
 }
 
@@ -323,7 +330,7 @@ MSA_DEV void kv_block(const AppendRopeArgs& a, int block, bool bad, Table<kKvTil
 // ---------------------------------------------------------------------------
 // index keys
 // ---------------------------------------------------------------------------
-// A CTA takes up to two heads of up to eight chunks, a warp each.  A warp stores its
+// A CTA takes some heads of up to eight chunks, a warp each.  A warp stores its
 // chunk's rows to the tail by itself (a decode step's one token, the last tokens of
 // a prompt).  A chunk that completes a block is the CTA's work, after that.  All of a
 // warp's or CTA's loads are under way together, the angles made behind them.
@@ -353,36 +360,40 @@ MSA_DEV void store_tail(const AppendRopeArgs& a, const cache::IndexPlan& x, int 
   const bool norm = a.ki.flags & MSA_ROPE_NORM, turn = turns(a.ki, j, a.q.an.R);
   int da, db;
   lane_dims(j, a.q.an.R, da, db);
-  // row r is token r / hn and head r % hn: the lane's head is the same in every step
-  const int shift = hn - 1, h = h0 + (lane >> 3 & shift);
-  IndexRows u;
+  for (int h1 = h0; h1 < h0 + hn; h1 += kIndexHeads) {
+    // row r is token r / heads and head r % heads: the lane's head is the same in every step
+    const int shift = min(kIndexHeads, h0 + hn - h1) - 1, h = h1 + (lane >> 3 & shift);
+    IndexRows u;
 #pragma unroll
-  for (int s = 0; s < kIndexSteps; ++s) {
-    const int i = (s * 4 + (lane >> 3)) >> shift;
-    u.ua[s] = u.ub[s] = make_uint4(0, 0, 0, 0);
-    if (i < n) {
-      const uint16_t* src = a.ki.x + (t0 + i) * a.ki.x_token + h * a.ki.x_head;
-      u.ua[s] = *reinterpret_cast<const uint4*>(src + da);
-      u.ub[s] = *reinterpret_cast<const uint4*>(src + db);
+    for (int s = 0; s < kIndexSteps; ++s) {
+      const int i = (s * 4 + (lane >> 3)) >> shift;
+      u.ua[s] = u.ub[s] = make_uint4(0, 0, 0, 0);
+      if (i < n) {
+        const uint16_t* src = a.ki.x + (t0 + i) * a.ki.x_token + h * a.ki.x_head;
+        u.ua[s] = *reinterpret_cast<const uint4*>(src + da);
+        u.ub[s] = *reinterpret_cast<const uint4*>(src + db);
+      }
     }
-  }
-  Values w;
-  load_weights<kAdjacent>(a.ki, h, da, db, a.q.offset, w);
-  Filler<kAdjacent>(a.q.an, lane, 32).fill(tab, a.q.an, t0, n);
-  __syncwarp();
-  uint16_t* tail = a.index_tail + ((int64_t)x.r * 2 + (x.open & 1)) * a.B * hs + h * 128;
+    Values w;
+    load_weights<kAdjacent>(a.ki, h, da, db, a.q.offset, w);
+    if (h1 == h0) {
+      Filler<kAdjacent>(a.q.an, lane, 32).fill(tab, a.q.an, t0, n);
+      __syncwarp();
+    }
+    uint16_t* tail = a.index_tail + ((int64_t)x.r * 2 + (x.open & 1)) * a.B * hs + h * 128;
 #pragma unroll
-  for (int s = 0; s < kIndexSteps; ++s) {
-    if (s * 4 >= n << shift) break;
-    const int i = (s * 4 + (lane >> 3)) >> shift;
-    Values v;
-    unpack<kAdjacent>(u.ua[s], u.ub[s], v);
-    norm_rotate(v, w, tab.cs[i < n ? i : 0], j, norm, turn, a.q.eps);
-    pack<kAdjacent>(v, u.ua[s], u.ub[s]);
-    if (i < n) {
-      uint16_t* row = tail + ((x.p0 + i) & (a.B - 1)) * hs;
-      *reinterpret_cast<uint4*>(row + da) = u.ua[s];
-      *reinterpret_cast<uint4*>(row + db) = u.ub[s];
+    for (int s = 0; s < kIndexSteps; ++s) {
+      if (s * 4 >= n << shift) break;
+      const int i = (s * 4 + (lane >> 3)) >> shift;
+      Values v;
+      unpack<kAdjacent>(u.ua[s], u.ub[s], v);
+      norm_rotate(v, w, tab.cs[i < n ? i : 0], j, norm, turn, a.q.eps);
+      pack<kAdjacent>(v, u.ua[s], u.ub[s]);
+      if (i < n) {
+        uint16_t* row = tail + ((x.p0 + i) & (a.B - 1)) * hs;
+        *reinterpret_cast<uint4*>(row + da) = u.ua[s];
+        *reinterpret_cast<uint4*>(row + db) = u.ub[s];
+      }
     }
   }
 }
@@ -392,14 +403,14 @@ MSA_DEV void store_tail(const AppendRopeArgs& a, const cache::IndexPlan& x, int 
 // to shared memory and are added in the order of the tokens, so that the mean does not
 // depend on how a prompt was cut.
 template <bool kAdjacent>
-MSA_DEV void average_block(const AppendRopeArgs& a, const cache::IndexPlan& x, int h0, int hn, IndexShared& s) {
+MSA_DEV void average_heads(const AppendRopeArgs& a, const cache::IndexPlan& x, int h0, int hn,
+                           const Filler<kAdjacent>& filler, bool& filled, IndexShared& s) {
   const int tid = threadIdx.x, g = tid >> 3, j = tid & 7;
   const int64_t hs = (int64_t)a.H * 128;
   const bool norm = a.ki.flags & MSA_ROPE_NORM, turn = turns(a.ki, j, a.q.an.R);
   int da, db;
   lane_dims(j, a.q.an.R, da, db);
   const int shift = hn - 1, sub = g & shift, h = h0 + sub;
-  const Filler<kAdjacent> filler(a.q.an, tid, kThreads);
   Values w;
   load_weights<kAdjacent>(a.ki, h, da, db, a.q.offset, w);
   const uint16_t* src = a.ki.x + h * a.ki.x_head;
@@ -418,7 +429,7 @@ MSA_DEV void average_block(const AppendRopeArgs& a, const cache::IndexPlan& x, i
         u.ub[e] = *reinterpret_cast<const uint4*>(row + db);
       }
     }
-    if (olds < count) filler.fill(s.tab, a.q.an, t, count - olds);
+    if (olds < count && !filled) filler.fill(s.tab, a.q.an, t, count - olds);
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < kIndexSteps; ++e) {
@@ -473,13 +484,23 @@ MSA_DEV void average_block(const AppendRopeArgs& a, const cache::IndexPlan& x, i
       *reinterpret_cast<uint4*>(row + da) = ua;
       *reinterpret_cast<uint4*>(row + db) = ub;
     });
-  __syncthreads();  // the shared memory is the next chunk's
+  // the angles serve the next heads where there is one table of them
+  filled = a.B == kIndexTokens && x.p0 == x.p1;
+}
+template <bool kAdjacent>
+MSA_DEV void average_block(const AppendRopeArgs& a, const cache::IndexPlan& x, int h0, int hn, IndexShared& s) {
+  const Filler<kAdjacent> filler(a.q.an, threadIdx.x, kThreads);
+  bool filled = false;
+  for (int h = h0; h < h0 + hn; h += kIndexHeads) {
+    average_heads<kAdjacent>(a, x, h, min(kIndexHeads, h0 + hn - h), filler, filled, s);
+    __syncthreads();  // the rows have been added up
+  }
 }
 
 template <bool kAdjacent>
 MSA_DEV void index_block(const AppendRopeArgs& a, int block, bool bad, IndexShared& s) {
-  const int row = block / a.index_groups, h0 = (block - row * a.index_groups) * kIndexHeads;
-  const int hn = min(kIndexHeads, a.H - h0);
+  const int row = block / a.index_groups, h0 = (block - row * a.index_groups) * a.index_heads;
+  const int hn = min(a.index_heads, a.H - h0);
   const int warp = threadIdx.x >> 5, g0 = row * a.index_chunks;
   cache::IndexPlan x;
   const bool todo = !__any_sync(0xffffffffu, bad) && warp < a.index_chunks && g0 + warp < a.NC &&
@@ -504,11 +525,9 @@ MSA_DEV bool takes_turn(int64_t& block, int64_t count, int64_t of) {
   block = after > before ? before : block - before;
   return after > before;
 }
-// kCtas: of an SM.  Two of them hold their values in registers (a step of 256 tokens 20
-// us, with three 23); large calls are bound by memory, where three count (4 x 8192
-// tokens 505 us, with three 461).
-template <bool kAdjacent, int kCtas>
-__global__ void __launch_bounds__(kThreads, kCtas) append_rope_kernel(AppendRopeArgs a) {
+constexpr int kAppendCtas = 2;  // of an SM: three spill (4 x 8192 tokens 444 us, with two 454; prompt pieces 56, 33)
+template <bool kAdjacent>
+__global__ void __launch_bounds__(kThreads, kAppendCtas) append_rope_kernel(AppendRopeArgs a) {
   extern __shared__ __align__(16) uint8_t s_raw[];
   cache::after_previous_kernel();
   const bool bad = status_bad(a.status);
@@ -598,9 +617,10 @@ extern "C" int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_
   while (rows < rope::kKvTile && rows * a.kv_heads < rope::kIndexRows) rows *= 2;
   a.kv_tile = rope::cut_tokens(a.T, a.kv_groups, sms, rows < 16 ? 16 : rows, rows);
   const int64_t kv_blocks = (int64_t)((a.T + a.kv_tile - 1) / a.kv_tile) * a.kv_groups;
-  // chunks of a CTA: fewer where the CTAs find room, so that blocks that end in neighbouring chunks (requests of one
-  // length) do not wait for one another
-  a.index_groups = (H + rope::kIndexHeads - 1) / rope::kIndexHeads;
+  // two heads and few chunks to a CTA where the CTAs find room, so that heads, and blocks that end in neighbouring
+  // chunks (requests of one length), do not wait for one another; else eight heads, which share their angles
+  a.index_heads = (int64_t)c->chunk_cap * H > 16 * (int64_t)sms ? 8 : rope::kIndexHeads;
+  a.index_groups = (H + a.index_heads - 1) / a.index_heads;
   a.index_chunks = rope::kWarps;
   auto index_ctas = [&](int64_t chunks) { return (c->chunk_cap + chunks - 1) / chunks * a.index_groups; };
   while (a.index_chunks > 1 && index_ctas(a.index_chunks / 2) <= sms) a.index_chunks /= 2;
@@ -617,9 +637,7 @@ extern "C" int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_
   if (index_blocks + kv_blocks + q_blocks > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
   a.index_blocks = (int)index_blocks;
   a.kv_blocks = (int)kv_blocks;
-  const bool large = index_blocks + kv_blocks + q_blocks > 8 * (int64_t)sms;
-  auto* kernel = p->adjacent ? (large ? rope::append_rope_kernel<true, 3> : rope::append_rope_kernel<true, 2>)
-                             : (large ? rope::append_rope_kernel<false, 3> : rope::append_rope_kernel<false, 2>);
+  auto* kernel = p->adjacent ? rope::append_rope_kernel<true> : rope::append_rope_kernel<false>;
   return cache::launch_kernel(kernel, dim3((unsigned)(index_blocks + kv_blocks + q_blocks)), rope::kThreads,
                               rope::kAppendShared, stream, 1, a);
 }
