@@ -639,9 +639,12 @@ def make_rope_problem(tokens, pairs, q=None, k=None, q_index=None, k_index=None,
     return s
 
 
+_FOUR = ctypes.c_void_p * 4
+
+
 def _addrs(tensors):
     """A C array of the device addresses of q, k, q_index and k_index (None: NULL)."""
-    return (ctypes.c_void_p * 4)(*[None if t is None else t.data_ptr() for t in tensors])
+    return _FOUR(*[None if t is None else t.data_ptr() for t in tensors])
 
 
 def msa_norm_rope(p, xs, positions, ys, d_status, stream=None):
@@ -733,8 +736,9 @@ class Rope:
     def _problem(self, tokens, xs, ys, v=None):
         """The description of calls with these tensors' shapes and strides."""
         every = (*xs, v) if v is not None else xs
-        key = (tokens, *((x.shape[1], *self._strides(x), *(self._strides(y) if y is not None else ()))
-                         if x is not None else None for x, y in zip(every, (*ys, None))))
+        key = (tokens, *map(_addr, self.weights),    # a parameter's storage may be replaced
+               *((x.shape[1], *self._strides(x), *(self._strides(y) if y is not None else ()))
+                 if x is not None else None for x, y in zip(every, (*ys, None))))
         p = self._problems.get(key)
         if p is None:
             if len(self._problems) >= 64:
@@ -751,6 +755,23 @@ class Rope:
             if x is not None:
                 self._rows(name, x, tokens)
         return tuple(named.values())
+
+    @staticmethod
+    def _like(xs):
+        """New tensors with the shapes and strides of xs; views of one buffer where they are views of one tensor."""
+        import torch
+        made, groups = [None] * len(xs), {}
+        for i, x in enumerate(xs):
+            if x is not None:
+                groups.setdefault((x.untyped_storage().data_ptr(), x.stride()), []).append(i)
+        for members in groups.values():
+            ends = [xs[i].storage_offset() + sum((n - 1) * s for n, s in zip(xs[i].shape, xs[i].stride())) + 1
+                    for i in members]
+            base = min(xs[i].storage_offset() for i in members)
+            buf = torch.empty(max(0, max(ends) - base), dtype=torch.bfloat16, device=xs[members[0]].device)
+            for i in members:
+                made[i] = buf.as_strided(xs[i].shape, xs[i].stride(), xs[i].storage_offset() - base)
+        return tuple(made)
 
     def _outputs(self, name, out, xs, tokens):
         import torch
@@ -784,7 +805,8 @@ class Rope:
         """msa_norm_rope_bwd: grads and inputs (what forward was given) are q, k, q_index, k_index in order, as many as
         there are (None: no such tensor).  Returns (gradients of the inputs, gradients of the weights), each a tuple like
         `inputs`; a weight's is None where there is none.  out: tensors for the inputs' gradients, with the inputs'
-        strides (views of the projection's gradient, where the inputs are views of its output)."""
+        strides (views of the projection's gradient, where the inputs are views of its output); new ones are laid out
+        as the inputs are."""
         import torch
         T = self._positions(positions)
         n = len(inputs)
@@ -798,8 +820,7 @@ class Rope:
                 self._rows(f"gradient of {name}", g, T, x.shape[1])
         with torch.cuda.device(self.device), torch.cuda.stream(stream):
             if out is None:
-                dxs = tuple(None if x is None else torch.empty_strided(x.shape, x.stride(), dtype=x.dtype,
-                                                                       device=x.device) for x in xs)
+                dxs = self._like(xs)
             else:
                 dxs = self._outputs("out", out, xs, T)
                 for name, dx, x in zip(self.NAMES, dxs, xs):

@@ -543,6 +543,13 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_rope_kernel(Appe
     rows_block<kAdjacent>(a.q, (int)block, bad, *reinterpret_cast<RowsShared*>(s_raw));
 }
 
+// Tokens of a tile: the most whose tiles still give every SM two CTAs.
+inline int cut_tokens(int64_t tokens, int64_t groups, int sms, int most, int least) {
+  int tile = most;
+  while (tile > least && (tokens + tile - 1) / tile * groups < 2 * (int64_t)sms) tile >>= 1;
+  return tile;
+}
+
 }  // namespace rope
 }  // namespace msa
 

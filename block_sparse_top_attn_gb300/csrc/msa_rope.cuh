@@ -335,13 +335,6 @@ inline Cut cut_rows(int64_t heads, int64_t tokens, int64_t sms, int warps, int m
   c.slices = (int)(tokens < most ? tokens : most > 1 ? most : 1);
   return c;
 }
-// Tokens of a tile: the most whose tiles still give every SM two CTAs.
-inline int cut_tokens(int64_t tokens, int64_t groups, int sms, int most, int least) {
-  int tile = most;
-  while (tile > least && (tokens + tile - 1) / tile * groups < 2 * (int64_t)sms) tile >>= 1;
-  return tile;
-}
-
 // Rows in and out, by CTAs of (slice of the tokens, group of heads).
 struct RowsArgs {
   Tensor t[kTensors];

@@ -624,11 +624,11 @@ int msa_norm_rope_bwd(const msa_rope_problem* p, const uint16_t* const* dy, cons
  *            K and V are written to the cache: their y strides, and K_INDEX's, are
  *            not used.  p.tokens = c.token_cap.
  * positions  device int32 [T, num_axes]; msa_cache_step's positions where there is
- *            one axis.  A token whose slot is -1, or whose first position is negative,
- *            is padding: none of its rows are written (a slot of the cache beside a
- *            negative first position, or a slot outside it, sets
- *            MSA_ERR_INVALID_CACHE).  With index keys, the rows that chunks covers
- *            must not be padding.
+ *            one axis.  A token whose first position is negative is padding: none of
+ *            its rows are written.  A token whose slot is -1 leaves out K and V.  A
+ *            slot outside the cache, or one beside a negative first position, leaves
+ *            them out too and sets MSA_ERR_INVALID_CACHE.  With index keys, the rows
+ *            that chunks covers must not be padding.
  * Other arguments as for msa_cache_append.  Deterministic where no error is found. */
 int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_problem* p, const uint16_t* q, const uint16_t* k,
                           const uint16_t* v, const uint16_t* q_index, const uint16_t* k_index,
