@@ -40,11 +40,11 @@ struct AppendRopeArgs {
 // ---------------------------------------------------------------------------
 // The cache keeps a value by the interval it lies in, so an error of fp32 counts
 // only next to a border, and there by a whole code.  With amp = |a cos| + |b sin| and
-// u = 2^-24, fp32 forms y to within 23 u amp: 13.5 u for the normed a and b (the sum
-// of 128 squares in chains of 4 and 6 more additions, halved by the root; rsqrtf 2
-// ulp, two products, the weight's offset), 5 u for the angle's function (1 ulp; its
-// argument's rounding and the scale), the products and the sum; the code's quotient
-// adds 2 u.  A group with a value (or a scale) nearer to a border than 32 u amp is
+// u = 2^-24, fp32 forms y to within 23 u amp: 13.5 u for the weighted a and b and the
+// inverse rms (the sum of 128 squares in chains of 4 and 6 more additions, halved by
+// the root; rsqrtf 2 ulp; the weight's offset and products), 5 u for the angle's
+// function (1 ulp; its argument's rounding and the scale), the products and the sum;
+// the code's quotient adds 2 u.  A group with a value (or a scale) nearer to a border than 32 u amp is
 // done again in fp64, from the inputs, behind the others: one group in 1,000, which
 // costs a step of 256 tokens 1 us of 10.
 constexpr float kUlps = 32.f;
@@ -203,7 +203,7 @@ MSA_DEV Half round_half(const float* v, float amp, float mul, bool exact) {
   h.scale = two & 0xFFu;
   h.codes = 0;
   h.doubt = h.scale != (uint32_t)two >> 8;
-  if (m >= 0x7F800000u) {  // a NaN scale: the group reads back as NaN
+  if (m >= 0x7F800000u || mul != mul) {  // a NaN scale: the group reads back as NaN
     h.scale = 0x7F;
     h.doubt = false;
   } else if (h.scale) {
@@ -226,7 +226,7 @@ MSA_DEV Half round_half(const float* v, float amp, float mul, bool exact) {
   return h;
 }
 
-// Largest |a cos| + |b sin| of each granule of a normed row.
+// Largest |a cos| + |b sin| of each granule of a weighted row.
 template <bool kAdjacent>
 MSA_DEV void amplitudes(const Values& v, const float4* row, int j, bool turn, float (&amp)[2]) {
   amp[0] = amp[1] = 0.f;
@@ -293,13 +293,24 @@ MSA_DEV void kv_block(const AppendRopeArgs& a, int block, bool bad, Table<kKvTil
     }
     if (!live) ua = ub = make_uint4(0, 0, 0, 0);  // padding may hold anything
     Values val;
-    unpack<kAdjacent>(ua, ub, val);
-    normalize(val, w, norm, a.q.eps);
     float amp[2], v[16];
-    amplitudes<kAdjacent>(val, tab.cs[i], j, turn, amp);
-    if (turn) rotate<false>(val, tab.cs[i], j);
+    const float r = weigh<kAdjacent>(
+        ua, ub, w, norm, a.q.eps, val,
+        [&](Values& x) {
+          amplitudes<kAdjacent>(x, tab.cs[i], j, turn, amp);
+          if (turn) rotate<false>(x, tab.cs[i], j);
+        },
+        [&](uint4& xa, uint4& xb) {
+          const uint16_t* x = a.k.x + t * a.k.x_token + h * a.k.x_head;
+          if (live) {
+            xa = *reinterpret_cast<const uint4*>(x + da);
+            xb = *reinterpret_cast<const uint4*>(x + db);
+          }
+        });
     in_order<kAdjacent>(val, v);
-    const Half ha = round_half(v, amp[0], a.k_mul, exact), hb = round_half(v + 8, amp[1], a.k_mul, exact);
+    // the inverse rms goes into the factor of the rounding
+    const float mul = r * a.k_mul;
+    const Half ha = round_half(v, amp[0], mul, exact), hb = round_half(v + 8, amp[1], mul, exact);
     if (live) {
       int tok;
       uint8_t* out = cache_tile(a, slot, h, tok);
@@ -385,10 +396,8 @@ MSA_DEV void store_tail(const AppendRopeArgs& a, const cache::IndexPlan& x, int 
     for (int s = 0; s < kIndexSteps; ++s) {
       if (s * 4 >= n << shift) break;
       const int i = (s * 4 + (lane >> 3)) >> shift;
-      Values v;
-      unpack<kAdjacent>(u.ua[s], u.ub[s], v);
-      norm_rotate(v, w, tab.cs[i < n ? i : 0], j, norm, turn, a.q.eps);
-      pack<kAdjacent>(v, u.ua[s], u.ub[s]);
+      norm_rotate<kAdjacent>(u.ua[s], u.ub[s], w, tab.cs[i < n ? i : 0], j, norm, turn, a.q.eps,
+                             [](uint4&, uint4&) {});
       if (i < n) {
         uint16_t* row = tail + ((x.p0 + i) & (a.B - 1)) * hs;
         *reinterpret_cast<uint4*>(row + da) = u.ua[s];
@@ -436,11 +445,9 @@ MSA_DEV void average_heads(const AppendRopeArgs& a, const cache::IndexPlan& x, i
       const int i = (e * kIndexRows + g) >> shift;
       const bool fresh = i >= olds && i < count;
       if (__any_sync(0xffffffffu, fresh)) {
-        Values v;
-        unpack<kAdjacent>(u.ua[e], u.ub[e], v);
-        norm_rotate(v, w, s.tab.cs[fresh ? i - olds : 0], j, norm, turn && fresh, a.q.eps);
-        uint4 oa, ob;
-        pack<kAdjacent>(v, oa, ob);
+        uint4 oa = u.ua[e], ob = u.ub[e];
+        norm_rotate<kAdjacent>(oa, ob, w, s.tab.cs[fresh ? i - olds : 0], j, norm, turn && fresh, a.q.eps,
+                               [](uint4&, uint4&) {});
         if (fresh) {
           u.ua[e] = oa;
           u.ub[e] = ob;

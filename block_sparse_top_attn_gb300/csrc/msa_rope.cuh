@@ -253,25 +253,6 @@ MSA_DEV void times(Values& v, const Values& w) {
   }
 }
 
-// 1 / sqrt(mean + eps) of a row's sum of squares.  Rows whose squares leave fp32's
-// range (elements above 10^18) are scaled by 2^-64 first, where eps does not count.
-// Whole warps call this; v holds the row times `scale` after it (v * result is the
-// normed row either way).
-MSA_DEV float inverse_rms(Values& v, float sum, float eps, float& scale) {
-  scale = 1.f;
-  if (__any_sync(0xffffffffu, !(sum < kInf))) {
-    const bool far = !(sum < kInf);
-    if (far) {
-      scale = 5.421010862427522e-20f;  // 2^-64
-      eps = 0.f;
-    }
-    times(v, scale);
-    const float again = row_sum(squares(v));
-    if (far) sum = again;
-  }
-  return rsqrtf(fmaf(sum, 1.f / 128.f, eps));
-}
-
 // The lane's pairs turned by the angles of a table's row; kBack: the other way.
 template <bool kBack>
 MSA_DEV void rotate(Values& v, const float4* row, int j) {
@@ -290,19 +271,47 @@ MSA_DEV void rotate(Values& v, const float4* row, int j) {
   }
 }
 
-// The row normed if `norm` (without a norm w is 1), not turned yet.
-MSA_DEV void normalize(Values& v, const Values& w, bool norm, float eps) {
-  float scale;
-  const float sum = row_sum(squares(v));
-  const float inv = inverse_rms(v, norm ? sum : 0.f, eps, scale);
-  times(v, norm ? inv : 1.f);
+// A row's values times its weights, and what is left of the norm, 1 / sqrt(mean(x^2) +
+// eps) (1 without a norm), which waits for the other lanes while the values are
+// turned.  Rows whose squares leave fp32's range (elements above 10^18) are scaled by
+// 2^-64 first, where eps does not count; their `scale` says so.
+// turn: what is done to the weighted values meanwhile; again(ua, ub): the row once
+// more.  Whole warps call it.
+template <bool kAdjacent, class Turn, class Again>
+MSA_DEV float weigh(uint4 ua, uint4 ub, const Values& w, bool norm, float eps, Values& v, Turn turn, Again again) {
+  unpack<kAdjacent>(ua, ub, v);
+  float sum = row_sum(squares(v));
   times(v, w);
+  turn(v);
+  if (__any_sync(0xffffffffu, norm && !(sum < kInf))) {
+    const bool far = norm && !(sum < kInf);
+    again(ua, ub);
+    unpack<kAdjacent>(ua, ub, v);
+    times(v, far ? 5.421010862427522e-20f : 1.f);  // 2^-64
+    const float scaled = row_sum(squares(v));
+    if (far) {
+      sum = scaled;
+      eps = 0.f;
+    }
+    times(v, w);
+    turn(v);
+  }
+  return norm ? rsqrtf(fmaf(sum, 1.f / 128.f, eps)) : 1.f;
 }
-// One row: normed, then turned by the angles at `row` if `turn` (this lane's dims
+// One row: normed, and turned by the angles at `row` if `turn` (this lane's dims
 // are: a turn by nothing would carry infinities from pair to pair).
-MSA_DEV void norm_rotate(Values& v, const Values& w, const float4* row, int j, bool norm, bool turn, float eps) {
-  normalize(v, w, norm, eps);
-  if (turn) rotate<false>(v, row, j);
+template <bool kAdjacent, class Again>
+MSA_DEV void norm_rotate(uint4& ua, uint4& ub, const Values& w, const float4* row, int j, bool norm, bool turn,
+                         float eps, Again again) {
+  Values v;
+  const float r = weigh<kAdjacent>(
+      ua, ub, w, norm, eps, v,
+      [&](Values& x) {
+        if (turn) rotate<false>(x, row, j);
+      },
+      again);
+  times(v, r);
+  pack<kAdjacent>(v, ua, ub);
 }
 
 // Host side.
@@ -461,10 +470,10 @@ MSA_DEV void rows_block(const RowsArgs& a, int block, bool bad, RowsShared& s) {
       copy((stage + kStages - 1) & (kStages - 1));
       stage = (stage + 1) & (kStages - 1);
       if (tab.live[i - at]) {
-        Values v;
-        unpack<kAdjacent>(ua, ub, v);
-        norm_rotate(v, w, tab.cs[i - at], j, norm, turn, a.eps);
-        pack<kAdjacent>(v, ua, ub);
+        norm_rotate<kAdjacent>(ua, ub, w, tab.cs[i - at], j, norm, turn, a.eps, [&](uint4& xa, uint4& xb) {
+          xa = row[sa];  // the stage is not copied to before the next row
+          xb = row[sb];
+        });
         if (live) {
           *reinterpret_cast<uint4*>(y + da) = ua;
           *reinterpret_cast<uint4*>(y + db) = ub;
