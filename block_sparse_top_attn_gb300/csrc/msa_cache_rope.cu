@@ -348,60 +348,63 @@ MSA_DEV void kv_block(const AppendRopeArgs& a, int block, bool bad, Table<kKvTil
 struct IndexShared {
   union {
     Table<kChunk> own[kWarps];
-    struct {
-      Table<kIndexTokens> tab;
-      uint4 rows[kIndexTokens][kIndexHeads][16];  // bf16, normed and rotated
-    };
+    Table<kIndexTokens> tab;
   };
+  uint4 rows[kIndexTokens][kIndexHeads][16];  // as they come, then normed and rotated; eight tokens a warp, or the CTA's
   int average[kWarps];
 };
 
-// Up to four rows of a lane's row group: loaded, then normed and rotated.
-struct IndexRows {
-  uint4 ua[4], ub[4];
-};
-constexpr int kIndexSteps = 4;
-static_assert(kIndexTokens * kIndexHeads <= kIndexSteps * kIndexRows && kChunk * kIndexHeads <= kIndexSteps * 4,
+// Rows wait in shared memory, where a lane copies its own granules and reads them back
+// itself, and take no registers while the angles are made.
+constexpr int kIndexSteps = 4;  // of a row for each eight lanes
+static_assert(kIndexTokens * kIndexHeads <= kIndexSteps * kIndexRows && kChunk * kIndexHeads <= kIndexSteps * 4 &&
+                  kChunk * kWarps <= kIndexTokens,
               "a CTA's rows of 64 tokens and a warp's of a chunk");
 
 template <bool kAdjacent>
-MSA_DEV void store_tail(const AppendRopeArgs& a, const cache::IndexPlan& x, int h0, int hn, Table<kChunk>& tab) {
+MSA_DEV void store_tail(const AppendRopeArgs& a, const cache::IndexPlan& x, int h0, int hn, int warp, IndexShared& s) {
   const int lane = threadIdx.x & 31, j = lane & 7, n = x.p1 - x.p0;  // at most a chunk
   const int64_t hs = (int64_t)a.H * 128, t0 = x.cu0 + x.p0 - x.past;
   const bool norm = a.ki.flags & MSA_ROPE_NORM, turn = turns(a.ki, j, a.q.an.R);
+  Table<kChunk>& tab = s.own[warp];
+  auto* rows = s.rows + warp * kChunk;
   int da, db;
   lane_dims(j, a.q.an.R, da, db);
   for (int h1 = h0; h1 < h0 + hn; h1 += kIndexHeads) {
     // row r is token r / heads and head r % heads: the lane's head is the same in every step
-    const int shift = min(kIndexHeads, h0 + hn - h1) - 1, h = h1 + (lane >> 3 & shift);
-    IndexRows u;
+    const int shift = min(kIndexHeads, h0 + hn - h1) - 1, sub = lane >> 3 & shift, h = h1 + sub;
 #pragma unroll
-    for (int s = 0; s < kIndexSteps; ++s) {
-      const int i = (s * 4 + (lane >> 3)) >> shift;
-      u.ua[s] = u.ub[s] = make_uint4(0, 0, 0, 0);
+    for (int e = 0; e < kIndexSteps; ++e) {
+      const int i = (e * 4 + (lane >> 3)) >> shift;
       if (i < n) {
         const uint16_t* src = a.ki.x + (t0 + i) * a.ki.x_token + h * a.ki.x_head;
-        u.ua[s] = *reinterpret_cast<const uint4*>(src + da);
-        u.ub[s] = *reinterpret_cast<const uint4*>(src + db);
+        copy16(&rows[i][sub][da >> 3], src + da);
+        copy16(&rows[i][sub][db >> 3], src + db);
       }
     }
+    copies_commit();
     Values w;
     load_weights<kAdjacent>(a.ki, h, da, db, a.q.offset, w);
     if (h1 == h0) {
       Filler<kAdjacent>(a.q.an, lane, 32).fill(tab, a.q.an, t0, n);
       __syncwarp();
     }
+    copies_wait<0>();
     uint16_t* tail = a.index_tail + ((int64_t)x.r * 2 + (x.open & 1)) * a.B * hs + h * 128;
-#pragma unroll
-    for (int s = 0; s < kIndexSteps; ++s) {
-      if (s * 4 >= n << shift) break;
-      const int i = (s * 4 + (lane >> 3)) >> shift;
-      norm_rotate<kAdjacent>(u.ua[s], u.ub[s], w, tab.cs[i < n ? i : 0], j, norm, turn, a.q.eps,
-                             [](uint4&, uint4&) {});
+#pragma unroll 1
+    for (int e = 0; e * 4 < n << shift; ++e) {
+      const int i = (e * 4 + (lane >> 3)) >> shift, row = i < n ? i : 0;  // a row of its own, or any
+      uint4 ua, ub;
+      auto read = [&](uint4& xa, uint4& xb) {
+        xa = i < n ? rows[row][sub][da >> 3] : make_uint4(0, 0, 0, 0);
+        xb = i < n ? rows[row][sub][db >> 3] : make_uint4(0, 0, 0, 0);
+      };
+      read(ua, ub);
+      norm_rotate<kAdjacent>(ua, ub, w, tab.cs[row], j, norm, turn, a.q.eps, read);
       if (i < n) {
-        uint16_t* row = tail + ((x.p0 + i) & (a.B - 1)) * hs;
-        *reinterpret_cast<uint4*>(row + da) = u.ua[s];
-        *reinterpret_cast<uint4*>(row + db) = u.ub[s];
+        uint16_t* out = tail + ((x.p0 + i) & (a.B - 1)) * hs;
+        *reinterpret_cast<uint4*>(out + da) = ua;
+        *reinterpret_cast<uint4*>(out + db) = ub;
       }
     }
   }
@@ -420,79 +423,80 @@ MSA_DEV void average_heads(const AppendRopeArgs& a, const cache::IndexPlan& x, i
   int da, db;
   lane_dims(j, a.q.an.R, da, db);
   const int shift = hn - 1, sub = g & shift, h = h0 + sub;
-  Values w;
-  load_weights<kAdjacent>(a.ki, h, da, db, a.q.offset, w);
   const uint16_t* src = a.ki.x + h * a.ki.x_head;
   uint16_t* tail = a.index_tail + (int64_t)x.r * 2 * a.B * hs + h * 128;
-  // `count` (<= 64) tokens, of which the first `olds` are rows of `old`, the others the call's from token t on: each
-  // thread's parts of its rows to take(token, first granule, second granule).
-  auto rows = [&](const uint16_t* old, int olds, int64_t t, int count, auto take) {
-    IndexRows u;
-#pragma unroll
-    for (int e = 0; e < kIndexSteps; ++e) {
-      const int i = (e * kIndexRows + g) >> shift;
-      u.ua[e] = u.ub[e] = make_uint4(0, 0, 0, 0);
-      if (i < count) {
-        const uint16_t* row = i < olds ? old + i * hs : src + (t + i - olds) * a.ki.x_token;
-        u.ua[e] = *reinterpret_cast<const uint4*>(row + da);
-        u.ub[e] = *reinterpret_cast<const uint4*>(row + db);
-      }
-    }
-    if (olds < count && !filled) filler.fill(s.tab, a.q.an, t, count - olds);
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < kIndexSteps; ++e) {
-      const int i = (e * kIndexRows + g) >> shift;
-      const bool fresh = i >= olds && i < count;
-      if (__any_sync(0xffffffffu, fresh)) {
-        uint4 oa = u.ua[e], ob = u.ub[e];
-        norm_rotate<kAdjacent>(oa, ob, w, s.tab.cs[fresh ? i - olds : 0], j, norm, turn && fresh, a.q.eps,
-                               [](uint4&, uint4&) {});
-        if (fresh) {
-          u.ua[e] = oa;
-          u.ub[e] = ob;
-        }
-      }
-      if (i < count) take(i, u.ua[e], u.ub[e]);
-    }
-    __syncthreads();
-  };
   const int64_t slot = x.last >= 0 ? a.slot_map[x.last] : -1;
-  if (slot >= 0 && slot < a.slots) {  // else reported by the rows' own CTAs, or left out
-    const int olds = max(0, x.cu0 - (x.last - (a.B - 1)));  // tokens of earlier calls
-    const int64_t t = x.last - (a.B - 1);                    // token of the block's first position, were it of this call
-    float lo = 0.f, hi = 0.f;
-    for (int at = 0; at < a.B; at += kIndexTokens) {
-      rows(tail + ((int64_t)(x.avg_blk & 1) * a.B + at) * hs, max(0, min(kIndexTokens, olds - at)), t + max(at, olds),
-           kIndexTokens, [&](int i, uint4 ua, uint4 ub) {
-             s.rows[i][sub][da >> 3] = ua;
-             s.rows[i][sub][db >> 3] = ub;
-           });
-      if (tid < hn * 64) {
-        const uint32_t* row = reinterpret_cast<const uint32_t*>(s.rows[0][tid >> 6]) + (tid & 63);
-#pragma unroll 16
-        for (int i = 0; i < kIndexTokens; ++i) {
-          const uint32_t u = row[i * kIndexHeads * 64];
-          lo = __fadd_rn(lo, __uint_as_float(u << 16));
-          hi = __fadd_rn(hi, __uint_as_float(u & 0xFFFF0000u));
-        }
+  const bool average = slot >= 0 && slot < a.slots;  // else reported by the rows' own CTAs, or left out
+  const int olds = max(0, x.cu0 - (x.last - (a.B - 1)));  // tokens of the block from earlier calls
+  const int64_t block_t = x.last - (a.B - 1);  // token of the block's first position, were it of this call
+  float lo = 0.f, hi = 0.f;
+  // The segments of 64 tokens to average, then those to store (the rows of the incomplete block, behind the barriers
+  // that follow the tail's last reads).
+  const int averages = average ? a.B / kIndexTokens : 0, stores = (x.p1 - x.p0 + kIndexTokens - 1) / kIndexTokens;
+#pragma unroll 1
+  for (int seg = 0; seg < averages + stores; ++seg) {
+    const bool store = seg >= averages;
+    const int q = x.p0 + (seg - averages) * kIndexTokens, at = seg * kIndexTokens;
+    const int count = store ? min(kIndexTokens, x.p1 - q) : kIndexTokens;
+    const int old = store ? 0 : max(0, min(kIndexTokens, olds - at));          // rows from the tail, then fresh ones
+    const int64_t t = store ? x.cu0 + q - x.past : block_t + max(at, olds);  // token of the first of these
+    const uint16_t* from = tail + ((int64_t)(x.avg_blk & 1) * a.B + at) * hs;
+    if (seg) __syncthreads();  // the segment before has been added up
+#pragma unroll
+    for (int e = 0; e < kIndexSteps; ++e) {
+      const int i = (e * kIndexRows + g) >> shift;
+      if (i < count) {
+        const uint16_t* row = i < old ? from + i * hs : src + (t + i - old) * a.ki.x_token;
+        copy16(&s.rows[i][sub][da >> 3], row + da);
+        copy16(&s.rows[i][sub][db >> 3], row + db);
       }
     }
-    const float inv = 1.f / (float)a.B;  // a power of two: the product is the quotient
-    if (tid < hn * 64)
+    copies_commit();
+    if (old < count && !filled) filler.fill(s.tab, a.q.an, t, count - old);
+    Values w;
+    load_weights<kAdjacent>(a.ki, h, da, db, a.q.offset, w);
+    copies_wait<0>();
+    __syncthreads();  // the angles are there
+#pragma unroll 1
+    for (int e = 0; e < kIndexSteps; ++e) {
+      const int i = (e * kIndexRows + g) >> shift;
+      const bool fresh = i >= old && i < count;
+      if (!__any_sync(0xffffffffu, fresh)) continue;
+      const int row = fresh ? i : 0;  // a row of its own, or any
+      uint4 ua, ub;
+      auto read = [&](uint4& xa, uint4& xb) {
+        xa = fresh ? s.rows[row][sub][da >> 3] : make_uint4(0, 0, 0, 0);
+        xb = fresh ? s.rows[row][sub][db >> 3] : make_uint4(0, 0, 0, 0);
+      };
+      read(ua, ub);
+      norm_rotate<kAdjacent>(ua, ub, w, s.tab.cs[fresh ? i - old : 0], j, norm, turn && fresh, a.q.eps, read);
+      if (!fresh) continue;
+      if (store) {
+        uint16_t* out = tail + ((int64_t)(x.open & 1) * a.B + ((q + i) & (a.B - 1))) * hs;
+        *reinterpret_cast<uint4*>(out + da) = ua;
+        *reinterpret_cast<uint4*>(out + db) = ub;
+      } else {
+        s.rows[i][sub][da >> 3] = ua;
+        s.rows[i][sub][db >> 3] = ub;
+      }
+    }
+    __syncthreads();  // the rows are there, the angles have been read
+    if (store || tid >= hn * 64) continue;
+    const uint32_t* row = reinterpret_cast<const uint32_t*>(s.rows[0][tid >> 6]) + (tid & 63);
+#pragma unroll 8
+    for (int i = 0; i < kIndexTokens; ++i) {
+      const uint32_t u = row[i * kIndexHeads * 64];
+      lo = __fadd_rn(lo, __uint_as_float(u << 16));
+      hi = __fadd_rn(hi, __uint_as_float(u & 0xFFFF0000u));
+    }
+    if (seg == averages - 1) {
+      const float inv = 1.f / (float)a.B;  // a power of two: the product is the quotient
       *reinterpret_cast<uint32_t*>(a.index_pool + (slot / a.B) * hs + h0 * 128 + 2 * tid) =
           pack_bf16x2(lo * inv, hi * inv);
+    }
   }
-  // the rows of the incomplete block, behind the barriers that follow the tail's last reads
-  uint16_t* dst = tail + (int64_t)(x.open & 1) * a.B * hs;
-  for (int q = x.p0; q < x.p1; q += kIndexTokens)
-    rows(nullptr, 0, x.cu0 + q - x.past, min(kIndexTokens, x.p1 - q), [&](int i, uint4 ua, uint4 ub) {
-      uint16_t* row = dst + ((q + i) & (a.B - 1)) * hs;
-      *reinterpret_cast<uint4*>(row + da) = ua;
-      *reinterpret_cast<uint4*>(row + db) = ub;
-    });
   // the angles serve the next heads where there is one table of them
-  filled = a.B == kIndexTokens && x.p0 == x.p1;
+  filled = averages == 1 && stores == 0;
 }
 template <bool kAdjacent>
 MSA_DEV void average_block(const AppendRopeArgs& a, const cache::IndexPlan& x, int h0, int hn, IndexShared& s) {
@@ -513,7 +517,7 @@ MSA_DEV void index_block(const AppendRopeArgs& a, int block, bool bad, IndexShar
   const bool todo = !__any_sync(0xffffffffu, bad) && warp < a.index_chunks && g0 + warp < a.NC &&
                     cache::plan_index(a, g0 + warp, (threadIdx.x & 31) == 0, x);
   const bool average = todo && x.last >= 0;
-  if (todo && !average) store_tail<kAdjacent>(a, x, h0, hn, s.own[warp]);
+  if (todo && !average) store_tail<kAdjacent>(a, x, h0, hn, warp, s);
   if ((threadIdx.x & 31) == 0) s.average[warp] = average;
   __syncthreads();
   for (int i = 0; i < a.index_chunks; ++i)
@@ -532,7 +536,9 @@ MSA_DEV bool takes_turn(int64_t& block, int64_t count, int64_t of) {
   block = after > before ? before : block - before;
   return after > before;
 }
-constexpr int kAppendCtas = 2;  // of an SM: three spill (4 x 8192 tokens 444 us, with two 454; prompt pieces 56, 33)
+// CTAs of an SM.  With three the index keys' code spills: 4 x 8192 tokens 433 us against
+// 445, but 2,200 tokens of prompt pieces 41 against 33 and a step of 256 12.8 against 10.4.
+constexpr int kAppendCtas = 2;
 template <bool kAdjacent>
 __global__ void __launch_bounds__(kThreads, kAppendCtas) append_rope_kernel(AppendRopeArgs a) {
   extern __shared__ __align__(16) uint8_t s_raw[];

@@ -308,11 +308,17 @@ def test_views_in_place_and_order_of_dims(B):
     for a, b in zip((*dxs, *dws), (*dxw, *dww)):
         assert torch.equal(a, b)
     assert bool((grad[:, 34:36] == 5.0).all())
-    dxs, _ = L.rope.backward(pos, dys, xs)
-    assert all(torch.equal(a, b) for a, b in zip(dxs, dxw))
+    dxs, _ = L.rope.backward(pos, dys, xs)      # new tensors, laid out as the inputs are, of one buffer
+    assert all(torch.equal(a, b) and a.stride() == x.stride() for a, b, x in zip(dxs, dxw, xs))
+    assert len({d.untyped_storage().data_ptr() for d in dxs}) == 1
     # in place: dx over dy, y over x
     over = [d.clone() for d in dys]
     dxs, dws = L.rope.backward(pos, over, [x.contiguous() for x in xs], out=over)
+    for a, b in zip((*over, *dws), (*dxw, *dww)):
+        assert torch.equal(a, b)
+    # dx over x itself
+    over = [x.contiguous() for x in xs]
+    dxs, dws = L.rope.backward(pos, dys, over, out=over)
     for a, b in zip((*over, *dws), (*dxw, *dww)):
         assert torch.equal(a, b)
     v = rows[:, 34:36].clone()
@@ -342,6 +348,19 @@ def test_rows_do_not_depend_on_the_call(B):
     for _ in range(3):
         again = L.rope.backward(_dev(pos), dy, x)
         assert all(torch.equal(a, b) for a, b in zip((*again[0], *again[1]), (*dxs, *dws)))
+
+
+def test_replaced_weights(B):
+    """A weight whose storage was replaced, and one that was changed in place: calls use what is there now."""
+    import torch
+    L = Layer(B, seed=28)
+    pos = L.positions(9)
+    x = _bf16(L.rng, (9, 16, 128))
+    for change in (lambda w: w.copy_(w * 2 + 1), lambda w: setattr(w, "data", w.clone() * 0.5)):
+        L.rope.forward(_dev(pos), to_bf16_tensor(x, "cuda"))
+        change(L.dev[0])
+        L.w[0] = _f64(L.dev[0])
+        _check_forward(L, 0, x, pos, L.rope.forward(_dev(pos), to_bf16_tensor(x, "cuda"))[0])
 
 
 def test_no_tokens(B):
@@ -613,6 +632,29 @@ def test_append_bytes(B, kw, exp, block):
     assert int(st[0].item()) == 0
     _without_codes_of_nan((got, want), ks, vs, slots, block)
     assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("block", [64, 128])
+def test_append_of_rows_as_they_are(B, block):
+    """K that is neither normed nor rotated: msa_cache_append's bytes, special rows and exact ties among them."""
+    import torch
+    L = Layer(B, seed=27, H=3)
+    rng, P, T = L.rng, 4, 90
+    k, v = (_special_rows(rng, _bf16(rng, (T, 3, 128))) for _ in range(2))
+    k, v = to_bf16_tensor(k, "cuda"), to_bf16_tensor(v, "cuda")
+    slots = _dev(rng.permutation(P * block)[:T], torch.int64)
+    c = B.make_cache_problem(num_requests=1, num_pages=P, max_blocks=P, num_q_heads=48, topk=1, token_cap=T, chunk_cap=1,
+                             block_size=block)
+    st = torch.zeros(4, dtype=torch.int32, device="cuda")
+    want, got = B.new_cache(c), B.new_cache(c)
+    B.msa_cache_append(c, k, v, None, slots, None, None, want, None, None, st)
+    still = B.RopeTensor(3, norm=False, rotate=False)
+    pos = torch.zeros(T, dtype=torch.int32, device="cuda")
+    for pairs in (None, L.rope.pairs):
+        got.zero_()
+        p = B.make_rope_problem(T, pairs, k=still, v=still)
+        B.msa_cache_append_rope(c, p, None, k, v, None, None, pos, slots, None, None, None, None, got, None, None, st)
+        assert torch.equal(got, want) and int(st[0].item()) == 0
 
 
 @pytest.mark.parametrize("kw", [dict(H=4), dict(H=4, adjacent=True, norm=False, axes=3)])
