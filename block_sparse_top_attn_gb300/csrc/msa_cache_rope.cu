@@ -28,7 +28,6 @@ struct AppendRopeArgs {
   int positions;         // max_blocks * B: a request's most tokens
   int64_t slots;         // num_pages * B
   float k_mul, v_mul;    // 2^-exp
-  bool wide;             // rows of v are aligned to 32 bytes
   int index_blocks, kv_blocks;  // CTAs of index keys, of K and V; the others take q's rows
   int index_heads, index_groups, index_chunks;  // heads of a CTA, CTAs of a chunk's heads, chunks of a CTA
   int kv_tile, kv_groups, kv_heads;  // tokens of a tile; groups of heads side by side, heads of a group
@@ -243,10 +242,15 @@ MSA_DEV void amplitudes(const Values& v, const float4* row, int j, bool turn, fl
   }
 }
 
-// K and V of a tile of tokens and a group of heads.
+// K and V of a tile of tokens and a group of heads, four rows of each a pass; the next
+// pass's are on their way meanwhile.
+struct KvShared {
+  Table<kKvTile> tab;
+  Stage ring[kWarps][2][2];  // K and V
+};
 template <bool kAdjacent>
-MSA_DEV void kv_block(const AppendRopeArgs& a, int block, bool bad, Table<kKvTile>& tab) {
-  const int tid = threadIdx.x, lane = tid & 31, j = lane & 7;
+MSA_DEV void kv_block(const AppendRopeArgs& a, int block, bool bad, KvShared& s) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, j = lane & 7;
   const int tile = block / a.kv_groups, group = block - tile * a.kv_groups;
   const int64_t t0 = (int64_t)tile * a.kv_tile;
   const int n = (int)min((int64_t)a.kv_tile, a.T - t0);
@@ -255,43 +259,56 @@ MSA_DEV void kv_block(const AppendRopeArgs& a, int block, bool bad, Table<kKvTil
   const bool exact = !norm && !turn;  // the lane's values are its inputs
   int da, db;
   lane_dims(j, a.q.an.R, da, db);
+  const int sa = granule_slot(da >> 3), sb = granule_slot(db >> 3);
   const int shift = 31 - __clz(a.kv_tile);
   // four tokens of a head side by side in a warp: their cache rows follow one another
-  uint4 ua, ub;
-  uint32_t vw[8];
-  int64_t slot;
-  int first;  // position
-  auto load = [&](int u) {
-    const int i = u & (a.kv_tile - 1), hs = u >> shift;
-    ua = ub = make_uint4(0, 0, 0, 0);
-    slot = -1;
-    first = 0;
+  int64_t slot = -1, next_slot;
+  int first = 0, next_first;  // position
+  auto load = [&](int base, int stage) {
+    const int u = base + (lane >> 3), i = u & (a.kv_tile - 1), hs = u >> shift;
+    next_slot = -1;
+    next_first = 0;
     if (i < n && hs < hn) {
       const int64_t t = t0 + i, h = h0 + hs;
-      const uint16_t* x = a.k.x + t * a.k.x_token + h * a.k.x_head;
-      slot = a.slot_map[t];
-      first = a.q.an.positions[t * a.q.an.A];
-      ua = *reinterpret_cast<const uint4*>(x + da);
-      ub = *reinterpret_cast<const uint4*>(x + db);
-      cache::load32(a.v + t * a.v_token + h * a.v_head + 16 * j, a.wide, vw);
+      next_slot = a.slot_map[t];
+      next_first = a.q.an.positions[t * a.q.an.A];
+      copy_row(s.ring[warp][stage][0], a.k.x + t * a.k.x_token + h * a.k.x_head, lane);
+      copy_row(s.ring[warp][stage][1], a.v + t * a.v_token + h * a.v_head, lane);
     }
+    copies_commit();
   };
-  load(tid >> 3);  // ahead of the angles: one chain of loads for both
+  load(warp * 4, 0);  // ahead of the angles: one chain of loads for both
   Values w;
   load_weights<kAdjacent>(a.k, h0, da, db, a.q.offset, w);
-  Filler<kAdjacent>(a.q.an, tid, kThreads).fill(tab, a.q.an, t0, n);
-  if (__syncthreads_or(bad)) return;
-  for (int base = (tid >> 5) * 4; base < hn << shift; base += kThreads / 8) {
+  Filler<kAdjacent>(a.q.an, tid, kThreads).fill(s.tab, a.q.an, t0, n);
+  if (__syncthreads_or(bad)) {
+    copies_wait<0>();
+    return;
+  }
+  const Table<kKvTile>& tab = s.tab;
+  int stage = 0;
+  for (int base = warp * 4; base < hn << shift; base += kThreads / 8, stage ^= 1) {
     const int u = base + (lane >> 3), i = u & (a.kv_tile - 1), hs = u >> shift, h = h0 + hs;
     const int64_t t = t0 + i;
-    if (base >= kThreads / 8) load(u);
+    slot = next_slot;
+    first = next_first;
+    __syncwarp();  // the next stage has been read
+    load(base + kThreads / 8, stage ^ 1);
     if (a.k.flags & MSA_ROPE_PER_HEAD) load_weights<kAdjacent>(a.k, hs < hn ? h : h0, da, db, a.q.offset, w);
     bool live = i < n && hs < hn;
     if (live && (slot < 0 || slot >= a.slots || first < 0)) {
       if (slot != -1) set_status(a.status, MSA_ERR_INVALID_CACHE);
       live = false;
     }
-    if (!live) ua = ub = make_uint4(0, 0, 0, 0);  // padding may hold anything
+    copies_wait<1>();
+    __syncwarp();  // the lanes' copies have landed
+    const uint4 *row = s.ring[warp][stage][0].row[lane >> 3], *vrow = s.ring[warp][stage][1].row[lane >> 3];
+    auto read = [&](uint4& xa, uint4& xb) {  // padding may hold anything
+      xa = live ? row[sa] : make_uint4(0, 0, 0, 0);
+      xb = live ? row[sb] : make_uint4(0, 0, 0, 0);
+    };
+    uint4 ua, ub;
+    read(ua, ub);
     Values val;
     float amp[2], v[16];
     const float r = weigh<kAdjacent>(
@@ -300,13 +317,7 @@ MSA_DEV void kv_block(const AppendRopeArgs& a, int block, bool bad, Table<kKvTil
           amplitudes<kAdjacent>(x, tab.cs[i], j, turn, amp);
           if (turn) rotate<false>(x, tab.cs[i], j);
         },
-        [&](uint4& xa, uint4& xb) {
-          const uint16_t* x = a.k.x + t * a.k.x_token + h * a.k.x_head;
-          if (live) {
-            xa = *reinterpret_cast<const uint4*>(x + da);
-            xb = *reinterpret_cast<const uint4*>(x + db);
-          }
-        });
+        read);
     in_order<kAdjacent>(val, v);
     // the inverse rms goes into the factor of the rounding
     const float mul = r * a.k_mul;
@@ -318,6 +329,8 @@ MSA_DEV void kv_block(const AppendRopeArgs& a, int block, bool bad, Table<kKvTil
       *reinterpret_cast<uint32_t*>(out + cache::OFF_KC + tok * cache::kRowBytes + (db >> 1)) = hb.codes;
       // of the two lanes of a group, one stores the first granules' scale, one the second's
       out[cache::OFF_KS + tok * cache::kScales + ((j & 1 ? db : da) >> 4)] = (uint8_t)(j & 1 ? hb.scale : ha.scale);
+      const uint4 v0 = vrow[granule_slot(2 * j)], v1 = vrow[granule_slot(2 * j + 1)];
+      const uint32_t vw[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
       uint2 vc;
       const uint32_t vs = cache::quantize16(vw, a.v_mul, vc);
       *reinterpret_cast<uint2*>(out + cache::OFF_VC + cache::v_code_offset(tok, j)) = vc;
@@ -527,7 +540,8 @@ MSA_DEV void index_block(const AppendRopeArgs& a, int block, bool bad, IndexShar
     }
 }
 
-constexpr size_t kAppendShared = sizeof(IndexShared) > sizeof(RowsShared) ? sizeof(IndexShared) : sizeof(RowsShared);
+constexpr size_t kAppendShared = sizeof(IndexShared);
+static_assert(sizeof(RowsShared) <= kAppendShared && sizeof(KvShared) <= kAppendShared, "one size for every CTA");
 // The CTAs of index keys come first: a block's mean takes longest.  Those of K and V
 // and of Q then take turns in proportion to their numbers: K's are bound by
 // instructions and Q's by memory, and an SM should hold both.
@@ -536,11 +550,12 @@ MSA_DEV bool takes_turn(int64_t& block, int64_t count, int64_t of) {
   block = after > before ? before : block - before;
   return after > before;
 }
-// CTAs of an SM.  With three the index keys' code spills: 4 x 8192 tokens 433 us against
-// 445, but 2,200 tokens of prompt pieces 41 against 33 and a step of 256 12.8 against 10.4.
-constexpr int kAppendCtas = 2;
-template <bool kAdjacent>
-__global__ void __launch_bounds__(kThreads, kAppendCtas) append_rope_kernel(AppendRopeArgs a) {
+// kCtas: of an SM.  Two leave room for more loads under way at once, which counts where
+// all CTAs run together (a step of 256 tokens 10.3 us, with three 12.8; 2,200 tokens of
+// prompt pieces 33, 41); where they come in many waves three do more (4 x 8192 tokens
+// 434 us, with three 417).
+template <bool kAdjacent, int kCtas>
+__global__ void __launch_bounds__(kThreads, kCtas) append_rope_kernel(AppendRopeArgs a) {
   extern __shared__ __align__(16) uint8_t s_raw[];
   cache::after_previous_kernel();
   const bool bad = status_bad(a.status);
@@ -551,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_rope_kernel(Appe
   }
   block -= a.index_blocks;
   if (takes_turn(block, a.kv_blocks, (int64_t)gridDim.x - a.index_blocks))
-    kv_block<kAdjacent>(a, (int)block, bad, *reinterpret_cast<Table<kKvTile>*>(s_raw));
+    kv_block<kAdjacent>(a, (int)block, bad, *reinterpret_cast<KvShared*>(s_raw));
   else
     rows_block<kAdjacent>(a.q, (int)block, bad, *reinterpret_cast<RowsShared*>(s_raw));
 }
@@ -624,7 +639,6 @@ extern "C" int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_
   a.v = v;
   a.v_token = t[MSA_ROPE_V].x_token;
   a.v_head = t[MSA_ROPE_V].x_head;
-  a.wide = cache::aligned32(v, nullptr) && a.v_token % 16 == 0 && a.v_head % 16 == 0;
   a.slot_map = slot_map; a.cu_tokens = cu_tokens; a.chunks = chunks;
   a.cache = kv_cache; a.index_tail = index_tail; a.index_pool = index_pool;
   a.positions = c->max_blocks * c->block_size;
@@ -657,7 +671,9 @@ extern "C" int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_
   if (index_blocks + kv_blocks + q_blocks > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
   a.index_blocks = (int)index_blocks;
   a.kv_blocks = (int)kv_blocks;
-  auto* kernel = p->adjacent ? rope::append_rope_kernel<true> : rope::append_rope_kernel<false>;
+  const bool many = index_blocks + kv_blocks + q_blocks > 8 * (int64_t)sms;
+  auto* kernel = p->adjacent ? (many ? rope::append_rope_kernel<true, 3> : rope::append_rope_kernel<true, 2>)
+                             : (many ? rope::append_rope_kernel<false, 3> : rope::append_rope_kernel<false, 2>);
   return cache::launch_kernel(kernel, dim3((unsigned)(index_blocks + kv_blocks + q_blocks)), rope::kThreads,
                               rope::kAppendShared, stream, 1, a);
 }
