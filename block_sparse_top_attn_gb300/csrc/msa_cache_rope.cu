@@ -651,9 +651,12 @@ extern "C" int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_
   while (rows < rope::kKvTile && rows * a.kv_heads < rope::kIndexRows) rows *= 2;
   a.kv_tile = rope::cut_tokens(a.T, a.kv_groups, sms, rows < 16 ? 16 : rows, rows);
   const int64_t kv_blocks = (int64_t)((a.T + a.kv_tile - 1) / a.kv_tile) * a.kv_groups;
-  // two heads and few chunks to a CTA where the CTAs find room, so that heads, and blocks that end in neighbouring
-  // chunks (requests of one length), do not wait for one another; else eight heads, which share their angles
-  a.index_heads = (int64_t)c->chunk_cap * H > 16 * (int64_t)sms ? 8 : rope::kIndexHeads;
+  // Few heads and chunks to a CTA where the CTAs find room, so that heads, and blocks that end in neighbouring chunks
+  // (requests of one length), do not wait for one another; else eight heads, which share their angles (4 x 8192 tokens
+  // 444 us, with two 470).  A mean takes longest among chunks of several tokens, by the capacities: one head there
+  // (prompt pieces 29 us, with two 32), two for single tokens (a step of 256 9.5, with one 13.1).
+  const bool prompts = c->token_cap / c->chunk_cap >= 3;
+  a.index_heads = (int64_t)c->chunk_cap * H > 16 * (int64_t)sms ? 8 : prompts ? 1 : rope::kIndexHeads;
   a.index_groups = (H + a.index_heads - 1) / a.index_heads;
   a.index_chunks = rope::kWarps;
   auto index_ctas = [&](int64_t chunks) { return (c->chunk_cap + chunks - 1) / chunks * a.index_groups; };
