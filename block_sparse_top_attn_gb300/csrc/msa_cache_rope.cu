@@ -48,12 +48,46 @@ struct AppendRopeArgs {
 // costs a step of 256 tokens 1 us of 10.
 constexpr float kUlps = 32.f;
 
-// Dim `d` of a K row times its weight and rotated, in fp64; what is left of the norm
-// is the row's inverse rms.
+// Cosine and sine of a fraction of a turn in fp64, to 10^-11: the quarter turns are
+// taken off exactly, and the Taylor polynomials do for the eighth that is left.  What
+// is nearer to a border than that is one value in 10^10; short code counts more here,
+// as the few warps that come this way fetch it anew (the library's functions: a step
+// of 64 tokens 8.3 us).
+MSA_DEV void cos_sin64(uint64_t turn, double& c, double& s) {
+  const uint64_t shifted = turn + (1ull << 61);
+  const int64_t rest = (int64_t)(turn - (shifted & (3ull << 62)));
+  const double x = (double)rest * 3.4061215800865545e-19, z = x * x;  // pi 2^-63
+  double sn = fma(z, -1.0 / 39916800, 1.0 / 362880), cs = fma(z, 1.0 / 479001600, -1.0 / 3628800);
+  sn = fma(z, sn, -1.0 / 5040);
+  cs = fma(z, cs, 1.0 / 40320);
+  sn = fma(z, sn, 1.0 / 120);
+  cs = fma(z, cs, -1.0 / 720);
+  sn = fma(z, sn, -1.0 / 6);
+  cs = fma(z, cs, 1.0 / 24);
+  sn = fma(x * z, sn, x);
+  cs = fma(z, cs, -0.5);
+  cs = fma(z, cs, 1.0);
+  const int quarter = (int)(shifted >> 62);
+  c = quarter & 1 ? sn : cs;
+  s = quarter & 1 ? cs : sn;
+  if (quarter == 1 || quarter == 2) c = -c;
+  if (quarter >= 2) s = -s;
+}
+// 1 / sqrt(m) in fp64 to 10^-13, m >= 2^-100: a step of Newton's method from the fp32 one.
+MSA_DEV double inverse_root64(double m) {
+  const bool far = m > 1e30;
+  double r = (double)rsqrtf((float)(far ? m * 2.938735877055719e-39 : m));  // 2^-128
+  if (far) r *= 5.421010862427522e-20;                                      // 2^-64
+  return fma(r * 0.5, fma(-m * r, r, 1.0), r);
+}
+
+// Dim `d` of a K row (in shared memory) times its weight and rotated, in fp64; what is
+// left of the norm is the row's inverse rms.
 template <bool kAdjacent>
-MSA_DEV double turned_dim(const AppendRopeArgs& a, const uint16_t* x, int head, int64_t t, int d) {
+MSA_DEV double turned_dim(const AppendRopeArgs& a, const uint4* row, int head, int64_t t, int d) {
   auto weighted = [&](int i) {
-    const double v = (double)__uint_as_float((uint32_t)x[i] << 16);
+    const uint32_t x = reinterpret_cast<const uint16_t*>(row + granule_slot(i >> 3))[i & 7];
+    const double v = (double)__uint_as_float(x << 16);
     if (!(a.k.flags & MSA_ROPE_NORM) || !a.k.w) return v;
     const int64_t at = (a.k.flags & MSA_ROPE_PER_HEAD ? head * 128 : 0) + i;
     const float w = a.k.flags & MSA_ROPE_WEIGHT_FP32
@@ -67,10 +101,9 @@ MSA_DEV double turned_dim(const AppendRopeArgs& a, const uint16_t* x, int head, 
   const bool second = kAdjacent ? d & 1 : d >= R / 2;
   const int p = kAdjacent ? d >> 1 : second ? d - R / 2 : d;
   const int partner = kAdjacent ? d ^ 1 : second ? p : d + R / 2;
-  const double other = weighted(partner);
   double s, c;
-  // half turns
-  sincospi((double)(int64_t)turn_of(a.q.an, load_pair(a.q.an, p), t) * 1.0842021724855044e-19, &s, &c);
+  cos_sin64(turn_of(a.q.an, load_pair(a.q.an, p), t), c, s);
+  const double other = weighted(partner);
   return (second ? fma(own, c, other * s) : fma(own, c, -(other * s))) * (double)a.q.an.scale;
 }
 
@@ -123,23 +156,25 @@ MSA_DEV uint8_t* cache_tile(const AppendRopeArgs& a, int64_t slot, int head, int
                        cache::kTileBytes;
 }
 
-// Codes and scale of 16 dims from dim0 on of token t's K row, in fp64, by a warp: lanes
-// 0 .. 15 a dim each (16 .. 31 the same ones).
+// Codes and scale of 16 dims from dim0 on of token t's K row, in fp64, by half a warp, a
+// lane a dim; the two halves of a warp may have different groups.
 template <bool kAdjacent>
-MSA_DEV void exact_group(const AppendRopeArgs& a, int64_t t, int head, int dim0) {
-  const int lane = threadIdx.x & 31;
-  const uint16_t* x = a.k.x + t * a.k.x_token + head * a.k.x_head;
-  const int d = dim0 + (lane & 15);
-  const double turned = turned_dim<kAdjacent>(a, x, head, t, d);
+MSA_DEV void exact_group(const AppendRopeArgs& a, const uint4* row, int64_t slot, int64_t t, int head, int dim0) {
+  const int lane = threadIdx.x & 15;
+  const double turned = turned_dim<kAdjacent>(a, row, head, t, dim0 + lane);
   double r = 1.0;
   if (a.k.flags & MSA_ROPE_NORM) {
-    const uint2 u = *reinterpret_cast<const uint2*>(x + lane * 4);
-    const double v[4] = {(double)__uint_as_float(u.x << 16), (double)__uint_as_float(u.x & 0xFFFF0000u),
-                         (double)__uint_as_float(u.y << 16), (double)__uint_as_float(u.y & 0xFFFF0000u)};
-    double s = (v[0] * v[0] + v[1] * v[1]) + (v[2] * v[2] + v[3] * v[3]);
+    const uint4 u = row[granule_slot(lane)];
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    double s = 0.0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    r = rsqrt(s * (1.0 / 128.0) + (double)a.q.eps);
+    for (int i = 0; i < 4; ++i) {
+      const double lo = (double)__uint_as_float(w[i] << 16), hi = (double)__uint_as_float(w[i] & 0xFFFF0000u);
+      s = fma(lo, lo, fma(hi, hi, s));
+    }
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    r = inverse_root64(fma(s, 1.0 / 128.0, (double)a.q.eps));
   }
   const double y = turned * (r * (double)a.k_mul);
   const Split own = split(fabs(y));
@@ -154,8 +189,8 @@ MSA_DEV void exact_group(const AppendRopeArgs& a, int64_t t, int head, int dim0)
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) codes |= __shfl_xor_sync(0xffffffffu, codes, o);
   int tok;
-  uint8_t* out = cache_tile(a, a.slot_map[t], head, tok);
-  if (lane == 0 || lane == 8)
+  uint8_t* out = cache_tile(a, slot, head, tok);
+  if ((lane & 7) == 0)
     *reinterpret_cast<uint32_t*>(out + cache::OFF_KC + tok * cache::kRowBytes + (dim0 >> 1) + (lane >> 1)) = codes;
   if (lane == 0) out[cache::OFF_KS + tok * cache::kScales + (dim0 >> 4)] = (uint8_t)s8;
 }
@@ -336,17 +371,23 @@ MSA_DEV void kv_block(const AppendRopeArgs& a, int block, bool bad, KvShared& s)
       *reinterpret_cast<uint2*>(out + cache::OFF_VC + cache::v_code_offset(tok, j)) = vc;
       out[cache::OFF_VS + j * cache::kTile + tok] = (uint8_t)vs;
     }
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const bool doubt = live && (s ? hb.doubt : ha.doubt);  // one of a group's lanes, or both
-      unsigned groups = __ballot_sync(0xffffffffu, doubt);
-      groups = (groups | groups >> 1) & 0x55555555u;
-      if (groups) __syncwarp();  // what is there of the group is overwritten
-      for (; groups; groups &= groups - 1) {
-        const int from = __ffs(groups) - 1;
-        exact_group<kAdjacent>(a, __shfl_sync(0xffffffffu, t, from), __shfl_sync(0xffffffffu, h, from),
-                               __shfl_sync(0xffffffffu, s ? db : da, from));
-      }
+    // Groups in doubt, by their first lane; two at a time.
+    auto groups = [&](bool doubt) {  // one of a group's lanes may see it, or both
+      const unsigned m = __ballot_sync(0xffffffffu, live && doubt);
+      return (uint64_t)((m | m >> 1) & 0x55555555u);
+    };
+    uint64_t left = groups(ha.doubt) | groups(hb.doubt) << 32;
+    if (left) __syncwarp();  // what is there of the groups is overwritten
+    while (left) {
+      const int one = __ffsll(left) - 1;
+      left &= left - 1;
+      const int two = left ? __ffsll(left) - 1 : one;
+      left &= left - 1;
+      const int mine = lane < 16 ? one : two, from = mine & 31;
+      const int dim_a = __shfl_sync(0xffffffffu, da, from), dim_b = __shfl_sync(0xffffffffu, db, from);
+      const int64_t at = __shfl_sync(0xffffffffu, slot, from), token = __shfl_sync(0xffffffffu, t, from);
+      const int head = __shfl_sync(0xffffffffu, h, from);
+      exact_group<kAdjacent>(a, s.ring[warp][stage][0].row[from >> 3], at, token, head, mine < 32 ? dim_a : dim_b);
     }
   }
 }
@@ -665,9 +706,12 @@ extern "C" int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_
   int64_t q_blocks = 0;
   if (a.q.heads) {
     a.q.cut = rope::cut_rows(a.q.heads, a.T, sms, 2 * rope::kWarps, rope::kWarps - 1);
-    // shares of 12 to 64 tokens: few enough CTAs for a step's to run at once, enough to mix with K's in a large call
+    // In a step all CTAs should run at once: q's tokens go to as many as the others leave room for (64 tokens: 6.9 us,
+    // in shares of 12 tokens 8.2).  Where that makes shares of more than 12 tokens, shares of 12 to 64, by the
+    // call's size: enough to mix with K's CTAs.
+    const int64_t room = (2 * (int64_t)sms - index_blocks - kv_blocks) / a.q.cut.groups;
     const int64_t per = (int64_t)a.T * a.q.cut.groups / (8 * (int64_t)sms);
-    const int64_t tokens = per < 12 ? 12 : per > 64 ? 64 : per;
+    const int64_t tokens = room > 0 && a.T <= 12 * room ? (a.T + room - 1) / room : per < 12 ? 12 : per > 64 ? 64 : per;
     a.q.cut.slices = (int)((a.T + tokens - 1) / tokens);
     q_blocks = (int64_t)a.q.cut.slices * a.q.cut.groups;
   }
