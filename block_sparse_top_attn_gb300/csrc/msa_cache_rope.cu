@@ -45,14 +45,14 @@ struct AppendRopeArgs {
 // function (1 ulp; its argument's rounding and the scale), the products and the sum;
 // the code's quotient adds 2 u.  A group with a value (or a scale) nearer to a border than 32 u amp is
 // done again in fp64, from the inputs, behind the others: one group in 1,000, which
-// costs a step of 256 tokens 1 us of 10.
+// costs a step of 64 tokens 1 us of 8.
 constexpr float kUlps = 32.f;
 
 // Cosine and sine of a fraction of a turn in fp64, to 10^-11: the quarter turns are
 // taken off exactly, and the Taylor polynomials do for the eighth that is left.  What
 // is nearer to a border than that is one value in 10^10; short code counts more here,
-// as the few warps that come this way fetch it anew (the library's functions: a step
-// of 64 tokens 8.3 us).
+// as the few warps that come this way fetch it anew (a step of 64 tokens 8.2 us, with
+// the library's functions 8.4).
 MSA_DEV void cos_sin64(uint64_t turn, double& c, double& s) {
   const uint64_t shifted = turn + (1ull << 61);
   const int64_t rest = (int64_t)(turn - (shifted & (3ull << 62)));
@@ -371,7 +371,7 @@ MSA_DEV void kv_block(const AppendRopeArgs& a, int block, bool bad, KvShared& s)
       *reinterpret_cast<uint2*>(out + cache::OFF_VC + cache::v_code_offset(tok, j)) = vc;
       out[cache::OFF_VS + j * cache::kTile + tok] = (uint8_t)vs;
     }
-    // Groups in doubt, by their first lane; two at a time.
+    // Groups in doubt, by their first lane; two at a time (64 tokens 7.7 us, one at a time 8.2).
     auto groups = [&](bool doubt) {  // one of a group's lanes may see it, or both
       const unsigned m = __ballot_sync(0xffffffffu, live && doubt);
       return (uint64_t)((m | m >> 1) & 0x55555555u);
@@ -706,8 +706,8 @@ extern "C" int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_
   int64_t q_blocks = 0;
   if (a.q.heads) {
     a.q.cut = rope::cut_rows(a.q.heads, a.T, sms, 2 * rope::kWarps, rope::kWarps - 1);
-    // In a step all CTAs should run at once: q's tokens go to as many as the others leave room for (64 tokens: 6.9 us,
-    // in shares of 12 tokens 8.2).  Where that makes shares of more than 12 tokens, shares of 12 to 64, by the
+    // In a step all CTAs should run at once: q's tokens go to as many as the others leave room for (a captured decode
+    // step of 64 requests 30.7 us, with shares of 12 tokens 32.0).  Where that makes shares of more than 12 tokens, shares of 12 to 64, by the
     // call's size: enough to mix with K's CTAs.
     const int64_t room = (2 * (int64_t)sms - index_blocks - kv_blocks) / a.q.cut.groups;
     const int64_t per = (int64_t)a.T * a.q.cut.groups / (8 * (int64_t)sms);

@@ -45,7 +45,7 @@ int check_problem(const msa_rope_problem* p) {
 constexpr int kRowCtas = 3;  // of the largest size on an SM
 // Most tokens of a CTA: SMs differ in speed, and shares that all start at once end
 // when the slowest does (131k tokens x 152 heads 1725 us, in shares of 32 tokens
-// 1464; 32k x 68 208 and 172).
+// 1464; 32k x 68 208 and 175).
 constexpr int kRowTokens = 32;
 constexpr int kRowThreads = 32 * (kRowWarps + 1);
 template <bool kAdjacent>

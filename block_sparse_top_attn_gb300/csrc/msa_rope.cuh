@@ -396,7 +396,7 @@ MSA_DEV void copy_row(Stage& s, const uint16_t* row, int lane) {
 // Two tables in turn: the CTA's warps behind those of the rows (one, as a rule) fill
 // one while the others use the other.
 // (Filled by all warps, each its part, between a barrier and the next: 32k tokens x
-// 68 heads 203 us, and the warps' registers spill.)
+// 68 heads 190 us, with registers that spill, against 180.)
 template <bool kAdjacent>
 MSA_DEV bool fill_tables(const Angles& a, Table<kTile> (&tab)[2], bool bad, int before, int64_t first, int n,
                          int apart) {
