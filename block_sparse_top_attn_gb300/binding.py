@@ -689,7 +689,8 @@ class Rope:
     *_weight    bf16 or fp32, [128] for all heads or [heads, 128]; None: a norm without weights.
     The tensors are bf16 [tokens, heads, 128] whose last dim is contiguous (views of one projection's output will do).
     Outputs are new tensors of the call's stream, or those given as `out`.  Nothing synchronises; calls keep no state
-    but the problem descriptions, so that one object may serve several streams and captured graphs.
+    but the problem descriptions, so that one object may serve several streams and captured graphs.  status: the
+    status word of the calls around it (int32, device), whose errors then stop these too.
     """
 
     NAMES = ("q", "k", "q_index", "k_index")
@@ -707,6 +708,7 @@ class Rope:
             if w is not None and w.device != self.device:
                 raise ValueError(f"{name}_weight: need a tensor on {self.device}")
         self._args = dict(adjacent=adjacent, eps=eps, weight_offset=weight_offset, cos_scale=cos_scale)
+        self.status = torch.zeros(4, dtype=torch.int32, device=self.device)     # stays 0: the table's axes are in range
         self._problems = {}
 
     def _rows(self, name, x, tokens, heads=None):
@@ -796,9 +798,8 @@ class Rope:
         xs = self._given(T, q=q, k=k, q_index=q_index, k_index=k_index)
         with torch.cuda.device(self.device), torch.cuda.stream(stream):
             ys = self._outputs("out", out, xs, T)
-            st = torch.zeros(4, dtype=torch.int32, device=self.device) if status is None else status
             if T:
-                msa_norm_rope(self._problem(T, xs, ys), xs, positions, ys, st)
+                msa_norm_rope(self._problem(T, xs, ys), xs, positions, ys, self.status if status is None else status)
         return tuple(y for y in ys if y is not None)
 
     def backward(self, positions, grads, inputs, out=None, status=None, stream=None):
@@ -827,11 +828,10 @@ class Rope:
                     if x is not None and self._strides(dx) != self._strides(x):
                         raise ValueError(f"out of {name}: need the input's strides")
             dws = tuple(None if x is None or w is None else torch.empty_like(w) for x, w in zip(xs, self.weights))
-            st = torch.zeros(4, dtype=torch.int32, device=self.device) if status is None else status
             if T:
                 p = self._problem(T, xs, dys)
                 ws = torch.empty(msa_norm_rope_bwd_bytes(p), dtype=torch.uint8, device=self.device)
-                msa_norm_rope_bwd(p, dys, xs, positions, dxs, dws, st, ws)
+                msa_norm_rope_bwd(p, dys, xs, positions, dxs, dws, self.status if status is None else status, ws)
             else:
                 for dw in dws:
                     if dw is not None:

@@ -242,7 +242,7 @@ MSA_DEV Half round_half(const float* v, float amp, float mul, bool exact) {
     h.doubt = false;
   } else if (h.scale) {
     const float inv = __frcp_rn(scale_value(h.scale)) * mul;
-    // a quotient is at most 6.4 here, three more roundings of it 2^-20
+    // the quotient's own roundings: 4 u of it, which is no more than amp
     const float dq = exact ? 0.f : fmaf(amp * inv, kError, 9.5367431640625e-7f);
     const uint64_t inv2 = f2_pack(inv, inv), up = f2_pack(dq, dq), down = f2_pack(-dq, -dq);
     const uint64_t snap = f2_pack(768.f, 768.f);

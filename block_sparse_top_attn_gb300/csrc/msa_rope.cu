@@ -9,7 +9,7 @@
 namespace msa {
 namespace rope {
 
-constexpr int64_t kMaxStride = int64_t(1) << 40;
+constexpr int64_t kMaxStride = int64_t(1) << 38;  // times 2^24 tokens: within 64 bits
 
 // Rows of `heads` heads of `tokens` tokens that do not overlap, in 16-byte steps.
 static bool bad_strides(int64_t token, int64_t head, int64_t heads, int64_t tokens) {

@@ -537,7 +537,7 @@ enum { MSA_ROPE_NORM = 1, MSA_ROPE_ROTATE = 2, MSA_ROPE_PER_HEAD = 4, MSA_ROPE_W
  *           its gradient) is fp32, else bf16.
  * weight    device, or NULL for a norm without one (w + weight_offset is then 1).
  * x_token, x_head, y_token, y_head  elements from one token's row, and one head's,
- *           to the next: positive multiples of 8 that keep the rows apart. */
+ *           to the next: multiples of 8 from 128 to 2^38 that keep the rows apart. */
 typedef struct {
   int32_t heads;
   uint32_t flags;
@@ -559,7 +559,8 @@ typedef struct {
  * eps           2^-100 .. 2^100.
  * cos_scale     > 0 and finite; 1 but for stretched contexts.
  * pairs         device [R / 2], written from msa_rope_pairs' output.  An axis out
- *               of range counts as 0 and sets MSA_ERR_INVALID_ARGUMENT. */
+ *               of range counts as 0 and sets MSA_ERR_INVALID_ARGUMENT; parts of
+ *               the call that come up behind that are left out. */
 typedef struct {
   int32_t tokens;
   int32_t head_dim;

@@ -350,6 +350,27 @@ def test_rows_do_not_depend_on_the_call(B):
         assert all(torch.equal(a, b) for a, b in zip((*again[0], *again[1]), (*dxs, *dws)))
 
 
+def test_rows_far_apart(B):
+    """Rows whose offsets pass 32 bits, in elements and in bytes."""
+    import torch
+    L = Layer(B, seed=29)
+    T, far = 4, (1 << 30) + 8
+    buf = torch.empty((T - 1) * far + 16 * 128, dtype=torch.bfloat16, device="cuda")
+    x = buf.as_strided((T, 16, 128), (far, 128, 1))
+    bits = _bf16(L.rng, (T, 16, 128))
+    x.copy_(to_bf16_tensor(bits, "cuda"))
+    pos = L.positions(T)
+    want, = L.rope.forward(_dev(pos), to_bf16_tensor(bits, "cuda"))
+    dy = to_bf16_tensor(_bf16(L.rng, (T, 16, 128)), "cuda")
+    (dxw,), (dww,) = L.rope.backward(_dev(pos), [dy], [to_bf16_tensor(bits, "cuda")])
+    (dx,), (dw,) = L.rope.backward(_dev(pos), [dy], [x], out=[x])
+    assert torch.equal(dx, dxw) and torch.equal(dw, dww)
+    x.copy_(to_bf16_tensor(bits, "cuda"))
+    got, = L.rope.forward(_dev(pos), x, out=[x])
+    _check_forward(L, 0, bits, pos, want)
+    assert torch.equal(got, want)
+
+
 def test_replaced_weights(B):
     """A weight whose storage was replaced, and one that was changed in place: calls use what is there now."""
     import torch
@@ -706,6 +727,25 @@ def test_scales_next_to_their_borders(B):
     want = np.zeros(tuple(cache.shape), np.uint8)
     _expected_cache(L, want, k, v, pos, slots, 64)
     assert np.array_equal(cache.cpu().numpy(), want)
+
+
+def test_append_far_into_a_large_cache(B):
+    """Slots whose bytes lie beyond 4 GB, and their groups that are done again."""
+    import torch
+    L = Layer(B, seed=30, H=2)
+    P, T = 260_000, 300
+    c = B.make_cache_problem(num_requests=1, num_pages=P, max_blocks=8, num_q_heads=32, topk=1, token_cap=T, chunk_cap=1)
+    cache, st = B.new_cache(c), torch.zeros(4, dtype=torch.int32, device="cuda")
+    pos = L.positions(T)
+    k, v = _bf16(L.rng, (T, 2, 128)), _bf16(L.rng, (T, 2, 128))
+    slots = P * 64 - 1 - np.arange(T)
+    B.msa_cache_append_rope(c, _append_problem(B, L, T, False, False), None, to_bf16_tensor(k, "cuda"),
+                            to_bf16_tensor(v, "cuda"), None, None, _dev(pos), _dev(slots, torch.int64), None, None,
+                            None, None, cache, None, None, st)
+    want = np.zeros((5, 2, 1, 9216), np.uint8)
+    _expected_cache(L, want, k, v, pos, slots - (P - 5) * 64, 64)
+    assert np.array_equal(cache[-5:].cpu().numpy(), want) and int(st[0].item()) == 0
+    assert not torch.any(cache[:-5])
 
 
 @pytest.mark.parametrize("kw", [dict(H=2), dict(H=1, adjacent=True, rotary=64), dict(H=3, axes=3, per_head=True, wide=False),
