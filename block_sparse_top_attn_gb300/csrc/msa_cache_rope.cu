@@ -39,11 +39,10 @@ struct AppendRopeArgs {
 // ---------------------------------------------------------------------------
 // The cache keeps a value by the interval it lies in, so an error of fp32 counts
 // only next to a border, and there by a whole code.  With amp = |a cos| + |b sin| and
-// u = 2^-24, fp32 forms y to within 23 u amp: 13.5 u for the weighted a and b and the
+// u = 2^-24, fp32 forms y to within 23 u amp: 12 u for the weighted a and b and the
 // inverse rms (the sum of 128 squares in chains of 4 and 6 more additions, halved by
-// the root; rsqrtf 2 ulp; the weight's offset and products), 5 u for the angle's
-// function (1 ulp; its argument's rounding and the scale), the products and the sum;
-// the code's quotient adds 2 u.  A group with a value (or a scale) nearer to a border than 32 u amp is
+// the root; rsqrtf 2 ulp; the weight's offset and products), 7 u for the cosine with
+// its scale, the products and the sum; the code's quotient adds 4 u.  A group with a value (or a scale) nearer to a border than 32 u amp is
 // done again in fp64, from the inputs, behind the others: one group in 1,000, which
 // costs a step of 64 tokens 1 us of 8.
 constexpr float kUlps = 32.f;
