@@ -274,7 +274,7 @@ constexpr int kSumParts = 16;
 __global__ void __launch_bounds__(32 * kSumParts) weight_sum_kernel(SumArgs a) {
   __shared__ float s_part[kSumParts][32];
   cache::after_previous_kernel();
-  if (__syncthreads_or(status_bad(a.status))) return;
+  const bool bad = status_bad(a.status);  // decided on below: the load does not hold up the others
   const int all = blockIdx.x >> 2;  // row of all tensors' weights
   int row = all, slot = a.slot[0], per = a.per[0], wide = a.wide[0];
   void* dw = a.dw[0];
@@ -301,8 +301,7 @@ __global__ void __launch_bounds__(32 * kSumParts) weight_sum_kernel(SumArgs a) {
     }
   }
   s_part[part][threadIdx.x & 31] = s;
-  __syncthreads();
-  if (part) return;
+  if (__syncthreads_or(bad) || part) return;
   s = 0.f;
 #pragma unroll
   for (int i = 0; i < kSumParts; ++i) s += s_part[i][threadIdx.x];
