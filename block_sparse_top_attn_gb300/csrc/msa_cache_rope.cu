@@ -42,86 +42,110 @@ struct AppendRopeArgs {
 // u = 2^-24, fp32 forms y to within 23 u amp: 12 u for the weighted a and b and the
 // inverse rms (the sum of 128 squares in chains of 4 and 6 more additions, halved by
 // the root; rsqrtf 2 ulp; the weight's offset and products), 7 u for the cosine with
-// its scale, the products and the sum; the code's quotient adds 4 u.  A group with a value (or a scale) nearer to a border than 32 u amp is
-// done again in fp64, from the inputs, behind the others: one group in 1,000, which
-// costs a step of 64 tokens 1 us of 8.
+// its scale, the products and the sum; the code's quotient adds 4 u.  A group with a
+// value (or a scale) nearer to a border than 32 u amp is done again exactly, from the
+// inputs, behind the others: one group in 1,000, which costs a step of 64 tokens 0.7
+// us of 6.0.
 constexpr float kUlps = 32.f;
 
-// Cosine and sine of a fraction of a turn in fp64, to 10^-11: the quarter turns are
-// taken off exactly, and the Taylor polynomials do for the eighth that is left.  What
-// is nearer to a border than that is one value in 10^10; short code counts more here,
-// as the few warps that come this way fetch it anew (a step of 64 tokens 8.2 us, with
-// the library's functions 8.4).
-MSA_DEV void cos_sin64(uint64_t turn, double& c, double& s) {
+// Exact enough means pairs of fp32, hi + lo, by the error-free sums and products of
+// Knuth and Dekker: an fp64 instruction takes a warp 70 cycles here, a product of
+// pairs 16 (a step of 64 tokens 6.0 us, in fp64 7.7).  Errors stay below 2^-38 of
+// amp; what is nearer to a border than that is one value in 10^10.
+struct Split {
+  float hi, lo;
+};
+// x as a pair, for constants.
+__host__ __device__ constexpr Split parts(double x) { return Split{(float)x, (float)(x - (double)(float)x)}; }
+MSA_DEV Split sum_of(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return Split{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+MSA_DEV Split sum_of(Split a, Split b) {
+  Split s = sum_of(a.hi, b.hi);
+  s.lo += a.lo + b.lo;
+  return s;
+}
+MSA_DEV Split product(Split a, Split b) {
+  const float p = __fmul_rn(a.hi, b.hi);
+  return Split{p, fmaf(a.hi, b.lo, fmaf(a.lo, b.hi, __fmaf_rn(a.hi, b.hi, -p)))};
+}
+// k + z * x, |k| above the product.
+MSA_DEV Split horner(Split k, Split z, Split x) {
+  const Split p = product(z, x);
+  const float s = __fadd_rn(k.hi, p.hi);
+  return Split{s, __fadd_rn(__fsub_rn(k.hi, s), p.hi) + (p.lo + k.lo)};
+}
+
+// Cosine and sine of a fraction of a turn: the quarter turns are taken off exactly, and
+// the Taylor polynomials do for the eighth that is left (48 of its bits).
+MSA_DEV void cos_sin_split(uint64_t turn, Split& c, Split& s) {
   const uint64_t shifted = turn + (1ull << 61);
   const int64_t rest = (int64_t)(turn - (shifted & (3ull << 62)));
-  const double x = (double)rest * 3.4061215800865545e-19, z = x * x;  // pi 2^-63
-  double sn = fma(z, -1.0 / 39916800, 1.0 / 362880), cs = fma(z, 1.0 / 479001600, -1.0 / 3628800);
-  sn = fma(z, sn, -1.0 / 5040);
-  cs = fma(z, cs, 1.0 / 40320);
-  sn = fma(z, sn, 1.0 / 120);
-  cs = fma(z, cs, -1.0 / 720);
-  sn = fma(z, sn, -1.0 / 6);
-  cs = fma(z, cs, 1.0 / 24);
-  sn = fma(x * z, sn, x);
-  cs = fma(z, cs, -0.5);
-  cs = fma(z, cs, 1.0);
+  const uint64_t size = rest < 0 ? 0 - (uint64_t)rest : (uint64_t)rest;  // up to 2^61
+  const float a = (float)(uint32_t)(size >> 37), b = (float)((uint32_t)(size >> 13) & 0xFFFFFFu);
+  constexpr Split unit = parts(4.681337853654911e-08);  // pi 2^-26
+  Split x;
+  x.hi = __fmul_rn(a, unit.hi);
+  x.lo = fmaf(b, 2.7902947984069054e-15f, fmaf(a, unit.lo, __fmaf_rn(a, unit.hi, -x.hi)));  // pi 2^-50
+  if (rest < 0) x = Split{-x.hi, -x.lo};
+  const Split z = product(x, x);
+  constexpr Split one = parts(1.0), s3 = parts(-1.0 / 6), s5 = parts(1.0 / 120), s7 = parts(-1.0 / 5040);
+  constexpr Split c2 = parts(-0.5), c4 = parts(1.0 / 24), c6 = parts(-1.0 / 720);
+  Split sn{fmaf(z.hi, fmaf(z.hi, 1.f / 6227020800.f, -1.f / 39916800.f), 1.f / 362880.f), 0.f};
+  Split cs{fmaf(z.hi, fmaf(z.hi, 1.f / 479001600.f, -1.f / 3628800.f), 1.f / 40320.f), 0.f};
+  sn = product(x, horner(one, z, horner(s3, z, horner(s5, z, horner(s7, z, sn)))));
+  cs = horner(one, z, horner(c2, z, horner(c4, z, horner(c6, z, cs))));
   const int quarter = (int)(shifted >> 62);
   c = quarter & 1 ? sn : cs;
   s = quarter & 1 ? cs : sn;
-  if (quarter == 1 || quarter == 2) c = -c;
-  if (quarter >= 2) s = -s;
+  if (quarter == 1 || quarter == 2) c = Split{-c.hi, -c.lo};
+  if (quarter >= 2) s = Split{-s.hi, -s.lo};
 }
-// 1 / sqrt(m) in fp64 to 10^-13, m >= 2^-100: a step of Newton's method from the fp32 one.
-MSA_DEV double inverse_root64(double m) {
-  const bool far = m > 1e30;
-  double r = (double)rsqrtf((float)(far ? m * 2.938735877055719e-39 : m));  // 2^-128
-  if (far) r *= 5.421010862427522e-20;                                      // 2^-64
-  return fma(r * 0.5, fma(-m * r, r, 1.0), r);
+// factor / sqrt(m), 2^-100 <= m: a step of Newton's method from the fp32 root of m
+// times an even power of two.
+MSA_DEV Split inverse_root(Split m, float factor) {
+  const int e = (int)(__float_as_uint(m.hi) >> 23) - 127 & ~1;
+  const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+  const float h = m.hi * down, l = m.lo * down, r = rsqrtf(h), p = __fmul_rn(r, r);
+  // 1 - m r^2
+  const float t = fmaf(-l, p, fmaf(-h, __fmaf_rn(r, r, -p), fmaf(-h, p, 1.f)));
+  factor *= __uint_as_float((uint32_t)(127 - e / 2) << 23);
+  return Split{r * factor, r * 0.5f * t * factor};
 }
 
-// Dim `d` of a K row (in shared memory) times its weight and rotated, in fp64; what is
-// left of the norm is the row's inverse rms.
+// Dim `d` of a K row (in shared memory) times `scale` and its weight and rotated; what
+// is left of the norm is the row's inverse rms.
 template <bool kAdjacent>
-MSA_DEV double turned_dim(const AppendRopeArgs& a, const uint4* row, int head, int64_t t, int d) {
+MSA_DEV Split turned_dim(const AppendRopeArgs& a, const uint4* row, float scale, int head, int64_t t, int d) {
   auto weighted = [&](int i) {
     const uint32_t x = reinterpret_cast<const uint16_t*>(row + granule_slot(i >> 3))[i & 7];
-    const double v = (double)__uint_as_float(x << 16);
+    const Split v{__uint_as_float(x << 16) * scale, 0.f};
     if (!(a.k.flags & MSA_ROPE_NORM) || !a.k.w) return v;
     const int64_t at = (a.k.flags & MSA_ROPE_PER_HEAD ? head * 128 : 0) + i;
     const float w = a.k.flags & MSA_ROPE_WEIGHT_FP32
                         ? static_cast<const float*>(a.k.w)[at]
                         : __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.k.w)[at] << 16);
-    return v * ((double)w + (double)a.q.offset);
+    return product(v, sum_of(w, a.q.offset));
   };
   const int R = a.q.an.R;
-  const double own = weighted(d);
+  const Split own = weighted(d);
   if (!(a.k.flags & MSA_ROPE_ROTATE) || d >= R) return own;
   const bool second = kAdjacent ? d & 1 : d >= R / 2;
   const int p = kAdjacent ? d >> 1 : second ? d - R / 2 : d;
   const int partner = kAdjacent ? d ^ 1 : second ? p : d + R / 2;
-  double s, c;
-  cos_sin64(turn_of(a.q.an, load_pair(a.q.an, p), t), c, s);
-  const double other = weighted(partner);
-  return (second ? fma(own, c, other * s) : fma(own, c, -(other * s))) * (double)a.q.an.scale;
+  Split s, c;
+  cos_sin_split(turn_of(a.q.an, load_pair(a.q.an, p), t), c, s);
+  if (!second) s = Split{-s.hi, -s.lo};
+  return product(sum_of(product(own, c), product(weighted(partner), s)), Split{a.q.an.scale, 0.f});
 }
 
 MSA_DEV float scale_value(uint32_t s8) {
   return __half2float(__ushort_as_half((uint16_t)(cache::e4m3x2_to_half(s8) & 0xFFFFu)));
 }
 
-// A non-negative fp64 value as two fp32: compared with a border that fp32 holds, the
-// second part decides where the first is equal.
-struct Split {
-  float hi, lo;
-};
-MSA_DEV Split split(double x) {
-  Split s;
-  s.hi = (float)x;
-  s.lo = s.hi < kInf ? (float)(x - (double)s.hi) : 0.f;
-  return s;
-}
-// x lies above the border, or on it and `up`.
+// A pair whose second part is no more than a rounding of the first lies above a border
+// that fp32 holds, or on it and `up`.
 MSA_DEV bool beyond(const Split& x, float border, bool up) {
   return x.hi > border || (x.hi == border && (x.lo > 0.f || (x.lo == 0.f && up)));
 }
@@ -155,28 +179,43 @@ MSA_DEV uint8_t* cache_tile(const AppendRopeArgs& a, int64_t slot, int head, int
                        cache::kTileBytes;
 }
 
-// Codes and scale of 16 dims from dim0 on of token t's K row, in fp64, by half a warp, a
-// lane a dim; the two halves of a warp may have different groups.
+// Codes and scale of 16 dims from dim0 on of token t's K row, by half a warp, a lane a
+// dim (the other half does the same).
 template <bool kAdjacent>
 MSA_DEV void exact_group(const AppendRopeArgs& a, const uint4* row, int64_t slot, int64_t t, int head, int dim0) {
   const int lane = threadIdx.x & 15;
-  const double turned = turned_dim<kAdjacent>(a, row, head, t, dim0 + lane);
-  double r = 1.0;
+  Split r{a.k_mul, 0.f};
+  float scale = 1.f;
   if (a.k.flags & MSA_ROPE_NORM) {
     const uint4 u = row[granule_slot(lane)];
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    double s = 0.0;
+    auto sum = [&]() {  // of the squares of the row times scale; a square is exact
+      Split s{0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const double lo = (double)__uint_as_float(w[i] << 16), hi = (double)__uint_as_float(w[i] & 0xFFFF0000u);
-      s = fma(lo, lo, fma(hi, hi, s));
+      for (int i = 0; i < 8; ++i) {
+        const float x = __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16) * scale;
+        s = sum_of(s, Split{__fmul_rn(x, x), 0.f});
+      }
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1)
+        s = sum_of(s, Split{__shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o)});
+      return s;
+    };
+    Split s = sum();
+    float eps = a.q.eps;
+    if (__any_sync(0xffffffffu, !(s.hi < kInf))) {  // all lanes have the same sum
+      scale = 5.421010862427522e-20f;               // 2^-64
+      eps *= scale * scale;
+      s = sum();
     }
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    r = inverse_root64(fma(s, 1.0 / 128.0, (double)a.q.eps));
+    Split m = sum_of(s.hi * (1.f / 128.f), eps);
+    m.lo += s.lo * (1.f / 128.f);
+    r = inverse_root(m, a.k_mul);
   }
-  const double y = turned * (r * (double)a.k_mul);
-  const Split own = split(fabs(y));
+  const Split turned = product(turned_dim<kAdjacent>(a, row, scale, head, t, dim0 + lane), r);
+  Split own = sum_of(turned.hi, turned.lo);
+  const bool negative = own.hi < 0.f;
+  own = Split{fabsf(own.hi), own.hi < kInf && own.hi > -kInf ? (negative ? -own.lo : own.lo) : 0.f};
   Split m = own;
 #pragma unroll
   for (int o = 1; o < 16; o <<= 1) {
@@ -184,7 +223,7 @@ MSA_DEV void exact_group(const AppendRopeArgs& a, const uint4* row, int64_t slot
     if (other.hi > m.hi || (other.hi == m.hi && other.lo > m.lo)) m = other;
   }
   const uint32_t s8 = exact_scale(m);
-  uint32_t codes = exact_code(own, y < 0.0, scale_value(s8)) << 4 * (lane & 7);
+  uint32_t codes = exact_code(own, negative, scale_value(s8)) << 4 * (lane & 7);
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) codes |= __shfl_xor_sync(0xffffffffu, codes, o);
   int tok;
@@ -370,23 +409,19 @@ MSA_DEV void kv_block(const AppendRopeArgs& a, int block, bool bad, KvShared& s)
       *reinterpret_cast<uint2*>(out + cache::OFF_VC + cache::v_code_offset(tok, j)) = vc;
       out[cache::OFF_VS + j * cache::kTile + tok] = (uint8_t)vs;
     }
-    // Groups in doubt, by their first lane; two at a time (64 tokens 7.7 us, one at a time 8.2).
+    // Groups in doubt, by their first lane.
     auto groups = [&](bool doubt) {  // one of a group's lanes may see it, or both
       const unsigned m = __ballot_sync(0xffffffffu, live && doubt);
       return (uint64_t)((m | m >> 1) & 0x55555555u);
     };
     uint64_t left = groups(ha.doubt) | groups(hb.doubt) << 32;
     if (left) __syncwarp();  // what is there of the groups is overwritten
-    while (left) {
-      const int one = __ffsll(left) - 1;
-      left &= left - 1;
-      const int two = left ? __ffsll(left) - 1 : one;
-      left &= left - 1;
-      const int mine = lane < 16 ? one : two, from = mine & 31;
-      const int dim_a = __shfl_sync(0xffffffffu, da, from), dim_b = __shfl_sync(0xffffffffu, db, from);
+    for (; left; left &= left - 1) {
+      const int group = __ffsll(left) - 1, from = group & 31;
+      const int dim0 = __shfl_sync(0xffffffffu, group < 32 ? da : db, from);
       const int64_t at = __shfl_sync(0xffffffffu, slot, from), token = __shfl_sync(0xffffffffu, t, from);
       const int head = __shfl_sync(0xffffffffu, h, from);
-      exact_group<kAdjacent>(a, s.ring[warp][stage][0].row[from >> 3], at, token, head, mine < 32 ? dim_a : dim_b);
+      exact_group<kAdjacent>(a, s.ring[warp][stage][0].row[from >> 3], at, token, head, dim0);
     }
   }
 }
@@ -706,8 +741,8 @@ extern "C" int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_
   if (a.q.heads) {
     a.q.cut = rope::cut_rows(a.q.heads, a.T, sms, 2 * rope::kWarps, rope::kWarps - 1);
     // In a step all CTAs should run at once: q's tokens go to as many as the others leave room for (a captured decode
-    // step of 64 requests 30.7 us, with shares of 12 tokens 32.0).  Where that makes shares of more than 12 tokens, shares of 12 to 64, by the
-    // call's size: enough to mix with K's CTAs.
+    // step of 64 requests 30.7 us, with shares of 12 tokens 32.0).  Where that makes shares of more than 12 tokens,
+    // shares of 12 to 64, by the call's size: enough to mix with K's CTAs.
     const int64_t room = (2 * (int64_t)sms - index_blocks - kv_blocks) / a.q.cut.groups;
     const int64_t per = (int64_t)a.T * a.q.cut.groups / (8 * (int64_t)sms);
     const int64_t tokens = room > 0 && a.T <= 12 * room ? (a.T + room - 1) / room : per < 12 ? 12 : per > 64 ? 64 : per;
