@@ -632,7 +632,7 @@ MSA_DEV bool takes_turn(int64_t& block, int64_t count, int64_t of) {
 template <bool kAdjacent, int kCtas>
 __global__ void __launch_bounds__(kThreads, kCtas) append_rope_kernel(AppendRopeArgs a) {
   extern __shared__ __align__(16) uint8_t s_raw[];
-  cache::after_previous_kernel();
+  after_previous_few();
   const bool bad = status_bad(a.status);
   int64_t block = blockIdx.x;
   if (block < a.index_blocks) {

@@ -51,7 +51,7 @@ constexpr int kRowThreads = 32 * (kRowWarps + 1);
 template <bool kAdjacent>
 __global__ void __launch_bounds__(kRowThreads, kRowCtas) norm_rope_kernel(RowsArgs a) {
   extern __shared__ __align__(16) uint8_t s_raw[];
-  cache::after_previous_kernel();
+  after_previous_few();
   rows_block<kAdjacent>(a, blockIdx.x, status_bad(a.status), *reinterpret_cast<RowsShared*>(s_raw));
 }
 
