@@ -29,6 +29,7 @@ struct AppendRopeArgs {
   int64_t slots;         // num_pages * B
   float k_mul, v_mul;    // 2^-exp
   int index_blocks, kv_blocks;  // CTAs of index keys, of K and V; the others take q's rows
+  uint64_t kv_turns;            // takes_turn
   int index_heads, index_groups, index_chunks;  // heads of a CTA, CTAs of a chunk's heads, chunks of a CTA
   int kv_tile, kv_groups, kv_heads;  // tokens of a tile; groups of heads side by side, heads of a group
   int32_t* status;
@@ -44,14 +45,14 @@ struct AppendRopeArgs {
 // the root; rsqrtf 2 ulp; the weight's offset and products), 7 u for the cosine with
 // its scale, the products and the sum; the code's quotient adds 4 u.  A group with a
 // value (or a scale) nearer to a border than 32 u amp is done again exactly, from the
-// inputs, behind the others: one group in 1,000, which costs a step of 64 tokens 0.7
-// us of 6.0.
+// inputs, behind the others: one group in 1,000, which costs a step of 64 tokens 0.7 us
+// of 5.1.
 constexpr float kUlps = 32.f;
 
 // Exact enough means pairs of fp32, hi + lo, by the error-free sums and products of
 // Knuth and Dekker: an fp64 instruction takes a warp 70 cycles here, a product of
-// pairs 16 (a step of 64 tokens 6.0 us, in fp64 7.7).  Errors stay below 2^-38 of
-// amp; what is nearer to a border than that is one value in 10^10.
+// pairs 16 (a step of 64 tokens was 7.7 us with fp64, and 6.0 with pairs).  Errors stay
+// below 2^-38 of amp; what is nearer to a border than that is one value in 10^10.
 struct Split {
   float hi, lo;
 };
@@ -617,22 +618,26 @@ MSA_DEV void index_block(const AppendRopeArgs& a, int block, bool bad, IndexShar
 
 constexpr size_t kAppendShared = sizeof(IndexShared);
 static_assert(sizeof(RowsShared) <= kAppendShared && sizeof(KvShared) <= kAppendShared, "one size for every CTA");
-// The CTAs of index keys come first: a block's mean takes longest.  Those of K and V
-// and of Q then take turns in proportion to their numbers: K's are bound by
-// instructions and Q's by memory, and an SM should hold both.
-MSA_DEV bool takes_turn(int64_t& block, int64_t count, int64_t of) {
-  const int64_t before = block * count / of, after = (block + 1) * count / of;
+// The CTAs of index keys come first: a block's mean takes longest.  Where CTAs come in
+// many waves, those of K and V and of Q then take turns in proportion to their numbers:
+// K's are bound by instructions and Q's by memory, and an SM should hold both (4 x 8192
+// tokens 407 us, with K's before Q's 435).  Where all run together K's come before Q's.
+// turns: count * 2^32 / of, rounded up, so that `of` turns take count.
+MSA_DEV bool takes_turn(int64_t& block, uint64_t turns) {
+  const int64_t before = (int64_t)(block * turns >> 32), after = (int64_t)((block + 1) * turns >> 32);
   block = after > before ? before : block - before;
   return after > before;
 }
 // kCtas: of an SM.  Two leave room for more loads under way at once, which counts where
-// all CTAs run together (a step of 256 tokens 10.3 us, with three 12.8; 2,200 tokens of
-// prompt pieces 33, 41); where they come in many waves three do more (4 x 8192 tokens
-// 434 us, with three 417).
+// all CTAs run together (a step of 256 tokens 8.0 us, with three 10.9; 2,900 tokens of
+// prompt pieces 27, 34); where they come in many waves three do more (4 x 8192 tokens
+// 423 us, with three 407).
 template <bool kAdjacent, int kCtas>
 __global__ void __launch_bounds__(kThreads, kCtas) append_rope_kernel(AppendRopeArgs a) {
   extern __shared__ __align__(16) uint8_t s_raw[];
-  after_previous_few();
+  // The next kernel's CTAs do not come up early: beside these they take slots and issue (a captured decode step of 16
+  // requests 22.6 us, with them 25.0; an append of 256 tokens and its read 11.6, 16.3).
+  cache::after_previous_kernel<false>();
   const bool bad = status_bad(a.status);
   int64_t block = blockIdx.x;
   if (block < a.index_blocks) {
@@ -640,7 +645,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) append_rope_kernel(AppendRope
     return;
   }
   block -= a.index_blocks;
-  if (takes_turn(block, a.kv_blocks, (int64_t)gridDim.x - a.index_blocks))
+  bool kv = block < a.kv_blocks;
+  if constexpr (kCtas == 3) kv = takes_turn(block, a.kv_turns);
+  else if (!kv) block -= a.kv_blocks;
+  if (kv)
     kv_block<kAdjacent>(a, (int)block, bad, *reinterpret_cast<KvShared*>(s_raw));
   else
     rows_block<kAdjacent>(a.q, (int)block, bad, *reinterpret_cast<RowsShared*>(s_raw));
@@ -722,14 +730,15 @@ extern "C" int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_
   a.v_mul = cache::exp2i(-c->v_exp);
   a.kv_groups = (H + 7) / 8;
   a.kv_heads = (H + a.kv_groups - 1) / a.kv_groups;
-  int rows = 4;  // tokens that give a CTA's eight warps work
-  while (rows < rope::kKvTile && rows * a.kv_heads < rope::kIndexRows) rows *= 2;
+  // Tokens that give half of a CTA's warps work (a step of 64 tokens 5.1 us, all of them 5.4).
+  int rows = 4;
+  while (rows < rope::kKvTile && rows * a.kv_heads < rope::kIndexRows / 2) rows *= 2;
   a.kv_tile = rope::cut_tokens(a.T, a.kv_groups, sms, rows < 16 ? 16 : rows, rows);
   const int64_t kv_blocks = (int64_t)((a.T + a.kv_tile - 1) / a.kv_tile) * a.kv_groups;
   // Few heads and chunks to a CTA where the CTAs find room, so that heads, and blocks that end in neighbouring chunks
   // (requests of one length), do not wait for one another; else eight heads, which share their angles (4 x 8192 tokens
-  // 444 us, with two 470).  A mean takes longest among chunks of several tokens, by the capacities: one head there
-  // (prompt pieces 29 us, with two 32), two for single tokens (a step of 256 9.5, with one 13.1).
+  // 406 us, with two 431).  A mean takes longest among chunks of several tokens, by the capacities: one head there
+  // (prompt pieces 27.2 us, with two 29.6), two for single tokens (a step of 256 8.1, with one 12.9).
   const bool prompts = c->token_cap / c->chunk_cap >= 3;
   a.index_heads = (int64_t)c->chunk_cap * H > 16 * (int64_t)sms ? 8 : prompts ? 1 : rope::kIndexHeads;
   a.index_groups = (H + a.index_heads - 1) / a.index_heads;
@@ -740,8 +749,8 @@ extern "C" int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_
   int64_t q_blocks = 0;
   if (a.q.heads) {
     a.q.cut = rope::cut_rows(a.q.heads, a.T, sms, 2 * rope::kWarps, rope::kWarps - 1);
-    // In a step all CTAs should run at once: q's tokens go to as many as the others leave room for (a captured decode
-    // step of 64 requests 30.7 us, with shares of 12 tokens 32.0).  Where that makes shares of more than 12 tokens,
+    // In a step all CTAs should run at once: q's tokens go to as many as the others leave room for (a step of 64 tokens
+    // 5.4 us, with shares of 12 tokens 6.1).  Where that makes shares of more than 12 tokens,
     // shares of 12 to 64, by the call's size: enough to mix with K's CTAs.
     const int64_t room = (2 * (int64_t)sms - index_blocks - kv_blocks) / a.q.cut.groups;
     const int64_t per = (int64_t)a.T * a.q.cut.groups / (8 * (int64_t)sms);
@@ -752,6 +761,8 @@ extern "C" int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_
   if (index_blocks + kv_blocks + q_blocks > INT32_MAX) return MSA_ERR_UNSUPPORTED_SHAPE;
   a.index_blocks = (int)index_blocks;
   a.kv_blocks = (int)kv_blocks;
+  const uint64_t turns = (uint64_t)(kv_blocks + q_blocks);
+  a.kv_turns = turns ? (((uint64_t)kv_blocks << 32) + turns - 1) / turns : 0;
   const bool many = index_blocks + kv_blocks + q_blocks > 8 * (int64_t)sms;
   auto* kernel = p->adjacent ? (many ? rope::append_rope_kernel<true, 3> : rope::append_rope_kernel<true, 2>)
                              : (many ? rope::append_rope_kernel<false, 3> : rope::append_rope_kernel<false, 2>);

@@ -374,17 +374,6 @@ struct RowsArgs {
   int32_t* status;
 };
 
-// after_previous_kernel, where the next kernel's CTAs come up early if this one leaves
-// SMs free only: beside CTAs on every SM they take the place of those still to come,
-// and the issue slots of those that run (an append of 256 tokens with a read of it
-// behind 17.0 us, so 12.0; a captured decode step of 256 requests 113.6, so 112.4; a
-// step of one request, always late, 22.1, so 21.4).
-constexpr unsigned kFewCtas = 152;
-MSA_DEV void after_previous_few() {
-  if (gridDim.x <= kFewCtas) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  cache::after_previous_kernel<false>();
-}
-
 // Index of the tensor that flattened head `hh` belongs to, and its head there.
 template <class Args>
 MSA_DEV int tensor_of(const Args& a, int hh, int& head) {
