@@ -169,13 +169,14 @@ MSA_DEV bool plan_index(const Args& a, int g, bool report, IndexPlan& x) {
   const int4 c = reinterpret_cast<const int4*>(a.chunks)[g];
   const int r = c.x, row0 = c.y, n = c.z, pos0 = c.w;
   if (r < 0) return false;
+  const int lb = 31 - __clz(a.B);  // a block is a power of two
   int cu0 = 0, cu1 = 0;
   bool good = r < a.R && n >= 1 && n <= kChunk && row0 >= 0 && row0 <= a.T - n && pos0 >= 0;
   if (good) {
     cu0 = a.cu_tokens[r];
     cu1 = a.cu_tokens[r + 1];
     good = cu0 >= 0 && cu0 <= row0 && cu1 >= row0 + n && cu1 <= a.T && pos0 >= row0 - cu0 &&
-           pos0 <= a.positions - (cu1 - row0) && pos0 % a.B + n <= a.B;
+           pos0 <= a.positions - (cu1 - row0) && (pos0 & (a.B - 1)) + n <= a.B;
   }
   if (!good) {
     if (report) set_status(a.status, MSA_ERR_INVALID_CACHE);
@@ -183,12 +184,12 @@ MSA_DEV bool plan_index(const Args& a, int g, bool report, IndexPlan& x) {
   }
   const int end = pos0 + (cu1 - row0);     // position behind the request's last new token
   const int past = pos0 - (row0 - cu0);
-  const int blk0 = past / a.B, blk = pos0 / a.B, open = end / a.B;
-  const bool shared_buffer = open > blk0 && (open & 1) == (blk0 & 1) && past % a.B != 0;
+  const int blk0 = past >> lb, blk = pos0 >> lb, open = end >> lb;
+  const bool shared_buffer = open > blk0 && (open & 1) == (blk0 & 1) && (past & (a.B - 1)) != 0;
   x.r = r; x.cu0 = cu0; x.past = past; x.open = open;
   x.last = -1;
   if (row0 == cu0 && open > blk0) x.last = cu0 + (blk0 + 1) * a.B - past - 1;
-  else if (row0 != cu0 && blk > blk0 && (pos0 + n) % a.B == 0) x.last = row0 + n - 1;
+  else if (row0 != cu0 && blk > blk0 && ((pos0 + n) & (a.B - 1)) == 0) x.last = row0 + n - 1;
   x.avg_blk = row0 == cu0 ? blk0 : blk;
   x.p0 = x.p1 = 0;
   if (shared_buffer) {

@@ -580,7 +580,7 @@ MSA_DEV void average_heads(const AppendRopeArgs& a, const cache::IndexPlan& x, i
     }
     if (seg == averages - 1) {
       const float inv = 1.f / (float)a.B;  // a power of two: the product is the quotient
-      *reinterpret_cast<uint32_t*>(a.index_pool + (slot / a.B) * hs + h0 * 128 + 2 * tid) =
+      *reinterpret_cast<uint32_t*>(a.index_pool + (slot >> (a.B == 128 ? 7 : 6)) * hs + h0 * 128 + 2 * tid) =
           pack_bf16x2(lo * inv, hi * inv);
     }
   }
