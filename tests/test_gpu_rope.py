@@ -698,6 +698,30 @@ def test_codes_of_many_values(B, kw):
     assert np.array_equal(cache.cpu().numpy(), want) and int(st[0].item()) == 0
 
 
+@pytest.mark.parametrize("kw", [dict(H=4), dict(H=3, adjacent=True, per_head=True, rotary=96)])
+@pytest.mark.parametrize("exp", [-32, 0, 9])
+def test_codes_of_rows_of_all_sizes(B, kw, exp):
+    """A million values of rows from 2^-12 to 2^119, whose squares leave fp32's range in a third of them: groups that
+    fp32 does not tell are those of the exact value there too."""
+    import torch
+    L = Layer(B, seed=44, base=1e4, **kw)
+    T = 3000
+    pos = L.positions(T, 1 << 17)
+    size = 2.0 ** np.array([-12, -3, 0, 40, 59, 61, 64, 90, 119])[np.arange(T) % 9]
+    k, v = (_bf16(L.rng, (T, L.H, 128), size[:, None, None]) for _ in range(2))
+    v = np.where(size[:, None, None] < 1e9, v, 0).astype(v.dtype)
+    c = B.make_cache_problem(num_requests=1, num_pages=T // 64 + 1, max_blocks=T // 64 + 1, num_q_heads=16 * L.H, topk=1,
+                             token_cap=T, chunk_cap=1, k_exp=exp, v_exp=0)
+    cache, st = B.new_cache(c), torch.zeros(4, dtype=torch.int32, device="cuda")
+    slots = L.rng.permutation(T).astype(np.int64)
+    B.msa_cache_append_rope(c, _append_problem(B, L, T, False, False), None, to_bf16_tensor(k, "cuda"),
+                            to_bf16_tensor(v, "cuda"), None, None, _dev(pos), _dev(slots, torch.int64), None, None,
+                            None, None, cache, None, None, st)
+    want = np.zeros(tuple(cache.shape), np.uint8)
+    _expected_cache(L, want, k, v, pos, slots, 64, (exp, 0))
+    assert np.array_equal(cache.cpu().numpy(), want) and int(st[0].item()) == 0
+
+
 def test_scales_next_to_their_borders(B):
     """Groups whose largest value is steered next to a border between two scales, on either side of it, by the weight:
     the scale is that of the exact value."""
