@@ -143,7 +143,7 @@ struct Filler {
     if (thread < n) tab.live[thread] = a.positions[(t0 + (int64_t)thread * apart) * a.A] >= 0;
     if (at < 0 || row0 >= n) return;
     // Positions a row ahead.  Not unrolled: in a short call the code's own way to the SM counts (a step of 256 tokens
-    // 10.4 us, so 9.4).
+    // 10.4 us, so 9.9).
     const int32_t* src = a.positions + (t0 + (int64_t)row0 * apart) * a.A;
     const int64_t next = (int64_t)step * apart * a.A;
     int q0 = src[p0.axis], q1 = src[p1.axis];
