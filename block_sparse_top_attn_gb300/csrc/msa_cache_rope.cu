@@ -205,8 +205,8 @@ MSA_DEV void exact_group(const AppendRopeArgs& a, const uint4* row, int64_t slot
     Split s = sum();
     float eps = a.q.eps;
     if (__any_sync(0xffffffffu, !(s.hi < kInf))) {  // all lanes have the same sum
-      scale = 5.421010862427522e-20f;               // 2^-64
-      eps *= scale * scale;
+      scale = kDown;
+      eps = eps * scale * scale;
       s = sum();
     }
     Split m = sum_of(s.hi * (1.f / 128.f), eps);

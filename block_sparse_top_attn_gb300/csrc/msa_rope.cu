@@ -84,15 +84,15 @@ struct GradArgs {
   int32_t* status;
 };
 
-// 1 / sqrt(mean + eps) of a row's sum of squares.  Rows whose squares leave fp32's
-// range are scaled by 2^-64 first (msa_rope.cuh); v holds the row times `scale` after
-// it (v * result is the normed row either way).  Whole warps call it.
+// 1 / sqrt(mean + eps) of a row's sum of squares.  v holds the row times `scale` (1, or
+// kDown where its squares leave fp32's range) after it: v * result is the normed row
+// either way.  Whole warps call it.
 MSA_DEV float inverse_rms(Values& v, float sum, float eps, float& scale) {
   scale = 1.f;
   if (__any_sync(0xffffffffu, !(sum < kInf))) {
     const bool far = !(sum < kInf);
     if (far) {
-      scale = 5.421010862427522e-20f;  // 2^-64
+      scale = kDown;
       eps = 0.f;
     }
     times(v, scale);

@@ -289,10 +289,14 @@ MSA_DEV void rotate(Values& v, const float4* row, int j) {
   }
 }
 
+// Rows whose squares leave fp32's range (they have an element above 2^60) are scaled by
+// this first: of any bf16 values 128 squares then sum to 2^127 at most, and what a small
+// value beside a large one loses, 2^-82, is 2^-139 of its normed one.
+constexpr float kDown = 3.3881317890172014e-21f;  // 2^-68
+
 // A row's values times its weights, and what is left of the norm, 1 / sqrt(mean(x^2) +
 // eps) (1 without a norm), which waits for the other lanes while the values are
-// turned.  Rows whose squares leave fp32's range (elements above 10^18) are scaled by
-// 2^-64 first, where eps does not count; their `scale` says so.
+// turned.
 // turn: what is done to the weighted values meanwhile; again(ua, ub): the row once
 // more.  Whole warps call it.
 template <bool kAdjacent, class Turn, class Again>
@@ -305,11 +309,11 @@ MSA_DEV float weigh(uint4 ua, uint4 ub, const Values& w, bool norm, float eps, V
     const bool far = norm && !(sum < kInf);
     again(ua, ub);
     unpack<kAdjacent>(ua, ub, v);
-    times(v, far ? 5.421010862427522e-20f : 1.f);  // 2^-64
+    times(v, far ? kDown : 1.f);
     const float scaled = row_sum(squares(v));
     if (far) {
       sum = scaled;
-      eps = 0.f;
+      eps = 0.f;  // no more than 2^-21 of the mean there
     }
     times(v, w);
     turn(v);

@@ -524,6 +524,8 @@ int msa_cache_fwd(const msa_cache_problem* p, const uint16_t* q, const uint8_t* 
  * token's num_axes positions (one for text; time, height and width of images and
  * video).  Angles are formed in 64-bit fixed point, so that they are as exact at
  * position 2^31 as at 1.  All else is fp32, rounded to bf16 once.
+ * Rows may hold any finite values.  Weights (offset added) times cos_scale may reach
+ * 2^62, and their products with the gradients 2^100: beyond, fp32 may overflow.
  *
  * The tensors of one call share a launch and their tokens' angles.  x and y may
  * be strided (parts of one projection's output), with strides in elements.

@@ -1,0 +1,78 @@
+"""GPU: norm and rotary positions at the ends of what the calls allow (the largest finite rows, inputs and outputs that
+share memory, padding, streams, status words), against the fp64 oracle with the bounds of ``test_gpu_rope``."""
+import numpy as np
+import pytest
+
+from oracle import msa_oracle as O
+from oracle import rope_oracle as R
+from tests._util import to_bf16_tensor
+from tests.test_gpu_cache import _bf16, _dev
+from tests.test_gpu_rope import B, Layer, _append_problem, _check_forward, _check_grad, _expected_cache, _f64  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+MOST = 0x7F7F       # the largest finite bf16
+LIMIT = 2.0 ** 128 - 2.0 ** 120
+
+
+def _large_rows(rng, shape):
+    """bf16 bits of rows (first axis) of every size whose squares leave fp32's range: all of the largest value, two large
+    values among ordinary ones, small values beside one large one; every fifth row is ordinary."""
+    T = shape[0]
+    x = rng.standard_normal(shape)
+    big = np.array([0, 100, 120, 123, 0, 124.5, 125, 126, 60, 64])
+    x *= (2.0 ** big[np.arange(T) % 10])[:, None, None]
+    i = np.arange(T) % 10
+    x[i == 8] *= 2.0 ** -118        # 2^-58, beside one of 2^64
+    x[i == 8, :, 77] = -2.0 ** 64
+    bits = O.f64_to_bf16(np.clip(x, -LIMIT, LIMIT))
+    sign = (rng.integers(0, 2, shape) << 15).astype(np.uint16)
+    bits[i == 7] = (MOST | sign)[i == 7]
+    two = np.flatnonzero(i == 5)
+    bits[two] = O.f64_to_bf16(rng.standard_normal((len(two), *shape[1:])))
+    bits[two, :, 3], bits[two, :, 90] = O.f64_to_bf16(np.float64(2.5e38)), MOST | 0x8000
+    return bits
+
+
+@pytest.mark.parametrize("kw", [dict(H=2), dict(adjacent=True, rotary=64, per_head=True, wide=False, offset=1.0, scale=1.2)])
+def test_largest_rows(B, kw):
+    """The definition's values for rows up to bf16's largest, forward and gradients; the ordinary rows beside them keep
+    their bits."""
+    import torch
+    L = Layer(B, seed=50, **kw)
+    T = 40
+    pos = L.positions(T)
+    x = [_large_rows(L.rng, (T, h, 128)) for h in L.heads]
+    dy = [_bf16(L.rng, (T, h, 128)) for h in L.heads]
+    put = lambda rows: [to_bf16_tensor(b, "cuda") for b in rows]
+    ys = L.rope.forward(_dev(pos), *put(x))
+    dxs, dws = L.rope.backward(_dev(pos), put(dy), put(x))
+    for i in range(4):
+        _check_forward(L, i, x[i], pos, ys[i])
+        _check_grad(L, i, O.bf16_to_f64(x[i]), O.bf16_to_f64(dy[i]), pos, dxs[i], dws[i])
+    plain = np.flatnonzero(np.isin(np.arange(T) % 10, (0, 4)))
+    alone = L.rope.forward(_dev(pos[plain]), *put([b[plain] for b in x]))
+    grads, _ = L.rope.backward(_dev(pos[plain]), put([b[plain] for b in dy]), put([b[plain] for b in x]))
+    at = _dev(plain).long()
+    for a, b in zip((*alone, *grads), (*ys, *dxs)):
+        assert torch.equal(a, b[at])
+
+
+@pytest.mark.parametrize("kw", [dict(H=4), dict(H=3, adjacent=True, per_head=True, rotary=96)])
+def test_codes_of_the_largest_rows(B, kw):
+    """Half a million values: groups that fp32 does not tell are those of the exact value there too."""
+    import torch
+    L = Layer(B, seed=51, **kw)
+    T = 1200
+    pos = L.positions(T, 1 << 17)
+    k, v = _large_rows(L.rng, (T, L.H, 128)), np.zeros((T, L.H, 128), np.uint16)
+    c = B.make_cache_problem(num_requests=1, num_pages=T // 64 + 1, max_blocks=T // 64 + 1, num_q_heads=16 * L.H, topk=1,
+                             token_cap=T, chunk_cap=1)
+    cache, st = B.new_cache(c), torch.zeros(4, dtype=torch.int32, device="cuda")
+    slots = L.rng.permutation(T).astype(np.int64)
+    B.msa_cache_append_rope(c, _append_problem(B, L, T, False, False), None, to_bf16_tensor(k, "cuda"),
+                            to_bf16_tensor(v, "cuda"), None, None, _dev(pos), _dev(slots, torch.int64), None, None,
+                            None, None, cache, None, None, st)
+    want = np.zeros(tuple(cache.shape), np.uint8)
+    _expected_cache(L, want, k, v, pos, slots, 64)
+    assert np.array_equal(cache.cpu().numpy(), want) and int(st[0].item()) == 0
