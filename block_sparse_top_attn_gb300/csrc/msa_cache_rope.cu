@@ -215,8 +215,11 @@ MSA_DEV void exact_group(const AppendRopeArgs& a, const uint4* row, int64_t slot
   }
   const Split turned = product(turned_dim<kAdjacent>(a, row, scale, head, t, dim0 + lane), r);
   Split own = sum_of(turned.hi, turned.lo);
+  // What saturates in any case is cut off: fp32 may not have held it, and then its second part is NaN.
+  constexpr float kMost = 1.8446744073709552e19f;  // 2^64
+  if (!(fabsf(turned.hi) < kMost)) own = Split{copysignf(kMost, turned.hi), 0.f};
   const bool negative = own.hi < 0.f;
-  own = Split{fabsf(own.hi), own.hi < kInf && own.hi > -kInf ? (negative ? -own.lo : own.lo) : 0.f};
+  own = Split{fabsf(own.hi), negative ? -own.lo : own.lo};
   Split m = own;
 #pragma unroll
   for (int o = 1; o < 16; o <<= 1) {

@@ -616,7 +616,8 @@ int msa_norm_rope_bwd(const msa_rope_problem* p, const uint16_t* const* dy, cons
  *  - K normed, rotated and rounded to 4 bits by msa_cache_append's rule, V rounded
  *    as it is, both written to the tokens' slots.  K is not rounded to bf16 in
  *    between: its codes and scales are those of the exact value of y (what lies
- *    closer to a border than fp32 can tell is computed again in pairs of fp32);
+ *    closer to a border than fp32 can tell is computed again in pairs of fp32).  A
+ *    value beyond fp32's range makes its group NaN, as an infinite one does;
  *  - index keys normed, rotated and rounded to bf16 as msa_norm_rope does, and kept
  *    by msa_cache_append's rule (index_tail and index_pool hold the same, bit for
  *    bit, as after the two calls).

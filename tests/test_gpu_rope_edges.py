@@ -76,3 +76,25 @@ def test_codes_of_the_largest_rows(B, kw):
     want = np.zeros(tuple(cache.shape), np.uint8)
     _expected_cache(L, want, k, v, pos, slots, 64)
     assert np.array_equal(cache.cpu().numpy(), want) and int(st[0].item()) == 0
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(adjacent=True, rotary=64, H=2)])
+@pytest.mark.parametrize("exp", [-32, -9])
+def test_codes_beyond_fp32(B, kw, exp):
+    """Rows without a norm whose values, in units of 2^exp, leave fp32's range: their groups saturate."""
+    import torch
+    L = Layer(B, seed=52, norm=False, **kw)
+    T = 60
+    pos = L.positions(T)
+    size = 2.0 ** np.array([0, 60, 90, 96, 100, 117, 119, 120, 122, 124])[np.arange(T) % 10]
+    k, v = _bf16(L.rng, (T, L.H, 128), size[:, None, None]), np.zeros((T, L.H, 128), np.uint16)
+    c = B.make_cache_problem(num_requests=1, num_pages=1, max_blocks=1, num_q_heads=16 * L.H, topk=1, token_cap=T,
+                             chunk_cap=1, k_exp=exp)
+    cache, st = B.new_cache(c), torch.zeros(4, dtype=torch.int32, device="cuda")
+    slots = L.rng.permutation(T)
+    B.msa_cache_append_rope(c, _append_problem(B, L, T, False, False), None, to_bf16_tensor(k, "cuda"),
+                            to_bf16_tensor(v, "cuda"), None, None, _dev(pos), _dev(slots, torch.int64), None, None,
+                            None, None, cache, None, None, st)
+    want = np.zeros(tuple(cache.shape), np.uint8)
+    _expected_cache(L, want, k, v, pos, slots, 64, (exp, 0))
+    assert np.array_equal(cache.cpu().numpy(), want) and int(st[0].item()) == 0
