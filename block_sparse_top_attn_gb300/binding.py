@@ -704,12 +704,15 @@ class Rope:
         self.columns = None if axes is None else self.pairs.num_axes
         self.weights = (q_weight, k_weight, q_index_weight, k_index_weight)
         self.norms = (norm, norm, index_norm, index_norm)
-        for name, w in zip(self.NAMES, self.weights):
-            if w is not None and w.device != self.device:
-                raise ValueError(f"{name}_weight: need a tensor on {self.device}")
+        self._check_weights()
         self._args = dict(adjacent=adjacent, eps=eps, weight_offset=weight_offset, cos_scale=cos_scale)
         self.status = torch.zeros(4, dtype=torch.int32, device=self.device)     # stays 0: the table's axes are in range
         self._problems = {}
+
+    def _check_weights(self):
+        for name, w in zip(self.NAMES, self.weights):
+            if w is not None and w.device != self.device:
+                raise ValueError(f"{name}_weight: need a tensor on {self.device}")
 
     def _rows(self, name, x, tokens, heads=None):
         import torch
@@ -738,13 +741,16 @@ class Rope:
     def _problem(self, tokens, xs, ys, v=None):
         """The description of calls with these tensors' shapes and strides."""
         every = (*xs, v) if v is not None else xs
-        key = (tokens, *map(_addr, self.weights),    # a parameter's storage may be replaced
+        # a parameter's storage may be replaced, by one of another type or shape at the same address
+        key = (tokens, *(None if w is None else (w.data_ptr(), w.dtype, w.shape, w.is_contiguous(), w.get_device())
+                         for w in self.weights),
                *((x.shape[1], *self._strides(x), *(self._strides(y) if y is not None else ()))
                  if x is not None else None for x, y in zip(every, (*ys, None))))
         p = self._problems.get(key)
         if p is None:
             if len(self._problems) >= 64:
                 self._problems.clear()
+            self._check_weights()
             ts = [None if x is None else RopeTensor(x.shape[1], norm, True, w, self._strides(x),
                                                     None if y is None else self._strides(y))
                   for x, y, norm, w in zip(xs, ys, self.norms, self.weights)]

@@ -98,3 +98,23 @@ def test_codes_beyond_fp32(B, kw, exp):
     want = np.zeros(tuple(cache.shape), np.uint8)
     _expected_cache(L, want, k, v, pos, slots, 64, (exp, 0))
     assert np.array_equal(cache.cpu().numpy(), want) and int(st[0].item()) == 0
+
+
+def test_weight_of_another_type_at_the_same_address(B):
+    """A weight whose data becomes bf16, one per head and fp32 again in the same memory: calls read, and write gradients,
+    by what it is now."""
+    import torch
+    L = Layer(B, seed=53)
+    T = 9
+    pos = L.positions(T)
+    x, dy = _bf16(L.rng, (T, 16, 128)), _bf16(L.rng, (T, 16, 128))
+    buf = torch.zeros(16 * 128 * 4, dtype=torch.uint8, device="cuda")
+    w = L.dev[0]
+    for dtype, shape in ((torch.float32, (128,)), (torch.bfloat16, (128,)), (torch.float32, (16, 128)),
+                         (torch.bfloat16, (16, 128)), (torch.float32, (128,))):
+        w.data = buf.view(dtype)[:int(np.prod(shape))].view(shape)
+        w.copy_(torch.from_numpy(L.rng.standard_normal(shape)))
+        L.w[0] = _f64(w)
+        _check_forward(L, 0, x, pos, L.rope.forward(_dev(pos), to_bf16_tensor(x, "cuda"))[0])
+        (dx,), (dw,) = L.rope.backward(_dev(pos), [to_bf16_tensor(dy, "cuda")], [to_bf16_tensor(x, "cuda")])
+        _check_grad(L, 0, O.bf16_to_f64(x), O.bf16_to_f64(dy), pos, dx, dw)

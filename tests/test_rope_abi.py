@@ -315,3 +315,32 @@ def test_rope_keeps_one_description_per_shape(B):
     for n in range(5, 200):
         rope._problem(n, (q, k, None, None), (q, k, None, None))
     assert len(rope._problems) <= 64
+
+
+def test_descriptions_follow_a_weights_type(B):
+    """A weight whose data is replaced by another type, shape or layout at the same address gets a description of its
+    own, with its checks."""
+    import torch
+    buf = torch.zeros(4096, dtype=torch.uint8)
+    w = torch.nn.Parameter(buf.view(torch.float32)[:256].view(2, 128), requires_grad=False)
+    rope = B.Rope(B.rope_frequencies(64), k_weight=w, device="cpu")
+    x = torch.zeros((4, 2, 128), dtype=torch.bfloat16)
+    flags = lambda: rope._problem(4, (None, x, None, None), (None, x, None, None)).tensor[1].flags
+    fp32, per_head = B.MSA_ROPE_WEIGHT_FP32, B.MSA_ROPE_PER_HEAD
+    base = B.MSA_ROPE_NORM | B.MSA_ROPE_ROTATE
+    assert flags() == base | fp32 | per_head
+    w.data = buf.view(torch.bfloat16)[:256].view(2, 128)
+    assert flags() == base | per_head
+    w.data = buf.view(torch.bfloat16)[:128]
+    assert flags() == base
+    w.data = buf.view(torch.float32)[:128]
+    assert flags() == base | fp32
+    assert {p.tensor[1].weight for p in rope._problems.values()} == {buf.data_ptr()}
+    for bad in (buf.view(torch.float32)[:256:2], buf.view(torch.float16)[:128], buf.view(torch.float32)[:64]):
+        w.data = bad
+        with pytest.raises(ValueError, match="weight"):
+            flags()
+    w.data = torch.zeros(128)
+    rope.device = torch.device("cuda", 0)       # as a weight that was moved away looks
+    with pytest.raises(ValueError, match="k_weight"):
+        flags()
