@@ -675,6 +675,28 @@ def msa_cache_append_rope(c, p, q, k, v, q_index, k_index, positions, slot_map, 
            "msa_cache_append_rope")
 
 
+class _Extent:
+    """A tensor's addresses as NumPy sees them; nothing is read."""
+
+    def __init__(self, x):
+        size = x.element_size()
+        self.__array_interface__ = dict(data=(x.data_ptr(), True), shape=tuple(x.shape), typestr=f"|V{size}",
+                                        strides=tuple(s * size for s in x.stride()), version=3)
+
+
+def _share_memory(a, b) -> bool:
+    """Whether two bf16 [tokens, heads, 128] tensors have elements in common, whatever their strides."""
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+    strides = a.stride()
+    if strides == b.stride() and strides[0] > 0:    # beside one another in the same rows, as a rule
+        at = (b.data_ptr() - a.data_ptr()) // a.element_size() % strides[0]
+        width = lambda x: (x.shape[1] - 1) * strides[1] + HEAD_DIM
+        if strides[1] > 0 and at >= width(a) and at + width(b) <= strides[0]:
+            return False
+    return np.shares_memory(np.asarray(_Extent(a)), np.asarray(_Extent(b)))
+
+
 class Rope:
     """Norm and rotary positions of one attention layer: the norms' weights, the frequencies, and the calls that apply
     them in training (forward, backward) and in serving (Cache.append_rope).
@@ -766,12 +788,15 @@ class Rope:
 
     @staticmethod
     def _like(xs):
-        """New tensors with the shapes and strides of xs; views of one buffer where they are views of one tensor."""
+        """New tensors with the shapes and strides of xs; views of one buffer where they are views of one tensor (and no
+        two of the same elements)."""
         import torch
         made, groups = [None] * len(xs), {}
         for i, x in enumerate(xs):
             if x is not None:
-                groups.setdefault((x.untyped_storage().data_ptr(), x.stride()), []).append(i)
+                key = (x.untyped_storage().data_ptr(), x.stride())
+                shared = any(_share_memory(x, xs[j]) for j in groups.get(key, ()))
+                groups.setdefault(i if shared else key, []).append(i)
         for members in groups.values():
             ends = [xs[i].storage_offset() + sum((n - 1) * s for n, s in zip(xs[i].shape, xs[i].stride())) + 1
                     for i in members]

@@ -118,3 +118,18 @@ def test_weight_of_another_type_at_the_same_address(B):
         _check_forward(L, 0, x, pos, L.rope.forward(_dev(pos), to_bf16_tensor(x, "cuda"))[0])
         (dx,), (dw,) = L.rope.backward(_dev(pos), [to_bf16_tensor(dy, "cuda")], [to_bf16_tensor(x, "cuda")])
         _check_grad(L, 0, O.bf16_to_f64(x), O.bf16_to_f64(dy), pos, dx, dw)
+
+
+def test_gradients_of_inputs_with_common_elements(B):
+    """One tensor as two inputs, and inputs that are parts of others: the bits of contiguous copies."""
+    import torch
+    L = Layer(B, seed=54, H=2, rotary=64)
+    T = 300
+    pos = _dev(L.positions(T))
+    rows = to_bf16_tensor(_bf16(L.rng, (T, 34, 128)), "cuda")
+    q, k = rows[:, :32], rows[:, 32:]
+    dys = [to_bf16_tensor(_bf16(L.rng, (T, h, 128)), "cuda") for h in L.heads]
+    for xs in ((q, k, k, k), (q, k, q[:, 4:6], q[:, 5:7]), (q, q[:, :2], k, q[:, 30:])):
+        want = L.rope.backward(pos, dys, [x.contiguous() for x in xs])
+        got = L.rope.backward(pos, dys, xs)
+        assert all(torch.equal(a, b) for a, b in zip((*got[0], *got[1]), (*want[0], *want[1])))

@@ -344,3 +344,26 @@ def test_descriptions_follow_a_weights_type(B):
     rope.device = torch.device("cuda", 0)       # as a weight that was moved away looks
     with pytest.raises(ValueError, match="k_weight"):
         flags()
+
+
+def test_new_gradients_share_no_memory(B):
+    """New tensors laid out as the inputs are: views of one buffer for views of one projection's output, tensors of their
+    own where two inputs have elements in common."""
+    import torch
+    rows = torch.zeros((5, 12, 128), dtype=torch.bfloat16)
+    place = lambda xs: [None if x is None else (x.data_ptr() - xs[0].data_ptr(), x.shape, x.stride()) for x in xs]
+    for xs in ((rows[:, :6], rows[:, 6:8], rows[:, 9:11], rows[:, 11:]), (rows[:, 0::2], rows[:, 1::2]),
+               (rows[:, 0:7:3], rows[:, 1:8:3], rows[:, 2:9:3])):
+        made = B.Rope._like(xs)
+        assert place(made) == place(xs) and len({x.untyped_storage().data_ptr() for x in made}) == 1
+    q, k = rows[:, :8], rows[:, 8:9]
+    for xs in ((q, k, q[:, :1], k), (None, k, None, k), (q, k, q, k), (q, rows[:, 7:9], rows[:, 8:10], rows[:, 9:11]),
+               (q[:1], q[:1], k[:1], q[:1]), (rows[:4], rows[1:], None, rows[:4])):
+        made = B.Rope._like(xs)
+        for i, (x, d) in enumerate(zip(xs, made)):
+            assert (x is None) == (d is None)
+            if x is None:
+                continue
+            assert d.shape == x.shape and d.stride() == x.stride() and d.dtype == x.dtype
+            d.fill_(i + 1)
+        assert all(d is None or bool((d == i + 1).all()) for i, d in enumerate(made))
