@@ -636,6 +636,7 @@ def make_rope_problem(tokens, pairs, q=None, k=None, q_index=None, k_index=None,
         if t is not None:
             s.tensor[i] = msa_rope_tensor(t.heads, t.flags, _addr(t.weight), *t.x_strides, *t.y_strides)
     s._keep = (pairs, q, k, q_index, k_index, v)
+    s._apart = set()    # addresses of tensors that were found apart (Rope)
     return s
 
 
@@ -806,6 +807,24 @@ class Rope:
                 made[i] = buf.as_strided(xs[i].shape, xs[i].stride(), xs[i].storage_offset() - base)
         return tuple(made)
 
+    def _check_apart(self, p, outs, *inputs):
+        """Refuses outputs that have elements in common with one another or with an input; an output may be an input of
+        its own role itself.  outs, inputs: tuples of the roles' tensors (what lies behind NAMES has no output)."""
+        key = tuple(_addr(x) for xs in (outs, *inputs) for x in xs)
+        if key in p._apart:     # seen before with these shapes and strides
+            return
+        place = lambda x: (x.data_ptr(), self._strides(x))
+        for i, y in enumerate(outs):
+            if y is None:
+                continue
+            others = [*outs[i + 1:], *(x for xs in inputs for j, x in enumerate(xs)
+                                       if x is not None and (j != i or place(x) != place(y)))]
+            if any(x is not None and _share_memory(x, y) for x in others):
+                raise ValueError(f"out of {self.NAMES[i]}: has elements in common with another tensor of the call")
+        if len(p._apart) >= 64:
+            p._apart.clear()
+        p._apart.add(key)
+
     def _outputs(self, name, out, xs, tokens):
         import torch
         if out is None:
@@ -823,22 +842,25 @@ class Rope:
 
     def forward(self, positions, q=None, k=None, q_index=None, k_index=None, out=None, status=None, stream=None):
         """msa_norm_rope of the tensors that are given: a tuple of their results, in that order.  out: tensors to
-        write to (the inputs themselves will do).  Rows of padding (a negative first position) are left as they were."""
+        write to, each its input itself or apart from all others.  Rows of padding (a negative first position) are left as they were."""
         import torch
         T = self._positions(positions)
         xs = self._given(T, q=q, k=k, q_index=q_index, k_index=k_index)
         with torch.cuda.device(self.device), torch.cuda.stream(stream):
             ys = self._outputs("out", out, xs, T)
             if T:
-                msa_norm_rope(self._problem(T, xs, ys), xs, positions, ys, self.status if status is None else status)
+                p = self._problem(T, xs, ys)
+                if out is not None:
+                    self._check_apart(p, ys, xs)
+                msa_norm_rope(p, xs, positions, ys, self.status if status is None else status)
         return tuple(y for y in ys if y is not None)
 
     def backward(self, positions, grads, inputs, out=None, status=None, stream=None):
         """msa_norm_rope_bwd: grads and inputs (what forward was given) are q, k, q_index, k_index in order, as many as
         there are (None: no such tensor).  Returns (gradients of the inputs, gradients of the weights), each a tuple like
         `inputs`; a weight's is None where there is none.  out: tensors for the inputs' gradients, with the inputs'
-        strides (views of the projection's gradient, where the inputs are views of its output); new ones are laid out
-        as the inputs are."""
+        strides (views of the projection's gradient, where the inputs are views of its output), each its own input or
+        gradient itself or apart from all others; new ones are laid out as the inputs are."""
         import torch
         T = self._positions(positions)
         n = len(inputs)
@@ -861,6 +883,8 @@ class Rope:
             dws = tuple(None if x is None or w is None else torch.empty_like(w) for x, w in zip(xs, self.weights))
             if T:
                 p = self._problem(T, xs, dys)
+                if out is not None:
+                    self._check_apart(p, dxs, xs, dys)
                 ws = torch.empty(msa_norm_rope_bwd_bytes(p), dtype=torch.uint8, device=self.device)
                 msa_norm_rope_bwd(p, dys, xs, positions, dxs, dws, self.status if status is None else status, ws)
             else:
@@ -983,7 +1007,8 @@ class Cache:
     def append_rope(self, rope, q, k, v, q_index=None, k_index=None, positions=None, out=None, stream=None):
         """msa_cache_append_rope: the step's q, k, v and index vectors as the projections give them (bf16
         [tokens, heads, 128], views will do), normed and rotated by `rope` (a Rope) on their way.  Returns (q, q_index)
-        for forward and select, new tensors or those given as `out` (q_index None where there is none).  positions:
+        for forward and select, new tensors or those given as `out` (q_index None where there is none; each its input
+        itself or apart from the others).  positions:
         the step's own, or int32 [tokens, axes] where rope has several axes."""
         import torch
         t = self._step_tables()
@@ -1006,6 +1031,8 @@ class Cache:
         with torch.cuda.device(self.device), torch.cuda.stream(stream):
             yq, _, yi, _ = rope._outputs("out", out, (q, None, q_index, None), T)
             p = rope._problem(T, (q, k, q_index, k_index), (yq, None, yi, None), v)
+            if out is not None:
+                rope._check_apart(p, (yq, None, yi, None), (q, k, q_index, k_index, v))
             msa_cache_append_rope(c, p, q, k, v, q_index, k_index, positions, self.slot_map, self.cu_tokens,
                                   self.chunks, yq, yi, self.cache, self.index_tail, self.index_pool, self.status)
         return yq, yi

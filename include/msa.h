@@ -583,7 +583,9 @@ int msa_rope_pairs(const double* inv_freq, const int32_t* axes, int32_t num_pair
 /* The forward.
  * x, y       host arrays of four device pointers (MSA_ROPE_Q .. MSA_ROPE_K_INDEX; p's
  *            V tensor is not used): bf16 rows in and out.  Entries of tensors with
- *            no heads are not looked at.  y may be x itself, with the same strides.
+ *            no heads are not looked at.  y may be x itself, with the same strides;
+ *            what is written shares no memory with other tensors of a call, here
+ *            and below, but where it is said.
  * positions  device int32 [tokens, num_axes].  A token whose first position is
  *            negative is padding: its rows of y are left as they were.  Other
  *            columns may be negative.

@@ -367,3 +367,58 @@ def test_new_gradients_share_no_memory(B):
             assert d.shape == x.shape and d.stride() == x.stride() and d.dtype == x.dtype
             d.fill_(i + 1)
         assert all(d is None or bool((d == i + 1).all()) for i, d in enumerate(made))
+
+
+def test_outputs_that_share_memory_are_refused(B, monkeypatch):
+    """Outputs that have elements in common with one another or with an input that is not theirs."""
+    import contextlib
+
+    import torch
+    for name in ("device", "stream"):
+        monkeypatch.setattr(torch.cuda, name, lambda *a: contextlib.nullcontext())
+    calls = []
+    for name in ("msa_norm_rope", "msa_norm_rope_bwd", "msa_cache_append_rope"):
+        monkeypatch.setattr(B, name, lambda *a, name=name: calls.append(name))
+    rope = B.Rope(B.rope_frequencies(64), device="cpu")
+    T = 3
+    pos = torch.zeros(T, dtype=torch.int32)
+    new = lambda h: torch.zeros((T, h, 128), dtype=torch.bfloat16)
+    rows = new(24)
+    q, k, qi, ki = rows[:, :16], rows[:, 16:18], rows[:, 18:20], rows[:, 20:22]
+    free = rows[:, 22:]
+    for xs, out in (((q, k), (q, k)), ((q, k), (q, free)), ((q, k), (new(16), k)), ((q, k, k), (q, free, new(2))),
+                    ((q, k, qi, ki), (q, k, qi, ki)), ((new(16), k), (q, free))):
+        rope.forward(pos, *xs, out=out)
+        rope.backward(pos, [new(x.shape[1]) for x in xs], [x.contiguous() for x in xs],
+                      out=[new(x.shape[1]) for x in xs])
+        assert calls == ["msa_norm_rope", "msa_norm_rope_bwd"], (xs, out)
+        calls.clear()
+    bad = (((q, k), (q, q[:, :2])), ((q, k), (new(16), q[:, 3:5])), ((q, k), (rows[:, 1:17], new(2))),
+           ((q, k, qi, ki), (q, k, ki, qi)), ((q, k, k), (q, k, free)), ((q, k, q[:, :2]), (q, new(2), new(2))),
+           ((q, k, qi), (new(16), free, free)), ((q, k, qi), (new(16), rows[:, 17:19], new(2))))
+    for xs, out in bad:
+        for _ in range(2):
+            with pytest.raises(ValueError, match="out of .*: has elements in common"):
+                rope.forward(pos, *xs, out=out)
+            with pytest.raises(ValueError, match="out of .*: has elements in common|strides"):
+                rope.backward(pos, [new(x.shape[1]) for x in xs], xs, out=out)
+    # gradients over their inputs or incoming gradients, but not over another's
+    x, g = (new(16), new(2)), (new(16), new(2))
+    for out in (x, g, (x[0], g[1]), (g[0], new(2))):
+        rope.backward(pos, g, x, out=out)
+    with pytest.raises(ValueError, match="out of k: has elements in common"):
+        rope.backward(pos, (new(16), g[1], new(2)), (new(16), new(2), x[1]), out=(new(16), x[1], new(2)))
+    # the cache's append
+    kv = B.Cache(num_requests=1, num_pages=4, max_blocks=2, num_q_heads=32, topk=2, max_tokens=T, device="cpu")
+    kv._now = t = kv._tables(T)
+    kv.slot_map, kv.positions, kv.chunks = t["slot_map"], t["positions"], t["chunks"]
+    wide = new(40)
+    q, k, v, qi, ki = wide[:, :32], wide[:, 32:34], wide[:, 34:36], wide[:, 36:38], wide[:, 38:]
+    calls.clear()
+    for out in ((q, qi), (new(32), qi), (q, new(2))):
+        kv.append_rope(rope, q, k, v, qi, ki, out=out)
+    assert len(calls) == 3
+    for out in ((q, k), (q, v), (q, ki), (wide[:, 2:34], new(2)), (q, q[:, :2])):
+        with pytest.raises(ValueError, match="out of .*: has elements in common"):
+            kv.append_rope(rope, q, k, v, qi, ki, out=out)
+    assert len(calls) == 3
