@@ -711,7 +711,7 @@ class Rope:
     norm        False: rotation only.  index_norm: the same for q_index and k_index.
     *_weight    bf16 or fp32, [128] for all heads or [heads, 128]; None: a norm without weights.
     The tensors are bf16 [tokens, heads, 128] whose last dim is contiguous (views of one projection's output will do).
-    Outputs are new tensors of the call's stream, or those given as `out`.  Nothing synchronises; calls keep no state
+    Outputs are new tensors of the call's stream, or those given as `out`.  No call synchronises; calls keep no state
     but the problem descriptions, so that one object may serve several streams and captured graphs.  status: the
     status word of the calls around it (int32, device), whose errors then stop these too.
     """
@@ -729,7 +729,9 @@ class Rope:
         self.norms = (norm, norm, index_norm, index_norm)
         self._check_weights()
         self._args = dict(adjacent=adjacent, eps=eps, weight_offset=weight_offset, cos_scale=cos_scale)
-        self.status = torch.zeros(4, dtype=torch.int32, device=self.device)     # stays 0: the table's axes are in range
+        # Stays 0: the table's axes are in range.  Copied from the host like the table, so that both are there when the
+        # constructor returns, whatever stream calls first.
+        self.status = torch.zeros(4, dtype=torch.int32).to(self.device)
         self._problems = {}
 
     def _check_weights(self):

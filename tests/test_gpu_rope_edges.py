@@ -133,3 +133,28 @@ def test_gradients_of_inputs_with_common_elements(B):
         want = L.rope.backward(pos, dys, [x.contiguous() for x in xs])
         got = L.rope.backward(pos, dys, xs)
         assert all(torch.equal(a, b) for a, b in zip((*got[0], *got[1]), (*want[0], *want[1])))
+
+
+def test_first_call_on_another_stream(B, monkeypatch):
+    """What the constructor makes is there for every stream, whatever its own has still to do."""
+    import torch
+    x = _bf16(np.random.default_rng(55), (30, 16, 128))
+    dev, pos, side = to_bf16_tensor(x, "cuda"), _dev(np.zeros(30)), torch.cuda.Stream()
+    B.Rope(B.rope_frequencies(128), norm=False).forward(pos, dev * 0, stream=side)     # a kernel's first launch may wait
+    busy = torch.zeros(1 << 28, device="cuda")
+    left = [torch.full((4,), 5, dtype=torch.int32, device="cuda") for _ in range(64)]
+    torch.cuda.synchronize()
+    del left
+    pairs = B.rope_pairs
+
+    def pairs_and_work(*args):
+        table = pairs(*args)
+        for _ in range(60):
+            busy.add_(1.0)
+        return table
+
+    monkeypatch.setattr(B, "rope_pairs", pairs_and_work)
+    rope = B.Rope(B.rope_frequencies(128), norm=False)
+    y, = rope.forward(pos, dev, stream=side)
+    side.synchronize()
+    assert torch.equal(y, dev) and not torch.any(rope.status)      # position 0 turns nothing
