@@ -85,7 +85,8 @@ class msa_rope_pair(ctypes.Structure):
 class msa_rope_problem(ctypes.Structure):
     _fields_ = [(name, ctypes.c_int32) for name in ("tokens", "head_dim", "rotary_dim", "num_axes", "adjacent")] + \
                [(name, ctypes.c_float) for name in ("eps", "weight_offset", "cos_scale")] + \
-               [("pairs", ctypes.c_void_p), ("tensor", msa_rope_tensor * MSA_ROPE_TENSORS)]
+               [("pairs", ctypes.c_void_p), ("tensor", msa_rope_tensor * MSA_ROPE_TENSORS),
+                ("zero_padding", ctypes.c_int32)]
 
 
 def _load():
@@ -622,15 +623,16 @@ class RopeTensor:
 
 
 def make_rope_problem(tokens, pairs, q=None, k=None, q_index=None, k_index=None, v=None, adjacent=False, eps=1e-6,
-                      weight_offset=0.0, cos_scale=1.0, num_axes=None) -> msa_rope_problem:
+                      weight_offset=0.0, cos_scale=1.0, num_axes=None, zero_padding=False) -> msa_rope_problem:
     """The C description of a norm and rotary call: RopePairs (None: nothing is rotated) and RopeTensors (None: the call
     has no such tensor; v is for msa_cache_append_rope).  It keeps the pairs and weights alive.  num_axes: the
-    positions' columns, where they are more than the pairs use."""
+    positions' columns, where they are more than the pairs use.  zero_padding: output rows of padding are zeros."""
     s = msa_rope_problem()
     s.tokens, s.head_dim, s.adjacent = int(tokens), HEAD_DIM, int(bool(adjacent))
     s.rotary_dim = pairs.rotary_dim if pairs is not None else 0
     s.num_axes = int(num_axes or (pairs.num_axes if pairs is not None else 1))
     s.eps, s.weight_offset, s.cos_scale = float(eps), float(weight_offset), float(cos_scale)
+    s.zero_padding = int(bool(zero_padding))
     s.pairs = pairs.table.data_ptr() if pairs is not None else None
     for i, t in enumerate((q, k, q_index, k_index, v)):
         if t is not None:
@@ -763,11 +765,11 @@ class Rope:
         T, H, _ = x.shape
         return (x.stride(0) if T > 1 else H * HEAD_DIM, x.stride(1) if H > 1 else HEAD_DIM)
 
-    def _problem(self, tokens, xs, ys, v=None):
-        """The description of calls with these tensors' shapes and strides."""
+    def _problem(self, tokens, xs, ys, v=None, zero=False):
+        """The description of calls with these tensors' shapes and strides.  zero: rows of padding are zeros."""
         every = (*xs, v) if v is not None else xs
         # a parameter's storage may be replaced, by one of another type or shape at the same address
-        key = (tokens, *(None if w is None else (w.data_ptr(), w.dtype, w.shape, w.is_contiguous(), w.get_device())
+        key = (tokens, zero, *(None if w is None else (w.data_ptr(), w.dtype, w.shape, w.is_contiguous(), w.get_device())
                          for w in self.weights),
                *((x.shape[1], *self._strides(x), *(self._strides(y) if y is not None else ()))
                  if x is not None else None for x, y in zip(every, (*ys, None))))
@@ -780,7 +782,7 @@ class Rope:
                                                     None if y is None else self._strides(y))
                   for x, y, norm, w in zip(xs, ys, self.norms, self.weights)]
             tv = None if v is None else RopeTensor(v.shape[1], False, False, None, self._strides(v))
-            p = self._problems[key] = make_rope_problem(tokens, self.pairs, *ts, tv, **self._args)
+            p = self._problems[key] = make_rope_problem(tokens, self.pairs, *ts, tv, zero_padding=zero, **self._args)
         return p
 
     def _given(self, tokens, **named):
@@ -844,14 +846,15 @@ class Rope:
 
     def forward(self, positions, q=None, k=None, q_index=None, k_index=None, out=None, status=None, stream=None):
         """msa_norm_rope of the tensors that are given: a tuple of their results, in that order.  out: tensors to
-        write to, each its input itself or apart from all others.  Rows of padding (a negative first position) are left as they were."""
+        write to, each its input itself or apart from all others.  Rows of padding (a negative first position) are zeros
+        in new tensors, and left as they were in `out`."""
         import torch
         T = self._positions(positions)
         xs = self._given(T, q=q, k=k, q_index=q_index, k_index=k_index)
         with torch.cuda.device(self.device), torch.cuda.stream(stream):
             ys = self._outputs("out", out, xs, T)
             if T:
-                p = self._problem(T, xs, ys)
+                p = self._problem(T, xs, ys, zero=out is None)
                 if out is not None:
                     self._check_apart(p, ys, xs)
                 msa_norm_rope(p, xs, positions, ys, self.status if status is None else status)
@@ -862,7 +865,8 @@ class Rope:
         there are (None: no such tensor).  Returns (gradients of the inputs, gradients of the weights), each a tuple like
         `inputs`; a weight's is None where there is none.  out: tensors for the inputs' gradients, with the inputs'
         strides (views of the projection's gradient, where the inputs are views of its output), each its own input or
-        gradient itself or apart from all others; new ones are laid out as the inputs are."""
+        gradient itself or apart from all others; new ones are laid out as the inputs are.  Rows of padding as in
+        forward: the gradients of what was padded are zeros in new tensors."""
         import torch
         T = self._positions(positions)
         n = len(inputs)
@@ -884,7 +888,7 @@ class Rope:
                         raise ValueError(f"out of {name}: need the input's strides")
             dws = tuple(None if x is None or w is None else torch.empty_like(w) for x, w in zip(xs, self.weights))
             if T:
-                p = self._problem(T, xs, dys)
+                p = self._problem(T, xs, dys, zero=out is None)
                 if out is not None:
                     self._check_apart(p, dxs, xs, dys)
                 ws = torch.empty(msa_norm_rope_bwd_bytes(p), dtype=torch.uint8, device=self.device)
@@ -1010,7 +1014,7 @@ class Cache:
         """msa_cache_append_rope: the step's q, k, v and index vectors as the projections give them (bf16
         [tokens, heads, 128], views will do), normed and rotated by `rope` (a Rope) on their way.  Returns (q, q_index)
         for forward and select, new tensors or those given as `out` (q_index None where there is none; each its input
-        itself or apart from the others).  positions:
+        itself or apart from the others); rows of padding are zeros in new ones, left as they were in `out`.  positions:
         the step's own, or int32 [tokens, axes] where rope has several axes."""
         import torch
         t = self._step_tables()
@@ -1032,7 +1036,7 @@ class Cache:
             raise ValueError("k_index: this cache keeps no index keys")
         with torch.cuda.device(self.device), torch.cuda.stream(stream):
             yq, _, yi, _ = rope._outputs("out", out, (q, None, q_index, None), T)
-            p = rope._problem(T, (q, k, q_index, k_index), (yq, None, yi, None), v)
+            p = rope._problem(T, (q, k, q_index, k_index), (yq, None, yi, None), v, out is None)
             if out is not None:
                 rope._check_apart(p, (yq, None, yi, None), (q, k, q_index, k_index, v))
             msa_cache_append_rope(c, p, q, k, v, q_index, k_index, positions, self.slot_map, self.cu_tokens,

@@ -718,6 +718,7 @@ extern "C" int msa_cache_append_rope(const msa_cache_problem* c, const msa_rope_
   a.q.eps = p->eps;
   a.q.offset = p->weight_offset;
   a.q.T = a.T;
+  a.q.zero = p->zero_padding;
   a.q.heads = nq + ni;
   a.q.status = a.status = d_status;
   a.k = tensor(MSA_ROPE_K, k, 0);

@@ -23,6 +23,7 @@ int check_problem(const msa_rope_problem* p) {
   if (p->head_dim != kHeadDim || p->tokens > cache::kMaxCount) return MSA_ERR_UNSUPPORTED_SHAPE;
   if (p->rotary_dim < 0 || p->rotary_dim > 128 || p->rotary_dim % 32) return MSA_ERR_UNSUPPORTED_SHAPE;
   if (p->num_axes < 1 || p->num_axes > 4) return MSA_ERR_UNSUPPORTED_SHAPE;
+  if (p->zero_padding < 0 || p->zero_padding > 1) return MSA_ERR_INVALID_ARGUMENT;
   constexpr float kMost = 1.2676506002282294e30f;  // 2^100
   if (!(p->eps >= 1.f / kMost && p->eps <= kMost) || !isfinite(p->weight_offset)) return MSA_ERR_INVALID_ARGUMENT;
   if (!(p->cos_scale > 0.f && p->cos_scale < kInf)) return MSA_ERR_INVALID_ARGUMENT;
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradCtas) norm_rope_bwd_kernel(
   const int apart = a.cut.slices, n = (a.T - slice + apart - 1) / apart;
   const int row_threads = 32 * a.cut.units * a.cut.phases;
   if (tid >= row_threads) {
-    if (!fill_tables<kAdjacent>(a.an, s.tab, bad, row_threads, slice, n, apart)) return;
+    if (!fill_tables<kAdjacent>(a.an, s.tab, bad, row_threads, slice, n, apart, [](int64_t) {})) return;
   } else if (!grad_rows<kAdjacent>(a, s, bad, slice, group, n, apart)) {
     return;
   }
@@ -264,6 +265,11 @@ __global__ void __launch_bounds__(kGradThreads, kGradCtas) norm_rope_bwd_kernel(
 }
 
 struct SumArgs {
+  Tensor t[kTensors];  // of the gradients' rows, for the zeros of padding
+  uint16_t* dx[kTensors];
+  const int32_t* positions;
+  int A, T, heads;
+  unsigned sums;  // CTAs that add; those behind them write zeros
   const float* partial;
   void* dw[kTensors];
   int wide[kTensors];  // fp32
@@ -273,13 +279,34 @@ struct SumArgs {
   int32_t* status;
 };
 
+constexpr int kSumParts = 16;
+// Zeros to the padding among the CTA's tokens, a warp 32 of them.  Here, where the loads
+// of the weights' sums leave time: in norm_rope_bwd_kernel, by the warps of the rows or by
+// those of the angles, the registers' different use made 32k tokens x 68 heads 281 us
+// of 261.
+MSA_DEV void zero_tokens(const SumArgs& a, int cta) {
+  const int lane = threadIdx.x & 31, t0 = cta * 32 * kSumParts + (threadIdx.x & ~31);
+  const bool padding = t0 + lane < a.T && a.positions[(int64_t)(t0 + lane) * a.A] < 0;
+  for (unsigned left = __ballot_sync(0xffffffffu, padding); left; left &= left - 1) {
+    const int64_t t = t0 + __ffs(left) - 1;
+    zero_heads(0, a.heads, lane, 32, [&](int hh) {
+      int head;
+      const int k = tensor_of(a, hh, head);
+      return a.dx[k] + t * a.t[k].x_token + head * a.t[k].x_head;
+    });
+  }
+}
+
 // A CTA adds up 32 dims of one row of weights: a warp every 16th slice, sixteen loads
 // in flight.
-constexpr int kSumParts = 16;
 __global__ void __launch_bounds__(32 * kSumParts) weight_sum_kernel(SumArgs a) {
   __shared__ float s_part[kSumParts][32];
   cache::after_previous_kernel();
   const bool bad = status_bad(a.status);  // decided on below: the load does not hold up the others
+  if (blockIdx.x >= a.sums) {
+    if (!__syncthreads_or(bad)) zero_tokens(a, (int)(blockIdx.x - a.sums));
+    return;
+  }
   const int all = blockIdx.x >> 2;  // row of all tensors' weights
   int row = all, slot = a.slot[0], per = a.per[0], wide = a.wide[0];
   void* dw = a.dw[0];
@@ -404,6 +431,7 @@ int msa_norm_rope(const msa_rope_problem* p, const uint16_t* const* x, const int
   a.eps = p->eps;
   a.offset = p->weight_offset;
   a.T = p->tokens;
+  a.zero = p->zero_padding;
   int32_t sms = 0;
   if ((rc = sm_count_current(&sms))) return rc;
   a.cut = rope::cut_rows(a.heads, a.T, sms, rope::kRowCtas * (rope::kRowWarps + 1),
@@ -476,8 +504,21 @@ int msa_norm_rope_bwd(const msa_rope_problem* p, const uint16_t* const* dy, cons
                               stream, 1, a);
     if (rc) return rc;
   }
-  if (rows == 0) return MSA_OK;
-  return cache::launch_kernel(rope::weight_sum_kernel, dim3((unsigned)rows * 4), 32 * rope::kSumParts, 0, stream, 1, s);
+  s.sums = (unsigned)rows * 4;
+  unsigned zeros = 0;
+  if (p->zero_padding && p->tokens) {
+    for (int i = 0; i < rope::kTensors; ++i) {
+      s.t[i] = a.t[i];
+      s.dx[i] = a.dx[i];
+    }
+    s.heads = g.heads;
+    s.positions = positions;
+    s.A = p->num_axes;
+    s.T = p->tokens;
+    zeros = ((unsigned)p->tokens + 32 * rope::kSumParts - 1) / (32 * rope::kSumParts);
+  }
+  if (s.sums + zeros == 0) return MSA_OK;
+  return cache::launch_kernel(rope::weight_sum_kernel, dim3(s.sums + zeros), 32 * rope::kSumParts, 0, stream, 1, s);
 }
 
 }  // extern "C"

@@ -374,6 +374,7 @@ struct RowsArgs {
   Angles an;
   float eps, offset;
   int T, heads;  // of all tensors
+  int zero;      // rows of padding are zeros
   Cut cut;
   int32_t* status;
 };
@@ -418,9 +419,10 @@ MSA_DEV void copy_row(Stage& s, const uint16_t* row, int lane) {
 // one while the others use the other.
 // (Filled by all warps, each its part, between a barrier and the next: 32k tokens x
 // 68 heads 190 us, with registers that spill, against 180.)
-template <bool kAdjacent>
+// padding(token): what they do about a token that is padding.
+template <bool kAdjacent, class Padding>
 MSA_DEV bool fill_tables(const Angles& a, Table<kTile> (&tab)[2], bool bad, int before, int64_t first, int n,
-                         int apart) {
+                         int apart, Padding padding) {
   const Filler<kAdjacent> filler(a, threadIdx.x - before, blockDim.x - before);
   auto fill = [&](int k) {
     if (k * kTile < n)
@@ -430,9 +432,18 @@ MSA_DEV bool fill_tables(const Angles& a, Table<kTile> (&tab)[2], bool bad, int 
   if (__syncthreads_or(bad)) return false;
   for (int k = 0; k * kTile < n; ++k) {
     fill(k + 1);
+    for (int i = 0; i < min(n - k * kTile, kTile); ++i)
+      if (!tab[k & 1].live[i]) padding(first + (int64_t)(k * kTile + i) * apart);
     __syncthreads();
   }
   return true;
+}
+// Rows of `heads` heads from hh on become zeros, by `threads` threads of which this is
+// `thread`; row(hh) is where a head's begins.
+template <class Row>
+MSA_DEV void zero_heads(int hh, int heads, int thread, int threads, Row row) {
+  for (int u = thread; u < heads * 16; u += threads)
+    *reinterpret_cast<uint4*>(row(hh + (u >> 4)) + 8 * (u & 15)) = make_uint4(0, 0, 0, 0);
 }
 struct RowsShared {
   Table<kTile> tab[2];
@@ -448,7 +459,16 @@ MSA_DEV void rows_block(const RowsArgs& a, int block, bool bad, RowsShared& s) {
   const int slice = block / a.cut.groups, group = block - slice * a.cut.groups;
   const int apart = a.cut.slices, n = (a.T - slice + apart - 1) / apart;
   if (warp >= a.cut.units * a.cut.phases) {
-    fill_tables<kAdjacent>(a.an, s.tab, bad, 32 * a.cut.units * a.cut.phases, slice, n, apart);
+    const int before = 32 * a.cut.units * a.cut.phases;
+    fill_tables<kAdjacent>(a.an, s.tab, bad, before, slice, n, apart, [&](int64_t t) {
+      if (!a.zero) return;
+      const int hh = group * a.cut.units * 4, heads = min(a.heads - hh, a.cut.units * 4);
+      zero_heads(hh, heads, tid - before, blockDim.x - before, [&](int h) {
+        int head;
+        const int k = tensor_of(a, h, head);
+        return a.y[k] + t * a.y_token[k] + head * a.y_head[k];
+      });
+    });
     return;
   }
   const int phase = warp / a.cut.units, unit = group * a.cut.units + warp - phase * a.cut.units;

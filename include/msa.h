@@ -562,7 +562,10 @@ typedef struct {
  * cos_scale     > 0 and finite; 1 but for stretched contexts.
  * pairs         device [R / 2], written from msa_rope_pairs' output.  An axis out
  *               of range counts as 0 and sets MSA_ERR_INVALID_ARGUMENT; parts of
- *               the call that come up behind that are left out. */
+ *               the call that come up behind that are left out.
+ * zero_padding  what becomes of the output rows (y, dx) of tokens that are padding:
+ *               0: they are left as they were, 1: they are zeros (outputs in new
+ *               memory, gradients that a sum over all rows follows). */
 typedef struct {
   int32_t tokens;
   int32_t head_dim;
@@ -574,6 +577,7 @@ typedef struct {
   float cos_scale;
   const msa_rope_pair* pairs;
   msa_rope_tensor tensor[MSA_ROPE_TENSORS];
+  int32_t zero_padding;
 } msa_rope_problem;
 
 /* Fills pairs[0 .. num_pairs) on the host from angular frequencies (radians per
@@ -587,8 +591,8 @@ int msa_rope_pairs(const double* inv_freq, const int32_t* axes, int32_t num_pair
  *            what is written shares no memory with other tensors of a call, here
  *            and below, but where it is said.
  * positions  device int32 [tokens, num_axes].  A token whose first position is
- *            negative is padding: its rows of y are left as they were.  Other
- *            columns may be negative.
+ *            negative is padding: its rows of y are left as they were, or zeros
+ *            (zero_padding).  Other columns may be negative.
  * Deterministic; a row's result does not depend on the call's other rows. */
 int msa_norm_rope(const msa_rope_problem* p, const uint16_t* const* x, const int32_t* positions, uint16_t* const* y,
                   int32_t* d_status, void* stream);
@@ -600,7 +604,8 @@ size_t msa_norm_rope_bwd_bytes(const msa_rope_problem* p);
  * dy         bf16, laid out by p's y strides: the gradients of y.
  * x          the forward's input (not its output: with y = x it is gone).
  * dx         bf16 out, laid out by p's x strides; may be x itself, or dy itself
- *            where the strides agree.  Rows of padding are left as they were.
+ *            where the strides agree.  Rows of padding are left as they were, or
+ *            zeros (zero_padding).
  * dw         host array of four device pointers, entries NULL where the gradient
  *            is not wanted or there is no weight: [128] or [heads, 128], in the
  *            weight's type, summed in fp32 over the tokens that are no padding
@@ -631,7 +636,8 @@ int msa_norm_rope_bwd(const msa_rope_problem* p, const uint16_t* const* dy, cons
  *            not used.  p.tokens = c.token_cap.
  * positions  device int32 [T, num_axes]; msa_cache_step's positions where there is
  *            one axis.  A token whose first position is negative is padding: none of
- *            its rows are written.  A token whose slot is -1 leaves out K and V.  A
+ *            its rows are written (but zeros to q_out and q_index_out, with
+ *            zero_padding).  A token whose slot is -1 leaves out K and V.  A
  *            slot outside the cache, or one beside a negative first position, leaves
  *            them out too and sets MSA_ERR_INVALID_CACHE.  With index keys, the rows
  *            that chunks covers must not be padding.

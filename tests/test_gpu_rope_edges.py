@@ -158,3 +158,64 @@ def test_first_call_on_another_stream(B, monkeypatch):
     y, = rope.forward(pos, dev, stream=side)
     side.synchronize()
     assert torch.equal(y, dev) and not torch.any(rope.status)      # position 0 turns nothing
+
+
+def _nan_blocks(*shapes):
+    """Fills memory that new tensors of these shapes are likely to get with NaN."""
+    import torch
+    left = [torch.full(s, float("nan"), dtype=torch.bfloat16, device="cuda") for s in shapes for _ in range(4)]
+    torch.cuda.synchronize()
+    del left
+
+
+@pytest.mark.parametrize("kw", [dict(H=2), dict(adjacent=True, rotary=96, axes=2, norm=False)])
+@pytest.mark.parametrize("T, gone", [(40, (0, 1, 5, 17, 30, 31, 38, 39)), (40, range(40)), (1100, range(3, 1100, 7)),
+                                     (1, [0])])
+def test_padding_of_new_tensors_is_zeros(B, kw, T, gone):
+    """Without `out`: rows of padding, whatever the inputs hold there, are zeros in results and gradients, and the
+    gradient of a projection before them is what the other rows give."""
+    import torch
+    L = Layer(B, seed=56, **kw)
+    pos, gone = L.positions(T), np.array(gone)
+    pos.reshape(T, -1)[gone, 0] = -1 - np.arange(len(gone))
+    live = np.setdiff1d(np.arange(T), gone)
+    n = sum(L.heads)
+    rows, dy = _bf16(L.rng, (T, n, 128)), [_bf16(L.rng, (T, h, 128)) for h in L.heads]
+    for b in (rows, *dy):
+        b[gone] = 0x7FC0
+    dev, dys = to_bf16_tensor(rows, "cuda"), [to_bf16_tensor(b, "cuda") for b in dy]
+    at = np.concatenate([[0], np.cumsum(L.heads)])
+    cut = [slice(a, b) for a, b in zip(at, at[1:])]
+    for xs in ([dev[:, c] for c in cut], [dev[:, c].contiguous() for c in cut]):
+        _nan_blocks((T, n, 128), *((T, h, 128) for h in L.heads))
+        ys = L.rope.forward(_dev(pos), *xs)
+        _nan_blocks((T, n, 128), *((T, h, 128) for h in L.heads))
+        dxs, dws = L.rope.backward(_dev(pos), dys, xs)
+        for i in range(4):
+            assert not np.any(_f64(ys[i])[gone]) and not np.any(_f64(dxs[i])[gone])
+            if len(live):
+                x, g = rows[live][:, cut[i]], dy[i][live]
+                _check_forward(L, i, x, pos[live], ys[i][_dev(live).long()])
+                _check_grad(L, i, O.bf16_to_f64(x), O.bf16_to_f64(g), pos[live], dxs[i][_dev(live).long()], dws[i])
+        hidden = torch.ones((T, 8), dtype=torch.bfloat16, device="cuda")
+        hidden[_dev(gone).long()] = 0
+        assert bool(torch.isfinite(hidden.T @ dxs[0].reshape(T, -1)).all())
+
+
+def test_padding_of_an_append(B):
+    """Token rows behind a step's last: zeros in new outputs, as they were in given ones."""
+    import torch
+    L = Layer(B, seed=57, H=2)
+    T, n = 12, 7
+    kv = B.Cache(num_requests=1, num_pages=4, max_blocks=2, num_q_heads=32, topk=2, max_tokens=T)
+    x = [to_bf16_tensor(_bf16(L.rng, (T, h, 128)), "cuda") for h in (32, 2, 2, 2, 2)]
+    for t in x:
+        t[n:] = float("nan")
+    kv.step(_dev([n]), T)
+    _nan_blocks((T, 32, 128), (T, 2, 128))
+    new = kv.append_rope(L.rope, *x)
+    given = kv.append_rope(L.rope, *x, out=[torch.full((T, h, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+                                            for h in (32, 2)])
+    for a, b in zip(new, given):
+        assert torch.equal(a[:n], b[:n]) and not torch.any(a[n:]) and bool((b[n:] == 7.0).all())
+    kv.check_status()

@@ -422,3 +422,23 @@ def test_outputs_that_share_memory_are_refused(B, monkeypatch):
         with pytest.raises(ValueError, match="out of .*: has elements in common"):
             kv.append_rope(rope, q, k, v, qi, ki, out=out)
     assert len(calls) == 3
+
+
+def test_padding_of_new_outputs(B):
+    """zero_padding is 0 or 1; a Rope's descriptions have it where the outputs are new."""
+    import torch
+    for value, code in ((2, 1), (-1, 1), (1, 0), (0, 0)):
+        p = _problem(B)
+        p.zero_padding = value
+        if code:
+            assert _forward(B, p) == code and _backward(B, p) == code and B.msa_norm_rope_bwd_bytes(p) == 0
+            assert _append(B, _cache_problem(B), p) == code
+        else:
+            assert B.msa_norm_rope_bwd_bytes(p) > 0
+            _passes(B, _append(B, _cache_problem(B), p))
+    assert [_problem(B, zero_padding=z).zero_padding for z in (False, True)] == [0, 1] and _problem(B).zero_padding == 0
+    rope = B.Rope(B.rope_frequencies(64), device="cpu")
+    x = torch.zeros((4, 2, 128), dtype=torch.bfloat16)
+    xs = (None, x, None, None)
+    new, given = rope._problem(4, xs, xs, zero=True), rope._problem(4, xs, xs)
+    assert new is not given and new.zero_padding == 1 and given.zero_padding == 0
