@@ -760,6 +760,11 @@ class Rope:
         return positions.shape[0]
 
     @staticmethod
+    def _aligned(positions):
+        """The positions on a border of 16 bytes, as the library asks for: a copy of a view that begins between two."""
+        return positions if positions.data_ptr() % 16 == 0 else positions.clone()
+
+    @staticmethod
     def _strides(x):
         # a dim of one row has no stride to speak of
         T, H, _ = x.shape
@@ -857,7 +862,7 @@ class Rope:
                 p = self._problem(T, xs, ys, zero=out is None)
                 if out is not None:
                     self._check_apart(p, ys, xs)
-                msa_norm_rope(p, xs, positions, ys, self.status if status is None else status)
+                msa_norm_rope(p, xs, self._aligned(positions), ys, self.status if status is None else status)
         return tuple(y for y in ys if y is not None)
 
     def backward(self, positions, grads, inputs, out=None, status=None, stream=None):
@@ -892,7 +897,8 @@ class Rope:
                 if out is not None:
                     self._check_apart(p, dxs, xs, dys)
                 ws = torch.empty(msa_norm_rope_bwd_bytes(p), dtype=torch.uint8, device=self.device)
-                msa_norm_rope_bwd(p, dys, xs, positions, dxs, dws, self.status if status is None else status, ws)
+                msa_norm_rope_bwd(p, dys, xs, self._aligned(positions), dxs, dws,
+                                  self.status if status is None else status, ws)
             else:
                 for dw in dws:
                     if dw is not None:
@@ -1039,8 +1045,9 @@ class Cache:
             p = rope._problem(T, (q, k, q_index, k_index), (yq, None, yi, None), v, out is None)
             if out is not None:
                 rope._check_apart(p, (yq, None, yi, None), (q, k, q_index, k_index, v))
-            msa_cache_append_rope(c, p, q, k, v, q_index, k_index, positions, self.slot_map, self.cu_tokens,
-                                  self.chunks, yq, yi, self.cache, self.index_tail, self.index_pool, self.status)
+            msa_cache_append_rope(c, p, q, k, v, q_index, k_index, rope._aligned(positions), self.slot_map,
+                                  self.cu_tokens, self.chunks, yq, yi, self.cache, self.index_tail, self.index_pool,
+                                  self.status)
         return yq, yi
 
     def select(self, q_index, stream=None):

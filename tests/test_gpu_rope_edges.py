@@ -219,3 +219,31 @@ def test_padding_of_an_append(B):
     for a, b in zip(new, given):
         assert torch.equal(a[:n], b[:n]) and not torch.any(a[n:]) and bool((b[n:] == 7.0).all())
     kv.check_status()
+
+
+@pytest.mark.parametrize("axes", [1, 3])
+def test_positions_that_begin_anywhere(B, axes):
+    """Parts of longer position tensors, which begin between two borders of 16 bytes: the bits of copies; captured, the
+    positions of the replay."""
+    import torch
+    L = Layer(B, seed=58, H=1, axes=axes)
+    T, n = 20, 13
+    pos = _dev(L.positions(T))
+    x = [to_bf16_tensor(_bf16(L.rng, (n, h, 128)), "cuda") for h in L.heads]
+
+    def run(p):
+        kv = B.Cache(num_requests=1, num_pages=4, max_blocks=2, num_q_heads=16, topk=2, max_tokens=n)
+        kv.step(_dev([n]), n)
+        out = kv.append_rope(L.rope, x[0], x[1], x[1], x[2], x[3], positions=p)
+        kv.check_status()
+        return (*L.rope.forward(p, *x), *sum(L.rope.backward(p, x, x), ()), *out, kv.cache, kv.index_tail)
+
+    for at in range(1, 5):
+        part = pos[at:at + n]
+        assert all(torch.equal(a, b) for a, b in zip(run(part), run(part.clone())))
+    g, part = torch.cuda.CUDAGraph(), pos[1:1 + n]
+    with torch.cuda.graph(g):
+        y = L.rope.forward(part, *x)
+    pos.copy_(_dev(L.positions(T)))
+    g.replay()
+    assert all(torch.equal(a, b) for a, b in zip(y, L.rope.forward(part.clone(), *x)))

@@ -442,3 +442,28 @@ def test_padding_of_new_outputs(B):
     xs = (None, x, None, None)
     new, given = rope._problem(4, xs, xs, zero=True), rope._problem(4, xs, xs)
     assert new is not given and new.zero_padding == 1 and given.zero_padding == 0
+
+
+def test_positions_reach_the_library_aligned(B, monkeypatch):
+    """Positions on a border of 16 bytes are passed on as they are, others as a copy."""
+    import contextlib
+
+    import torch
+    for name in ("device", "stream"):
+        monkeypatch.setattr(torch.cuda, name, lambda *a: contextlib.nullcontext())
+    seen = []
+    monkeypatch.setattr(B, "msa_norm_rope", lambda p, xs, positions, *a: seen.append(positions))
+    monkeypatch.setattr(B, "msa_norm_rope_bwd", lambda p, dys, xs, positions, *a: seen.append(positions))
+    rope = B.Rope(B.rope_frequencies(64), device="cpu")
+    pos = torch.arange(40, dtype=torch.int32)
+    x = torch.zeros((5, 2, 128), dtype=torch.bfloat16)
+    first = (-pos.data_ptr() // 4) % 4      # a border
+    for at in range(8):
+        part = pos[first + at:first + at + 5]
+        rope.forward(part, x)
+        rope.backward(part, (x,), (x,))
+        for got in seen:
+            assert torch.equal(got, part) and got.data_ptr() % 16 == 0
+            assert (got.data_ptr() == part.data_ptr()) == (at % 4 == 0)
+        assert len(seen) == 2
+        seen.clear()
