@@ -891,7 +891,8 @@ class Rope:
                 for name, dx, x in zip(self.NAMES, dxs, xs):
                     if x is not None and self._strides(dx) != self._strides(x):
                         raise ValueError(f"out of {name}: need the input's strides")
-            dws = tuple(None if x is None or w is None else torch.empty_like(w) for x, w in zip(xs, self.weights))
+            dws = tuple(None if x is None or w is None else torch.empty_like(w) if T and x.shape[1] else
+                        torch.zeros_like(w) for x, w in zip(xs, self.weights))     # no rows: the call does not write it
             if T:
                 p = self._problem(T, xs, dys, zero=out is None)
                 if out is not None:
@@ -899,10 +900,6 @@ class Rope:
                 ws = torch.empty(msa_norm_rope_bwd_bytes(p), dtype=torch.uint8, device=self.device)
                 msa_norm_rope_bwd(p, dys, xs, self._aligned(positions), dxs, dws,
                                   self.status if status is None else status, ws)
-            else:
-                for dw in dws:
-                    if dw is not None:
-                        dw.zero_()
         return dxs[:n], dws[:n]
 
 

@@ -247,3 +247,24 @@ def test_positions_that_begin_anywhere(B, axes):
     pos.copy_(_dev(L.positions(T)))
     g.replay()
     assert all(torch.equal(a, b) for a, b in zip(y, L.rope.forward(part.clone(), *x)))
+
+
+@pytest.mark.parametrize("T", [0, 5])
+@pytest.mark.parametrize("heads", [(0, 0, 0, 0), (16, 0, 1, 0), (0, 2, 0, 0)])
+def test_weights_of_tensors_without_heads(B, T, heads):
+    """A tensor of no heads, and calls of no tokens: the gradient of its weight is zeros."""
+    import torch
+    L = Layer(B, seed=59)
+    pos = L.positions(T)
+    x, dy = ([_bf16(L.rng, (T, h, 128)) for h in heads] for _ in range(2))
+    put = lambda rows: [to_bf16_tensor(b, "cuda") for b in rows]
+    left = [torch.full((128,), float("nan"), device="cuda") for _ in range(16)]
+    torch.cuda.synchronize()
+    del left
+    dxs, dws = L.rope.backward(_dev(pos), put(dy), put(x))
+    assert [tuple(d.shape) for d in dxs] == [(T, h, 128) for h in heads]
+    for i, h in enumerate(heads):
+        if T and h:
+            _check_grad(L, i, O.bf16_to_f64(x[i]), O.bf16_to_f64(dy[i]), pos, dxs[i], dws[i])
+        else:
+            assert not torch.any(dws[i] != 0), i
