@@ -759,6 +759,16 @@ class Rope:
                              f"{'(tokens,)' if cols is None else ('tokens', cols)} on {self.device}")
         return positions.shape[0]
 
+    def _status(self, status):
+        """The status word of a call, its own where none is given."""
+        import torch
+        if status is None:
+            return self.status
+        if not isinstance(status, torch.Tensor) or status.dtype != torch.int32 or status.numel() < 1 \
+                or status.device != self.device:
+            raise ValueError(f"status: need an int32 tensor on {self.device}")
+        return status
+
     @staticmethod
     def _aligned(positions):
         """The positions on a border of 16 bytes, as the library asks for: a copy of a view that begins between two."""
@@ -854,7 +864,7 @@ class Rope:
         write to, each its input itself or apart from all others.  Rows of padding (a negative first position) are zeros
         in new tensors, and left as they were in `out`."""
         import torch
-        T = self._positions(positions)
+        T, status = self._positions(positions), self._status(status)
         xs = self._given(T, q=q, k=k, q_index=q_index, k_index=k_index)
         with torch.cuda.device(self.device), torch.cuda.stream(stream):
             ys = self._outputs("out", out, xs, T)
@@ -862,7 +872,7 @@ class Rope:
                 p = self._problem(T, xs, ys, zero=out is None)
                 if out is not None:
                     self._check_apart(p, ys, xs)
-                msa_norm_rope(p, xs, self._aligned(positions), ys, self.status if status is None else status)
+                msa_norm_rope(p, xs, self._aligned(positions), ys, status)
         return tuple(y for y in ys if y is not None)
 
     def backward(self, positions, grads, inputs, out=None, status=None, stream=None):
@@ -873,7 +883,7 @@ class Rope:
         gradient itself or apart from all others; new ones are laid out as the inputs are.  Rows of padding as in
         forward: the gradients of what was padded are zeros in new tensors."""
         import torch
-        T = self._positions(positions)
+        T, status = self._positions(positions), self._status(status)
         n = len(inputs)
         if n > 4 or len(grads) != n or any((g is None) != (x is None) for g, x in zip(grads, inputs)):
             raise ValueError("grads: need one for each input")
@@ -898,8 +908,7 @@ class Rope:
                 if out is not None:
                     self._check_apart(p, dxs, xs, dys)
                 ws = torch.empty(msa_norm_rope_bwd_bytes(p), dtype=torch.uint8, device=self.device)
-                msa_norm_rope_bwd(p, dys, xs, self._aligned(positions), dxs, dws,
-                                  self.status if status is None else status, ws)
+                msa_norm_rope_bwd(p, dys, xs, self._aligned(positions), dxs, dws, status, ws)
         return dxs[:n], dws[:n]
 
 

@@ -467,3 +467,16 @@ def test_positions_reach_the_library_aligned(B, monkeypatch):
             assert (got.data_ptr() == part.data_ptr()) == (at % 4 == 0)
         assert len(seen) == 2
         seen.clear()
+
+
+def test_status_words_are_checked(B):
+    """A status word that the device cannot write is refused before the launch."""
+    import torch
+    rope = B.Rope(B.rope_frequencies(64), device="cpu")
+    pos, x = torch.zeros(4, dtype=torch.int32), torch.zeros((4, 2, 128), dtype=torch.bfloat16)
+    for bad in (torch.zeros(4, dtype=torch.int64), torch.zeros(0, dtype=torch.int32), 0, [0],
+                torch.zeros(4, dtype=torch.int32, device="meta")):
+        with pytest.raises(ValueError, match="status"):
+            rope.forward(pos, x, status=bad)
+        with pytest.raises(ValueError, match="status"):
+            rope.backward(pos, (x,), (x,), status=bad)
