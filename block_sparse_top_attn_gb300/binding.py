@@ -759,6 +759,10 @@ class Rope:
                              f"{'(tokens,)' if cols is None else ('tokens', cols)} on {self.device}")
         return positions.shape[0]
 
+    def _check_stream(self, stream):
+        if stream is not None and stream.device != self.device:
+            raise ValueError(f"stream: need one of {self.device}")
+
     def _status(self, status):
         """The status word of a call, its own where none is given."""
         import torch
@@ -865,6 +869,7 @@ class Rope:
         in new tensors, and left as they were in `out`."""
         import torch
         T, status = self._positions(positions), self._status(status)
+        self._check_stream(stream)
         xs = self._given(T, q=q, k=k, q_index=q_index, k_index=k_index)
         with torch.cuda.device(self.device), torch.cuda.stream(stream):
             ys = self._outputs("out", out, xs, T)
@@ -884,6 +889,7 @@ class Rope:
         forward: the gradients of what was padded are zeros in new tensors."""
         import torch
         T, status = self._positions(positions), self._status(status)
+        self._check_stream(stream)
         n = len(inputs)
         if n > 4 or len(grads) != n or any((g is None) != (x is None) for g, x in zip(grads, inputs)):
             raise ValueError("grads: need one for each input")
@@ -1034,6 +1040,7 @@ class Cache:
         T = c.token_cap
         if rope.device != self.device:
             raise ValueError(f"rope: need one on {self.device}")
+        rope._check_stream(stream)
         if positions is None:
             if rope.columns is not None:
                 raise ValueError("positions: a rope with several axes needs them")

@@ -480,3 +480,22 @@ def test_status_words_are_checked(B):
             rope.forward(pos, x, status=bad)
         with pytest.raises(ValueError, match="status"):
             rope.backward(pos, (x,), (x,), status=bad)
+
+
+def test_streams_of_other_devices_are_refused(B):
+    """A launch there would read this device's memory from another."""
+    import torch
+
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    rope = B.Rope(B.rope_frequencies(64), device="cpu")
+    pos, x = torch.zeros(4, dtype=torch.int32), torch.zeros((4, 1, 128), dtype=torch.bfloat16)
+    kv = B.Cache(num_requests=2, num_pages=4, max_blocks=2, num_q_heads=16, topk=2, max_tokens=4, device="cpu")
+    kv._now = t = kv._tables(4)
+    kv.slot_map, kv.positions, kv.chunks = t["slot_map"], t["positions"], t["chunks"]
+    q = torch.zeros((4, 16, 128), dtype=torch.bfloat16)
+    for call in (lambda s: rope.forward(pos, x, stream=s), lambda s: rope.backward(pos, (x,), (x,), stream=s),
+                 lambda s: kv.append_rope(rope, q, x, x, x, x, stream=s)):
+        with pytest.raises(ValueError, match="stream"):
+            call(Stream)
