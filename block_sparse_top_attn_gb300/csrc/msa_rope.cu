@@ -383,6 +383,18 @@ bool bad_rows(const msa_rope_problem* p, T* const* ptrs) {
   return false;
 }
 
+// f / 2 pi modulo a turn, in units of 2^-64, rounded once: the quotient in two parts,
+// q + rest, by 2 pi in two parts, so that it is within 2^-104 of itself.
+uint64_t turns_per_position(double f) {
+  constexpr double kHi = 6.283185307179586, kLo = 2.4492935982947064e-16;  // 2 pi
+  const double q = f / kHi;
+  double rest = fma(-q, kLo, fma(-q, kHi, f)) / kHi;
+  rest -= floor(rest + 0.5);                    // a q beyond 2^52 leaves whole turns
+  const double part = ldexp(q - floor(q), 64);  // < 2^64: a double below 1 is at most 1 - 2^-53
+  const double whole = floor(part);
+  return (uint64_t)whole + (uint64_t)(int64_t)floor(part - whole + ldexp(rest, 64) + 0.5);
+}
+
 template <class Args>
 int set_tensors(Args& a, const msa_rope_problem* p, const uint16_t* const* x) {
   int end = 0;
@@ -404,9 +416,7 @@ int msa_rope_pairs(const double* inv_freq, const int32_t* axes, int32_t num_pair
   if (!inv_freq || !pairs || num_pairs < 0 || num_pairs > kHeadDim / 2) return MSA_ERR_INVALID_ARGUMENT;
   for (int i = 0; i < num_pairs; ++i) {
     if (!isfinite(inv_freq[i])) return MSA_ERR_INVALID_ARGUMENT;
-    const double turns = fabs(inv_freq[i]) / 6.283185307179586476925;
-    const double part = ldexp(turns - floor(turns), 64);  // < 2^64: a double below 1 is at most 1 - 2^-53
-    const uint64_t u = part < 4503599627370496.0 ? (uint64_t)(part + 0.5) : (uint64_t)part;
+    const uint64_t u = turns_per_position(fabs(inv_freq[i]));
     pairs[i].turns = inv_freq[i] < 0 ? 0 - u : u;
     pairs[i].axis = axes ? axes[i] : 0;
     pairs[i].reserved = 0;

@@ -522,8 +522,9 @@ int msa_cache_fwd(const msa_cache_problem* p, const uint16_t* q, const uint8_t* 
  *   (a, b) -> cos_scale * (a cos t - b sin t, b cos t + a sin t)
  * with t = 2 pi * turns[p] / 2^64 * position[axis[p]]: each pair follows one of a
  * token's num_axes positions (one for text; time, height and width of images and
- * video).  Angles are formed in 64-bit fixed point, so that they are as exact at
- * position 2^31 as at 1.  All else is fp32, rounded to bf16 once.
+ * video).  Angles are formed in 64-bit fixed point, which loses nothing at any
+ * position; the table's own rounding, 2^-65 of a turn, counts once a position: 2^-34
+ * at position 2^31, less than fp32 tells.  All else is fp32, rounded to bf16 once.
  * Rows may hold any finite values.  Weights (offset added) times cos_scale may reach
  * 2^62, and their products with the gradients 2^100: beyond, fp32 may overflow.
  *
@@ -581,7 +582,9 @@ typedef struct {
 } msa_rope_problem;
 
 /* Fills pairs[0 .. num_pairs) on the host from angular frequencies (radians per
- * position, as rotary tables give them) and position columns (NULL: 0). */
+ * position, as rotary tables give them) and position columns (NULL: 0).  turns is
+ * the frequency's quotient by 2 pi, modulo 1, rounded once to 2^-64 (frequencies of
+ * up to 2^38; beyond, within 2^-100 of the quotient). */
 int msa_rope_pairs(const double* inv_freq, const int32_t* axes, int32_t num_pairs, msa_rope_pair* pairs);
 
 /* The forward.
@@ -623,8 +626,9 @@ int msa_norm_rope_bwd(const msa_rope_problem* p, const uint16_t* const* dy, cons
  *  - K normed, rotated and rounded to 4 bits by msa_cache_append's rule, V rounded
  *    as it is, both written to the tokens' slots.  K is not rounded to bf16 in
  *    between: its codes and scales are those of the exact value of y (what lies
- *    closer to a border than fp32 can tell is computed again in pairs of fp32).  A
- *    value beyond fp32's range makes its group NaN, as an infinite one does;
+ *    closer to a border than fp32 can tell is computed again in pairs of fp32, within
+ *    2^-38, which leaves about one value in 10^10).  A value beyond fp32's range
+ *    makes its group NaN, as an infinite one does;
  *  - index keys normed, rotated and rounded to bf16 as msa_norm_rope does, and kept
  *    by msa_cache_append's rule (index_tail and index_pool hold the same, bit for
  *    bit, as after the two calls).

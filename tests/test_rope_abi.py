@@ -499,3 +499,28 @@ def test_streams_of_other_devices_are_refused(B):
                  lambda s: kv.append_rope(rope, q, x, x, x, x, stream=s)):
         with pytest.raises(ValueError, match="stream"):
             call(Stream)
+
+
+def test_pairs_are_rounded_once(B):
+    """The quotient by 2 pi is exact to the table's last bit: half of it, and 2^-3 of that for the arithmetic."""
+    rng = np.random.default_rng(0)
+    f = [B.rope_frequencies(128, 5e6), B.rope_frequencies(128), B.rope_frequencies(128, 1e9)]
+    f += [np.exp(rng.uniform(-60, 26, 64)) for _ in range(20)] + [rng.uniform(-7, 7, 64)]
+    f += [2.0 ** np.arange(-70, 38)[:64], 2.0 ** np.arange(-70, 38)[44:], 2 * math.pi * np.arange(1.0, 65),
+          np.nextafter(2 * math.pi * np.arange(1.0, 65), 0), 2.0 ** -np.arange(1060.0, 1074)]
+    # 2 pi to 75 digits
+    two_pi = Fraction(6283185307179586476925286766559005768394338798750211641949889184615632812572, 10 ** 75)
+
+    def off(w, turns):
+        x = (Fraction(int(turns) % 2 ** 64, 2 ** 64) - Fraction(float(w)) / two_pi) % 1
+        return min(x, 1 - x)
+
+    def table(part):
+        part = np.concatenate([part, np.ones(-len(part) % 64)])
+        return zip(part, B.rope_pairs(part, device="cpu").table.numpy()[:, 0])
+
+    for part in f:
+        for w, turns in table(part):
+            assert off(w, turns) <= Fraction(9, 8 * 2 ** 65), w
+    for w, turns in table(2.0 ** rng.uniform(38, 110, 64)):
+        assert off(w, turns) <= Fraction(9, 8 * 2 ** 65) + Fraction(float(w)) / two_pi / 2 ** 100, w
