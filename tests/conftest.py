@@ -7,12 +7,25 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
 
+# Tests of the argument checks that pass good arguments too, with addresses that are none: without a GPU such a call ends
+# at the device check, with one it would launch on them.
+NEED_NO_GPU = {("test_rope_abi.py", name) for name in
+               ("test_null_and_misaligned_pointers", "test_no_tokens_need_no_rows", "test_append_arguments")}
+
 
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs a CUDA device (GB300, sm_103a)")
     config.addinivalue_line("markers", "slow: takes more than a few seconds of CPU")
+    if "not gpu" in (config.option.markexpr or ""):
+        os.environ["CUDA_VISIBLE_DEVICES"] = ""     # the tests for CPUs see none
 
 
 def pytest_collection_modifyitems(config, items):
     # files named test_zz_* run after every other test file
     items.sort(key=lambda it: os.path.basename(str(it.fspath)).startswith("test_zz_"))
+    alone = [it for it in items if (os.path.basename(str(it.fspath)), getattr(it, "originalname", None)) in NEED_NO_GPU]
+    if alone and "gpu" not in (config.option.markexpr or ""):
+        import torch
+        if torch.cuda.is_available():
+            for it in alone:
+                it.add_marker(pytest.mark.skip(reason="passes addresses that are none: -m 'not gpu' runs it"))

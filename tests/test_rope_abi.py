@@ -435,7 +435,6 @@ def test_padding_of_new_outputs(B):
             assert _append(B, _cache_problem(B), p) == code
         else:
             assert B.msa_norm_rope_bwd_bytes(p) > 0
-            _passes(B, _append(B, _cache_problem(B), p))
     assert [_problem(B, zero_padding=z).zero_padding for z in (False, True)] == [0, 1] and _problem(B).zero_padding == 0
     rope = B.Rope(B.rope_frequencies(64), device="cpu")
     x = torch.zeros((4, 2, 128), dtype=torch.bfloat16)
