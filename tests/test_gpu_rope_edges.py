@@ -268,3 +268,19 @@ def test_weights_of_tensors_without_heads(B, T, heads):
             _check_grad(L, i, O.bf16_to_f64(x[i]), O.bf16_to_f64(dy[i]), pos, dxs[i], dws[i])
         else:
             assert not torch.any(dws[i] != 0), i
+
+
+@pytest.mark.parametrize("T", [1, 5, 400])
+def test_a_bad_axis(B, T):
+    """A pair's axis behind the positions' columns counts as the first and is reported; parts of the call that come up
+    behind the report leave their rows as they were."""
+    import torch
+    L = Layer(B, seed=60)
+    x, pos = to_bf16_tensor(_bf16(L.rng, (T, 1, 128)), "cuda"), _dev(L.positions(T))
+    y, st = torch.full_like(x, 2.0), torch.zeros(4, dtype=torch.int32, device="cuda")
+    p = B.make_rope_problem(T, B.rope_pairs(L.freq, [0, 2] * 32), k=B.RopeTensor(1, weight=L.dev[1]), eps=1e-6, num_axes=1)
+    B.msa_norm_rope(p, [None, x, None, None], pos, [None, y, None, None], st)
+    assert int(st[0].item()) == B.MSA_ERR_INVALID_ARGUMENT
+    want = L.rope.forward(pos, None, x)[0]
+    done, left = (y == want).all(-1), (y == 2.0).all(-1)
+    assert bool((done | left).all()) and bool(done.any()) and (T > 1 or bool(done.all()))
