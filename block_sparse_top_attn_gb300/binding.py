@@ -812,8 +812,8 @@ class Rope:
 
     @staticmethod
     def _like(xs):
-        """New tensors with the shapes and strides of xs; views of one buffer where they are views of one tensor (and no
-        two of the same elements)."""
+        """New tensors with the shapes and strides of xs; views of one buffer where they are views of one tensor (no two
+        of the same elements, and not so far apart that the buffer were more than twice as large as their own)."""
         import torch
         made, groups = [None] * len(xs), {}
         for i, x in enumerate(xs):
@@ -821,13 +821,21 @@ class Rope:
                 key = (x.untyped_storage().data_ptr(), x.stride())
                 shared = any(_share_memory(x, xs[j]) for j in groups.get(key, ()))
                 groups.setdefault(i if shared else key, []).append(i)
-        for members in groups.values():
-            ends = [xs[i].storage_offset() + sum((n - 1) * s for n, s in zip(xs[i].shape, xs[i].stride())) + 1
-                    for i in members]
+        extent = lambda x: max(0, sum((n - 1) * s for n, s in zip(x.shape, x.stride())) + 1)
+
+        def make(members):
             base = min(xs[i].storage_offset() for i in members)
-            buf = torch.empty(max(0, max(ends) - base), dtype=torch.bfloat16, device=xs[members[0]].device)
+            size = max(xs[i].storage_offset() + extent(xs[i]) for i in members) - base
+            if len(members) > 1 and size > 2 * sum(extent(xs[i]) for i in members):
+                for i in members:
+                    make([i])
+                return
+            buf = torch.empty(size, dtype=torch.bfloat16, device=xs[members[0]].device)
             for i in members:
                 made[i] = buf.as_strided(xs[i].shape, xs[i].stride(), xs[i].storage_offset() - base)
+
+        for members in groups.values():
+            make(members)
         return tuple(made)
 
     def _check_apart(self, p, outs, *inputs):

@@ -523,3 +523,19 @@ def test_pairs_are_rounded_once(B):
             assert off(w, turns) <= Fraction(9, 8 * 2 ** 65), w
     for w, turns in table(2.0 ** rng.uniform(38, 110, 64)):
         assert off(w, turns) <= Fraction(9, 8 * 2 ** 65) + Fraction(float(w)) / two_pi / 2 ** 100, w
+
+
+def test_new_gradients_of_views_far_apart(B):
+    """Views far apart in one large buffer get memory of their own, not the distance between them."""
+    import torch
+    layers = torch.zeros((40, 6, 2, 128), dtype=torch.bfloat16)
+    size = lambda made: sum({x.untyped_storage().data_ptr(): x.untyped_storage().nbytes() for x in made}.values())
+    for xs in ((layers[0], layers[39]), (layers[3], layers[20], layers[21], layers[39]), (layers[5], layers[6])):
+        made = B.Rope._like(xs)
+        assert size(made) == len(xs) * layers[0].numel() * 2
+        assert all(d.shape == x.shape and d.stride() == x.stride() for d, x in zip(made, xs))
+    row = layers.view(1, -1, 128)       # one token: parts of its row, with a gap
+    made = B.Rope._like((row[:, :16], row[:, 16:17], row[:, 18:19]))
+    assert len({x.untyped_storage().data_ptr() for x in made}) == 1
+    none = layers[:, :0]
+    assert [d.shape for d in B.Rope._like((none[0], none[1]))] == [(0, 2, 128)] * 2
