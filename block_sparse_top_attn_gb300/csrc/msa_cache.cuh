@@ -98,6 +98,20 @@ MSA_DEV uint32_t unsigned_zeros(uint32_t w) {
   return w & (((m << 1 | m << 2 | m << 3) & 0x88888888u) | 0x77777777u);
 }
 
+// Eight e2m1 codes of eight values, zeros without a sign.
+MSA_DEV uint32_t e2m1x8(const float (&x)[8]) {
+  uint32_t codes;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(codes)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return unsigned_zeros(codes);
+}
+
 // One group of 16 bf16 values (8 words) to codes (8 bytes) and an e4m3 scale.
 // Quotients are formed so that the conversions' ties are those of the exact
 // ones: max / 6 with one correction step (exact where the quotient has 24 bits,
@@ -133,16 +147,9 @@ MSA_DEV uint32_t quantize16(const uint32_t (&w)[8], float mul, uint2& codes) {
       q[2 * i] = __fadd_rn(__fmaf_rn(__uint_as_float(x << 16), inv, 768.f), -768.f);
       q[2 * i + 1] = __fadd_rn(__fmaf_rn(__uint_as_float(x & 0xFFFF0000u), inv, 768.f), -768.f);
     }
-    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
-        "mov.b32 %0, {a, b, c, d};\n\t}"
-        : "=r"(out[h])
-        : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+    out[h] = e2m1x8(q);
   }
-  codes = make_uint2(unsigned_zeros(out[0]), unsigned_zeros(out[1]));
+  codes = make_uint2(out[0], out[1]);
   return s8;
 }
 

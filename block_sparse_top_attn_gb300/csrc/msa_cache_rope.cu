@@ -242,21 +242,11 @@ struct Half {
   uint32_t codes, scale;  // codes of the lane's eight, the group's scale
   bool doubt;             // fp32 does not tell
 };
-// Eight e2m1 codes, zeros without a sign.
 MSA_DEV uint32_t codes8(const uint64_t (&q)[4]) {
   float x[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) f2_unpack(q[i], x[2 * i], x[2 * i + 1]);
-  uint32_t out;
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
-      "mov.b32 %0, {a, b, c, d};\n\t}"
-      : "=r"(out)
-      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
-  return cache::unsigned_zeros(out);
+  return cache::e2m1x8(x);
 }
 // Rounds with the error to either side: where the results differ, there is a border
 // between them.  exact: the values are the inputs themselves, and rounded by
