@@ -688,16 +688,8 @@ class _Extent:
 
 
 def _share_memory(a, b) -> bool:
-    """Whether two bf16 [tokens, heads, 128] tensors have elements in common, whatever their strides."""
-    if a.numel() == 0 or b.numel() == 0:
-        return False
-    strides = a.stride()
-    if strides == b.stride() and strides[0] > 0:    # beside one another in the same rows, as a rule
-        at = (b.data_ptr() - a.data_ptr()) // a.element_size() % strides[0]
-        width = lambda x: (x.shape[1] - 1) * strides[1] + HEAD_DIM
-        if strides[1] > 0 and at >= width(a) and at + width(b) <= strides[0]:
-            return False
-    return np.shares_memory(np.asarray(_Extent(a)), np.asarray(_Extent(b)))
+    """Whether two tensors have elements in common, whatever their strides."""
+    return a.numel() > 0 and b.numel() > 0 and np.shares_memory(np.asarray(_Extent(a)), np.asarray(_Extent(b)))
 
 
 class Rope:
@@ -781,17 +773,18 @@ class Rope:
     @staticmethod
     def _strides(x):
         # a dim of one row has no stride to speak of
-        T, H, _ = x.shape
-        return (x.stride(0) if T > 1 else H * HEAD_DIM, x.stride(1) if H > 1 else HEAD_DIM)
+        (T, H, _), (token, head, _) = x.shape, x.stride()
+        return (token if T > 1 else H * HEAD_DIM, head if H > 1 else HEAD_DIM)
 
     def _problem(self, tokens, xs, ys, v=None, zero=False):
         """The description of calls with these tensors' shapes and strides.  zero: rows of padding are zeros."""
         every = (*xs, v) if v is not None else xs
         # a parameter's storage may be replaced, by one of another type or shape at the same address
-        key = (tokens, zero, *(None if w is None else (w.data_ptr(), w.dtype, w.shape, w.is_contiguous(), w.get_device())
-                         for w in self.weights),
-               *((x.shape[1], *self._strides(x), *(self._strides(y) if y is not None else ()))
-                 if x is not None else None for x, y in zip(every, (*ys, None))))
+        key = (tokens, zero,
+               *[None if w is None else (w.data_ptr(), w.dtype, w.shape, w.is_contiguous(), w.get_device())
+                 for w in self.weights],
+               *[None if x is None else (x.shape[1], self._strides(x), None if y is None else self._strides(y))
+                 for x, y in zip(every, (*ys, None))])
         p = self._problems.get(key)
         if p is None:
             if len(self._problems) >= 64:
@@ -818,30 +811,41 @@ class Rope:
         made, groups = [None] * len(xs), {}
         for i, x in enumerate(xs):
             if x is not None:
-                key = (x.untyped_storage().data_ptr(), x.stride())
-                shared = any(_share_memory(x, xs[j]) for j in groups.get(key, ()))
-                groups.setdefault(i if shared else key, []).append(i)
-        extent = lambda x: max(0, sum((n - 1) * s for n, s in zip(x.shape, x.stride())) + 1)
+                (T, H, _), (row, head, last) = shape, strides = x.shape, x.stride()
+                width = (H - 1) * head + (HEAD_DIM - 1) * last + 1          # of a token
+                m = (x.storage_offset(), width, (T - 1) * row + width if T and H else 0, i, shape, strides)
+                groups.setdefault((x.untyped_storage().data_ptr(), strides), []).append(m)
 
         def make(members):
-            base = min(xs[i].storage_offset() for i in members)
-            size = max(xs[i].storage_offset() + extent(xs[i]) for i in members) - base
-            if len(members) > 1 and size > 2 * sum(extent(xs[i]) for i in members):
-                for i in members:
-                    make([i])
+            base = members[0][0]
+            size = max(m[0] + m[2] for m in members) - base
+            if len(members) > 1 and size > 2 * sum(m[2] for m in members):
+                for m in members:
+                    make([m])
                 return
-            buf = torch.empty(size, dtype=torch.bfloat16, device=xs[members[0]].device)
-            for i in members:
-                made[i] = buf.as_strided(xs[i].shape, xs[i].stride(), xs[i].storage_offset() - base)
+            buf = torch.empty(size, dtype=torch.bfloat16, device=xs[members[0][3]].device)
+            for at, _, _, i, shape, strides in members:
+                made[i] = buf.as_strided(shape, strides, at - base)
 
-        for members in groups.values():
+        for (_, (row, _, _)), members in groups.items():
+            members.sort()
+            ends = [m[0] + m[1] for m in members]
+            # beside one another within a row, as a rule
+            if any(a > m[0] for a, m in zip(ends, members[1:])) or ends[-1] - members[0][0] > row:
+                apart = []
+                for m in members:
+                    if any(_share_memory(xs[m[3]], xs[o[3]]) for o in apart):
+                        make([m])
+                    else:
+                        apart.append(m)
+                members = apart
             make(members)
         return tuple(made)
 
     def _check_apart(self, p, outs, *inputs):
         """Refuses outputs that have elements in common with one another or with an input; an output may be an input of
         its own role itself.  outs, inputs: tuples of the roles' tensors (what lies behind NAMES has no output)."""
-        key = tuple(_addr(x) for xs in (outs, *inputs) for x in xs)
+        key = tuple([None if x is None else x.data_ptr() for xs in (outs, *inputs) for x in xs])
         if key in p._apart:     # seen before with these shapes and strides
             return
         place = lambda x: (x.data_ptr(), self._strides(x))
