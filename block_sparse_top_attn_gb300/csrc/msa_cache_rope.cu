@@ -40,13 +40,13 @@ struct AppendRopeArgs {
 // ---------------------------------------------------------------------------
 // The cache keeps a value by the interval it lies in, so an error of fp32 counts
 // only next to a border, and there by a whole code.  With amp = |a cos| + |b sin| and
-// u = 2^-24, fp32 forms y to within 23 u amp: 12 u for the weighted a and b and the
+// u = 2^-24, fp32 forms y to within 21 u amp: 12 u for the weighted a and b and the
 // inverse rms (the sum of 128 squares in chains of 4 and 6 more additions, halved by
-// the root; rsqrtf 2 ulp; the weight's offset and products), 7 u for the cosine with
-// its scale, the products and the sum; the code's quotient adds 4 u.  A group with a
-// value (or a scale) nearer to a border than 32 u amp is done again exactly, from the
-// inputs, behind the others: one group in 1,000, which costs a step of 64 tokens 0.7 us
-// of 5.1.
+// the root; rsqrtf 2 ulp; the weight's offset and products), 9 u for the cosine (6), its
+// scale, the products and the sum.  The code's quotient adds 4 u, and the eps that is
+// left out of rows scaled by kDown up to 4 u: 29 u in all.  A group with a value (or a
+// scale) nearer to a border than 32 u amp is done again exactly, from the inputs, behind
+// the others: one group in 1,000, which costs a step of 64 tokens 0.7 us of 5.1.
 constexpr float kUlps = 32.f;
 
 // Exact enough means pairs of fp32, hi + lo, by the error-free sums and products of

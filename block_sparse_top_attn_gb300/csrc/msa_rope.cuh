@@ -57,7 +57,7 @@ MSA_DEV void lane_dims(int j, int R, int& a, int& b) {
 
 // Cosine and sine of a fraction of a turn.  The quarter turns are taken off exactly,
 // and the eighth that is left is as exact as its 24 bits, so that the Taylor
-// polynomials of degrees 9 and 10 (off by 2^-29 and less of the value) serve: within
+// polynomials of degrees 9 and 10 (off by 2^-28.5 and 2^-32 of the value) serve: within
 // 6 u of a relative error, u = 2^-24: 4 u from the argument, 2 u from the sums.
 MSA_DEV void cos_sin(uint64_t turn, float scale, float& c, float& s) {
   const uint64_t shifted = turn + (1ull << 61);

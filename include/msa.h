@@ -612,7 +612,10 @@ size_t msa_norm_rope_bwd_bytes(const msa_rope_problem* p);
  * dw         host array of four device pointers, entries NULL where the gradient
  *            is not wanted or there is no weight: [128] or [heads, 128], in the
  *            weight's type, summed in fp32 over the tokens that are no padding
- *            (and over the heads that share it).  Overwritten, not added to.
+ *            (and over the heads that share it).  Overwritten, not added to.  The
+ *            chains of additions grow with the rows: 131072 tokens x 152 heads make
+ *            2,185 long ones, and sums that are off by 0.2 x 2^-24 of the sum of the
+ *            magnitudes, 7.3 x 2^-24 where all products have one sign.
  * ws         msa_norm_rope_bwd_bytes(p), overwritten before it is read.
  * Deterministic. */
 int msa_norm_rope_bwd(const msa_rope_problem* p, const uint16_t* const* dy, const uint16_t* const* x,
